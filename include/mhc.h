@@ -76,9 +76,10 @@ typedef struct {
                           * Costs latency on small batches (fewer slices). */
 } mhc_params;
 
-/* Element type of norm_w. The DeepSeek boundary kernel reads bf16 weights;
- * fp32 is the common checkpoint dtype. */
-typedef enum { MHC_F32 = 0, MHC_BF16 = 1 } mhc_dtype;
+/* Element types. norm_w of the boundary is F32 or BF16 (the DeepSeek boundary
+ * kernel reads bf16 weights; fp32 is the common checkpoint dtype); F16 is for
+ * the gated residual block below. */
+typedef enum { MHC_F32 = 0, MHC_BF16 = 1, MHC_F16 = 2 } mhc_dtype;
 
 /* ---------------------------------------------------------------------- */
 /* Weight preparation ("mhc_boundary" page, prepare_boundary_weight).       */
@@ -256,6 +257,154 @@ mhc_status mhc_boundary_fused_noalloc(const uint16_t *x, const uint16_t *residua
                                       uint16_t *residual_out, uint16_t *layer_input,
                                       float *pre_out, float *post_out, float *comb_out,
                                       void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Gated residual block with a norm on either side (one residual stream),   */
+/* its backward pass, and activation checkpoints in 8 bits. The pages have  */
+/* no counterpart of these entry points.                                    */
+
+/*
+ * Per token, between one block of a network (whose output is y) and the next
+ * (whose input is h):
+ *   n  = y * rstd_post * (w_post + weight_offset),  rstd_post = 1 / sqrt(mean(y^2) + eps_post)
+ *   residual_out = scale * residual + act(gate) * n
+ *   h  = residual_out * rstd_pre * (w_pre + weight_offset),
+ *        rstd_pre = 1 / sqrt(mean(residual_out^2) + eps_pre)
+ * post_norm == 0 leaves the first line out (n = y, rstd_post = 1, and w_post
+ * must be NULL). A NULL weight means a weight_offset + w of 1.
+ * All arithmetic is fp32; h comes from the unrounded residual_out, and each
+ * output is rounded once.
+ *
+ * Unlike the boundary's, these entry points take any hidden in [1, 65536],
+ * and rows that lie `stride` elements apart (>= 0; the elements of a row are
+ * contiguous); a pointer needs its element type's alignment only. Rows on
+ * 16-byte boundaries (pointer and stride) and hidden a multiple of 8 take
+ * the vector loads.
+ */
+typedef enum {
+    MHC_GATE_NONE = 0,      /* act(gate) = 1 */
+    MHC_GATE_CHANNEL = 1,   /* gate [H] */
+    MHC_GATE_TOKEN = 2,     /* gate [T], gate_stride apart */
+    MHC_GATE_FULL = 3       /* gate [T, H], rows gate_stride apart */
+} mhc_gate_form;
+
+typedef enum { MHC_ACT_NONE = 0, MHC_ACT_SIGMOID = 1, MHC_ACT_TANH = 2 } mhc_gate_act;
+
+typedef enum {
+    MHC_SCALE_NONE = 0,     /* scale = 1 */
+    MHC_SCALE_ONE = 1,      /* scale [1] */
+    MHC_SCALE_CHANNEL = 2   /* scale [H] */
+} mhc_scale_form;
+
+typedef struct {
+    int64_t tokens;               /* T >= 0 */
+    int hidden;                   /* H in [1, 65536] */
+    mhc_dtype dtype;              /* y, h, their gradients */
+    mhc_dtype residual_dtype;     /* residual, residual_out, their gradients: dtype or F32 */
+    const void *w_post;           /* [H] or NULL */
+    const void *w_pre;            /* [H] or NULL */
+    mhc_dtype w_post_dtype, w_pre_dtype;
+    const void *gate;             /* by gate_form; NULL with MHC_GATE_NONE */
+    mhc_dtype gate_dtype;         /* dtype or F32 */
+    mhc_gate_form gate_form;
+    mhc_gate_act gate_act;
+    int64_t gate_stride;          /* elements; TOKEN and FULL */
+    const float *res_scale;       /* by scale_form; NULL with MHC_SCALE_NONE */
+    mhc_scale_form scale_form;
+    float eps_post, eps_pre;      /* >= 0 */
+    float weight_offset;          /* added to w_post and w_pre (1 where weights are kept as w - 1) */
+    int post_norm;
+} mhc_block;
+
+/*
+ * An activation checkpoint: rows in groups of 32 values (the last one of a row
+ * may be shorter), one scale byte a group. With m the group's largest
+ * magnitude and Q the format's largest value (448 for E4M3, 127 for INT8),
+ * k is the least integer, at least -126, with m <= Q * 2^k; the scale byte is
+ * k + 127 and a value x is held as x * 2^-k rounded to nearest, ties to even.
+ * Scaling by 2^-k is exact, so a code is off by that one rounding and is
+ * bitwise the same whatever path wrote it. A group with an infinity or a NaN
+ * has the scale byte 255 and codes 0, and reads back as NaN throughout.
+ */
+typedef enum { MHC_CKPT_E4M3 = 1, MHC_CKPT_INT8 = 2 } mhc_ckpt_format;
+
+typedef struct {
+    uint8_t *codes;    /* [T, H] contiguous */
+    uint8_t *scales;   /* [T, ceil(H / 32)] contiguous */
+} mhc_ckpt;
+
+/*
+ * The block boundary above. y, residual: inputs. residual_out [T, H] of
+ * residual_dtype (may be exactly the residual buffer when residual_stride is
+ * H) and h [T, H] of dtype: outputs, contiguous. rstd: [T, 2] fp32 (rstd_post,
+ * rstd_pre), what the backward pass needs beside y and residual, or NULL.
+ * ckpt_y, ckpt_residual, ckpt_h: each NULL or a checkpoint to write of the
+ * inputs y and residual and of the rounded h, in the same pass.
+ */
+mhc_status mhc_block_norm(const mhc_block *block, const void *y, int64_t y_stride,
+                          const void *residual, int64_t residual_stride, void *residual_out,
+                          void *h, float *rstd, mhc_ckpt_format format, const mhc_ckpt *ckpt_y,
+                          const mhc_ckpt *ckpt_residual, const mhc_ckpt *ckpt_h, void *stream);
+
+/* Bytes of device scratch of mhc_block_norm_backward: the partial sums over
+ * tokens of the weights' gradients. 0 when T == 0. Needs no initialisation. */
+size_t mhc_block_norm_backward_workspace_bytes(int64_t tokens, int hidden);
+
+/*
+ * Backward pass of mhc_block_norm. d_residual_out [T, H] of residual_dtype (or
+ * NULL: zero) and d_h [T, H] of dtype: the outputs' gradients. y and residual:
+ * the inputs, or NULL with ckpt_y / ckpt_residual given: then their
+ * checkpointed values are used. rstd as mhc_block_norm wrote it;
+ * residual_out is formed anew from y and residual. With ro the unrounded
+ * residual_out and n, g = act(gate) as above:
+ *   D          = d_residual_out + rstd_pre*d_h*w2 - ro*rstd_pre^3*mean(d_h*w2*ro)
+ *   d_residual = scale * D                 d_res_scale = sum residual * D
+ *   d_y        = rstd_post*g*D*w1 - y*rstd_post^3*mean(g*D*w1*y)   (post_norm 0: g*D)
+ *   d_w_post   = sum_t g*D*y*rstd_post     d_w_pre = sum_t d_h*ro*rstd_pre
+ *   d_gate     = act'(gate) * n * D, summed over what the gate is shared by
+ * Outputs: d_y [T, H] of dtype, d_residual [T, H] of residual_dtype (may be
+ * exactly the d_residual_out buffer when its stride is H), both contiguous;
+ * d_w_post, d_w_pre [H] fp32; d_gate [H] fp32 (CHANNEL), [T] fp32 (TOKEN) or
+ * [T, H] of gate_dtype (FULL); d_res_scale [1] or [H] fp32. Any of the last
+ * four may be NULL where it is not wanted, and must be where there is no such
+ * input. Sums over tokens run in an order fixed by (T, H): results are the
+ * same run to run. T == 0 writes zeros to the sums.
+ */
+mhc_status mhc_block_norm_backward(const mhc_block *block, const void *d_residual_out,
+                                   int64_t d_residual_out_stride, const void *d_h,
+                                   int64_t d_h_stride, const void *y, int64_t y_stride,
+                                   const void *residual, int64_t residual_stride,
+                                   mhc_ckpt_format format, const mhc_ckpt *ckpt_y,
+                                   const mhc_ckpt *ckpt_residual, const float *rstd, void *d_y,
+                                   void *d_residual, float *d_w_post, float *d_w_pre,
+                                   void *d_gate, float *d_res_scale, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* x [T, H] of dtype, rows `stride` elements apart -> out. */
+mhc_status mhc_ckpt_pack(const void *x, int64_t stride, mhc_dtype dtype, int64_t tokens,
+                         int hidden, mhc_ckpt_format format, const mhc_ckpt *out, void *stream);
+
+/* What the checkpoint stands for -> x [T, H] of dtype, contiguous. F32 holds
+ * every value exactly, BF16 all but those below 2^-126 (rounded); F16 rounds. */
+mhc_status mhc_ckpt_unpack(const mhc_ckpt *ckpt, mhc_ckpt_format format, int64_t tokens,
+                           int hidden, mhc_dtype dtype, void *x, void *stream);
+
+/* Bytes of device scratch of mhc_ckpt_linear_dw. Needs no initialisation. */
+size_t mhc_ckpt_linear_dw_workspace_bytes(int64_t tokens, int n, int k);
+
+/*
+ * Weight gradient of a projection out = x W^T whose input was checkpointed:
+ *   d_w[i][j] = sum_t d_out[t][i] * x[t][j]      (accumulate: added to d_w)
+ * d_out: [T, n] of dtype (BF16 or F16), rows d_out_stride elements apart.
+ * x: a checkpoint [T, k]; its values are exact in bf16 (with an F16 d_out they
+ * are rounded to fp16). d_w: [n, k] contiguous, of d_w_dtype (any); products
+ * and sums are fp32, rounded once. n, k in [1, 65536]. T == 0 writes zeros
+ * (accumulate: leaves d_w as it is).
+ */
+mhc_status mhc_ckpt_linear_dw(const void *d_out, int64_t d_out_stride, mhc_dtype dtype,
+                              const mhc_ckpt *x, mhc_ckpt_format format, int64_t tokens, int n,
+                              int k, void *d_w, mhc_dtype d_w_dtype, int accumulate,
+                              void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------- */
 /* Status and diagnostics.                                                  */

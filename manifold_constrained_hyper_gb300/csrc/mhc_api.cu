@@ -593,6 +593,35 @@ mhc_status run_boundary(int mode, const uint16_t *x, const uint16_t *residual, c
 
 }  // namespace
 
+namespace mhc {
+
+int require_device(int *sms, unsigned int **status) {
+    DeviceInfo *dev = nullptr;
+    if (mhc_status s = current_device(&dev)) return s;
+    *sms = dev->sms;
+    if (status) *status = dev->status;
+    return MHC_OK;
+}
+int note_launch(cudaError_t e) { return launched(e); }
+bool pdl_enabled() { return g_pdl.load() != 0; }
+unsigned long long wait_timeout_ns() { return g_timeout_ns.load(); }
+
+bool encode_rows16(CUtensorMap *m, bool bf16, const void *ptr, unsigned long long inner,
+                   unsigned long long rows, unsigned long long pitch_bytes, unsigned int box_rows) {
+    if (!get_encoder()) return false;
+    cuuint64_t dims[2] = {inner, rows};
+    cuuint64_t strides[1] = {pitch_bytes};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                    const_cast<void *>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace mhc
+
 extern "C" {
 
 size_t mhc_weight_bytes(int hidden) {

@@ -10,14 +10,16 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmhc.so")
 _lib = None
 
-MHC_F32, MHC_BF16 = 0, 1
+MHC_F32, MHC_BF16, MHC_F16 = 0, 1, 2
 STATUS_NAMES = {0: "MHC_OK", 1: "MHC_ERR_NULL", 2: "MHC_ERR_ALIGN", 3: "MHC_ERR_SHAPE",
                 4: "MHC_ERR_UNSUPPORTED", 5: "MHC_ERR_ALIAS", 6: "MHC_ERR_CUDA",
                 7: "MHC_ERR_DEVICE_TIMEOUT", 8: "MHC_ERR_WORKSPACE"}
@@ -29,7 +31,9 @@ EXPORTS = ("mhc_weight_bytes", "mhc_prepare_weight", "mhc_post", "mhc_workspace_
            "mhc_plan", "mhc_debug_record_between", "mhc_boundary_fused_noalloc",
            "mhc_debug_rcp_check", "mhc_pre_split_k", "mhc_debug_coef_check", "mhc_plan_cluster",
            "mhc_debug_set_decode_path", "mhc_debug_set_pdl", "mhc_debug_delayed_copy",
-           "mhc_debug_launch_count")
+           "mhc_debug_launch_count", "mhc_block_norm", "mhc_block_norm_backward",
+           "mhc_block_norm_backward_workspace_bytes", "mhc_ckpt_pack", "mhc_ckpt_unpack",
+           "mhc_ckpt_linear_dw", "mhc_ckpt_linear_dw_workspace_bytes")
 
 
 class MhcError(RuntimeError):
@@ -43,6 +47,22 @@ class _Params(ctypes.Structure):
                 ("hc_post_mult", ctypes.c_float), ("sinkhorn_eps", ctypes.c_float),
                 ("norm_eps", ctypes.c_float), ("sinkhorn_iters", ctypes.c_int),
                 ("batch_invariant", ctypes.c_int)]
+
+
+class _Block(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int), ("w_post", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p), ("w_post_dtype", ctypes.c_int),
+                ("w_pre_dtype", ctypes.c_int), ("gate", ctypes.c_void_p),
+                ("gate_dtype", ctypes.c_int), ("gate_form", ctypes.c_int),
+                ("gate_act", ctypes.c_int), ("gate_stride", ctypes.c_int64),
+                ("res_scale", ctypes.c_void_p), ("scale_form", ctypes.c_int),
+                ("eps_post", ctypes.c_float), ("eps_pre", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("post_norm", ctypes.c_int)]
+
+
+class _Ckpt(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 @dataclass
@@ -75,7 +95,7 @@ def load():
                            "`python -c 'import __graft_entry__ as g; g.build()'`")
     lib = ctypes.CDLL(_LIB_PATH)
     P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-    PP = ctypes.POINTER(_Params)
+    PP, PB, PC = (ctypes.POINTER(c) for c in (_Params, _Block, _Ckpt))
     sig = {
         "mhc_weight_bytes": (sz, [i32]),
         "mhc_prepare_weight": (i32, [P, i32, P, P]),
@@ -101,6 +121,14 @@ def load():
         "mhc_debug_set_pdl": (None, [i32]),
         "mhc_debug_delayed_copy": (i32, [P, P, i64, ctypes.c_uint32, P]),
         "mhc_debug_launch_count": (ctypes.c_uint64, []),
+        "mhc_block_norm": (i32, [PB, P, i64, P, i64, P, P, P, i32, PC, PC, PC, P]),
+        "mhc_block_norm_backward_workspace_bytes": (sz, [i64, i32]),
+        "mhc_block_norm_backward": (i32, [PB, P, i64, P, i64, P, i64, P, i64, i32, PC, PC, P, P, P,
+                                          P, P, P, P, P, sz, P]),
+        "mhc_ckpt_pack": (i32, [P, i64, i32, i64, i32, i32, PC, P]),
+        "mhc_ckpt_unpack": (i32, [PC, i32, i64, i32, i32, P, P]),
+        "mhc_ckpt_linear_dw_workspace_bytes": (sz, [i64, i32, i32]),
+        "mhc_ckpt_linear_dw": (i32, [P, i64, i32, PC, i32, i64, i32, i32, P, i32, i32, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -399,3 +427,334 @@ def mhc_debug_record_between(event):
 
 def mhc_status_string(code: int) -> str:
     return load().mhc_status_string(int(code)).decode()
+
+
+# ---------------------------------------------------------------------------
+# Gated residual block, its backward pass, and 8-bit activation checkpoints
+
+_DTYPES = {torch.float32: MHC_F32, torch.bfloat16: MHC_BF16, torch.float16: MHC_F16}
+_GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = 0, 1, 2, 3
+_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
+_SCALE_NONE, _SCALE_ONE, _SCALE_CHANNEL = 0, 1, 2
+_FORMATS = {"e4m3": 1, "int8": 2}
+CKPT_GROUP = 32
+
+
+@dataclass
+class BlockParams:
+    """What shapes a gated residual block beside its tensors. gate_act: "none",
+    "sigmoid" or "tanh", applied to the gate. weight_offset is added to both
+    norms' weights (1 where they are kept as w - 1). post_norm False leaves the
+    norm of the block's output out."""
+    eps_post: float = 1e-6
+    eps_pre: float = 1e-6
+    gate_act: str = "none"
+    weight_offset: float = 0.0
+    post_norm: bool = True
+
+
+_DEFAULT_BLOCK_PARAMS = BlockParams()
+
+
+class Checkpoint:
+    """An activation [T, H] kept in 8 bits: codes [T, H] and scales
+    [T, ceil(H / 32)], uint8 and contiguous, in fmt "e4m3" or "int8"."""
+
+    __slots__ = ("codes", "scales", "fmt")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: str):
+        if fmt not in _FORMATS:
+            raise ValueError(f"checkpoint format must be one of {sorted(_FORMATS)}: got {fmt!r}")
+        for t, name in ((codes, "codes"), (scales, "scales")):
+            if t.dtype != torch.uint8 or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous 2-D CUDA uint8 tensor")
+        T, H = codes.shape
+        if tuple(scales.shape) != (T, -(-H // CKPT_GROUP)) or scales.device != codes.device:
+            raise ValueError(f"scales must be [{T}, {-(-H // CKPT_GROUP)}] on the codes' device: "
+                             f"got {tuple(scales.shape)}")
+        self.codes, self.scales, self.fmt = codes, scales, fmt
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _c(self):
+        return _Ckpt(self.codes.data_ptr(), self.scales.data_ptr())
+
+
+class BlockGrads(NamedTuple):
+    """Gradients of mhc_block_norm's inputs; None where there is no such input."""
+    d_y: torch.Tensor
+    d_residual: torch.Tensor
+    d_w_post: torch.Tensor | None
+    d_w_pre: torch.Tensor | None
+    d_gate: torch.Tensor | None
+    d_res_scale: torch.Tensor | None
+
+
+def _on(stream):
+    """Where outputs and workspaces of a call on `stream` are allocated: there."""
+    return torch.cuda.stream(stream) if stream is not None else nullcontext()
+
+
+def ckpt_empty(tokens: int, hidden: int, fmt: str = "e4m3", device="cuda") -> Checkpoint:
+    """A checkpoint to be written."""
+    return Checkpoint(torch.empty(tokens, hidden, dtype=torch.uint8, device=device),
+                      torch.empty(tokens, -(-hidden // CKPT_GROUP), dtype=torch.uint8,
+                                  device=device), fmt)
+
+
+def _matrix(t, name, T, H, dtype, device):
+    """A CUDA tensor [T, H] of `dtype` whose rows are contiguous: its row stride."""
+    if t.dtype != dtype or t.device != device or t.dim() != 2 or t.shape[0] != T \
+            or t.shape[1] != H or (H > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a [{T}, {H}] {dtype} tensor on {device} with contiguous "
+                         f"rows: got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.stride(0)
+
+
+def _whole(t, name, shape, dtype, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {shape} {dtype} tensor on {device}: got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t
+
+
+def _out(t, name, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None \
+        else _whole(t, name, shape, dtype, device)
+
+
+def _held(c, name, T, H, device):
+    if tuple(c.codes.shape) != (T, H) or c.codes.device != device:
+        raise ValueError(f"{name} must be a [{T}, {H}] checkpoint on {device}: got "
+                         f"{tuple(c.codes.shape)} on {c.codes.device}")
+    return c
+
+
+def _format(*cks):
+    """The one format of the checkpoints given (0: none given)."""
+    fmts = {c.fmt for c in cks if c is not None}
+    if len(fmts) > 1:
+        raise ValueError("the checkpoints of a call must have one format")
+    return _FORMATS[fmts.pop()] if fmts else 0
+
+
+def _weight(w, name, H, device):
+    if w is None:
+        return None, MHC_F32
+    if w.dtype not in _DTYPES or tuple(w.shape) != (H,) or not w.is_contiguous() or w.device != device:
+        raise ValueError(f"{name} must be a contiguous [{H}] float tensor on {device}: got "
+                         f"{tuple(w.shape)} {w.dtype} on {w.device}")
+    return w.data_ptr(), _DTYPES[w.dtype]
+
+
+def _block_c(T, H, dtype, r_dtype, device, w_post, w_pre, gate, res_scale, params):
+    """The C struct of a block from its tensors (the gate's and the scale's
+    forms are told by their shapes)."""
+    p = params if params is not None else _DEFAULT_BLOCK_PARAMS
+    if dtype not in _DTYPES or (r_dtype != dtype and r_dtype != torch.float32):
+        raise ValueError(f"y must be float32, bfloat16 or float16 and residual the same or "
+                         f"float32: got {dtype} and {r_dtype}")
+    wp, wpt = _weight(w_post, "w_post", H, device)
+    wq, wqt = _weight(w_pre, "w_pre", H, device)
+    form, gate_p, gate_t, gate_stride = _GATE_NONE, None, MHC_F32, 0
+    if gate is not None:
+        if gate.device != device or (gate.dtype != dtype and gate.dtype != torch.float32):
+            raise ValueError(f"gate must be {dtype} or float32 on {device}: got {gate.dtype} on "
+                             f"{gate.device}")
+        shape = tuple(gate.shape)
+        if shape == (H,) and (H == 1 or gate.stride(0) == 1):
+            form = _GATE_CHANNEL
+        elif shape == (T, 1):
+            form, gate_stride = _GATE_TOKEN, gate.stride(0)
+        elif shape == (T, H) and gate.stride(1) == 1:
+            form, gate_stride = _GATE_FULL, gate.stride(0)
+        else:
+            raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}] with contiguous rows: "
+                             f"got {shape}")
+        gate_p, gate_t = gate.data_ptr(), _DTYPES[gate.dtype]
+    if p.gate_act not in _ACTS or (gate is None and p.gate_act != "none"):
+        raise ValueError(f"gate_act must be one of {sorted(_ACTS)}, and \"none\" without a gate: "
+                         f"got {p.gate_act!r}")
+    scale_form, scale_p = _SCALE_NONE, None
+    if res_scale is not None:
+        n = res_scale.numel()
+        if res_scale.dtype != torch.float32 or res_scale.device != device or res_scale.dim() > 1 \
+                or n not in (1, H) or not res_scale.is_contiguous():
+            raise ValueError(f"res_scale must be a contiguous [1] or [{H}] float32 tensor on "
+                             f"{device}: got {tuple(res_scale.shape)} {res_scale.dtype} on "
+                             f"{res_scale.device}")
+        scale_form, scale_p = (_SCALE_ONE if n == 1 else _SCALE_CHANNEL), res_scale.data_ptr()
+    return _Block(T, H, _DTYPES[dtype], _DTYPES[r_dtype], wp, wq, wpt, wqt, gate_p, gate_t, form,
+                  _ACTS[p.gate_act], gate_stride, scale_p, scale_form, p.eps_post, p.eps_pre,
+                  p.weight_offset, int(bool(p.post_norm)))
+
+
+def _cuda_2d(t, name):
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    return t.shape[0], t.shape[1], t.device
+
+
+def _c(ck):
+    return None if ck is None else ck._c()
+
+
+def mhc_block_norm(y, residual, w_post=None, w_pre=None, gate=None, res_scale=None,
+                   params: BlockParams | None = None, *, residual_out=None, h=None, rstd=None,
+                   ckpt_y: Checkpoint | None = None, ckpt_residual: Checkpoint | None = None,
+                   ckpt_h: Checkpoint | None = None, stream=None):
+    """The gated residual block's boundary:
+
+        n = y * rstd_post * w_post
+        residual_out = res_scale * residual + act(gate) * n
+        h = residual_out * rstd_pre * w_pre
+
+    y [T, H] (float32, bfloat16 or float16) and residual [T, H] (the same or
+    float32) may be strided rows; w_post, w_pre [H]; gate [H], [T, 1] or
+    [T, H], of y's type or float32; res_scale [1] or [H] float32; each may be
+    None. ckpt_y, ckpt_residual and ckpt_h are checkpoints to write of y,
+    residual and h in the same pass. Returns (residual_out, h, rstd), rstd
+    [T, 2] being what mhc_block_norm_backward needs beside y and residual.
+    residual_out may be the residual itself."""
+    T, H, dev = _cuda_2d(y, "y")
+    ys = _matrix(y, "y", T, H, y.dtype, dev)
+    rs = _matrix(residual, "residual", T, H, residual.dtype, dev)
+    b = _block_c(T, H, y.dtype, residual.dtype, dev, w_post, w_pre, gate, res_scale, params)
+    for c, name in ((ckpt_y, "ckpt_y"), (ckpt_residual, "ckpt_residual"), (ckpt_h, "ckpt_h")):
+        if c is not None:
+            _held(c, name, T, H, dev)
+    fmt = _format(ckpt_y, ckpt_residual, ckpt_h)
+    with _on(stream):
+        residual_out = _out(residual_out, "residual_out", (T, H), residual.dtype, dev)
+        h = _out(h, "h", (T, H), y.dtype, dev)
+        rstd = _out(rstd, "rstd", (T, 2), torch.float32, dev)
+    _check(load().mhc_block_norm(b, y.data_ptr(), ys, residual.data_ptr(), rs,
+                                 residual_out.data_ptr(), h.data_ptr(), rstd.data_ptr(), fmt,
+                                 _c(ckpt_y), _c(ckpt_residual), _c(ckpt_h), _stream(stream, dev)),
+           "mhc_block_norm")
+    return residual_out, h, rstd
+
+
+def block_norm_backward_workspace_bytes(tokens: int, hidden: int) -> int:
+    return int(load().mhc_block_norm_backward_workspace_bytes(tokens, hidden))
+
+
+def mhc_block_norm_backward(d_residual_out, d_h, y, residual, rstd, w_post=None, w_pre=None,
+                            gate=None, res_scale=None, params: BlockParams | None = None, *,
+                            residual_dtype=None, d_y=None, d_residual=None, workspace=None,
+                            stream=None) -> BlockGrads:
+    """Gradients of mhc_block_norm's inputs from those of residual_out (None:
+    zero) and h. y and residual are the inputs or Checkpoints of them; rstd,
+    the weights, the gate, the scale and params as in the forward call.
+    residual_dtype (d_residual_out's, else d_h's, unless given) is needed only
+    where neither d_residual_out nor the residual itself tells it. The
+    gradients of weights, of a [H] or [T, 1] gate and of res_scale are float32;
+    d_residual may be d_residual_out itself."""
+    T, H, dev = _cuda_2d(d_h, "d_h")
+    dhs = _matrix(d_h, "d_h", T, H, d_h.dtype, dev)
+    if residual_dtype is None:
+        residual_dtype = d_residual_out.dtype if d_residual_out is not None \
+            else residual.dtype if isinstance(residual, torch.Tensor) else d_h.dtype
+    drs = 0 if d_residual_out is None else _matrix(d_residual_out, "d_residual_out", T, H,
+                                                   residual_dtype, dev)
+    b = _block_c(T, H, d_h.dtype, residual_dtype, dev, w_post, w_pre, gate, res_scale, params)
+    cy = cr = yp = rp = None
+    ys = rs = 0
+    if isinstance(y, Checkpoint):
+        cy = _held(y, "y", T, H, dev)
+    else:
+        yp, ys = y.data_ptr(), _matrix(y, "y", T, H, d_h.dtype, dev)
+    if isinstance(residual, Checkpoint):
+        cr = _held(residual, "residual", T, H, dev)
+    else:
+        rp, rs = residual.data_ptr(), _matrix(residual, "residual", T, H, residual_dtype, dev)
+    fmt = _format(cy, cr)
+    _whole(rstd, "rstd", (T, 2), torch.float32, dev)
+    need = int(load().mhc_block_norm_backward_workspace_bytes(T, H))
+    f32 = torch.float32
+    with _on(stream):
+        d_y = _out(d_y, "d_y", (T, H), d_h.dtype, dev)
+        d_residual = _out(d_residual, "d_residual", (T, H), residual_dtype, dev)
+        d_w_post = torch.empty(H, dtype=f32, device=dev) if w_post is not None else None
+        d_w_pre = torch.empty(H, dtype=f32, device=dev) if w_pre is not None else None
+        d_gate = None if gate is None else torch.empty(
+            gate.shape, dtype=gate.dtype if b.gate_form == _GATE_FULL else f32, device=dev)
+        d_scale = None if res_scale is None else torch.empty(res_scale.shape, dtype=f32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _check(load().mhc_block_norm_backward(
+        b, _p(d_residual_out), drs, d_h.data_ptr(), dhs, yp, ys, rp, rs, fmt, _c(cy), _c(cr),
+        rstd.data_ptr(), d_y.data_ptr(), d_residual.data_ptr(), _p(d_w_post), _p(d_w_pre),
+        _p(d_gate), _p(d_scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream, dev)), "mhc_block_norm_backward")
+    return BlockGrads(d_y, d_residual, d_w_post, d_w_pre, d_gate, d_scale)
+
+
+def mhc_ckpt_pack(x, fmt: str = "e4m3", *, out: Checkpoint | None = None, stream=None) -> Checkpoint:
+    """x [T, H] (float32, bfloat16 or float16, rows may be strided) kept in 8 bits."""
+    T, H, dev = _cuda_2d(x, "x")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x must be float32, bfloat16 or float16: got {x.dtype}")
+    s = _matrix(x, "x", T, H, x.dtype, dev)
+    if out is None:
+        with _on(stream):
+            out = ckpt_empty(T, H, fmt, dev)
+    elif out.fmt != fmt:
+        raise ValueError(f"out has the format {out.fmt!r}, not {fmt!r}")
+    _held(out, "out", T, H, dev)
+    _check(load().mhc_ckpt_pack(x.data_ptr(), s, _DTYPES[x.dtype], T, H, _FORMATS[fmt], out._c(),
+                                _stream(stream, dev)), "mhc_ckpt_pack")
+    return out
+
+
+def mhc_ckpt_unpack(ckpt: Checkpoint, dtype=torch.bfloat16, *, out=None, stream=None):
+    """The values [T, H] that a checkpoint stands for, in `dtype`."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16: got {dtype}")
+    T, H = ckpt.codes.shape
+    dev = ckpt.codes.device
+    with _on(stream):
+        out = _out(out, "out", (T, H), dtype, dev)
+    _check(load().mhc_ckpt_unpack(ckpt._c(), _FORMATS[ckpt.fmt], T, H, _DTYPES[dtype],
+                                  out.data_ptr(), _stream(stream, dev)), "mhc_ckpt_unpack")
+    return out
+
+
+def ckpt_linear_dw_workspace_bytes(tokens: int, n: int, k: int) -> int:
+    return int(load().mhc_ckpt_linear_dw_workspace_bytes(tokens, n, k))
+
+
+def mhc_ckpt_linear_dw(d_out, x: Checkpoint, *, d_w=None, dtype=torch.float32,
+                       accumulate: bool = False, workspace=None, stream=None):
+    """d_w [N, K] = d_out^T x, the weight gradient of out = x W^T, from d_out
+    [T, N] (bfloat16 or float16, rows may be strided) and the checkpoint of
+    x [T, K]. accumulate adds to the d_w given."""
+    T, N, dev = _cuda_2d(d_out, "d_out")
+    if d_out.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"d_out must be bfloat16 or float16: got {d_out.dtype}")
+    s = _matrix(d_out, "d_out", T, N, d_out.dtype, dev)
+    K = x.codes.shape[1]
+    _held(x, "x", T, K, dev)
+    if d_w is not None:
+        dtype = d_w.dtype
+    elif accumulate:
+        raise ValueError("accumulate needs the d_w to add to")
+    if dtype not in _DTYPES:
+        raise ValueError(f"d_w must be float32, bfloat16 or float16: got {dtype}")
+    need = int(load().mhc_ckpt_linear_dw_workspace_bytes(T, N, K))
+    with _on(stream):
+        d_w = _out(d_w, "d_w", (N, K), dtype, dev)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().mhc_ckpt_linear_dw(d_out.data_ptr(), s, _DTYPES[d_out.dtype], x._c(),
+                                     _FORMATS[x.fmt], T, N, K, d_w.data_ptr(), _DTYPES[dtype],
+                                     int(bool(accumulate)), _p(workspace), ws_bytes,
+                                     _stream(stream, dev)), "mhc_ckpt_linear_dw")
+    return d_w
