@@ -389,8 +389,12 @@ mhc_status mhc_ckpt_pack(const void *x, int64_t stride, mhc_dtype dtype, int64_t
 mhc_status mhc_ckpt_unpack(const mhc_ckpt *ckpt, mhc_ckpt_format format, int64_t tokens,
                            int hidden, mhc_dtype dtype, void *x, void *stream);
 
-/* Bytes of device scratch of mhc_ckpt_linear_dw. Needs no initialisation. */
-size_t mhc_ckpt_linear_dw_workspace_bytes(int64_t tokens, int n, int k);
+/* Bytes of device scratch of mhc_ckpt_linear_dw: x in 16 bits, the sums of
+ * tokens that are split, and, unless `aligned` (d_out is on a
+ * 16-byte boundary and its stride, at least n, a multiple of 16 bytes), d_out's
+ * rows on such boundaries. 0 when T == 0 or
+ * the call would be refused for its sizes. Needs no initialisation. */
+size_t mhc_ckpt_linear_dw_workspace_bytes(int64_t tokens, int n, int k, int aligned);
 
 /*
  * Weight gradient of a projection out = x W^T whose input was checkpointed:
@@ -398,8 +402,9 @@ size_t mhc_ckpt_linear_dw_workspace_bytes(int64_t tokens, int n, int k);
  * d_out: [T, n] of dtype (BF16 or F16), rows d_out_stride elements apart.
  * x: a checkpoint [T, k]; its values are exact in bf16 (with an F16 d_out they
  * are rounded to fp16). d_w: [n, k] contiguous, of d_w_dtype (any); products
- * and sums are fp32, rounded once. n, k in [1, 65536]. T == 0 writes zeros
- * (accumulate: leaves d_w as it is).
+ * and sums are fp32, rounded once; the order of the sums is fixed by the
+ * sizes. T < 2^31 - 64; n, k in [1, 65536]. T == 0 writes zeros (accumulate:
+ * leaves d_w as it is).
  */
 mhc_status mhc_ckpt_linear_dw(const void *d_out, int64_t d_out_stride, mhc_dtype dtype,
                               const mhc_ckpt *x, mhc_ckpt_format format, int64_t tokens, int n,

@@ -120,6 +120,9 @@ bool form_spans(const mhc_block *b, Span out[4]) {
     return true;
 }
 
+// Tokens of a weight gradient at most: what a box's 32-bit row coordinate reaches.
+constexpr int64_t kDwMaxTokens = (int64_t(1) << 31) - 64;
+
 bool ckpt_ok(const mhc_ckpt *c) { return c->codes && c->scales; }
 
 }  // namespace
@@ -311,11 +314,10 @@ mhc_status mhc_ckpt_unpack(const mhc_ckpt *ckpt, mhc_ckpt_format format, int64_t
         launch_ckpt_unpack(a, dtype, format, sms, pdl_enabled(), static_cast<cudaStream_t>(stream))));
 }
 
-size_t mhc_ckpt_linear_dw_workspace_bytes(int64_t tokens, int n, int k) {
-    (void)tokens;
-    (void)n;
-    (void)k;
-    return 0;
+size_t mhc_ckpt_linear_dw_workspace_bytes(int64_t tokens, int n, int k, int aligned) {
+    if (tokens <= 0 || n < 1 || n > kBlockMaxHidden || k < 1 || k > kBlockMaxHidden || tokens > kDwMaxTokens)
+        return 0;
+    return dw_workspace(tokens, n, k, aligned != 0);
 }
 
 mhc_status mhc_ckpt_linear_dw(const void *d_out, int64_t d_out_stride, mhc_dtype dtype, const mhc_ckpt *x,
@@ -325,11 +327,12 @@ mhc_status mhc_ckpt_linear_dw(const void *d_out, int64_t d_out_stride, mhc_dtype
     if (tokens < 0 || d_out_stride < 0 || !dtype_ok(d_w_dtype) || !format_ok(format)) return MHC_ERR_SHAPE;
     if (n < 1 || n > kBlockMaxHidden || k < 1 || k > kBlockMaxHidden) return MHC_ERR_UNSUPPORTED;
     if (dtype != MHC_BF16 && dtype != MHC_F16) return MHC_ERR_UNSUPPORTED;
-    if (!size_fits(tokens, n) || !size_fits(tokens, k)) return MHC_ERR_SHAPE;
+    if (tokens > kDwMaxTokens) return MHC_ERR_UNSUPPORTED;
     if (!d_w) return MHC_ERR_NULL;
     if (tokens > 0 && (!d_out || !x || !ckpt_ok(x))) return MHC_ERR_NULL;
     if (!aligned(d_out, 2) || !aligned(d_w, size_of(d_w_dtype)) || !aligned(workspace, 16)) return MHC_ERR_ALIGN;
-    const size_t need = mhc_ckpt_linear_dw_workspace_bytes(tokens, n, k);
+    const bool rows16 = dw_rows_aligned(d_out, d_out_stride, tokens, n);
+    const size_t need = mhc_ckpt_linear_dw_workspace_bytes(tokens, n, k, rows16);
     if (need && !workspace) return MHC_ERR_NULL;
     if (workspace_bytes < need) return MHC_ERR_WORKSPACE;
     Span ins[3] = {};
@@ -342,7 +345,8 @@ mhc_status mhc_ckpt_linear_dw(const void *d_out, int64_t d_out_stride, mhc_dtype
     if (aliased(outs, 2, ins, 3, -1, -1)) return MHC_ERR_ALIAS;
     if (tokens == 0 && accumulate) return MHC_OK;
     int sms = 0;
-    if (int s = require_device(&sms, nullptr)) return static_cast<mhc_status>(s);
+    unsigned int *status = nullptr;
+    if (int s = require_device(&sms, &status)) return static_cast<mhc_status>(s);
     DwArgs a = {};
     a.d_out = d_out;
     a.d_out_stride = d_out_stride;
@@ -355,7 +359,9 @@ mhc_status mhc_ckpt_linear_dw(const void *d_out, int64_t d_out_stride, mhc_dtype
     a.d_w = d_w;
     a.d_w_dtype = d_w_dtype;
     a.accumulate = accumulate != 0;
-    return static_cast<mhc_status>(note_launch(launch_dw(a, pdl_enabled(), static_cast<cudaStream_t>(stream))));
+    a.workspace = workspace;
+    return static_cast<mhc_status>(
+        launch_dw(a, rows16, sms, status, pdl_enabled(), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -99,7 +99,12 @@ struct DwArgs {
     int n, k;
     void *d_w;
     int d_w_dtype, accumulate;
+    void *workspace;
 };
-cudaError_t launch_dw(const DwArgs &a, bool pdl, cudaStream_t s);
+// Whether the rows of d_out lie apart and on 16-byte boundaries (else they are copied there first).
+bool dw_rows_aligned(const void *d_out, long long stride, long long T, int n);
+size_t dw_workspace(long long T, int n, int k, bool d_aligned);
+// An mhc_status: several launches, each counted.
+int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bool pdl, cudaStream_t s);
 
 }  // namespace mhc

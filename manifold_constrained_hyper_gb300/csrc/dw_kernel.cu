@@ -1,56 +1,465 @@
-// Weight gradient of a projection from its checkpointed input:
-// d_w[i][j] = sum_t d_out[t][i] * x[t][j].
+// Weight gradient of a projection from its checkpointed input,
+// d_w[i][j] = sum_t d_out[t][i] * x[t][j], on the 5th-generation tensor cores.
+//
+// The checkpoint's values are exact in bf16, so a first kernel writes them
+// out in 16 bits (3 bytes of traffic a value) and the product runs on plain
+// 16-bit operands: unpacking them inside it would convert every value once
+// per 256 rows of d_w, and pass it twice more through shared memory, which
+// the operands' own traffic already fills.
+//
+// Both operands lie with the long axis (tokens) outermost, so a box of 64
+// columns x 64 tokens lands in shared memory as 64 rows of 128 bytes and the
+// MMA reads both "transposed" (the M and N axes contiguous). A pair of CTAs
+// (cta_group::2) forms a 256 x 256 tile of d_w: each holds 128 columns of
+// d_out and 128 of x per step of 64 tokens (32 KB, six steps in flight), and
+// its half of the sums in tensor memory, in two buffers, so that the
+// epilogue of one tile runs under the next tile's products. Where there are
+// too few tiles for the machine the tokens are split, and a second kernel
+// adds the splits in their order.
+#include <atomic>
+
 #include "block_common.cuh"
+#include "mhc_internal.h"
 
 namespace mhc {
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+constexpr int kTile = 256;                          // of d_w, either way, by a pair of CTAs
+constexpr int kHalf = kTile / 2;                    // what one CTA loads of either operand
+constexpr int kStep = 64;                           // tokens per pipeline stage
+constexpr int kBoxBytes = kStep * 128;              // 64 columns x 64 tokens, 16 bits
+constexpr int kStageBytes = 4 * kBoxBytes;          // two boxes of either operand
+constexpr int kStages = 6;
+constexpr int kThreads = 192;                       // loads, products, four warps of epilogue
+constexpr int kBars = 2 * kStages + 5;
+constexpr int kSmem = kStages * kStageBytes + 1024 /* alignment */ + 256 /* barriers */;
+constexpr int kTmemCols = 512;
+constexpr int kBand = 8;                            // rows of tiles that are walked together
 
-// 64 x 64 outputs a CTA, 4 x 4 a thread, 16 tokens a step.
-__global__ void __launch_bounds__(256) dw_tile_kernel(const DwArgs a) {
-    __shared__ float sd[kStep][kTile], sx[kStep][kTile];
-    griddep_wait();
-    const int tiles_k = (a.k + kTile - 1) / kTile, groups = (a.k + 31) / 32;
-    const int i0 = static_cast<int>(blockIdx.x / tiles_k) * kTile, j0 = static_cast<int>(blockIdx.x % tiles_k) * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (long long t0 = 0; t0 < a.T; t0 += kStep) {
-        for (int e = threadIdx.x; e < kStep * kTile; e += 256) {
-            const long long t = t0 + e / kTile;
-            const int i = i0 + e % kTile, j = j0 + e % kTile;
-            sd[e / kTile][e % kTile] = t < a.T && i < a.n ? load_any(a.d_out, a.dtype, t * a.d_out_stride + i) : 0.f;
-            float x = t < a.T && j < a.k ? ckpt_load(a.x, a.format, t, a.k, groups, j) : 0.f;
-            if (a.dtype == MHC_F16) x = to_f32(from_f32<__half>(x));
-            sx[e / kTile][e % kTile] = x;
+enum DwSite : int { SITE_DW_EMPTY = 60, SITE_DW_FULL, SITE_DW_ACC_EMPTY, SITE_DW_ACC_FULL, SITE_DW_DRAIN };
+
+struct GemmArgs {
+    long long T;
+    int n, k;
+    int tiles_n, tiles_k, splits, steps_per_split, steps;
+    int f16;                        // operands fp16, else bf16
+    void *out;                      // d_w, or the splits' fp32 sums [splits][n][k]
+    int out_dtype, accumulate, wide;    // wide: rows of out lie on 32-byte boundaries
+    unsigned int *status;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ void dw_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t dw_cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t dw_map_to_rank(uint32_t addr, uint32_t rank) {
+    uint32_t d;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ void arrive_at_rank(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// A box into this CTA's shared memory, its bytes counted at a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m, int c0, int c1,
+                                              uint32_t cluster_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
+        ::"r"(d_tmem), "l"(ad), "l"(bd), "r"(idesc), "r"(add) : "memory");
+}
+// Arrive at `bar` in both CTAs when every product issued so far is done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+// Columns contiguous, 128-byte rows in the 128-byte swizzle: 8 tokens an
+// atom of 1024 bytes, the next 64 columns a box further on.
+__device__ __forceinline__ uint64_t desc_columns(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, int dtype) {
+    if (dtype == MHC_BF16) return bf2_pack_rn(f2_pack(a, b));
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Columns [j, j + 32) of one row of out, `row` its first element.
+__device__ __forceinline__ void store_row(const GemmArgs &a, long long row, int j, const uint32_t (&v)[32]) {
+    if (a.wide) {
+        // k is a multiple of 8 here: groups of 8 columns are in or out as a whole
+        if (a.out_dtype == MHC_F32) {
+            float *p = static_cast<float *>(a.out) + row + j;
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                if (j + c >= a.k) break;
+                uint4 lo = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                uint4 hi = make_uint4(v[c + 4], v[c + 5], v[c + 6], v[c + 7]);
+                if (a.accumulate) {
+                    float *const o[8] = {reinterpret_cast<float *>(&lo.x), reinterpret_cast<float *>(&lo.y),
+                                         reinterpret_cast<float *>(&lo.z), reinterpret_cast<float *>(&lo.w),
+                                         reinterpret_cast<float *>(&hi.x), reinterpret_cast<float *>(&hi.y),
+                                         reinterpret_cast<float *>(&hi.z), reinterpret_cast<float *>(&hi.w)};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) *o[e] += p[c + e];
+                }
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                             ::"l"(reinterpret_cast<uint64_t>(p + c)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
+                               "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+            }
+        } else {
+            uint16_t *p = static_cast<uint16_t *>(a.out) + row + j;
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                if (j + c >= a.k) break;
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = __uint_as_float(v[c + 2 * e]), y = __uint_as_float(v[c + 2 * e + 1]);
+                    if (a.accumulate) {
+                        x += load_any(p, a.out_dtype, c + 2 * e);
+                        y += load_any(p, a.out_dtype, c + 2 * e + 1);
+                    }
+                    w[e] = pack16(x, y, a.out_dtype);
+                }
+                *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    acc[r][c] = fmaf(sd[k][ty * 4 + r], sx[k][tx + 16 * c], acc[r][c]);
-        __syncthreads();
+        return;
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int i = i0 + ty * 4 + r, j = j0 + tx + 16 * c;
-            if (i >= a.n || j >= a.k) continue;
-            const long long at = static_cast<long long>(i) * a.k + j;
-            const float v = a.accumulate ? load_any(a.d_w, a.d_w_dtype, at) + acc[r][c] : acc[r][c];
-            store_any(a.d_w, a.d_w_dtype, at, v);
+    for (int c = 0; c < 32; ++c) {
+        if (j + c >= a.k) break;
+        float x = __uint_as_float(v[c]);
+        if (a.accumulate) x += load_any(a.out, a.out_dtype, row + j + c);
+        store_any(a.out, a.out_dtype, row + j + c, x);
+    }
+}
+
+// Work item -> tile row, tile column, split. Tiles are walked in bands of
+// kBand rows, so that the tiles in flight share columns of both operands in L2.
+__device__ __forceinline__ void item_place(const GemmArgs &a, int item, int *ti, int *tj, int *split) {
+    const int tiles = a.tiles_n * a.tiles_k;
+    *split = item / tiles;
+    const int r = item - *split * tiles;
+    const int band = r / (kBand * a.tiles_k), first = band * kBand;
+    const int rows = a.tiles_n - first < kBand ? a.tiles_n - first : kBand;
+    const int q = r - band * kBand * a.tiles_k;
+    *tj = q / rows;
+    *ti = first + q - *tj * rows;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant__ CUtensorMap map_x,
+               const GemmArgs a) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    uint8_t *const basep = raw + (base - smem_addr(raw));
+    const uint32_t bars = base + kStages * kStageBytes;
+    const uint32_t full = bars, empty = bars + 8 * kStages, acc_full = bars + 16 * kStages,
+                   acc_empty = acc_full + 16, drain = acc_full + 32;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + kStages * kStageBytes + 8 * kBars);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = dw_cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int items = a.tiles_n * a.tiles_k * a.splits;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + 8 * s, 1);             // the leader's: its own announcement of both CTAs' bytes
+            mbar_init(empty + 8 * s, 1);
         }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full + 8 * b, 1);
+            mbar_init(acc_empty + 8 * b, 8);        // the leader's: four warps of either CTA
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&map_d);
+        tma_prefetch_desc(&map_x);
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(tmem_slot)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    dw_cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------ loads, either CTA its halves
+        uint32_t it = 0;
+        bool ok = true;
+        for (int item = pair; item < items && ok; item += pairs) {
+            int ti, tj, split;
+            item_place(a, item, &ti, &tj, &split);
+            const int s0 = split * a.steps_per_split;
+            const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
+            const int ci = ti * kTile + static_cast<int>(rank) * kHalf, cj = tj * kTile + static_cast<int>(rank) * kHalf;
+            for (int st = s0; st < s1; ++st, ++it) {
+                const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+                if (!mbar_wait(empty + 8 * s, ph ^ 1, abort_flag, a.timeout_ns, a.status, SITE_DW_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kStageBytes);
+                const uint32_t bar = dw_map_to_rank(full + 8 * s, 0), dst = base + s * kStageBytes;
+                const int t = st * kStep;
+                tma_load_pair(dst, &map_d, ci, t, bar);
+                tma_load_pair(dst + kBoxBytes, &map_d, ci + 64, t, bar);
+                tma_load_pair(dst + 2 * kBoxBytes, &map_x, cj, t, bar);
+                tma_load_pair(dst + 3 * kBoxBytes, &map_x, cj + 64, t, bar);
+            }
+        }
+        // every stage's last release has arrived before this CTA may exit
+        for (uint32_t k = it > kStages ? it - kStages : 0; k < it && ok; ++k)
+            ok = mbar_wait(empty + 8 * (k % kStages), (k / kStages) & 1, abort_flag, a.timeout_ns, a.status,
+                           SITE_DW_EMPTY);
+        if (!ok && rank == 0) {
+            // gave up: both CTAs' copies still in flight land before they exit
+            int gave_up = 0;
+            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
+                mbar_wait(full + 8 * (k % kStages), (k / kStages) & 1, &gave_up, a.timeout_ns, a.status, SITE_DW_DRAIN);
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ------------------------------------------------ products, the leader for both
+        const uint32_t fmt = a.f16 ? 0u : 1u;
+        const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | (1u << 16) |
+                               (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+        uint32_t it = 0, done = 0;
+        bool ok = true;
+        for (int item = pair; item < items && ok; item += pairs, ++done) {
+            int ti, tj, split;
+            item_place(a, item, &ti, &tj, &split);
+            const int s0 = split * a.steps_per_split;
+            const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
+            const uint32_t buf = done & 1, acc = tmem + buf * kTile;
+            if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status,
+                           SITE_DW_ACC_EMPTY)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            for (int st = s0; st < s1; ++st, ++it) {
+                const uint32_t s = it % kStages;
+                if (!mbar_wait(full + 8 * s, (it / kStages) & 1, abort_flag, a.timeout_ns, a.status, SITE_DW_FULL)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = base + s * kStageBytes, sb = sa + 2 * kBoxBytes;
+#pragma unroll
+                for (int q = 0; q < kStep / 16; ++q)
+                    mma_pair(acc, desc_columns(sa + q * 2048), desc_columns(sb + q * 2048), idesc, st > s0 || q > 0);
+                commit_pair(empty + 8 * s);
+            }
+            if (ok) commit_pair(acc_full + 8 * buf);
+        }
+        if (!ok) {
+            // the products issued end before tensor memory is freed
+            int gave_up = 0;
+            commit_pair(drain);
+            mbar_wait(drain, 0, &gave_up, a.timeout_ns, a.status, SITE_DW_DRAIN);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------ epilogue, either CTA its 128 rows
+        const int quad = warp & 3;                  // the tensor-memory lanes this warp may read
+        uint32_t done = 0;
+        for (int item = pair; item < items; item += pairs, ++done) {
+            int ti, tj, split;
+            item_place(a, item, &ti, &tj, &split);
+            const uint32_t buf = done & 1;
+            const bool ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, a.timeout_ns, a.status,
+                                      SITE_DW_ACC_FULL);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int i = ti * kTile + static_cast<int>(rank) * kHalf + quad * 32 + lane;
+            const long long row = (static_cast<long long>(split) * a.n + i) * a.k;
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+                const int j = tj * kTile + c;
+                if (j >= a.k) break;
+                uint32_t v[32];
+                tmem_ld32(tmem + buf * kTile + c + (static_cast<uint32_t>(quad * 32) << 16), v);
+                tmem_ld_wait();
+                if (i < a.n) store_row(a, row, j, v);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at_rank(dw_map_to_rank(acc_empty + 8 * buf, 0));
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    dw_cluster_sync();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// d_w from the splits' sums, in their order (none: zeros).
+__global__ void __launch_bounds__(256) dw_join_kernel(const float *parts, int splits, long long count, void *d_w,
+                                                      int dtype, int accumulate) {
+    griddep_wait();
+    const long long step = static_cast<long long>(gridDim.x) * 256;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < count; i += step) {
+        float v = 0.f;
+        for (int s = 0; s < splits; ++s) v += parts[s * count + i];
+        store_any(d_w, dtype, i, accumulate ? load_any(d_w, dtype, i) + v : v);
+    }
+}
+
+// Rows of d_out that no 16-byte load reaches, onto 16-byte boundaries.
+__global__ void __launch_bounds__(256) dw_align_kernel(const uint16_t *src, long long stride, uint16_t *dst,
+                                                       long long pitch, long long T, int n) {
+    griddep_wait();
+    for (long long t = blockIdx.x; t < T; t += gridDim.x)
+        for (int i = threadIdx.x; i < n; i += 256) dst[t * pitch + i] = src[t * stride + i];
+}
+
+std::atomic<int> g_dw_smem[64];
+
+long long pitch16(int w) { return (w + 7) / 8 * 8; }
+size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+// How a call runs: the splits of the tokens and the workspace's parts.
+struct DwPlan {
+    int tiles_n, tiles_k, steps, splits, steps_per_split;
+    size_t x_bytes, d_bytes, part_bytes;
+};
+
+// Splits: with fewer tiles than pairs of CTAs, as many as give every pair an
+// item of at least 8 steps (512 tokens).
+DwPlan dw_plan(long long T, int n, int k, bool d_aligned) {
+    DwPlan p;
+    p.tiles_n = (n + kTile - 1) / kTile;
+    p.tiles_k = (k + kTile - 1) / kTile;
+    p.steps = static_cast<int>((T + kStep - 1) / kStep);
+    const long long tiles = static_cast<long long>(p.tiles_n) * p.tiles_k;
+    long long s = (kGridCap / 2) / tiles;
+    if (s > p.steps / 8) s = p.steps / 8;
+    if (s < 1) s = 1;
+    p.steps_per_split = p.steps ? static_cast<int>((p.steps + s - 1) / s) : 0;
+    p.splits = p.steps ? (p.steps + p.steps_per_split - 1) / p.steps_per_split : 0;
+    p.x_bytes = up256(static_cast<size_t>(T) * pitch16(k) * 2);
+    p.d_bytes = d_aligned ? 0 : up256(static_cast<size_t>(T) * pitch16(n) * 2);
+    p.part_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * n * k * 4 : 0;
+    return p;
 }
 
 }  // namespace
 
-cudaError_t launch_dw(const DwArgs &a, bool pdl, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>((a.n + kTile - 1) / kTile) * static_cast<unsigned>((a.k + kTile - 1) / kTile);
-    return launch_block_kernel(dw_tile_kernel, grid, 256, 0, pdl, s, a);
+bool dw_rows_aligned(const void *d_out, long long stride, long long T, int n) {
+    return (reinterpret_cast<uintptr_t>(d_out) & 15u) == 0 &&
+           (T == 1 || (stride % 8 == 0 && stride >= n && stride < (1ll << 38)));
+}
+
+size_t dw_workspace(long long T, int n, int k, bool d_aligned) {
+    if (T == 0) return 0;
+    const DwPlan p = dw_plan(T, n, k, d_aligned);
+    return p.x_bytes + p.d_bytes + p.part_bytes;
+}
+
+int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
+    const DwPlan p = dw_plan(a.T, a.n, a.k, d_aligned);
+    const long long count = static_cast<long long>(a.n) * a.k;
+    const long long join_blocks = (count + 1023) / 1024, join_cap = static_cast<long long>(sms) * 16;
+    const unsigned join_grid = static_cast<unsigned>(join_blocks < join_cap ? join_blocks : join_cap);
+    if (p.steps == 0)
+        return note_launch(launch_block_kernel(dw_join_kernel, join_grid, 256, 0, pdl, s,
+                                               static_cast<const float *>(nullptr), 0, count, a.d_w, a.d_w_dtype, 0));
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    void *const x16 = ws;
+    void *const d16 = ws + p.x_bytes;
+    float *const parts = reinterpret_cast<float *>(ws + p.x_bytes + p.d_bytes);
+    const long long xp = pitch16(a.k), dp = d_aligned ? (a.T == 1 ? pitch16(a.n) : a.d_out_stride) : pitch16(a.n);
+    const CkptArgs u = {nullptr, x16, xp, a.T, a.k, a.x};
+    if (int e = note_launch(launch_ckpt_unpack(u, a.dtype, a.format, sms, pdl, s))) return e;
+    if (!d_aligned) {
+        const long long cap = static_cast<long long>(sms) * 8;
+        if (int e = note_launch(launch_block_kernel(
+                dw_align_kernel, static_cast<unsigned>(a.T < cap ? a.T : cap), 256, 0, pdl, s,
+                static_cast<const uint16_t *>(a.d_out), a.d_out_stride, static_cast<uint16_t *>(d16), dp, a.T, a.n)))
+            return e;
+    }
+    CUtensorMap md, mx;
+    if (!encode_rows16(&md, a.dtype == MHC_BF16, d_aligned ? a.d_out : d16, a.n, a.T, dp * 2, kStep) ||
+        !encode_rows16(&mx, a.dtype == MHC_BF16, x16, a.k, a.T, xp * 2, kStep))
+        return MHC_ERR_CUDA;
+    GemmArgs g = {};
+    g.T = a.T;
+    g.n = a.n;
+    g.k = a.k;
+    g.tiles_n = p.tiles_n;
+    g.tiles_k = p.tiles_k;
+    g.splits = p.splits;
+    g.steps_per_split = p.steps_per_split;
+    g.steps = p.steps;
+    g.f16 = a.dtype == MHC_F16;
+    g.out = p.splits > 1 ? static_cast<void *>(parts) : a.d_w;
+    g.out_dtype = p.splits > 1 ? MHC_F32 : a.d_w_dtype;
+    g.accumulate = p.splits > 1 ? 0 : a.accumulate;
+    g.wide = a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
+    g.status = status;
+    g.timeout_ns = wait_timeout_ns();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
+    if (!g_dw_smem[dev & 63].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(dw_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+            return MHC_ERR_CUDA;
+        g_dw_smem[dev & 63].store(1, std::memory_order_release);
+    }
+    const long long items = static_cast<long long>(p.tiles_n) * p.tiles_k * p.splits, pairs = sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(items < pairs ? items : pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    if (int e = note_launch(cudaLaunchKernelEx(&cfg, dw_gemm_kernel, md, mx, g))) return e;
+    if (p.splits == 1) return MHC_OK;
+    return note_launch(launch_block_kernel(dw_join_kernel, join_grid, 256, 0, pdl, s, static_cast<const float *>(parts),
+                                           p.splits, count, a.d_w, a.d_w_dtype, a.accumulate));
 }
 
 }  // namespace mhc

@@ -127,7 +127,7 @@ def load():
                                           P, P, P, P, P, sz, P]),
         "mhc_ckpt_pack": (i32, [P, i64, i32, i64, i32, i32, PC, P]),
         "mhc_ckpt_unpack": (i32, [PC, i32, i64, i32, i32, P, P]),
-        "mhc_ckpt_linear_dw_workspace_bytes": (sz, [i64, i32, i32]),
+        "mhc_ckpt_linear_dw_workspace_bytes": (sz, [i64, i32, i32, i32]),
         "mhc_ckpt_linear_dw": (i32, [P, i64, i32, PC, i32, i64, i32, i32, P, i32, i32, P, sz, P]),
     }
     for name, (res, args) in sig.items():
@@ -726,8 +726,9 @@ def mhc_ckpt_unpack(ckpt: Checkpoint, dtype=torch.bfloat16, *, out=None, stream=
     return out
 
 
-def ckpt_linear_dw_workspace_bytes(tokens: int, n: int, k: int) -> int:
-    return int(load().mhc_ckpt_linear_dw_workspace_bytes(tokens, n, k))
+def ckpt_linear_dw_workspace_bytes(tokens: int, n: int, k: int, aligned: bool = True) -> int:
+    """aligned: d_out's address and row stride (at least n) are multiples of 16 bytes."""
+    return int(load().mhc_ckpt_linear_dw_workspace_bytes(tokens, n, k, int(aligned)))
 
 
 def mhc_ckpt_linear_dw(d_out, x: Checkpoint, *, d_w=None, dtype=torch.float32,
@@ -747,7 +748,8 @@ def mhc_ckpt_linear_dw(d_out, x: Checkpoint, *, d_w=None, dtype=torch.float32,
         raise ValueError("accumulate needs the d_w to add to")
     if dtype not in _DTYPES:
         raise ValueError(f"d_w must be float32, bfloat16 or float16: got {dtype}")
-    need = int(load().mhc_ckpt_linear_dw_workspace_bytes(T, N, K))
+    aligned = d_out.data_ptr() % 16 == 0 and ((s % 8 == 0 and N <= s < 1 << 38) or T == 1)
+    need = int(load().mhc_ckpt_linear_dw_workspace_bytes(T, N, K, aligned))
     with _on(stream):
         d_w = _out(d_w, "d_w", (N, K), dtype, dev)
         if workspace is None and need:

@@ -183,6 +183,14 @@ def test_weight_gradient_of_strided_rows(pad, offset):
     _check_dw(150, 200, 96, BF, "e4m3", FP32, pad, offset)
 
 
+def test_weight_gradient_of_one_row_for_every_token():
+    d = torch.randn(1, 136, device="cuda").to(BF).expand(70, 136)
+    c = ops.mhc_ckpt_pack(torch.randn(70, 264, device="cuda"), "int8")
+    x = ref.unpack(c.codes, c.scales, "int8")
+    want = d.double().t() @ x
+    within(ops.mhc_ckpt_linear_dw(d, c), want, _dw_bound(d.double(), x, 70, FP32, want), "d_w")
+
+
 @pytest.mark.parametrize("out", list(TYPES))
 @pytest.mark.parametrize("N,K", [(130, 288), (67, 51)])
 def test_weight_gradient_added_to_what_is_there(out, N, K):
