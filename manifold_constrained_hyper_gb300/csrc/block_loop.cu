@@ -202,7 +202,7 @@ cudaError_t bwd_loop(const BlockBwdArgs &a, bool pdl, int *parts, cudaStream_t s
 
 }  // namespace
 
-cudaError_t launch_block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bool pdl,
+cudaError_t launch_block_fwd_loop(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bool pdl,
                              cudaStream_t s) {
     if (dtype == MHC_F32) return fwd_loop<float, float>(a, sms, pdl, s);
     if (dtype == MHC_BF16)
