@@ -259,7 +259,6 @@ mhc_status mhc_block_norm_backward(const mhc_block *block, const void *d_residua
         a.d_gate = block->gate_form == MHC_GATE_CHANNEL ? nullptr : d_gate;
         a.sums = sums;
         a.scale_sums = sums + most * kBackSums * static_cast<size_t>(H);
-        a.want_scale = d_res_scale != nullptr;
         if (int s = note_launch(launch_block_bwd(a, block->dtype, block->residual_dtype, sms, pdl_enabled(),
                                                  &parts, st)))
             return static_cast<mhc_status>(s);

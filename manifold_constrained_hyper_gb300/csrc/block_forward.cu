@@ -15,6 +15,7 @@ cudaError_t launch_block_fwd_loop(const BlockFwdArgs &a, int dtype, int r_dtype,
 namespace {
 
 constexpr int kMaxStages = 4;
+constexpr size_t kSmemMost = 224 * 1024;            // dynamic, of an SM
 enum FwdSite : int { SITE_FWD_ROW = 70 };
 
 struct FwdRing {
@@ -230,7 +231,7 @@ cudaError_t fwd_rows_by(const BlockFwdArgs &a, int sms, bool pdl, cudaStream_t s
         ring.y_bytes = f.H * sizeof(TY);
         ring.r_bytes = f.H * sizeof(TR);
         ring.g_bytes = f.gate_form == MHC_GATE_FULL ? f.H * elem_bytes(f.gate_dtype) : 0;
-        const size_t bytes = ring.y_bytes + ring.r_bytes + ring.g_bytes, most = 224 * 1024;
+        const size_t bytes = ring.y_bytes + ring.r_bytes + ring.g_bytes, most = kSmemMost;
         while (per_sm > 1 && most / per_sm < 2 * bytes + 1536) --per_sm;
         long long stages = static_cast<long long>((most / per_sm - 1536) / bytes);
         ring.stages = static_cast<int>(stages < 1 ? 1 : stages > kMaxStages ? kMaxStages : stages);
@@ -240,7 +241,7 @@ cudaError_t fwd_rows_by(const BlockFwdArgs &a, int sms, bool pdl, cudaStream_t s
         if (require_device(&n, &status)) return cudaErrorUnknown;
         ring.status = status;
         ring.timeout_ns = wait_timeout_ns();
-        if (cudaError_t e = grant_smem(block_fwd_kernel<TY, TR, MODE, COLS>, grant, smem)) return e;
+        if (cudaError_t e = grant_smem(block_fwd_kernel<TY, TR, MODE, COLS>, grant, smem, kSmemMost)) return e;
     }
     const long long cap = static_cast<long long>(sms) * per_sm;
     return launch_block_kernel(block_fwd_kernel<TY, TR, MODE, COLS>, static_cast<unsigned>(f.T < cap ? f.T : cap), threads,

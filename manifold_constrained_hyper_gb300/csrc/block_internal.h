@@ -58,7 +58,6 @@ struct BlockBwdArgs {
     void *d_y, *d_r;
     void *d_gate;                                   // written here for TOKEN and FULL
     float *sums, *scale_sums;
-    int want_scale;                                 // d_res_scale is wanted
 };
 
 struct BlockSumArgs {

@@ -1,6 +1,7 @@
-// The gated residual block and its backward pass for any width, stride and
-// alignment: one CTA per row, a warp per group of 32 columns, each pass over
-// the row reading it again (from L1 or L2 after the first).
+// The gated residual block and its backward pass for rows too wide for
+// registers (above 16384 and 8192 columns): one CTA per row, a warp per group
+// of 32 columns, each pass over the row reading it again (from L1 or L2 after
+// the first). Any stride and alignment.
 #include "block_common.cuh"
 
 namespace mhc {
@@ -155,37 +156,6 @@ __global__ void block_bwd_loop_kernel(const BlockBwdArgs a) {
     if (threadIdx.x == 0) a.scale_sums[blockIdx.x] = s[0];
 }
 
-// Sums over the row kernel's CTAs, in their order: thread per column.
-__global__ void block_sums_kernel(const BlockSumArgs a) {
-    griddep_wait();
-    const BlockForm &f = a.f;
-    const int H = f.H, i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < H) {
-        float v[kBackSums] = {0.f, 0.f, 0.f};
-        for (int p = 0; p < a.parts; ++p)
-#pragma unroll
-            for (int k = 0; k < kBackSums; ++k)
-                if (k < 2 || f.scale_form == MHC_SCALE_CHANNEL)
-                    v[k] += a.sums[(static_cast<long long>(p) * kBackSums + k) * H + i];
-        float g = 1.f, slope = 1.f;
-        if (f.gate_form == MHC_GATE_CHANNEL) {
-            const float z = load_any(f.gate, f.gate_dtype, i);
-            g = gate_value(z, f.gate_act);
-            slope = gate_slope(z, g, f.gate_act);
-        }
-        if (a.d_w_post) a.d_w_post[i] = g * v[0];
-        if (a.d_gate)
-            a.d_gate[i] = slope * weight_at(f.w_post, f.w_post_dtype, f.weight_offset, i) * v[0];
-        if (a.d_w_pre) a.d_w_pre[i] = v[1];
-        if (a.d_res_scale && f.scale_form == MHC_SCALE_CHANNEL) a.d_res_scale[i] = v[2];
-    }
-    if (i == 0 && a.d_res_scale && f.scale_form == MHC_SCALE_ONE) {
-        float v = 0.f;
-        for (int p = 0; p < a.parts; ++p) v += a.scale_sums[p];
-        a.d_res_scale[0] = v;
-    }
-}
-
 unsigned loop_threads(int H) { return H <= 256 ? 64 : H <= 2048 ? 256 : 512; }
 
 template <class TY, class TR>
@@ -203,7 +173,7 @@ cudaError_t bwd_loop(const BlockBwdArgs &a, bool pdl, int *parts, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_block_fwd_loop(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bool pdl,
-                             cudaStream_t s) {
+                                  cudaStream_t s) {
     if (dtype == MHC_F32) return fwd_loop<float, float>(a, sms, pdl, s);
     if (dtype == MHC_BF16)
         return r_dtype == MHC_F32 ? fwd_loop<__nv_bfloat16, float>(a, sms, pdl, s)
@@ -212,18 +182,14 @@ cudaError_t launch_block_fwd_loop(const BlockFwdArgs &a, int dtype, int r_dtype,
                               : fwd_loop<__half, __half>(a, sms, pdl, s);
 }
 
-cudaError_t launch_block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bool pdl,
-                             int *parts, cudaStream_t s) {
+cudaError_t launch_block_bwd_loop(const BlockBwdArgs &a, int dtype, int r_dtype, bool pdl,
+                                  int *parts, cudaStream_t s) {
     if (dtype == MHC_F32) return bwd_loop<float, float>(a, pdl, parts, s);
     if (dtype == MHC_BF16)
         return r_dtype == MHC_F32 ? bwd_loop<__nv_bfloat16, float>(a, pdl, parts, s)
                                   : bwd_loop<__nv_bfloat16, __nv_bfloat16>(a, pdl, parts, s);
     return r_dtype == MHC_F32 ? bwd_loop<__half, float>(a, pdl, parts, s)
                               : bwd_loop<__half, __half>(a, pdl, parts, s);
-}
-
-cudaError_t launch_block_sums(const BlockSumArgs &a, bool pdl, cudaStream_t s) {
-    return launch_block_kernel(block_sums_kernel, (a.f.H + 127) / 128, 128, 0, pdl, s, a);
 }
 
 }  // namespace mhc

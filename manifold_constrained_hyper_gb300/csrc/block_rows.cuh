@@ -97,19 +97,18 @@ inline bool params16(const BlockForm &f) {
     return true;
 }
 
-// Opts a kernel in to `smem` bytes of dynamic shared memory, once per device.
+// Opts a kernel in to `smem` bytes of dynamic shared memory (all of its calls: at most `most`), once per device.
 struct SmemGrant {
     std::atomic<int> bytes[64];
 };
 template <class K>
-inline cudaError_t grant_smem(K kern, SmemGrant &g, size_t smem) {
+inline cudaError_t grant_smem(K kern, SmemGrant &g, size_t smem, size_t most) {
     if (smem <= 48 * 1024) return cudaSuccess;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     std::atomic<int> &cur = g.bytes[dev & 63];
-    // once for all sizes: the most a block may have
     if (cur.load(std::memory_order_acquire)) return cudaSuccess;
-    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kClusterSmemMax - 1024))
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most)))
         return e;
     cur.store(1, std::memory_order_release);
     return cudaSuccess;
