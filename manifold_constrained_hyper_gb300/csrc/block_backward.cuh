@@ -1,0 +1,485 @@
+// Backward pass of the gated residual block for rows of up to 8192 columns.
+//
+// With D the gradient that reaches residual_out, the row needs two sums that
+// follow one another: mean(d_h w2 ro) for D, then mean(g D w1 y) for d_y. D is
+// linear in the first, so the second splits into two sums that need no D, and
+// one reduction of three sums serves the row.
+//
+// Bound by memory: 12 bytes a column with 16-bit types. A CTA's groups of warps
+// have a row each in flight, 16 columns a thread; the rows to come are staged in
+// shared memory by bulk copies. What every row needs again, both weights, the
+// scale and the sums over tokens (d_w_post, d_w_pre, d_res_scale), lies in
+// tensor memory, 16 columns of six arrays for each thread: in registers they
+// would not leave room for the row, and in shared memory not for the rows to
+// come. The sums leave it once, and a second kernel adds the CTAs' in their order.
+#pragma once
+#include "block_rows.cuh"
+
+namespace mhc {
+
+cudaError_t launch_block_bwd_loop(const BlockBwdArgs &a, int dtype, int r_dtype, bool pdl, int *parts, cudaStream_t s);
+
+namespace {
+
+constexpr int kBwdRuns = 2;
+constexpr int kBwdStages = 32;
+constexpr int kBwdGroups = 15;                      // named barriers 1 .. 15
+constexpr int kBwdThreads = 512;
+constexpr size_t kBwdSmem = 216 * 1024;             // dynamic; the group sums take 6 KB beside it
+constexpr int kBwdArrays = 6;                       // in tensor memory: 16 warps, four to a quadrant of lanes
+constexpr int kBwdTmemCols = 512;
+static_assert(4 * kBwdArrays * kBwdRuns * 8 <= kBwdTmemCols, "four warps' arrays fit a quadrant's columns");
+enum BwdSite : int { SITE_BWD_ROW = 75 };
+enum BwdArray : int { T_W1, T_W2, T_SCALE, T_DW1, T_DW2, T_DSCALE };
+
+struct BwdRing {
+    int groups;                                     // of a CTA, blockDim.x / groups threads each
+    int stages;
+    uint32_t bytes[5], stage_bytes;                 // y, residual (or their codes), d_ro, d_h, gate: of a row
+    unsigned int *status;
+    unsigned long long timeout_ns;
+};
+
+// FULL, SCALED, HELD: whether a call may have a full gate, a channel scale,
+// checkpoints in the place of y or residual.
+template <class TY, class TR, int MODE, bool FULL, bool SCALED, bool HELD>
+__global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBwdArgs a, const BwdRing ring) {
+    constexpr int RUNS = kBwdRuns, MAXW = kBwdThreads / 32;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float red[kBwdGroups][2][3 * MAXW];
+    __shared__ __align__(8) uint64_t bars[kBwdStages];
+    __shared__ float scale_red[32];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const BlockForm &f = a.f;
+    const int H = f.H, groups = (H + 31) / 32;
+    Place at;
+    at.H = H;
+    at.threads = blockDim.x / ring.groups;
+    const int grp = threadIdx.x / at.threads, tid = threadIdx.x - grp * at.threads;
+    at.thread = tid;
+    const int warp = tid >> 5, warps = at.threads >> 5;
+    const bool full_gate = FULL && f.gate_form == MHC_GATE_FULL, scaled = SCALED && f.scale_form == MHC_SCALE_CHANNEL;
+    const bool token_gate = f.gate_form == MHC_GATE_TOKEN;
+    const size_t ge = f.gate_dtype == MHC_F32 ? 4 : 2;
+    const uint32_t bar = smem_addr(bars);
+
+    if (threadIdx.x < 32) {
+        tmem_alloc(smem_addr(&tmem_slot), kBwdTmemCols);
+        tmem_relinquish();
+    }
+    for (int i = threadIdx.x; i < kBwdGroups * 2 * 3 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    if (MODE == ROWS_RING && threadIdx.x == 0) {
+        for (int s = 0; s < ring.stages; ++s) mbar_init(bar + 8 * s, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // this thread's arrays: its warp's quadrant of lanes, the warp's share of the columns
+    const uint32_t tmem0 = tmem_slot, cta_warp = threadIdx.x >> 5;
+    const uint32_t tmem = tmem0 + ((cta_warp & 3) << 21) + (cta_warp >> 2) * (kBwdArrays * RUNS * 8);
+    auto cell = [&](int array, int j) { return tmem + (array * RUNS + j) * 8; };
+    griddep_wait();
+    // The CTA's rows are blockIdx.x + k gridDim.x, k = 0, 1, ...: group k mod
+    // groups takes row k, from stage k mod stages.
+    const long long row0 = blockIdx.x + static_cast<long long>(grp) * gridDim.x;
+    const long long row_step = static_cast<long long>(gridDim.x) * ring.groups;
+    auto fetch = [&](long long t, int s) {          // one thread
+        const uint32_t b = bar + 8 * s;
+        uint32_t dst = smem_addr(smem) + s * ring.stage_bytes;
+        const uint64_t pol = policy_evict_first();
+        mbar_arrive_expect_tx(b, ring.stage_bytes);
+        bulk_load(dst, !HELD || a.y ? static_cast<const void *>(static_cast<const TY *>(a.y) + t * a.y_stride)
+                                    : a.ck_y.codes + t * H, ring.bytes[0], b, pol);
+        dst += ring.bytes[0];
+        bulk_load(dst, !HELD || a.residual
+                           ? static_cast<const void *>(static_cast<const TR *>(a.residual) + t * a.r_stride)
+                           : a.ck_r.codes + t * H, ring.bytes[1], b, pol);
+        dst += ring.bytes[1];
+        if (ring.bytes[2])
+            bulk_load(dst, static_cast<const TR *>(a.d_ro) + t * a.d_ro_stride, ring.bytes[2], b, pol);
+        dst += ring.bytes[2];
+        bulk_load(dst, static_cast<const TY *>(a.d_h) + t * a.d_h_stride, ring.bytes[3], b, pol);
+        dst += ring.bytes[3];
+        if (FULL && ring.bytes[4])
+            bulk_load(dst, static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge, ring.bytes[4], b, pol);
+    };
+    if (MODE == ROWS_RING && threadIdx.x == 0)
+        for (int s = 0; s < ring.stages; ++s) {
+            const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
+            if (t < f.T) fetch(t, s);
+        }
+    __syncwarp();
+    // w1 = (w_post + offset) * act of a channel gate, w2 = w_pre + offset, a channel scale; the sums
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+        Run w = load_weights<MODE>(f.w_post, f.w_post_dtype, f.weight_offset, at, j);
+        if (f.gate_form == MHC_GATE_CHANNEL) {
+            Run g = load_run_any<MODE>(f.gate, f.gate_dtype, at, j);
+            run_gate(g, f.gate_act);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w.p[i] = mul2(w.p[i], g.p[i]);
+        }
+        __syncwarp();
+        tmem_run_store(cell(T_W1, j), w);
+        w = load_weights<MODE>(f.w_pre, f.w_pre_dtype, f.weight_offset, at, j);
+        __syncwarp();
+        tmem_run_store(cell(T_W2, j), w);
+        if (SCALED) {
+            w = load_scale<MODE>(f, at, j);
+            __syncwarp();
+            tmem_run_store(cell(T_SCALE, j), w);
+        }
+        tmem_run_store(cell(T_DW1, j), run_splat(0.f));
+        tmem_run_store(cell(T_DW2, j), run_splat(0.f));
+        if (SCALED) tmem_run_store(cell(T_DSCALE, j), run_splat(0.f));
+    }
+    tmem_st_wait();
+    const uint64_t scale = splat2(f.scale_form == MHC_SCALE_ONE ? *f.res_scale : 1.f);
+    uint64_t scale2 = 0;
+
+    // What a row needs beside its columns, fetched a row ahead and left as it
+    // was loaded: arithmetic on it here would wait for it.
+    struct Ahead {
+        float rstd1, rstd2;
+        uint32_t token;                             // bits of its gate
+        uint32_t by[RUNS], br[RUNS];                // scale bytes of the runs, where rows are vectors
+    };
+    auto ahead = [&](long long t) {
+        Ahead n = {};
+        if (t >= f.T) return n;
+        n.rstd1 = a.rstd[2 * t];
+        n.rstd2 = a.rstd[2 * t + 1];
+        if (token_gate)
+            n.token = f.gate_dtype == MHC_F32 ? static_cast<const uint32_t *>(f.gate)[t * f.gate_stride]
+                                              : static_cast<const uint16_t *>(f.gate)[t * f.gate_stride];
+        if (MODE == ROWS_ANY || !HELD) return n;
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) {
+            const int g = run_read_col(at, j) / 32;
+            if (!a.y) n.by[j] = a.ck_y.scales[t * groups + g];
+            if (!a.residual) n.br[j] = a.ck_r.scales[t * groups + g];
+        }
+        return n;
+    };
+    auto token_of = [&](uint32_t bits) {
+        if (f.gate_dtype == MHC_F32) return __uint_as_float(bits);
+        if (f.gate_dtype == MHC_BF16) return __uint_as_float(bits << 16);
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+    };
+
+    // A wait that runs out is recorded, and the rows left go by with what the
+    // stages hold: no later wait takes long, and nothing more is fetched.
+    int which = 0, s = grp, last = -1;
+    uint32_t phase = 0;
+    bool ok = true;
+    Ahead next = ahead(row0);
+    for (long long t = row0; t < f.T; t += row_step) {
+        // the columns' addresses are formed anew for each row: kept across rows, those of every
+        // tensor would take the registers that hold the row
+        if (MODE == ROWS_ANY) asm volatile("" : "+r"(at.thread));
+        const Ahead now = next;
+        next = ahead(t + row_step);
+        const float rstd1 = f.post_norm ? now.rstd1 : 1.f, rstd2 = now.rstd2;
+        float token = 1.f, token_slope = 0.f;
+        if (token_gate) gate_both(token_of(now.token), f.gate_act, &token, &token_slope);
+        const uint8_t *const st = smem + s * ring.stage_bytes;
+        const uint8_t *const st_r = st + ring.bytes[0], *const st_f = st_r + ring.bytes[1],
+                      *const st_h = st_f + ring.bytes[2], *const st_g = st_h + ring.bytes[3];
+        if (MODE == ROWS_RING) {
+            ok = mbar_wait(bar + 8 * s, phase, &abort_flag, ring.timeout_ns, ring.status, SITE_BWD_ROW) && ok;
+            __syncwarp();
+        }
+
+        // a run of y, the residual, the gradients, the full gate, from the stage or from memory
+        auto held = [&](const Ckpt &c, const uint8_t *staged, uint32_t byte, int j) {
+            if constexpr (MODE != ROWS_ANY) {
+                const uint8_t *const codes = MODE == ROWS_RING ? staged : c.codes + t * H;
+                return ckpt_values8(*reinterpret_cast<const uint2 *>(codes + run_read_col(at, j)), byte, a.format);
+            } else {
+                const int col = run_col<MODE>(at, j);
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = col + e * at.threads;
+                    v[e] = i < H ? ckpt_load(c, a.format, t, H, groups, i) : 0.f;
+                }
+                return run_of(v);
+            }
+        };
+        auto load_y = [&](int j) {
+            if (HELD && !a.y) return held(a.ck_y, st, now.by[j], j);
+            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st), at, j);
+            else return load_run<MODE>(static_cast<const TY *>(a.y) + t * a.y_stride, at, j);
+        };
+        auto load_r = [&](int j) {
+            if (HELD && !a.residual) return held(a.ck_r, st_r, now.br[j], j);
+            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(st_r), at, j);
+            else return load_run<MODE>(static_cast<const TR *>(a.residual) + t * a.r_stride, at, j);
+        };
+        auto load_dh = [&](int j) {
+            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st_h), at, j);
+            else return load_run<MODE>(static_cast<const TY *>(a.d_h) + t * a.d_h_stride, at, j);
+        };
+        auto load_df = [&](int j) {
+            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(st_f), at, j);
+            else return load_run<MODE>(static_cast<const TR *>(a.d_ro) + t * a.d_ro_stride, at, j);
+        };
+        auto load_z = [&](int j) {
+            if constexpr (MODE == ROWS_RING) return staged_run_any(st_g, f.gate_dtype, at, j);
+            else return load_run_any<MODE>(static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge, f.gate_dtype, at, j);
+        };
+
+        const uint64_t r2 = splat2(rstd2), tr2 = splat2(token * rstd1);
+        uint64_t s0 = 0, s1 = 0, s2 = 0;
+        Run ev[RUNS];                               // d_ro + rstd_pre d_h w2
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) {
+            Run w1, w2, sc, sum2;
+            __syncwarp();
+            tmem_run_load(cell(T_W1, j), w1);
+            if (SCALED) tmem_run_load(cell(T_SCALE, j), sc);
+            tmem_run_load(cell(T_W2, j), w2);
+            tmem_run_load(cell(T_DW2, j), sum2);
+            Run y = load_y(j), ro = load_r(j);
+            if (full_gate) {
+                Run z = load_z(j);
+                run_gate(z, f.gate_act);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], z.p[i]);
+            }
+            const Run dh = load_dh(j);
+            ev[j] = run_splat(0.f);
+            if (a.d_ro) ev[j] = load_df(j);
+            __syncwarp();
+            tmem_run_wait(w1);
+            tmem_run_wait(w2);
+            tmem_run_wait(sum2);
+            if (SCALED) tmem_run_wait(sc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y.p[i] = mul2(y.p[i], w1.p[i]);                            // g w1 y, without a token's gate
+                ro.p[i] = fma2(y.p[i], tr2, mul2(SCALED ? sc.p[i] : scale, ro.p[i]));
+                sum2.p[i] = fma2(mul2(dh.p[i], r2), ro.p[i], sum2.p[i]);
+                const uint64_t dv = mul2(dh.p[i], w2.p[i]);
+                ev[j].p[i] = fma2(r2, dv, ev[j].p[i]);
+                s0 = fma2(dv, ro.p[i], s0);
+                s1 = fma2(y.p[i], ev[j].p[i], s1);
+                s2 = fma2(y.p[i], ro.p[i], s2);
+            }
+            tmem_run_store(cell(T_DW2, j), sum2);
+        }
+        float sum[3] = {f2_lo(s0) + f2_hi(s0), f2_lo(s1) + f2_hi(s1), f2_lo(s2) + f2_hi(s2)};
+        group_sum<3, MAXW>(sum, red[grp][which], 1 + grp, warp, warps);
+        which ^= 1;
+        if (MODE == ROWS_RING) {
+            // every thread of the group is past its row before: that row's stage is free
+            if (warps == 1) __syncwarp();
+            const long long refill = t - row_step + static_cast<long long>(ring.stages) * gridDim.x;
+            if (tid == 0 && last >= 0 && refill < f.T && ok) fetch(refill, last);
+            __syncwarp();
+            last = s;
+            // the group's next row: `groups` stages on, their number more than that
+            s += ring.groups;
+            if (s >= ring.stages) {
+                s -= ring.stages;
+                phase ^= 1;
+            }
+        }
+        const float q = rstd2 * (rstd2 * (rstd2 * (sum[0] * f.inv_h)));
+        const float c1 = fmaf(-q, sum[2], sum[1]);
+        const float p = f.post_norm ? rstd1 * (rstd1 * (rstd1 * (token * c1 * f.inv_h))) : 0.f;
+        const uint64_t q2 = splat2(-q), p2 = splat2(-p);
+        tmem_st_wait();
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) {
+            Run w1, sc, sum1, sums;
+            tmem_run_load(cell(T_W1, j), w1);
+            tmem_run_load(cell(T_DW1, j), sum1);
+            if (SCALED) {
+                tmem_run_load(cell(T_SCALE, j), sc);
+                tmem_run_load(cell(T_DSCALE, j), sums);
+            }
+            Run y = load_y(j), r = load_r(j);
+            __syncwarp();
+            tmem_run_wait(w1);
+            tmem_run_wait(sum1);
+            if (SCALED) {
+                tmem_run_wait(sc);
+                tmem_run_wait(sums);
+            }
+            if (full_gate) {
+                Run z = load_z(j);
+                const uint64_t u1 = splat2(rstd1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float g0, g1, h0, h1;
+                    gate_both(f2_lo(z.p[i]), f.gate_act, &g0, &h0);
+                    gate_both(f2_hi(z.p[i]), f.gate_act, &g1, &h1);
+                    const uint64_t g = f2_pack(g0, g1), u = mul2(y.p[i], u1), wu = mul2(w1.p[i], u);
+                    const uint64_t ro = fma2(g, wu, mul2(SCALED ? sc.p[i] : scale, r.p[i])), D = fma2(q2, ro, ev[j].p[i]);
+                    const uint64_t gD = mul2(g, D);
+                    sum1.p[i] = fma2(gD, u, sum1.p[i]);
+                    z.p[i] = mul2(f2_pack(h0, h1), mul2(wu, D));                            // d_gate
+                    y.p[i] = fma2(p2, y.p[i], mul2(u1, mul2(w1.p[i], gD)));                 // d_y
+                    ev[j].p[i] = D;
+                }
+                if (a.d_gate) {
+                    if (f.gate_dtype == MHC_F32) store_run<MODE>(static_cast<float *>(a.d_gate) + t * H, at, j, z);
+                    else store_run<MODE>(static_cast<TY *>(a.d_gate) + t * H, at, j, z);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t ro = fma2(mul2(y.p[i], w1.p[i]), tr2, mul2(SCALED ? sc.p[i] : scale, r.p[i]));
+                    const uint64_t D = fma2(q2, ro, ev[j].p[i]), trD = mul2(tr2, D);
+                    sum1.p[i] = fma2(trD, y.p[i], sum1.p[i]);
+                    y.p[i] = fma2(p2, y.p[i], mul2(w1.p[i], trD));
+                    ev[j].p[i] = D;
+                }
+            }
+            store_run<MODE>(static_cast<TY *>(a.d_y) + t * H, at, j, y);
+            if (!SCALED && (MODE == ROWS_ANY || run_col<MODE>(at, j) < H)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) scale2 = fma2(r.p[i], ev[j].p[i], scale2);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (SCALED) sums.p[i] = fma2(r.p[i], ev[j].p[i], sums.p[i]);
+                ev[j].p[i] = mul2(SCALED ? sc.p[i] : scale, ev[j].p[i]);
+            }
+            store_run<MODE>(static_cast<TR *>(a.d_r) + t * H, at, j, ev[j]);
+            __syncwarp();
+            tmem_run_store(cell(T_DW1, j), sum1);
+            if (SCALED) tmem_run_store(cell(T_DSCALE, j), sums);
+        }
+        tmem_st_wait();
+        if (token_gate && a.d_gate && tid == 0) static_cast<float *>(a.d_gate)[t] = token_slope * rstd1 * c1;
+    }
+    if (MODE == ROWS_RING && !ok && tid == 0) {
+        // copies that may still be in flight, before the CTA's memory goes: each
+        // stage's last, in either parity
+        int gave_up = 0;
+        for (int k = 0; k < 2 * ring.stages; ++k)
+            mbar_wait(bar + 8 * (k >> 1), k & 1, &gave_up, ring.timeout_ns, ring.status, SITE_BWD_ROW);
+    }
+
+    // the groups' sums, one group after the other (in the place of the stages), then out
+    __syncthreads();
+    float *const out = a.sums + static_cast<long long>(blockIdx.x) * kBackSums * H;
+    float *const kept = reinterpret_cast<float *>(smem);
+    auto leave = [&](int array, float *to) {
+        for (int g = 0; g < ring.groups; ++g) {
+            if (g == grp)
+#pragma unroll
+                for (int j = 0; j < RUNS; ++j) {
+                    Run acc;
+                    __syncwarp();
+                    tmem_run_load(cell(array, j), acc);
+                    tmem_run_wait(acc);
+                    if (g > 0) {
+                        const Run before = kept_run(kept, at, j);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc.p[i] = add2(before.p[i], acc.p[i]);
+                    }
+                    if (g < ring.groups - 1) keep_run(kept, at, j, acc);
+                    else store_run<MODE>(to, at, j, acc);
+                }
+            __syncthreads();
+        }
+    };
+    leave(T_DW1, out);
+    leave(T_DW2, out + H);
+    if (scaled) leave(T_DSCALE, out + 2 * static_cast<long long>(H));
+    float total[1] = {f2_lo(scale2) + f2_hi(scale2)};
+    if (SCALED && f.scale_form == MHC_SCALE_ONE) {
+        // a single scale in the general form: its columns' sums
+        total[0] = 0.f;
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) {
+            Run acc;
+            __syncwarp();
+            tmem_run_load(cell(T_DSCALE, j), acc);
+            tmem_run_wait(acc);
+            if (MODE == ROWS_ANY || run_col<MODE>(at, j) < H)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) total[0] += f2_lo(acc.p[i]) + f2_hi(acc.p[i]);
+        }
+    }
+    block_sum<1>(total, scale_red);
+    if (threadIdx.x == 0) a.scale_sums[blockIdx.x] = total[0];
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        tc_fence_after();
+        tmem_dealloc(tmem0, kBwdTmemCols);
+    }
+}
+
+template <class TY, class TR, int MODE, bool FULL, bool SCALED, bool HELD>
+cudaError_t bwd_launch(const BlockBwdArgs &a, const BwdRing &ring, unsigned grid, int threads, size_t smem, bool pdl,
+                       cudaStream_t s) {
+    static SmemGrant grant;
+    auto kern = block_bwd_kernel<TY, TR, MODE, FULL, SCALED, HELD>;
+    if (cudaError_t e = grant_smem(kern, grant, smem, kBwdSmem)) return e;
+    return launch_block_kernel(kern, grid, threads * ring.groups, smem, pdl, s, a, ring);
+}
+
+template <class TY, class TR>
+cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bool pdl, int *parts, cudaStream_t s) {
+    const BlockForm &f = a.f;
+    const int H = f.H;
+    if (H > 8192) return launch_block_bwd_loop(a, dtype, r_dtype, pdl, parts, s);
+    const bool full = f.gate_form == MHC_GATE_FULL, scaled = f.scale_form == MHC_SCALE_CHANNEL;
+    const bool held = !a.y || !a.residual;
+    auto codes_fit = [&](const Ckpt &c) { return (reinterpret_cast<uintptr_t>(c.codes) & 15u) == 0; };
+    const bool vec = H % 8 == 0 && (a.y ? rows_of_runs(a.y, a.y_stride, sizeof(TY), f.T) : codes_fit(a.ck_y)) &&
+                     (a.residual ? rows_of_runs(a.residual, a.r_stride, sizeof(TR), f.T) : codes_fit(a.ck_r)) &&
+                     (!a.d_ro || rows_of_runs(a.d_ro, a.d_ro_stride, sizeof(TR), f.T)) &&
+                     rows_of_runs(a.d_h, a.d_h_stride, sizeof(TY), f.T) && rows_of_runs(a.d_y, H, sizeof(TY), f.T) &&
+                     rows_of_runs(a.d_r, H, sizeof(TR), f.T) && rows_of_runs(a.sums, H, 4, f.T) && params_of_runs(f) &&
+                     (!full || (rows_of_runs(f.gate, f.gate_stride, elem_bytes(f.gate_dtype), f.T) &&
+                                (!a.d_gate || rows_of_runs(a.d_gate, H, elem_bytes(f.gate_dtype), f.T))));
+    BwdRing ring = {};
+    const int threads = row_threads(H, kBwdRuns);
+    // as many groups as fit, but no more than give every SM a row
+    long long groups = kBwdThreads / threads;
+    const long long rows = (f.T + sms - 1) / sms;
+    if (groups > kBwdGroups) groups = kBwdGroups;
+    ring.groups = static_cast<int>(rows < groups ? rows : groups);
+    const unsigned grid = static_cast<unsigned>(f.T < sms ? f.T : sms);
+    *parts = static_cast<int>(grid);
+    const size_t column = static_cast<size_t>(threads) * kBwdRuns * 32;     // the groups' sums at the end
+    if (!vec) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, column, pdl, s);
+    ring.bytes[0] = H * (a.y ? sizeof(TY) : 1);
+    ring.bytes[1] = H * (a.residual ? sizeof(TR) : 1);
+    ring.bytes[2] = a.d_ro ? H * sizeof(TR) : 0;
+    ring.bytes[3] = H * sizeof(TY);
+    ring.bytes[4] = full ? H * elem_bytes(f.gate_dtype) : 0;
+    for (uint32_t b : ring.bytes) ring.stage_bytes += b;
+    long long stages = static_cast<long long>(kBwdSmem / ring.stage_bytes);
+    if (stages > kBwdStages) stages = kBwdStages;
+    if (stages > rows) stages = rows;
+    // codes' rows on 16-byte boundaries, more than a row an SM, and two stages at least
+    if ((held && H % 16 != 0) || stages < 2)
+        return bwd_launch<TY, TR, ROWS_VEC, true, true, true>(a, ring, grid, threads, column, pdl, s);
+    // a stage for each group and one to fill meanwhile, or all of the rows
+    if (ring.groups >= stages) ring.groups = static_cast<int>(stages == rows ? stages : stages - 1);
+    ring.stages = static_cast<int>(stages);
+    size_t smem = static_cast<size_t>(ring.stage_bytes) * ring.stages;
+    if (smem < column) smem = column;
+    int n = 0;
+    if (require_device(&n, &ring.status)) return cudaErrorUnknown;
+    ring.timeout_ns = wait_timeout_ns();
+    if (full) return bwd_launch<TY, TR, ROWS_RING, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+    if (held)
+        return scaled ? bwd_launch<TY, TR, ROWS_RING, false, true, true>(a, ring, grid, threads, smem, pdl, s)
+                      : bwd_launch<TY, TR, ROWS_RING, false, false, true>(a, ring, grid, threads, smem, pdl, s);
+    return scaled ? bwd_launch<TY, TR, ROWS_RING, false, true, false>(a, ring, grid, threads, smem, pdl, s)
+                  : bwd_launch<TY, TR, ROWS_RING, false, false, false>(a, ring, grid, threads, smem, pdl, s);
+}
+
+}  // namespace
+}  // namespace mhc

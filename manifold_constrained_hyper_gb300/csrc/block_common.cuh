@@ -37,23 +37,33 @@ __device__ __forceinline__ float weight_at(const void *w, int dtype, float offse
     return w ? load_any(w, dtype, i) + offset : 1.f;
 }
 
-// act(z) and, from its value, act'(z). tanh and sigmoid by CUDA's expf and
-// tanhf: their few ulp are far below the outputs' rounding.
+// act(z). The sigmoid from e = exp(-|z|) <= 1, as 1 / (1 + e) or e / (1 + e):
+// no overflow, and the divisor stays in [1, 2], where the approximate division
+// is off by 2 ulp. exp and tanh are CUDA's own, a few ulp, far below a
+// 16-bit output's rounding and of the size of an fp32 one's.
 __device__ __forceinline__ float gate_value(float z, int act) {
-    if (act == MHC_ACT_SIGMOID) return 1.f / (1.f + expf(-z));
+    if (act == MHC_ACT_SIGMOID) {
+        const float e = expf(-fabsf(z));
+        return __fdividef(z < 0.f ? e : 1.f, 1.f + e);
+    }
     if (act == MHC_ACT_TANH) return tanhf(z);
     return z;
 }
-// The slope of the sigmoid and of tanh: g (1 - g) and (1 - g) (1 + g). In
-// the tails 1 - g is formed anew from z: where g has rounded to 1 the product would be 0.
-__device__ __forceinline__ float gate_slope(float z, float g, int act) {
-    if (act == MHC_ACT_SIGMOID) return g * (1.f / (1.f + expf(z)));
-    if (act == MHC_ACT_TANH) {
-        if (fabsf(z) < 1.f) return (1.f - g) * (1.f + g);
-        const float e = expf(-2.f * fabsf(z));      // 1 - tanh^2 = 4 e / (1 + e)^2
-        return 4.f * e / ((1.f + e) * (1.f + e));
+// act(z) and act'(z) together. The sigmoid's slope is e / (1 + e)^2, that of
+// tanh four times the sigmoid's at 2 z: in these forms neither vanishes where
+// the value has rounded to 1.
+__device__ __forceinline__ void gate_both(float z, int act, float *g, float *slope) {
+    *g = z;
+    *slope = 1.f;
+    if (act == MHC_ACT_SIGMOID) {
+        const float e = expf(-fabsf(z)), s = __fdividef(1.f, 1.f + e);
+        *g = z < 0.f ? e * s : s;
+        *slope = e * s * s;
+    } else if (act == MHC_ACT_TANH) {
+        *g = tanhf(z);
+        const float e = expf(-2.f * fabsf(z)), s = __fdividef(1.f, 1.f + e);
+        *slope = 4.f * e * s * s;
     }
-    return 1.f;
 }
 
 // ---------------------------------------------------------------- checkpoints

@@ -1,0 +1,300 @@
+// The gated residual block's boundary for rows of up to 8192 columns: a group
+// of warps holds a row in registers, so that y, residual and a full gate are
+// read once and both norms' sums run over registers; what every row needs (both
+// weights with their offset and a channel gate, a channel scale) lies in
+// shared memory.
+//
+// Bound by memory: 8 bytes a column with 16-bit types (10 with a full gate),
+// which leaves the issue slots some 40 instructions a column at full rate; so
+// the arithmetic is on packed pairs and a thread holds 32 columns, over which
+// a row's fixed costs (two sums, a wait, addresses) spread. A row's two sums
+// follow one another: a CTA's groups have a row each in flight, and the rows
+// to come are staged in shared memory by bulk copies meanwhile, a stage
+// refilled as soon as its row is in registers.
+#pragma once
+#include "block_rows.cuh"
+
+namespace mhc {
+
+cudaError_t launch_block_fwd_loop(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bool pdl, cudaStream_t s);
+
+namespace {
+
+constexpr int kFwdStages = 32;
+constexpr int kFwdGroups = 15;                      // named barriers 1 .. 15
+constexpr size_t kFwdSmem = 224 * 1024;             // dynamic
+enum FwdSite : int { SITE_FWD_ROW = 70 };
+
+struct FwdRing {
+    int groups;                                     // of a CTA, blockDim.x / groups threads each
+    int stages;
+    uint32_t y_bytes, r_bytes, g_bytes;             // of a row; g_bytes 0: no full gate
+    unsigned int *status;
+    unsigned long long timeout_ns;
+};
+
+// FULL, SCALED, CKPT: whether a call may have a full gate, a channel scale,
+// checkpoints. RUNS of 8 columns a thread: 4 in blocks of up to 512 threads of 128
+// registers; 1, up to 1024 threads of 64, where a CTA has one row only.
+template <class TY, class TR, int MODE, int RUNS, bool FULL, bool SCALED, bool CKPT>
+__global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(const BlockFwdArgs a, const FwdRing ring) {
+    constexpr int MAXW = RUNS == 1 ? 32 : 8, GROUPS = RUNS == 1 ? 1 : kFwdGroups;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float red[GROUPS][2][MAXW];
+    __shared__ __align__(8) uint64_t bars[kFwdStages];
+    __shared__ int abort_flag;
+    const BlockForm &f = a.f;
+    Place at;
+    at.H = f.H;
+    at.threads = blockDim.x / ring.groups;
+    const int grp = GROUPS == 1 ? 0 : threadIdx.x / at.threads;
+    at.thread = threadIdx.x - grp * at.threads;
+    const int warp = at.thread >> 5, warps = at.threads >> 5;
+    const bool full_gate = FULL && f.gate_form == MHC_GATE_FULL;
+    const uint32_t stage_bytes = ring.y_bytes + ring.r_bytes + ring.g_bytes;
+    const size_t ge = f.gate_dtype == MHC_F32 ? 4 : 2;
+    // (w_post + offset) * act of a channel gate; w_pre + offset; a channel scale; then the stages
+    float *const w1_kept = reinterpret_cast<float *>(smem), *const w2_kept = w1_kept + 8 * RUNS * at.threads,
+          *const sc_kept = w2_kept + 8 * RUNS * at.threads;
+    const uint32_t stage0 = (SCALED ? 3 : 2) * 32 * RUNS * at.threads;
+    const uint32_t bar = smem_addr(bars);
+
+    for (int i = threadIdx.x; i < GROUPS * 2 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    if (MODE == ROWS_RING && threadIdx.x == 0) {
+        for (int s = 0; s < ring.stages; ++s) mbar_init(bar + 8 * s, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    // The CTA's rows are blockIdx.x + k gridDim.x, k = 0, 1, ...: group k mod
+    // groups takes row k, from stage k mod stages.
+    auto fetch = [&](long long t, int s) {          // one thread
+        const uint32_t b = bar + 8 * s, dst = smem_addr(smem) + stage0 + s * stage_bytes;
+        const uint64_t pol = policy_evict_first();
+        mbar_arrive_expect_tx(b, stage_bytes);
+        bulk_load(dst, static_cast<const TY *>(a.y) + t * a.y_stride, ring.y_bytes, b, pol);
+        bulk_load(dst + ring.y_bytes, static_cast<const TR *>(a.residual) + t * a.r_stride, ring.r_bytes, b, pol);
+        if (FULL && ring.g_bytes)
+            bulk_load(dst + ring.y_bytes + ring.r_bytes,
+                      static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge, ring.g_bytes, b, pol);
+    };
+    if (MODE == ROWS_RING && threadIdx.x == 0)
+        for (int s = 0; s < ring.stages; ++s) {
+            const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
+            if (t < f.T) fetch(t, s);
+        }
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+        if (grp > 0) break;
+        Run w = load_weights<MODE>(f.w_post, f.w_post_dtype, f.weight_offset, at, j);
+        if (f.gate_form == MHC_GATE_CHANNEL) {
+            Run g = load_run_any<MODE>(f.gate, f.gate_dtype, at, j);
+            run_gate(g, f.gate_act);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w.p[i] = mul2(w.p[i], g.p[i]);
+        }
+        keep_run(w1_kept, at, j, w);
+        keep_run(w2_kept, at, j, load_weights<MODE>(f.w_pre, f.w_pre_dtype, f.weight_offset, at, j));
+        if (SCALED) keep_run(sc_kept, at, j, load_scale<MODE>(f, at, j));
+    }
+    if (ring.groups > 1) __syncthreads();           // one group: each thread reads what it wrote
+    const uint64_t scale = splat2(f.scale_form == MHC_SCALE_ONE ? *f.res_scale : 1.f);
+
+    // A wait that runs out is recorded, and the rows left go by with what the
+    // stages hold: no later wait takes long, and nothing more is fetched.
+    int which = 0, s = grp;
+    uint32_t phase = 0;
+    bool ok = true;
+    const long long row_step = static_cast<long long>(gridDim.x) * ring.groups;
+    for (long long t = blockIdx.x + static_cast<long long>(grp) * gridDim.x; t < f.T; t += row_step) {
+        // the columns' addresses are formed anew for each row: kept across rows, those of every
+        // tensor would take the registers that hold the row
+        if (MODE == ROWS_ANY) asm volatile("" : "+r"(at.thread));
+        const uint8_t *const st = smem + stage0 + s * stage_bytes;
+        if (MODE == ROWS_RING)
+            ok = mbar_wait(bar + 8 * s, phase, &abort_flag, ring.timeout_ns, ring.status, SITE_FWD_ROW) && ok;
+        auto load_y = [&](int j) {
+            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st), at, j);
+            else return load_run<MODE>(static_cast<const TY *>(a.y) + t * a.y_stride, at, j);
+        };
+        auto load_r = [&](int j) {
+            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(st + ring.y_bytes), at, j);
+            else return load_run<MODE>(static_cast<const TR *>(a.residual) + t * a.r_stride, at, j);
+        };
+        auto load_z = [&](int j) {
+            if constexpr (MODE == ROWS_RING)
+                return staged_run_any(st + ring.y_bytes + ring.r_bytes, f.gate_dtype, at, j);
+            else return load_run_any<MODE>(static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge, f.gate_dtype, at, j);
+        };
+        Run y[RUNS], v[RUNS];
+        uint64_t s2 = 0;
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) {
+            y[j] = load_y(j);
+            v[j] = load_r(j);
+        }
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) {
+            // past the row's end stands its last run again: not in the sums
+            const bool in = MODE == ROWS_ANY || run_col<MODE>(at, j) < f.H;
+            if (in) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s2 = fma2(y[j].p[i], y[j].p[i], s2);
+            }
+            if (CKPT && a.ck_y.codes) store_ckpt<MODE>(a.ck_y, a.format, t, at, j, y[j]);
+            if (CKPT && a.ck_r.codes) store_ckpt<MODE>(a.ck_r, a.format, t, at, j, v[j]);
+            if (full_gate) {
+                Run g = load_z(j);
+                run_gate(g, f.gate_act);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[j].p[i] = mul2(y[j].p[i], g.p[i]);
+            }
+            const Run w = kept_run(w1_kept, at, j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[j].p[i] = mul2(y[j].p[i], w.p[i]);
+            if constexpr (SCALED) {
+                const Run sc = kept_run(sc_kept, at, j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j].p[i] = mul2(v[j].p[i], sc.p[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j].p[i] = mul2(v[j].p[i], in ? scale : 0ull);
+            }
+        }
+        float rstd1 = 1.f, sum[1];
+        if (f.post_norm) {
+            sum[0] = f2_lo(s2) + f2_hi(s2);
+            group_sum<1, MAXW>(sum, red[grp][which], 1 + grp, warp, warps);
+            which ^= 1;
+            rstd1 = __frsqrt_rn(fmaf(sum[0], f.inv_h, f.eps_post));
+        } else if (MODE == ROWS_RING && warps > 1) {
+            named_barrier_sync(1 + grp, at.threads);
+        }
+        if (MODE == ROWS_RING) {
+            // the row is in registers: its stage is free
+            if (warps == 1) __syncwarp();
+            const long long next = t + static_cast<long long>(ring.stages) * gridDim.x;
+            if (at.thread == 0 && next < f.T && ok) fetch(next, s);
+            // the group's next row: `groups` stages on, their number more than that
+            s += ring.groups;
+            if (s >= ring.stages) {
+                s -= ring.stages;
+                phase ^= 1;
+            }
+        }
+        float tr = rstd1;
+        if (f.gate_form == MHC_GATE_TOKEN)
+            tr *= gate_value(load_any(f.gate, f.gate_dtype, t * f.gate_stride), f.gate_act);
+        const uint64_t tr2 = splat2(tr);
+        s2 = 0;
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[j].p[i] = fma2(y[j].p[i], tr2, v[j].p[i]);
+                s2 = fma2(v[j].p[i], v[j].p[i], s2);
+            }
+            store_run<MODE>(static_cast<TR *>(a.residual_out) + t * f.H, at, j, v[j]);
+        }
+        sum[0] = f2_lo(s2) + f2_hi(s2);
+        group_sum<1, MAXW>(sum, red[grp][which], 1 + grp, warp, warps);
+        which ^= 1;
+        const float rstd2 = __frsqrt_rn(fmaf(sum[0], f.inv_h, f.eps_pre));
+        const uint64_t r2 = splat2(rstd2);
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) {
+            const Run w = kept_run(w2_kept, at, j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j].p[i] = mul2(mul2(v[j].p[i], r2), w.p[i]);
+            store_run<MODE>(static_cast<TY *>(a.h) + t * f.H, at, j, v[j]);
+            if (CKPT && a.ck_h.codes) {
+                // of h as it is stored
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[j].p[i] = f2_pack(to_f32(from_f32<TY>(f2_lo(v[j].p[i]))), to_f32(from_f32<TY>(f2_hi(v[j].p[i]))));
+                store_ckpt<MODE>(a.ck_h, a.format, t, at, j, v[j]);
+            }
+        }
+        if (a.rstd && at.thread == 0) {
+            a.rstd[2 * t] = rstd1;
+            a.rstd[2 * t + 1] = rstd2;
+        }
+    }
+    if (MODE == ROWS_RING && !ok && at.thread == 0) {
+        // copies that may still be in flight, before the CTA's memory goes: each
+        // stage's last, in either parity
+        int gave_up = 0;
+        for (int k = 0; k < 2 * ring.stages; ++k)
+            mbar_wait(bar + 8 * (k >> 1), k & 1, &gave_up, ring.timeout_ns, ring.status, SITE_FWD_ROW);
+    }
+}
+
+template <class TY, class TR, int MODE, int RUNS, bool FULL, bool SCALED, bool CKPT>
+cudaError_t fwd_launch(const BlockFwdArgs &a, const FwdRing &ring, unsigned grid, int threads, size_t smem, bool pdl,
+                       cudaStream_t s) {
+    static SmemGrant grant;
+    auto kern = block_fwd_kernel<TY, TR, MODE, RUNS, FULL, SCALED, CKPT>;
+    if (cudaError_t e = grant_smem(kern, grant, smem, kFwdSmem)) return e;
+    return launch_block_kernel(kern, grid, threads * ring.groups, smem, pdl, s, a, ring);
+}
+
+template <class TY, class TR>
+cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bool pdl, cudaStream_t s) {
+    const BlockForm &f = a.f;
+    if (f.H > 8192) return launch_block_fwd_loop(a, dtype, r_dtype, sms, pdl, s);
+    const bool full = f.gate_form == MHC_GATE_FULL, scaled = f.scale_form == MHC_SCALE_CHANNEL;
+    const Ckpt cks[] = {a.ck_y, a.ck_r, a.ck_h};
+    bool vec = f.H % 8 == 0 && rows_of_runs(a.y, a.y_stride, sizeof(TY), f.T) &&
+               rows_of_runs(a.residual, a.r_stride, sizeof(TR), f.T) &&
+               rows_of_runs(a.residual_out, f.H, sizeof(TR), f.T) && rows_of_runs(a.h, f.H, sizeof(TY), f.T) &&
+               params_of_runs(f) && (!full || rows_of_runs(f.gate, f.gate_stride, elem_bytes(f.gate_dtype), f.T));
+    bool ckpt = false;
+    for (const Ckpt &c : cks) {
+        vec = vec && (reinterpret_cast<uintptr_t>(c.codes) & 7u) == 0;
+        ckpt = ckpt || c.codes;
+    }
+    FwdRing ring = {};
+    ring.groups = 1;
+    if (vec && f.T <= sms) {
+        // a CTA for each row, a thread for each run of it
+        const int threads = row_threads(f.H, 1);
+        return fwd_launch<TY, TR, ROWS_VEC, 1, true, true, true>(a, ring, static_cast<unsigned>(f.T), threads,
+                                                                 3 * 32 * threads, pdl, s);
+    }
+    // as many groups as fit, but no more than give every SM a row
+    const int threads = row_threads(f.H, 4);
+    long long groups = 512 / threads;
+    const long long rows = (f.T + sms - 1) / sms;
+    if (groups > kFwdGroups) groups = kFwdGroups;
+    ring.groups = static_cast<int>(rows < groups ? rows : groups);
+    const unsigned grid = static_cast<unsigned>(f.T < sms ? f.T : sms);
+    const size_t kept = static_cast<size_t>(vec && !full && !scaled ? 2 : 3) * 128 * threads;
+    if (!vec) return fwd_launch<TY, TR, ROWS_ANY, 4, true, true, true>(a, ring, grid, threads, kept, pdl, s);
+    ring.y_bytes = f.H * sizeof(TY);
+    ring.r_bytes = f.H * sizeof(TR);
+    ring.g_bytes = full ? f.H * elem_bytes(f.gate_dtype) : 0;
+    // a stage for each group and one to fill meanwhile, or all of the rows; with the widest types (96 KB a
+    // row of 8192) one stage and one group
+    const size_t bytes = ring.y_bytes + ring.r_bytes + ring.g_bytes;
+    long long stages = static_cast<long long>((kFwdSmem - kept) / bytes);
+    if (stages > kFwdStages) stages = kFwdStages;
+    if (stages > rows) stages = rows;
+    if (ring.groups >= stages) ring.groups = static_cast<int>(stages == rows || stages == 1 ? stages : stages - 1);
+    ring.stages = static_cast<int>(stages);
+    const size_t smem = kept + bytes * ring.stages;
+    int n = 0;
+    if (require_device(&n, &ring.status)) return cudaErrorUnknown;
+    ring.timeout_ns = wait_timeout_ns();
+    if (full)
+        return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, true, true, true>(a, ring, grid, threads, smem, pdl, s)
+                    : fwd_launch<TY, TR, ROWS_RING, 4, true, true, false>(a, ring, grid, threads, smem, pdl, s);
+    if (scaled)
+        return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, false, true, true>(a, ring, grid, threads, smem, pdl, s)
+                    : fwd_launch<TY, TR, ROWS_RING, 4, false, true, false>(a, ring, grid, threads, smem, pdl, s);
+    return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, false, false, true>(a, ring, grid, threads, smem, pdl, s)
+                : fwd_launch<TY, TR, ROWS_RING, 4, false, false, false>(a, ring, grid, threads, smem, pdl, s);
+}
+
+}  // namespace
+}  // namespace mhc

@@ -95,6 +95,11 @@ __global__ void block_bwd_loop_kernel(const BlockBwdArgs a) {
         const float rstd1 = f.post_norm ? a.rstd[2 * t] : 1.f, rstd2 = a.rstd[2 * t + 1];
         const float token = token_gate(f, t);
         const float gate_all = f.gate_form == MHC_GATE_TOKEN ? token : 1.f;
+        auto slope_at = [&](float z) {
+            float g, slope;
+            gate_both(z, f.gate_act, &g, &slope);
+            return slope;
+        };
         struct Elem { float y, r, df, dh, w1, w2, a, g, z, u, n, ro; };
         auto load = [&](int i) {
             Elem e;
@@ -143,11 +148,11 @@ __global__ void block_bwd_loop_kernel(const BlockBwdArgs a) {
             if (f.scale_form == MHC_SCALE_CHANNEL) sums[2 * H + i] = first ? s2 : sums[2 * H + i] + s2;
             else scale_sum += s2;
             if (f.gate_form == MHC_GATE_FULL && a.d_gate)
-                store_any(a.d_gate, f.gate_dtype, t * H + i, gate_slope(e.z, e.g, f.gate_act) * e.n * D);
+                store_any(a.d_gate, f.gate_dtype, t * H + i, slope_at(e.z) * e.n * D);
         }
         if (f.gate_form == MHC_GATE_TOKEN && a.d_gate && threadIdx.x == 0) {
             const float z = load_any(f.gate, f.gate_dtype, t * f.gate_stride);
-            static_cast<float *>(a.d_gate)[t] = gate_slope(z, token, f.gate_act) * rstd1 * c1;
+            static_cast<float *>(a.d_gate)[t] = slope_at(z) * rstd1 * c1;
         }
     }
     float s[1] = {scale_sum};

@@ -14,86 +14,221 @@ enum RowMode : int {
     ROWS_VEC = 1,       // 16-byte loads (the same, or a few rows only)
     ROWS_ANY = 2        // single elements, any boundary
 };
-// A thread's COLS columns: run j covers VEC of them from (j * threads + thread) * VEC.
-template <int MODE, int COLS>
-struct Runs {
-    static constexpr int kVec = MODE == ROWS_ANY ? 1 : 8;
-    static constexpr int kRuns = COLS / kVec;
-};
-inline int row_threads(int H, int cols) { return ((H + cols - 1) / cols + 31) / 32 * 32; }
+// A thread holds RUNS runs of 8 columns of its group's row: with vector loads
+// run j is the columns from (j * threads + thread) * 8, with single ones the
+// columns (8 j + e) * threads + thread.
+inline int row_threads(int H, int runs) { return ((H + 8 * runs - 1) / (8 * runs) + 31) / 32 * 32; }
 
-// Sums of N values over a group of `warps` whole warps that share the named
-// barrier `bar`, in one fixed order, for every thread of it. `red`: 32 N floats of the
-// group's own; the caller alternates between two, so that a value is read by
-// all before it is written again.
-template <int N>
+struct Place {
+    int thread, threads, H;                         // of the group
+};
+template <int MODE>
+__device__ __forceinline__ int run_col(const Place &p, int j) {
+    return MODE == ROWS_ANY ? j * 8 * p.threads + p.thread : (j * p.threads + p.thread) * 8;
+}
+// Where run j of vector loads is read: past the row's end its last run again,
+// so that no load needs a guard. Of a checkpoint's group that the row's end
+// cuts, this is the same group, whose maximum it leaves as it is.
+__device__ __forceinline__ int run_read_col(const Place &p, int j) {
+    const int c = run_col<ROWS_VEC>(p, j);
+    return c < p.H ? c : p.H - 8;
+}
+// Run j of a row in global memory; past the row's end 0 with single loads,
+// the row's last run with vector loads.
+template <int MODE, class T>
+__device__ __forceinline__ Run load_run(const T *row, const Place &p, int j) {
+    if constexpr (MODE != ROWS_ANY) return load8(row + run_read_col(p, j));
+    const int c = run_col<MODE>(p, j);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e * p.threads < p.H ? to_f32(row[c + e * p.threads]) : 0.f;
+    return run_of(v);
+}
+template <int MODE, class T>
+__device__ __forceinline__ void store_run(T *row, const Place &p, int j, const Run &r) {
+    const int c = run_col<MODE>(p, j);
+    if constexpr (MODE != ROWS_ANY) {
+        if (c < p.H) store8(row + c, r);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (c + e * p.threads < p.H) row[c + e * p.threads] = from_f32<T>(run_at(r, e));
+}
+// Of a type known at run time: a weight, a scale, a gate.
+template <int MODE>
+__device__ __forceinline__ Run load_run_any(const void *row, int dtype, const Place &p, int j) {
+    if (dtype == MHC_F32) return load_run<MODE>(static_cast<const float *>(row), p, j);
+    if (dtype == MHC_BF16) return load_run<MODE>(static_cast<const __nv_bfloat16 *>(row), p, j);
+    return load_run<MODE>(static_cast<const __half *>(row), p, j);
+}
+// Run j of a row staged in shared memory.
+template <class T>
+__device__ __forceinline__ Run staged_run(const T *row, const Place &p, int j) {
+    return load8_shared(row + run_read_col(p, j));
+}
+__device__ __forceinline__ Run staged_run_any(const void *row, int dtype, const Place &p, int j) {
+    if (dtype == MHC_F32) return staged_run(static_cast<const float *>(row), p, j);
+    if (dtype == MHC_BF16) return staged_run(static_cast<const __nv_bfloat16 *>(row), p, j);
+    return staged_run(static_cast<const __half *>(row), p, j);
+}
+// What a thread keeps in shared memory of its own columns for every row: run j
+// in two halves of 16 bytes, each half of all threads together (no two of a
+// warp's eight on the same banks). RUNS * 8 * threads floats an array.
+__device__ __forceinline__ Run kept_run(const float *kept, const Place &p, int j) {
+    const ulonglong2 *const q = reinterpret_cast<const ulonglong2 *>(kept) + 2 * j * p.threads + p.thread;
+    const ulonglong2 a = q[0], b = q[p.threads];
+    Run r;
+    r.p[0] = a.x;
+    r.p[1] = a.y;
+    r.p[2] = b.x;
+    r.p[3] = b.y;
+    return r;
+}
+__device__ __forceinline__ void keep_run(float *kept, const Place &p, int j, const Run &r) {
+    ulonglong2 *const q = reinterpret_cast<ulonglong2 *>(kept) + 2 * j * p.threads + p.thread;
+    q[0] = make_ulonglong2(r.p[0], r.p[1]);
+    q[p.threads] = make_ulonglong2(r.p[2], r.p[3]);
+}
+// A run in tensor memory: 8 columns of the warp's 32 lanes. Whole warps. The
+// values are there after tmem_run_wait on them.
+__device__ __forceinline__ void tmem_run_load(uint32_t taddr, Run &r) {
+    uint32_t v[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = (static_cast<uint64_t>(v[2 * i + 1]) << 32) | v[2 * i];
+}
+__device__ __forceinline__ void tmem_run_wait(Run &r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+l"(r.p[0]), "+l"(r.p[1]), "+l"(r.p[2]), "+l"(r.p[3]) :: "memory");
+}
+__device__ __forceinline__ void tmem_run_store(uint32_t taddr, const Run &r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(static_cast<uint32_t>(r.p[0])), "r"(static_cast<uint32_t>(r.p[0] >> 32)),
+                   "r"(static_cast<uint32_t>(r.p[1])), "r"(static_cast<uint32_t>(r.p[1] >> 32)),
+                   "r"(static_cast<uint32_t>(r.p[2])), "r"(static_cast<uint32_t>(r.p[2] >> 32)),
+                   "r"(static_cast<uint32_t>(r.p[3])), "r"(static_cast<uint32_t>(r.p[3] >> 32)) : "memory");
+}
+// The residual's scale of run j; past the row's end 0, as of the weights.
+template <int MODE>
+__device__ __forceinline__ Run load_scale(const BlockForm &f, const Place &p, int j) {
+    if (MODE != ROWS_ANY && run_col<MODE>(p, j) >= p.H) return run_splat(0.f);
+    if (f.scale_form == MHC_SCALE_CHANNEL) return load_run<MODE>(f.res_scale, p, j);
+    return run_splat(f.scale_form == MHC_SCALE_ONE ? *f.res_scale : 1.f);
+}
+// Weights of run j with their offset, 1 where there are none; past the row's
+// end 0, so that what they multiply leaves the row's sums alone.
+template <int MODE>
+__device__ __forceinline__ Run load_weights(const void *w, int dtype, float offset, const Place &p, int j) {
+    if (MODE != ROWS_ANY && run_col<MODE>(p, j) >= p.H) return run_splat(0.f);
+    if (!w) return run_splat(1.f);
+    Run r = load_run_any<MODE>(w, dtype, p, j);
+    if (offset != 0.f) {
+        const uint64_t o = splat2(offset);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.p[i] = add2(r.p[i], o);
+    }
+    return r;
+}
+__device__ __forceinline__ void run_gate(Run &r, int act) {
+    if (act == MHC_ACT_NONE) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = f2_pack(gate_value(f2_lo(r.p[i]), act), gate_value(f2_hi(r.p[i]), act));
+}
+// Run j of a row's checkpoint. Whole warps call it.
+template <int FMT, int MODE>
+__device__ __forceinline__ void store_ckpt(const Ckpt &c, long long t, const Place &p, int j, const Run &r) {
+    const int groups = (p.H + 31) / 32, col = run_col<MODE>(p, j);
+    uint8_t *const codes = c.codes + t * p.H, *const scales = c.scales + t * groups;
+    if constexpr (MODE != ROWS_ANY) {
+        const uint32_t byte = ckpt_byte_quad<FMT>(r);
+        if (col >= p.H) return;
+        *reinterpret_cast<uint2 *>(codes + col) = ckpt_codes8<FMT>(r, byte);
+        if ((threadIdx.x & 3) == 0) scales[col / 32] = static_cast<uint8_t>(byte);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = col + e * p.threads;
+            uint32_t byte;
+            const uint32_t code = ckpt_encode_lane<FMT>(run_at(r, e), &byte);
+            if (i < p.H) codes[i] = static_cast<uint8_t>(code);
+            if (i < p.H && (threadIdx.x & 31) == 0) scales[i / 32] = static_cast<uint8_t>(byte);
+        }
+    }
+}
+template <int MODE>
+__device__ __forceinline__ void store_ckpt(const Ckpt &c, int format, long long t, const Place &p, int j, const Run &r) {
+    if (format == MHC_CKPT_E4M3) store_ckpt<MHC_CKPT_E4M3, MODE>(c, t, p, j, r);
+    else store_ckpt<MHC_CKPT_INT8, MODE>(c, t, p, j, r);
+}
+
+// Sums of N values (1 or 3) over a group of up to MAXW whole warps that share
+// the named barrier `bar`, in one fixed order, for every thread of it. Within a
+// warp by shuffles (of three sums two at a time: after the first two steps a
+// lane carries one of them); across warps every thread adds all of them itself
+// (16-byte broadcasts: half the latency of a second round of shuffles). `red`:
+// N MAXW floats of the group's own on a 16-byte boundary, zero beyond its
+// warps; the caller alternates between two, so that a value is read by all
+// before it is written again.
+template <int N, int MAXW>
 __device__ __forceinline__ void group_sum(float (&v)[N], float *red, int bar, int warp, int warps) {
     const int lane = threadIdx.x & 31;
+    float x = v[0];
+    if constexpr (N == 3) {
+        // lane bit 4 picks v0 or v1 (with v2 beside v0), bit 3 then v0 or v2
+        const bool up = lane & 16, mid = lane & 8;
+        const float give = up ? v[0] : v[1], keep = up ? v[1] : v[0];
+        const float a = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+        const float b = v[2] + __shfl_xor_sync(0xffffffffu, v[2], 16);
+        const float give2 = mid ? a : b, keep2 = mid ? b : a;
+        // lanes 0-7: v0, 8-15: v2, 16-23: v1, 24-31: v2 once more
+        x = keep2 + __shfl_xor_sync(0xffffffffu, give2, 8);
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+        for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (warps == 1) {
+            v[0] = __shfl_sync(0xffffffffu, x, 0);
+            v[1] = __shfl_sync(0xffffffffu, x, 16);
+            v[2] = __shfl_sync(0xffffffffu, x, 8);
+            return;
+        }
+        if ((lane & 7) == 0 && lane < 24) red[(lane == 0 ? 0 : lane == 16 ? 1 : 2) * MAXW + warp] = x;
+    } else {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (warps == 1) return;
-    if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) red[k * 32 + warp] = v[k];
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        v[0] = x;
+        if (warps == 1) return;
+        if (lane == 0) red[warp] = x;
     }
     named_barrier_sync(bar, warps * 32);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        v[k] = lane < warps ? red[k * 32 + lane] : 0.f;
+        uint64_t s[MAXW / 4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        for (int i = 0; i < MAXW / 4; ++i) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(red + k * MAXW + 4 * i);
+            s[i] = add2(w.x, w.y);
+        }
+#pragma unroll
+        for (int n = MAXW / 8; n > 0; n >>= 1)
+#pragma unroll
+            for (int i = 0; i < n; ++i) s[i] = add2(s[i], s[i + n]);
+        v[k] = f2_lo(s[0]) + f2_hi(s[0]);
     }
 }
 
-// VEC parameters (weights, scales) of a run; past the row's end `fill`.
-template <int VEC>
-__device__ __forceinline__ void load_params(const void *p, int dtype, int c, float (&v)[VEC]) {
-    if (dtype == MHC_F32) load_run<VEC>(static_cast<const float *>(p) + c, v);
-    else if (dtype == MHC_BF16) load_run<VEC>(static_cast<const __nv_bfloat16 *>(p) + c, v);
-    else load_run<VEC>(static_cast<const __half *>(p) + c, v);
-}
-template <int VEC>
-__device__ __forceinline__ void load_weights(const void *w, int dtype, float offset, int c, float (&v)[VEC]) {
-    if (!w) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = 1.f;
-        return;
-    }
-    load_params<VEC>(w, dtype, c, v);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] += offset;
-}
-template <int VEC>
-__device__ __forceinline__ void load_scale(const BlockForm &f, int c, float (&v)[VEC]) {
-    if (f.scale_form == MHC_SCALE_CHANNEL) {
-        load_run<VEC>(f.res_scale + c, v);
-        return;
-    }
-    const float a = f.scale_form == MHC_SCALE_ONE ? *f.res_scale : 1.f;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = a;
-}
-template <int VEC>
-__device__ __forceinline__ void gate_values(float (&v)[VEC], int act) {
-    if (act == MHC_ACT_NONE) return;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = gate_value(v[e], act);
-}
-
-// A row's bytes are a multiple of 16 and so are its address and stride.
-inline bool rows16(const void *p, long long stride, int H, int elem, long long T) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && static_cast<long long>(H) * elem % 16 == 0 &&
-           (T == 1 || stride * elem % 16 == 0);
+// Rows of runs: 8 elements a multiple of what a row's address and stride are
+// multiples of (16 bytes; 32 for fp32).
+inline bool rows_of_runs(const void *p, long long stride, int elem, long long T) {
+    return reinterpret_cast<uintptr_t>(p) % (8 * elem) == 0 && (T == 1 || stride % 8 == 0);
 }
 inline int elem_bytes(int dtype) { return dtype == MHC_F32 ? 4 : 2; }
 // Weights and scales can be read 8 at a time.
-inline bool params16(const BlockForm &f) {
+inline bool params_of_runs(const BlockForm &f) {
     const void *const p[] = {f.w_post, f.w_pre, f.scale_form == MHC_SCALE_CHANNEL ? f.res_scale : nullptr,
                              f.gate_form == MHC_GATE_CHANNEL ? f.gate : nullptr};
     for (const void *q : p)
-        if (reinterpret_cast<uintptr_t>(q) & 15u) return false;
+        if (reinterpret_cast<uintptr_t>(q) & 31u) return false;
     return true;
 }
 
@@ -103,7 +238,7 @@ struct SmemGrant {
 };
 template <class K>
 inline cudaError_t grant_smem(K kern, SmemGrant &g, size_t smem, size_t most) {
-    if (smem <= 48 * 1024) return cudaSuccess;
+    if (smem <= 32 * 1024) return cudaSuccess;      // with the kernels' static arrays, below 48 KB
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     std::atomic<int> &cur = g.bytes[dev & 63];

@@ -1,0 +1,14 @@
+// The gated residual block's row kernels: y of __nv_bfloat16, residual of __nv_bfloat16.
+#include "block_backward.cuh"
+#include "block_forward.cuh"
+
+namespace mhc {
+
+cudaError_t block_fwd_bf16(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bool pdl, cudaStream_t s) {
+    return block_fwd<__nv_bfloat16, __nv_bfloat16>(a, dtype, r_dtype, sms, pdl, s);
+}
+cudaError_t block_bwd_bf16(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bool pdl, int *parts, cudaStream_t s) {
+    return block_bwd<__nv_bfloat16, __nv_bfloat16>(a, dtype, r_dtype, sms, pdl, parts, s);
+}
+
+}  // namespace mhc

@@ -1,0 +1,93 @@
+// Dispatch of the gated residual block's row kernels by type, and the kernel that
+// ends the backward pass: sums over tokens from the row kernel's CTAs.
+#include "block_common.cuh"
+
+namespace mhc {
+
+#define MHC_ROWS(T)                                                                                              \
+    cudaError_t block_fwd_##T(const BlockFwdArgs &, int, int, int, bool, cudaStream_t);                          \
+    cudaError_t block_bwd_##T(const BlockBwdArgs &, int, int, int, bool, int *, cudaStream_t)
+MHC_ROWS(bf16);
+MHC_ROWS(bf16_f32);
+MHC_ROWS(f16);
+MHC_ROWS(f16_f32);
+MHC_ROWS(f32);
+#undef MHC_ROWS
+
+namespace {
+
+// Sums over the row kernel's CTAs, in an order that their number fixes: 32 columns a block, a warp
+// every 16th CTA, the warps' sums then in turn.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(32 * kSumWarps) block_sums_kernel(const BlockSumArgs a) {
+    __shared__ float part[kSumWarps][32];
+    griddep_wait();
+    const BlockForm &f = a.f;
+    const int H = f.H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = blockIdx.y;
+    const int c = blockIdx.x * 32 + lane;
+    float v = 0.f;
+    if (c < H) {
+#pragma unroll 4
+        for (int p = warp; p < a.parts; p += kSumWarps)
+            v += a.sums[(static_cast<long long>(p) * kBackSums + k) * H + c];
+    }
+    part[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && c < H) {
+        v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSumWarps; ++w) v += part[w][lane];
+        if (k == 0) {
+            float g = 1.f, slope = 1.f;
+            if (f.gate_form == MHC_GATE_CHANNEL) gate_both(load_any(f.gate, f.gate_dtype, c), f.gate_act, &g, &slope);
+            if (a.d_w_post) a.d_w_post[c] = g * v;
+            if (a.d_gate) a.d_gate[c] = slope * weight_at(f.w_post, f.w_post_dtype, f.weight_offset, c) * v;
+        } else if (k == 1) {
+            if (a.d_w_pre) a.d_w_pre[c] = v;
+        } else {
+            a.d_res_scale[c] = v;
+        }
+    }
+    if (k == 0 && blockIdx.x == 0 && a.d_res_scale && f.scale_form == MHC_SCALE_ONE && warp == 1) {
+        v = 0.f;
+        for (int p = lane; p < a.parts; p += 32) v += a.scale_sums[p];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) a.d_res_scale[0] = v;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bool pdl, cudaStream_t s) {
+    const bool wide = r_dtype == MHC_F32;
+    auto rows = dtype == MHC_F32 ? block_fwd_f32
+                : dtype == MHC_BF16 ? (wide ? block_fwd_bf16_f32 : block_fwd_bf16)
+                                    : (wide ? block_fwd_f16_f32 : block_fwd_f16);
+    return rows(a, dtype, r_dtype, sms, pdl, s);
+}
+
+cudaError_t launch_block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bool pdl, int *parts,
+                             cudaStream_t s) {
+    const bool wide = r_dtype == MHC_F32;
+    auto rows = dtype == MHC_F32 ? block_bwd_f32
+                : dtype == MHC_BF16 ? (wide ? block_bwd_bf16_f32 : block_bwd_bf16)
+                                    : (wide ? block_bwd_f16_f32 : block_bwd_f16);
+    return rows(a, dtype, r_dtype, sms, pdl, parts, s);
+}
+
+cudaError_t launch_block_sums(const BlockSumArgs &a, bool pdl, cudaStream_t s) {
+    const unsigned kinds = a.d_res_scale && a.f.scale_form == MHC_SCALE_CHANNEL ? 3 : 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.f.H + 31) / 32), kinds);
+    cfg.blockDim = dim3(32 * kSumWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, block_sums_kernel, a);
+}
+
+}  // namespace mhc

@@ -36,8 +36,8 @@ __global__ void ckpt_unpack_kernel(const CkptArgs a, int format) {
     }
 }
 
-// Eight values a lane, four lanes a group, for rows on 16-byte boundaries with
-// H a multiple of 8. A lane has kRuns runs in flight, each a block's width
+// Eight values a lane, four lanes a group, for rows on boundaries of 8 elements
+// with H a multiple of 8. A lane has kRuns runs in flight, each a block's width
 // from the next; the lanes past a row's end (where H is no multiple of 32)
 // hold zeros, so that every lane takes part in its group's maximum.
 constexpr int kRuns = 4;
@@ -59,20 +59,19 @@ __global__ void __launch_bounds__(kThreads) ckpt_pack_vec_kernel(const CkptArgs 
     const int groups = (a.H + 31) / 32;
     // whole warps enter: a warp's runs start at a multiple of 32, and total is one of 4
     for (I i0 = static_cast<I>(blockIdx.x) * (kThreads * kRuns) + (threadIdx.x & ~31u); i0 < total; i0 += step) {
-        float v[kRuns][8];
+        Run v[kRuns];
         long long t[kRuns];
         int c[kRuns];
         bool in[kRuns];
 #pragma unroll
         for (int r = 0; r < kRuns; ++r) {
             in[r] = run_place<I>(i0 + r * kThreads + (threadIdx.x & 31), total, per_row, a.H, &t[r], &c[r]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[r][e] = 0.f;
-            if (in[r]) load_run<8>(static_cast<const T *>(a.x) + t[r] * a.stride + c[r], v[r]);
+            v[r] = run_splat(0.f);
+            if (in[r]) v[r] = load8(static_cast<const T *>(a.x) + t[r] * a.stride + c[r]);
         }
 #pragma unroll
         for (int r = 0; r < kRuns; ++r) {
-            const uint32_t byte = ckpt_byte_quad<FMT>(v[r], 0xffffffffu);
+            const uint32_t byte = ckpt_byte_quad<FMT>(v[r]);
             if (!in[r]) continue;
             *reinterpret_cast<uint2 *>(a.c.codes + t[r] * a.H + c[r]) = ckpt_codes8<FMT>(v[r], byte);
             if ((threadIdx.x & 3) == 0) a.c.scales[t[r] * groups + c[r] / 32] = static_cast<uint8_t>(byte);
@@ -102,17 +101,15 @@ __global__ void __launch_bounds__(kThreads) ckpt_unpack_vec_kernel(const CkptArg
 #pragma unroll
         for (int r = 0; r < kRuns; ++r) {
             if (!in[r]) continue;
-            float v[8];
-            ckpt_values8(w[r], byte[r], FMT, v);
-            store_run<8>(static_cast<T *>(a.out) + t[r] * a.stride + c[r], v);
+            store8(static_cast<T *>(a.out) + t[r] * a.stride + c[r], ckpt_values8(w[r], byte[r], FMT));
         }
     }
 }
 
-// Whether the runs of 8 are there: rows of x on 16-byte boundaries, of codes on 8-byte ones.
+// Whether the runs of 8 are there: rows of x on boundaries of 8 elements, of codes on 8-byte ones.
 bool runs_fit(const CkptArgs &a, const void *x, int elem) {
-    return a.H % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 &&
-           (reinterpret_cast<uintptr_t>(a.c.codes) & 7u) == 0 && (a.T == 1 || a.stride * elem % 16 == 0);
+    return a.H % 8 == 0 && reinterpret_cast<uintptr_t>(x) % (8 * elem) == 0 &&
+           (reinterpret_cast<uintptr_t>(a.c.codes) & 7u) == 0 && (a.T == 1 || a.stride % 8 == 0);
 }
 // The index type: 32 bits where the runs and a grid's step past them fit.
 bool small_index(const CkptArgs &a) { return a.T * ckpt_groups(a.H) * 4 < (1ll << 31); }

@@ -1,146 +1,155 @@
-// Runs of VEC consecutive elements of a row as fp32 values: VEC 8 by 16-byte
-// loads and stores (which need the row on a 16-byte boundary), VEC 1 by
-// single elements, for rows on any boundary.
+// Runs of 8 values of a row as 4 packed pairs of fp32 (f32x2 arithmetic), and
+// their 8-bit checkpoints.
 #pragma once
 #include "block_common.cuh"
 
 namespace mhc {
 
-template <int VEC>
-__device__ __forceinline__ void load_run(const float *p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
+struct Run {
+    uint64_t p[4];
+};
+__device__ __forceinline__ uint64_t splat2(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ float run_at(const Run &r, int e) { return e & 1 ? f2_hi(r.p[e >> 1]) : f2_lo(r.p[e >> 1]); }
+__device__ __forceinline__ Run run_of(const float (&v)[8]) {
+    Run r;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = p[e];
-    }
+    for (int i = 0; i < 4; ++i) r.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+    return r;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w, const __nv_bfloat16 *) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+__device__ __forceinline__ Run run_splat(float v) {
+    Run r;
+    r.p[0] = r.p[1] = r.p[2] = r.p[3] = splat2(v);
+    return r;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w, const __half *) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+
+__device__ __forceinline__ uint64_t unpack2(uint32_t w, const __nv_bfloat16 *) { return bf2_unpack(w); }
+__device__ __forceinline__ uint64_t unpack2(uint32_t w, const __half *) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return f2_pack(f.x, f.y);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16 *) {
-    return bf2_pack_rn(f2_pack(a, b));
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, const __half *) {
-    const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t pack2(uint64_t v, const __nv_bfloat16 *) { return bf2_pack_rn(v); }
+__device__ __forceinline__ uint32_t pack2(uint64_t v, const __half *) {
+    const __half2 h = __floats2half2_rn(f2_lo(v), f2_hi(v));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-template <int VEC, class T>
-__device__ __forceinline__ void unpack_run(const uint4 &w, float (&v)[VEC], const T *tag) {
-    static_assert(VEC == 8, "eight 16-bit values a vector");
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack2(u[e], tag);
-        v[2 * e] = f.x;
-        v[2 * e + 1] = f.y;
-    }
+// 8 consecutive values of a row in global memory: 16-bit ones from a 16-byte
+// boundary, fp32 from a 32-byte one.
+__device__ __forceinline__ Run load8(const float *p) {
+    Run r;
+    asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
+                 : "=l"(r.p[0]), "=l"(r.p[1]), "=l"(r.p[2]), "=l"(r.p[3])
+                 : "l"(reinterpret_cast<uint64_t>(p)) : "memory");
+    return r;
 }
-template <int VEC, class T>
-__device__ __forceinline__ void load_run(const T *p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        unpack_run<VEC>(*reinterpret_cast<const uint4 *>(p), v, p);
-    } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = to_f32(p[e]);
-    }
+template <class T>
+__device__ __forceinline__ Run unpack8(const uint4 &w, const T *tag) {
+    Run r;
+    r.p[0] = unpack2(w.x, tag);
+    r.p[1] = unpack2(w.y, tag);
+    r.p[2] = unpack2(w.z, tag);
+    r.p[3] = unpack2(w.w, tag);
+    return r;
 }
-template <int VEC>
-__device__ __forceinline__ void store_run(float *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) p[e] = v[e];
-    }
+template <class T>
+__device__ __forceinline__ Run load8(const T *p) {
+    return unpack8(*reinterpret_cast<const uint4 *>(p), p);
 }
-template <int VEC, class T>
-__device__ __forceinline__ void store_run(T *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(v[0], v[1], p), pack2(v[2], v[3], p),
-                                                   pack2(v[4], v[5], p), pack2(v[6], v[7], p));
-    } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) p[e] = from_f32<T>(v[e]);
-    }
+// The same from shared memory. fp32: neighbouring threads' 32 bytes would put
+// two of every eight on the same banks; every other four threads read their
+// second half first.
+__device__ __forceinline__ Run load8_shared(const float *p) {
+    const ulonglong2 *const q = reinterpret_cast<const ulonglong2 *>(p);
+    const int swap = (threadIdx.x >> 2) & 1;
+    const ulonglong2 a = q[swap], b = q[swap ^ 1];
+    Run r;
+    r.p[0] = swap ? b.x : a.x;
+    r.p[1] = swap ? b.y : a.y;
+    r.p[2] = swap ? a.x : b.x;
+    r.p[3] = swap ? a.y : b.y;
+    return r;
+}
+template <class T>
+__device__ __forceinline__ Run load8_shared(const T *p) {
+    return unpack8(*reinterpret_cast<const uint4 *>(p), p);
+}
+__device__ __forceinline__ void store8(float *p, const Run &r) {
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};"
+                 ::"l"(reinterpret_cast<uint64_t>(p)), "l"(r.p[0]), "l"(r.p[1]), "l"(r.p[2]), "l"(r.p[3]) : "memory");
+}
+template <class T>
+__device__ __forceinline__ void store8(T *p, const Run &r) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(r.p[0], p), pack2(r.p[1], p), pack2(r.p[2], p), pack2(r.p[3], p));
 }
 
 // ---------------------------------------------------------------- checkpoints
 // Four codes in a word, from four scaled values.
 template <int FMT>
-__device__ __forceinline__ uint32_t ckpt_code4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t ckpt_code4(uint64_t a, uint64_t b) {
     if (FMT == MHC_CKPT_E4M3) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f2_lo(a), f2_hi(a)), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f2_lo(b), f2_hi(b)), __NV_SATFINITE, __NV_E4M3);
         return lo | (hi << 16);
     }
     // x + 1.5 * 2^23 rounds x to a whole number, ties to even, in its lowest byte
-    const uint32_t w0 = __float_as_uint(a + 12582912.f), w1 = __float_as_uint(b + 12582912.f);
-    const uint32_t w2 = __float_as_uint(c + 12582912.f), w3 = __float_as_uint(d + 12582912.f);
-    return __byte_perm(__byte_perm(w0, w1, 0x0040), __byte_perm(w2, w3, 0x0040), 0x5410);
+    const uint64_t one = splat2(12582912.f);
+    const uint64_t u = add2(a, one), v = add2(b, one);
+    return __byte_perm(__byte_perm(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32), 0x0040),
+                       __byte_perm(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32), 0x0040), 0x5410);
 }
 // Four codes' values, unscaled.
 template <int FMT>
-__device__ __forceinline__ void ckpt_value4(uint32_t w, float (&v)[4]) {
+__device__ __forceinline__ void ckpt_value4(uint32_t w, uint64_t *a, uint64_t *b) {
     if (FMT == MHC_CKPT_E4M3) {
         const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
         const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-        const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
-        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+        const float2 f = __half22float2(__half2(lo)), g = __half22float2(__half2(hi));
+        *a = f2_pack(f.x, f.y);
+        *b = f2_pack(g.x, g.y);
     } else {
         // code + 128 in the low byte of 2^23: minus 2^23 + 128 is the code
         const uint32_t u = w ^ 0x80808080u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[e] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u | e)) - 8388736.f;
+        const uint64_t off = splat2(-8388736.f);
+        *a = add2((static_cast<uint64_t>(__byte_perm(u, 0x4B000000u, 0x7441)) << 32) | __byte_perm(u, 0x4B000000u, 0x7440), off);
+        *b = add2((static_cast<uint64_t>(__byte_perm(u, 0x4B000000u, 0x7443)) << 32) | __byte_perm(u, 0x4B000000u, 0x7442), off);
     }
 }
 // Scale byte of the group of which this lane holds 8 values and its 3
-// neighbours (lanes 4 i .. 4 i + 3) the rest; `m` the largest magnitude of the
-// lane's own, as bits.
+// neighbours (lanes 4 i .. 4 i + 3) the rest. Whole warps call it.
 template <int FMT>
-__device__ __forceinline__ uint32_t ckpt_byte_quad(const float (&v)[8], unsigned mask) {
+__device__ __forceinline__ uint32_t ckpt_byte_quad(const Run &r) {
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const uint32_t b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+        const uint32_t b = __float_as_uint(run_at(r, e)) & 0x7FFFFFFFu;
         m = m > b ? m : b;
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        const uint32_t n = __shfl_xor_sync(mask, m, o);
+        const uint32_t n = __shfl_xor_sync(0xffffffffu, m, o);
         m = m > n ? m : n;
     }
     return ckpt_scale_byte<FMT>(m);
 }
 template <int FMT>
-__device__ __forceinline__ uint2 ckpt_codes8(const float (&v)[8], uint32_t byte) {
+__device__ __forceinline__ uint2 ckpt_codes8(const Run &r, uint32_t byte) {
     if (byte == 255u) return make_uint2(0u, 0u);
-    const float s = ckpt_inverse(byte);
-    return make_uint2(ckpt_code4<FMT>(v[0] * s, v[1] * s, v[2] * s, v[3] * s),
-                      ckpt_code4<FMT>(v[4] * s, v[5] * s, v[6] * s, v[7] * s));
+    const uint64_t s = splat2(ckpt_inverse(byte));
+    return make_uint2(ckpt_code4<FMT>(mul2(r.p[0], s), mul2(r.p[1], s)),
+                      ckpt_code4<FMT>(mul2(r.p[2], s), mul2(r.p[3], s)));
 }
-__device__ __forceinline__ void ckpt_values8(uint2 w, uint32_t byte, int format, float (&v)[8]) {
-    float a[4], b[4];
+__device__ __forceinline__ Run ckpt_values8(uint2 w, uint32_t byte, int format) {
+    Run r;
     if (format == MHC_CKPT_E4M3) {
-        ckpt_value4<MHC_CKPT_E4M3>(w.x, a);
-        ckpt_value4<MHC_CKPT_E4M3>(w.y, b);
+        ckpt_value4<MHC_CKPT_E4M3>(w.x, &r.p[0], &r.p[1]);
+        ckpt_value4<MHC_CKPT_E4M3>(w.y, &r.p[2], &r.p[3]);
     } else {
-        ckpt_value4<MHC_CKPT_INT8>(w.x, a);
-        ckpt_value4<MHC_CKPT_INT8>(w.y, b);
+        ckpt_value4<MHC_CKPT_INT8>(w.x, &r.p[0], &r.p[1]);
+        ckpt_value4<MHC_CKPT_INT8>(w.y, &r.p[2], &r.p[3]);
     }
-    const float s = ckpt_unit(byte);
+    const uint64_t s = splat2(ckpt_unit(byte));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[e] = a[e] * s;
-        v[4 + e] = b[e] * s;
-    }
+    for (int i = 0; i < 4; ++i) r.p[i] = mul2(r.p[i], s);
+    return r;
 }
 
 }  // namespace mhc
