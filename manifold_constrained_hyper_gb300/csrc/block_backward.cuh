@@ -13,6 +13,8 @@
 // would not leave room for the row, and in shared memory not for the rows to
 // come. The sums leave it once, and a second kernel adds the CTAs' in their order.
 #pragma once
+#include <type_traits>
+
 #include "block_rows.cuh"
 
 namespace mhc {
@@ -35,7 +37,9 @@ enum BwdArray : int { T_W1, T_W2, T_SCALE, T_DW1, T_DW2, T_DSCALE };
 struct BwdRing {
     int groups;                                     // of a CTA, blockDim.x / groups threads each
     int stages;
-    uint32_t bytes[5], stage_bytes;                 // y, residual (or their codes), d_ro, d_h, gate: of a row
+    // bytes of a row's place in a stage, 0 where there is none: y, residual (or their
+    // codes), d_ro, d_h, gate, the scale bytes of y and residual
+    uint32_t place[7], stage_bytes;
     unsigned int *status;
     unsigned long long timeout_ns;
 };
@@ -45,6 +49,7 @@ struct BwdRing {
 template <class TY, class TR, int MODE, bool FULL, bool SCALED, bool HELD>
 __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBwdArgs a, const BwdRing ring) {
     constexpr int RUNS = kBwdRuns, MAXW = kBwdThreads / 32;
+    constexpr bool STAGED = MODE != ROWS_VEC;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float red[kBwdGroups][2][3 * MAXW];
     __shared__ __align__(8) uint64_t bars[kBwdStages];
@@ -61,7 +66,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     const int warp = tid >> 5, warps = at.threads >> 5;
     const bool full_gate = FULL && f.gate_form == MHC_GATE_FULL, scaled = SCALED && f.scale_form == MHC_SCALE_CHANNEL;
     const bool token_gate = f.gate_form == MHC_GATE_TOKEN;
-    const size_t ge = f.gate_dtype == MHC_F32 ? 4 : 2;
+    const uint32_t ge = f.gate_dtype == MHC_F32 ? 4 : 2;
+    const bool y_held = HELD && !a.y, r_held = HELD && !a.residual;
     const uint32_t bar = smem_addr(bars);
 
     if (threadIdx.x < 32) {
@@ -69,7 +75,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         tmem_relinquish();
     }
     for (int i = threadIdx.x; i < kBwdGroups * 2 * 3 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
-    if (MODE == ROWS_RING && threadIdx.x == 0) {
+    if (STAGED && threadIdx.x == 0) {
         for (int s = 0; s < ring.stages; ++s) mbar_init(bar + 8 * s, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -86,27 +92,47 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     // groups takes row k, from stage k mod stages.
     const long long row0 = blockIdx.x + static_cast<long long>(grp) * gridDim.x;
     const long long row_step = static_cast<long long>(gridDim.x) * ring.groups;
+    // where a row's parts begin in global memory, and their bytes
+    struct Source {
+        const void *p[7];
+        uint32_t bytes[7];
+    };
+    auto source = [&](long long t) {
+        Source c = {};
+        c.p[0] = y_held ? static_cast<const void *>(a.ck_y.codes + t * H) : static_cast<const TY *>(a.y) + t * a.y_stride;
+        c.bytes[0] = H * (y_held ? 1 : sizeof(TY));
+        c.p[1] = r_held ? static_cast<const void *>(a.ck_r.codes + t * H)
+                        : static_cast<const TR *>(a.residual) + t * a.r_stride;
+        c.bytes[1] = H * (r_held ? 1 : sizeof(TR));
+        c.p[2] = static_cast<const TR *>(a.d_ro) + t * a.d_ro_stride;
+        c.bytes[2] = a.d_ro ? H * sizeof(TR) : 0;
+        c.p[3] = static_cast<const TY *>(a.d_h) + t * a.d_h_stride;
+        c.bytes[3] = H * sizeof(TY);
+        c.p[4] = static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge;
+        c.bytes[4] = full_gate ? H * ge : 0;
+        c.p[5] = a.ck_y.scales + t * groups;
+        c.bytes[5] = y_held ? groups : 0;
+        c.p[6] = a.ck_r.scales + t * groups;
+        c.bytes[6] = r_held ? groups : 0;
+        return c;
+    };
+    constexpr int PARTS = HELD ? 7 : FULL ? 5 : 4;
     auto fetch = [&](long long t, int s) {          // one thread
         const uint32_t b = bar + 8 * s;
-        uint32_t dst = smem_addr(smem) + s * ring.stage_bytes;
+        uint32_t dst = smem_addr(smem) + s * ring.stage_bytes, total = 0;
         const uint64_t pol = policy_evict_first();
-        mbar_arrive_expect_tx(b, ring.stage_bytes);
-        bulk_load(dst, !HELD || a.y ? static_cast<const void *>(static_cast<const TY *>(a.y) + t * a.y_stride)
-                                    : a.ck_y.codes + t * H, ring.bytes[0], b, pol);
-        dst += ring.bytes[0];
-        bulk_load(dst, !HELD || a.residual
-                           ? static_cast<const void *>(static_cast<const TR *>(a.residual) + t * a.r_stride)
-                           : a.ck_r.codes + t * H, ring.bytes[1], b, pol);
-        dst += ring.bytes[1];
-        if (ring.bytes[2])
-            bulk_load(dst, static_cast<const TR *>(a.d_ro) + t * a.d_ro_stride, ring.bytes[2], b, pol);
-        dst += ring.bytes[2];
-        bulk_load(dst, static_cast<const TY *>(a.d_h) + t * a.d_h_stride, ring.bytes[3], b, pol);
-        dst += ring.bytes[3];
-        if (FULL && ring.bytes[4])
-            bulk_load(dst, static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge, ring.bytes[4], b, pol);
+        const Source c = source(t);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k)
+            if (c.bytes[k]) total += skewed_bytes(c.p[k], c.bytes[k]);
+        mbar_arrive_expect_tx(b, total);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            if (c.bytes[k]) bulk_load_row(dst, c.p[k], c.bytes[k], b, pol);
+            dst += ring.place[k];
+        }
     };
-    if (MODE == ROWS_RING && threadIdx.x == 0)
+    if (STAGED && threadIdx.x == 0)
         for (int s = 0; s < ring.stages; ++s) {
             const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
             if (t < f.T) fetch(t, s);
@@ -145,7 +171,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     struct Ahead {
         float rstd1, rstd2;
         uint32_t token;                             // bits of its gate
-        uint32_t by[RUNS], br[RUNS];                // scale bytes of the runs, where rows are vectors
     };
     auto ahead = [&](long long t) {
         Ahead n = {};
@@ -155,13 +180,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         if (token_gate)
             n.token = f.gate_dtype == MHC_F32 ? static_cast<const uint32_t *>(f.gate)[t * f.gate_stride]
                                               : static_cast<const uint16_t *>(f.gate)[t * f.gate_stride];
-        if (MODE == ROWS_ANY || !HELD) return n;
-#pragma unroll
-        for (int j = 0; j < RUNS; ++j) {
-            const int g = run_read_col(at, j) / 32;
-            if (!a.y) n.by[j] = a.ck_y.scales[t * groups + g];
-            if (!a.residual) n.br[j] = a.ck_r.scales[t * groups + g];
-        }
         return n;
     };
     auto token_of = [&](uint32_t bits) {
@@ -185,51 +203,57 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         const float rstd1 = f.post_norm ? now.rstd1 : 1.f, rstd2 = now.rstd2;
         float token = 1.f, token_slope = 0.f;
         if (token_gate) gate_both(token_of(now.token), f.gate_act, &token, &token_slope);
-        const uint8_t *const st = smem + s * ring.stage_bytes;
-        const uint8_t *const st_r = st + ring.bytes[0], *const st_f = st_r + ring.bytes[1],
-                      *const st_h = st_f + ring.bytes[2], *const st_g = st_h + ring.bytes[3];
-        if (MODE == ROWS_RING) {
+        const uint8_t *st[7];
+        st[0] = smem + s * ring.stage_bytes;
+#pragma unroll
+        for (int k = 1; k < PARTS; ++k) st[k] = st[k - 1] + ring.place[k - 1];
+        if (STAGED) {
             ok = mbar_wait(bar + 8 * s, phase, &abort_flag, ring.timeout_ns, ring.status, SITE_BWD_ROW) && ok;
             __syncwarp();
         }
 
         // a run of y, the residual, the gradients, the full gate, from the stage or from memory
-        auto held = [&](const Ckpt &c, const uint8_t *staged, uint32_t byte, int j) {
+        auto row_run = [&](int k, const auto *row, int j) {
+            using T = typename std::remove_cv<typename std::remove_reference<decltype(*row)>::type>::type;
+            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const T *>(st[k]), at, j);
+            else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(row, at, j);
+            else return staged_single(reinterpret_cast<const T *>(st[k] + skew16(row)), at, j);
+        };
+        auto held = [&](const Ckpt &c, int k, int k_scales, int j) {
+            const uint8_t *const codes = c.codes + t * H, *const scales = c.scales + t * groups;
+            const uint8_t *const byte_at = STAGED ? st[k_scales] + skew16(scales) : scales;
             if constexpr (MODE != ROWS_ANY) {
-                const uint8_t *const codes = MODE == ROWS_RING ? staged : c.codes + t * H;
-                return ckpt_values8(*reinterpret_cast<const uint2 *>(codes + run_read_col(at, j)), byte, a.format);
+                const int i = run_read_col(at, j);
+                return ckpt_values8(*reinterpret_cast<const uint2 *>((STAGED ? st[k] : codes) + i), byte_at[i / 32], a.format);
             } else {
                 const int col = run_col<MODE>(at, j);
+                const uint8_t *const code_at = st[k] + skew16(codes);
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int i = col + e * at.threads;
-                    v[e] = i < H ? ckpt_load(c, a.format, t, H, groups, i) : 0.f;
+                    v[e] = 0.f;
+                    if (i < H)
+                        v[e] = (a.format == MHC_CKPT_E4M3 ? ckpt_value<MHC_CKPT_E4M3>(code_at[i])
+                                                          : ckpt_value<MHC_CKPT_INT8>(code_at[i])) *
+                               ckpt_unit(byte_at[i / 32]);
                 }
                 return run_of(v);
             }
         };
         auto load_y = [&](int j) {
-            if (HELD && !a.y) return held(a.ck_y, st, now.by[j], j);
-            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st), at, j);
-            else return load_run<MODE>(static_cast<const TY *>(a.y) + t * a.y_stride, at, j);
+            if (y_held) return held(a.ck_y, 0, 5, j);
+            return row_run(0, static_cast<const TY *>(a.y) + t * a.y_stride, j);
         };
         auto load_r = [&](int j) {
-            if (HELD && !a.residual) return held(a.ck_r, st_r, now.br[j], j);
-            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(st_r), at, j);
-            else return load_run<MODE>(static_cast<const TR *>(a.residual) + t * a.r_stride, at, j);
+            if (r_held) return held(a.ck_r, 1, 6, j);
+            return row_run(1, static_cast<const TR *>(a.residual) + t * a.r_stride, j);
         };
-        auto load_dh = [&](int j) {
-            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st_h), at, j);
-            else return load_run<MODE>(static_cast<const TY *>(a.d_h) + t * a.d_h_stride, at, j);
-        };
-        auto load_df = [&](int j) {
-            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(st_f), at, j);
-            else return load_run<MODE>(static_cast<const TR *>(a.d_ro) + t * a.d_ro_stride, at, j);
-        };
+        auto load_df = [&](int j) { return row_run(2, static_cast<const TR *>(a.d_ro) + t * a.d_ro_stride, j); };
+        auto load_dh = [&](int j) { return row_run(3, static_cast<const TY *>(a.d_h) + t * a.d_h_stride, j); };
         auto load_z = [&](int j) {
-            if constexpr (MODE == ROWS_RING) return staged_run_any(st_g, f.gate_dtype, at, j);
-            else return load_run_any<MODE>(static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge, f.gate_dtype, at, j);
+            return f.gate_dtype == MHC_F32 ? row_run(4, static_cast<const float *>(f.gate) + t * f.gate_stride, j)
+                                           : row_run(4, static_cast<const TY *>(f.gate) + t * f.gate_stride, j);
         };
 
         const uint64_t r2 = splat2(rstd2), tr2 = splat2(token * rstd1);
@@ -274,7 +298,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         float sum[3] = {f2_lo(s0) + f2_hi(s0), f2_lo(s1) + f2_hi(s1), f2_lo(s2) + f2_hi(s2)};
         group_sum<3, MAXW>(sum, red[grp][which], 1 + grp, warp, warps);
         which ^= 1;
-        if (MODE == ROWS_RING) {
+        if (STAGED) {
             // every thread of the group is past its row before: that row's stage is free
             if (warps == 1) __syncwarp();
             const long long refill = t - row_step + static_cast<long long>(ring.stages) * gridDim.x;
@@ -358,7 +382,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         tmem_st_wait();
         if (token_gate && a.d_gate && tid == 0) static_cast<float *>(a.d_gate)[t] = token_slope * rstd1 * c1;
     }
-    if (MODE == ROWS_RING && !ok && tid == 0) {
+    if (STAGED && !ok && tid == 0) {
         // copies that may still be in flight, before the CTA's memory goes: each
         // stage's last, in either parity
         int gave_up = 0;
@@ -435,7 +459,7 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     const bool full = f.gate_form == MHC_GATE_FULL, scaled = f.scale_form == MHC_SCALE_CHANNEL;
     const bool held = !a.y || !a.residual;
     auto codes_fit = [&](const Ckpt &c) { return (reinterpret_cast<uintptr_t>(c.codes) & 15u) == 0; };
-    const bool vec = H % 8 == 0 && (a.y ? rows_of_runs(a.y, a.y_stride, sizeof(TY), f.T) : codes_fit(a.ck_y)) &&
+    const bool vec = H % (held ? 16 : 8) == 0 && (a.y ? rows_of_runs(a.y, a.y_stride, sizeof(TY), f.T) : codes_fit(a.ck_y)) &&
                      (a.residual ? rows_of_runs(a.residual, a.r_stride, sizeof(TR), f.T) : codes_fit(a.ck_r)) &&
                      (!a.d_ro || rows_of_runs(a.d_ro, a.d_ro_stride, sizeof(TR), f.T)) &&
                      rows_of_runs(a.d_h, a.d_h_stride, sizeof(TY), f.T) && rows_of_runs(a.d_y, H, sizeof(TY), f.T) &&
@@ -452,19 +476,23 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     const unsigned grid = static_cast<unsigned>(f.T < sms ? f.T : sms);
     *parts = static_cast<int>(grid);
     const size_t column = static_cast<size_t>(threads) * kBwdRuns * 32;     // the groups' sums at the end
-    if (!vec) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, column, pdl, s);
-    ring.bytes[0] = H * (a.y ? sizeof(TY) : 1);
-    ring.bytes[1] = H * (a.residual ? sizeof(TR) : 1);
-    ring.bytes[2] = a.d_ro ? H * sizeof(TR) : 0;
-    ring.bytes[3] = H * sizeof(TY);
-    ring.bytes[4] = full ? H * elem_bytes(f.gate_dtype) : 0;
-    for (uint32_t b : ring.bytes) ring.stage_bytes += b;
+    const int scale_bytes = static_cast<int>(ckpt_groups(H));
+    ring.place[0] = row_place(H, a.y ? sizeof(TY) : 1, !vec);
+    ring.place[1] = row_place(H, a.residual ? sizeof(TR) : 1, !vec);
+    ring.place[2] = a.d_ro ? row_place(H, sizeof(TR), !vec) : 0;
+    ring.place[3] = row_place(H, sizeof(TY), !vec);
+    ring.place[4] = full ? row_place(H, elem_bytes(f.gate_dtype), !vec) : 0;
+    ring.place[5] = a.y ? 0 : row_place(scale_bytes, 1, true);
+    ring.place[6] = a.residual ? 0 : row_place(scale_bytes, 1, true);
+    for (uint32_t b : ring.place) ring.stage_bytes += b;
     long long stages = static_cast<long long>(kBwdSmem / ring.stage_bytes);
     if (stages > kBwdStages) stages = kBwdStages;
     if (stages > rows) stages = rows;
-    // codes' rows on 16-byte boundaries, more than a row an SM, and two stages at least
-    if ((held && H % 16 != 0) || stages < 2)
+    // two stages at least, or all of the rows; else (the widest types above 5000 columns and more) from memory
+    if (stages < 2 && stages < rows) {
+        if (!vec) return launch_block_bwd_loop(a, dtype, r_dtype, pdl, parts, s);
         return bwd_launch<TY, TR, ROWS_VEC, true, true, true>(a, ring, grid, threads, column, pdl, s);
+    }
     // a stage for each group and one to fill meanwhile, or all of the rows
     if (ring.groups >= stages) ring.groups = static_cast<int>(stages == rows ? stages : stages - 1);
     ring.stages = static_cast<int>(stages);
@@ -473,6 +501,7 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     int n = 0;
     if (require_device(&n, &ring.status)) return cudaErrorUnknown;
     ring.timeout_ns = wait_timeout_ns();
+    if (!vec) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (full) return bwd_launch<TY, TR, ROWS_RING, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (held)
         return scaled ? bwd_launch<TY, TR, ROWS_RING, false, true, true>(a, ring, grid, threads, smem, pdl, s)

@@ -28,17 +28,18 @@ enum FwdSite : int { SITE_FWD_ROW = 70 };
 struct FwdRing {
     int groups;                                     // of a CTA, blockDim.x / groups threads each
     int stages;
-    uint32_t y_bytes, r_bytes, g_bytes;             // of a row; g_bytes 0: no full gate
+    uint32_t y_place, r_place, g_place;             // bytes of a row's place in a stage; g_place 0: no full gate
     unsigned int *status;
     unsigned long long timeout_ns;
 };
 
 // FULL, SCALED, CKPT: whether a call may have a full gate, a channel scale,
-// checkpoints. RUNS of 8 columns a thread: 4 in blocks of up to 512 threads of 128
-// registers; 1, up to 1024 threads of 64, where a CTA has one row only.
+// checkpoints. RUNS of 8 columns a thread: 4, and 2 of single elements, in blocks of up to 512 threads of
+// 128 registers; 1, up to 1024 threads of 64, where a CTA has one row only.
 template <class TY, class TR, int MODE, int RUNS, bool FULL, bool SCALED, bool CKPT>
 __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(const BlockFwdArgs a, const FwdRing ring) {
-    constexpr int MAXW = RUNS == 1 ? 32 : 8, GROUPS = RUNS == 1 ? 1 : kFwdGroups;
+    constexpr int MAXW = 32 / RUNS, GROUPS = RUNS == 1 ? 1 : kFwdGroups;
+    constexpr bool STAGED = MODE != ROWS_VEC;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float red[GROUPS][2][MAXW];
     __shared__ __align__(8) uint64_t bars[kFwdStages];
@@ -51,8 +52,9 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     at.thread = threadIdx.x - grp * at.threads;
     const int warp = at.thread >> 5, warps = at.threads >> 5;
     const bool full_gate = FULL && f.gate_form == MHC_GATE_FULL;
-    const uint32_t stage_bytes = ring.y_bytes + ring.r_bytes + ring.g_bytes;
-    const size_t ge = f.gate_dtype == MHC_F32 ? 4 : 2;
+    const uint32_t stage_bytes = ring.y_place + ring.r_place + ring.g_place;
+    const uint32_t ge = f.gate_dtype == MHC_F32 ? 4 : 2;
+    const uint32_t y_bytes = f.H * sizeof(TY), r_bytes = f.H * sizeof(TR), g_bytes = f.H * ge;    // of a row
     // (w_post + offset) * act of a channel gate; w_pre + offset; a channel scale; then the stages
     float *const w1_kept = reinterpret_cast<float *>(smem), *const w2_kept = w1_kept + 8 * RUNS * at.threads,
           *const sc_kept = w2_kept + 8 * RUNS * at.threads;
@@ -60,7 +62,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     const uint32_t bar = smem_addr(bars);
 
     for (int i = threadIdx.x; i < GROUPS * 2 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
-    if (MODE == ROWS_RING && threadIdx.x == 0) {
+    if (STAGED && threadIdx.x == 0) {
         for (int s = 0; s < ring.stages; ++s) mbar_init(bar + 8 * s, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -72,14 +74,23 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     auto fetch = [&](long long t, int s) {          // one thread
         const uint32_t b = bar + 8 * s, dst = smem_addr(smem) + stage0 + s * stage_bytes;
         const uint64_t pol = policy_evict_first();
-        mbar_arrive_expect_tx(b, stage_bytes);
-        bulk_load(dst, static_cast<const TY *>(a.y) + t * a.y_stride, ring.y_bytes, b, pol);
-        bulk_load(dst + ring.y_bytes, static_cast<const TR *>(a.residual) + t * a.r_stride, ring.r_bytes, b, pol);
-        if (FULL && ring.g_bytes)
-            bulk_load(dst + ring.y_bytes + ring.r_bytes,
-                      static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge, ring.g_bytes, b, pol);
+        const TY *const y = static_cast<const TY *>(a.y) + t * a.y_stride;
+        const TR *const r = static_cast<const TR *>(a.residual) + t * a.r_stride;
+        const uint8_t *const g = static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge;
+        if (MODE == ROWS_RING) {
+            mbar_arrive_expect_tx(b, stage_bytes);
+            bulk_load(dst, y, y_bytes, b, pol);
+            bulk_load(dst + ring.y_place, r, r_bytes, b, pol);
+            if (FULL && ring.g_place) bulk_load(dst + ring.y_place + ring.r_place, g, g_bytes, b, pol);
+        } else {
+            mbar_arrive_expect_tx(b, skewed_bytes(y, y_bytes) + skewed_bytes(r, r_bytes) +
+                                         (FULL && ring.g_place ? skewed_bytes(g, g_bytes) : 0));
+            bulk_load_row(dst, y, y_bytes, b, pol);
+            bulk_load_row(dst + ring.y_place, r, r_bytes, b, pol);
+            if (FULL && ring.g_place) bulk_load_row(dst + ring.y_place + ring.r_place, g, g_bytes, b, pol);
+        }
     };
-    if (MODE == ROWS_RING && threadIdx.x == 0)
+    if (STAGED && threadIdx.x == 0)
         for (int s = 0; s < ring.stages; ++s) {
             const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
             if (t < f.T) fetch(t, s);
@@ -112,20 +123,29 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         // tensor would take the registers that hold the row
         if (MODE == ROWS_ANY) asm volatile("" : "+r"(at.thread));
         const uint8_t *const st = smem + stage0 + s * stage_bytes;
-        if (MODE == ROWS_RING)
+        if (STAGED)
             ok = mbar_wait(bar + 8 * s, phase, &abort_flag, ring.timeout_ns, ring.status, SITE_FWD_ROW) && ok;
+        const TY *const y_row = static_cast<const TY *>(a.y) + t * a.y_stride;
+        const TR *const r_row = static_cast<const TR *>(a.residual) + t * a.r_stride;
+        const uint8_t *const g_row = static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge;
         auto load_y = [&](int j) {
             if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st), at, j);
-            else return load_run<MODE>(static_cast<const TY *>(a.y) + t * a.y_stride, at, j);
+            else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(y_row, at, j);
+            else return staged_single(reinterpret_cast<const TY *>(st + skew16(y_row)), at, j);
         };
         auto load_r = [&](int j) {
-            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(st + ring.y_bytes), at, j);
-            else return load_run<MODE>(static_cast<const TR *>(a.residual) + t * a.r_stride, at, j);
+            const uint8_t *const row = st + ring.y_place;
+            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(row), at, j);
+            else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(r_row, at, j);
+            else return staged_single(reinterpret_cast<const TR *>(row + skew16(r_row)), at, j);
         };
         auto load_z = [&](int j) {
-            if constexpr (MODE == ROWS_RING)
-                return staged_run_any(st + ring.y_bytes + ring.r_bytes, f.gate_dtype, at, j);
-            else return load_run_any<MODE>(static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge, f.gate_dtype, at, j);
+            const uint8_t *const row = st + ring.y_place + ring.r_place;
+            if constexpr (MODE == ROWS_RING) return staged_run_any(row, f.gate_dtype, at, j);
+            else if constexpr (MODE == ROWS_VEC) return load_run_any<MODE>(g_row, f.gate_dtype, at, j);
+            else return f.gate_dtype == MHC_F32
+                            ? staged_single(reinterpret_cast<const float *>(row + skew16(g_row)), at, j)
+                            : staged_single(reinterpret_cast<const TY *>(row + skew16(g_row)), at, j);
         };
         Run y[RUNS], v[RUNS];
         uint64_t s2 = 0;
@@ -168,10 +188,10 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
             group_sum<1, MAXW>(sum, red[grp][which], 1 + grp, warp, warps);
             which ^= 1;
             rstd1 = __frsqrt_rn(fmaf(sum[0], f.inv_h, f.eps_post));
-        } else if (MODE == ROWS_RING && warps > 1) {
+        } else if (STAGED && warps > 1) {
             named_barrier_sync(1 + grp, at.threads);
         }
-        if (MODE == ROWS_RING) {
+        if (STAGED) {
             // the row is in registers: its stage is free
             if (warps == 1) __syncwarp();
             const long long next = t + static_cast<long long>(ring.stages) * gridDim.x;
@@ -221,7 +241,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
             a.rstd[2 * t + 1] = rstd2;
         }
     }
-    if (MODE == ROWS_RING && !ok && at.thread == 0) {
+    if (STAGED && !ok && at.thread == 0) {
         // copies that may still be in flight, before the CTA's memory goes: each
         // stage's last, in either parity
         int gave_up = 0;
@@ -263,20 +283,19 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
                                                                  3 * 32 * threads, pdl, s);
     }
     // as many groups as fit, but no more than give every SM a row
-    const int threads = row_threads(f.H, 4);
+    const int runs = vec ? 4 : 2, threads = row_threads(f.H, runs);
     long long groups = 512 / threads;
     const long long rows = (f.T + sms - 1) / sms;
     if (groups > kFwdGroups) groups = kFwdGroups;
     ring.groups = static_cast<int>(rows < groups ? rows : groups);
     const unsigned grid = static_cast<unsigned>(f.T < sms ? f.T : sms);
-    const size_t kept = static_cast<size_t>(vec && !full && !scaled ? 2 : 3) * 128 * threads;
-    if (!vec) return fwd_launch<TY, TR, ROWS_ANY, 4, true, true, true>(a, ring, grid, threads, kept, pdl, s);
-    ring.y_bytes = f.H * sizeof(TY);
-    ring.r_bytes = f.H * sizeof(TR);
-    ring.g_bytes = full ? f.H * elem_bytes(f.gate_dtype) : 0;
+    const size_t kept = static_cast<size_t>(vec && !full && !scaled ? 2 : 3) * 32 * runs * threads;
+    ring.y_place = row_place(f.H, sizeof(TY), !vec);
+    ring.r_place = row_place(f.H, sizeof(TR), !vec);
+    ring.g_place = full ? row_place(f.H, elem_bytes(f.gate_dtype), !vec) : 0;
     // a stage for each group and one to fill meanwhile, or all of the rows; with the widest types (96 KB a
     // row of 8192) one stage and one group
-    const size_t bytes = ring.y_bytes + ring.r_bytes + ring.g_bytes;
+    const size_t bytes = ring.y_place + ring.r_place + ring.g_place;
     long long stages = static_cast<long long>((kFwdSmem - kept) / bytes);
     if (stages > kFwdStages) stages = kFwdStages;
     if (stages > rows) stages = rows;
@@ -286,6 +305,7 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
     int n = 0;
     if (require_device(&n, &ring.status)) return cudaErrorUnknown;
     ring.timeout_ns = wait_timeout_ns();
+    if (!vec) return fwd_launch<TY, TR, ROWS_ANY, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (full)
         return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, true, true, true>(a, ring, grid, threads, smem, pdl, s)
                     : fwd_launch<TY, TR, ROWS_RING, 4, true, true, false>(a, ring, grid, threads, smem, pdl, s);

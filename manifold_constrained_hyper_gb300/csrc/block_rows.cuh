@@ -10,9 +10,9 @@ namespace mhc {
 
 // How a row kernel gets its rows.
 enum RowMode : int {
-    ROWS_RING = 0,      // staged ahead of use by bulk copies (rows on 16-byte boundaries)
-    ROWS_VEC = 1,       // 16-byte loads (the same, or a few rows only)
-    ROWS_ANY = 2        // single elements, any boundary
+    ROWS_RING = 0,      // staged ahead of use by bulk copies, runs of 8 (rows on boundaries of 8 elements)
+    ROWS_VEC = 1,       // runs of 8 from global memory: a few rows only, or rows too wide for two stages
+    ROWS_ANY = 2        // staged, single elements: any boundary
 };
 // A thread holds RUNS runs of 8 columns of its group's row: with vector loads
 // run j is the columns from (j * threads + thread) * 8, with single ones the
@@ -66,6 +66,28 @@ __device__ __forceinline__ Run load_run_any(const void *row, int dtype, const Pl
 template <class T>
 __device__ __forceinline__ Run staged_run(const T *row, const Place &p, int j) {
     return load8_shared(row + run_read_col(p, j));
+}
+// The same on any boundary, single elements; what lies past the row's end is 0.
+template <class T>
+__device__ __forceinline__ Run staged_single(const T *row, const Place &p, int j) {
+    const int c = run_col<ROWS_ANY>(p, j);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e * p.threads < p.H ? to_f32(row[c + e * p.threads]) : 0.f;
+    return run_of(v);
+}
+// Bulk copies start and end on 16-byte boundaries: a row that does not is
+// copied with what shares its first and last 16 bytes (within the allocation,
+// which begins and ends on such a boundary), and begins `skew` bytes into its place.
+__device__ __forceinline__ uint32_t skew16(const void *p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u; }
+__device__ __forceinline__ uint32_t skewed_bytes(const void *p, uint32_t bytes) { return (skew16(p) + bytes + 15u) & ~15u; }
+__device__ __forceinline__ void bulk_load_row(uint32_t dst, const void *p, uint32_t bytes, uint32_t bar, uint64_t policy) {
+    bulk_load(dst, static_cast<const uint8_t *>(p) - skew16(p), skewed_bytes(p, bytes), bar, policy);
+}
+// A row's place in a stage.
+inline uint32_t row_place(int H, int elem, bool any) {
+    const uint32_t bytes = static_cast<uint32_t>(H) * elem;
+    return any ? (bytes + 15 + 15) / 16 * 16 : bytes;
 }
 __device__ __forceinline__ Run staged_run_any(const void *row, int dtype, const Place &p, int j) {
     if (dtype == MHC_F32) return staged_run(static_cast<const float *>(row), p, j);

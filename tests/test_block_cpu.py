@@ -2,6 +2,9 @@
 the 64-bit forms' gradients against differences, the entry points' refusals
 (before any device work), and the workspace sizes."""
 import ctypes
+import os
+import struct
+import subprocess
 
 import pytest
 import torch
@@ -74,19 +77,35 @@ def _P(v):
     return ctypes.c_void_p(v)
 
 
+def _ckpt(codes, scales):
+    return ops._CKPT.pack(codes or 0, scales or 0)
+
+
 def _block(**over):
     v = dict(tokens=4, hidden=64, dtype=1, residual_dtype=1, w_post=A * 1, w_pre=A * 2, w_post_dtype=0,
              w_pre_dtype=0, gate=A * 3, gate_dtype=0, gate_form=1, gate_act=0, gate_stride=64,
              res_scale=A * 4, scale_form=2, eps_post=1e-6, eps_pre=1e-6, weight_offset=0.0, post_norm=1)
     v.update(over)
-    b = ops._Block()
-    for k, x in v.items():
-        setattr(b, k, x)
-    return b
+    return ops._BLOCK.pack(*(0 if x is None else x for x in v.values()))
 
 
 def _norm(lib, b, y=A * 5, ys=64, r=A * 6, rs=64, ro=A * 7, h=A * 8, rstd=A * 9, fmt=0, cy=None, cr=None, ch=None):
     return lib.mhc_block_norm(b, _P(y), ys, _P(r), rs, _P(ro), _P(h), _P(rstd), fmt, cy, cr, ch, None)
+
+
+def test_the_packed_structures_are_the_compiler_s(tmp_path):
+    fields = ("tokens hidden dtype residual_dtype w_post w_pre w_post_dtype w_pre_dtype gate gate_dtype gate_form "
+              "gate_act gate_stride res_scale scale_form eps_post eps_pre weight_offset post_norm").split()
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    src = tmp_path / "layout.c"
+    src.write_text('#include "mhc.h"\n#include <stddef.h>\n#include <stdio.h>\nint main(void) {'
+                   + "".join(f'printf("%zu ", offsetof(mhc_block, {f}));' for f in fields)
+                   + 'printf("%zu %zu", sizeof(mhc_block), sizeof(mhc_ckpt)); return 0; }')
+    subprocess.run(["gcc", "-I", include, str(src), "-o", str(tmp_path / "layout")], check=True)
+    got = [int(v) for v in subprocess.check_output([str(tmp_path / "layout")]).split()]
+    codes = "qiiiPPiiPiiiqPifffi"
+    want = [struct.calcsize("@" + codes[:i] + "0" + codes[i]) for i in range(len(codes))]
+    assert got == want + [ops._BLOCK.size, ops._CKPT.size]
 
 
 def test_refusals_of_the_block(lib):
@@ -122,12 +141,12 @@ def test_refusals_of_the_block(lib):
     assert _norm(lib, _block(), h=A * 2) == 5
     assert _norm(lib, _block(tokens=0, gate=None, res_scale=None), y=None, r=None, ro=None, h=None) == 0
     # checkpoints: format, missing parts, overlap
-    ck = ops._Ckpt(A * 10, A * 11)
+    ck = _ckpt(A * 10, A * 11)
     assert _norm(lib, _block(), fmt=0, cy=ck) == 3
     assert _norm(lib, _block(), fmt=3, cr=ck) == 3
-    assert _norm(lib, _block(), fmt=1, ch=ops._Ckpt(A * 10, None)) == 1
+    assert _norm(lib, _block(), fmt=1, ch=_ckpt(A * 10, None)) == 1
     assert _norm(lib, _block(), fmt=1, cy=ck, cr=ck) == 5
-    assert _norm(lib, _block(), fmt=2, cy=ops._Ckpt(A * 7 + 8, A * 11)) == 5
+    assert _norm(lib, _block(), fmt=2, cy=_ckpt(A * 7 + 8, A * 11)) == 5
 
 
 def _back(lib, b, dr=A * 20, drs=64, dh=A * 21, dhs=64, y=A * 22, ys=64, r=A * 23, rs=64, fmt=0, cy=None, cr=None,
@@ -145,10 +164,10 @@ def test_refusals_of_the_backward_pass(lib):
     for k in ("drs", "dhs", "ys", "rs"):
         assert _back(lib, _block(), **{k: -1}) == 3, k
     assert _back(lib, _block(), wsb=16) == 8
-    ck = ops._Ckpt(A * 40, A * 41)
+    ck = _ckpt(A * 40, A * 41)
     assert _back(lib, _block(), fmt=1, cy=ck) == 3                    # y and its checkpoint
     assert _back(lib, _block(), fmt=0, cy=ck, y=None) == 3
-    assert _back(lib, _block(), fmt=1, cy=ops._Ckpt(None, A * 41), y=None) == 1
+    assert _back(lib, _block(), fmt=1, cy=_ckpt(None, A * 41), y=None) == 1
     # gradients of what is not there
     assert _back(lib, _block(w_post=None)) == 3
     assert _back(lib, _block(w_pre=None)) == 3
@@ -161,11 +180,11 @@ def test_refusals_of_the_backward_pass(lib):
     assert _back(lib, _block(), dres=A * 20 + 2) == 5
     assert _back(lib, _block(), dw1=A * 28) == 5
     assert _back(lib, _block(), ws=A * 24 - 64) == 5
-    assert _back(lib, _block(), fmt=1, cr=ops._Ckpt(A * 26, A * 41), r=None) == 5
+    assert _back(lib, _block(), fmt=1, cr=_ckpt(A * 26, A * 41), r=None) == 5
 
 
 def test_refusals_of_the_checkpoints(lib):
-    ck = ops._Ckpt(A * 2, A * 3)
+    ck = _ckpt(A * 2, A * 3)
     ok = [_P(A), 64, 1, 4, 64, 1]
     assert lib.mhc_ckpt_pack(*ok[:3], -1, 64, 1, ck, None) == 3
     assert lib.mhc_ckpt_pack(_P(A), -1, 1, 4, 64, 1, ck, None) == 3
@@ -175,9 +194,9 @@ def test_refusals_of_the_checkpoints(lib):
     assert lib.mhc_ckpt_pack(_P(A), 64, 1, 4, 65537, 1, ck, None) == 4
     assert lib.mhc_ckpt_pack(None, 64, 1, 4, 64, 1, ck, None) == 1
     assert lib.mhc_ckpt_pack(*ok, None, None) == 1
-    assert lib.mhc_ckpt_pack(*ok, ops._Ckpt(A * 2, None), None) == 1
+    assert lib.mhc_ckpt_pack(*ok, _ckpt(A * 2, None), None) == 1
     assert lib.mhc_ckpt_pack(_P(A + 1), 64, 1, 4, 64, 1, ck, None) == 2
-    assert lib.mhc_ckpt_pack(*ok, ops._Ckpt(A + 16, A * 3), None) == 5
+    assert lib.mhc_ckpt_pack(*ok, _ckpt(A + 16, A * 3), None) == 5
     assert lib.mhc_ckpt_pack(None, 64, 1, 0, 64, 1, None, None) == 0
     un = [ck, 1, 4, 64, 1]
     assert lib.mhc_ckpt_unpack(ck, 0, 4, 64, 1, _P(A), None) == 3
@@ -192,7 +211,7 @@ def test_refusals_of_the_checkpoints(lib):
 
 
 def test_refusals_of_the_weight_gradient(lib):
-    ck = ops._Ckpt(A * 2, A * 3)
+    ck = _ckpt(A * 2, A * 3)
 
     def dw(d=A, s=64, t=1, x=ck, fmt=1, T=4, n=64, k=32, w=A * 4, wt=0, acc=0, ws=A * 5, wsb=1 << 19):
         return lib.mhc_ckpt_linear_dw(_P(d), s, t, x, fmt, T, n, k, _P(w), wt, acc, _P(ws), wsb, None)
@@ -204,7 +223,7 @@ def test_refusals_of_the_weight_gradient(lib):
     assert dw(t=0) == 4                       # an fp32 gradient
     for bad in (dict(n=0), dict(k=0), dict(n=65537), dict(k=65537)):
         assert dw(**bad) == 4, bad
-    for bad in (dict(d=None), dict(x=None), dict(w=None), dict(x=ops._Ckpt(None, A))):
+    for bad in (dict(d=None), dict(x=None), dict(w=None), dict(x=_ckpt(None, A))):
         assert dw(**bad) == 1, bad
     assert dw(d=A + 1) == 2
     assert dw(w=A * 4 + 2) == 2
