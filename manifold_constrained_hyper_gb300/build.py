@@ -1,6 +1,7 @@
-"""Build libmhc.so (the C-ABI library) in-tree for sm_103a with nvcc.
+"""Build libmhc.so (the C-ABI library) in-tree for sm_103a with nvcc, and
+_binding.so, the part of the Python binding that is C++, with the host compiler.
 
-Each translation unit under csrc/ compiles in parallel; the objects link into
+Each translation unit under csrc/ compiles in parallel; the CUDA objects link into
 ``manifold_constrained_hyper_gb300/libmhc.so`` (static CUDA runtime). Build
 products go to ``_build/`` and are git-ignored.
 """
@@ -8,8 +9,10 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmhc.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -30,14 +34,34 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
+def _build_binding():
+    """_binding.so against the torch that is installed (its headers and libraries)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    nvcc = shutil.which(NVCC)
+    cuda = os.path.dirname(os.path.dirname(nvcc)) if nvcc else "/usr/local/cuda"
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(a for i in include for a in ("-isystem", i)), "-I", INCLUDE,
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding failed to build:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -59,8 +83,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, len(_sources()))) as ex:
+    with ThreadPoolExecutor(max_workers=1 + len(_sources())) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(compile_one, _sources()))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

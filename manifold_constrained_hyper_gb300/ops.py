@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libmhc.so (include/mhc.h).
+"""Thin binding of libmhc.so (include/mhc.h): ctypes, and for the gated residual
+block, the checkpoints and the weight gradient the C++ of csrc/binding.cpp.
 
 Argument marshalling only: every step of the boundary runs in the library's
 CUDA kernels. Tensors are torch CUDA tensors (bf16 tensors travel as their
@@ -10,8 +11,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
-from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -50,12 +49,6 @@ class _Params(ctypes.Structure):
                 ("batch_invariant", ctypes.c_int)]
 
 
-# mhc_block and mhc_ckpt of include/mhc.h, packed by hand: a third of what
-# filling a ctypes structure costs
-_BLOCK = struct.Struct("@qiiiPPiiPiiiqPifffi4x")
-_CKPT = struct.Struct("@PP")
-
-
 @dataclass
 class Params:
     hc_norm_eps: float = 1e-6
@@ -87,7 +80,7 @@ def load():
     lib = ctypes.CDLL(_LIB_PATH)
     P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     PP = ctypes.POINTER(_Params)
-    PB = PC = P                    # structures as bytes
+    PB = PC = P                    # structures, by address
     sig = {
         "mhc_weight_bytes": (sz, [i32]),
         "mhc_prepare_weight": (i32, [P, i32, P, P]),
@@ -425,11 +418,36 @@ def mhc_status_string(code: int) -> str:
 # Gated residual block, its backward pass, and 8-bit activation checkpoints
 
 _DTYPES = {torch.float32: MHC_F32, torch.bfloat16: MHC_BF16, torch.float16: MHC_F16}
-_GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = 0, 1, 2, 3
-_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
-_SCALE_NONE, _SCALE_ONE, _SCALE_CHANNEL = 0, 1, 2
 _FORMATS = {"e4m3": 1, "int8": 2}
 CKPT_GROUP = 32
+_fast = None
+
+
+def load_binding():
+    """The C++ binding (raises if it has not been built), over load()'s library."""
+    global _fast
+    if _fast is None:
+        lib = load()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the C++ binding is missing: build it with `python -c 'import "
+                               "__graft_entry__ as g; g.build()'`") from e
+        _binding.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "mhc_block_norm", "mhc_block_norm_backward", "mhc_block_norm_backward_workspace_bytes",
+            "mhc_ckpt_pack", "mhc_ckpt_unpack", "mhc_ckpt_linear_dw",
+            "mhc_ckpt_linear_dw_workspace_bytes")), MhcError)
+        _fast = _binding
+    return _fast
+
+
+def _at(stream, call, *args):
+    """call(*args) with `stream` as torch's current one: its outputs and workspace are
+    allocated there too."""
+    if stream is None:
+        return call(*args)
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 @dataclass
@@ -474,9 +492,6 @@ class Checkpoint:
     def device(self):
         return self.codes.device
 
-    def _c(self):
-        return _CKPT.pack(self.codes.data_ptr(), self.scales.data_ptr())
-
 
 class BlockGrads(NamedTuple):
     """Gradients of mhc_block_norm's inputs; None where there is no such input."""
@@ -488,53 +503,25 @@ class BlockGrads(NamedTuple):
     d_res_scale: torch.Tensor | None
 
 
-_NOWHERE_ELSE = nullcontext()
+def _held(codes, scales, fmt) -> Checkpoint:
+    c = Checkpoint.__new__(Checkpoint)
+    c.codes, c.scales, c.fmt = codes, scales, fmt
+    return c
 
 
-def _on(stream):
-    """Where outputs and workspaces of a call on `stream` are allocated: there."""
-    return torch.cuda.stream(stream) if stream is not None else _NOWHERE_ELSE
+def _format_number(fmt):
+    n = _FORMATS.get(fmt)
+    if n is None:
+        raise ValueError(f"checkpoint format must be one of {sorted(_FORMATS)}: got {fmt!r}")
+    return n
 
 
 def ckpt_empty(tokens: int, hidden: int, fmt: str = "e4m3", device="cuda") -> Checkpoint:
     """A checkpoint to be written."""
-    if fmt not in _FORMATS:
-        raise ValueError(f"checkpoint format must be one of {sorted(_FORMATS)}: got {fmt!r}")
-    c = Checkpoint.__new__(Checkpoint)
-    c.codes = torch.empty((tokens, hidden), dtype=torch.uint8, device=device)
-    c.scales = torch.empty((tokens, -(-hidden // CKPT_GROUP)), dtype=torch.uint8, device=device)
-    c.fmt = fmt
-    return c
-
-
-def _matrix(t, name, shape, dtype, device):
-    """A CUDA tensor `shape` = [T, H] of `dtype` whose rows are contiguous: its row stride."""
-    if t.dtype is dtype and t.shape == shape and t.device == device:
-        if t.is_contiguous():
-            return shape[1]
-        if shape[1] == 1 or t.stride(1) == 1:
-            return t.stride(0)
-    raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor on {device} with contiguous "
-                     f"rows: got {list(t.shape)} {t.dtype} on {t.device}")
-
-
-def _whole(t, name, shape, dtype, device):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor on {device}: "
-                         f"got {list(t.shape)} {t.dtype} on {t.device}")
-    return t
-
-
-def _out(t, name, shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device) if t is None \
-        else _whole(t, name, shape, dtype, device)
-
-
-def _held(c, name, shape, device):
-    if c.codes.shape != shape or c.codes.device != device:
-        raise ValueError(f"{name} must be a {list(shape)} checkpoint on {device}: got "
-                         f"{list(c.codes.shape)} on {c.codes.device}")
-    return c._c()
+    _format_number(fmt)
+    return _held(torch.empty((tokens, hidden), dtype=torch.uint8, device=device),
+                 torch.empty((tokens, -(-hidden // CKPT_GROUP)), dtype=torch.uint8, device=device),
+                 fmt)
 
 
 def _format(*cks):
@@ -548,67 +535,8 @@ def _format(*cks):
     return _FORMATS[fmt] if fmt is not None else 0
 
 
-def _weight(w, name, H, device):
-    if w is None:
-        return 0, MHC_F32
-    t = _DTYPES.get(w.dtype)
-    if t is None or w.shape != (H,) or not w.is_contiguous() or w.device != device:
-        raise ValueError(f"{name} must be a contiguous [{H}] float tensor on {device}: got "
-                         f"{list(w.shape)} {w.dtype} on {w.device}")
-    return w.data_ptr(), t
-
-
-def _block_c(shape, dtype, r_dtype, device, w_post, w_pre, gate, res_scale, params):
-    """The C struct of a block from its tensors, as bytes, and the gate's form (its
-    and the scale's are told by their shapes)."""
-    p = params if params is not None else _DEFAULT_BLOCK_PARAMS
-    T, H = shape
-    t = _DTYPES.get(dtype)
-    if t is None or (r_dtype is not dtype and r_dtype is not torch.float32):
-        raise ValueError(f"y must be float32, bfloat16 or float16 and residual the same or "
-                         f"float32: got {dtype} and {r_dtype}")
-    wp, wpt = _weight(w_post, "w_post", H, device)
-    wq, wqt = _weight(w_pre, "w_pre", H, device)
-    act = _ACTS.get(p.gate_act)
-    if act is None or (act and gate is None):
-        raise ValueError(f"gate_act must be one of {sorted(_ACTS)}, and \"none\" without a gate: "
-                         f"got {p.gate_act!r}")
-    form, gate_p, gate_t, gate_stride = _GATE_NONE, 0, MHC_F32, 0
-    if gate is not None:
-        gate_t = _DTYPES.get(gate.dtype)
-        gs = gate.shape
-        if (gate_t != t and gate_t != MHC_F32) or gate.device != device:
-            raise ValueError(f"gate must be {dtype} or float32 on {device}: got {gate.dtype} on "
-                             f"{gate.device}")
-        if gs == (H,) and (gate.is_contiguous() or H == 1):
-            form = _GATE_CHANNEL
-        elif gs == (T, 1):
-            form, gate_stride = _GATE_TOKEN, gate.stride(0)
-        elif gs == shape and gate.stride(1) == 1:
-            form, gate_stride = _GATE_FULL, gate.stride(0)
-        else:
-            raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}] with contiguous rows: "
-                             f"got {list(gs)}")
-        gate_p = gate.data_ptr()
-    scale_form, scale_p = _SCALE_NONE, 0
-    if res_scale is not None:
-        n = res_scale.numel()
-        if res_scale.dtype is not torch.float32 or res_scale.dim() > 1 or (n != 1 and n != H) \
-                or not res_scale.is_contiguous() or res_scale.device != device:
-            raise ValueError(f"res_scale must be a contiguous [1] or [{H}] float32 tensor on "
-                             f"{device}: got {list(res_scale.shape)} {res_scale.dtype} on "
-                             f"{res_scale.device}")
-        scale_form, scale_p = (_SCALE_ONE if n == 1 else _SCALE_CHANNEL), res_scale.data_ptr()
-    return _BLOCK.pack(T, H, t, MHC_F32 if r_dtype is torch.float32 else t, wp, wq, wpt, wqt, gate_p,
-                       gate_t, form, act, gate_stride, scale_p, scale_form, p.eps_post, p.eps_pre,
-                       p.weight_offset, 1 if p.post_norm else 0), form
-
-
-def _cuda_2d(t, name):
-    shape = t.shape
-    if len(shape) != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    return shape, t.device
+def _parts(c):
+    return (None, None) if c is None else (c.codes, c.scales)
 
 
 def mhc_block_norm(y, residual, w_post=None, w_pre=None, gate=None, res_scale=None,
@@ -628,27 +556,14 @@ def mhc_block_norm(y, residual, w_post=None, w_pre=None, gate=None, res_scale=No
     residual and h in the same pass. Returns (residual_out, h, rstd), rstd
     [T, 2] being what mhc_block_norm_backward needs beside y and residual.
     residual_out may be the residual itself."""
-    shape, dev = _cuda_2d(y, "y")
-    dtype, r_dtype = y.dtype, residual.dtype
-    ys = _matrix(y, "y", shape, dtype, dev)
-    rs = _matrix(residual, "residual", shape, r_dtype, dev)
-    b, _ = _block_c(shape, dtype, r_dtype, dev, w_post, w_pre, gate, res_scale, params)
-    fmt, cy, cr, ch = 0, None, None, None
-    if ckpt_y is not None or ckpt_residual is not None or ckpt_h is not None:
-        fmt = _format(ckpt_y, ckpt_residual, ckpt_h)
-        cy = None if ckpt_y is None else _held(ckpt_y, "ckpt_y", shape, dev)
-        cr = None if ckpt_residual is None else _held(ckpt_residual, "ckpt_residual", shape, dev)
-        ch = None if ckpt_h is None else _held(ckpt_h, "ckpt_h", shape, dev)
-    with _on(stream):
-        residual_out = _out(residual_out, "residual_out", shape, r_dtype, dev)
-        h = _out(h, "h", shape, dtype, dev)
-        rstd = _out(rstd, "rstd", (shape[0], 2), torch.float32, dev)
-    code = (_lib or load()).mhc_block_norm(b, y.data_ptr(), ys, residual.data_ptr(), rs,
-                                           residual_out.data_ptr(), h.data_ptr(), rstd.data_ptr(),
-                                           fmt, cy, cr, ch, _stream(stream, dev))
-    if code:
-        raise MhcError(code, "mhc_block_norm")
-    return residual_out, h, rstd
+    f = (_fast or load_binding()).block_norm
+    p = _DEFAULT_BLOCK_PARAMS if params is None else params
+    if ckpt_y is None and ckpt_residual is None and ckpt_h is None:
+        return _at(stream, f, y, residual, w_post, w_pre, gate, res_scale, p, residual_out, h, rstd,
+                   0, None, None, None, None, None, None)
+    return _at(stream, f, y, residual, w_post, w_pre, gate, res_scale, p, residual_out, h, rstd,
+               _format(ckpt_y, ckpt_residual, ckpt_h), *_parts(ckpt_y), *_parts(ckpt_residual),
+               *_parts(ckpt_h))
 
 
 def block_norm_backward_workspace_bytes(tokens: int, hidden: int) -> int:
@@ -662,106 +577,42 @@ def mhc_block_norm_backward(d_residual_out, d_h, y, residual, rstd, w_post=None,
     """Gradients of mhc_block_norm's inputs from those of residual_out (None:
     zero) and h. y and residual are the inputs or Checkpoints of them; rstd,
     the weights, the gate, the scale and params as in the forward call.
-    residual_dtype (d_residual_out's, else d_h's, unless given) is needed only
-    where neither d_residual_out nor the residual itself tells it. The
-    gradients of weights, of a [H] or [T, 1] gate and of res_scale are float32
-    (those of [H] rows of one allocation); d_residual may be d_residual_out itself."""
-    shape, dev = _cuda_2d(d_h, "d_h")
-    T, H = shape
-    dtype = d_h.dtype
-    dhs = _matrix(d_h, "d_h", shape, dtype, dev)
-    if residual_dtype is None:
-        residual_dtype = d_residual_out.dtype if d_residual_out is not None \
-            else residual.dtype if isinstance(residual, torch.Tensor) else dtype
-    drs = 0 if d_residual_out is None else _matrix(d_residual_out, "d_residual_out", shape,
-                                                   residual_dtype, dev)
-    b, form = _block_c(shape, dtype, residual_dtype, dev, w_post, w_pre, gate, res_scale, params)
-    cy = cr = yp = rp = None
-    ys = rs = fmt = 0
-    if isinstance(y, Checkpoint):
-        cy, fmt = _held(y, "y", shape, dev), _FORMATS[y.fmt]
-    else:
-        yp, ys = y.data_ptr(), _matrix(y, "y", shape, dtype, dev)
-    if isinstance(residual, Checkpoint):
-        cr = _held(residual, "residual", shape, dev)
-        fmt = _format(residual, y if cy is not None else None)
-    else:
-        rp, rs = residual.data_ptr(), _matrix(residual, "residual", shape, residual_dtype, dev)
-    _whole(rstd, "rstd", (T, 2), torch.float32, dev)
-    lib = _lib or load()
-    f32 = torch.float32
-    channel = form == _GATE_CHANNEL
-    per_channel = res_scale is not None and res_scale.numel() != 1
-    d_w_post = d_w_pre = d_gate = d_scale = None
-    with _on(stream):
-        d_y = _out(d_y, "d_y", shape, dtype, dev)
-        d_residual = _out(d_residual, "d_residual", shape, residual_dtype, dev)
-        rows = (w_post is not None) + (w_pre is not None) + channel + per_channel
-        if rows:
-            own = iter(torch.empty((rows, H), dtype=f32, device=dev).unbind(0))
-            if w_post is not None:
-                d_w_post = next(own)
-            if w_pre is not None:
-                d_w_pre = next(own)
-            if channel:
-                d_gate = next(own)
-            if per_channel:
-                d_scale = next(own)
-        if gate is not None and not channel:
-            d_gate = torch.empty(gate.shape, dtype=gate.dtype if form == _GATE_FULL else f32,
-                                 device=dev)
-        if res_scale is not None and not per_channel:
-            d_scale = torch.empty(res_scale.shape, dtype=f32, device=dev)
-        if workspace is None:
-            need = lib.mhc_block_norm_backward_workspace_bytes(T, H)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    code = lib.mhc_block_norm_backward(
-        b, _p(d_residual_out), drs, d_h.data_ptr(), dhs, yp, ys, rp, rs, fmt, cy, cr,
-        rstd.data_ptr(), d_y.data_ptr(), d_residual.data_ptr(), _p(d_w_post), _p(d_w_pre),
-        _p(d_gate), _p(d_scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream(stream, dev))
-    if code:
-        raise MhcError(code, "mhc_block_norm_backward")
-    return BlockGrads(d_y, d_residual, d_w_post, d_w_pre, d_gate, d_scale)
+    residual_dtype (d_residual_out's, else the residual's, else d_h's, unless
+    given) is needed only where none of them tells it. The gradients of
+    weights, of a [H] or [T, 1] gate and of res_scale are float32; d_residual
+    may be d_residual_out itself."""
+    f = (_fast or load_binding()).block_norm_backward
+    cy = y if isinstance(y, Checkpoint) else None
+    cr = residual if isinstance(residual, Checkpoint) else None
+    typed = None if residual_dtype is None else torch.empty(0, dtype=residual_dtype)
+    return BlockGrads(*_at(
+        stream, f, d_residual_out, d_h, y if cy is None else None, residual if cr is None else None,
+        rstd, w_post, w_pre, gate, res_scale, _DEFAULT_BLOCK_PARAMS if params is None else params,
+        typed, d_y, d_residual, workspace, _format(cy, cr), *_parts(cy), *_parts(cr)))
 
 
 def mhc_ckpt_pack(x, fmt: str = "e4m3", *, out: Checkpoint | None = None, stream=None) -> Checkpoint:
     """x [T, H] (float32, bfloat16 or float16, rows may be strided) kept in 8 bits."""
-    shape, dev = _cuda_2d(x, "x")
-    t = _DTYPES.get(x.dtype)
-    if t is None:
-        raise ValueError(f"x must be float32, bfloat16 or float16: got {x.dtype}")
-    s = _matrix(x, "x", shape, x.dtype, dev)
-    T, H = shape
+    f = (_fast or load_binding()).ckpt_pack
     if out is None:
-        with _on(stream):
-            out = ckpt_empty(T, H, fmt, dev)
-        c = out._c()
-    else:
-        if out.fmt != fmt:
-            raise ValueError(f"out has the format {out.fmt!r}, not {fmt!r}")
-        c = _held(out, "out", shape, dev)
-    code = (_lib or load()).mhc_ckpt_pack(x.data_ptr(), s, t, T, H, _FORMATS[fmt], c,
-                                          _stream(stream, dev))
-    if code:
-        raise MhcError(code, "mhc_ckpt_pack")
+        return _held(*_at(stream, f, x, _format_number(fmt), None, None), fmt)
+    if out.fmt != fmt:
+        raise ValueError(f"out has the format {out.fmt!r}, not {fmt!r}")
+    _at(stream, f, x, _format_number(fmt), out.codes, out.scales)
     return out
+
+
+def _dtype_number(dtype, name):
+    t = _DTYPES.get(dtype)
+    if t is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16: got {dtype}")
+    return t
 
 
 def mhc_ckpt_unpack(ckpt: Checkpoint, dtype=torch.bfloat16, *, out=None, stream=None):
     """The values [T, H] that a checkpoint stands for, in `dtype`."""
-    t = _DTYPES.get(dtype)
-    if t is None:
-        raise ValueError(f"dtype must be float32, bfloat16 or float16: got {dtype}")
-    shape = ckpt.codes.shape
-    dev = ckpt.codes.device
-    with _on(stream):
-        out = _out(out, "out", shape, dtype, dev)
-    code = (_lib or load()).mhc_ckpt_unpack(ckpt._c(), _FORMATS[ckpt.fmt], shape[0], shape[1], t,
-                                            out.data_ptr(), _stream(stream, dev))
-    if code:
-        raise MhcError(code, "mhc_ckpt_unpack")
-    return out
+    return _at(stream, (_fast or load_binding()).ckpt_unpack, ckpt.codes, ckpt.scales,
+               _FORMATS[ckpt.fmt], _dtype_number(dtype, "dtype"), out)
 
 
 def ckpt_linear_dw_workspace_bytes(tokens: int, n: int, k: int, aligned: bool = True) -> int:
@@ -774,34 +625,9 @@ def mhc_ckpt_linear_dw(d_out, x: Checkpoint, *, d_w=None, dtype=torch.float32,
     """d_w [N, K] = d_out^T x, the weight gradient of out = x W^T, from d_out
     [T, N] (bfloat16 or float16, rows may be strided) and the checkpoint of
     x [T, K]. accumulate adds to the d_w given."""
-    shape, dev = _cuda_2d(d_out, "d_out")
-    t_in = d_out.dtype
-    if t_in is not torch.bfloat16 and t_in is not torch.float16:
-        raise ValueError(f"d_out must be bfloat16 or float16: got {t_in}")
-    s = _matrix(d_out, "d_out", shape, t_in, dev)
-    T, N = shape
-    K = x.codes.shape[1]
-    c = _held(x, "x", (T, K), dev)
     if d_w is not None:
         dtype = d_w.dtype
     elif accumulate:
         raise ValueError("accumulate needs the d_w to add to")
-    t = _DTYPES.get(dtype)
-    if t is None:
-        raise ValueError(f"d_w must be float32, bfloat16 or float16: got {dtype}")
-    lib = _lib or load()
-    dp = d_out.data_ptr()
-    with _on(stream):
-        d_w = _out(d_w, "d_w", (N, K), dtype, dev)
-        if workspace is None:
-            aligned = dp % 16 == 0 and ((s % 8 == 0 and N <= s < 1 << 38) or T == 1)
-            need = lib.mhc_ckpt_linear_dw_workspace_bytes(T, N, K, aligned)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    code = lib.mhc_ckpt_linear_dw(dp, s, _DTYPES[t_in], c, _FORMATS[x.fmt], T, N, K,
-                                  d_w.data_ptr(), t, 1 if accumulate else 0, _p(workspace), ws_bytes,
-                                  _stream(stream, dev))
-    if code:
-        raise MhcError(code, "mhc_ckpt_linear_dw")
-    return d_w
+    return _at(stream, (_fast or load_binding()).ckpt_linear_dw, d_out, x.codes, x.scales,
+               _FORMATS[x.fmt], d_w, _dtype_number(dtype, "d_w"), accumulate, workspace)

@@ -70,6 +70,9 @@ def test_the_plain_checkpoint_round_trip():
     assert ref.pack(top, "e4m3")[1].flatten().tolist() == [127, 128]
 
 
+# mhc_block and mhc_ckpt of include/mhc.h
+_BLOCK = struct.Struct("@qiiiPPiiPiiiqPifffi4x")
+_CKPT = struct.Struct("@PP")
 A = 0x100000           # an aligned address that is never read
 
 
@@ -78,7 +81,7 @@ def _P(v):
 
 
 def _ckpt(codes, scales):
-    return ops._CKPT.pack(codes or 0, scales or 0)
+    return _CKPT.pack(codes or 0, scales or 0)
 
 
 def _block(**over):
@@ -86,7 +89,7 @@ def _block(**over):
              w_pre_dtype=0, gate=A * 3, gate_dtype=0, gate_form=1, gate_act=0, gate_stride=64,
              res_scale=A * 4, scale_form=2, eps_post=1e-6, eps_pre=1e-6, weight_offset=0.0, post_norm=1)
     v.update(over)
-    return ops._BLOCK.pack(*(0 if x is None else x for x in v.values()))
+    return _BLOCK.pack(*(0 if x is None else x for x in v.values()))
 
 
 def _norm(lib, b, y=A * 5, ys=64, r=A * 6, rs=64, ro=A * 7, h=A * 8, rstd=A * 9, fmt=0, cy=None, cr=None, ch=None):
@@ -105,7 +108,7 @@ def test_the_packed_structures_are_the_compiler_s(tmp_path):
     got = [int(v) for v in subprocess.check_output([str(tmp_path / "layout")]).split()]
     codes = "qiiiPPiiPiiiqPifffi"
     want = [struct.calcsize("@" + codes[:i] + "0" + codes[i]) for i in range(len(codes))]
-    assert got == want + [ops._BLOCK.size, ops._CKPT.size]
+    assert got == want + [_BLOCK.size, _CKPT.size]
 
 
 def test_refusals_of_the_block(lib):
@@ -242,7 +245,7 @@ def test_workspace_sizes(lib):
     assert ops.ckpt_linear_dw_workspace_bytes(0, 64, 64) == 0
 
 
-def test_the_binding_refuses_on_the_host():
+def test_the_binding_refuses_on_the_host(lib):
     y = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         ops.mhc_block_norm(y, y)
