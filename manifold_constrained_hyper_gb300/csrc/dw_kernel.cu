@@ -5,7 +5,8 @@
 // out in 16 bits (3 bytes of traffic a value) and the product runs on plain
 // 16-bit operands: unpacking them inside it would convert every value once
 // per 256 rows of d_w, and pass it twice more through shared memory, which
-// the operands' own traffic already fills.
+// the operands' own traffic already fills. The same kernel copies a d_out whose
+// rows TMA cannot read.
 //
 // Both operands lie with the long axis (tokens) outermost, so a box of 64
 // columns x 64 tokens lands in shared memory as 64 rows of 128 bytes and the
@@ -18,14 +19,14 @@
 // adds the splits in their order.
 #include <atomic>
 
-#include "block_common.cuh"
 #include "mhc_internal.h"
+#include "vec_io.cuh"
 
 namespace mhc {
 namespace {
 
-constexpr int kTile = 256;                          // of d_w, either way, by a pair of CTAs
-constexpr int kHalf = kTile / 2;                    // what one CTA loads of either operand
+constexpr int kTile = 256;                          // rows of d_w by a pair of CTAs, and columns at most
+constexpr int kHalf = kTile / 2;                    // what one CTA loads of either operand at most
 constexpr int kStep = 64;                           // tokens per pipeline stage
 constexpr int kBoxBytes = kStep * 128;              // 64 columns x 64 tokens, 16 bits
 constexpr int kStageBytes = 4 * kBoxBytes;          // two boxes of either operand
@@ -42,6 +43,7 @@ struct GemmArgs {
     long long T;
     int n, k;
     int tiles_n, tiles_k, splits, steps_per_split, steps;
+    int tile_k;                     // columns of a tile: 256, or 128 for few tiles
     int f16;                        // operands fp16, else bf16
     void *out;                      // d_w, or the splits' fp32 sums [splits][n][k]
     int out_dtype, accumulate, wide;    // wide: rows of out lie on 32-byte boundaries
@@ -226,20 +228,20 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
             item_place(a, item, &ti, &tj, &split);
             const int s0 = split * a.steps_per_split;
             const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
-            const int ci = ti * kTile + static_cast<int>(rank) * kHalf, cj = tj * kTile + static_cast<int>(rank) * kHalf;
+            const int ci = ti * kTile + static_cast<int>(rank) * kHalf, cj = tj * a.tile_k + static_cast<int>(rank) * (a.tile_k / 2);
             for (int st = s0; st < s1; ++st, ++it) {
                 const uint32_t s = it % kStages, ph = (it / kStages) & 1;
                 if (!mbar_wait(empty + 8 * s, ph ^ 1, abort_flag, a.timeout_ns, a.status, SITE_DW_EMPTY)) {
                     ok = false;
                     break;
                 }
-                if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kStageBytes);
+                if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kBoxBytes * (a.tile_k == kTile ? 8 : 6));
                 const uint32_t bar = dw_map_to_rank(full + 8 * s, 0), dst = base + s * kStageBytes;
                 const int t = st * kStep;
                 tma_load_pair(dst, &map_d, ci, t, bar);
                 tma_load_pair(dst + kBoxBytes, &map_d, ci + 64, t, bar);
                 tma_load_pair(dst + 2 * kBoxBytes, &map_x, cj, t, bar);
-                tma_load_pair(dst + 3 * kBoxBytes, &map_x, cj + 64, t, bar);
+                if (a.tile_k == kTile) tma_load_pair(dst + 3 * kBoxBytes, &map_x, cj + 64, t, bar);
             }
         }
         // every stage's last release has arrived before this CTA may exit
@@ -256,7 +258,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
         // ------------------------------------------------ products, the leader for both
         const uint32_t fmt = a.f16 ? 0u : 1u;
         const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | (1u << 16) |
-                               (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+                               (static_cast<uint32_t>(a.tile_k >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
         uint32_t it = 0, done = 0;
         bool ok = true;
         for (int item = pair; item < items && ok; item += pairs, ++done) {
@@ -307,8 +309,8 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
             const int i = ti * kTile + static_cast<int>(rank) * kHalf + quad * 32 + lane;
             const long long row = (static_cast<long long>(split) * a.n + i) * a.k;
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-                const int j = tj * kTile + c;
+            for (int c = 0; c < a.tile_k; c += 32) {
+                const int j = tj * a.tile_k + c;
                 if (j >= a.k) break;
                 uint32_t v[32];
                 tmem_ld32(tmem + buf * kTile + c + (static_cast<uint32_t>(quad * 32) << 16), v);
@@ -341,12 +343,83 @@ __global__ void __launch_bounds__(256) dw_join_kernel(const float *parts, int sp
     }
 }
 
-// Rows of d_out that no 16-byte load reaches, onto 16-byte boundaries.
-__global__ void __launch_bounds__(256) dw_align_kernel(const uint16_t *src, long long stride, uint16_t *dst,
-                                                       long long pitch, long long T, int n) {
+// The operands as the products read them: the checkpoint's values in 16 bits,
+// and, where its rows do not allow 16-byte loads, d_out; each in rows on 16-byte
+// boundaries. Eight columns a lane, kRuns of them in flight; past a row's
+// end stands 0 (the copies above cut rows at their length).
+struct PrepareArgs {
+    Ckpt x;
+    long long T;
+    int k, n;                       // n: columns of d_out to copy, 0 where none are
+    uint16_t *x16, *d16;
+    long long x_pitch, d_pitch;
+    const uint16_t *d_out;
+    long long d_stride;
+    int runs;                       // 8 codes at once: k a multiple of 8 and the codes on 8 bytes
+};
+constexpr int kRuns = 4;
+template <class T, int FMT, class I>
+__global__ void __launch_bounds__(256) dw_prepare_kernel(const PrepareArgs a) {
     griddep_wait();
-    for (long long t = blockIdx.x; t < T; t += gridDim.x)
-        for (int i = threadIdx.x; i < n; i += 256) dst[t * pitch + i] = src[t * stride + i];
+    const I per_x = static_cast<I>((a.k + 7) / 8), per_d = static_cast<I>((a.n + 7) / 8);
+    const I total_x = static_cast<I>(a.T) * per_x, total = total_x + static_cast<I>(a.T) * per_d;
+    const int groups = (a.k + 31) / 32;
+    for (I i0 = static_cast<I>(blockIdx.x) * (256 * kRuns) + threadIdx.x; i0 < total;
+         i0 += static_cast<I>(gridDim.x) * (256 * kRuns)) {
+        uint4 w[kRuns];
+        uint32_t byte[kRuns];
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r) {
+            const I i = i0 + r * 256;
+            w[r] = make_uint4(0u, 0u, 0u, 0u);
+            byte[r] = 0;
+            if (i < total_x) {
+                const I t = i / per_x;
+                const int c = static_cast<int>(i - t * per_x) * 8;
+                const uint8_t *const codes = a.x.codes + static_cast<long long>(t) * a.k + c;
+                byte[r] = a.x.scales[static_cast<long long>(t) * groups + c / 32];
+                if (a.runs) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(codes);
+                    w[r].x = v.x;
+                    w[r].y = v.y;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (c + e < a.k) (e < 4 ? w[r].x : w[r].y) |= static_cast<uint32_t>(codes[e]) << (8 * (e & 3));
+                }
+            } else if (i < total) {
+                const I t = (i - total_x) / per_d;
+                const int c = static_cast<int>(i - total_x - t * per_d) * 8;
+                const uint16_t *const src = a.d_out + static_cast<long long>(t) * a.d_stride + c;
+                uint32_t v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? src[e] : 0u;
+                w[r] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r) {
+            const I i = i0 + r * 256;
+            if (i < total_x) {
+                const I t = i / per_x;
+                const int c = static_cast<int>(i - t * per_x) * 8;
+                const Run v = ckpt_values8(make_uint2(w[r].x, w[r].y), byte[r], FMT);
+                store8(reinterpret_cast<T *>(a.x16 + static_cast<long long>(t) * a.x_pitch + c), v);
+            } else if (i < total) {
+                const I t = (i - total_x) / per_d;
+                const int c = static_cast<int>(i - total_x - t * per_d) * 8;
+                *reinterpret_cast<uint4 *>(a.d16 + static_cast<long long>(t) * a.d_pitch + c) = w[r];
+            }
+        }
+    }
+}
+template <class T, int FMT>
+cudaError_t launch_prepare(const PrepareArgs &a, int sms, bool pdl, cudaStream_t s) {
+    const long long total = a.T * ((a.k + 7) / 8 + (a.n + 7) / 8);
+    const long long need = (total + 256 * kRuns - 1) / (256 * kRuns), cap = static_cast<long long>(sms) * 8;
+    return launch_block_kernel(total < (1ll << 31) ? dw_prepare_kernel<T, FMT, unsigned>
+                                                   : dw_prepare_kernel<T, FMT, unsigned long long>,
+                               static_cast<unsigned>(need < cap ? need : cap), 256, 0, pdl, s, a);
 }
 
 std::atomic<int> g_dw_smem[64];
@@ -356,16 +429,18 @@ size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 // How a call runs: the splits of the tokens and the workspace's parts.
 struct DwPlan {
-    int tiles_n, tiles_k, steps, splits, steps_per_split;
+    int tile_k, tiles_n, tiles_k, steps, splits, steps_per_split;
     size_t x_bytes, d_bytes, part_bytes;
 };
 
-// Splits: with fewer tiles than pairs of CTAs, as many as give every pair an
-// item of at least 8 steps (512 tokens).
+// Tiles of 128 columns where those of 256 would leave half of the pairs of CTAs
+// idle. Splits: with fewer tiles than pairs, as many as give every pair an item
+// of at least 8 steps (512 tokens).
 DwPlan dw_plan(long long T, int n, int k, bool d_aligned) {
     DwPlan p;
     p.tiles_n = (n + kTile - 1) / kTile;
-    p.tiles_k = (k + kTile - 1) / kTile;
+    p.tile_k = static_cast<long long>(p.tiles_n) * ((k + kTile - 1) / kTile) <= kGridCap / 4 ? kTile / 2 : kTile;
+    p.tiles_k = (k + p.tile_k - 1) / p.tile_k;
     p.steps = static_cast<int>((T + kStep - 1) / kStep);
     const long long tiles = static_cast<long long>(p.tiles_n) * p.tiles_k;
     long long s = (kGridCap / 2) / tiles;
@@ -405,15 +480,16 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     void *const d16 = ws + p.x_bytes;
     float *const parts = reinterpret_cast<float *>(ws + p.x_bytes + p.d_bytes);
     const long long xp = pitch16(a.k), dp = d_aligned ? (a.T == 1 ? pitch16(a.n) : a.d_out_stride) : pitch16(a.n);
-    const CkptArgs u = {nullptr, x16, xp, a.T, a.k, a.x};
-    if (int e = note_launch(launch_ckpt_unpack(u, a.dtype, a.format, sms, pdl, s))) return e;
-    if (!d_aligned) {
-        const long long cap = static_cast<long long>(sms) * 8;
-        if (int e = note_launch(launch_block_kernel(
-                dw_align_kernel, static_cast<unsigned>(a.T < cap ? a.T : cap), 256, 0, pdl, s,
-                static_cast<const uint16_t *>(a.d_out), a.d_out_stride, static_cast<uint16_t *>(d16), dp, a.T, a.n)))
-            return e;
-    }
+    const PrepareArgs u = {a.x, a.T, a.k, d_aligned ? 0 : a.n, static_cast<uint16_t *>(x16), static_cast<uint16_t *>(d16), xp,
+                           pitch16(a.n), static_cast<const uint16_t *>(a.d_out), a.d_out_stride,
+                           a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x.codes) & 7u) == 0};
+    // a third faster where there is nothing but runs of 8 of the checkpoint
+    const bool plain = d_aligned && u.runs, e4m3 = a.format == MHC_CKPT_E4M3;
+    const CkptArgs c = {nullptr, x16, xp, a.T, a.k, a.x};
+    auto prepare = a.dtype == MHC_BF16 ? (e4m3 ? launch_prepare<__nv_bfloat16, MHC_CKPT_E4M3> : launch_prepare<__nv_bfloat16, MHC_CKPT_INT8>)
+                                       : (e4m3 ? launch_prepare<__half, MHC_CKPT_E4M3> : launch_prepare<__half, MHC_CKPT_INT8>);
+    if (int e = note_launch(plain ? launch_ckpt_unpack(c, a.dtype, a.format, sms, pdl, s) : prepare(u, sms, pdl, s)))
+        return e;
     CUtensorMap md, mx;
     if (!encode_rows16(&md, a.dtype == MHC_BF16, d_aligned ? a.d_out : d16, a.n, a.T, dp * 2, kStep) ||
         !encode_rows16(&mx, a.dtype == MHC_BF16, x16, a.k, a.T, xp * 2, kStep))
@@ -422,6 +498,7 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     g.T = a.T;
     g.n = a.n;
     g.k = a.k;
+    g.tile_k = p.tile_k;
     g.tiles_n = p.tiles_n;
     g.tiles_k = p.tiles_k;
     g.splits = p.splits;
