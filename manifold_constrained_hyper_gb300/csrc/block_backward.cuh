@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             using T = typename std::remove_cv<typename std::remove_reference<decltype(*row)>::type>::type;
             if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const T *>(st[k]), at, j);
             else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(row, at, j);
+            else if constexpr (MODE == ROWS_SKEW) return staged_skewed<T>(st[k], skew16(row), at, j);
             else return staged_single(reinterpret_cast<const T *>(st[k] + skew16(row)), at, j);
         };
         auto held = [&](const Ckpt &c, int k, int k_scales, int j) {
@@ -224,7 +225,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             const uint8_t *const byte_at = STAGED ? st[k_scales] + skew16(scales) : scales;
             if constexpr (MODE != ROWS_ANY) {
                 const int i = run_read_col(at, j);
-                return ckpt_values8(*reinterpret_cast<const uint2 *>((STAGED ? st[k] : codes) + i), byte_at[i / 32], a.format);
+                return ckpt_values8(*reinterpret_cast<const uint2 *>((STAGED ? st[k] + skew16(codes) : codes) + i), byte_at[i / 32],
+                                    a.format);
             } else {
                 const int col = run_col<MODE>(at, j);
                 const uint8_t *const code_at = st[k] + skew16(codes);
@@ -458,14 +460,17 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     if (H > 8192) return launch_block_bwd_loop(a, dtype, r_dtype, pdl, parts, s);
     const bool full = f.gate_form == MHC_GATE_FULL, scaled = f.scale_form == MHC_SCALE_CHANNEL;
     const bool held = !a.y || !a.residual;
-    auto codes_fit = [&](const Ckpt &c) { return (reinterpret_cast<uintptr_t>(c.codes) & 15u) == 0; };
-    const bool vec = H % (held ? 16 : 8) == 0 && (a.y ? rows_of_runs(a.y, a.y_stride, sizeof(TY), f.T) : codes_fit(a.ck_y)) &&
-                     (a.residual ? rows_of_runs(a.residual, a.r_stride, sizeof(TR), f.T) : codes_fit(a.ck_r)) &&
+    // what is written, the weights and the codes allow runs of 8; the inputs too
+    auto codes_fit = [&](const Ckpt &c) { return (reinterpret_cast<uintptr_t>(c.codes) & 7u) == 0; };
+    const bool out_vec = H % 8 == 0 && (a.y || codes_fit(a.ck_y)) && (a.residual || codes_fit(a.ck_r)) &&
+                         rows_of_runs(a.d_y, H, sizeof(TY), f.T) && rows_of_runs(a.d_r, H, sizeof(TR), f.T) &&
+                         rows_of_runs(a.sums, H, 4, f.T) && params_of_runs(f) &&
+                         (!full || !a.d_gate || rows_of_runs(a.d_gate, H, elem_bytes(f.gate_dtype), f.T));
+    const bool vec = out_vec && (!a.y || rows_of_runs(a.y, a.y_stride, sizeof(TY), f.T)) &&
+                     (!a.residual || rows_of_runs(a.residual, a.r_stride, sizeof(TR), f.T)) &&
                      (!a.d_ro || rows_of_runs(a.d_ro, a.d_ro_stride, sizeof(TR), f.T)) &&
-                     rows_of_runs(a.d_h, a.d_h_stride, sizeof(TY), f.T) && rows_of_runs(a.d_y, H, sizeof(TY), f.T) &&
-                     rows_of_runs(a.d_r, H, sizeof(TR), f.T) && rows_of_runs(a.sums, H, 4, f.T) && params_of_runs(f) &&
-                     (!full || (rows_of_runs(f.gate, f.gate_stride, elem_bytes(f.gate_dtype), f.T) &&
-                                (!a.d_gate || rows_of_runs(a.d_gate, H, elem_bytes(f.gate_dtype), f.T))));
+                     rows_of_runs(a.d_h, a.d_h_stride, sizeof(TY), f.T) &&
+                     (!full || rows_of_runs(f.gate, f.gate_stride, elem_bytes(f.gate_dtype), f.T));
     BwdRing ring = {};
     const int threads = row_threads(H, kBwdRuns);
     // as many groups as fit, but no more than give every SM a row
@@ -477,8 +482,8 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     *parts = static_cast<int>(grid);
     const size_t column = static_cast<size_t>(threads) * kBwdRuns * 32;     // the groups' sums at the end
     const int scale_bytes = static_cast<int>(ckpt_groups(H));
-    ring.place[0] = row_place(H, a.y ? sizeof(TY) : 1, !vec);
-    ring.place[1] = row_place(H, a.residual ? sizeof(TR) : 1, !vec);
+    ring.place[0] = row_place(H, a.y ? sizeof(TY) : 1, !vec || !a.y);
+    ring.place[1] = row_place(H, a.residual ? sizeof(TR) : 1, !vec || !a.residual);
     ring.place[2] = a.d_ro ? row_place(H, sizeof(TR), !vec) : 0;
     ring.place[3] = row_place(H, sizeof(TY), !vec);
     ring.place[4] = full ? row_place(H, elem_bytes(f.gate_dtype), !vec) : 0;
@@ -501,7 +506,8 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     int n = 0;
     if (require_device(&n, &ring.status)) return cudaErrorUnknown;
     ring.timeout_ns = wait_timeout_ns();
-    if (!vec) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+    if (!out_vec) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+    if (!vec) return bwd_launch<TY, TR, ROWS_SKEW, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (full) return bwd_launch<TY, TR, ROWS_RING, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (held)
         return scaled ? bwd_launch<TY, TR, ROWS_RING, false, true, true>(a, ring, grid, threads, smem, pdl, s)

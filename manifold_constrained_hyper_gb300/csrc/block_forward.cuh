@@ -131,18 +131,23 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         auto load_y = [&](int j) {
             if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st), at, j);
             else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(y_row, at, j);
+            else if constexpr (MODE == ROWS_SKEW) return staged_skewed<TY>(st, skew16(y_row), at, j);
             else return staged_single(reinterpret_cast<const TY *>(st + skew16(y_row)), at, j);
         };
         auto load_r = [&](int j) {
             const uint8_t *const row = st + ring.y_place;
             if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(row), at, j);
             else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(r_row, at, j);
+            else if constexpr (MODE == ROWS_SKEW) return staged_skewed<TR>(row, skew16(r_row), at, j);
             else return staged_single(reinterpret_cast<const TR *>(row + skew16(r_row)), at, j);
         };
         auto load_z = [&](int j) {
             const uint8_t *const row = st + ring.y_place + ring.r_place;
             if constexpr (MODE == ROWS_RING) return staged_run_any(row, f.gate_dtype, at, j);
             else if constexpr (MODE == ROWS_VEC) return load_run_any<MODE>(g_row, f.gate_dtype, at, j);
+            else if constexpr (MODE == ROWS_SKEW)
+                return f.gate_dtype == MHC_F32 ? staged_skewed<float>(row, skew16(g_row), at, j)
+                                               : staged_skewed<TY>(row, skew16(g_row), at, j);
             else return f.gate_dtype == MHC_F32
                             ? staged_single(reinterpret_cast<const float *>(row + skew16(g_row)), at, j)
                             : staged_single(reinterpret_cast<const TY *>(row + skew16(g_row)), at, j);
@@ -265,15 +270,17 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
     if (f.H > 8192) return launch_block_fwd_loop(a, dtype, r_dtype, sms, pdl, s);
     const bool full = f.gate_form == MHC_GATE_FULL, scaled = f.scale_form == MHC_SCALE_CHANNEL;
     const Ckpt cks[] = {a.ck_y, a.ck_r, a.ck_h};
-    bool vec = f.H % 8 == 0 && rows_of_runs(a.y, a.y_stride, sizeof(TY), f.T) &&
-               rows_of_runs(a.residual, a.r_stride, sizeof(TR), f.T) &&
-               rows_of_runs(a.residual_out, f.H, sizeof(TR), f.T) && rows_of_runs(a.h, f.H, sizeof(TY), f.T) &&
-               params_of_runs(f) && (!full || rows_of_runs(f.gate, f.gate_stride, elem_bytes(f.gate_dtype), f.T));
+    // what is written and the weights allow runs of 8; the inputs too
+    bool out_vec = f.H % 8 == 0 && rows_of_runs(a.residual_out, f.H, sizeof(TR), f.T) &&
+                   rows_of_runs(a.h, f.H, sizeof(TY), f.T) && params_of_runs(f);
     bool ckpt = false;
     for (const Ckpt &c : cks) {
-        vec = vec && (reinterpret_cast<uintptr_t>(c.codes) & 7u) == 0;
+        out_vec = out_vec && (reinterpret_cast<uintptr_t>(c.codes) & 7u) == 0;
         ckpt = ckpt || c.codes;
     }
+    const bool vec = out_vec && rows_of_runs(a.y, a.y_stride, sizeof(TY), f.T) &&
+                     rows_of_runs(a.residual, a.r_stride, sizeof(TR), f.T) &&
+                     (!full || rows_of_runs(f.gate, f.gate_stride, elem_bytes(f.gate_dtype), f.T));
     FwdRing ring = {};
     ring.groups = 1;
     if (vec && f.T <= sms) {
@@ -305,7 +312,8 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
     int n = 0;
     if (require_device(&n, &ring.status)) return cudaErrorUnknown;
     ring.timeout_ns = wait_timeout_ns();
-    if (!vec) return fwd_launch<TY, TR, ROWS_ANY, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+    if (!out_vec) return fwd_launch<TY, TR, ROWS_ANY, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+    if (!vec) return fwd_launch<TY, TR, ROWS_SKEW, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (full)
         return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, true, true, true>(a, ring, grid, threads, smem, pdl, s)
                     : fwd_launch<TY, TR, ROWS_RING, 4, true, true, false>(a, ring, grid, threads, smem, pdl, s);

@@ -12,7 +12,8 @@ namespace mhc {
 enum RowMode : int {
     ROWS_RING = 0,      // staged ahead of use by bulk copies, runs of 8 (rows on boundaries of 8 elements)
     ROWS_VEC = 1,       // runs of 8 from global memory: a few rows only, or rows too wide for two stages
-    ROWS_ANY = 2        // staged, single elements: any boundary
+    ROWS_ANY = 2,       // staged, single elements: any boundary
+    ROWS_SKEW = 3       // staged, runs of 8 of inputs on any boundary; what is written is on boundaries of 8 elements
 };
 // A thread holds RUNS runs of 8 columns of its group's row: with vector loads
 // run j is the columns from (j * threads + thread) * 8, with single ones the
@@ -67,6 +68,11 @@ template <class T>
 __device__ __forceinline__ Run staged_run(const T *row, const Place &p, int j) {
     return load8_shared(row + run_read_col(p, j));
 }
+// The same `skew` bytes into its place.
+template <class T>
+__device__ __forceinline__ Run staged_skewed(const uint8_t *place, uint32_t skew, const Place &p, int j) {
+    return load8_skewed(reinterpret_cast<const uint4 *>(place + run_read_col(p, j) * sizeof(T)), skew, static_cast<const T *>(nullptr));
+}
 // The same on any boundary, single elements; what lies past the row's end is 0.
 template <class T>
 __device__ __forceinline__ Run staged_single(const T *row, const Place &p, int j) {
@@ -84,10 +90,10 @@ __device__ __forceinline__ uint32_t skewed_bytes(const void *p, uint32_t bytes) 
 __device__ __forceinline__ void bulk_load_row(uint32_t dst, const void *p, uint32_t bytes, uint32_t bar, uint64_t policy) {
     bulk_load(dst, static_cast<const uint8_t *>(p) - skew16(p), skewed_bytes(p, bytes), bar, policy);
 }
-// A row's place in a stage.
+// A row's place in a stage; on any boundary with the 16 bytes past it that runs of 8 may read.
 inline uint32_t row_place(int H, int elem, bool any) {
     const uint32_t bytes = static_cast<uint32_t>(H) * elem;
-    return any ? (bytes + 15 + 15) / 16 * 16 : bytes;
+    return any ? (bytes + 15 + 15) / 16 * 16 + 16 : bytes;
 }
 __device__ __forceinline__ Run staged_run_any(const void *row, int dtype, const Place &p, int j) {
     if (dtype == MHC_F32) return staged_run(static_cast<const float *>(row), p, j);

@@ -347,6 +347,19 @@ __global__ void __launch_bounds__(256) dw_join_kernel(const float *parts, int sp
 // and, where its rows do not allow 16-byte loads, d_out; each in rows on 16-byte
 // boundaries. Eight columns a lane, kRuns of them in flight; past a row's
 // end stands 0 (the copies above cut rows at their length).
+// Bytes [addr, addr + 8 N) of a row that ends at `end`, from the aligned 8-byte words
+// that hold them (a word that holds none of the row is not read).
+template <int N>
+__device__ __forceinline__ void load_words(uintptr_t addr, uintptr_t end, uint64_t (&out)[N]) {
+    const uintptr_t first = addr & ~static_cast<uintptr_t>(7);
+    const uint32_t bits = static_cast<uint32_t>(addr - first) * 8;
+    uint64_t w[N + 1];
+#pragma unroll
+    for (int i = 0; i <= N; ++i)
+        w[i] = first + 8 * i < end ? *reinterpret_cast<const uint64_t *>(first + 8 * i) : 0ull;
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = bits ? (w[i] >> bits) | (w[i + 1] << (64 - bits)) : w[i];
+}
 struct PrepareArgs {
     Ckpt x;
     long long T;
@@ -355,7 +368,6 @@ struct PrepareArgs {
     long long x_pitch, d_pitch;
     const uint16_t *d_out;
     long long d_stride;
-    int runs;                       // 8 codes at once: k a multiple of 8 and the codes on 8 bytes
 };
 constexpr int kRuns = 4;
 template <class T, int FMT, class I>
@@ -376,25 +388,20 @@ __global__ void __launch_bounds__(256) dw_prepare_kernel(const PrepareArgs a) {
             if (i < total_x) {
                 const I t = i / per_x;
                 const int c = static_cast<int>(i - t * per_x) * 8;
-                const uint8_t *const codes = a.x.codes + static_cast<long long>(t) * a.k + c;
                 byte[r] = a.x.scales[static_cast<long long>(t) * groups + c / 32];
-                if (a.runs) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(codes);
-                    w[r].x = v.x;
-                    w[r].y = v.y;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (c + e < a.k) (e < 4 ? w[r].x : w[r].y) |= static_cast<uint32_t>(codes[e]) << (8 * (e & 3));
-                }
+                const uintptr_t row = reinterpret_cast<uintptr_t>(a.x.codes) + static_cast<uintptr_t>(t) * a.k;
+                uint64_t v[1];
+                load_words<1>(row + c, row + a.k, v);
+                w[r].x = static_cast<uint32_t>(v[0]);
+                w[r].y = static_cast<uint32_t>(v[0] >> 32);
             } else if (i < total) {
                 const I t = (i - total_x) / per_d;
                 const int c = static_cast<int>(i - total_x - t * per_d) * 8;
-                const uint16_t *const src = a.d_out + static_cast<long long>(t) * a.d_stride + c;
-                uint32_t v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? src[e] : 0u;
-                w[r] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+                const uintptr_t row = reinterpret_cast<uintptr_t>(a.d_out + static_cast<long long>(t) * a.d_stride);
+                uint64_t v[2];
+                load_words<2>(row + 2 * c, row + 2 * static_cast<uintptr_t>(a.n), v);
+                w[r] = make_uint4(static_cast<uint32_t>(v[0]), static_cast<uint32_t>(v[0] >> 32), static_cast<uint32_t>(v[1]),
+                                  static_cast<uint32_t>(v[1] >> 32));
             }
         }
 #pragma unroll
@@ -481,10 +488,9 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     float *const parts = reinterpret_cast<float *>(ws + p.x_bytes + p.d_bytes);
     const long long xp = pitch16(a.k), dp = d_aligned ? (a.T == 1 ? pitch16(a.n) : a.d_out_stride) : pitch16(a.n);
     const PrepareArgs u = {a.x, a.T, a.k, d_aligned ? 0 : a.n, static_cast<uint16_t *>(x16), static_cast<uint16_t *>(d16), xp,
-                           pitch16(a.n), static_cast<const uint16_t *>(a.d_out), a.d_out_stride,
-                           a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x.codes) & 7u) == 0};
+                           pitch16(a.n), static_cast<const uint16_t *>(a.d_out), a.d_out_stride};
     // a third faster where there is nothing but runs of 8 of the checkpoint
-    const bool plain = d_aligned && u.runs, e4m3 = a.format == MHC_CKPT_E4M3;
+    const bool plain = d_aligned && a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x.codes) & 7u) == 0, e4m3 = a.format == MHC_CKPT_E4M3;
     const CkptArgs c = {nullptr, x16, xp, a.T, a.k, a.x};
     auto prepare = a.dtype == MHC_BF16 ? (e4m3 ? launch_prepare<__nv_bfloat16, MHC_CKPT_E4M3> : launch_prepare<__nv_bfloat16, MHC_CKPT_INT8>)
                                        : (e4m3 ? launch_prepare<__half, MHC_CKPT_E4M3> : launch_prepare<__half, MHC_CKPT_INT8>);

@@ -72,6 +72,35 @@ template <class T>
 __device__ __forceinline__ Run load8_shared(const T *p) {
     return unpack8(*reinterpret_cast<const uint4 *>(p), p);
 }
+// 8 values that begin `skew` bytes past a 16-byte boundary `p`: the aligned words
+// around them, picked by the bits of skew (the same for a whole row).
+template <class T>
+__device__ __forceinline__ Run load8_skewed(const uint4 *p, uint32_t skew, const T *tag) {
+    const uint4 a = p[0], b = p[1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t t[6], u[5];
+#pragma unroll
+    for (int j = 0; j < 6; ++j) t[j] = skew & 8 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) u[j] = skew & 4 ? t[j + 1] : t[j];
+    const uint32_t bits = (skew & 2) * 8;
+    return unpack8(make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
+                              __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits)), tag);
+}
+__device__ __forceinline__ Run load8_skewed(const uint4 *p, uint32_t skew, const float *) {
+    const uint4 a = p[0], b = p[1], c = p[2];
+    const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+    uint32_t t[9];
+#pragma unroll
+    for (int j = 0; j < 9; ++j) t[j] = skew & 8 ? w[j + 2] : w[j];
+    Run r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = skew & 4 ? t[2 * i + 1] : t[2 * i], hi = skew & 4 ? t[2 * i + 2] : t[2 * i + 1];
+        r.p[i] = (static_cast<uint64_t>(hi) << 32) | lo;
+    }
+    return r;
+}
 __device__ __forceinline__ void store8(float *p, const Run &r) {
     asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};"
                  ::"l"(reinterpret_cast<uint64_t>(p)), "l"(r.p[0]), "l"(r.p[1]), "l"(r.p[2]), "l"(r.p[3]) : "memory");
