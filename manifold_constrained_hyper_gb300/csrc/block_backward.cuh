@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         tmem_alloc(smem_addr(&tmem_slot), kBwdTmemCols);
         tmem_relinquish();
     }
-    for (int i = threadIdx.x; i < kBwdGroups * 2 * 3 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    for (int i = threadIdx.x; i < ring.groups * 2 * 3 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
     if (STAGED && threadIdx.x == 0) {
         for (int s = 0; s < ring.stages; ++s) mbar_init(bar + 8 * s, 1);
         abort_flag = 0;
@@ -141,23 +141,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     // w1 = (w_post + offset) * act of a channel gate, w2 = w_pre + offset, a channel scale; the sums
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-        Run w = load_weights<MODE>(f.w_post, f.w_post_dtype, f.weight_offset, at, j);
-        if (f.gate_form == MHC_GATE_CHANNEL) {
-            Run g = load_run_any<MODE>(f.gate, f.gate_dtype, at, j);
-            run_gate(g, f.gate_act);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w.p[i] = mul2(w.p[i], g.p[i]);
-        }
+        const RowParams p = load_row_params<MODE>(f, at, j);
         __syncwarp();
-        tmem_run_store(cell(T_W1, j), w);
-        w = load_weights<MODE>(f.w_pre, f.w_pre_dtype, f.weight_offset, at, j);
-        __syncwarp();
-        tmem_run_store(cell(T_W2, j), w);
-        if (SCALED) {
-            w = load_scale<MODE>(f, at, j);
-            __syncwarp();
-            tmem_run_store(cell(T_SCALE, j), w);
-        }
+        tmem_run_store(cell(T_W1, j), p.w1);
+        tmem_run_store(cell(T_W2, j), p.w2);
+        if (SCALED) tmem_run_store(cell(T_SCALE, j), p.sc);
         tmem_run_store(cell(T_DW1, j), run_splat(0.f));
         tmem_run_store(cell(T_DW2, j), run_splat(0.f));
         if (SCALED) tmem_run_store(cell(T_DSCALE, j), run_splat(0.f));
@@ -233,12 +221,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int i = col + e * at.threads;
-                    v[e] = 0.f;
-                    if (i < H)
-                        v[e] = (a.format == MHC_CKPT_E4M3 ? ckpt_value<MHC_CKPT_E4M3>(code_at[i])
-                                                          : ckpt_value<MHC_CKPT_INT8>(code_at[i])) *
-                               ckpt_unit(byte_at[i / 32]);
+                    const int i = min(col + e * at.threads, H - 1);
+                    v[e] = (a.format == MHC_CKPT_E4M3 ? ckpt_value<MHC_CKPT_E4M3>(code_at[i])
+                                                      : ckpt_value<MHC_CKPT_INT8>(code_at[i])) *
+                           ckpt_unit(byte_at[i / 32]);
                 }
                 return run_of(v);
             }
@@ -367,7 +353,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
                 }
             }
             store_run<MODE>(static_cast<TY *>(a.d_y) + t * H, at, j, y);
-            if (!SCALED && (MODE == ROWS_ANY || run_col<MODE>(at, j) < H)) {
+            if (!SCALED && run_col<MODE>(at, j) < H) {          // (single elements are SCALED)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) scale2 = fma2(r.p[i], ev[j].p[i], scale2);
             }
@@ -429,9 +415,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             __syncwarp();
             tmem_run_load(cell(T_DSCALE, j), acc);
             tmem_run_wait(acc);
-            if (MODE == ROWS_ANY || run_col<MODE>(at, j) < H)
+            acc = run_within<MODE>(acc, at, j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) total[0] += f2_lo(acc.p[i]) + f2_hi(acc.p[i]);
+            for (int i = 0; i < 4; ++i) total[0] += f2_lo(acc.p[i]) + f2_hi(acc.p[i]);
         }
     }
     block_sum<1>(total, scale_red);

@@ -21,6 +21,7 @@ cudaError_t launch_block_fwd_loop(const BlockFwdArgs &a, int dtype, int r_dtype,
 namespace {
 
 constexpr int kFwdStages = 32;
+constexpr int kFwdNarrow = 1024;                    // columns up to which rows go by registers alone
 constexpr int kFwdGroups = 15;                      // named barriers 1 .. 15
 constexpr size_t kFwdSmem = 224 * 1024;             // dynamic
 enum FwdSite : int { SITE_FWD_ROW = 70 };
@@ -34,11 +35,11 @@ struct FwdRing {
 };
 
 // FULL, SCALED, CKPT: whether a call may have a full gate, a channel scale,
-// checkpoints. RUNS of 8 columns a thread: 4, and 2 of single elements, in blocks of up to 512 threads of
-// 128 registers; 1, up to 1024 threads of 64, where a CTA has one row only.
+// checkpoints. RUNS of 8 columns a thread: 4, and 2 of rows on any boundary, in blocks of up to 512
+// threads of 128 registers; 1, up to 1024 threads of 64, for a few rows or narrow ones.
 template <class TY, class TR, int MODE, int RUNS, bool FULL, bool SCALED, bool CKPT>
 __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(const BlockFwdArgs a, const FwdRing ring) {
-    constexpr int MAXW = 32 / RUNS, GROUPS = RUNS == 1 ? 1 : kFwdGroups;
+    constexpr int MAXW = 32 / RUNS, GROUPS = RUNS == 1 ? 32 : kFwdGroups;
     constexpr bool STAGED = MODE != ROWS_VEC;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float red[GROUPS][2][MAXW];
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     Place at;
     at.H = f.H;
     at.threads = blockDim.x / ring.groups;
-    const int grp = GROUPS == 1 ? 0 : threadIdx.x / at.threads;
+    const int grp = threadIdx.x / at.threads;
     at.thread = threadIdx.x - grp * at.threads;
     const int warp = at.thread >> 5, warps = at.threads >> 5;
     const bool full_gate = FULL && f.gate_form == MHC_GATE_FULL;
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     const uint32_t stage0 = (SCALED ? 3 : 2) * 32 * RUNS * at.threads;
     const uint32_t bar = smem_addr(bars);
 
-    for (int i = threadIdx.x; i < GROUPS * 2 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    for (int i = threadIdx.x; i < ring.groups * 2 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
     if (STAGED && threadIdx.x == 0) {
         for (int s = 0; s < ring.stages; ++s) mbar_init(bar + 8 * s, 1);
         abort_flag = 0;
@@ -95,19 +96,14 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
             const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
             if (t < f.T) fetch(t, s);
         }
+    if (grp == 0) {
 #pragma unroll
-    for (int j = 0; j < RUNS; ++j) {
-        if (grp > 0) break;
-        Run w = load_weights<MODE>(f.w_post, f.w_post_dtype, f.weight_offset, at, j);
-        if (f.gate_form == MHC_GATE_CHANNEL) {
-            Run g = load_run_any<MODE>(f.gate, f.gate_dtype, at, j);
-            run_gate(g, f.gate_act);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w.p[i] = mul2(w.p[i], g.p[i]);
+        for (int j = 0; j < RUNS; ++j) {
+            const RowParams p = load_row_params<MODE>(f, at, j);
+            keep_run(w1_kept, at, j, p.w1);
+            keep_run(w2_kept, at, j, p.w2);
+            if (SCALED) keep_run(sc_kept, at, j, p.sc);
         }
-        keep_run(w1_kept, at, j, w);
-        keep_run(w2_kept, at, j, load_weights<MODE>(f.w_pre, f.w_pre_dtype, f.weight_offset, at, j));
-        if (SCALED) keep_run(sc_kept, at, j, load_scale<MODE>(f, at, j));
     }
     if (ring.groups > 1) __syncthreads();           // one group: each thread reads what it wrote
     const uint64_t scale = splat2(f.scale_form == MHC_SCALE_ONE ? *f.res_scale : 1.f);
@@ -161,11 +157,12 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         }
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
-            // past the row's end stands its last run again: not in the sums
-            const bool in = MODE == ROWS_ANY || run_col<MODE>(at, j) < f.H;
+            // past the row's end stands its last run, or element, again: not in the sums
+            const bool in = run_col<MODE>(at, j) < f.H;
             if (in) {
+                const Run v = MODE == ROWS_ANY ? run_within<MODE>(y[j], at, j) : y[j];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s2 = fma2(y[j].p[i], y[j].p[i], s2);
+                for (int i = 0; i < 4; ++i) s2 = fma2(v.p[i], v.p[i], s2);
             }
             if (CKPT && a.ck_y.codes) store_ckpt<MODE>(a.ck_y, a.format, t, at, j, y[j]);
             if (CKPT && a.ck_r.codes) store_ckpt<MODE>(a.ck_r, a.format, t, at, j, v[j]);
@@ -260,7 +257,8 @@ cudaError_t fwd_launch(const BlockFwdArgs &a, const FwdRing &ring, unsigned grid
                        cudaStream_t s) {
     static SmemGrant grant;
     auto kern = block_fwd_kernel<TY, TR, MODE, RUNS, FULL, SCALED, CKPT>;
-    if (cudaError_t e = grant_smem(kern, grant, smem, kFwdSmem)) return e;
+    // with one run a thread: the kept columns of 1024 threads
+    if (cudaError_t e = grant_smem(kern, grant, smem, RUNS == 1 ? 96 * 1024 : kFwdSmem)) return e;
     return launch_block_kernel(kern, grid, threads * ring.groups, smem, pdl, s, a, ring);
 }
 
@@ -283,16 +281,19 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
                      (!full || rows_of_runs(f.gate, f.gate_stride, elem_bytes(f.gate_dtype), f.T));
     FwdRing ring = {};
     ring.groups = 1;
-    if (vec && f.T <= sms) {
-        // a CTA for each row, a thread for each run of it
+    const long long rows = (f.T + sms - 1) / sms;
+    if (vec && (rows == 1 || f.H <= kFwdNarrow)) {
+        // a thread for each run of a row; a row's warp needs no barrier
         const int threads = row_threads(f.H, 1);
-        return fwd_launch<TY, TR, ROWS_VEC, 1, true, true, true>(a, ring, static_cast<unsigned>(f.T), threads,
-                                                                 3 * 32 * threads, pdl, s);
+        long long groups = 1024 / threads;
+        if (threads > 32 && groups > kFwdGroups) groups = kFwdGroups;
+        ring.groups = static_cast<int>(rows < groups ? rows : groups);
+        return fwd_launch<TY, TR, ROWS_VEC, 1, true, true, true>(a, ring, static_cast<unsigned>(f.T < sms ? f.T : sms),
+                                                                 threads, 3 * 32 * threads, pdl, s);
     }
     // as many groups as fit, but no more than give every SM a row
     const int runs = vec ? 4 : 2, threads = row_threads(f.H, runs);
     long long groups = 512 / threads;
-    const long long rows = (f.T + sms - 1) / sms;
     if (groups > kFwdGroups) groups = kFwdGroups;
     ring.groups = static_cast<int>(rows < groups ? rows : groups);
     const unsigned grid = static_cast<unsigned>(f.T < sms ? f.T : sms);

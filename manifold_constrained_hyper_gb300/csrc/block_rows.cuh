@@ -73,13 +73,23 @@ template <class T>
 __device__ __forceinline__ Run staged_skewed(const uint8_t *place, uint32_t skew, const Place &p, int j) {
     return load8_skewed(reinterpret_cast<const uint4 *>(place + run_read_col(p, j) * sizeof(T)), skew, static_cast<const T *>(nullptr));
 }
-// The same on any boundary, single elements; what lies past the row's end is 0.
+// The same on any boundary, single elements; past the row's end stands its last one again.
 template <class T>
 __device__ __forceinline__ Run staged_single(const T *row, const Place &p, int j) {
     const int c = run_col<ROWS_ANY>(p, j);
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e * p.threads < p.H ? to_f32(row[c + e * p.threads]) : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(row[min(c + e * p.threads, p.H - 1)]);
+    return run_of(v);
+}
+// A run with what lies past the row's end set to 0.
+template <int MODE>
+__device__ __forceinline__ Run run_within(const Run &r, const Place &p, int j) {
+    const int c = run_col<MODE>(p, j);
+    if (MODE != ROWS_ANY) return c < p.H ? r : run_splat(0.f);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e * p.threads < p.H ? run_at(r, e) : 0.f;
     return run_of(v);
 }
 // Bulk copies start and end on 16-byte boundaries: a row that does not is
@@ -138,31 +148,98 @@ __device__ __forceinline__ void tmem_run_store(uint32_t taddr, const Run &r) {
                    "r"(static_cast<uint32_t>(r.p[2])), "r"(static_cast<uint32_t>(r.p[2] >> 32)),
                    "r"(static_cast<uint32_t>(r.p[3])), "r"(static_cast<uint32_t>(r.p[3] >> 32)) : "memory");
 }
-// The residual's scale of run j; past the row's end 0, as of the weights.
-template <int MODE>
-__device__ __forceinline__ Run load_scale(const BlockForm &f, const Place &p, int j) {
-    if (MODE != ROWS_ANY && run_col<MODE>(p, j) >= p.H) return run_splat(0.f);
-    if (f.scale_form == MHC_SCALE_CHANNEL) return load_run<MODE>(f.res_scale, p, j);
-    return run_splat(f.scale_form == MHC_SCALE_ONE ? *f.res_scale : 1.f);
-}
-// Weights of run j with their offset, 1 where there are none; past the row's
-// end 0, so that what they multiply leaves the row's sums alone.
-template <int MODE>
-__device__ __forceinline__ Run load_weights(const void *w, int dtype, float offset, const Place &p, int j) {
-    if (MODE != ROWS_ANY && run_col<MODE>(p, j) >= p.H) return run_splat(0.f);
-    if (!w) return run_splat(1.f);
-    Run r = load_run_any<MODE>(w, dtype, p, j);
-    if (offset != 0.f) {
-        const uint64_t o = splat2(offset);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.p[i] = add2(r.p[i], o);
-    }
-    return r;
-}
 __device__ __forceinline__ void run_gate(Run &r, int act) {
     if (act == MHC_ACT_NONE) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) r.p[i] = f2_pack(gate_value(f2_lo(r.p[i]), act), gate_value(f2_hi(r.p[i]), act));
+}
+// Run j of a vector parameter as it lies in memory, of a type known at run time.
+// Predicated loads, no branches: those of all parameters are in flight together,
+// and a kernel's start goes by one latency instead of one for each of them.
+struct RawParam {
+    uint32_t w[8];
+};
+template <int MODE>
+__device__ __forceinline__ RawParam raw_param(const void *p, int dtype, const Place &at, int j) {
+    RawParam r = {};
+    const int wide = p && dtype == MHC_F32, narrow = p && dtype != MHC_F32;
+    if constexpr (MODE != ROWS_ANY) {
+        const uint64_t a = reinterpret_cast<uint64_t>(p) + static_cast<uint64_t>(run_read_col(at, j)) * (wide ? 4 : 2);
+        asm volatile(
+            "{\n.reg .pred p, q;\nsetp.ne.b32 p, %9, 0;\nsetp.ne.b32 q, %10, 0;\n"
+            "@p ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+            "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%8];\n}"
+            : "+r"(r.w[0]), "+r"(r.w[1]), "+r"(r.w[2]), "+r"(r.w[3]), "+r"(r.w[4]), "+r"(r.w[5]), "+r"(r.w[6]), "+r"(r.w[7])
+            : "l"(a), "r"(wide), "r"(narrow) : "memory");
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint64_t c = static_cast<uint64_t>(min(run_col<ROWS_ANY>(at, j) + e * at.threads, at.H - 1));
+            asm volatile(
+                "{\n.reg .pred p, q;\nsetp.ne.b32 p, %2, 0;\nsetp.ne.b32 q, %3, 0;\n"
+                "@p ld.global.b32 %0, [%1];\n@q ld.global.u16 %0, [%1];\n}"
+                : "+r"(r.w[e]) : "l"(reinterpret_cast<uint64_t>(p) + c * (wide ? 4 : 2)), "r"(wide), "r"(narrow) : "memory");
+        }
+    }
+    return r;
+}
+template <int MODE>
+__device__ __forceinline__ Run param_run(const RawParam &r, int dtype) {
+    float v[8];
+    if (dtype == MHC_F32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r.w[e]);
+        return run_of(v);
+    }
+    if constexpr (MODE != ROWS_ANY) {
+        const uint4 w = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        return dtype == MHC_BF16 ? unpack8(w, static_cast<const __nv_bfloat16 *>(nullptr))
+                                 : unpack8(w, static_cast<const __half *>(nullptr));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = dtype == MHC_BF16 ? __uint_as_float(r.w[e] << 16)
+                                 : __half2float(__ushort_as_half(static_cast<unsigned short>(r.w[e])));
+    return run_of(v);
+}
+// What every row of a block needs of run j: w1 = (w_post + offset) * act of a
+// channel gate, w2 = w_pre + offset, the residual's scale (1 where there is
+// none); past the row's end 0, so that what they multiply leaves the row's sums alone.
+struct RowParams {
+    Run w1, w2, sc;
+};
+template <int MODE>
+__device__ __forceinline__ RowParams load_row_params(const BlockForm &f, const Place &at, int j) {
+    const bool gated = f.gate_form == MHC_GATE_CHANNEL, scaled = f.scale_form == MHC_SCALE_CHANNEL;
+    const RawParam r1 = raw_param<MODE>(f.w_post, f.w_post_dtype, at, j), r2 = raw_param<MODE>(f.w_pre, f.w_pre_dtype, at, j),
+                   rg = raw_param<MODE>(gated ? f.gate : nullptr, f.gate_dtype, at, j),
+                   rs = raw_param<MODE>(scaled ? f.res_scale : nullptr, MHC_F32, at, j);
+    const float one = f.scale_form == MHC_SCALE_ONE ? *f.res_scale : 1.f;
+    RowParams p;
+    const uint64_t offset = splat2(f.weight_offset);
+    p.w1 = run_splat(1.f);
+    if (f.w_post) {
+        p.w1 = param_run<MODE>(r1, f.w_post_dtype);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.w1.p[i] = add2(p.w1.p[i], offset);
+    }
+    if (gated) {
+        Run g = param_run<MODE>(rg, f.gate_dtype);
+        run_gate(g, f.gate_act);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.w1.p[i] = mul2(p.w1.p[i], g.p[i]);
+    }
+    p.w2 = run_splat(1.f);
+    if (f.w_pre) {
+        p.w2 = param_run<MODE>(r2, f.w_pre_dtype);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.w2.p[i] = add2(p.w2.p[i], offset);
+    }
+    p.sc = scaled ? param_run<MODE>(rs, MHC_F32) : run_splat(one);
+    p.w1 = run_within<MODE>(p.w1, at, j);
+    p.w2 = run_within<MODE>(p.w2, at, j);
+    p.sc = run_within<MODE>(p.sc, at, j);
+    return p;
 }
 // Run j of a row's checkpoint. Whole warps call it.
 template <int FMT, int MODE>

@@ -33,7 +33,8 @@ constexpr int kStageBytes = 4 * kBoxBytes;          // two boxes of either opera
 constexpr int kStages = 6;
 constexpr int kThreads = 192;                       // loads, products, four warps of epilogue
 constexpr int kBars = 2 * kStages + 5;
-constexpr int kSmem = kStages * kStageBytes + 1024 /* alignment */ + 256 /* barriers */;
+constexpr int kTurnBytes = 4 * 32 * 33 * 4;         // a 32 x 32 piece of the sums for each epilogue warp
+constexpr int kSmem = kStages * kStageBytes + 1024 /* alignment */ + 256 /* barriers */ + kTurnBytes;
 constexpr int kTmemCols = 512;
 constexpr int kBand = 8;                            // rows of tiles that are walked together
 
@@ -106,60 +107,27 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "r"(taddr) : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack16(float a, float b, int dtype) {
-    if (dtype == MHC_BF16) return bf2_pack_rn(f2_pack(a, b));
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-// Columns [j, j + 32) of one row of out, `row` its first element.
+// Columns [j, j + 32) of one row of out on a 32-byte boundary, `row` its first
+// element. k is a multiple of 8 here: groups of 8 columns are in or out as a whole.
 __device__ __forceinline__ void store_row(const GemmArgs &a, long long row, int j, const uint32_t (&v)[32]) {
-    if (a.wide) {
-        // k is a multiple of 8 here: groups of 8 columns are in or out as a whole
-        if (a.out_dtype == MHC_F32) {
-            float *p = static_cast<float *>(a.out) + row + j;
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-                if (j + c >= a.k) break;
-                uint4 lo = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-                uint4 hi = make_uint4(v[c + 4], v[c + 5], v[c + 6], v[c + 7]);
-                if (a.accumulate) {
-                    float *const o[8] = {reinterpret_cast<float *>(&lo.x), reinterpret_cast<float *>(&lo.y),
-                                         reinterpret_cast<float *>(&lo.z), reinterpret_cast<float *>(&lo.w),
-                                         reinterpret_cast<float *>(&hi.x), reinterpret_cast<float *>(&hi.y),
-                                         reinterpret_cast<float *>(&hi.z), reinterpret_cast<float *>(&hi.w)};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) *o[e] += p[c + e];
-                }
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                             ::"l"(reinterpret_cast<uint64_t>(p + c)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
-                               "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
-            }
-        } else {
-            uint16_t *p = static_cast<uint16_t *>(a.out) + row + j;
-#pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-                if (j + c >= a.k) break;
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = __uint_as_float(v[c + 2 * e]), y = __uint_as_float(v[c + 2 * e + 1]);
-                    if (a.accumulate) {
-                        x += load_any(p, a.out_dtype, c + 2 * e);
-                        y += load_any(p, a.out_dtype, c + 2 * e + 1);
-                    }
-                    w[e] = pack16(x, y, a.out_dtype);
-                }
-                *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < 32; c += 8) {
         if (j + c >= a.k) break;
-        float x = __uint_as_float(v[c]);
-        if (a.accumulate) x += load_any(a.out, a.out_dtype, row + j + c);
-        store_any(a.out, a.out_dtype, row + j + c, x);
+        Run r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.p[i] = (static_cast<uint64_t>(v[c + 2 * i + 1]) << 32) | v[c + 2 * i];
+        const long long at = row + j + c;
+        auto put = [&](auto *p) {
+            if (a.accumulate) {
+                const Run old = load8(p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r.p[i] = add2(old.p[i], r.p[i]);
+            }
+            store8(p, r);
+        };
+        if (a.out_dtype == MHC_F32) put(static_cast<float *>(a.out) + at);
+        else if (a.out_dtype == MHC_BF16) put(static_cast<__nv_bfloat16 *>(a.out) + at);
+        else put(static_cast<__half *>(a.out) + at);
     }
 }
 
@@ -187,6 +155,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                    acc_empty = acc_full + 16, drain = acc_full + 32;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + kStages * kStageBytes + 8 * kBars);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *const turn = reinterpret_cast<float *>(basep + kStages * kStageBytes + 256);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = dw_cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -315,7 +284,27 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                 uint32_t v[32];
                 tmem_ld32(tmem + buf * kTile + c + (static_cast<uint32_t>(quad * 32) << 16), v);
                 tmem_ld_wait();
-                if (i < a.n) store_row(a, row, j, v);
+                if (a.wide) {
+                    if (i < a.n) store_row(a, row, j, v);
+                    continue;
+                }
+                // rows on any boundary: the piece turned in shared memory, then a row a store
+                float *const piece = turn + (warp - 2) * 32 * 33;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) piece[lane * 33 + e] = __uint_as_float(v[e]);
+                __syncwarp();
+                const int i0 = i - lane, rows = a.n - i0 < 32 ? a.n - i0 : 32;
+                if (j + lane < a.k) {
+                    const long long at = row - static_cast<long long>(lane) * a.k + j + lane;
+#pragma unroll 4
+                    for (int r = 0; r < rows; ++r) {
+                        float x = piece[r * 33 + lane];
+                        const long long p = at + static_cast<long long>(r) * a.k;
+                        if (a.accumulate) x += load_any(a.out, a.out_dtype, p);
+                        store_any(a.out, a.out_dtype, p, x);
+                    }
+                }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
@@ -442,7 +431,9 @@ struct DwPlan {
 
 // Tiles of 128 columns where those of 256 would leave half of the pairs of CTAs
 // idle. Splits: with fewer tiles than pairs, as many as give every pair an item
-// of at least 8 steps (512 tokens).
+// of at least 4 steps (256 tokens), from 12 steps on: below, the second kernel
+// costs more than the steps it saves (528 tokens into 1568 x 32: 10.1 us in two
+// splits, 7.9 in one; 1230 into 587 x 216: 13.0 us in five, 14.0 in two).
 DwPlan dw_plan(long long T, int n, int k, bool d_aligned) {
     DwPlan p;
     p.tiles_n = (n + kTile - 1) / kTile;
@@ -451,7 +442,8 @@ DwPlan dw_plan(long long T, int n, int k, bool d_aligned) {
     p.steps = static_cast<int>((T + kStep - 1) / kStep);
     const long long tiles = static_cast<long long>(p.tiles_n) * p.tiles_k;
     long long s = (kGridCap / 2) / tiles;
-    if (s > p.steps / 8) s = p.steps / 8;
+    if (s > p.steps / 4) s = p.steps / 4;
+    if (p.steps < 12) s = 1;
     if (s < 1) s = 1;
     p.steps_per_split = p.steps ? static_cast<int>((p.steps + s - 1) / s) : 0;
     p.splits = p.steps ? (p.steps + p.steps_per_split - 1) / p.steps_per_split : 0;
