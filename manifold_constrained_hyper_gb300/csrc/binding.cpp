@@ -193,6 +193,13 @@ void check(mhc_status s, const char *where) {
     throw std::runtime_error("");
 }
 
+// n elements of `t` from `at` on, a tensor of its own over the same storage.
+at::Tensor part_of(const at::Tensor &t, int64_t at, int64_t n) {
+    at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+    v.unsafeGetTensorImpl()->set_storage_offset(at);
+    v.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return v;
+}
 PyObject *wrap(const at::Tensor &t) {
     if (t.defined()) return THPVariable_Wrap(t);
     Py_RETURN_NONE;
@@ -281,11 +288,21 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor d_y = whole(tensor(a[11], "d_y", true), "d_y", {s.T, s.H}, t, s.device),
                          d_residual = whole(tensor(a[12], "d_residual", true), "d_residual", {s.T, s.H}, rt, s.device);
         at::Tensor d_w_post, d_w_pre, d_gate, d_scale, workspace = tensor(a[13], "workspace", true);
-        if (w_post.defined()) d_w_post = at::empty({s.H}, f32);
-        if (w_pre.defined()) d_w_pre = at::empty({s.H}, f32);
-        if (gate.defined())
+        // the [H] ones rows of one allocation
+        const bool channel = b.gate_form == MHC_GATE_CHANNEL, per_channel = b.scale_form == MHC_SCALE_CHANNEL;
+        const int rows_of_h = w_post.defined() + w_pre.defined() + channel + per_channel;
+        if (rows_of_h) {
+            const at::Tensor all = at::empty({rows_of_h * s.H}, f32);
+            int64_t at = 0;
+            const auto next = [&] { return part_of(all, s.H * at++, s.H); };
+            if (w_post.defined()) d_w_post = next();
+            if (w_pre.defined()) d_w_pre = next();
+            if (channel) d_gate = next();
+            if (per_channel) d_scale = next();
+        }
+        if (gate.defined() && !channel)
             d_gate = at::empty(gate.sizes(), b.gate_form == MHC_GATE_FULL ? f32.dtype(gate.scalar_type()) : f32);
-        if (res_scale.defined()) d_scale = at::empty(res_scale.sizes(), f32);
+        if (res_scale.defined() && !per_channel) d_scale = at::empty(res_scale.sizes(), f32);
         if (!workspace.defined()) {
             const size_t need = g_lib.backward_bytes(s.T, b.hidden);
             workspace = at::empty({static_cast<int64_t>(need < 16 ? 16 : need)}, f32.dtype(at::kByte));

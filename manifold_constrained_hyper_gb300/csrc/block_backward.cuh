@@ -9,7 +9,8 @@
 // have a row each in flight, 16 columns a thread; the rows to come are staged in
 // shared memory by bulk copies. What every row needs again, both weights, the
 // scale and the sums over tokens (d_w_post, d_w_pre, d_res_scale), lies in
-// tensor memory, 16 columns of six arrays for each thread: in registers they
+// tensor memory, 16 columns of each array for a thread, and so do a full gate's
+// values and slopes between the two passes over a row: in registers they
 // would not leave room for the row, and in shared memory not for the rows to
 // come. The sums leave it once, and a second kernel adds the CTAs' in their order.
 #pragma once
@@ -28,11 +29,11 @@ constexpr int kBwdStages = 32;
 constexpr int kBwdGroups = 15;                      // named barriers 1 .. 15
 constexpr int kBwdThreads = 512;
 constexpr size_t kBwdSmem = 216 * 1024;             // dynamic; the group sums take 6 KB beside it
-constexpr int kBwdArrays = 6;                       // in tensor memory: 16 warps, four to a quadrant of lanes
+constexpr int kBwdArrays = 8;                       // in tensor memory: 16 warps, four to a quadrant of lanes
 constexpr int kBwdTmemCols = 512;
 static_assert(4 * kBwdArrays * kBwdRuns * 8 <= kBwdTmemCols, "four warps' arrays fit a quadrant's columns");
 enum BwdSite : int { SITE_BWD_ROW = 75 };
-enum BwdArray : int { T_W1, T_W2, T_SCALE, T_DW1, T_DW2, T_DSCALE };
+enum BwdArray : int { T_W1, T_W2, T_SCALE, T_DW1, T_DW2, T_DSCALE, T_GATE, T_SLOPE };
 
 struct BwdRing {
     int groups;                                     // of a CTA, blockDim.x / groups threads each
@@ -257,10 +258,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             tmem_run_load(cell(T_DW2, j), sum2);
             Run y = load_y(j), ro = load_r(j);
             if (full_gate) {
-                Run z = load_z(j);
-                run_gate(z, f.gate_act);
+                Run z = load_z(j), slope;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], z.p[i]);
+                for (int i = 0; i < 4; ++i) {
+                    float g0, g1, h0, h1;
+                    gate_both(f2_lo(z.p[i]), f.gate_act, &g0, &h0);
+                    gate_both(f2_hi(z.p[i]), f.gate_act, &g1, &h1);
+                    z.p[i] = f2_pack(g0, g1);
+                    slope.p[i] = f2_pack(h0, h1);
+                    y.p[i] = mul2(y.p[i], z.p[i]);
+                }
+                __syncwarp();
+                tmem_run_store(cell(T_GATE, j), z);
+                tmem_run_store(cell(T_SLOPE, j), slope);
             }
             const Run dh = load_dh(j);
             ev[j] = run_splat(0.f);
@@ -323,18 +333,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
                 tmem_run_wait(sums);
             }
             if (full_gate) {
-                Run z = load_z(j);
+                Run gate, z;                        // z: the slope, then d_gate
+                tmem_run_load(cell(T_GATE, j), gate);
+                tmem_run_load(cell(T_SLOPE, j), z);
+                tmem_run_wait(gate);
+                tmem_run_wait(z);
                 const uint64_t u1 = splat2(rstd1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float g0, g1, h0, h1;
-                    gate_both(f2_lo(z.p[i]), f.gate_act, &g0, &h0);
-                    gate_both(f2_hi(z.p[i]), f.gate_act, &g1, &h1);
-                    const uint64_t g = f2_pack(g0, g1), u = mul2(y.p[i], u1), wu = mul2(w1.p[i], u);
+                    const uint64_t g = gate.p[i], u = mul2(y.p[i], u1), wu = mul2(w1.p[i], u);
                     const uint64_t ro = fma2(g, wu, mul2(SCALED ? sc.p[i] : scale, r.p[i])), D = fma2(q2, ro, ev[j].p[i]);
                     const uint64_t gD = mul2(g, D);
                     sum1.p[i] = fma2(gD, u, sum1.p[i]);
-                    z.p[i] = mul2(f2_pack(h0, h1), mul2(wu, D));                            // d_gate
+                    z.p[i] = mul2(z.p[i], mul2(wu, D));                                     // d_gate
                     y.p[i] = fma2(p2, y.p[i], mul2(u1, mul2(w1.p[i], gD)));                 // d_y
                     ev[j].p[i] = D;
                 }
@@ -494,7 +505,9 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     ring.timeout_ns = wait_timeout_ns();
     if (!out_vec) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (!vec) return bwd_launch<TY, TR, ROWS_SKEW, true, true, true>(a, ring, grid, threads, smem, pdl, s);
-    if (full) return bwd_launch<TY, TR, ROWS_RING, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+    if (full)
+        return scaled || held ? bwd_launch<TY, TR, ROWS_RING, true, true, true>(a, ring, grid, threads, smem, pdl, s)
+                              : bwd_launch<TY, TR, ROWS_RING, true, false, false>(a, ring, grid, threads, smem, pdl, s);
     if (held)
         return scaled ? bwd_launch<TY, TR, ROWS_RING, false, true, true>(a, ring, grid, threads, smem, pdl, s)
                       : bwd_launch<TY, TR, ROWS_RING, false, false, true>(a, ring, grid, threads, smem, pdl, s);

@@ -142,16 +142,20 @@ __device__ __forceinline__ void ckpt_value4(uint32_t w, uint64_t *a, uint64_t *b
         *b = add2((static_cast<uint64_t>(__byte_perm(u, 0x4B000000u, 0x7443)) << 32) | __byte_perm(u, 0x4B000000u, 0x7442), off);
     }
 }
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 // Scale byte of the group of which this lane holds 8 values and its 3
 // neighbours (lanes 4 i .. 4 i + 3) the rest. Whole warps call it.
 template <int FMT>
 __device__ __forceinline__ uint32_t ckpt_byte_quad(const Run &r) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t b = __float_as_uint(run_at(r, e)) & 0x7FFFFFFFu;
-        m = m > b ? m : b;
-    }
+    // three at a time, a NaN winning (its bits are above infinity's)
+    float x = max3_abs(run_at(r, 0), run_at(r, 1), run_at(r, 2));
+    x = max3_abs(x, run_at(r, 3), run_at(r, 4));
+    x = max3_abs(x, run_at(r, 5), run_at(r, 6));
+    uint32_t m = __float_as_uint(max3_abs(x, x, run_at(r, 7)));
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         const uint32_t n = __shfl_xor_sync(0xffffffffu, m, o);

@@ -579,8 +579,8 @@ def mhc_block_norm_backward(d_residual_out, d_h, y, residual, rstd, w_post=None,
     the weights, the gate, the scale and params as in the forward call.
     residual_dtype (d_residual_out's, else the residual's, else d_h's, unless
     given) is needed only where none of them tells it. The gradients of
-    weights, of a [H] or [T, 1] gate and of res_scale are float32; d_residual
-    may be d_residual_out itself."""
+    weights, of a [H] or [T, 1] gate and of res_scale are float32 (those of [H]
+    rows of one allocation); d_residual may be d_residual_out itself."""
     f = (_fast or load_binding()).block_norm_backward
     cy = y if isinstance(y, Checkpoint) else None
     cr = residual if isinstance(residual, Checkpoint) else None
