@@ -33,7 +33,17 @@ constexpr int kBwdArrays = 8;                       // in tensor memory: 16 warp
 constexpr int kBwdTmemCols = 512;
 static_assert(4 * kBwdArrays * kBwdRuns * 8 <= kBwdTmemCols, "four warps' arrays fit a quadrant's columns");
 enum BwdSite : int { SITE_BWD_ROW = 75 };
-enum BwdArray : int { T_W1, T_W2, T_SCALE, T_DW1, T_DW2, T_DSCALE, T_GATE, T_SLOPE };
+enum BwdArray : int { T_W1, T_W2, T_SCALE, T_DW1, T_DW2, T_DSCALE, T_Y, T_R, T_GATE, T_SLOPE };
+
+// The place of an array among a thread's eight. y and the residual go there in
+// the first pass over a row, unpacked, and come back in the second, but where a
+// full gate's two arrays and a channel scale's leave no room for them.
+template <bool FULL, bool SCALED>
+__device__ constexpr int bwd_cell(int array) {
+    if (array == T_GATE) return SCALED ? 6 : 2;
+    if (array == T_SLOPE) return SCALED ? 7 : 5;
+    return array;
+}
 
 struct BwdRing {
     int groups;                                     // of a CTA, blockDim.x / groups threads each
@@ -51,6 +61,7 @@ template <class TY, class TR, int MODE, bool FULL, bool SCALED, bool HELD>
 __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBwdArgs a, const BwdRing ring) {
     constexpr int RUNS = kBwdRuns, MAXW = kBwdThreads / 32;
     constexpr bool STAGED = MODE != ROWS_VEC;
+    constexpr bool KEPT = !(FULL && SCALED);        // y and the residual between the passes
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float red[kBwdGroups][2][3 * MAXW];
     __shared__ __align__(8) uint64_t bars[kBwdStages];
@@ -87,7 +98,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     // this thread's arrays: its warp's quadrant of lanes, the warp's share of the columns
     const uint32_t tmem0 = tmem_slot, cta_warp = threadIdx.x >> 5;
     const uint32_t tmem = tmem0 + ((cta_warp & 3) << 21) + (cta_warp >> 2) * (kBwdArrays * RUNS * 8);
-    auto cell = [&](int array, int j) { return tmem + (array * RUNS + j) * 8; };
+    auto cell = [&](int array, int j) { return tmem + (bwd_cell<FULL, SCALED>(array) * RUNS + j) * 8; };
     griddep_wait();
     // The CTA's rows are blockIdx.x + k gridDim.x, k = 0, 1, ...: group k mod
     // groups takes row k, from stage k mod stages.
@@ -257,6 +268,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             tmem_run_load(cell(T_W2, j), w2);
             tmem_run_load(cell(T_DW2, j), sum2);
             Run y = load_y(j), ro = load_r(j);
+            if (KEPT) {
+                __syncwarp();
+                tmem_run_store(cell(T_Y, j), y);
+                tmem_run_store(cell(T_R, j), ro);
+            }
             if (full_gate) {
                 Run z = load_z(j), slope;
 #pragma unroll
@@ -297,10 +313,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         group_sum<3, MAXW>(sum, red[grp][which], 1 + grp, warp, warps);
         which ^= 1;
         if (STAGED) {
-            // every thread of the group is past its row before: that row's stage is free
+            // every thread of the group is past its first pass, the last to read the row's stage where y and
+            // the residual are kept: the stage is free. Else the stage of its row before is.
             if (warps == 1) __syncwarp();
-            const long long refill = t - row_step + static_cast<long long>(ring.stages) * gridDim.x;
-            if (tid == 0 && last >= 0 && refill < f.T && ok) fetch(refill, last);
+            const long long refill = (KEPT ? t : t - row_step) + static_cast<long long>(ring.stages) * gridDim.x;
+            const int stage = KEPT ? s : last;
+            if (tid == 0 && stage >= 0 && refill < f.T && ok) fetch(refill, stage);
             __syncwarp();
             last = s;
             // the group's next row: `groups` stages on, their number more than that
@@ -324,10 +342,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
                 tmem_run_load(cell(T_SCALE, j), sc);
                 tmem_run_load(cell(T_DSCALE, j), sums);
             }
-            Run y = load_y(j), r = load_r(j);
-            __syncwarp();
+            Run y, r;
+            if (KEPT) {
+                tmem_run_load(cell(T_Y, j), y);
+                tmem_run_load(cell(T_R, j), r);
+            } else {
+                y = load_y(j);
+                r = load_r(j);
+                __syncwarp();
+            }
             tmem_run_wait(w1);
             tmem_run_wait(sum1);
+            if (KEPT) {
+                tmem_run_wait(y);
+                tmem_run_wait(r);
+            }
             if (SCALED) {
                 tmem_run_wait(sc);
                 tmem_run_wait(sums);
