@@ -231,6 +231,8 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F body) {
         PyErr_SetString(PyExc_ValueError, e.what.c_str());
     } catch (const std::exception &e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
     }
     return nullptr;
 }

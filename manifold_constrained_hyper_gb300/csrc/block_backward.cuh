@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float red[kBwdGroups][2][3 * MAXW];
     __shared__ __align__(8) uint64_t bars[kBwdStages];
+    __shared__ volatile int armed[kBwdStages];      // the filling each stage is in
     __shared__ float scale_red[32];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -88,7 +89,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     }
     for (int i = threadIdx.x; i < ring.groups * 2 * 3 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
     if (STAGED && threadIdx.x == 0) {
-        for (int s = 0; s < ring.stages; ++s) mbar_init(bar + 8 * s, 1);
+        for (int s = 0; s < ring.stages; ++s) {
+            mbar_init(bar + 8 * s, 1);
+            armed[s] = -1;
+        }
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         return c;
     };
     constexpr int PARTS = HELD ? 7 : FULL ? 5 : 4;
-    auto fetch = [&](long long t, int s) {          // one thread
+    auto fetch = [&](long long t, int s, int filling) {     // one thread
         const uint32_t b = bar + 8 * s;
         uint32_t dst = smem_addr(smem) + s * ring.stage_bytes, total = 0;
         const uint64_t pol = policy_evict_first();
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
 #pragma unroll
         for (int k = 0; k < PARTS; ++k)
             if (c.bytes[k]) total += skewed_bytes(c.p[k], c.bytes[k]);
-        mbar_arrive_expect_tx(b, total);
+        stage_arm(&armed[s], filling, b, total);
 #pragma unroll
         for (int k = 0; k < PARTS; ++k) {
             if (c.bytes[k]) bulk_load_row(dst, c.p[k], c.bytes[k], b, pol);
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     if (STAGED && threadIdx.x == 0)
         for (int s = 0; s < ring.stages; ++s) {
             const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
-            if (t < f.T) fetch(t, s);
+            if (t < f.T) fetch(t, s, 0);
         }
     __syncwarp();
     // w1 = (w_post + offset) * act of a channel gate, w2 = w_pre + offset, a channel scale; the sums
@@ -190,8 +194,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
 
     // A wait that runs out is recorded, and the rows left go by with what the
     // stages hold: no later wait takes long, and nothing more is fetched.
-    int which = 0, s = grp, last = -1;
-    uint32_t phase = 0;
+    int which = 0, s = grp, filling = 0, last = -1, last_filling = 0;
     bool ok = true;
     Ahead next = ahead(row0);
     for (long long t = row0; t < f.T; t += row_step) {
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
 #pragma unroll
         for (int k = 1; k < PARTS; ++k) st[k] = st[k - 1] + ring.place[k - 1];
         if (STAGED) {
-            ok = mbar_wait(bar + 8 * s, phase, &abort_flag, ring.timeout_ns, ring.status, SITE_BWD_ROW) && ok;
+            ok = stage_wait(&armed[s], filling, bar + 8 * s, &abort_flag, ring.timeout_ns, ring.status, SITE_BWD_ROW) && ok;
             __syncwarp();
         }
 
@@ -318,14 +321,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             if (warps == 1) __syncwarp();
             const long long refill = (KEPT ? t : t - row_step) + static_cast<long long>(ring.stages) * gridDim.x;
             const int stage = KEPT ? s : last;
-            if (tid == 0 && stage >= 0 && refill < f.T && ok) fetch(refill, stage);
+            if (tid == 0 && stage >= 0 && refill < f.T && ok) fetch(refill, stage, 1 + (KEPT ? filling : last_filling));
             __syncwarp();
             last = s;
+            last_filling = filling;
             // the group's next row: `groups` stages on, their number more than that
             s += ring.groups;
             if (s >= ring.stages) {
                 s -= ring.stages;
-                phase ^= 1;
+                ++filling;
             }
         }
         const float q = rstd2 * (rstd2 * (rstd2 * (sum[0] * f.inv_h)));

@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float red[GROUPS][2][MAXW];
     __shared__ __align__(8) uint64_t bars[kFwdStages];
+    __shared__ volatile int armed[kFwdStages];      // the filling each stage is in
     __shared__ int abort_flag;
     const BlockForm &f = a.f;
     Place at;
@@ -66,7 +67,10 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
 
     for (int i = threadIdx.x; i < ring.groups * 2 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
     if (STAGED && threadIdx.x == 0) {
-        for (int s = 0; s < ring.stages; ++s) mbar_init(bar + 8 * s, 1);
+        for (int s = 0; s < ring.stages; ++s) {
+            mbar_init(bar + 8 * s, 1);
+            armed[s] = -1;
+        }
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -74,20 +78,20 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     griddep_wait();
     // The CTA's rows are blockIdx.x + k gridDim.x, k = 0, 1, ...: group k mod
     // groups takes row k, from stage k mod stages.
-    auto fetch = [&](long long t, int s) {          // one thread
+    auto fetch = [&](long long t, int s, int filling) {     // one thread
         const uint32_t b = bar + 8 * s, dst = smem_addr(smem) + stage0 + s * stage_bytes;
         const uint64_t pol = policy_evict_first();
         const TY *const y = static_cast<const TY *>(a.y) + t * a.y_stride;
         const TR *const r = static_cast<const TR *>(a.residual) + t * a.r_stride;
         const uint8_t *const g = static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge;
         if (MODE == ROWS_RING) {
-            mbar_arrive_expect_tx(b, stage_bytes);
+            stage_arm(&armed[s], filling, b, stage_bytes);
             bulk_load(dst, y, y_bytes, b, pol);
             bulk_load(dst + ring.y_place, r, r_bytes, b, pol);
             if (FULL && ring.g_place) bulk_load(dst + ring.y_place + ring.r_place, g, g_bytes, b, pol);
         } else {
-            mbar_arrive_expect_tx(b, skewed_bytes(y, y_bytes) + skewed_bytes(r, r_bytes) +
-                                         (FULL && ring.g_place ? skewed_bytes(g, g_bytes) : 0));
+            stage_arm(&armed[s], filling, b, skewed_bytes(y, y_bytes) + skewed_bytes(r, r_bytes) +
+                                                 (FULL && ring.g_place ? skewed_bytes(g, g_bytes) : 0));
             bulk_load_row(dst, y, y_bytes, b, pol);
             bulk_load_row(dst + ring.y_place, r, r_bytes, b, pol);
             if (FULL && ring.g_place) bulk_load_row(dst + ring.y_place + ring.r_place, g, g_bytes, b, pol);
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     if (STAGED && threadIdx.x == 0)
         for (int s = 0; s < ring.stages; ++s) {
             const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
-            if (t < f.T) fetch(t, s);
+            if (t < f.T) fetch(t, s, 0);
         }
     if (grp == 0) {
 #pragma unroll
@@ -112,8 +116,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
 
     // A wait that runs out is recorded, and the rows left go by with what the
     // stages hold: no later wait takes long, and nothing more is fetched.
-    int which = 0, s = grp;
-    uint32_t phase = 0;
+    int which = 0, s = grp, filling = 0;
     bool ok = true;
     const long long row_step = static_cast<long long>(gridDim.x) * ring.groups;
     for (long long t = blockIdx.x + static_cast<long long>(grp) * gridDim.x; t < f.T; t += row_step) {
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         if (MODE == ROWS_ANY) asm volatile("" : "+r"(at.thread));
         const uint8_t *const st = smem + stage0 + s * stage_bytes;
         if (STAGED)
-            ok = mbar_wait(bar + 8 * s, phase, &abort_flag, ring.timeout_ns, ring.status, SITE_FWD_ROW) && ok;
+            ok = stage_wait(&armed[s], filling, bar + 8 * s, &abort_flag, ring.timeout_ns, ring.status, SITE_FWD_ROW) && ok;
         const TY *const y_row = static_cast<const TY *>(a.y) + t * a.y_stride;
         const TR *const r_row = static_cast<const TR *>(a.residual) + t * a.r_stride;
         const uint8_t *const g_row = static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge;
@@ -199,12 +202,12 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
             // the row is in registers: its stage is free
             if (warps == 1) __syncwarp();
             const long long next = t + static_cast<long long>(ring.stages) * gridDim.x;
-            if (at.thread == 0 && next < f.T && ok) fetch(next, s);
+            if (at.thread == 0 && next < f.T && ok) fetch(next, s, filling + 1);
             // the group's next row: `groups` stages on, their number more than that
             s += ring.groups;
             if (s >= ring.stages) {
                 s -= ring.stages;
-                phase ^= 1;
+                ++filling;
             }
         }
         float tr = rstd1;

@@ -268,6 +268,32 @@ __device__ __forceinline__ void store_ckpt(const Ckpt &c, int format, long long 
     else store_ckpt<MHC_CKPT_INT8, MODE>(c, t, p, j, r);
 }
 
+// Wait for a stage's row. The groups of a CTA share its stages and run at their
+// own pace: one may come to a stage whose row before last has not yet landed, where the parity of
+// its own phase would read as passed. `armed` says which filling the stage is in; a filling
+// begins only when the one before has been read. Bounded, like mbar_wait.
+__device__ __forceinline__ bool stage_wait(volatile int *armed, int filling, uint32_t bar, volatile int *abort_flag,
+                                           uint64_t timeout_ns, unsigned int *status, int site) {
+    if (*armed != filling) {
+        const uint64_t t0 = globaltimer_ns();
+        while (*armed != filling) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > timeout_ns) {
+                record_failure(status, 7, site);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+    return mbar_wait(bar, filling & 1, abort_flag, timeout_ns, status, site);
+}
+// Begin a filling: its bytes announced to the barrier, then the stage marked.
+__device__ __forceinline__ void stage_arm(volatile int *armed, int filling, uint32_t bar, uint32_t bytes) {
+    mbar_arrive_expect_tx(bar, bytes);
+    __threadfence_block();
+    *armed = filling;
+}
+
 // Sums of N values (1 or 3) over a group of up to MAXW whole warps that share
 // the named barrier `bar`, in one fixed order, for every thread of it. Within a
 // warp by shuffles (of three sums two at a time: after the first two steps a

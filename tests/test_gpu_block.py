@@ -152,6 +152,30 @@ def test_more_rows_than_blocks(T):
         check_backward(x, d, form, p, rstd=rstd)
 
 
+@pytest.mark.parametrize("T,H,types,gate,pad", [(3100, 1984, "fp32", "token", 16), (4000, 544, "bf16+", "full", 0),
+                                                 (2500, 1032, "bf16", "channel", 0), (1900, 4096, "fp16", "token", 0),
+                                                 (1100, 7168, "bf16", "full", 0), (1500, 2056, "bf16", "token", 3),
+                                                 (2000, 1031, "fp16+", "full", 0)])
+def test_many_rows_in_flight(T, H, types, gate, pad):
+    """Rows staged ahead, many a block: groups of warps that share the stages go at
+    their own pace, and each must find its own row in its stage every time."""
+    x, d, form = make(T, H, types, gate, "sigmoid", "one", pad)
+    p = params("sigmoid")
+    args = (x["w_post"], x["w_pre"], x["gate"], x["res_scale"], p)
+    _, ro, h, rstd = check_forward(x, form, p)
+    got = check_backward(x, d, form, p, rstd=rstd)
+    cold = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for _ in range(12):
+        cold.zero_()                                # the rows come from memory again, in no order
+        again = ops.mhc_block_norm(x["y"], x["residual"], *args)
+        for a, b in zip((ro, h, rstd), again):
+            assert torch.equal(a, b)
+        cold.zero_()
+        for a, b in zip(got, ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], rstd, *args)):
+            assert torch.equal(a, b)
+    assert ops.mhc_get_device_status() == 0
+
+
 @pytest.mark.parametrize("w_dtype", [FP32, BF, FP16])
 @pytest.mark.parametrize("H", [640, 99])
 def test_weight_types_offsets_and_missing_ones(w_dtype, H):
@@ -298,6 +322,33 @@ def test_captured_in_a_graph(H):
         torch.cuda.synchronize()
         for a, b in zip(got, both()):
             assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the first, a middle and the last rows against the plain form."""
+    T, H = 327_700, 6560
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.empty(T, H, dtype=BF, device="cuda").normal_(generator=g)
+    assert x.numel() > 2 ** 31
+    w = 1 + 0.1 * torch.randn(H, generator=g, device="cuda")
+    ck = ops.ckpt_empty(T, H, "int8")
+    ro, h, rstd = ops.mhc_block_norm(x, x, w, w, ckpt_y=ck)
+    d = ops.mhc_block_norm_backward(x, x, ck, x, rstd, w, w)
+    for at in (0, T // 2, T - 3):
+        rows = x[at:at + 3]
+        f = ref.block(rows, rows, w, w)
+        b = ref.forward_bounds(f, BF, BF)
+        within(ro[at:at + 3], f["ro"], b["residual_out"], "residual_out")
+        within(h[at:at + 3], f["h"], b["h"], "h")
+        codes, scales = ref.pack(rows, "int8")
+        assert torch.equal(ck.codes[at:at + 3], codes) and torch.equal(ck.scales[at:at + 3], scales)
+        f = ref.block(ref.unpack(codes, scales, "int8"), rows, w, w)
+        f["n"] = f["y"] * rstd[at:at + 3, :1].double() * f["w1"]
+        f["ro"] = f["r"] + f["n"]
+        want, size = ref.backward(f, rows, rows, rstd[at:at + 3], "none", "none")
+        b = ref.backward_bounds(want, size, T, H, BF, BF, "none", None)
+        for k in ("d_y", "d_residual"):
+            within(getattr(d, k)[at:at + 3], want[k], b[k], k)
 
 
 def test_gradients_against_differences():
