@@ -13,8 +13,8 @@
 // MMA reads both "transposed" (the M and N axes contiguous). A pair of CTAs
 // (cta_group::2) forms a 256 x 256 tile of d_w: each holds 128 columns of
 // d_out and 128 of x per step of 64 tokens (32 KB, six steps in flight), and
-// its half of the sums in tensor memory, in two buffers, so that the
-// epilogue of one tile runs under the next tile's products. Where there are
+// its half of the sums in tensor memory, in two buffers, so that what one
+// holds is read and stored under the products into the other. Where there are
 // too few tiles for the machine the tokens are split, and a second kernel
 // adds the splits in their order.
 #include <atomic>
@@ -31,9 +31,17 @@ constexpr int kStep = 64;                           // tokens per pipeline stage
 constexpr int kBoxBytes = kStep * 128;              // 64 columns x 64 tokens, 16 bits
 constexpr int kStageBytes = 4 * kBoxBytes;          // two boxes of either operand
 constexpr int kStages = 6;
-constexpr int kThreads = 192;                       // loads, products, four warps of epilogue
+constexpr int kSumWarps = 8;                        // epilogue: two to a quadrant of tensor-memory lanes
+constexpr int kThreads = 64 + 32 * kSumWarps;       // loads, products, epilogue
+// Steps of 64 tokens that tensor memory adds up by itself. The tensor cores cut
+// what an addition shifts out, so a long chain of them drifts (4096 tokens in
+// one: 4.2e-6 of the result, in pieces of 16 steps 9e-7, of 8 steps 4.2e-7); the epilogue
+// adds the pieces in fp32 registers, rounded to nearest, while the next piece's
+// products run into the other buffer. A d_w of 16 bits is rounded by up to 2^-9 or 2^-11
+// of itself at the end, so longer pieces do there.
+constexpr int kChain32 = 8, kChain16 = 64;
 constexpr int kBars = 2 * kStages + 5;
-constexpr int kTurnBytes = 4 * 32 * 33 * 4;         // a 32 x 32 piece of the sums for each epilogue warp
+constexpr int kTurnBytes = kSumWarps * 32 * 33 * 4;         // a 32 x 32 piece of the sums for each epilogue warp
 constexpr int kSmem = kStages * kStageBytes + 1024 /* alignment */ + 256 /* barriers */ + kTurnBytes;
 constexpr int kTmemCols = 512;
 constexpr int kBand = 8;                            // rows of tiles that are walked together
@@ -45,6 +53,7 @@ struct GemmArgs {
     int n, k;
     int tiles_n, tiles_k, splits, steps_per_split, steps;
     int tile_k;                     // columns of a tile: 256, or 128 for few tiles
+    int chain;                      // steps between two additions in registers
     int f16;                        // operands fp16, else bf16
     void *out;                      // d_w, or the splits' fp32 sums [splits][n][k]
     int out_dtype, accumulate, wide;    // wide: rows of out lie on 32-byte boundaries
@@ -95,15 +104,39 @@ __device__ __forceinline__ uint64_t desc_columns(uint32_t addr) {
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
            (static_cast<uint64_t>(2) << 61);
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+// 32, or 16, columns of this warp's 32 lanes, there when it returns.
+__device__ __forceinline__ void tmem_ld32_now(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint64_t *v) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        w[2 * e] = static_cast<uint32_t>(v[e]);
+        w[2 * e + 1] = static_cast<uint32_t>(v[e] >> 32);
+    }
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+        ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+          "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_now(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr) : "memory");
 }
 
@@ -168,7 +201,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full + 8 * b, 1);
-            mbar_init(acc_empty + 8 * b, 8);        // the leader's: four warps of either CTA
+            mbar_init(acc_empty + 8 * b, 2 * kSumWarps);    // the leader's: the epilogue warps of either CTA
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -230,32 +263,35 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                                (static_cast<uint32_t>(a.tile_k >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
         uint32_t it = 0, done = 0;
         bool ok = true;
-        for (int item = pair; item < items && ok; item += pairs, ++done) {
+        for (int item = pair; item < items && ok; item += pairs) {
             int ti, tj, split;
             item_place(a, item, &ti, &tj, &split);
             const int s0 = split * a.steps_per_split;
             const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
-            const uint32_t buf = done & 1, acc = tmem + buf * kTile;
-            if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status,
-                           SITE_DW_ACC_EMPTY)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            for (int st = s0; st < s1; ++st, ++it) {
-                const uint32_t s = it % kStages;
-                if (!mbar_wait(full + 8 * s, (it / kStages) & 1, abort_flag, a.timeout_ns, a.status, SITE_DW_FULL)) {
+            for (int c0 = s0; c0 < s1 && ok; c0 += a.chain, ++done) {
+                const uint32_t buf = done & 1, acc = tmem + buf * kTile;
+                if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status,
+                               SITE_DW_ACC_EMPTY)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t sa = base + s * kStageBytes, sb = sa + 2 * kBoxBytes;
+                const int c1 = c0 + a.chain < s1 ? c0 + a.chain : s1;
+                for (int st = c0; st < c1; ++st, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!mbar_wait(full + 8 * s, (it / kStages) & 1, abort_flag, a.timeout_ns, a.status, SITE_DW_FULL)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = base + s * kStageBytes, sb = sa + 2 * kBoxBytes;
 #pragma unroll
-                for (int q = 0; q < kStep / 16; ++q)
-                    mma_pair(acc, desc_columns(sa + q * 2048), desc_columns(sb + q * 2048), idesc, st > s0 || q > 0);
-                commit_pair(empty + 8 * s);
+                    for (int q = 0; q < kStep / 16; ++q)
+                        mma_pair(acc, desc_columns(sa + q * 2048), desc_columns(sb + q * 2048), idesc, st > c0 || q > 0);
+                    commit_pair(empty + 8 * s);
+                }
+                if (ok) commit_pair(acc_full + 8 * buf);
             }
-            if (ok) commit_pair(acc_full + 8 * buf);
         }
         if (!ok) {
             // the products issued end before tensor memory is freed
@@ -266,30 +302,66 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
     } else if (warp >= 2) {
         // ------------------------------------------------ epilogue, either CTA its 128 rows
         const int quad = warp & 3;                  // the tensor-memory lanes this warp may read
+        const int width = a.tile_k / 2;             // the columns it sums: the tile's first or second half
+        const int first = (warp - 2) / 4 * width;
+        float *const piece = turn + (warp - 2) * 32 * 33;
         uint32_t done = 0;
-        for (int item = pair; item < items; item += pairs, ++done) {
+        bool ok = true;
+        for (int item = pair; item < items && ok; item += pairs) {
             int ti, tj, split;
             item_place(a, item, &ti, &tj, &split);
-            const uint32_t buf = done & 1;
-            const bool ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, a.timeout_ns, a.status,
-                                      SITE_DW_ACC_FULL);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
+            const int s0 = split * a.steps_per_split;
+            const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
+            uint64_t sum[4][16];
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sum[p][e] = 0ull;
+            uint32_t part = 0;
+            for (int c0 = s0; c0 < s1; c0 += a.chain, ++done) {
+                const uint32_t buf = done & 1;
+                const bool last = c0 + a.chain >= s1;
+                ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, a.timeout_ns, a.status, SITE_DW_ACC_FULL);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                part = tmem + buf * kTile + first + (static_cast<uint32_t>(quad * 32) << 16);
+                if (c0 > s0 || !last) {
+                    // one of several pieces; the last one's place takes the sum
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        if (32 * p >= width) break;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t v[16];
+                            tmem_ld16_now(part + 32 * p + 16 * h, v);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                sum[p][8 * h + e] = add2(sum[p][8 * h + e], (static_cast<uint64_t>(v[2 * e + 1]) << 32) | v[2 * e]);
+                            if (last) tmem_st16(part + 32 * p + 16 * h, &sum[p][8 * h]);
+                        }
+                    }
+                    if (last) tmem_st_wait();
+                }
+                if (last) break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at_rank(dw_map_to_rank(acc_empty + 8 * buf, 0));
+            }
+            if (!ok) break;
             const int i = ti * kTile + static_cast<int>(rank) * kHalf + quad * 32 + lane;
             const long long row = (static_cast<long long>(split) * a.n + i) * a.k;
 #pragma unroll 1
-            for (int c = 0; c < a.tile_k; c += 32) {
-                const int j = tj * a.tile_k + c;
+            for (int c = 0; c < width; c += 32) {
+                const int j = tj * a.tile_k + first + c;
                 if (j >= a.k) break;
                 uint32_t v[32];
-                tmem_ld32(tmem + buf * kTile + c + (static_cast<uint32_t>(quad * 32) << 16), v);
-                tmem_ld_wait();
+                tmem_ld32_now(part + c, v);
                 if (a.wide) {
                     if (i < a.n) store_row(a, row, j, v);
                     continue;
                 }
                 // rows on any boundary: the piece turned in shared memory, then a row a store
-                float *const piece = turn + (warp - 2) * 32 * 33;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) piece[lane * 33 + e] = __uint_as_float(v[e]);
                 __syncwarp();
@@ -299,16 +371,17 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
 #pragma unroll 4
                     for (int r = 0; r < rows; ++r) {
                         float x = piece[r * 33 + lane];
-                        const long long p = at + static_cast<long long>(r) * a.k;
-                        if (a.accumulate) x += load_any(a.out, a.out_dtype, p);
-                        store_any(a.out, a.out_dtype, p, x);
+                        const long long q = at + static_cast<long long>(r) * a.k;
+                        if (a.accumulate) x += load_any(a.out, a.out_dtype, q);
+                        store_any(a.out, a.out_dtype, q, x);
                     }
                 }
                 __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at_rank(dw_map_to_rank(acc_empty + 8 * buf, 0));
+            if (lane == 0) arrive_at_rank(dw_map_to_rank(acc_empty + 8 * (done & 1), 0));
+            ++done;
         }
     }
     __syncwarp();
@@ -506,6 +579,7 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     g.out = p.splits > 1 ? static_cast<void *>(parts) : a.d_w;
     g.out_dtype = p.splits > 1 ? MHC_F32 : a.d_w_dtype;
     g.accumulate = p.splits > 1 ? 0 : a.accumulate;
+    g.chain = a.d_w_dtype == MHC_F32 ? kChain32 : kChain16;
     g.wide = a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
     g.status = status;
     g.timeout_ns = wait_timeout_ns();

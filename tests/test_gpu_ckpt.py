@@ -210,6 +210,26 @@ def test_weight_gradient_is_exact_for_small_whole_numbers():
         assert torch.equal(ops.mhc_ckpt_linear_dw(d, c), want)
 
 
+@pytest.mark.parametrize("K", [1288, 1283])
+def test_weight_gradient_of_many_tokens_in_one_sum(K):
+    """Tiles enough that the tokens are not split: sums in several pieces, exact
+    for whole numbers, and for values of one sign off by no more than the cuts of a piece."""
+    T, N = 4209, 2048
+    g = torch.Generator(device="cuda").manual_seed(K)
+    d = torch.randint(-4, 5, (T, N), generator=g, device="cuda").to(BF)
+    c = ops.mhc_ckpt_pack(torch.randint(-15, 16, (T, K), generator=g, device="cuda").float(), "int8")
+    want = d.double().t() @ ops.mhc_ckpt_unpack(c, FP32).double()
+    assert torch.equal(ops.mhc_ckpt_linear_dw(d, c), want.float())
+    assert torch.equal(ops.mhc_ckpt_linear_dw(d, c, d_w=torch.empty(N, K, dtype=BF, device="cuda")), want.to(BF))
+    d = torch.rand(T, N, generator=g, device="cuda").to(BF)
+    c = ops.mhc_ckpt_pack(torch.rand(T, K, generator=g, device="cuda"), "e4m3")
+    want = d.double().t() @ ref.unpack(c.codes, c.scales, "e4m3")
+    # 32 products of 16 tokens to a piece of 512, each of which may cut 2^-23 of
+    # the sum so far twice; then 9 pieces rounded to nearest
+    bound = want * (32 * 2 * 2.0 ** -23 + 9 * 2.0 ** -24)
+    assert ((ops.mhc_ckpt_linear_dw(d, c).double() - want).abs() <= bound).all()
+
+
 def test_weight_gradient_of_no_tokens_and_refusals():
     c = ops.mhc_ckpt_pack(torch.empty(0, 64, dtype=BF, device="cuda"))
     d = torch.empty(0, 48, dtype=BF, device="cuda")
