@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
 
     // A wait that runs out is recorded, and the rows left go by with what the
     // stages hold: no later wait takes long, and nothing more is fetched.
-    int which = 0, s = grp, filling = 0, last = -1, last_filling = 0;
+    int which = 0, s = grp, filling = 0;
     bool ok = true;
     Ahead next = ahead(row0);
     for (long long t = row0; t < f.T; t += row_step) {
@@ -315,23 +315,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         float sum[3] = {f2_lo(s0) + f2_hi(s0), f2_lo(s1) + f2_hi(s1), f2_lo(s2) + f2_hi(s2)};
         group_sum<3, MAXW>(sum, red[grp][which], 1 + grp, warp, warps);
         which ^= 1;
-        if (STAGED) {
-            // every thread of the group is past its first pass, the last to read the row's stage where y and
-            // the residual are kept: the stage is free. Else the stage of its row before is.
+        // The row's stage is free when every thread of the group has read it: past the first pass where y and
+        // the residual are kept, else past the second. Then the group's next row: `groups` stages
+        // on, their number more than that.
+        auto release = [&] {
             if (warps == 1) __syncwarp();
-            const long long refill = (KEPT ? t : t - row_step) + static_cast<long long>(ring.stages) * gridDim.x;
-            const int stage = KEPT ? s : last;
-            if (tid == 0 && stage >= 0 && refill < f.T && ok) fetch(refill, stage, 1 + (KEPT ? filling : last_filling));
+            const long long refill = t + static_cast<long long>(ring.stages) * gridDim.x;
+            if (tid == 0 && refill < f.T && ok) fetch(refill, s, 1 + filling);
             __syncwarp();
-            last = s;
-            last_filling = filling;
-            // the group's next row: `groups` stages on, their number more than that
             s += ring.groups;
             if (s >= ring.stages) {
                 s -= ring.stages;
                 ++filling;
             }
-        }
+        };
+        if (STAGED && KEPT) release();
         const float q = rstd2 * (rstd2 * (rstd2 * (sum[0] * f.inv_h)));
         const float c1 = fmaf(-q, sum[2], sum[1]);
         const float p = f.post_norm ? rstd1 * (rstd1 * (rstd1 * (token * c1 * f.inv_h))) : 0.f;
@@ -412,6 +410,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             if (SCALED) tmem_run_store(cell(T_DSCALE, j), sums);
         }
         tmem_st_wait();
+        if (STAGED && !KEPT) {
+            if (warps > 1) named_barrier_sync(1 + grp, at.threads);
+            release();
+        }
         if (token_gate && a.d_gate && tid == 0) static_cast<float *>(a.d_gate)[t] = token_slope * rstd1 * c1;
     }
     if (STAGED && !ok && tid == 0) {
@@ -422,33 +424,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             mbar_wait(bar + 8 * (k >> 1), k & 1, &gave_up, ring.timeout_ns, ring.status, SITE_BWD_ROW);
     }
 
-    // the groups' sums, one group after the other (in the place of the stages), then out
+    // The groups' sums, through the place of the stages, each column's then in the groups'
+    // order; an array's halves go round the groups. One group's straight out.
     __syncthreads();
     float *const out = a.sums + static_cast<long long>(blockIdx.x) * kBackSums * H;
-    float *const kept = reinterpret_cast<float *>(smem);
-    auto leave = [&](int array, float *to) {
-        for (int g = 0; g < ring.groups; ++g) {
-            if (g == grp)
+    const int arrays = scaled ? 3 : 2, column = at.threads * RUNS * 8;
 #pragma unroll
-                for (int j = 0; j < RUNS; ++j) {
-                    Run acc;
-                    __syncwarp();
-                    tmem_run_load(cell(array, j), acc);
-                    tmem_run_wait(acc);
-                    if (g > 0) {
-                        const Run before = kept_run(kept, at, j);
+    for (int k = 0; k < (SCALED ? 3 : 2); ++k) {
+        if (k >= arrays) break;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc.p[i] = add2(before.p[i], acc.p[i]);
-                    }
-                    if (g < ring.groups - 1) keep_run(kept, at, j, acc);
-                    else store_run<MODE>(to, at, j, acc);
-                }
-            __syncthreads();
+        for (int j = 0; j < RUNS; ++j) {
+            Run acc;
+            __syncwarp();
+            tmem_run_load(cell(T_DW1 + k, j), acc);
+            tmem_run_wait(acc);
+            if (ring.groups == 1) store_run<MODE>(out + static_cast<long long>(k) * H, at, j, acc);
+            else keep_run(reinterpret_cast<float *>(smem) + (k * ring.groups + grp) * column, at, j, acc);
         }
-    };
-    leave(T_DW1, out);
-    leave(T_DW2, out + H);
-    if (scaled) leave(T_DSCALE, out + 2 * static_cast<long long>(H));
+    }
+    if (ring.groups > 1) {
+        __syncthreads();
+        for (int i = grp; i < arrays * RUNS; i += ring.groups) {
+            const int k = i / RUNS, j = i - k * RUNS;
+            const float *const kept = reinterpret_cast<const float *>(smem) + k * ring.groups * column;
+            Run acc = kept_run(kept, at, j);
+            for (int g = 1; g < ring.groups; ++g) {
+                const Run more = kept_run(kept + g * column, at, j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc.p[e] = add2(acc.p[e], more.p[e]);
+            }
+            store_run<MODE>(out + static_cast<long long>(k) * H, at, j, acc);
+        }
+    }
     float total[1] = {f2_lo(scale2) + f2_hi(scale2)};
     if (SCALED && f.scale_form == MHC_SCALE_ONE) {
         // a single scale in the general form: its columns' sums
@@ -508,9 +515,10 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     const long long rows = (f.T + sms - 1) / sms;
     if (groups > kBwdGroups) groups = kBwdGroups;
     ring.groups = static_cast<int>(rows < groups ? rows : groups);
+    // where the groups' sums meet at the end
+    auto sums = [&] { return ring.groups == 1 ? 0 : static_cast<size_t>(3) * ring.groups * threads * kBwdRuns * 32; };
     const unsigned grid = static_cast<unsigned>(f.T < sms ? f.T : sms);
     *parts = static_cast<int>(grid);
-    const size_t column = static_cast<size_t>(threads) * kBwdRuns * 32;     // the groups' sums at the end
     const int scale_bytes = static_cast<int>(ckpt_groups(H));
     ring.place[0] = row_place(H, a.y ? sizeof(TY) : 1, !vec || !a.y);
     ring.place[1] = row_place(H, a.residual ? sizeof(TR) : 1, !vec || !a.residual);
@@ -526,13 +534,13 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     // two stages at least, or all of the rows; else (the widest types above 5000 columns and more) from memory
     if (stages < 2 && stages < rows) {
         if (!vec) return launch_block_bwd_loop(a, dtype, r_dtype, pdl, parts, s);
-        return bwd_launch<TY, TR, ROWS_VEC, true, true, true>(a, ring, grid, threads, column, pdl, s);
+        return bwd_launch<TY, TR, ROWS_VEC, true, true, true>(a, ring, grid, threads, sums(), pdl, s);
     }
     // a stage for each group and one to fill meanwhile, or all of the rows
     if (ring.groups >= stages) ring.groups = static_cast<int>(stages == rows ? stages : stages - 1);
     ring.stages = static_cast<int>(stages);
     size_t smem = static_cast<size_t>(ring.stage_bytes) * ring.stages;
-    if (smem < column) smem = column;
+    if (smem < sums()) smem = sums();
     int n = 0;
     if (require_device(&n, &ring.status)) return cudaErrorUnknown;
     ring.timeout_ns = wait_timeout_ns();
