@@ -395,9 +395,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
                 }
             }
             store_run<MODE>(static_cast<TY *>(a.d_y) + t * H, at, j, y);
-            if (!SCALED && run_col<MODE>(at, j) < H) {          // (single elements are SCALED)
+            if (!SCALED && run_col<MODE>(at, j) < H) {
+                const Run d = MODE == ROWS_ANY ? run_within<MODE>(ev[j], at, j) : ev[j];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) scale2 = fma2(r.p[i], ev[j].p[i], scale2);
+                for (int i = 0; i < 4; ++i) scale2 = fma2(r.p[i], d.p[i], scale2);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -544,7 +545,11 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     int n = 0;
     if (require_device(&n, &ring.status)) return cudaErrorUnknown;
     ring.timeout_ns = wait_timeout_ns();
-    if (!out_vec) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+    if (!out_vec) {
+        if (held || (full && scaled)) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+        return full ? bwd_launch<TY, TR, ROWS_ANY, true, false, false>(a, ring, grid, threads, smem, pdl, s)
+                    : bwd_launch<TY, TR, ROWS_ANY, false, true, false>(a, ring, grid, threads, smem, pdl, s);
+    }
     if (!vec) return bwd_launch<TY, TR, ROWS_SKEW, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (full)
         return scaled || held ? bwd_launch<TY, TR, ROWS_RING, true, true, true>(a, ring, grid, threads, smem, pdl, s)
