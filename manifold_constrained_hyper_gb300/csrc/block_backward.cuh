@@ -545,12 +545,16 @@ cudaError_t block_bwd(const BlockBwdArgs &a, int dtype, int r_dtype, int sms, bo
     int n = 0;
     if (require_device(&n, &ring.status)) return cudaErrorUnknown;
     ring.timeout_ns = wait_timeout_ns();
-    if (!out_vec) {
-        if (held || (full && scaled)) return bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, smem, pdl, s);
-        return full ? bwd_launch<TY, TR, ROWS_ANY, true, false, false>(a, ring, grid, threads, smem, pdl, s)
-                    : bwd_launch<TY, TR, ROWS_ANY, false, true, false>(a, ring, grid, threads, smem, pdl, s);
+    if (!vec) {
+        if (held || (full && scaled))
+            return out_vec ? bwd_launch<TY, TR, ROWS_SKEW, true, true, true>(a, ring, grid, threads, smem, pdl, s)
+                           : bwd_launch<TY, TR, ROWS_ANY, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+        if (full)
+            return out_vec ? bwd_launch<TY, TR, ROWS_SKEW, true, false, false>(a, ring, grid, threads, smem, pdl, s)
+                           : bwd_launch<TY, TR, ROWS_ANY, true, false, false>(a, ring, grid, threads, smem, pdl, s);
+        return out_vec ? bwd_launch<TY, TR, ROWS_SKEW, false, true, false>(a, ring, grid, threads, smem, pdl, s)
+                       : bwd_launch<TY, TR, ROWS_ANY, false, true, false>(a, ring, grid, threads, smem, pdl, s);
     }
-    if (!vec) return bwd_launch<TY, TR, ROWS_SKEW, true, true, true>(a, ring, grid, threads, smem, pdl, s);
     if (full)
         return scaled || held ? bwd_launch<TY, TR, ROWS_RING, true, true, true>(a, ring, grid, threads, smem, pdl, s)
                               : bwd_launch<TY, TR, ROWS_RING, true, false, false>(a, ring, grid, threads, smem, pdl, s);

@@ -318,8 +318,12 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
     int n = 0;
     if (require_device(&n, &ring.status)) return cudaErrorUnknown;
     ring.timeout_ns = wait_timeout_ns();
-    if (!out_vec) return fwd_launch<TY, TR, ROWS_ANY, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s);
-    if (!vec) return fwd_launch<TY, TR, ROWS_SKEW, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+    if (!out_vec)
+        return ckpt ? fwd_launch<TY, TR, ROWS_ANY, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s)
+                    : fwd_launch<TY, TR, ROWS_ANY, 2, true, true, false>(a, ring, grid, threads, smem, pdl, s);
+    if (!vec)
+        return ckpt ? fwd_launch<TY, TR, ROWS_SKEW, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s)
+                    : fwd_launch<TY, TR, ROWS_SKEW, 2, true, true, false>(a, ring, grid, threads, smem, pdl, s);
     if (full)
         return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, true, true, true>(a, ring, grid, threads, smem, pdl, s)
                     : fwd_launch<TY, TR, ROWS_RING, 4, true, true, false>(a, ring, grid, threads, smem, pdl, s);
