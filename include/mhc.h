@@ -277,9 +277,11 @@ mhc_status mhc_boundary_fused_noalloc(const uint16_t *x, const uint16_t *residua
  *
  * Unlike the boundary's, these entry points take any hidden in [1, 65536],
  * and rows that lie `stride` elements apart (>= 0; the elements of a row are
- * contiguous); a pointer needs its element type's alignment only. Rows on
- * 16-byte boundaries (pointer and stride) and hidden a multiple of 8 take
- * the vector loads.
+ * contiguous); a pointer needs its element type's alignment only. Fastest are
+ * rows on boundaries of 8 elements (pointers and strides, hidden a multiple of
+ * 8). Rows off 16-byte boundaries are read in whole blocks of 16 bytes: up to
+ * 15 bytes before and after a row are read too (and left alone), which any
+ * device allocation that begins and ends on such a boundary holds.
  */
 typedef enum {
     MHC_GATE_NONE = 0,      /* act(gate) = 1 */

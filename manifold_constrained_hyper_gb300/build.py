@@ -51,7 +51,7 @@ def _build_binding():
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *(a for i in include for a in ("-isystem", i)), "-I", INCLUDE,
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-lc10",
-           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"the binding failed to build:\n{r.stdout}\n{r.stderr}")

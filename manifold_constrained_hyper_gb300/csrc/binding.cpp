@@ -6,7 +6,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -68,10 +68,15 @@ int64_t rows(const at::Tensor &t, const char *name, const Shape &s, at::ScalarTy
                       s.device.str() + " with contiguous rows: got " + str(t)};
     return t.stride(0);
 }
+// A new tensor, without the dispatcher's part of a torch.empty: allocations are half of a
+// small call's time (three of them and the call 6.3 us, so 5.4).
+at::Tensor fresh(c10::IntArrayRef size, at::ScalarType type, c10::Device device) {
+    return at::Tensor(at::detail::empty_cuda(size, type, device, std::nullopt));
+}
 // `given`, or a new tensor.
 at::Tensor whole(const at::Tensor &given, const char *name, c10::IntArrayRef size, at::ScalarType type,
                  c10::Device device) {
-    if (!given.defined()) return at::empty(size, at::TensorOptions(device).dtype(type));
+    if (!given.defined()) return fresh(size, type, device);
     if (given.sizes() != size || given.scalar_type() != type || given.device() != device || !given.is_contiguous())
         throw Refused{std::string(name) + " must be a contiguous " + str(size) + " " + c10::toString(type) + " tensor on " +
                       device.str() + ": got " + str(given)};
@@ -193,12 +198,19 @@ void check(mhc_status s, const char *where) {
     throw std::runtime_error("");
 }
 
-// n elements of `t` from `at` on, a tensor of its own over the same storage.
-at::Tensor part_of(const at::Tensor &t, int64_t at, int64_t n) {
+// Elements of `t` from `at` on, a tensor of its own over the same storage.
+at::Tensor part_of(const at::Tensor &t, int64_t at, c10::IntArrayRef size) {
     at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
     v.unsafeGetTensorImpl()->set_storage_offset(at);
-    v.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    v.unsafeGetTensorImpl()->set_sizes_contiguous(size);
     return v;
+}
+// A checkpoint's two tensors, of one allocation.
+void empty_ckpt(const Shape &s, at::Tensor *codes, at::Tensor *scales) {
+    const int64_t groups = (s.H + 31) / 32, first = (s.T * s.H + 15) / 16 * 16;
+    const at::Tensor all = fresh({first + s.T * groups}, at::kByte, s.device);
+    *codes = part_of(all, 0, {s.T, s.H});
+    *scales = part_of(all, first, {s.T, groups});
 }
 PyObject *wrap(const at::Tensor &t) {
     if (t.defined()) return THPVariable_Wrap(t);
@@ -286,28 +298,38 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Held cy = held(a[15], a[16], "y", s), cr = held(a[17], a[18], "residual", s);
         whole(rstd, "rstd", {s.T, 2}, at::kFloat, s.device);
         const c10::cuda::CUDAGuard guard(s.device);
-        const at::TensorOptions f32 = at::TensorOptions(s.device).dtype(at::kFloat);
         const at::Tensor d_y = whole(tensor(a[11], "d_y", true), "d_y", {s.T, s.H}, t, s.device),
                          d_residual = whole(tensor(a[12], "d_residual", true), "d_residual", {s.T, s.H}, rt, s.device);
         at::Tensor d_w_post, d_w_pre, d_gate, d_scale, workspace = tensor(a[13], "workspace", true);
-        // the [H] ones rows of one allocation
-        const bool channel = b.gate_form == MHC_GATE_CHANNEL, per_channel = b.scale_form == MHC_SCALE_CHANNEL;
-        const int rows_of_h = w_post.defined() + w_pre.defined() + channel + per_channel;
-        if (rows_of_h) {
-            const at::Tensor all = at::empty({rows_of_h * s.H}, f32);
-            int64_t at = 0;
-            const auto next = [&] { return part_of(all, s.H * at++, s.H); };
-            if (w_post.defined()) d_w_post = next();
-            if (w_pre.defined()) d_w_pre = next();
-            if (channel) d_gate = next();
-            if (per_channel) d_scale = next();
+        // the fp32 ones, parts of one allocation
+        const bool full = b.gate_form == MHC_GATE_FULL;
+        struct Part {
+            at::Tensor *to;
+            c10::IntArrayRef size;
+        };
+        const Part parts[] = {{w_post.defined() ? &d_w_post : nullptr, w_post.defined() ? w_post.sizes() : c10::IntArrayRef()},
+                              {w_pre.defined() ? &d_w_pre : nullptr, w_pre.defined() ? w_pre.sizes() : c10::IntArrayRef()},
+                              {gate.defined() && !full ? &d_gate : nullptr, gate.defined() ? gate.sizes() : c10::IntArrayRef()},
+                              {res_scale.defined() ? &d_scale : nullptr, res_scale.defined() ? res_scale.sizes() : c10::IntArrayRef()}};
+        int64_t count = 0;
+        bool any = false;
+        for (const Part &p : parts) {
+            any = any || p.to;
+            if (p.to) count += c10::multiply_integers(p.size);
         }
-        if (gate.defined() && !channel)
-            d_gate = at::empty(gate.sizes(), b.gate_form == MHC_GATE_FULL ? f32.dtype(gate.scalar_type()) : f32);
-        if (res_scale.defined() && !per_channel) d_scale = at::empty(res_scale.sizes(), f32);
+        if (any) {
+            const at::Tensor all = fresh({count}, at::kFloat, s.device);
+            int64_t at = 0;
+            for (const Part &p : parts) {
+                if (!p.to) continue;
+                *p.to = part_of(all, at, p.size);
+                at += c10::multiply_integers(p.size);
+            }
+        }
+        if (full) d_gate = fresh(gate.sizes(), gate.scalar_type(), s.device);
         if (!workspace.defined()) {
             const size_t need = g_lib.backward_bytes(s.T, b.hidden);
-            workspace = at::empty({static_cast<int64_t>(need < 16 ? 16 : need)}, f32.dtype(at::kByte));
+            workspace = fresh({static_cast<int64_t>(need < 16 ? 16 : need)}, at::kByte, s.device);
         }
         check(g_lib.backward(&b, ptr(d_ro), drs, d_h.data_ptr(), dhs, ptr(y), ys, ptr(residual), rs,
                              static_cast<mhc_ckpt_format>(format), cy.get(), cr.get(),
@@ -317,6 +339,20 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                              stream_on(s.device)),
               "mhc_block_norm_backward");
         return tuple({d_y, d_residual, d_w_post, d_w_pre, d_gate, d_scale});
+    });
+}
+
+// tokens, hidden, the device's number (-1: the current one) -> codes, scales
+PyObject *ckpt_empty(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject * {
+        const int64_t T = PyLong_AsLongLong(a[0]), H = PyLong_AsLongLong(a[1]);
+        const long device = PyLong_AsLong(a[2]);
+        if (PyErr_Occurred()) throw std::runtime_error("");
+        if (T < 0 || H < 0) throw Refused{"a checkpoint's sizes must not be negative: got " + str({T, H})};
+        at::Tensor codes, scales;
+        empty_ckpt({T, H, c10::Device(c10::kCUDA, device < 0 ? c10::cuda::current_device() : static_cast<int8_t>(device))},
+                   &codes, &scales);
+        return tuple({codes, scales});
     });
 }
 
@@ -332,9 +368,7 @@ PyObject *ckpt_pack(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const c10::cuda::CUDAGuard guard(s.device);
         Held out = held(a[2], a[3], "out", s);
         if (!out.codes.defined()) {
-            const at::TensorOptions u8 = at::TensorOptions(s.device).dtype(at::kByte);
-            out.codes = at::empty({s.T, s.H}, u8);
-            out.scales = at::empty({s.T, (s.H + 31) / 32}, u8);
+            empty_ckpt(s, &out.codes, &out.scales);
             out.c = {static_cast<uint8_t *>(out.codes.data_ptr()), static_cast<uint8_t *>(out.scales.data_ptr())};
         }
         check(g_lib.pack(x.data_ptr(), stride, static_cast<mhc_dtype>(t), s.T,
@@ -385,7 +419,7 @@ PyObject *ckpt_linear_dw(PyObject *, PyObject *const *a, Py_ssize_t n) {
             const bool aligned = reinterpret_cast<uintptr_t>(d_out.data_ptr()) % 16 == 0 &&
                                  (s.T == 1 || (stride % 8 == 0 && stride >= s.H && stride < (int64_t(1) << 38)));
             const size_t need = g_lib.dw_bytes(s.T, N, k, aligned);
-            if (need) workspace = at::empty({static_cast<int64_t>(need)}, at::TensorOptions(s.device).dtype(at::kByte));
+            if (need) workspace = fresh({static_cast<int64_t>(need)}, at::kByte, s.device);
         }
         check(g_lib.dw(d_out.data_ptr(), stride, static_cast<mhc_dtype>(dtype_of(t)), &x.c,
                        static_cast<mhc_ckpt_format>(format), s.T, N, k, d_w.data_ptr(), static_cast<mhc_dtype>(type),
@@ -417,7 +451,7 @@ PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 #define MHC_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MHC_METHOD(init),          MHC_METHOD(block_norm),  MHC_METHOD(block_norm_backward),
-                           MHC_METHOD(ckpt_pack),     MHC_METHOD(ckpt_unpack), MHC_METHOD(ckpt_linear_dw),
+                           MHC_METHOD(ckpt_empty),    MHC_METHOD(ckpt_pack),     MHC_METHOD(ckpt_unpack), MHC_METHOD(ckpt_linear_dw),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

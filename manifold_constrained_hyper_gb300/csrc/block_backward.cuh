@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         auto row_run = [&](int k, const auto *row, int j) {
             using T = typename std::remove_cv<typename std::remove_reference<decltype(*row)>::type>::type;
             if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const T *>(st[k]), at, j);
-            else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(row, at, j);
+            else if constexpr (MODE == ROWS_VEC) return load_run(row, at, j);
             else if constexpr (MODE == ROWS_SKEW) return staged_skewed<T>(st[k], skew16(row), at, j);
             else return staged_single(reinterpret_cast<const T *>(st[k] + skew16(row)), at, j);
         };

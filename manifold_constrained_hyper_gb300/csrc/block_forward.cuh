@@ -131,21 +131,21 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         const uint8_t *const g_row = static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge;
         auto load_y = [&](int j) {
             if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st), at, j);
-            else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(y_row, at, j);
+            else if constexpr (MODE == ROWS_VEC) return load_run(y_row, at, j);
             else if constexpr (MODE == ROWS_SKEW) return staged_skewed<TY>(st, skew16(y_row), at, j);
             else return staged_single(reinterpret_cast<const TY *>(st + skew16(y_row)), at, j);
         };
         auto load_r = [&](int j) {
             const uint8_t *const row = st + ring.y_place;
             if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(row), at, j);
-            else if constexpr (MODE == ROWS_VEC) return load_run<MODE>(r_row, at, j);
+            else if constexpr (MODE == ROWS_VEC) return load_run(r_row, at, j);
             else if constexpr (MODE == ROWS_SKEW) return staged_skewed<TR>(row, skew16(r_row), at, j);
             else return staged_single(reinterpret_cast<const TR *>(row + skew16(r_row)), at, j);
         };
         auto load_z = [&](int j) {
             const uint8_t *const row = st + ring.y_place + ring.r_place;
             if constexpr (MODE == ROWS_RING) return staged_run_any(row, f.gate_dtype, at, j);
-            else if constexpr (MODE == ROWS_VEC) return load_run_any<MODE>(g_row, f.gate_dtype, at, j);
+            else if constexpr (MODE == ROWS_VEC) return load_run_any(g_row, f.gate_dtype, at, j);
             else if constexpr (MODE == ROWS_SKEW)
                 return f.gate_dtype == MHC_F32 ? staged_skewed<float>(row, skew16(g_row), at, j)
                                                : staged_skewed<TY>(row, skew16(g_row), at, j);

@@ -1,5 +1,6 @@
 // The gated residual block and its backward pass for rows too wide for
-// registers (above 16384 and 8192 columns): one CTA per row, a warp per group
+// registers (above 8192 columns; backward also the widest rows on any boundary of which
+// two do not fit shared memory): one CTA per row, a warp per group
 // of 32 columns, each pass over the row reading it again (from L1 or L2 after
 // the first). Any stride and alignment.
 #include "block_common.cuh"

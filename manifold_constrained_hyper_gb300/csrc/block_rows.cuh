@@ -34,34 +34,26 @@ __device__ __forceinline__ int run_read_col(const Place &p, int j) {
     const int c = run_col<ROWS_VEC>(p, j);
     return c < p.H ? c : p.H - 8;
 }
-// Run j of a row in global memory; past the row's end 0 with single loads,
-// the row's last run with vector loads.
-template <int MODE, class T>
+// Run j of a row in global memory, and of a type known at run time.
+template <class T>
 __device__ __forceinline__ Run load_run(const T *row, const Place &p, int j) {
-    if constexpr (MODE != ROWS_ANY) return load8(row + run_read_col(p, j));
-    const int c = run_col<MODE>(p, j);
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e * p.threads < p.H ? to_f32(row[c + e * p.threads]) : 0.f;
-    return run_of(v);
+    return load8(row + run_read_col(p, j));
+}
+__device__ __forceinline__ Run load_run_any(const void *row, int dtype, const Place &p, int j) {
+    if (dtype == MHC_F32) return load_run(static_cast<const float *>(row), p, j);
+    if (dtype == MHC_BF16) return load_run(static_cast<const __nv_bfloat16 *>(row), p, j);
+    return load_run(static_cast<const __half *>(row), p, j);
 }
 template <int MODE, class T>
 __device__ __forceinline__ void store_run(T *row, const Place &p, int j, const Run &r) {
     const int c = run_col<MODE>(p, j);
     if constexpr (MODE != ROWS_ANY) {
         if (c < p.H) store8(row + c, r);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (c + e * p.threads < p.H) row[c + e * p.threads] = from_f32<T>(run_at(r, e));
-}
-// Of a type known at run time: a weight, a scale, a gate.
-template <int MODE>
-__device__ __forceinline__ Run load_run_any(const void *row, int dtype, const Place &p, int j) {
-    if (dtype == MHC_F32) return load_run<MODE>(static_cast<const float *>(row), p, j);
-    if (dtype == MHC_BF16) return load_run<MODE>(static_cast<const __nv_bfloat16 *>(row), p, j);
-    return load_run<MODE>(static_cast<const __half *>(row), p, j);
+        for (int e = 0; e < 8; ++e)
+            if (c + e * p.threads < p.H) row[c + e * p.threads] = from_f32<T>(run_at(r, e));
+    }
 }
 // Run j of a row staged in shared memory.
 template <class T>
@@ -86,11 +78,14 @@ __device__ __forceinline__ Run staged_single(const T *row, const Place &p, int j
 template <int MODE>
 __device__ __forceinline__ Run run_within(const Run &r, const Place &p, int j) {
     const int c = run_col<MODE>(p, j);
-    if (MODE != ROWS_ANY) return c < p.H ? r : run_splat(0.f);
-    float v[8];
+    if constexpr (MODE != ROWS_ANY) {
+        return c < p.H ? r : run_splat(0.f);
+    } else {
+        float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e * p.threads < p.H ? run_at(r, e) : 0.f;
-    return run_of(v);
+        for (int e = 0; e < 8; ++e) v[e] = c + e * p.threads < p.H ? run_at(r, e) : 0.f;
+        return run_of(v);
+    }
 }
 // Bulk copies start and end on 16-byte boundaries: a row that does not is
 // copied with what shares its first and last 16 bytes (within the allocation,
@@ -195,12 +190,13 @@ __device__ __forceinline__ Run param_run(const RawParam &r, int dtype) {
         const uint4 w = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
         return dtype == MHC_BF16 ? unpack8(w, static_cast<const __nv_bfloat16 *>(nullptr))
                                  : unpack8(w, static_cast<const __half *>(nullptr));
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] = dtype == MHC_BF16 ? __uint_as_float(r.w[e] << 16)
-                                 : __half2float(__ushort_as_half(static_cast<unsigned short>(r.w[e])));
-    return run_of(v);
+        for (int e = 0; e < 8; ++e)
+            v[e] = dtype == MHC_BF16 ? __uint_as_float(r.w[e] << 16)
+                                     : __half2float(__ushort_as_half(static_cast<unsigned short>(r.w[e])));
+        return run_of(v);
+    }
 }
 // What every row of a block needs of run j: w1 = (w_post + offset) * act of a
 // channel gate, w2 = w_pre + offset, the residual's scale (1 where there is

@@ -519,9 +519,10 @@ def _format_number(fmt):
 def ckpt_empty(tokens: int, hidden: int, fmt: str = "e4m3", device="cuda") -> Checkpoint:
     """A checkpoint to be written."""
     _format_number(fmt)
-    return _held(torch.empty((tokens, hidden), dtype=torch.uint8, device=device),
-                 torch.empty((tokens, -(-hidden // CKPT_GROUP)), dtype=torch.uint8, device=device),
-                 fmt)
+    d = device if isinstance(device, torch.device) else torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"a checkpoint lies on a CUDA device: got {d}")
+    return _held(*(_fast or load_binding()).ckpt_empty(tokens, hidden, -1 if d.index is None else d.index), fmt)
 
 
 def _format(*cks):
@@ -579,16 +580,20 @@ def mhc_block_norm_backward(d_residual_out, d_h, y, residual, rstd, w_post=None,
     the weights, the gate, the scale and params as in the forward call.
     residual_dtype (d_residual_out's, else the residual's, else d_h's, unless
     given) is needed only where none of them tells it. The gradients of
-    weights, of a [H] or [T, 1] gate and of res_scale are float32 (those of [H]
-    rows of one allocation); d_residual may be d_residual_out itself."""
+    weights, of a [H] or [T, 1] gate and of res_scale are float32 (parts of
+    one allocation); d_residual may be d_residual_out itself."""
     f = (_fast or load_binding()).block_norm_backward
+    p = _DEFAULT_BLOCK_PARAMS if params is None else params
+    typed = None if residual_dtype is None else torch.empty(0, dtype=residual_dtype)
     cy = y if isinstance(y, Checkpoint) else None
     cr = residual if isinstance(residual, Checkpoint) else None
-    typed = None if residual_dtype is None else torch.empty(0, dtype=residual_dtype)
-    return BlockGrads(*_at(
+    if cy is None and cr is None:
+        return BlockGrads._make(_at(stream, f, d_residual_out, d_h, y, residual, rstd, w_post, w_pre, gate,
+                                    res_scale, p, typed, d_y, d_residual, workspace, 0, None, None, None, None))
+    return BlockGrads._make(_at(
         stream, f, d_residual_out, d_h, y if cy is None else None, residual if cr is None else None,
-        rstd, w_post, w_pre, gate, res_scale, _DEFAULT_BLOCK_PARAMS if params is None else params,
-        typed, d_y, d_residual, workspace, _format(cy, cr), *_parts(cy), *_parts(cr)))
+        rstd, w_post, w_pre, gate, res_scale, p, typed, d_y, d_residual, workspace, _format(cy, cr),
+        *_parts(cy), *_parts(cr)))
 
 
 def mhc_ckpt_pack(x, fmt: str = "e4m3", *, out: Checkpoint | None = None, stream=None) -> Checkpoint:

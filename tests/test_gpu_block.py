@@ -260,6 +260,9 @@ def test_no_tokens():
                                     e["w_pre"], e["gate"], e["res_scale"])
     for k in ("d_w_post", "d_w_pre", "d_gate", "d_res_scale"):
         assert (getattr(g, k) == 0).all(), k
+    z = torch.empty(0, 1, device="cuda")
+    g = ops.mhc_block_norm_backward(d["d_ro"][:0], d["d_h"][:0], e["y"], e["residual"], rstd, gate=z)
+    assert g.d_gate.shape == (0, 1) and g.d_w_post is None and g.d_res_scale is None
 
 
 def test_in_place():
