@@ -409,19 +409,6 @@ __global__ void __launch_bounds__(256) dw_join_kernel(const float *parts, int sp
 // and, where its rows do not allow 16-byte loads, d_out; each in rows on 16-byte
 // boundaries. Eight columns a lane, kRuns of them in flight; past a row's
 // end stands 0 (the copies above cut rows at their length).
-// Bytes [addr, addr + 8 N) of a row that ends at `end`, from the aligned 8-byte words
-// that hold them (a word that holds none of the row is not read).
-template <int N>
-__device__ __forceinline__ void load_words(uintptr_t addr, uintptr_t end, uint64_t (&out)[N]) {
-    const uintptr_t first = addr & ~static_cast<uintptr_t>(7);
-    const uint32_t bits = static_cast<uint32_t>(addr - first) * 8;
-    uint64_t w[N + 1];
-#pragma unroll
-    for (int i = 0; i <= N; ++i)
-        w[i] = first + 8 * i < end ? *reinterpret_cast<const uint64_t *>(first + 8 * i) : 0ull;
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = bits ? (w[i] >> bits) | (w[i + 1] << (64 - bits)) : w[i];
-}
 struct PrepareArgs {
     Ckpt x;
     long long T;

@@ -101,6 +101,73 @@ __device__ __forceinline__ Run load8_skewed(const uint4 *p, uint32_t skew, const
     }
     return r;
 }
+// Bytes [addr, addr + 8 N) of a row that ends at `end`, from the aligned 8-byte words
+// that hold them (a word that holds none of the row is not read).
+template <int N>
+__device__ __forceinline__ void load_words(uintptr_t addr, uintptr_t end, uint64_t (&out)[N]) {
+    const uintptr_t first = addr & ~static_cast<uintptr_t>(7);
+    const uint32_t bits = static_cast<uint32_t>(addr - first) * 8;
+    uint64_t w[N + 1];
+#pragma unroll
+    for (int i = 0; i <= N; ++i)
+        w[i] = first + 8 * i < end ? *reinterpret_cast<const uint64_t *>(first + 8 * i) : 0ull;
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = bits ? (w[i] >> bits) | (w[i + 1] << (64 - bits)) : w[i];
+}
+// Values [c, c + 8) of a row of H on any boundary; past its end 0.
+template <class T>
+__device__ __forceinline__ Run load8_any(const T *row, int c, int H) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+    Run r;
+    if constexpr (sizeof(T) == 4) {
+        load_words<4>(at + 4 * static_cast<uintptr_t>(c), at + 4 * static_cast<uintptr_t>(H), r.p);
+    } else {
+        uint64_t w[2];
+        load_words<2>(at + 2 * static_cast<uintptr_t>(c), at + 2 * static_cast<uintptr_t>(H), w);
+        r = unpack8(make_uint4(static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[0] >> 32), static_cast<uint32_t>(w[1]),
+                               static_cast<uint32_t>(w[1] >> 32)), row);
+    }
+    if (c + 8 > H) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = c + e < H ? run_at(r, e) : 0.f;
+        r = run_of(v);
+    }
+    return r;
+}
+// The first `n` of 8 elements of ELEM bytes each, held in w, to any boundary; two at a time
+// where `pairs` (the address is a multiple of two elements).
+template <int ELEM>
+__device__ __forceinline__ void store_words(uint8_t *p, const uint64_t (&w)[ELEM], bool pairs, int n) {
+    if (pairs && n == 8) {
+#pragma unroll
+        for (int b = 0; b < 8 * ELEM; b += 2 * ELEM) {
+            const uint64_t two = w[b / 8] >> (b % 8 * 8);
+            if constexpr (ELEM == 4) *reinterpret_cast<uint64_t *>(p + b) = two;
+            else if constexpr (ELEM == 2) *reinterpret_cast<uint32_t *>(p + b) = static_cast<uint32_t>(two);
+            else *reinterpret_cast<uint16_t *>(p + b) = static_cast<uint16_t>(two);
+        }
+        return;
+    }
+#pragma unroll
+    for (int b = 0; b < 8 * ELEM; b += ELEM) {
+        if (b >= n * ELEM) break;
+        const uint64_t one = w[b / 8] >> (b % 8 * 8);
+        if constexpr (ELEM == 4) *reinterpret_cast<uint32_t *>(p + b) = static_cast<uint32_t>(one);
+        else if constexpr (ELEM == 2) *reinterpret_cast<uint16_t *>(p + b) = static_cast<uint16_t>(one);
+        else p[b] = static_cast<uint8_t>(one);
+    }
+}
+template <class T>
+__device__ __forceinline__ void store8_any(T *p, const Run &r, bool pairs, int n) {
+    if constexpr (sizeof(T) == 4) {
+        store_words<4>(reinterpret_cast<uint8_t *>(p), r.p, pairs, n);
+    } else {
+        const uint64_t w[2] = {static_cast<uint64_t>(pack2(r.p[1], p)) << 32 | pack2(r.p[0], p),
+                               static_cast<uint64_t>(pack2(r.p[3], p)) << 32 | pack2(r.p[2], p)};
+        store_words<2>(reinterpret_cast<uint8_t *>(p), w, pairs, n);
+    }
+}
 __device__ __forceinline__ void store8(float *p, const Run &r) {
     asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};"
                  ::"l"(reinterpret_cast<uint64_t>(p)), "l"(r.p[0]), "l"(r.p[1]), "l"(r.p[2]), "l"(r.p[3]) : "memory");
