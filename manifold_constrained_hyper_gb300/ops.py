@@ -416,6 +416,7 @@ def mhc_status_string(code: int) -> str:
 
 # ---------------------------------------------------------------------------
 # Gated residual block, its backward pass, and 8-bit activation checkpoints
+# (new tensors of a small call, up to 512 KB in all, are parts of one allocation)
 
 _DTYPES = {torch.float32: MHC_F32, torch.bfloat16: MHC_BF16, torch.float16: MHC_F16}
 _FORMATS = {"e4m3": 1, "int8": 2}
@@ -580,8 +581,8 @@ def mhc_block_norm_backward(d_residual_out, d_h, y, residual, rstd, w_post=None,
     the weights, the gate, the scale and params as in the forward call.
     residual_dtype (d_residual_out's, else the residual's, else d_h's, unless
     given) is needed only where none of them tells it. The gradients of
-    weights, of a [H] or [T, 1] gate and of res_scale are float32 (parts of
-    one allocation); d_residual may be d_residual_out itself."""
+    weights, of a [H] or [T, 1] gate and of res_scale are float32 (always parts
+    of one allocation); d_residual may be d_residual_out itself."""
     f = (_fast or load_binding()).block_norm_backward
     p = _DEFAULT_BLOCK_PARAMS if params is None else params
     typed = None if residual_dtype is None else torch.empty(0, dtype=residual_dtype)
