@@ -13,6 +13,10 @@
 // values and slopes between the two passes over a row: in registers they
 // would not leave room for the row, and in shared memory not for the rows to
 // come. The sums leave it once, and a second kernel adds the CTAs' in their order.
+//
+// Measured, bf16, channel gate and scale: 8192 x 7168 136 us, 5.2 TB/s of the bytes that it must
+// move (0.77 of a copy's rate), from int8 checkpoints 154; strided by 7171 elements 163,
+// 7169 wide 194 (single elements); 512 x 7168 15 us, and 4.2 for the second kernel.
 #pragma once
 #include <type_traits>
 

@@ -10,7 +10,12 @@
 // a row's fixed costs (two sums, a wait, addresses) spread. A row's two sums
 // follow one another: a CTA's groups have a row each in flight, and the rows
 // to come are staged in shared memory by bulk copies meanwhile, a stage
-// refilled as soon as its row is in registers.
+// refilled as soon as its row is in registers. With 16 columns a thread
+// 8192 x 7168 takes 2 to 10 % longer.
+//
+// Measured, bf16: 8192 x 7168 with a full sigmoid gate 101 us, 5.8 TB/s of the bytes that it
+// must move (0.87 of a copy's rate), with a channel gate and scale 86; strided by
+// 7171 elements 146, 7169 wide 205 (single elements: bound by instructions); one row of 7168 4.5 us.
 #pragma once
 #include "block_rows.cuh"
 
@@ -287,6 +292,7 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
     FwdRing ring = {};
     ring.groups = 1;
     const long long rows = (f.T + sms - 1) / sms;
+    // one row a CTA at most: nothing to stage ahead (1 x 7168 4.5 us, staged 5.4; 64 x 2048 2.9 and 5.2)
     if (vec && (rows == 1 || f.H <= kFwdNarrow)) {
         // a thread for each run of a row; a row's warp needs no barrier
         const int threads = row_threads(f.H, 1);

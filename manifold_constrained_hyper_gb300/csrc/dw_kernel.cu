@@ -17,6 +17,9 @@
 // holds is read and stored under the products into the other. Where there are
 // too few tiles for the machine the tokens are split, and a second kernel
 // adds the splits in their order.
+//
+// Measured: 8192 tokens, 7168 x 4096 bf16: 291 us with the unpacking, 1655 TFLOP/s (0.87 of a library
+// product's burst rate, 0.96 of its sustained one); 4096 tokens, 2048 x 2048 fp32: 33 us.
 #include <atomic>
 
 #include "mhc_internal.h"
@@ -44,7 +47,8 @@ constexpr int kBars = 2 * kStages + 5;
 constexpr int kTurnBytes = kSumWarps * 32 * 33 * 4;         // a 32 x 32 piece of the sums for each epilogue warp
 constexpr int kSmem = kStages * kStageBytes + 1024 /* alignment */ + 256 /* barriers */ + kTurnBytes;
 constexpr int kTmemCols = 512;
-constexpr int kBand = 8;                            // rows of tiles that are walked together
+// Rows of tiles that are walked together (8192 tokens, 4096 x 7168: 296 us; one by one 309, 4 302, 16 298).
+constexpr int kBand = 8;
 
 enum DwSite : int { SITE_DW_EMPTY = 60, SITE_DW_FULL, SITE_DW_ACC_EMPTY, SITE_DW_ACC_FULL, SITE_DW_DRAIN };
 
@@ -490,7 +494,7 @@ struct DwPlan {
 };
 
 // Tiles of 128 columns where those of 256 would leave half of the pairs of CTAs
-// idle. Splits: with fewer tiles than pairs, as many as give every pair an item
+// idle (333 tokens into 519 x 1096 9.6 us, with 256 11.1; 154 into 1568 x 592 7.3 and 8.6). Splits: with fewer tiles than pairs, as many as give every pair an item
 // of at least 4 steps (256 tokens), from 12 steps on: below, the second kernel
 // costs more than the steps it saves (528 tokens into 1568 x 32: 10.1 us in two
 // splits, 7.9 in one; 1230 into 587 x 216: 13.0 us in five, 14.0 in two).
