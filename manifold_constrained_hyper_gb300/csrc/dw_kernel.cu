@@ -397,16 +397,43 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-// d_w from the splits' sums, in their order (none: zeros).
+// d_w from the splits' sums, in their order (none: zeros). VEC elements a thread (4 where the
+// splits' sums lie on 16-byte boundaries, else 1), the loads of eight splits in flight: few elements of
+// many splits are bound by latency.
+template <int VEC>
 __global__ void __launch_bounds__(256) dw_join_kernel(const float *parts, int splits, long long count, void *d_w,
                                                       int dtype, int accumulate) {
     griddep_wait();
-    const long long step = static_cast<long long>(gridDim.x) * 256;
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < count; i += step) {
-        float v = 0.f;
-        for (int s = 0; s < splits; ++s) v += parts[s * count + i];
-        store_any(d_w, dtype, i, accumulate ? load_any(d_w, dtype, i) + v : v);
+    const long long step = static_cast<long long>(gridDim.x) * 256 * VEC;
+    for (long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * VEC; i < count; i += step) {
+        float v[VEC] = {};
+        for (int s0 = 0; s0 < splits; s0 += 8) {
+            alignas(16) float w[8][VEC];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) w[s][e] = 0.f;
+                if (s0 + s >= splits) continue;
+                const float *const p = parts + (s0 + s) * count + i;
+                if constexpr (VEC == 4) *reinterpret_cast<float4 *>(w[s]) = *reinterpret_cast<const float4 *>(p);
+                else w[s][0] = *p;
+            }
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[e] += w[s][e];
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            store_any(d_w, dtype, i + e, accumulate ? load_any(d_w, dtype, i + e) + v[e] : v[e]);
     }
+}
+cudaError_t launch_join(const float *parts, int splits, long long count, void *d_w, int dtype, int accumulate, int sms, bool pdl,
+                        cudaStream_t s) {
+    const int vec = splits && count % 4 == 0 ? 4 : 1;
+    const long long need = (count + 256 * vec - 1) / (256 * vec), cap = static_cast<long long>(sms) * 16;
+    return launch_block_kernel(vec == 4 ? dw_join_kernel<4> : dw_join_kernel<1>, static_cast<unsigned>(need < cap ? need : cap), 256,
+                               0, pdl, s, parts, splits, count, d_w, dtype, accumulate);
 }
 
 // The operands as the products read them: the checkpoint's values in 16 bits,
@@ -533,11 +560,7 @@ size_t dw_workspace(long long T, int n, int k, bool d_aligned) {
 int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
     const DwPlan p = dw_plan(a.T, a.n, a.k, d_aligned);
     const long long count = static_cast<long long>(a.n) * a.k;
-    const long long join_blocks = (count + 1023) / 1024, join_cap = static_cast<long long>(sms) * 16;
-    const unsigned join_grid = static_cast<unsigned>(join_blocks < join_cap ? join_blocks : join_cap);
-    if (p.steps == 0)
-        return note_launch(launch_block_kernel(dw_join_kernel, join_grid, 256, 0, pdl, s,
-                                               static_cast<const float *>(nullptr), 0, count, a.d_w, a.d_w_dtype, 0));
+    if (p.steps == 0) return note_launch(launch_join(nullptr, 0, count, a.d_w, a.d_w_dtype, 0, sms, pdl, s));
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     void *const x16 = ws;
     void *const d16 = ws + p.x_bytes;
@@ -598,8 +621,7 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     cfg.numAttrs = pdl ? 2 : 1;
     if (int e = note_launch(cudaLaunchKernelEx(&cfg, dw_gemm_kernel, md, mx, g))) return e;
     if (p.splits == 1) return MHC_OK;
-    return note_launch(launch_block_kernel(dw_join_kernel, join_grid, 256, 0, pdl, s, static_cast<const float *>(parts),
-                                           p.splits, count, a.d_w, a.d_w_dtype, a.accumulate));
+    return note_launch(launch_join(parts, p.splits, count, a.d_w, a.d_w_dtype, a.accumulate, sms, pdl, s));
 }
 
 }  // namespace mhc
