@@ -521,10 +521,10 @@ struct DwPlan {
 };
 
 // Tiles of 128 columns where those of 256 would leave half of the pairs of CTAs
-// idle (333 tokens into 519 x 1096 9.6 us, with 256 11.1; 154 into 1568 x 592 7.3 and 8.6). Splits: with fewer tiles than pairs, as many as give every pair an item
-// of at least 4 steps (256 tokens), from 12 steps on: below, the second kernel
-// costs more than the steps it saves (528 tokens into 1568 x 32: 10.1 us in two
-// splits, 7.9 in one; 1230 into 587 x 216: 13.0 us in five, 14.0 in two).
+// idle (333 tokens into 519 x 1096 9.6 us, with 256 11.1; 154 into 1568 x 592 7.3 and 8.6). Splits: with fewer tiles
+// than pairs, as many as give every pair an item of at least 4 steps (256 tokens), from 12 steps on: below,
+// the second kernel costs about what the steps save (520 tokens into 2048 x 512: 11.1 us in two splits,
+// 10.4 in one; 700 into 512 x 512 9.8 and 10.6; 1230 into 587 x 216 10.8 in five, 12.5 in two).
 DwPlan dw_plan(long long T, int n, int k, bool d_aligned) {
     DwPlan p;
     p.tiles_n = (n + kTile - 1) / kTile;
