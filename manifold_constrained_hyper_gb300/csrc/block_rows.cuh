@@ -3,7 +3,6 @@
 #pragma once
 #include <atomic>
 
-#include "mhc_internal.h"
 #include "vec_io.cuh"
 
 namespace mhc {

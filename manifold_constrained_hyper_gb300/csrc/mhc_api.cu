@@ -8,6 +8,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "block_internal.h"
 #include "mhc.h"
 #include "mhc_internal.h"
 

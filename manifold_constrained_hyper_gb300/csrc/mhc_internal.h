@@ -194,16 +194,4 @@ cudaError_t launch_rcp_check(uint32_t first, unsigned long long count, unsigned 
                              cudaStream_t s);
 unsigned int *device_status_word();   // of the current device; NULL on failure
 
-// What the entry points share (mhc_api.cu). Both return an mhc_status.
-// Whether the current device runs this library; its SM count and status word.
-int require_device(int *sms, unsigned int **status);
-int note_launch(cudaError_t e);       // of one kernel launch; counts it when it went out
-bool pdl_enabled();                   // launch as programmatic dependents
-unsigned long long wait_timeout_ns();
-// cuTensorMapEncodeTiled for a 2D row-major tensor of 16-bit elements: `inner`
-// of them a row, rows `pitch_bytes` apart, boxes of 64 x box_rows in the
-// 128-byte swizzle.
-bool encode_rows16(CUtensorMap *m, bool bf16, const void *ptr, unsigned long long inner,
-                   unsigned long long rows, unsigned long long pitch_bytes, unsigned int box_rows);
-
 }  // namespace mhc
