@@ -92,11 +92,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         tmem_relinquish();
     }
     for (int i = threadIdx.x; i < ring.groups * 2 * 3 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
-    if (STAGED && threadIdx.x == 0) {
-        for (int s = 0; s < ring.stages; ++s) {
-            mbar_init(bar + 8 * s, 1);
-            armed[s] = -1;
-        }
+    if (STAGED && threadIdx.x < ring.stages) {          // 32 at most: the first warp, a lane a stage
+        mbar_init(bar + 8 * threadIdx.x, 1);
+        armed[threadIdx.x] = -1;
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -137,7 +135,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         return c;
     };
     constexpr int PARTS = HELD ? 7 : FULL ? 5 : 4;
-    auto fetch = [&](long long t, int s, int filling) {     // one thread
+    auto fetch = [&](long long t, int s, int filling) {     // one thread a stage
         const uint32_t b = bar + 8 * s;
         uint32_t dst = smem_addr(smem) + s * ring.stage_bytes, total = 0;
         const uint64_t pol = policy_evict_first();
@@ -152,11 +150,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             dst += ring.place[k];
         }
     };
-    if (STAGED && threadIdx.x == 0)
-        for (int s = 0; s < ring.stages; ++s) {
-            const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
-            if (t < f.T) fetch(t, s, 0);
-        }
+    if (STAGED && threadIdx.x < ring.stages) {
+        const long long t = blockIdx.x + static_cast<long long>(threadIdx.x) * gridDim.x;
+        if (t < f.T) fetch(t, threadIdx.x, 0);
+    }
     __syncwarp();
     // w1 = (w_post + offset) * act of a channel gate, w2 = w_pre + offset, a channel scale; the sums
 #pragma unroll

@@ -71,8 +71,13 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     const uint32_t bar = smem_addr(bars);
 
     for (int i = threadIdx.x; i < ring.groups * 2 * MAXW; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
-    if (STAGED && threadIdx.x == 0) {
-        for (int s = 0; s < ring.stages; ++s) {
+    // The stages are set up, and filled for the first time, by a lane of the first warp each; with
+    // checkpoints and 32 columns a thread by one thread: there the registers are short (spills:
+    // 8192 x 7168 with int8 checkpoints 116 us, 159).
+    constexpr bool LANES = !(CKPT && RUNS == 4);
+    const int first_stage = LANES ? threadIdx.x : 0, stage_step = LANES ? 32 : 1;
+    if (STAGED && threadIdx.x < (LANES ? 32 : 1)) {
+        for (int s = first_stage; s < ring.stages; s += stage_step) {
             mbar_init(bar + 8 * s, 1);
             armed[s] = -1;
         }
@@ -83,7 +88,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
     griddep_wait();
     // The CTA's rows are blockIdx.x + k gridDim.x, k = 0, 1, ...: group k mod
     // groups takes row k, from stage k mod stages.
-    auto fetch = [&](long long t, int s, int filling) {     // one thread
+    auto fetch = [&](long long t, int s, int filling) {     // one thread a stage
         const uint32_t b = bar + 8 * s, dst = smem_addr(smem) + stage0 + s * stage_bytes;
         const uint64_t pol = policy_evict_first();
         const TY *const y = static_cast<const TY *>(a.y) + t * a.y_stride;
@@ -102,8 +107,8 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
             if (FULL && ring.g_place) bulk_load_row(dst + ring.y_place + ring.r_place, g, g_bytes, b, pol);
         }
     };
-    if (STAGED && threadIdx.x == 0)
-        for (int s = 0; s < ring.stages; ++s) {
+    if (STAGED && threadIdx.x < (LANES ? 32 : 1))
+        for (int s = first_stage; s < ring.stages; s += stage_step) {
             const long long t = blockIdx.x + static_cast<long long>(s) * gridDim.x;
             if (t < f.T) fetch(t, s, 0);
         }
