@@ -13,10 +13,12 @@
 // refilled as soon as its row is in registers. With 16 columns a thread
 // 8192 x 7168 takes 2 to 10 % longer.
 //
-// Measured, bf16: 8192 x 7168 with a full sigmoid gate 101 us, 5.8 TB/s of the bytes that it
-// must move (0.87 of a copy's rate), with a channel gate and scale 86; strided by
+// Measured, bf16: 8192 x 7168 with a full sigmoid gate 99.5 us, 5.9 TB/s of the bytes that it
+// must move (0.88 of a copy's rate), with a channel gate and scale 86; strided by
 // 7171 elements 146, 7169 wide 205 (single elements: bound by instructions); one row of 7168 4.5 us.
 #pragma once
+#include <type_traits>
+
 #include "block_rows.cuh"
 
 namespace mhc {
@@ -42,7 +44,7 @@ struct FwdRing {
 };
 
 // FULL, SCALED, CKPT: whether a call may have a full gate, a channel scale,
-// checkpoints. RUNS of 8 columns a thread: 4, and 2 of rows on any boundary, in blocks of up to 512
+// checkpoints. RUNS of 8 columns a thread: 4, and 2 of rows on any boundary or most with checkpoints, in blocks of up to 512
 // threads of 128 registers; 1, up to 1024 threads of 64, for a few rows or narrow ones.
 template <class TY, class TR, int MODE, int RUNS, bool FULL, bool SCALED, bool CKPT>
 __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(const BlockFwdArgs a, const FwdRing ring) {
@@ -308,7 +310,13 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
                                                                  threads, 3 * 32 * threads, pdl, s);
     }
     // as many groups as fit, but no more than give every SM a row
-    const int runs = vec ? 4 : 2, threads = row_threads(f.H, runs);
+    // 32 columns a thread; with checkpoints 16, since their registers would spill (a step, forward and backward,
+    // of 4096 x 4096 with an fp32 residual and e4m3 checkpoints 98.9 us, with 32 columns 109.7; with a
+    // full gate 144 and 173), but where nothing does (bf16 alone) and 16 would leave one row a CTA in
+    // flight (8192 x 7168 with int8 checkpoints: 275 us, with 16 columns 283).
+    constexpr bool kWideCkpt = std::is_same<TR, __nv_bfloat16>::value;
+    const bool wide_ckpt = kWideCkpt && !full && f.H > 4096;
+    const int runs = vec && (!ckpt || wide_ckpt) ? 4 : 2, threads = row_threads(f.H, runs);
     long long groups = 512 / threads;
     if (groups > kFwdGroups) groups = kFwdGroups;
     ring.groups = static_cast<int>(rows < groups ? rows : groups);
@@ -335,14 +343,19 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
     if (!vec)
         return ckpt ? fwd_launch<TY, TR, ROWS_SKEW, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s)
                     : fwd_launch<TY, TR, ROWS_SKEW, 2, true, true, false>(a, ring, grid, threads, smem, pdl, s);
-    if (full)
-        return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, true, true, true>(a, ring, grid, threads, smem, pdl, s)
-                    : fwd_launch<TY, TR, ROWS_RING, 4, true, true, false>(a, ring, grid, threads, smem, pdl, s);
-    if (scaled)
-        return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, false, true, true>(a, ring, grid, threads, smem, pdl, s)
-                    : fwd_launch<TY, TR, ROWS_RING, 4, false, true, false>(a, ring, grid, threads, smem, pdl, s);
-    return ckpt ? fwd_launch<TY, TR, ROWS_RING, 4, false, false, true>(a, ring, grid, threads, smem, pdl, s)
-                : fwd_launch<TY, TR, ROWS_RING, 4, false, false, false>(a, ring, grid, threads, smem, pdl, s);
+    if (ckpt && runs == 2) {
+        if (full) return fwd_launch<TY, TR, ROWS_RING, 2, true, true, true>(a, ring, grid, threads, smem, pdl, s);
+        return scaled ? fwd_launch<TY, TR, ROWS_RING, 2, false, true, true>(a, ring, grid, threads, smem, pdl, s)
+                      : fwd_launch<TY, TR, ROWS_RING, 2, false, false, true>(a, ring, grid, threads, smem, pdl, s);
+    }
+    if constexpr (kWideCkpt) {
+        if (ckpt)
+            return scaled ? fwd_launch<TY, TR, ROWS_RING, 4, false, true, true>(a, ring, grid, threads, smem, pdl, s)
+                          : fwd_launch<TY, TR, ROWS_RING, 4, false, false, true>(a, ring, grid, threads, smem, pdl, s);
+    }
+    if (full) return fwd_launch<TY, TR, ROWS_RING, 4, true, true, false>(a, ring, grid, threads, smem, pdl, s);
+    return scaled ? fwd_launch<TY, TR, ROWS_RING, 4, false, true, false>(a, ring, grid, threads, smem, pdl, s)
+                  : fwd_launch<TY, TR, ROWS_RING, 4, false, false, false>(a, ring, grid, threads, smem, pdl, s);
 }
 
 }  // namespace
