@@ -179,7 +179,7 @@ mhc_status mhc_block_norm(const mhc_block *block, const void *y, int64_t y_strid
 size_t mhc_block_norm_backward_workspace_bytes(int64_t tokens, int hidden) {
     if (tokens <= 0 || hidden < 1 || hidden > kBlockMaxHidden) return 0;
     const size_t parts = static_cast<size_t>(tokens < kBackMaxParts ? tokens : kBackMaxParts);
-    return (parts * kBackSums * static_cast<size_t>(hidden) + parts) * sizeof(float);
+    return (parts * kBackSums * static_cast<size_t>(hidden) + 2 * parts) * sizeof(float);
 }
 
 mhc_status mhc_block_norm_backward(const mhc_block *block, const void *d_residual_out,

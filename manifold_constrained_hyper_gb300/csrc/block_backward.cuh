@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     __shared__ __align__(16) float red[kBwdGroups][2][3 * MAXW];
     __shared__ __align__(8) uint64_t bars[kBwdStages];
     __shared__ volatile int armed[kBwdStages];      // the filling each stage is in
-    __shared__ float scale_red[32];
+    __shared__ float scale_red[64];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const BlockForm &f = a.f;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
     }
     tmem_st_wait();
     const uint64_t scale = splat2(f.scale_form == MHC_SCALE_ONE ? *f.res_scale : 1.f);
-    uint64_t scale2 = 0;
+    LongSum scale_sum;
 
     // What a row needs beside its columns, fetched a row ahead and left as it
     // was loaded: arithmetic on it here would wait for it.
@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         const float c1 = fmaf(-q, sum[2], sum[1]);
         const float p = f.post_norm ? rstd1 * (rstd1 * (rstd1 * (token * c1 * f.inv_h))) : 0.f;
         const uint64_t q2 = splat2(-q), p2 = splat2(-p);
+        uint64_t scale2 = 0;                        // a single scale's terms of this row
         tmem_st_wait();
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             tmem_run_store(cell(T_DW1, j), sum1);
             if (SCALED) tmem_run_store(cell(T_DSCALE, j), sums);
         }
+        if (!SCALED) scale_sum.add(f2_lo(scale2) + f2_hi(scale2));
         tmem_st_wait();
         if (STAGED && !KEPT) {
             if (warps > 1) named_barrier_sync(1 + grp, at.threads);
@@ -458,10 +460,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             store_run<MODE>(out + static_cast<long long>(k) * H, at, j, acc);
         }
     }
-    float total[1] = {f2_lo(scale2) + f2_hi(scale2)};
     if (SCALED && f.scale_form == MHC_SCALE_ONE) {
         // a single scale in the general form: its columns' sums
-        total[0] = 0.f;
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
             Run acc;
@@ -470,11 +470,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             tmem_run_wait(acc);
             acc = run_within<MODE>(acc, at, j);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) total[0] += f2_lo(acc.p[i]) + f2_hi(acc.p[i]);
+            for (int i = 0; i < 4; ++i) {
+                scale_sum.add(f2_lo(acc.p[i]));
+                scale_sum.add(f2_hi(acc.p[i]));
+            }
         }
     }
-    block_sum<1>(total, scale_red);
-    if (threadIdx.x == 0) a.scale_sums[blockIdx.x] = total[0];
+    block_long_sum(scale_sum, scale_red);
+    if (threadIdx.x == 0) {
+        a.scale_sums[2 * blockIdx.x] = scale_sum.hi;
+        a.scale_sums[2 * blockIdx.x + 1] = scale_sum.lo;
+    }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x < 32) {

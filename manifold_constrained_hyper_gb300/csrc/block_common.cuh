@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <cfloat>
+
 #include "block_internal.h"
 #include "ptx.cuh"
 
@@ -148,6 +150,47 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float *red) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     }
+}
+
+// A sum held as hi + lo, where lo gathers what each addition to hi rounded off (the error of an
+// addition of two floats is a float, formed here by Knuth's two-sum): 48 bits. For the gradient of
+// a single scale, a sum over all tokens and columns whose terms may all but cancel (2047 x 1102:
+// 2.3 million terms). No infinity or NaN is lost: it stays in hi.
+struct LongSum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = __fadd_rn(hi, x), b = __fsub_rn(t, hi);
+        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(x, b));
+        hi = t;
+    }
+    __device__ __forceinline__ void add(const LongSum &o) {
+        add(o.hi);
+        lo += o.lo;
+    }
+    __device__ __forceinline__ void add_warp() {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            LongSum other;
+            other.hi = __shfl_xor_sync(0xffffffffu, hi, o);
+            other.lo = __shfl_xor_sync(0xffffffffu, lo, o);
+            add(other);
+        }
+    }
+    __device__ __forceinline__ float value() const { return fabsf(hi) <= FLT_MAX ? hi + lo : hi; }
+};
+// Over the block, for its first warp. `red`: 64 floats of shared memory.
+__device__ __forceinline__ void block_long_sum(LongSum &s, float *red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x + 31) >> 5;
+    s.add_warp();
+    if (lane == 0) {
+        red[warp] = s.hi;
+        red[32 + warp] = s.lo;
+    }
+    __syncthreads();
+    if (warp) return;
+    s.hi = lane < warps ? red[lane] : 0.f;
+    s.lo = lane < warps ? red[32 + lane] : 0.f;
+    s.add_warp();
 }
 
 // Launch of a kernel on `s`, as a programmatic dependent of the one before it

@@ -59,7 +59,7 @@ struct BlockFwdArgs {
 
 // Sums over tokens, one set per CTA of the row kernel: sums[p][0] for d_w_post
 // (and a channel gate), sums[p][1] for d_w_pre, sums[p][2] for a channel
-// scale, each [H]; scale_sums[p] for a single scale.
+// scale, each [H]; scale_sums[p][2] for a single scale, in two floats.
 constexpr int kBackSums = 3;
 struct BlockBwdArgs {
     BlockForm f;

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(512) block_bwd_loop_kernel(const BlockBwdArgs 
     const int H = f.H, groups = (H + 31) / 32, step = blockDim.x * N;
     const bool gated = f.gate_form == MHC_GATE_CHANNEL || f.gate_form == MHC_GATE_FULL;
     float *const sums = a.sums + static_cast<long long>(blockIdx.x) * kBackSums * H;
-    float scale_sum = 0.f;
+    LongSum scale_sum;
     bool first = true;
     int which = 0;
     for (long long t = blockIdx.x; t < f.T; t += gridDim.x, first = false, which ^= 1) {
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(512) block_bwd_loop_kernel(const BlockBwdArgs 
             }
         }
         block_sum(s, red[which]);
+        float row_scale = 0.f;
         const float q = rstd2 * (rstd2 * (rstd2 * (s[0] * f.inv_h)));
         const float c1 = fmaf(-q, s[2], s[1]);
         const float p = f.post_norm ? rstd1 * (rstd1 * (rstd1 * (token * c1 * f.inv_h))) : 0.f;
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(512) block_bwd_loop_kernel(const BlockBwdArgs 
                 add(sums + 2 * static_cast<long long>(H), s2);
             } else {
 #pragma unroll
-                for (int e = 0; e < N; ++e) scale_sum += s2[e];
+                for (int e = 0; e < N; ++e) row_scale += s2[e];
             }
         }
         if (f.gate_form == MHC_GATE_TOKEN && a.d_gate && threadIdx.x == 0) {
@@ -250,11 +251,14 @@ __global__ void __launch_bounds__(512) block_bwd_loop_kernel(const BlockBwdArgs 
             gate_both(load_any(f.gate, f.gate_dtype, t * f.gate_stride), f.gate_act, &g, &slope);
             static_cast<float *>(a.d_gate)[t] = slope * rstd1 * c1;
         }
+        scale_sum.add(row_scale);
     }
-    float s[1] = {scale_sum};
     __syncthreads();
-    block_sum(s, red[0]);
-    if (threadIdx.x == 0) a.scale_sums[blockIdx.x] = s[0];
+    block_long_sum(scale_sum, red[0]);
+    if (threadIdx.x == 0) {
+        a.scale_sums[2 * blockIdx.x] = scale_sum.hi;
+        a.scale_sums[2 * blockIdx.x + 1] = scale_sum.lo;
+    }
 }
 
 bool codes_fit(const Ckpt &c) { return (reinterpret_cast<uintptr_t>(c.codes) & 7u) == 0; }

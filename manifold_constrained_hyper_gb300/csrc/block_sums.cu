@@ -64,11 +64,15 @@ __global__ void __launch_bounds__(32 * kSumWarps) block_sums_kernel(const BlockS
         }
     }
     if (k == 0 && blockIdx.x == 0 && a.d_res_scale && f.scale_form == MHC_SCALE_ONE && warp == kSumWarps - 1) {
-        float s = 0.f;
-        for (int p = lane; p < a.parts; p += 32) s += a.scale_sums[p];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) a.d_res_scale[0] = s;
+        LongSum s;
+        for (int p = lane; p < a.parts; p += 32) {
+            LongSum part;
+            part.hi = a.scale_sums[2 * p];
+            part.lo = a.scale_sums[2 * p + 1];
+            s.add(part);
+        }
+        s.add_warp();
+        if (lane == 0) a.d_res_scale[0] = s.value();
     }
 }
 

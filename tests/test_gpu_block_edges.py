@@ -1,0 +1,92 @@
+"""The gated residual block, the checkpoints and the weight gradient at the edges
+of their range: long sums, infinities, values past fp16, one token, no tokens."""
+
+import pytest
+import torch
+
+from manifold_constrained_hyper_gb300 import ops
+from tests import block_ref as ref
+from tests.test_gpu_block import BF, FP16, FP32, PAIRS, check_backward, check_forward, make, params, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from manifold_constrained_hyper_gb300 import build
+    build.build()
+    ops.load()
+
+
+# ------------------------------------------------------------------ sums over tokens
+
+# every way a row goes: staged on boundaries, off them (inputs alone, outputs too), from
+# memory (the widest types), by the loop; with a full gate, and from checkpoints
+SUMS = [(2047, 1102, "fp32", "full", 0, False), (1500, 1032, "bf16", "none", 0, False), (1500, 1032, "bf16", "token", 3, False),
+        (1500, 2056, "fp16+", "channel", 0, True), (1200, 1031, "bf16+", "full", 0, True), (1300, 520, "bf16", "full", 8, True),
+        (700, 7168, "fp32", "token", 0, False), (330, 8192, "fp32", "full", 0, False), (330, 7171, "fp32", "none", 0, False),
+        (700, 8200, "bf16", "channel", 0, False), (700, 8203, "bf16", "none", 0, True), (4000, 64, "fp16", "none", 0, False)]
+
+
+def _whole(g, T, H, dtype, lo, hi, pad=0):
+    t = torch.randint(lo, hi, (T, H + pad), generator=g, device="cuda").to(dtype)
+    return t[:, :H] if pad else t
+
+
+@pytest.mark.parametrize("T,H,types,gate,pad,held", SUMS)
+@pytest.mark.parametrize("scale", ["one", "channel"])
+def test_sums_over_tokens_are_exact_for_whole_numbers(T, H, types, gate, pad, held, scale):
+    """With d_h = 0 and whole numbers everywhere, D is d_residual_out and every term is a whole
+    number. A column's sums stay below 2^24 and have to be exact; a single scale's sum passes
+    2^24 by far: its thread's terms of a row are exact, and what joins them holds 48 bits, so
+    that it is off by its own rounding alone."""
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    dt, rt = PAIRS[types]
+    gt = dt if gate == "full" else FP32
+    y, r = _whole(g, T, H, dt, -2, 3, pad), _whole(g, T, H, rt, 1, 128, pad)
+    d_ro, d_h = _whole(g, T, H, rt, 1, 64, pad), torch.zeros(T, H, dtype=dt, device="cuda")
+    w_post, w_pre = (_whole(g, 1, H, FP32, 1, 3)[0] for _ in range(2))
+    z = {"none": lambda: None, "channel": lambda: _whole(g, 1, H, gt, -1, 2)[0], "token": lambda: _whole(g, T, 1, gt, -1, 2),
+         "full": lambda: _whole(g, T, H, gt, -1, 2)}[gate]()
+    a = torch.full((1,), 2.0, device="cuda") if scale == "one" else _whole(g, 1, H, FP32, 1, 3)[0]
+    rstd = torch.ones(T, 2, device="cuda")
+    args = (rstd, w_post, w_pre, z, a, params())
+    f = {"y": ops.mhc_ckpt_pack(y, "int8") if held else y, "residual": ops.mhc_ckpt_pack(r, "int8") if held else r}
+    got = ops.mhc_block_norm_backward(d_ro, d_h, f["y"], f["residual"], *args, residual_dtype=rt)
+    Y, R, D = y.double(), r.double(), d_ro.double()
+    gz = 1.0 if z is None else z.double()
+    assert torch.equal(got.d_w_post, (gz * D * Y).sum(0).float())
+    ds = R * D
+    assert torch.equal(got.d_res_scale, (ds.sum(0) if scale == "channel" else ds.sum().reshape(1)).float())
+    if z is not None and gate != "full":
+        dg = Y * w_post.double() * D
+        assert torch.equal(got.d_gate, (dg.sum(0) if gate == "channel" else dg.sum(1, keepdim=True)).float())
+    # d_w_pre needs no D: whole numbers of d_h, ro = a r + g y w_post
+    r = _whole(g, T, H, rt, -3, 4, pad)
+    d_h = _whole(g, T, H, dt, -3, 4, pad)
+    ro = a.double() * r.double() + gz * Y * w_post.double()
+    got = ops.mhc_block_norm_backward(None, d_h, f["y"], ops.mhc_ckpt_pack(r, "int8") if held else r, *args, residual_dtype=rt)
+    assert torch.equal(got.d_w_pre, (d_h.double() * ro).sum(0).float())
+
+
+@pytest.mark.parametrize("T,H,types,gate,pad,held", SUMS)
+def test_single_scale_gradient_of_a_stream(T, H, types, gate, pad, held):
+    """A gradient with a part along the stream, as a loss's has: the sum is of the size of its
+    magnitudes. Each D passes two row sums (2 steps(H) roundings); then a thread adds at most 16
+    columns of a row, or a column of at most T / 152 + 1 rows, and the rest holds 48 bits."""
+    x, d, form = make(T, H, types, gate, "sigmoid" if gate != "none" else "none", "one", pad)
+    p = params(form["act"])
+    d["d_ro"].add_((0.05 * x["residual"].float()).to(d["d_ro"].dtype))
+    rstd = ops.mhc_block_norm(x["y"], x["residual"], x["w_post"], x["w_pre"], x["gate"], x["res_scale"], p)[2]
+    y, r, values = x["y"], x["residual"], {}
+    if held:
+        y, r = ops.mhc_ckpt_pack(y, "e4m3"), ops.mhc_ckpt_pack(r, "e4m3")
+        values = {"y": ref.unpack(y.codes, y.scales, "e4m3"), "residual": ref.unpack(r.codes, r.scales, "e4m3")}
+    f = ref.block(**{**x, **values}, gate_act=form["act"])
+    f["n"] = f["y"] * rstd[:, :1].double() * f["w1"]
+    f["ro"] = f["a"] * f["r"] + f["g"] * f["n"]
+    want, size = ref.backward(f, d["d_ro"], d["d_h"], rstd, gate, "one", form["act"])
+    got = ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], y, r, rstd, x["w_post"], x["w_pre"], x["gate"], x["res_scale"], p)
+    bound = (2 * ref.steps(H) + 16 + T / 152 + 1) * ref.EPS * size["d_res_scale"] + ref.EPS * want["d_res_scale"].abs()
+    assert bound < 1e-3 * want["d_res_scale"].abs()             # a sum that is missing a part shows
+    within(got.d_res_scale, want["d_res_scale"], bound, "d_res_scale")
