@@ -265,12 +265,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         Run ev[RUNS];                               // d_ro + rstd_pre d_h w2
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
-            Run w1, w2, sc, sum2;
+            LoadingRun w1_in, w2_in, sc_in, sum2_in;
             __syncwarp();
-            tmem_run_load(cell(T_W1, j), w1);
-            if (SCALED) tmem_run_load(cell(T_SCALE, j), sc);
-            tmem_run_load(cell(T_W2, j), w2);
-            tmem_run_load(cell(T_DW2, j), sum2);
+            tmem_run_load(cell(T_W1, j), w1_in);
+            if (SCALED) tmem_run_load(cell(T_SCALE, j), sc_in);
+            tmem_run_load(cell(T_W2, j), w2_in);
+            tmem_run_load(cell(T_DW2, j), sum2_in);
             Run y = load_y(j), ro = load_r(j);
             if (KEPT) {
                 __syncwarp();
@@ -296,10 +296,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             ev[j] = run_splat(0.f);
             if (a.d_ro) ev[j] = load_df(j);
             __syncwarp();
-            tmem_run_wait(w1);
-            tmem_run_wait(w2);
-            tmem_run_wait(sum2);
-            if (SCALED) tmem_run_wait(sc);
+            const Run w1 = tmem_run_wait(w1_in), w2 = tmem_run_wait(w2_in);
+            Run sum2 = tmem_run_wait(sum2_in), sc;
+            if (SCALED) sc = tmem_run_wait(sc_in);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 y.p[i] = mul2(y.p[i], w1.p[i]);                            // g w1 y, without a token's gate
@@ -339,38 +338,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         tmem_st_wait();
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
-            Run w1, sc, sum1, sums;
-            tmem_run_load(cell(T_W1, j), w1);
-            tmem_run_load(cell(T_DW1, j), sum1);
+            LoadingRun w1_in, sc_in, sum1_in, sums_in, y_in, r_in;
+            tmem_run_load(cell(T_W1, j), w1_in);
+            tmem_run_load(cell(T_DW1, j), sum1_in);
             if (SCALED) {
-                tmem_run_load(cell(T_SCALE, j), sc);
-                tmem_run_load(cell(T_DSCALE, j), sums);
+                tmem_run_load(cell(T_SCALE, j), sc_in);
+                tmem_run_load(cell(T_DSCALE, j), sums_in);
             }
-            Run y, r;
+            Run y, r, sc, sums;
             if (KEPT) {
-                tmem_run_load(cell(T_Y, j), y);
-                tmem_run_load(cell(T_R, j), r);
+                tmem_run_load(cell(T_Y, j), y_in);
+                tmem_run_load(cell(T_R, j), r_in);
             } else {
                 y = load_y(j);
                 r = load_r(j);
                 __syncwarp();
             }
-            tmem_run_wait(w1);
-            tmem_run_wait(sum1);
+            const Run w1 = tmem_run_wait(w1_in);
+            Run sum1 = tmem_run_wait(sum1_in);
             if (KEPT) {
-                tmem_run_wait(y);
-                tmem_run_wait(r);
+                y = tmem_run_wait(y_in);
+                r = tmem_run_wait(r_in);
             }
             if (SCALED) {
-                tmem_run_wait(sc);
-                tmem_run_wait(sums);
+                sc = tmem_run_wait(sc_in);
+                sums = tmem_run_wait(sums_in);
             }
             if (full_gate) {
-                Run gate, z;                        // z: the slope, then d_gate
-                tmem_run_load(cell(T_GATE, j), gate);
-                tmem_run_load(cell(T_SLOPE, j), z);
-                tmem_run_wait(gate);
-                tmem_run_wait(z);
+                LoadingRun gate_in, slope_in;
+                tmem_run_load(cell(T_GATE, j), gate_in);
+                tmem_run_load(cell(T_SLOPE, j), slope_in);
+                const Run gate = tmem_run_wait(gate_in);
+                Run z = tmem_run_wait(slope_in);    // the slope, then d_gate
                 const uint64_t u1 = splat2(rstd1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -438,10 +437,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         if (k >= arrays) break;
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
-            Run acc;
+            LoadingRun acc_in;
             __syncwarp();
-            tmem_run_load(cell(T_DW1 + k, j), acc);
-            tmem_run_wait(acc);
+            tmem_run_load(cell(T_DW1 + k, j), acc_in);
+            const Run acc = tmem_run_wait(acc_in);
             if (ring.groups == 1) store_run<MODE>(out + static_cast<long long>(k) * H, at, j, acc);
             else keep_run(reinterpret_cast<float *>(smem) + (k * ring.groups + grp) * column, at, j, acc);
         }
@@ -464,11 +463,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         // a single scale in the general form: its columns' sums
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
-            Run acc;
+            LoadingRun acc_in;
             __syncwarp();
-            tmem_run_load(cell(T_DSCALE, j), acc);
-            tmem_run_wait(acc);
-            acc = run_within<MODE>(acc, at, j);
+            tmem_run_load(cell(T_DSCALE, j), acc_in);
+            const Run acc = run_within<MODE>(tmem_run_wait(acc_in), at, j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 scale_sum.add(f2_lo(acc.p[i]));

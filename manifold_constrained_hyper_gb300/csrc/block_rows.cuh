@@ -122,18 +122,25 @@ __device__ __forceinline__ void keep_run(float *kept, const Place &p, int j, con
     q[0] = make_ulonglong2(r.p[0], r.p[1]);
     q[p.threads] = make_ulonglong2(r.p[2], r.p[3]);
 }
-// A run in tensor memory: 8 columns of the warp's 32 lanes. Whole warps. The
-// values are there after tmem_run_wait on them.
-__device__ __forceinline__ void tmem_run_load(uint32_t taddr, Run &r) {
+// A run in tensor memory: 8 columns of the warp's 32 lanes. Whole warps. The load leaves its
+// registers undefined until the wait, so they stand as they are in between: only the wait, which
+// takes them, gives a run.
+struct LoadingRun {
     uint32_t v[8];
+};
+__device__ __forceinline__ void tmem_run_load(uint32_t taddr, LoadingRun &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "=r"(r.v[0]), "=r"(r.v[1]), "=r"(r.v[2]), "=r"(r.v[3]), "=r"(r.v[4]), "=r"(r.v[5]), "=r"(r.v[6]), "=r"(r.v[7])
                  : "r"(taddr) : "memory");
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.p[i] = (static_cast<uint64_t>(v[2 * i + 1]) << 32) | v[2 * i];
 }
-__device__ __forceinline__ void tmem_run_wait(Run &r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+l"(r.p[0]), "+l"(r.p[1]), "+l"(r.p[2]), "+l"(r.p[3]) :: "memory");
+__device__ __forceinline__ Run tmem_run_wait(LoadingRun &l) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(l.v[0]), "+r"(l.v[1]), "+r"(l.v[2]), "+r"(l.v[3]), "+r"(l.v[4]), "+r"(l.v[5]), "+r"(l.v[6]), "+r"(l.v[7])
+                 :: "memory");
+    Run r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = (static_cast<uint64_t>(l.v[2 * i + 1]) << 32) | l.v[2 * i];
+    return r;
 }
 __device__ __forceinline__ void tmem_run_store(uint32_t taddr, const Run &r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
