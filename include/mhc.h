@@ -386,8 +386,13 @@ mhc_status mhc_block_norm_backward(const mhc_block *block, const void *d_residua
 mhc_status mhc_ckpt_pack(const void *x, int64_t stride, mhc_dtype dtype, int64_t tokens,
                          int hidden, mhc_ckpt_format format, const mhc_ckpt *out, void *stream);
 
-/* What the checkpoint stands for -> x [T, H] of dtype, contiguous. F32 holds
- * every value exactly, BF16 all but those below 2^-126 (rounded); F16 rounds. */
+/*
+ * What the checkpoint stands for -> x [T, H] of dtype, contiguous. F32 holds
+ * every value exactly but 2^128, which the largest values of F32 and BF16 may
+ * round to and which reads as infinity; BF16 the same and all but those below
+ * 2^-126 (rounded). F16 rounds, and gives the largest finite value (65504) of
+ * either sign for what lies past it: finite values of any type read back finite.
+ */
 mhc_status mhc_ckpt_unpack(const mhc_ckpt *ckpt, mhc_ckpt_format format, int64_t tokens,
                            int hidden, mhc_dtype dtype, void *x, void *stream);
 

@@ -145,7 +145,8 @@ cudaError_t launch_ckpt_pack(const CkptArgs &a, int dtype, int format, int sms, 
 }
 
 cudaError_t launch_ckpt_unpack(const CkptArgs &a, int dtype, int format, int sms, bool pdl, cudaStream_t s) {
-    auto run = dtype == MHC_F32 ? unpack<float> : dtype == MHC_BF16 ? unpack<__nv_bfloat16> : unpack<__half>;
+    // what a finite value's checkpoint stands for may lie past fp16's largest (65504: 65536), and stays finite
+    auto run = dtype == MHC_F32 ? unpack<float> : dtype == MHC_BF16 ? unpack<__nv_bfloat16> : unpack<FiniteHalf>;
     return run(a, format, sms, pdl, s);
 }
 

@@ -43,6 +43,15 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v, const __half *) {
     const __half2 h = __floats2half2_rn(f2_lo(v), f2_hi(v));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// An fp16 element that is written as the largest finite one where the value lies past it; NaN stays.
+struct FiniteHalf {
+    uint16_t bits;
+};
+__device__ __forceinline__ uint32_t pack2(uint64_t v, const FiniteHalf *) {
+    uint32_t w;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(f2_hi(v)), "f"(f2_lo(v)));
+    return w;
+}
 // 8 consecutive values of a row in global memory: 16-bit ones from a 16-byte
 // boundary, fp32 from a 32-byte one.
 __device__ __forceinline__ Run load8(const float *p) {

@@ -616,7 +616,8 @@ def _dtype_number(dtype, name):
 
 
 def mhc_ckpt_unpack(ckpt: Checkpoint, dtype=torch.bfloat16, *, out=None, stream=None):
-    """The values [T, H] that a checkpoint stands for, in `dtype`."""
+    """The values [T, H] that a checkpoint stands for, in `dtype` (float16: at most its
+    largest finite value)."""
     return _at(stream, (_fast or load_binding()).ckpt_unpack, ckpt.codes, ckpt.scales,
                _FORMATS[ckpt.fmt], _dtype_number(dtype, "dtype"), out)
 

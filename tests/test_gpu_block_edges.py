@@ -90,3 +90,23 @@ def test_single_scale_gradient_of_a_stream(T, H, types, gate, pad, held):
     bound = (2 * ref.steps(H) + 16 + T / 152 + 1) * ref.EPS * size["d_res_scale"] + ref.EPS * want["d_res_scale"].abs()
     assert bound < 1e-3 * want["d_res_scale"].abs()             # a sum that is missing a part shows
     within(got.d_res_scale, want["d_res_scale"], bound, "d_res_scale")
+
+
+# ------------------------------------------------------------------ values past fp16
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("H", [64, 77])
+def test_finite_values_stay_finite_in_fp16(fmt, H):
+    """What a checkpoint of fp16's largest values stands for may be 65536: read back as the
+    largest fp16 value, and so are a wider stream's values past it."""
+    x = torch.zeros(6, H, device="cuda")
+    x[0, 3], x[1, 40], x[2, :] = 65504.0, -65504.0, torch.linspace(62000, 65504, H, device="cuda")
+    x[3, 5], x[4, H - 1], x[5, 0] = 1e6, -3e38, 65519.0
+    for t in (x.clamp(-65504, 65504).half(), x):
+        c = ops.mhc_ckpt_pack(t, fmt)
+        want = ref.unpack(c.codes, c.scales, fmt).clamp(-65504.0, 65504.0).half()
+        assert torch.equal(ops.mhc_ckpt_unpack(c, FP16), want)
+    x[1, 0] = float("nan")
+    got = ops.mhc_ckpt_unpack(ops.mhc_ckpt_pack(x, fmt), FP16)
+    assert torch.isnan(got[1, :32]).all() and torch.isfinite(got[1, 32:]).all() and torch.isfinite(got[0]).all()
