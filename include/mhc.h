@@ -397,7 +397,7 @@ mhc_status mhc_ckpt_unpack(const mhc_ckpt *ckpt, mhc_ckpt_format format, int64_t
                            int hidden, mhc_dtype dtype, void *x, void *stream);
 
 /* Bytes of device scratch of mhc_ckpt_linear_dw: x in 16 bits, the sums of
- * tokens that are split, and, unless `aligned` (d_out is on a
+ * tokens that are split, scales of x's columns, and, unless `aligned` (d_out is on a
  * 16-byte boundary and its stride, at least n, a multiple of 16 bytes), d_out's
  * rows on such boundaries. 0 when T == 0 or
  * the call would be refused for its sizes. Needs no initialisation. */
@@ -407,8 +407,12 @@ size_t mhc_ckpt_linear_dw_workspace_bytes(int64_t tokens, int n, int k, int alig
  * Weight gradient of a projection out = x W^T whose input was checkpointed:
  *   d_w[i][j] = sum_t d_out[t][i] * x[t][j]      (accumulate: added to d_w)
  * d_out: [T, n] of dtype (BF16 or F16), rows d_out_stride elements apart.
- * x: a checkpoint [T, k]; its values are exact in bf16 (with an F16 d_out they
- * are rounded to fp16). d_w: [n, k] contiguous, of d_w_dtype (any); products
+ * x: a checkpoint [T, k]; its values are exact in bf16, but 2^128 is infinite.
+ * With an F16 d_out they go to fp16 without a power of two that the values of a
+ * group of 32 columns share over up to 1024 tokens, and that their sums get back:
+ * with 2^K the largest of their scales, nothing overflows, and a value is off by
+ * at most 2^(K - 32) (E4M3) or 2^(K - 34) (INT8); those whose own scale is within
+ * 2^22 or 2^33 of it are exact. d_w: [n, k] contiguous, of d_w_dtype (any); products
  * and sums are fp32, rounded once; the order of the sums is fixed by the
  * sizes. T < 2^31 - 64; n, k in [1, 65536]. T == 0 writes zeros (accumulate:
  * leaves d_w as it is).

@@ -14,7 +14,10 @@
 // (cta_group::2) forms a 256 x 256 tile of d_w: each holds 128 columns of
 // d_out and 128 of x per step of 64 tokens (32 KB, six steps in flight), and
 // its half of the sums in tensor memory, in two buffers, so that what one
-// holds is read and stored under the products into the other. Where there are
+// holds is read and stored under the products into the other. With an fp16
+// d_out (both operands of a product have one type) x goes to fp16, whose range
+// does not hold a checkpoint's: every 32 columns of every piece of the sums (below)
+// give up the power of two of their largest scale, which their sums get back. Where there are
 // too few tiles for the machine the tokens are split, and a second kernel
 // adds the splits in their order.
 //
@@ -43,6 +46,9 @@ constexpr int kThreads = 64 + 32 * kSumWarps;       // loads, products, epilogue
 // products run into the other buffer. A d_w of 16 bits is rounded by up to 2^-9 or 2^-11
 // of itself at the end, so longer pieces do there.
 constexpr int kChain32 = 8, kChain16 = 64;
+// With fp16 operands a piece is also what shares a power of two: shorter ones for a 16-bit d_w too,
+// so that preparing x has work for every SM.
+constexpr int kChainF16 = 16;
 constexpr int kBars = 2 * kStages + 5;
 constexpr int kTurnBytes = kSumWarps * 32 * 33 * 4;         // a 32 x 32 piece of the sums for each epilogue warp
 constexpr int kSmem = kStages * kStageBytes + 1024 /* alignment */ + 256 /* barriers */ + kTurnBytes;
@@ -61,6 +67,8 @@ struct GemmArgs {
     int f16;                        // operands fp16, else bf16
     void *out;                      // d_w, or the splits' fp32 sums [splits][n][k]
     int out_dtype, accumulate, wide;    // wide: rows of out lie on 32-byte boundaries
+    const uint8_t *top;             // fp16: [splits * pieces][groups], the largest scale byte of x's groups of columns in a piece
+    int pieces, groups, shift;      // pieces of a split at most
     unsigned int *status;
     unsigned long long timeout_ns;
 };
@@ -142,6 +150,13 @@ __device__ __forceinline__ void tmem_ld16_now(uint32_t taddr, uint32_t (&v)[16])
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr) : "memory");
+}
+
+// 2^(top - 127 - shift), what sums of fp16 operands are multiplied by; top >= 1 and shift < 23, so
+// that it is subnormal at the least.
+__device__ __forceinline__ float top_unit(int top, int shift) {
+    const int e = top - shift;
+    return __uint_as_float(e > 0 ? static_cast<uint32_t>(e) << 23 : 1u << (22 + e));
 }
 
 // Columns [j, j + 32) of one row of out on a 32-byte boundary, `row` its first
@@ -322,9 +337,18 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 16; ++e) sum[p][e] = 0ull;
             uint32_t part = 0;
+            float unit[4] = {1.f, 1.f, 1.f, 1.f};
             for (int c0 = s0; c0 < s1; c0 += a.chain, ++done) {
                 const uint32_t buf = done & 1;
                 const bool last = c0 + a.chain >= s1;
+                if (a.top) {
+                    // on their way while the products go on
+                    const uint8_t *const top = a.top + static_cast<long long>(split * a.pieces + (c0 - s0) / a.chain) * a.groups;
+                    const int g = (tj * a.tile_k + first) / kCkptGroup;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (32 * p < width && g + p < a.groups) unit[p] = top_unit(top[g + p], a.shift);
+                }
                 ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, a.timeout_ns, a.status, SITE_DW_ACC_FULL);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -341,11 +365,15 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                             tmem_ld16_now(part + 32 * p + 16 * h, v);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                sum[p][8 * h + e] = add2(sum[p][8 * h + e], (static_cast<uint64_t>(v[2 * e + 1]) << 32) | v[2 * e]);
+                                sum[p][8 * h + e] = fma2((static_cast<uint64_t>(v[2 * e + 1]) << 32) | v[2 * e], splat2(unit[p]),
+                                                         sum[p][8 * h + e]);
                             if (last) tmem_st16(part + 32 * p + 16 * h, &sum[p][8 * h]);
                         }
                     }
                     if (last) tmem_st_wait();
+                    // the pieces' powers of two are in the sum
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) unit[p] = 1.f;
                 }
                 if (last) break;
                 tc_fence_before();
@@ -361,6 +389,11 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                 if (j >= a.k) break;
                 uint32_t v[32];
                 tmem_ld32_now(part + c, v);
+                if (a.top) {
+                    const float u = c == 0 ? unit[0] : c == 32 ? unit[1] : c == 64 ? unit[2] : unit[3];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * u);
+                }
                 if (a.wide) {
                     if (i < a.n) store_row(a, row, j, v);
                     continue;
@@ -509,6 +542,102 @@ cudaError_t launch_prepare(const PrepareArgs &a, int sms, bool pdl, cudaStream_t
                                static_cast<unsigned>(need < cap ? need : cap), 256, 0, pdl, s, a);
 }
 
+// The same with fp16 operands. A CTA takes the columns of one or two groups through the tokens of
+// one piece: the largest scale byte of either first (255, not a number, left out, 1 at least), while the
+// first codes are on their way, then x * 2^-(its k) * 2^shift, where the largest code is below
+// fp16's largest value: 448 * 2^7, 127 * 2^9. The CTAs past x's copy d_out.
+struct PieceArgs {
+    int steps, steps_per_split, chain, pieces;
+    int columns, column_blocks;     // of a CTA: 32 or 64; CTAs a piece
+    long long x_blocks;
+    uint8_t *top;
+    int shift, plain;               // plain: codes on boundaries of 8
+};
+constexpr int kPieceTokens = kStep * kChainF16;
+template <int FMT>
+__global__ void __launch_bounds__(256) dw_prepare_f16_kernel(const PrepareArgs a, const PieceArgs b) {
+    __shared__ uint8_t bytes[2 * kPieceTokens];
+    __shared__ uint32_t red[2][8];
+    griddep_wait();
+    if (blockIdx.x >= b.x_blocks) {
+        const long long per_d = (a.n + 7) / 8, total = a.T * per_d;
+        for (long long i = (blockIdx.x - b.x_blocks) * 256 + threadIdx.x; i < total; i += (gridDim.x - b.x_blocks) * 256) {
+            const long long t = i / per_d;
+            const int c = static_cast<int>(i - t * per_d) * 8;
+            const uintptr_t row = reinterpret_cast<uintptr_t>(a.d_out + t * a.d_stride);
+            uint64_t v[2];
+            load_words<2>(row + 2 * c, row + 2 * static_cast<uintptr_t>(a.n), v);
+            *reinterpret_cast<uint4 *>(a.d16 + t * a.d_pitch + c) =
+                make_uint4(static_cast<uint32_t>(v[0]), static_cast<uint32_t>(v[0] >> 32), static_cast<uint32_t>(v[1]),
+                           static_cast<uint32_t>(v[1] >> 32));
+        }
+        return;
+    }
+    const int piece = static_cast<int>(blockIdx.x / b.column_blocks), block = static_cast<int>(blockIdx.x - static_cast<long long>(piece) * b.column_blocks);
+    const int split = piece / b.pieces, s0 = split * b.steps_per_split + (piece - split * b.pieces) * b.chain;
+    const int s1 = min(min(s0 + b.chain, (split + 1) * b.steps_per_split), b.steps);
+    if (s0 >= s1) return;
+    const long long t0 = static_cast<long long>(s0) * kStep;
+    const int tokens = static_cast<int>((static_cast<long long>(s1) * kStep < a.T ? static_cast<long long>(s1) * kStep : a.T) - t0);
+    const int groups = (a.k + 31) / 32, g0 = block * (b.columns / 32), mine = min(b.columns / 32, groups - g0);
+    // a thread 8 columns of a token, `lanes` of them a token
+    const int lanes = b.columns / 8, rows = 256 / lanes, row0 = threadIdx.x / lanes, lane = threadIdx.x - row0 * lanes;
+    const int c = g0 * 32 + lane * 8, g = lane / 4;
+    auto load = [&](int first, uint2 (&w)[kRuns]) {
+#pragma unroll
+        for (int q = 0; q < kRuns; ++q) {
+            const int r = first + q * rows;
+            if (r >= tokens || c >= a.k) continue;
+            const uintptr_t row = reinterpret_cast<uintptr_t>(a.x.codes) + static_cast<uintptr_t>(t0 + r) * a.k;
+            if (b.plain) {
+                w[q] = *reinterpret_cast<const uint2 *>(row + c);
+            } else {
+                uint64_t v[1];
+                load_words<1>(row + c, row + a.k, v);
+                w[q] = make_uint2(static_cast<uint32_t>(v[0]), static_cast<uint32_t>(v[0] >> 32));
+            }
+        }
+    };
+    uint2 w[kRuns], next[kRuns];
+    load(row0, w);
+    uint32_t most[2] = {1u, 1u};
+    for (int i = threadIdx.x; i < tokens; i += 256) {
+        const uint8_t *const scales = a.x.scales + (t0 + i) * groups + g0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (e >= mine) break;
+            const uint32_t byte = scales[e];
+            bytes[2 * i + e] = static_cast<uint8_t>(byte);
+            if (byte != 255u) most[e] = max(most[e], byte);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        most[e] = __reduce_max_sync(0xffffffffu, most[e]);
+        if ((threadIdx.x & 31) == 0) red[e][threadIdx.x >> 5] = most[e];
+    }
+    __syncthreads();
+    uint32_t top = 1u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, red[g][i]);
+    if (row0 == 0 && lane % 4 == 0 && g < mine) b.top[static_cast<long long>(piece) * groups + g0 + g] = static_cast<uint8_t>(top);
+    const int add = b.shift + 127 - static_cast<int>(top);
+    for (int first = row0; first < tokens; first += kRuns * rows) {
+        load(first + kRuns * rows, next);
+#pragma unroll
+        for (int q = 0; q < kRuns; ++q) {
+            const int r = first + q * rows;
+            if (r < tokens && c < a.k) {
+                // the scale byte of 2^(k - top + shift): 0 stands for 0, below all that fp16 holds of a code
+                uint32_t byte = bytes[2 * r + g];
+                if (byte != 255u) byte = static_cast<uint32_t>(max(static_cast<int>(byte) + add, 0));
+                store8(reinterpret_cast<__half *>(a.x16 + (t0 + r) * a.x_pitch + c), ckpt_values8(w[q], byte, FMT));
+            }
+            w[q] = next[q];
+        }
+    }
+}
+
 std::atomic<int> g_dw_smem[64];
 
 long long pitch16(int w) { return (w + 7) / 8 * 8; }
@@ -517,7 +646,7 @@ size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 // How a call runs: the splits of the tokens and the workspace's parts.
 struct DwPlan {
     int tile_k, tiles_n, tiles_k, steps, splits, steps_per_split;
-    size_t x_bytes, d_bytes, part_bytes;
+    size_t x_bytes, d_bytes, part_bytes, top_bytes;
 };
 
 // Tiles of 128 columns where those of 256 would leave half of the pairs of CTAs
@@ -541,6 +670,7 @@ DwPlan dw_plan(long long T, int n, int k, bool d_aligned) {
     p.x_bytes = up256(static_cast<size_t>(T) * pitch16(k) * 2);
     p.d_bytes = d_aligned ? 0 : up256(static_cast<size_t>(T) * pitch16(n) * 2);
     p.part_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * n * k * 4 : 0;
+    p.top_bytes = static_cast<size_t>(p.splits) * ((p.steps_per_split + kChain32 - 1) / kChain32) * ckpt_groups(k);
     return p;
 }
 
@@ -554,7 +684,7 @@ bool dw_rows_aligned(const void *d_out, long long stride, long long T, int n) {
 size_t dw_workspace(long long T, int n, int k, bool d_aligned) {
     if (T == 0) return 0;
     const DwPlan p = dw_plan(T, n, k, d_aligned);
-    return p.x_bytes + p.d_bytes + p.part_bytes;
+    return p.x_bytes + p.d_bytes + p.part_bytes + p.top_bytes;
 }
 
 int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
@@ -571,10 +701,30 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     // a third faster where there is nothing but runs of 8 of the checkpoint
     const bool plain = d_aligned && a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x.codes) & 7u) == 0, e4m3 = a.format == MHC_CKPT_E4M3;
     const CkptArgs c = {nullptr, x16, xp, a.T, a.k, a.x};
-    auto prepare = a.dtype == MHC_BF16 ? (e4m3 ? launch_prepare<__nv_bfloat16, MHC_CKPT_E4M3> : launch_prepare<__nv_bfloat16, MHC_CKPT_INT8>)
-                                       : (e4m3 ? launch_prepare<__half, MHC_CKPT_E4M3> : launch_prepare<__half, MHC_CKPT_INT8>);
-    if (int e = note_launch(plain ? launch_ckpt_unpack(c, a.dtype, a.format, sms, pdl, s) : prepare(u, sms, pdl, s)))
-        return e;
+    PieceArgs b = {};
+    if (a.dtype == MHC_F16) {
+        b.steps = p.steps;
+        b.steps_per_split = p.steps_per_split;
+        b.chain = a.d_w_dtype == MHC_F32 ? kChain32 : kChainF16;
+        b.pieces = (p.steps_per_split + b.chain - 1) / b.chain;
+        b.top = ws + p.x_bytes + p.d_bytes + p.part_bytes;
+        b.shift = e4m3 ? 7 : 9;
+        b.plain = a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x.codes) & 7u) == 0;
+        // rows of 64 bytes where that leaves CTAs for every SM
+        const long long pieces = static_cast<long long>(p.splits) * b.pieces;
+        b.columns = pieces * ((a.k + 63) / 64) >= 2 * sms ? 64 : 32;
+        b.column_blocks = (a.k + b.columns - 1) / b.columns;
+        b.x_blocks = pieces * b.column_blocks;
+        const long long need = (a.T * ((u.n + 7) / 8) + 255) / 256, cap = static_cast<long long>(sms) * 8;
+        const unsigned grid = static_cast<unsigned>(b.x_blocks + (need < cap ? need : cap));
+        if (int e = note_launch(launch_block_kernel(e4m3 ? dw_prepare_f16_kernel<MHC_CKPT_E4M3> : dw_prepare_f16_kernel<MHC_CKPT_INT8>,
+                                                    grid, 256, 0, pdl, s, u, b)))
+            return e;
+    } else {
+        auto prepare = e4m3 ? launch_prepare<__nv_bfloat16, MHC_CKPT_E4M3> : launch_prepare<__nv_bfloat16, MHC_CKPT_INT8>;
+        if (int e = note_launch(plain ? launch_ckpt_unpack(c, a.dtype, a.format, sms, pdl, s) : prepare(u, sms, pdl, s)))
+            return e;
+    }
     CUtensorMap md, mx;
     if (!encode_rows16(&md, a.dtype == MHC_BF16, d_aligned ? a.d_out : d16, a.n, a.T, dp * 2, kStep) ||
         !encode_rows16(&mx, a.dtype == MHC_BF16, x16, a.k, a.T, xp * 2, kStep))
@@ -593,7 +743,11 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     g.out = p.splits > 1 ? static_cast<void *>(parts) : a.d_w;
     g.out_dtype = p.splits > 1 ? MHC_F32 : a.d_w_dtype;
     g.accumulate = p.splits > 1 ? 0 : a.accumulate;
-    g.chain = a.d_w_dtype == MHC_F32 ? kChain32 : kChain16;
+    g.chain = a.d_w_dtype == MHC_F32 ? kChain32 : g.f16 ? kChainF16 : kChain16;
+    g.top = b.top;
+    g.pieces = b.pieces;
+    g.groups = static_cast<int>(ckpt_groups(a.k));
+    g.shift = b.shift;
     g.wide = a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
     g.status = status;
     g.timeout_ns = wait_timeout_ns();

@@ -110,3 +110,46 @@ def test_finite_values_stay_finite_in_fp16(fmt, H):
     x[1, 0] = float("nan")
     got = ops.mhc_ckpt_unpack(ops.mhc_ckpt_pack(x, fmt), FP16)
     assert torch.isnan(got[1, :32]).all() and torch.isfinite(got[1, 32:]).all() and torch.isfinite(got[0]).all()
+
+
+@pytest.mark.parametrize("fmt,h", [("e4m3", 7), ("int8", 9)])
+@pytest.mark.parametrize("T,N,K,pad", [(70, 40, 96, 0), (333, 264, 200, 3), (1300, 136, 264, 0), (45, 31, 77, 1),
+                                       (2100, 2048, 1288, 0), (2100, 2048, 1288, 8), (1, 64, 64, 0), (40001, 24, 72, 0)])
+def test_fp16_weight_gradient_of_any_range(fmt, h, T, N, K, pad):
+    """x in fp16 shares a power of two in 32 columns, whose largest scale 2^k becomes 2^h there:
+    at the ends of fp16's range, past it and below it the products are what they are elsewhere.
+    What lies 2^(h + 24) below a column's scale is rounded, by 2^(k - h - 25) at most."""
+    g = torch.Generator(device="cuda").manual_seed(T + K)
+    d = (0.05 * torch.randn(T, N + pad, generator=g, device="cuda")).half()[:, :N]
+    x = torch.randn(T, K, generator=g, device="cuda")
+    top = x.clamp(-1, 1) * 65504
+    top[T // 2, 0], top[0, K - 1] = 65504.0, -65504.0
+    wide = x * torch.exp2(torch.randint(-100, 100, (1, K), generator=g, device="cuda").float())
+    loud = x * torch.exp2(torch.randint(-8, 12, (T, 1), generator=g, device="cuda").float())
+    for v in (top.half(), wide, loud.bfloat16(), x * 2.0 ** -60):
+        c = ops.mhc_ckpt_pack(v, fmt)
+        held = ref.unpack(c.codes, c.scales, fmt)
+        want = d.double().t() @ held
+        k = (c.scales.max(0).values.double() - 127).repeat_interleave(32)[:K]
+        for out in (FP32, BF):
+            err = (1.1 * T + 34) * 2.0 ** -23 * (d.double().abs().t() @ held.abs())
+            err = err + torch.exp2(k - h - 25) * d.double().abs().sum(0)[:, None]
+            bound = err + ref.half_step(out) * (want.abs() + err) + ref.tiny(out)
+            within(ops.mhc_ckpt_linear_dw(d, c, dtype=out), want, bound, "d_w")
+    w = torch.randn(N, K, generator=g, device="cuda")
+    c = ops.mhc_ckpt_pack(top, fmt)
+    held = ref.unpack(c.codes, c.scales, fmt)
+    want = d.double().t() @ held + w.double()
+    err = (1.1 * T + 36) * 2.0 ** -23 * (d.double().abs().t() @ held.abs() + w.double().abs())
+    within(ops.mhc_ckpt_linear_dw(d, c, d_w=w.clone(), accumulate=True), want, err, "d_w")
+
+
+def test_fp16_weight_gradient_of_a_group_that_is_not_a_number():
+    x = torch.randn(40, 96, device="cuda")
+    x[7, 40] = float("inf")                     # its group: columns 32 .. 63
+    d = torch.randn(40, 72, device="cuda").half()
+    got = ops.mhc_ckpt_linear_dw(d, ops.mhc_ckpt_pack(x))
+    assert torch.isnan(got[:, 32:64]).all() and torch.isfinite(got[:, :32]).all() and torch.isfinite(got[:, 64:]).all()
+    x[:, 32:64] = float("nan")                  # no scale at all in these columns
+    got = ops.mhc_ckpt_linear_dw(d, ops.mhc_ckpt_pack(x))
+    assert torch.isnan(got[:, 32:64]).all() and torch.isfinite(got[:, :32]).all() and torch.isfinite(got[:, 64:]).all()
