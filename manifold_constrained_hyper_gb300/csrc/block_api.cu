@@ -265,6 +265,12 @@ mhc_status mhc_block_norm_backward(const mhc_block *block, const void *d_residua
     }
     BlockSumArgs b = {};
     b.f = a.f;
+    if (T == 0) {
+        // zeros, whatever the weights and the gate hold: neither is read (a gate may be missing here)
+        b.f.gate_form = MHC_GATE_NONE;
+        b.f.gate = nullptr;
+        b.f.w_post = nullptr;
+    }
     b.sums = a.sums;
     b.scale_sums = a.scale_sums;
     b.parts = parts;

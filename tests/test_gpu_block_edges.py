@@ -153,3 +153,27 @@ def test_fp16_weight_gradient_of_a_group_that_is_not_a_number():
     x[:, 32:64] = float("nan")                  # no scale at all in these columns
     got = ops.mhc_ckpt_linear_dw(d, ops.mhc_ckpt_pack(x))
     assert torch.isnan(got[:, 32:64]).all() and torch.isfinite(got[:, :32]).all() and torch.isfinite(got[:, 64:]).all()
+
+
+# ------------------------------------------------------------------ one token, no tokens
+
+
+def test_no_tokens_read_nothing():
+    """Sums over no tokens are zeros whatever the weights and the gate hold, a gate that is
+    not there among them."""
+    from tests.test_block_cpu import _back, _block
+    H = 96
+    grads = {k: torch.full((H,), 7.0, device="cuda") for k in ("dw1", "dw2", "dg", "ds")}
+    w = torch.full((H,), float("nan"), device="cuda")
+    gate = torch.full((H,), float("inf"), device="cuda")
+    for g in (None, gate.data_ptr()):
+        for act in (0, 1):
+            for t in grads.values():
+                t.fill_(7.0)
+            b = _block(tokens=0, hidden=H, w_post=w.data_ptr(), w_pre=w.data_ptr(), gate=g, gate_act=act, res_scale=None)
+            torch.cuda.synchronize()
+            assert _back(ops.load(), b, dr=None, dh=None, y=None, r=None, rstd=None, dy=None, dres=None, ws=None, wsb=0,
+                         **{k: t.data_ptr() for k, t in grads.items()}) == 0
+            torch.cuda.synchronize()
+            for k, t in grads.items():
+                assert (t == 0).all(), (k, g, act)
