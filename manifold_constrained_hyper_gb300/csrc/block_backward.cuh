@@ -98,6 +98,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
         abort_flag = 0;
         fence_mbar_init();
     }
+    if (STAGED)
+        for (int s = threadIdx.x; s < ring.stages; s += blockDim.x) {
+            uint8_t *place = smem + s * ring.stage_bytes;
+#pragma unroll
+            for (int k = 0; k < 5; ++k) {
+                zero_place_end(place, ring.place[k], MODE != ROWS_RING);
+                place += ring.place[k];
+            }
+        }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -229,8 +238,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
             const uint8_t *const byte_at = STAGED ? st[k_scales] + skew16(scales) : scales;
             if constexpr (MODE != ROWS_ANY) {
                 const int i = run_read_col(at, j);
-                return ckpt_values8(*reinterpret_cast<const uint2 *>((STAGED ? st[k] + skew16(codes) : codes) + i), byte_at[i / 32],
-                                    a.format);
+                uint2 w = *reinterpret_cast<const uint2 *>((STAGED ? st[k] + skew16(codes) : codes) + i);
+                if (!run_in<MODE>(at, j)) w = make_uint2(0u, 0u);
+                return ckpt_values8(w, byte_at[i / 32], a.format);
             } else {
                 const int col = run_col<MODE>(at, j);
                 const uint8_t *const code_at = st[k] + skew16(codes);
@@ -238,9 +248,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int i = min(col + e * at.threads, H - 1);
-                    v[e] = (a.format == MHC_CKPT_E4M3 ? ckpt_value<MHC_CKPT_E4M3>(code_at[i])
+                    const float x = (a.format == MHC_CKPT_E4M3 ? ckpt_value<MHC_CKPT_E4M3>(code_at[i])
                                                       : ckpt_value<MHC_CKPT_INT8>(code_at[i])) *
                            ckpt_unit(byte_at[i / 32]);
+                    v[e] = col + e * at.threads < H ? x : 0.f;
                 }
                 return run_of(v);
             }
@@ -306,10 +317,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) block_bwd_kernel(const BlockBw
                 sum2.p[i] = fma2(mul2(dh.p[i], r2), ro.p[i], sum2.p[i]);
                 const uint64_t dv = mul2(dh.p[i], w2.p[i]);
                 ev[j].p[i] = fma2(r2, dv, ev[j].p[i]);
-                s0 = fma2(dv, ro.p[i], s0);
-                s1 = fma2(y.p[i], ev[j].p[i], s1);
-                s2 = fma2(y.p[i], ro.p[i], s2);
+                if (MODE != ROWS_VEC || run_in<MODE>(at, j)) {
+                    s0 = fma2(dv, ro.p[i], s0);
+                    s1 = fma2(y.p[i], ev[j].p[i], s1);
+                    s2 = fma2(y.p[i], ro.p[i], s2);
+                }
             }
+            if (MODE == ROWS_VEC) __syncwarp();
             tmem_run_store(cell(T_DW2, j), sum2);
         }
         float sum[3] = {f2_lo(s0) + f2_hi(s0), f2_lo(s1) + f2_hi(s1), f2_lo(s2) + f2_hi(s2)};

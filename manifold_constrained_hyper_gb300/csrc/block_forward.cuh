@@ -39,6 +39,7 @@ struct FwdRing {
     int groups;                                     // of a CTA, blockDim.x / groups threads each
     int stages;
     uint32_t y_place, r_place, g_place;             // bytes of a row's place in a stage; g_place 0: no full gate
+    uint32_t row_bytes;                             // of its copies, in ROWS_RING
     unsigned int *status;
     unsigned long long timeout_ns;
 };
@@ -50,6 +51,9 @@ template <class TY, class TR, int MODE, int RUNS, bool FULL, bool SCALED, bool C
 __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(const BlockFwdArgs a, const FwdRing ring) {
     constexpr int MAXW = 32 / RUNS, GROUPS = RUNS == 1 ? 32 : kFwdGroups;
     constexpr bool STAGED = MODE != ROWS_VEC;
+    // past the row's end its last run again, left out of the sums, instead of zeros: from global memory, and
+    // where the zeros' place takes registers that are not there (8192 x 7168 with int8 checkpoints: spills, 10 us)
+    constexpr bool GUARD = MODE == ROWS_VEC || (CKPT && RUNS == 4);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float red[GROUPS][2][MAXW];
     __shared__ __align__(8) uint64_t bars[kFwdStages];
@@ -86,6 +90,13 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         abort_flag = 0;
         fence_mbar_init();
     }
+    if (STAGED && !GUARD)
+        for (int s = threadIdx.x; s < ring.stages; s += blockDim.x) {
+            uint8_t *const place = smem + stage0 + s * stage_bytes;
+            zero_place_end(place, ring.y_place, MODE != ROWS_RING);
+            zero_place_end(place + ring.y_place, ring.r_place, MODE != ROWS_RING);
+            zero_place_end(place + ring.y_place + ring.r_place, ring.g_place, MODE != ROWS_RING);
+        }
     __syncthreads();
     griddep_wait();
     // The CTA's rows are blockIdx.x + k gridDim.x, k = 0, 1, ...: group k mod
@@ -97,7 +108,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         const TR *const r = static_cast<const TR *>(a.residual) + t * a.r_stride;
         const uint8_t *const g = static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge;
         if (MODE == ROWS_RING) {
-            stage_arm(&armed[s], filling, b, stage_bytes);
+            stage_arm(&armed[s], filling, b, ring.row_bytes);
             bulk_load(dst, y, y_bytes, b, pol);
             bulk_load(dst + ring.y_place, r, r_bytes, b, pol);
             if (FULL && ring.g_place) bulk_load(dst + ring.y_place + ring.r_place, g, g_bytes, b, pol);
@@ -142,14 +153,14 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         const TR *const r_row = static_cast<const TR *>(a.residual) + t * a.r_stride;
         const uint8_t *const g_row = static_cast<const uint8_t *>(f.gate) + t * f.gate_stride * ge;
         auto load_y = [&](int j) {
-            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TY *>(st), at, j);
+            if constexpr (MODE == ROWS_RING) return staged_run<GUARD>(reinterpret_cast<const TY *>(st), at, j);
             else if constexpr (MODE == ROWS_VEC) return load_run(y_row, at, j);
             else if constexpr (MODE == ROWS_SKEW) return staged_skewed<TY>(st, skew16(y_row), at, j);
             else return staged_single(reinterpret_cast<const TY *>(st + skew16(y_row)), at, j);
         };
         auto load_r = [&](int j) {
             const uint8_t *const row = st + ring.y_place;
-            if constexpr (MODE == ROWS_RING) return staged_run(reinterpret_cast<const TR *>(row), at, j);
+            if constexpr (MODE == ROWS_RING) return staged_run<GUARD>(reinterpret_cast<const TR *>(row), at, j);
             else if constexpr (MODE == ROWS_VEC) return load_run(r_row, at, j);
             else if constexpr (MODE == ROWS_SKEW) return staged_skewed<TR>(row, skew16(r_row), at, j);
             else return staged_single(reinterpret_cast<const TR *>(row + skew16(r_row)), at, j);
@@ -174,12 +185,9 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
         }
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
-            // past the row's end stands its last run, or element, again: not in the sums
-            const bool in = run_col<MODE>(at, j) < f.H;
-            if (in) {
-                const Run v = MODE == ROWS_ANY ? run_within<MODE>(y[j], at, j) : y[j];
+            if (!GUARD || run_in<MODE>(at, j)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s2 = fma2(v.p[i], v.p[i], s2);
+                for (int i = 0; i < 4; ++i) s2 = fma2(y[j].p[i], y[j].p[i], s2);
             }
             if (CKPT && a.ck_y.codes) store_ckpt<MODE>(a.ck_y, a.format, t, at, j, y[j]);
             if (CKPT && a.ck_r.codes) store_ckpt<MODE>(a.ck_r, a.format, t, at, j, v[j]);
@@ -198,7 +206,7 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
                 for (int i = 0; i < 4; ++i) v[j].p[i] = mul2(v[j].p[i], sc.p[i]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[j].p[i] = mul2(v[j].p[i], in ? scale : 0ull);
+                for (int i = 0; i < 4; ++i) v[j].p[i] = mul2(v[j].p[i], scale);
             }
         }
         float rstd1 = 1.f, sum[1];
@@ -230,9 +238,10 @@ __global__ void __launch_bounds__(RUNS == 1 ? 1024 : 512, 1) block_fwd_kernel(co
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[j].p[i] = fma2(y[j].p[i], tr2, v[j].p[i]);
-                s2 = fma2(v[j].p[i], v[j].p[i], s2);
+            for (int i = 0; i < 4; ++i) v[j].p[i] = fma2(y[j].p[i], tr2, v[j].p[i]);
+            if (!GUARD || run_in<MODE>(at, j)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s2 = fma2(v[j].p[i], v[j].p[i], s2);
             }
             store_run<MODE>(static_cast<TR *>(a.residual_out) + t * f.H, at, j, v[j]);
         }
@@ -325,6 +334,7 @@ cudaError_t block_fwd(const BlockFwdArgs &a, int dtype, int r_dtype, int sms, bo
     ring.y_place = row_place(f.H, sizeof(TY), !vec);
     ring.r_place = row_place(f.H, sizeof(TR), !vec);
     ring.g_place = full ? row_place(f.H, elem_bytes(f.gate_dtype), !vec) : 0;
+    ring.row_bytes = static_cast<uint32_t>(f.H) * (sizeof(TY) + sizeof(TR) + (full ? elem_bytes(f.gate_dtype) : 0));
     // a stage for each group and one to fill meanwhile, or all of the rows; with the widest types (96 KB a
     // row of 8192) one stage and one group
     const size_t bytes = ring.y_place + ring.r_place + ring.g_place;

@@ -26,13 +26,17 @@ template <int MODE>
 __device__ __forceinline__ int run_col(const Place &p, int j) {
     return MODE == ROWS_ANY ? j * 8 * p.threads + p.thread : (j * p.threads + p.thread) * 8;
 }
-// Where run j of vector loads is read: past the row's end its last run again,
-// so that no load needs a guard. Of a checkpoint's group that the row's end
-// cuts, this is the same group, whose maximum it leaves as it is.
+// Past a row's end a staged thread reads zeros that lie behind it: no load needs a guard, and the row's
+// sums and a checkpoint's group that the end cuts are what they are without them. (The row's last run again,
+// times a weight of 0, would be NaN of an infinity there, and through the sums the whole row.) From global
+// memory it reads the last run again, which run_in leaves out of the sums and run_within of parameters. A
+// group that the end cuts is the last run's own, whose maximum that leaves as it is.
 __device__ __forceinline__ int run_read_col(const Place &p, int j) {
     const int c = run_col<ROWS_VEC>(p, j);
     return c < p.H ? c : p.H - 8;
 }
+template <int MODE>
+__device__ __forceinline__ bool run_in(const Place &p, int j) { return run_col<MODE>(p, j) < p.H; }
 // Run j of a row in global memory, and of a type known at run time.
 template <class T>
 __device__ __forceinline__ Run load_run(const T *row, const Place &p, int j) {
@@ -54,24 +58,35 @@ __device__ __forceinline__ void store_run(T *row, const Place &p, int j, const R
             if (c + e * p.threads < p.H) row[c + e * p.threads] = from_f32<T>(run_at(r, e));
     }
 }
-// Run j of a row staged in shared memory.
-template <class T>
+// Zeros at the end of a row's place in a stage (zero_place_end), which no copy reaches: behind a row that
+// begins where its place does, those of one run; on any boundary kPlaceEnd bytes.
+constexpr int kRunEnd = 32, kPlaceEnd = 64;
+// Run j of a row staged in shared memory; AGAIN: past the row's end its last run.
+template <bool AGAIN = false, class T>
 __device__ __forceinline__ Run staged_run(const T *row, const Place &p, int j) {
-    return load8_shared(row + run_read_col(p, j));
+    return load8_shared(row + (AGAIN ? run_read_col(p, j) : min(run_col<ROWS_RING>(p, j), p.H)));
 }
-// The same `skew` bytes into its place.
+// The same `skew` bytes into its place; what it reads past the row's end begins 16 bytes (32 of fp32) on.
 template <class T>
 __device__ __forceinline__ Run staged_skewed(const uint8_t *place, uint32_t skew, const Place &p, int j) {
-    return load8_skewed(reinterpret_cast<const uint4 *>(place + run_read_col(p, j) * sizeof(T)), skew, static_cast<const T *>(nullptr));
+    const int c = run_col<ROWS_SKEW>(p, j);
+    return load8_skewed(reinterpret_cast<const uint4 *>(place + (c < p.H ? c : p.H + 8) * sizeof(T)), skew, static_cast<const T *>(nullptr));
 }
-// The same on any boundary, single elements; past the row's end stands its last one again.
+// The same on any boundary, single elements: one element of the zeros for every row, however skewed, and
+// every type, so that one index serves all of a row's tensors.
 template <class T>
 __device__ __forceinline__ Run staged_single(const T *row, const Place &p, int j) {
-    const int c = run_col<ROWS_ANY>(p, j);
+    const int c = run_col<ROWS_ANY>(p, j), zero = (2 * p.H + 30) / 16 * 8;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = to_f32(row[min(c + e * p.threads, p.H - 1)]);
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(row[c + e * p.threads < p.H ? c + e * p.threads : zero]);
     return run_of(v);
+}
+__device__ __forceinline__ void zero_place_end(uint8_t *place, uint32_t bytes, bool any) {
+    if (!bytes) return;
+#pragma unroll
+    for (int i = 16; i <= kPlaceEnd; i += 16)
+        if (any || i <= kRunEnd) *reinterpret_cast<uint4 *>(place + bytes - i) = make_uint4(0u, 0u, 0u, 0u);
 }
 // A run with what lies past the row's end set to 0.
 template <int MODE>
@@ -94,10 +109,14 @@ __device__ __forceinline__ uint32_t skewed_bytes(const void *p, uint32_t bytes) 
 __device__ __forceinline__ void bulk_load_row(uint32_t dst, const void *p, uint32_t bytes, uint32_t bar, uint64_t policy) {
     bulk_load(dst, static_cast<const uint8_t *>(p) - skew16(p), skewed_bytes(p, bytes), bar, policy);
 }
-// A row's place in a stage; on any boundary with the 16 bytes past it that runs of 8 may read.
+// A row's place in a stage. On any boundary copies write (bytes + 30) / 16 * 16 at most, and the zeros
+// follow. Single elements: element (2 H + 30) / 16 * 8 of a row up to 14 (or 12) bytes into its place lies
+// in them whole: of 2 bytes it begins where they do or up to 14 bytes on, of 4 between 4 H + 30 and 4 H + 72,
+// and they reach from 4 H + 30 at most to 4 H + 79 at least. Runs of 8 (H a multiple of 8): those from
+// element H + 8 on, 32 bytes or 48, begin there or 16 bytes on.
 inline uint32_t row_place(int H, int elem, bool any) {
     const uint32_t bytes = static_cast<uint32_t>(H) * elem;
-    return any ? (bytes + 15 + 15) / 16 * 16 + 16 : bytes;
+    return any ? (bytes + 15 + 15) / 16 * 16 + kPlaceEnd : bytes + kRunEnd;
 }
 __device__ __forceinline__ Run staged_run_any(const void *row, int dtype, const Place &p, int j) {
     if (dtype == MHC_F32) return staged_run(static_cast<const float *>(row), p, j);

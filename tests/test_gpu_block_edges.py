@@ -155,6 +155,78 @@ def test_fp16_weight_gradient_of_a_group_that_is_not_a_number():
     assert torch.isnan(got[:, 32:64]).all() and torch.isfinite(got[:, :32]).all() and torch.isfinite(got[:, 64:]).all()
 
 
+# ------------------------------------------------------------------ infinities
+
+ROWS = [(6, 264, 0), (400, 1032, 0), (400, 1032, 3), (6, 77, 0), (400, 333, 0), (4, 8200, 0), (4, 8203, 0), (400, 72, 0)]
+
+
+def _same_kind(got, want, what):
+    """NaN and the infinities where they are in `want`, which is in 64 bits."""
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+    inf = torch.isinf(want)
+    assert torch.equal(torch.isinf(got), inf), what
+    assert torch.equal(got.double()[inf], want[inf]), what
+
+
+@pytest.mark.parametrize("T,H,pad", ROWS)
+@pytest.mark.parametrize("types", ["bf16", "fp32"])
+@pytest.mark.parametrize("post_norm", [True, False])
+@pytest.mark.parametrize("held", [False, True])
+def test_an_infinity_does_the_same_in_every_column(T, H, pad, types, post_norm, held):
+    for name, gate, scale in (("residual", "none", "none"), ("residual", "full", "channel"), ("y", "channel", "one")):
+        x, _, form = make(T, H, types, gate, "none", scale, pad)
+        if gate == "channel":
+            x["gate"] = x["gate"].abs() + 0.5
+        for i, c in enumerate((0, H // 2, H - 9, H - 1)):
+            x[name][i % T, c] = float("inf")
+        if not post_norm:
+            x["w_post"] = None
+        kw = {"ckpt_h": ops.ckpt_empty(T, H, "int8")} if held else {}
+        ro, h, rstd = ops.mhc_block_norm(x["y"], x["residual"], x["w_post"], x["w_pre"], x["gate"], x["res_scale"],
+                                         params(post_norm=post_norm), **kw)
+        f = ref.block(**x, post_norm=post_norm)
+        _same_kind(ro, f["ro"], (name, "residual_out"))
+        _same_kind(rstd, f["rstd"], (name, "rstd"))
+        _same_kind(h, f["h"], (name, "h"))
+        bad = ~torch.isfinite(f["ro"]).all(1)
+        assert (h[bad][torch.isfinite(h[bad])] == 0).all()
+        if held:
+            codes, scales = ref.pack(h, "int8")
+            assert torch.equal(kw["ckpt_h"].scales, scales) and torch.equal(kw["ckpt_h"].codes, codes)
+
+
+@pytest.mark.parametrize("T,H,pad", ROWS)
+@pytest.mark.parametrize("types", ["bf16", "fp32"])
+@pytest.mark.parametrize("gate,scale,held", [("none", "none", False), ("full", "channel", False), ("full", "one", False),
+                                             ("token", "channel", True), ("none", "one", True)])
+def test_a_gradient_s_infinity_does_the_same_in_every_column(T, H, pad, types, gate, scale, held):
+    """An infinite gradient of residual_out leaves its row's other d_residual alone and makes
+    d_y infinite; one of h makes the row's d_residual infinite."""
+    for name, which in (("d_ro", ("d_residual", "d_y")), ("d_h", ("d_residual",))):
+        x, d, form = make(T, H, types, gate, "none" if gate == "none" else "sigmoid", scale, pad)
+        p = params(form["act"])
+        rstd = ops.mhc_block_norm(x["y"], x["residual"], x["w_post"], x["w_pre"], x["gate"], x["res_scale"], p)[2]
+        for i, c in enumerate((0, H // 2, H - 9, H - 1)):
+            # nothing else in this row's sum is infinite, and nothing at its place is zero
+            x["y"][i % T, c], x["residual"][i % T, c], x["w_post"][c], x["w_pre"][c] = 1.0, 1.0, 1.0, 1.0
+            if gate == "full":
+                x["gate"][i % T, c] = 1.0
+            d[name][i % T, c] = float("inf")
+        y, r, values = x["y"], x["residual"], {}
+        if held:
+            y, r = ops.mhc_ckpt_pack(y, "int8"), ops.mhc_ckpt_pack(r, "int8")
+            values = {"y": ref.unpack(y.codes, y.scales, "int8"), "residual": ref.unpack(r.codes, r.scales, "int8")}
+        f = ref.block(**{**x, **values}, gate_act=form["act"])
+        f["n"] = f["y"] * rstd[:, :1].double() * f["w1"]
+        f["ro"] = f["a"] * f["r"] + f["g"] * f["n"]
+        want, _ = ref.backward(f, d["d_ro"], d["d_h"], rstd, gate, scale, form["act"])
+        got = ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], y, r, rstd, x["w_post"], x["w_pre"], x["gate"],
+                                          x["res_scale"], p)
+        for k in which:
+            # a checkpoint's zero times an infinity is NaN in both
+            _same_kind(getattr(got, k), want[k], (name, k))
+
+
 # ------------------------------------------------------------------ one token, no tokens
 
 
