@@ -338,7 +338,7 @@ typedef struct {
 /*
  * The block boundary above. y, residual: inputs. residual_out [T, H] of
  * residual_dtype (may be exactly the residual buffer when residual_stride is
- * H) and h [T, H] of dtype: outputs, contiguous. rstd: [T, 2] fp32 (rstd_post,
+ * H or there is one token) and h [T, H] of dtype: outputs, contiguous. rstd: [T, 2] fp32 (rstd_post,
  * rstd_pre), what the backward pass needs beside y and residual, or NULL.
  * ckpt_y, ckpt_residual, ckpt_h: each NULL or a checkpoint to write of the
  * inputs y and residual and of the rounded h, in the same pass.
@@ -365,7 +365,7 @@ size_t mhc_block_norm_backward_workspace_bytes(int64_t tokens, int hidden);
  *   d_w_post   = sum_t g*D*y*rstd_post     d_w_pre = sum_t d_h*ro*rstd_pre
  *   d_gate     = act'(gate) * n * D, summed over what the gate is shared by
  * Outputs: d_y [T, H] of dtype, d_residual [T, H] of residual_dtype (may be
- * exactly the d_residual_out buffer when its stride is H), both contiguous;
+ * exactly the d_residual_out buffer when its stride is H or T is 1), both contiguous;
  * d_w_post, d_w_pre [H] fp32; d_gate [H] fp32 (CHANNEL), [T] fp32 (TOKEN) or
  * [T, H] of gate_dtype (FULL); d_res_scale [1] or [H] fp32. Any of the last
  * four may be NULL where it is not wanted, and must be where there is no such

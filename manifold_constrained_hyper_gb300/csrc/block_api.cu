@@ -158,7 +158,8 @@ mhc_status mhc_block_norm(const mhc_block *block, const void *y, int64_t y_strid
                          codes_span(ckpt_y, T, H), scales_span(ckpt_y, T, H),
                          codes_span(ckpt_residual, T, H), scales_span(ckpt_residual, T, H),
                          codes_span(ckpt_h, T, H), scales_span(ckpt_h, T, H)};
-    if (aliased(outs, 9, ins, 6, residual_stride == H ? 0 : -1, 1)) return MHC_ERR_ALIAS;
+    // one row has no stride
+    if (aliased(outs, 9, ins, 6, T == 1 || residual_stride == H ? 0 : -1, 1)) return MHC_ERR_ALIAS;
     int sms = 0;
     if (int s = require_device(&sms, nullptr)) return static_cast<mhc_status>(s);
     a.y = y;
@@ -233,7 +234,7 @@ mhc_status mhc_block_norm_backward(const mhc_block *block, const void *d_residua
                              {d_w_pre, d_w_pre ? nh : 0}, {d_gate, d_gate ? ng : 0},
                              {d_res_scale, d_res_scale ? (block->scale_form == MHC_SCALE_CHANNEL ? nh : 4) : 0},
                              {workspace, need}};
-        if (aliased(outs, 7, ins, 13, d_residual_out_stride == H ? 0 : -1, 0)) return MHC_ERR_ALIAS;
+        if (aliased(outs, 7, ins, 13, T == 1 || d_residual_out_stride == H ? 0 : -1, 0)) return MHC_ERR_ALIAS;
     }
     int sms = 0;
     if (int s = require_device(&sms, nullptr)) return static_cast<mhc_status>(s);

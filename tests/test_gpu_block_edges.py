@@ -230,6 +230,29 @@ def test_a_gradient_s_infinity_does_the_same_in_every_column(T, H, pad, types, g
 # ------------------------------------------------------------------ one token, no tokens
 
 
+@pytest.mark.parametrize("H", [512, 77])
+def test_one_token_in_place_in_wider_rows(H):
+    """One row has no stride: a slice of wider rows is updated where it lies."""
+    for types in ("bf16", "bf16+"):
+        x, d, form = make(1, H, types, "token", "sigmoid", "channel")
+        p = params("sigmoid")
+        args = (x["w_post"], x["w_pre"], x["gate"], x["res_scale"], p)
+        want = ops.mhc_block_norm(x["y"], x["residual"], *args)
+        wide = torch.zeros(3, H + 24, dtype=x["residual"].dtype, device="cuda")
+        r = wide[:1, :H]
+        r.copy_(x["residual"])
+        got = ops.mhc_block_norm(x["y"], r, *args, residual_out=r)
+        assert got[0] is r and all(torch.equal(a, b) for a, b in zip(want, got))
+        gw = ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], want[2], *args)
+        dr = wide[1:2, :H]
+        dr.copy_(d["d_ro"])
+        gg = ops.mhc_block_norm_backward(dr, d["d_h"], x["y"], x["residual"], want[2], *args, d_residual=dr)
+        assert all(torch.equal(a, b) for a, b in zip(gw, gg))
+        assert (wide[2] == 0).all() and (wide[:2, H:] == 0).all()
+    with pytest.raises(ops.MhcError, match="ALIAS"):
+        ops.mhc_block_norm(x["y"], wide[:1, :H], *args, residual_out=wide[:1, 4:H + 4])
+
+
 def test_no_tokens_read_nothing():
     """Sums over no tokens are zeros whatever the weights and the gate hold, a gate that is
     not there among them."""
