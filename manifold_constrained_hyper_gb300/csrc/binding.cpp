@@ -163,6 +163,14 @@ Held held(PyObject *codes, PyObject *scales, const char *name, const Shape &s) {
     return h;
 }
 
+// A workspace argument; undefined for None. Its address goes to the kernels as it is.
+at::Tensor scratch(PyObject *o, c10::Device device) {
+    at::Tensor t = tensor(o, "workspace", true);
+    if (t.defined() && (t.device() != device || !t.is_contiguous()))
+        throw Refused{"workspace must be a contiguous tensor on " + device.str() + ": got " + str(t)};
+    return t;
+}
+
 double number(PyObject *o, PyObject *name) {
     PyObject *v = PyObject_GetAttr(o, name);
     const double d = v ? PyFloat_AsDouble(v) : -1.0;
@@ -351,7 +359,7 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const long format = PyLong_AsLong(a[14]);
         const Held cy = held(a[15], a[16], "y", s), cr = held(a[17], a[18], "residual", s);
         const c10::cuda::CUDAGuard guard(s.device);
-        at::Tensor d_y, d_residual, d_w_post, d_w_pre, d_gate, d_scale, workspace = tensor(a[13], "workspace", true), same;
+        at::Tensor d_y, d_residual, d_w_post, d_w_pre, d_gate, d_scale, workspace = scratch(a[13], s.device), same;
         NewTensors fresh_ones(s.device);
         fresh_ones.add_or(&same, rstd, "rstd", {s.T, 2}, at::kFloat);
         fresh_ones.add_or(&d_y, tensor(a[11], "d_y", true), "d_y", {s.T, s.H}, t);
@@ -449,7 +457,7 @@ PyObject *ckpt_linear_dw(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const long format = PyLong_AsLong(a[3]), type = PyLong_AsLong(a[5]);
         const c10::cuda::CUDAGuard guard(s.device);
         const int N = s.H > INT32_MAX ? INT32_MAX : static_cast<int>(s.H), k = K > INT32_MAX ? INT32_MAX : static_cast<int>(K);
-        at::Tensor d_w, workspace = tensor(a[7], "workspace", true);
+        at::Tensor d_w, workspace = scratch(a[7], s.device);
         NewTensors fresh_ones(s.device);
         fresh_ones.add_or(&d_w, tensor(a[4], "d_w", true), "d_w", {s.H, K}, scalar_of(type));
         if (!workspace.defined()) {

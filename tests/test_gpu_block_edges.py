@@ -272,3 +272,25 @@ def test_no_tokens_read_nothing():
             torch.cuda.synchronize()
             for k, t in grads.items():
                 assert (t == 0).all(), (k, g, act)
+
+
+# ------------------------------------------------------------------ what the binding gives and takes
+
+
+def test_a_workspace_is_device_bytes():
+    """Refused before anything is launched: the workspace's address goes to the kernels."""
+    x, d, form = make(4, 64, "bf16", "none", "none", "none")
+    rstd = torch.ones(4, 2, device="cuda")
+    n = ops.block_norm_backward_workspace_bytes(4, 64)
+    c = ops.mhc_ckpt_pack(x["y"])
+    m = ops.ckpt_linear_dw_workspace_bytes(4, 64, 64)
+    for bad in (lambda k: torch.empty(k, dtype=torch.uint8), lambda k: torch.empty(2 * k, dtype=torch.uint8, device="cuda")[::2],
+                lambda k: torch.empty(k, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], rstd, workspace=bad(n))
+        with pytest.raises(ValueError, match="workspace"):
+            ops.mhc_ckpt_linear_dw(d["d_h"], c, workspace=bad(m))
+    want = ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], rstd)
+    got = ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], rstd,
+                                      workspace=torch.empty(n // 4 + 1, device="cuda"))
+    assert torch.equal(want.d_y, got.d_y)
