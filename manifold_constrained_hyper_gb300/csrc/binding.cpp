@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -171,6 +172,14 @@ at::Tensor scratch(PyObject *o, c10::Device device) {
     return t;
 }
 
+// Nothing here records a history: outputs of tensors whose gradients are being recorded would end
+// them without a word.
+void no_history(const at::Tensor &t, const char *name, const char *call) {
+    if (t.defined() && t.requires_grad() && c10::GradMode::is_enabled())
+        throw Refused{std::string(name) + " requires grad, and " + call + " records no history: call it under "
+                      "torch.no_grad(), or both directions in a torch.autograd.Function"};
+}
+
 double number(PyObject *o, PyObject *name) {
     PyObject *v = PyObject_GetAttr(o, name);
     const double d = v ? PyFloat_AsDouble(v) : -1.0;
@@ -315,6 +324,12 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor y = tensor(a[0], "y"), residual = tensor(a[1], "residual"), w_post = tensor(a[2], "w_post", true),
                          w_pre = tensor(a[3], "w_pre", true), gate = tensor(a[4], "gate", true),
                          res_scale = tensor(a[5], "res_scale", true);
+        no_history(y, "y", "mhc_block_norm");
+        no_history(residual, "residual", "mhc_block_norm");
+        no_history(w_post, "w_post", "mhc_block_norm");
+        no_history(w_pre, "w_pre", "mhc_block_norm");
+        no_history(gate, "gate", "mhc_block_norm");
+        no_history(res_scale, "res_scale", "mhc_block_norm");
         const Shape s = shape_2d(y, "y");
         const at::ScalarType t = y.scalar_type(), rt = residual.scalar_type();
         const int64_t ys = rows(y, "y", s, t), rs = rows(residual, "residual", s, rt);
@@ -347,6 +362,8 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                          w_post = tensor(a[5], "w_post", true), w_pre = tensor(a[6], "w_pre", true),
                          gate = tensor(a[7], "gate", true), res_scale = tensor(a[8], "res_scale", true),
                          typed = tensor(a[10], "residual_dtype", true);
+        no_history(d_ro, "d_residual_out", "mhc_block_norm_backward");
+        no_history(d_h, "d_h", "mhc_block_norm_backward");
         const Shape s = shape_2d(d_h, "d_h");
         const at::ScalarType t = d_h.scalar_type();
         const at::ScalarType rt = typed.defined() ? typed.scalar_type() : d_ro.defined() ? d_ro.scalar_type()
@@ -446,6 +463,7 @@ PyObject *ckpt_unpack(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *ckpt_linear_dw(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject * {
         const at::Tensor d_out = tensor(a[0], "d_out"), codes = tensor(a[1], "x");
+        no_history(d_out, "d_out", "mhc_ckpt_linear_dw");
         const Shape s = shape_2d(d_out, "d_out");
         const at::ScalarType t = d_out.scalar_type();
         if (t != at::kBFloat16 && t != at::kHalf)

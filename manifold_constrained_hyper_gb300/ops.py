@@ -557,7 +557,9 @@ def mhc_block_norm(y, residual, w_post=None, w_pre=None, gate=None, res_scale=No
     None. ckpt_y, ckpt_residual and ckpt_h are checkpoints to write of y,
     residual and h in the same pass. Returns (residual_out, h, rstd), rstd
     [T, 2] being what mhc_block_norm_backward needs beside y and residual.
-    residual_out may be the residual itself."""
+    residual_out may be the residual itself. No history is recorded: while
+    gradients are, tensors that require them are refused (wrap the two
+    directions in a torch.autograd.Function, or call under no_grad)."""
     f = (_fast or load_binding()).block_norm
     p = _DEFAULT_BLOCK_PARAMS if params is None else params
     if ckpt_y is None and ckpt_residual is None and ckpt_h is None:
@@ -582,7 +584,9 @@ def mhc_block_norm_backward(d_residual_out, d_h, y, residual, rstd, w_post=None,
     residual_dtype (d_residual_out's, else the residual's, else d_h's, unless
     given) is needed only where none of them tells it. The gradients of
     weights, of a [H] or [T, 1] gate and of res_scale are float32 (always parts
-    of one allocation); d_residual may be d_residual_out itself."""
+    of one allocation); d_residual may be d_residual_out itself. Not
+    differentiable itself: gradients of outputs that require grad are refused
+    while gradients are recorded."""
     f = (_fast or load_binding()).block_norm_backward
     p = _DEFAULT_BLOCK_PARAMS if params is None else params
     typed = None if residual_dtype is None else torch.empty(0, dtype=residual_dtype)
@@ -598,7 +602,8 @@ def mhc_block_norm_backward(d_residual_out, d_h, y, residual, rstd, w_post=None,
 
 
 def mhc_ckpt_pack(x, fmt: str = "e4m3", *, out: Checkpoint | None = None, stream=None) -> Checkpoint:
-    """x [T, H] (float32, bfloat16 or float16, rows may be strided) kept in 8 bits."""
+    """x [T, H] (float32, bfloat16 or float16, rows may be strided) kept in 8 bits:
+    its values, as of a detached tensor."""
     f = (_fast or load_binding()).ckpt_pack
     if out is None:
         return _held(*_at(stream, f, x, _format_number(fmt), None, None), fmt)
@@ -631,7 +636,8 @@ def mhc_ckpt_linear_dw(d_out, x: Checkpoint, *, d_w=None, dtype=torch.float32,
                        accumulate: bool = False, workspace=None, stream=None):
     """d_w [N, K] = d_out^T x, the weight gradient of out = x W^T, from d_out
     [T, N] (bfloat16 or float16, rows may be strided) and the checkpoint of
-    x [T, K]. accumulate adds to the d_w given."""
+    x [T, K]. accumulate adds to the d_w given. A d_out that requires grad is
+    refused while gradients are recorded."""
     if d_w is not None:
         dtype = d_w.dtype
     elif accumulate:

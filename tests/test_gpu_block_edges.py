@@ -277,6 +277,55 @@ def test_no_tokens_read_nothing():
 # ------------------------------------------------------------------ what the binding gives and takes
 
 
+def test_gradients_do_not_go_missing():
+    """No call records a history: tensors whose gradients are being recorded are refused where
+    these would end without a word."""
+    x, d, form = make(4, 64, "bf16", "full", "sigmoid", "one")
+    p = params("sigmoid")
+    names = ("y", "residual", "w_post", "w_pre", "gate", "res_scale")
+    want = ops.mhc_block_norm(*(x[k] for k in names), p)
+    for k in names:
+        t = {**x, k: x[k].detach().clone().requires_grad_()}
+        with pytest.raises(ValueError, match="grad"):
+            ops.mhc_block_norm(*(t[n] for n in names), p)
+        with torch.no_grad():
+            got = ops.mhc_block_norm(*(t[n] for n in names), p)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    rest = (x["w_post"], x["w_pre"], x["gate"], x["res_scale"], p)
+    for k in ("d_ro", "d_h"):
+        t = {**d, k: d[k].clone().requires_grad_()}
+        with pytest.raises(ValueError, match="grad"):
+            ops.mhc_block_norm_backward(t["d_ro"], t["d_h"], x["y"], x["residual"], want[2], *rest)
+    # of the forward pass's own inputs the gradients are what is asked for
+    w = x["w_post"].clone().requires_grad_()
+    ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], want[2], w, *rest[1:])
+    c = ops.mhc_ckpt_pack(x["y"])
+    with pytest.raises(ValueError, match="grad"):
+        ops.mhc_ckpt_linear_dw(d["d_h"].clone().requires_grad_(), c)
+    with torch.no_grad():
+        ops.mhc_ckpt_linear_dw(d["d_h"].clone().requires_grad_(), c)
+
+    class Block(torch.autograd.Function):
+        """The pair as a user wraps it."""
+
+        @staticmethod
+        def forward(ctx, y, r, w_post, w_pre, gate, scale):
+            ro, h, rstd = ops.mhc_block_norm(y, r, w_post, w_pre, gate, scale, p)
+            ctx.save_for_backward(y, r, rstd, w_post, w_pre, gate, scale)
+            return ro, h
+
+        @staticmethod
+        def backward(ctx, d_ro, d_h):
+            y, r, rstd, *rest = ctx.saved_tensors
+            return tuple(ops.mhc_block_norm_backward(d_ro, d_h, y, r, rstd, *rest, p))
+
+    t = {k: x[k].detach().clone().requires_grad_() for k in names}
+    ro, h = Block.apply(*(t[k] for k in names))
+    torch.autograd.backward((ro, h), (d["d_ro"], d["d_h"]))
+    for k, v in zip(names, ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], want[2], *rest)):
+        assert torch.equal(t[k].grad, v.to(x[k].dtype)), k
+
+
 def test_a_workspace_is_device_bytes():
     """Refused before anything is launched: the workspace's address goes to the kernels."""
     x, d, form = make(4, 64, "bf16", "none", "none", "none")
