@@ -416,7 +416,6 @@ def mhc_status_string(code: int) -> str:
 
 # ---------------------------------------------------------------------------
 # Gated residual block, its backward pass, and 8-bit activation checkpoints
-# (new tensors of a small call, up to 512 KB in all, are parts of one allocation)
 
 _DTYPES = {torch.float32: MHC_F32, torch.bfloat16: MHC_BF16, torch.float16: MHC_F16}
 _FORMATS = {"e4m3": 1, "int8": 2}

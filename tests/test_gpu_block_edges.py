@@ -277,6 +277,24 @@ def test_no_tokens_read_nothing():
 # ------------------------------------------------------------------ what the binding gives and takes
 
 
+def test_outputs_have_storages_of_their_own():
+    """What is kept of a small call holds nothing else, and what is freed frees nothing else."""
+    x, d, form = make(8, 256, "bf16", "full", "sigmoid", "one")
+    p = params("sigmoid")
+    args = (x["w_post"], x["w_pre"], x["gate"], x["res_scale"], p)
+    out = ops.mhc_block_norm(x["y"], x["residual"], *args)
+    for t in out:
+        assert t.storage_offset() == 0 and t.untyped_storage().nbytes() == t.numel() * t.element_size()
+    g = ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], out[2], *args)
+    for t in (g.d_y, g.d_residual, g.d_gate):
+        assert t.storage_offset() == 0 and t.untyped_storage().nbytes() == t.numel() * t.element_size()
+    # the fp32 gradients of the parameters alone are together
+    assert g.d_w_post.untyped_storage().nbytes() < 3 * 256 * 4 + 3 * 256
+    c = ops.mhc_ckpt_pack(x["y"])
+    d_w = ops.mhc_ckpt_linear_dw(d["d_h"], c)
+    assert d_w.storage_offset() == 0 and d_w.untyped_storage().nbytes() == d_w.numel() * 4
+
+
 def test_gradients_do_not_go_missing():
     """No call records a history: tensors whose gradients are being recorded are refused where
     these would end without a word."""
