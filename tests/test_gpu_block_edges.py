@@ -92,6 +92,28 @@ def test_single_scale_gradient_of_a_stream(T, H, types, gate, pad, held):
     within(got.d_res_scale, want["d_res_scale"], bound, "d_res_scale")
 
 
+# ------------------------------------------------------------------ the widest rows, many a block
+
+
+@pytest.mark.parametrize("T,H,types,gate,scale,pad", [(400, 7168, "fp32", "token", "one", 0), (400, 7168, "fp32", "full", "channel", 0),
+                                                      (400, 8192, "fp32", "full", "one", 0), (400, 8192, "fp32", "none", "none", 3),
+                                                      (400, 7168, "fp32", "full", "one", 3), (400, 8184, "bf16+", "full", "channel", 0),
+                                                      (320, 8191, "fp32", "token", "channel", 0), (400, 5600, "fp32", "full", "none", 0)])
+@pytest.mark.parametrize("held", [False, True])
+def test_rows_of_which_two_do_not_fit_shared_memory(T, H, types, gate, scale, pad, held):
+    x, d, form = make(T, H, types, gate, "none" if gate == "none" else "sigmoid", scale, pad)
+    p = params(form["act"])
+    cks = {k: ops.ckpt_empty(T, H, "int8") for k in ("ckpt_y", "ckpt_residual")} if held else {}
+    _, _, _, rstd = check_forward(x, form, p, **cks)
+    if not held:
+        return check_backward(x, d, form, p, rstd=rstd)
+    values = {k[5:]: ref.unpack(c.codes, c.scales, "int8") for k, c in cks.items()}
+    for k, c in cks.items():
+        codes, scales = ref.pack(x[k[5:]], "int8")
+        assert torch.equal(c.codes, codes) and torch.equal(c.scales, scales)
+    check_backward(x, d, form, p, cks["ckpt_y"], cks["ckpt_residual"], rstd, values)
+
+
 # ------------------------------------------------------------------ values past fp16
 
 
