@@ -10,6 +10,7 @@
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "mhc.h"
@@ -294,7 +295,8 @@ PyObject *tuple(std::initializer_list<at::Tensor> ts) {
     return r;
 }
 
-// Runs an entry point's body; no C++ exception passes into Python.
+// Runs an entry point's body; no C++ exception passes into Python. torch's own become what torch raises
+// (an allocation that fails: torch.OutOfMemoryError).
 template <class F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F body) {
     if (n != want) {
@@ -305,10 +307,8 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F body) {
         return body();
     } catch (const Refused &e) {
         PyErr_SetString(PyExc_ValueError, e.what.c_str());
-    } catch (const std::exception &e) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+        if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

@@ -383,3 +383,11 @@ def test_a_workspace_is_device_bytes():
     got = ops.mhc_block_norm_backward(d["d_ro"], d["d_h"], x["y"], x["residual"], rstd,
                                       workspace=torch.empty(n // 4 + 1, device="cuda"))
     assert torch.equal(want.d_y, got.d_y)
+
+
+def test_an_allocation_that_fails_raises_torch_s_error():
+    """More than the device holds: what a program that shrinks its batch catches."""
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        ops.ckpt_empty(1 << 25, 65536)
+    x = torch.randn(4, 64, device="cuda")
+    assert ops.mhc_ckpt_unpack(ops.mhc_ckpt_pack(x, "int8"), FP32).shape == x.shape
