@@ -64,13 +64,15 @@ struct GemmArgs {
     int tiles_n, tiles_k, splits, steps_per_split, steps;
     int tile_k;                     // columns of a tile: 256, or 128 for few tiles
     int chain;                      // steps between two additions in registers
-    int f16;                        // operands fp16, else bf16
     void *out;                      // d_w, or the splits' fp32 sums [splits][n][k]
     int out_dtype, accumulate, wide;    // wide: rows of out lie on 32-byte boundaries
-    const uint8_t *top;             // fp16: [splits * pieces][groups], the largest scale byte of x's groups of columns in a piece
-    int pieces, groups, shift;      // pieces of a split at most
     unsigned int *status;
     unsigned long long timeout_ns;
+};
+// fp16: the largest scale byte of x's groups of columns in a piece.
+struct TopArgs {
+    const uint8_t *top;             // [splits * pieces][groups]
+    int pieces, groups, shift;      // pieces of a split at most
 };
 
 __device__ __forceinline__ void dw_cluster_sync() {
@@ -196,9 +198,10 @@ __device__ __forceinline__ void item_place(const GemmArgs &a, int item, int *ti,
     *ti = first + q - *tj * rows;
 }
 
+template <bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
 dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant__ CUtensorMap map_x,
-               const GemmArgs a) {
+               const GemmArgs a, const TopArgs b) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     uint8_t *const basep = raw + (base - smem_addr(raw));
@@ -277,7 +280,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ------------------------------------------------ products, the leader for both
-        const uint32_t fmt = a.f16 ? 0u : 1u;
+        const uint32_t fmt = F16 ? 0u : 1u;
         const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | (1u << 16) |
                                (static_cast<uint32_t>(a.tile_k >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
         uint32_t it = 0, done = 0;
@@ -337,17 +340,18 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 16; ++e) sum[p][e] = 0ull;
             uint32_t part = 0;
-            float unit[4] = {1.f, 1.f, 1.f, 1.f};
+            float unit[4] = {1.f, 1.f, 1.f, 1.f};      // fp16: the power of two that each 32 columns get back
+            auto more = [](uint64_t sum, uint64_t v, float u) { return F16 ? fma2(v, splat2(u), sum) : add2(sum, v); };
             for (int c0 = s0; c0 < s1; c0 += a.chain, ++done) {
                 const uint32_t buf = done & 1;
                 const bool last = c0 + a.chain >= s1;
-                if (a.top) {
+                if constexpr (F16) {
                     // on their way while the products go on
-                    const uint8_t *const top = a.top + static_cast<long long>(split * a.pieces + (c0 - s0) / a.chain) * a.groups;
+                    const uint8_t *const top = b.top + static_cast<long long>(split * b.pieces + (c0 - s0) / a.chain) * b.groups;
                     const int g = (tj * a.tile_k + first) / kCkptGroup;
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        if (32 * p < width && g + p < a.groups) unit[p] = top_unit(top[g + p], a.shift);
+                        if (32 * p < width && g + p < b.groups) unit[p] = top_unit(top[g + p], b.shift);
                 }
                 ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, a.timeout_ns, a.status, SITE_DW_ACC_FULL);
                 ok = __all_sync(0xffffffffu, ok);
@@ -365,15 +369,16 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                             tmem_ld16_now(part + 32 * p + 16 * h, v);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                sum[p][8 * h + e] = fma2((static_cast<uint64_t>(v[2 * e + 1]) << 32) | v[2 * e], splat2(unit[p]),
-                                                         sum[p][8 * h + e]);
+                                sum[p][8 * h + e] = more(sum[p][8 * h + e], (static_cast<uint64_t>(v[2 * e + 1]) << 32) | v[2 * e], unit[p]);
                             if (last) tmem_st16(part + 32 * p + 16 * h, &sum[p][8 * h]);
                         }
                     }
                     if (last) tmem_st_wait();
-                    // the pieces' powers of two are in the sum
+                    if constexpr (F16) {
+                        // the pieces' powers of two are in the sum
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) unit[p] = 1.f;
+                        for (int p = 0; p < 4; ++p) unit[p] = 1.f;
+                    }
                 }
                 if (last) break;
                 tc_fence_before();
@@ -389,7 +394,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                 if (j >= a.k) break;
                 uint32_t v[32];
                 tmem_ld32_now(part + c, v);
-                if (a.top) {
+                if constexpr (F16) {
                     const float u = c == 0 ? unit[0] : c == 32 ? unit[1] : c == 64 ? unit[2] : unit[3];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * u);
@@ -739,23 +744,19 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     g.splits = p.splits;
     g.steps_per_split = p.steps_per_split;
     g.steps = p.steps;
-    g.f16 = a.dtype == MHC_F16;
     g.out = p.splits > 1 ? static_cast<void *>(parts) : a.d_w;
     g.out_dtype = p.splits > 1 ? MHC_F32 : a.d_w_dtype;
     g.accumulate = p.splits > 1 ? 0 : a.accumulate;
-    g.chain = a.d_w_dtype == MHC_F32 ? kChain32 : g.f16 ? kChainF16 : kChain16;
-    g.top = b.top;
-    g.pieces = b.pieces;
-    g.groups = static_cast<int>(ckpt_groups(a.k));
-    g.shift = b.shift;
+    g.chain = a.d_w_dtype == MHC_F32 ? kChain32 : a.dtype == MHC_F16 ? kChainF16 : kChain16;
+    const TopArgs top = {b.top, b.pieces, static_cast<int>(ckpt_groups(a.k)), b.shift};
     g.wide = a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
     g.status = status;
     g.timeout_ns = wait_timeout_ns();
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
     if (!g_dw_smem[dev & 63].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(dw_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-            return MHC_ERR_CUDA;
+        for (auto kern : {dw_gemm_kernel<false>, dw_gemm_kernel<true>})
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return MHC_ERR_CUDA;
         g_dw_smem[dev & 63].store(1, std::memory_order_release);
     }
     const long long items = static_cast<long long>(p.tiles_n) * p.tiles_k * p.splits, pairs = sms / 2;
@@ -773,7 +774,7 @@ int launch_dw(const DwArgs &a, bool d_aligned, int sms, unsigned int *status, bo
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    if (int e = note_launch(cudaLaunchKernelEx(&cfg, dw_gemm_kernel, md, mx, g))) return e;
+    if (int e = note_launch(cudaLaunchKernelEx(&cfg, a.dtype == MHC_F16 ? dw_gemm_kernel<true> : dw_gemm_kernel<false>, md, mx, g, top))) return e;
     if (p.splits == 1) return MHC_OK;
     return note_launch(launch_join(parts, p.splits, count, a.d_w, a.d_w_dtype, a.accumulate, sms, pdl, s));
 }
