@@ -78,7 +78,8 @@ class Stack:
         return h
 
     def step(self, x, target, fmt=None, lr=0.02):
-        """One step of gradient descent on mean((h - target)^2) / 2: the loss before it."""
+        """One step of gradient descent on half a token's squared distance from its target, the mean
+        over tokens. Returns half the mean square over tokens and columns before it."""
         h = self.forward(x, fmt)
         diff = h.float() - target.float()
         d_r, d_h = None, (diff / diff.shape[0]).to(h.dtype)

@@ -349,7 +349,9 @@ mhc_status mhc_block_norm(const mhc_block *block, const void *y, int64_t y_strid
                           const mhc_ckpt *ckpt_residual, const mhc_ckpt *ckpt_h, void *stream);
 
 /* Bytes of device scratch of mhc_block_norm_backward: the partial sums over
- * tokens of the weights' gradients. 0 when T == 0. Needs no initialisation. */
+ * tokens of the weights' gradients. 0 when T == 0. Needs no initialisation. It lies
+ * on a 16-byte boundary; only from a 32-byte one on does the call go by runs of 8
+ * elements, else by single ones. */
 size_t mhc_block_norm_backward_workspace_bytes(int64_t tokens, int hidden);
 
 /*
@@ -369,8 +371,9 @@ size_t mhc_block_norm_backward_workspace_bytes(int64_t tokens, int hidden);
  * d_w_post, d_w_pre [H] fp32; d_gate [H] fp32 (CHANNEL), [T] fp32 (TOKEN) or
  * [T, H] of gate_dtype (FULL); d_res_scale [1] or [H] fp32. Any of the last
  * four may be NULL where it is not wanted, and must be where there is no such
- * input. Sums over tokens run in an order fixed by (T, H): results are the
- * same run to run. T == 0 writes zeros to the sums.
+ * input. Sums over tokens run in an order fixed by the call's sizes, types, forms
+ * and alignment: results are the same run to run. The sum of a single scale's
+ * gradient is held in 48 bits. T == 0 writes zeros to the sums.
  */
 mhc_status mhc_block_norm_backward(const mhc_block *block, const void *d_residual_out,
                                    int64_t d_residual_out_stride, const void *d_h,

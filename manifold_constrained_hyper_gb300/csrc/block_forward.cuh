@@ -13,9 +13,9 @@
 // refilled as soon as its row is in registers. With 16 columns a thread
 // 8192 x 7168 takes 2 to 10 % longer.
 //
-// Measured, bf16: 8192 x 7168 with a full sigmoid gate 99.5 us, 5.9 TB/s of the bytes that it
-// must move (0.88 of a copy's rate), with a channel gate and scale 86; strided by
-// 7171 elements 146, 7169 wide 205 (single elements: bound by instructions); one row of 7168 4.5 us.
+// Measured, bf16: 8192 x 7168 with a full sigmoid gate 99.6 us, 5.9 TB/s of the bytes that it
+// must move (0.88 of a copy's rate), with a channel gate and scale 80 to 84; strided by
+// 7171 elements 100 to 112, 7169 wide 158 (single elements: bound by instructions); one row of 7168 4.7 us.
 #pragma once
 #include <type_traits>
 

@@ -4,8 +4,8 @@
 // each pass over the row reading it again (from L1 or L2 after the first). N is 8 for
 // rows on boundaries of 8 elements, else 1. Bound by L2: every row reads the parameters
 // again in each pass (fp32 ones are four to eight times a 16-bit row's own bytes). Measured,
-// bf16, channel gate and scale: 2048 x 8200 113 us forward and 204 backward, 8201 wide 135 and
-// 446 (2048 x 8192 by the row kernels: 26 and 48).
+// bf16, channel gate and scale: 2048 x 8200 111 us forward and 202 backward, 8201 wide 133 and
+// 437 (2048 x 8192 by the row kernels: 28 and 48).
 #include "block_rows.cuh"
 
 namespace mhc {
