@@ -426,6 +426,125 @@ mhc_status mhc_ckpt_linear_dw(const void *d_out, int64_t d_out_stride, mhc_dtype
                               void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/*
+ * The layers on either side of a boundary: layer norm, the projection with its
+ * epilogue, their gradients, and the orthogonalised update of a weight.
+ * Matrices are rows `stride` elements apart (>= 0) on any boundary of their
+ * type; outputs are contiguous. Sums are fp32 and rounded once; their order is
+ * fixed by the call's sizes, types and alignment. tokens < 2^31 - 1024, other
+ * sizes in [1, 65536]; workspaces lie on a 16-byte boundary and need no
+ * initialisation.
+ */
+typedef enum {
+    MHC_LINEAR_NONE = 0,
+    MHC_LINEAR_RELU = 1,
+    MHC_LINEAR_RELU2 = 2,       /* relu squared */
+    MHC_LINEAR_SILU = 3,        /* z / (1 + exp(-z)) */
+    MHC_LINEAR_GELU = 4,        /* z * Phi(z), by erfc */
+    MHC_LINEAR_GELU_TANH = 5    /* 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+} mhc_linear_act;
+
+/* Whether `rows` rows of 16-bit elements lie as the tensor cores' loads want
+ * them: on 16-byte boundaries, the stride a multiple of 8 and at least n (one
+ * row: any stride). Others are copied into the workspace first. */
+int mhc_linear_rows_aligned(const void *p, int64_t stride, int64_t rows, int n);
+
+/* Bytes of device scratch of mhc_linear, mhc_linear_dx and mhc_linear_dw: sums
+ * of a split product, column sums (dw with a bias) and copies of operands that
+ * are not aligned as above. 0 when T == 0 or the call would be refused for its sizes. */
+size_t mhc_linear_workspace_bytes(int64_t tokens, int n, int k, int x_aligned, int w_aligned);
+size_t mhc_linear_dx_workspace_bytes(int64_t tokens, int n, int k, int d_out_aligned, int w_aligned);
+size_t mhc_linear_dw_workspace_bytes(int64_t tokens, int n, int k, int d_out_aligned, int x_aligned,
+                                     int bias);
+
+/*
+ * A projection with its epilogue:
+ *   z = x w^T + bias,   out = act(z) + residual
+ * x [T, k] and w [n, k] of dtype (BF16 or F16); bias [n] of bias_dtype (dtype
+ * or F32) or NULL; residual [T, n] of out_dtype or NULL; out [T, n] of
+ * out_dtype (dtype or F32), which may be exactly the residual buffer when its
+ * stride is n or T is 1; z_out [T, n] of dtype, what the backward pass of act
+ * needs, or NULL (out is formed from the unrounded z). Up to 64 tokens the
+ * weights are streamed once through all SMs.
+ */
+mhc_status mhc_linear(const void *x, int64_t x_stride, const void *w, int64_t w_stride, mhc_dtype dtype,
+                      int64_t tokens, int n, int k, const void *bias, mhc_dtype bias_dtype,
+                      const void *residual, int64_t residual_stride, mhc_linear_act act, void *out,
+                      mhc_dtype out_dtype, void *z_out, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * The gradient of its input, through the activation of the layer below:
+ *   d_x = (d_out w) * act'(z)
+ * d_out [T, n], w [n, k], z [T, k] of dtype; z NULL with MHC_LINEAR_NONE: the
+ * product alone. d_x [T, k] of d_x_dtype (dtype or F32). relu'(0) = 0.
+ */
+mhc_status mhc_linear_dx(const void *d_out, int64_t d_out_stride, const void *w, int64_t w_stride,
+                         mhc_dtype dtype, int64_t tokens, int n, int k, const void *z, int64_t z_stride,
+                         mhc_linear_act act, void *d_x, mhc_dtype d_x_dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * The gradients of its weight and bias:
+ *   d_w = d_out^T x,   d_bias = sum over tokens of d_out
+ * d_out [T, n] and x [T, k] of dtype; d_w [n, k] of d_w_dtype (any); d_bias [n]
+ * fp32 or NULL. accumulate: both are added to what is there. T == 0 writes zeros
+ * (accumulate: leaves them).
+ */
+mhc_status mhc_linear_dw(const void *d_out, int64_t d_out_stride, const void *x, int64_t x_stride,
+                         mhc_dtype dtype, int64_t tokens, int n, int k, void *d_w, mhc_dtype d_w_dtype,
+                         float *d_bias, int accumulate, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * Layer norm of each row, with mean and variance over its H values:
+ *   out = (x - mean) * rstd * w + b,   rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ * x [T, H] of dtype (any); w, b [H] of w_dtype, b_dtype (any), each or NULL
+ * (1 and 0); out [T, H] of out_dtype: dtype, or any 16-bit type beside an F32
+ * x. stats [T, 2] fp32 (mean, rstd), what the backward pass needs, or NULL.
+ */
+mhc_status mhc_layer_norm(const void *x, int64_t x_stride, mhc_dtype dtype, int64_t tokens, int hidden,
+                          const void *w, mhc_dtype w_dtype, const void *b, mhc_dtype b_dtype, float eps,
+                          void *out, mhc_dtype out_dtype, float *stats, void *stream);
+
+/* Bytes of device scratch of mhc_layer_norm_backward: partial sums over tokens. */
+size_t mhc_layer_norm_backward_workspace_bytes(int64_t tokens, int hidden);
+
+/*
+ * Its backward pass. With h = (x - mean) * rstd and e = d_out * w:
+ *   d_x = rstd * (e - mean(e) - h * mean(e * h)) + d_residual
+ *   d_w = sum over tokens of d_out * h,   d_b = sum over tokens of d_out
+ * d_out [T, H] of out_dtype as above; x, stats as in the forward call; d_residual [T, H]
+ * of dtype: the gradient that reaches x past the norm, or NULL; d_x [T, H] of dtype, which
+ * may be exactly the d_residual buffer when its stride is H or T is 1; d_w, d_b [H] fp32, each or
+ * NULL. T == 0 writes zeros to the sums.
+ */
+mhc_status mhc_layer_norm_backward(const void *d_out, int64_t d_out_stride, mhc_dtype out_dtype,
+                                   const void *x, int64_t x_stride, mhc_dtype dtype, const float *stats,
+                                   int64_t tokens, int hidden, const void *w, mhc_dtype w_dtype,
+                                   const void *d_residual, int64_t d_residual_stride, void *d_x,
+                                   float *d_w, float *d_b, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* Bytes of device scratch of mhc_orthogonalize. */
+size_t mhc_orthogonalize_workspace_bytes(int batch, int m, int n);
+
+/*
+ * The orthogonalised update of `batch` weights [m, n], batch_stride elements
+ * apart, by Newton-Schulz products:
+ *   X = G / (|G| + eps)  (the Frobenius norm),  then `steps` times
+ *   A = X X^T,  X <- (a I + b A + c A A) X
+ * G of dtype (any); out [batch, m, n] of out_dtype (BF16 or F16: matrices are
+ * held in 22 bits between the products, which is what a 16-bit result takes).
+ * steps in [1, 100]; |a|, |b|, |c| <= 1000; elements of the products past
+ * 16 overflow to infinity. A G of zeros gives zeros. batch in [0, 65535].
+ */
+mhc_status mhc_orthogonalize(const void *g, int64_t row_stride, int64_t batch_stride, mhc_dtype dtype,
+                             int batch, int m, int n, int steps, float a, float b, float c, float eps,
+                             void *out, mhc_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* Status and diagnostics.                                                  */
 
 /* Synchronises `stream`, then reads and clears the current device's status

@@ -26,6 +26,18 @@ struct Entries {
     decltype(&mhc_ckpt_unpack) unpack;
     decltype(&mhc_ckpt_linear_dw) dw;
     decltype(&mhc_ckpt_linear_dw_workspace_bytes) dw_bytes;
+    decltype(&mhc_linear) linear;
+    decltype(&mhc_linear_workspace_bytes) linear_bytes;
+    decltype(&mhc_linear_dx) linear_dx;
+    decltype(&mhc_linear_dx_workspace_bytes) linear_dx_bytes;
+    decltype(&mhc_linear_dw) linear_dw;
+    decltype(&mhc_linear_dw_workspace_bytes) linear_dw_bytes;
+    decltype(&mhc_linear_rows_aligned) rows_aligned;
+    decltype(&mhc_layer_norm) layer_norm;
+    decltype(&mhc_layer_norm_backward) layer_norm_backward;
+    decltype(&mhc_layer_norm_backward_workspace_bytes) layer_norm_backward_bytes;
+    decltype(&mhc_orthogonalize) orthogonalize;
+    decltype(&mhc_orthogonalize_workspace_bytes) orthogonalize_bytes;
 } g_lib;
 PyObject *g_error = nullptr;
 PyObject *g_eps_post, *g_eps_pre, *g_gate_act, *g_weight_offset, *g_post_norm;
@@ -490,21 +502,260 @@ PyObject *ckpt_linear_dw(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// A matrix of 16-bit rows as a product reads it.
+struct Rows {
+    at::Tensor t;
+    int64_t rows, stride;
+    int width;
+    bool aligned;
+};
+int width_of(int64_t w) { return w > INT32_MAX ? INT32_MAX : static_cast<int>(w); }
+Rows product_rows(const at::Tensor &t, const char *name, const Shape &s, at::ScalarType type) {
+    Rows r{t, s.T, rows(t, name, s, type), width_of(s.H), false};
+    r.aligned = g_lib.rows_aligned(t.data_ptr(), r.stride, s.T, r.width) != 0;
+    return r;
+}
+at::ScalarType half_type(const at::Tensor &t, const char *name) {
+    const at::ScalarType s = t.scalar_type();
+    if (s != at::kBFloat16 && s != at::kHalf)
+        throw Refused{std::string(name) + " must be bfloat16 or float16: got " + c10::toString(s)};
+    return s;
+}
+// A parameter [H], contiguous, of float32 or one other type (any: of the three).
+void parameter(const at::Tensor &t, const char *name, int64_t H, c10::Device device, at::ScalarType other, bool any) {
+    if (!t.defined()) return;
+    const at::ScalarType s = t.scalar_type();
+    if (t.dim() != 1 || t.size(0) != H || t.device() != device || !t.is_contiguous() ||
+        !(any ? dtype_of(s) >= 0 : s == at::kFloat || s == other))
+        throw Refused{std::string(name) + " must be a contiguous " + str({H}) + " tensor of " +
+                      (any ? "float32, bfloat16 or float16" : std::string("float32 or ") + c10::toString(other)) + " on " +
+                      device.str() + ": got " + str(t)};
+}
+void workspace_or(at::Tensor *workspace, size_t need, NewTensors *made) {
+    if (!workspace->defined() && need) made->add(workspace, {static_cast<int64_t>(need)}, at::kByte);
+}
+mhc_dtype mhc_type(at::ScalarType t) { return static_cast<mhc_dtype>(dtype_of(t)); }
+
+// x, w, bias, residual, act, out, z, whether z is wanted, out's type (-1: the residual's, else x's), workspace -> out, z
+PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject * {
+        const at::Tensor x = tensor(a[0], "x"), w = tensor(a[1], "w"), bias = tensor(a[2], "bias", true),
+                         residual = tensor(a[3], "residual", true);
+        for (auto [t, name] : {std::pair{&x, "x"}, {&w, "w"}, {&bias, "bias"}, {&residual, "residual"}})
+            no_history(*t, name, "mhc_linear");
+        const Shape s = shape_2d(x, "x"), ws = shape_2d(w, "w");
+        const at::ScalarType t = half_type(x, "x");
+        const Rows xr = product_rows(x, "x", s, t), wr = product_rows(w, "w", {ws.T, s.H, s.device}, t);
+        const int64_t N = ws.T;
+        parameter(bias, "bias", N, s.device, t, false);
+        const long act = PyLong_AsLong(a[4]), type = PyLong_AsLong(a[8]);
+        at::Tensor out = tensor(a[5], "out", true), z = tensor(a[6], "z", true);
+        const at::ScalarType o = out.defined() ? out.scalar_type() : type >= 0 ? scalar_of(type) : residual.defined() ? residual.scalar_type() : t;
+        if (o != t && o != at::kFloat) throw Refused{std::string("out must be float32 or of x's type: got ") + c10::toString(o)};
+        const Shape os{s.T, N, s.device};
+        const int64_t rstride = residual.defined() ? rows(residual, "residual", os, o) : 0;
+        const c10::cuda::CUDAGuard guard(s.device);
+        at::Tensor workspace = scratch(a[9], s.device), out_, z_;
+        NewTensors made(s.device);
+        made.add_or(&out_, out, "out", {s.T, N}, o);
+        if (z.defined() || PyObject_IsTrue(a[7]) == 1) made.add_or(&z_, z, "z", {s.T, N}, t);
+        workspace_or(&workspace, g_lib.linear_bytes(s.T, width_of(N), xr.width, xr.aligned, wr.aligned), &made);
+        made.make();
+        check(g_lib.linear(x.data_ptr(), xr.stride, w.data_ptr(), wr.stride, mhc_type(t), s.T, width_of(N), xr.width, ptr(bias),
+                           bias.defined() ? mhc_type(bias.scalar_type()) : MHC_F32, ptr(residual), rstride,
+                           static_cast<mhc_linear_act>(act), out_.data_ptr(), mhc_type(o), ptr(z_), ptr(workspace),
+                           workspace.defined() ? workspace.nbytes() : 0, stream_on(s.device)),
+              "mhc_linear");
+        return z_.defined() ? tuple({out_, z_}) : wrap(out_);
+    });
+}
+
+// d_out, w, z, act, d_x, its type (-1: d_out's), workspace -> d_x
+PyObject *linear_dx(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject * {
+        const at::Tensor d_out = tensor(a[0], "d_out"), w = tensor(a[1], "w"), z = tensor(a[2], "z", true);
+        for (auto [t, name] : {std::pair{&d_out, "d_out"}, {&w, "w"}, {&z, "z"}}) no_history(*t, name, "mhc_linear_dx");
+        const Shape s = shape_2d(d_out, "d_out"), ws = shape_2d(w, "w");
+        const at::ScalarType t = half_type(d_out, "d_out");
+        const Rows dr = product_rows(d_out, "d_out", s, t), wr = product_rows(w, "w", {s.H, ws.H, s.device}, t);
+        const int64_t K = ws.H;
+        const long act = PyLong_AsLong(a[3]), type = PyLong_AsLong(a[5]);
+        if (act != MHC_LINEAR_NONE && !z.defined()) throw Refused{"z is needed for the slope of the activation"};
+        if (act == MHC_LINEAR_NONE && z.defined()) throw Refused{"z has no use without an activation"};
+        const int64_t zstride = z.defined() ? rows(z, "z", {s.T, K, s.device}, t) : 0;
+        at::Tensor given = tensor(a[4], "d_x", true), d_x, workspace = scratch(a[6], s.device);
+        const at::ScalarType o = given.defined() ? given.scalar_type() : type >= 0 ? scalar_of(type) : t;
+        if (o != t && o != at::kFloat) throw Refused{std::string("d_x must be float32 or of d_out's type: got ") + c10::toString(o)};
+        const c10::cuda::CUDAGuard guard(s.device);
+        NewTensors made(s.device);
+        made.add_or(&d_x, given, "d_x", {s.T, K}, o);
+        workspace_or(&workspace, g_lib.linear_dx_bytes(s.T, dr.width, width_of(K), dr.aligned, wr.aligned), &made);
+        made.make();
+        check(g_lib.linear_dx(d_out.data_ptr(), dr.stride, w.data_ptr(), wr.stride, mhc_type(t), s.T, dr.width, width_of(K), ptr(z),
+                              zstride, static_cast<mhc_linear_act>(act), d_x.data_ptr(), mhc_type(o), ptr(workspace),
+                              workspace.defined() ? workspace.nbytes() : 0, stream_on(s.device)),
+              "mhc_linear_dx");
+        return wrap(d_x);
+    });
+}
+
+// d_out, x, d_w, its type, whether the bias's is wanted, d_bias, accumulate, workspace -> d_w, d_bias
+PyObject *linear_dw(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject * {
+        const at::Tensor d_out = tensor(a[0], "d_out"), x = tensor(a[1], "x");
+        for (auto [t, name] : {std::pair{&d_out, "d_out"}, {&x, "x"}}) no_history(*t, name, "mhc_linear_dw");
+        const Shape s = shape_2d(d_out, "d_out"), xs = shape_2d(x, "x");
+        const at::ScalarType t = half_type(d_out, "d_out");
+        const Rows dr = product_rows(d_out, "d_out", s, t), xr = product_rows(x, "x", {s.T, xs.H, s.device}, t);
+        const int64_t K = xs.H;
+        const long type = PyLong_AsLong(a[3]);
+        const at::Tensor bias = tensor(a[5], "d_bias", true);
+        at::Tensor d_w, d_bias, workspace = scratch(a[7], s.device);
+        const c10::cuda::CUDAGuard guard(s.device);
+        NewTensors made(s.device);
+        made.add_or(&d_w, tensor(a[2], "d_w", true), "d_w", {s.H, K}, scalar_of(type));
+        if (bias.defined() || PyObject_IsTrue(a[4]) == 1) made.add_or(&d_bias, bias, "d_bias", {s.H}, at::kFloat);
+        const bool with_bias = bias.defined() || PyObject_IsTrue(a[4]) == 1;
+        workspace_or(&workspace, g_lib.linear_dw_bytes(s.T, dr.width, width_of(K), dr.aligned, xr.aligned, with_bias), &made);
+        made.make();
+        check(g_lib.linear_dw(d_out.data_ptr(), dr.stride, x.data_ptr(), xr.stride, mhc_type(t), s.T, dr.width, width_of(K),
+                              d_w.data_ptr(), static_cast<mhc_dtype>(type), static_cast<float *>(ptr(d_bias)),
+                              PyObject_IsTrue(a[6]) == 1, ptr(workspace), workspace.defined() ? workspace.nbytes() : 0,
+                              stream_on(s.device)),
+              "mhc_linear_dw");
+        return with_bias ? tuple({d_w, d_bias}) : wrap(d_w);
+    });
+}
+
+// out's type beside x's
+void norm_type(at::ScalarType x, at::ScalarType out, const char *name) {
+    if (dtype_of(x) < 0) throw Refused{std::string("x must be float32, bfloat16 or float16: got ") + c10::toString(x)};
+    if (dtype_of(out) < 0 || (out != x && x != at::kFloat))
+        throw Refused{std::string(name) + " must be of x's type, or of 16 bits beside a float32 x: got " + c10::toString(out)};
+}
+
+// x, w, b, eps, out, stats, out's type (-1: x's) -> out, stats
+PyObject *layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject * {
+        const at::Tensor x = tensor(a[0], "x"), w = tensor(a[1], "w", true), b = tensor(a[2], "b", true);
+        for (auto [t, name] : {std::pair{&x, "x"}, {&w, "w"}, {&b, "b"}}) no_history(*t, name, "mhc_layer_norm");
+        const Shape s = shape_2d(x, "x");
+        const at::ScalarType t = x.scalar_type();
+        const long type = PyLong_AsLong(a[6]);
+        const double eps = PyFloat_AsDouble(a[3]);
+        if (PyErr_Occurred()) throw std::runtime_error("");
+        const at::Tensor given = tensor(a[4], "out", true);
+        const at::ScalarType o = given.defined() ? given.scalar_type() : type >= 0 ? scalar_of(type) : t;
+        norm_type(t, o, "out");
+        const int64_t stride = rows(x, "x", s, t);
+        parameter(w, "w", s.H, s.device, t, true);
+        parameter(b, "b", s.H, s.device, t, true);
+        const c10::cuda::CUDAGuard guard(s.device);
+        at::Tensor out, stats;
+        NewTensors made(s.device);
+        made.add_or(&out, given, "out", {s.T, s.H}, o);
+        made.add_or(&stats, tensor(a[5], "stats", true), "stats", {s.T, 2}, at::kFloat);
+        made.make();
+        check(g_lib.layer_norm(x.data_ptr(), stride, mhc_type(t), s.T, width_of(s.H), ptr(w),
+                               w.defined() ? mhc_type(w.scalar_type()) : MHC_F32, ptr(b),
+                               b.defined() ? mhc_type(b.scalar_type()) : MHC_F32, static_cast<float>(eps), out.data_ptr(),
+                               mhc_type(o), static_cast<float *>(stats.data_ptr()), stream_on(s.device)),
+              "mhc_layer_norm");
+        return tuple({out, stats});
+    });
+}
+
+// d_out, x, stats, w, whether the bias's is wanted, d_residual, d_x, workspace -> d_x, d_w, d_b
+PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject * {
+        const at::Tensor d_out = tensor(a[0], "d_out"), x = tensor(a[1], "x"), stats = tensor(a[2], "stats"),
+                         w = tensor(a[3], "w", true), d_residual = tensor(a[5], "d_residual", true);
+        for (auto [t, name] : {std::pair{&d_out, "d_out"}, {&d_residual, "d_residual"}})
+            no_history(*t, name, "mhc_layer_norm_backward");
+        const Shape s = shape_2d(x, "x");
+        const at::ScalarType t = x.scalar_type(), o = d_out.scalar_type();
+        norm_type(t, o, "d_out");
+        const int64_t xstride = rows(x, "x", s, t), dstride = rows(d_out, "d_out", s, o),
+                      rstride = d_residual.defined() ? rows(d_residual, "d_residual", s, t) : 0;
+        if (stats.dim() != 2 || stats.size(0) != s.T || stats.size(1) != 2 || stats.scalar_type() != at::kFloat ||
+            stats.device() != s.device || !stats.is_contiguous())
+            throw Refused{"stats must be a contiguous " + str({s.T, 2}) + " float32 tensor on " + s.device.str() + ": got " + str(stats)};
+        parameter(w, "w", s.H, s.device, t, true);
+        const bool bias = PyObject_IsTrue(a[4]) == 1;
+        const c10::cuda::CUDAGuard guard(s.device);
+        at::Tensor d_x, d_w, d_b, workspace = scratch(a[7], s.device);
+        NewTensors made(s.device);
+        made.add_or(&d_x, tensor(a[6], "d_x", true), "d_x", {s.T, s.H}, t);
+        if (w.defined()) made.add(&d_w, {s.H}, at::kFloat, true);
+        if (bias) made.add(&d_b, {s.H}, at::kFloat, true);
+        if (w.defined() || bias) workspace_or(&workspace, g_lib.layer_norm_backward_bytes(s.T, width_of(s.H)), &made);
+        made.make();
+        check(g_lib.layer_norm_backward(d_out.data_ptr(), dstride, mhc_type(o), x.data_ptr(), xstride, mhc_type(t),
+                                        static_cast<const float *>(stats.data_ptr()), s.T, width_of(s.H), ptr(w),
+                                        w.defined() ? mhc_type(w.scalar_type()) : MHC_F32, ptr(d_residual), rstride,
+                                        d_x.data_ptr(), static_cast<float *>(ptr(d_w)), static_cast<float *>(ptr(d_b)),
+                                        ptr(workspace), workspace.defined() ? workspace.nbytes() : 0, stream_on(s.device)),
+              "mhc_layer_norm_backward");
+        return tuple({d_x, d_w, d_b});
+    });
+}
+
+// g, steps, a, b, c, eps, out, its type, workspace -> out
+PyObject *orthogonalize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject * {
+        const at::Tensor g = tensor(a[0], "g");
+        no_history(g, "g", "mhc_orthogonalize");
+        const int64_t dims = g.dim();
+        if ((dims != 2 && dims != 3) || !g.is_cuda()) throw Refused{"g must be a 2-D or 3-D CUDA tensor"};
+        const at::ScalarType t = g.scalar_type();
+        if (dtype_of(t) < 0) throw Refused{std::string("g must be float32, bfloat16 or float16: got ") + c10::toString(t)};
+        const int64_t B = dims == 3 ? g.size(0) : 1, M = g.size(dims - 2), N = g.size(dims - 1);
+        if (N > 1 && g.stride(dims - 1) != 1) throw Refused{"g's rows must be contiguous: got strides " + str(g.strides())};
+        const long steps = PyLong_AsLong(a[1]), type = PyLong_AsLong(a[7]);
+        const double ca = PyFloat_AsDouble(a[2]), cb = PyFloat_AsDouble(a[3]), cc = PyFloat_AsDouble(a[4]), eps = PyFloat_AsDouble(a[5]);
+        if (PyErr_Occurred()) throw std::runtime_error("");
+        if (type != MHC_BF16 && type != MHC_F16) throw Refused{"out must be bfloat16 or float16"};
+        const c10::cuda::CUDAGuard guard(g.device());
+        at::Tensor out, workspace = scratch(a[8], g.device());
+        NewTensors made(g.device());
+        made.add_or(&out, tensor(a[6], "out", true), "out", g.sizes(), scalar_of(type));
+        const int batch = width_of(B), m = width_of(M), k = width_of(N);
+        workspace_or(&workspace, g_lib.orthogonalize_bytes(batch, m, k), &made);
+        made.make();
+        check(g_lib.orthogonalize(g.data_ptr(), g.stride(dims - 2), dims == 3 ? g.stride(0) : 0, mhc_type(t), batch, m, k,
+                                  steps > INT32_MAX ? INT32_MAX : steps < 0 ? -1 : static_cast<int>(steps), static_cast<float>(ca),
+                                  static_cast<float>(cb), static_cast<float>(cc), static_cast<float>(eps), out.data_ptr(),
+                                  static_cast<mhc_dtype>(type), ptr(workspace), workspace.defined() ? workspace.nbytes() : 0,
+                                  stream_on(g.device())),
+              "mhc_orthogonalize");
+        return wrap(out);
+    });
+}
+
 // The entry points' addresses, in the order of Entries, and the error class.
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 8, [&]() -> PyObject * {
-        void *p[7];
-        for (int i = 0; i < 7; ++i) {
+    return guarded(n, 20, [&]() -> PyObject * {
+        constexpr int kEntries = 19;
+        void *p[kEntries];
+        for (int i = 0; i < kEntries; ++i) {
             p[i] = PyLong_AsVoidPtr(a[i]);
             if (!p[i]) throw std::runtime_error("an entry point is missing");
         }
         g_lib = {reinterpret_cast<decltype(g_lib.norm)>(p[0]), reinterpret_cast<decltype(g_lib.backward)>(p[1]),
                  reinterpret_cast<decltype(g_lib.backward_bytes)>(p[2]), reinterpret_cast<decltype(g_lib.pack)>(p[3]),
                  reinterpret_cast<decltype(g_lib.unpack)>(p[4]), reinterpret_cast<decltype(g_lib.dw)>(p[5]),
-                 reinterpret_cast<decltype(g_lib.dw_bytes)>(p[6])};
-        Py_INCREF(a[7]);
+                 reinterpret_cast<decltype(g_lib.dw_bytes)>(p[6]), reinterpret_cast<decltype(g_lib.linear)>(p[7]),
+                 reinterpret_cast<decltype(g_lib.linear_bytes)>(p[8]), reinterpret_cast<decltype(g_lib.linear_dx)>(p[9]),
+                 reinterpret_cast<decltype(g_lib.linear_dx_bytes)>(p[10]), reinterpret_cast<decltype(g_lib.linear_dw)>(p[11]),
+                 reinterpret_cast<decltype(g_lib.linear_dw_bytes)>(p[12]), reinterpret_cast<decltype(g_lib.rows_aligned)>(p[13]),
+                 reinterpret_cast<decltype(g_lib.layer_norm)>(p[14]),
+                 reinterpret_cast<decltype(g_lib.layer_norm_backward)>(p[15]),
+                 reinterpret_cast<decltype(g_lib.layer_norm_backward_bytes)>(p[16]),
+                 reinterpret_cast<decltype(g_lib.orthogonalize)>(p[17]),
+                 reinterpret_cast<decltype(g_lib.orthogonalize_bytes)>(p[18])};
+        Py_INCREF(a[kEntries]);
         Py_XDECREF(g_error);
-        g_error = a[7];
+        g_error = a[kEntries];
         Py_RETURN_NONE;
     });
 }
@@ -512,6 +763,8 @@ PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define MHC_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MHC_METHOD(init),          MHC_METHOD(block_norm),  MHC_METHOD(block_norm_backward),
                            MHC_METHOD(ckpt_empty),    MHC_METHOD(ckpt_pack),     MHC_METHOD(ckpt_unpack), MHC_METHOD(ckpt_linear_dw),
+                           MHC_METHOD(linear),        MHC_METHOD(linear_dx),     MHC_METHOD(linear_dw),   MHC_METHOD(layer_norm),
+                           MHC_METHOD(layer_norm_backward), MHC_METHOD(orthogonalize),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

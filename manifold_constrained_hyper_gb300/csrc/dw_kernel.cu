@@ -28,6 +28,7 @@
 #include <atomic>
 
 #include "mhc_internal.h"
+#include "pair_mma.cuh"
 #include "vec_io.cuh"
 
 namespace mhc {
@@ -35,8 +36,8 @@ namespace {
 
 constexpr int kTile = 256;                          // rows of d_w by a pair of CTAs, and columns at most
 constexpr int kHalf = kTile / 2;                    // what one CTA loads of either operand at most
-constexpr int kStep = 64;                           // tokens per pipeline stage
-constexpr int kBoxBytes = kStep * 128;              // 64 columns x 64 tokens, 16 bits
+constexpr int kStep = kPairStep;                    // tokens per pipeline stage
+constexpr int kBoxBytes = kPairBoxBytes;            // 64 columns x 64 tokens, 16 bits
 constexpr int kStageBytes = 4 * kBoxBytes;          // two boxes of either operand
 constexpr int kStages = 6;
 constexpr int kSumWarps = 8;                        // epilogue: two to a quadrant of tensor-memory lanes
@@ -76,85 +77,6 @@ struct TopArgs {
     const uint8_t *top;             // [splits * pieces][groups]
     int pieces, groups, shift;      // pieces of a split at most
 };
-
-__device__ __forceinline__ void dw_cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t dw_cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t dw_map_to_rank(uint32_t addr, uint32_t rank) {
-    uint32_t d;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
-    return d;
-}
-__device__ __forceinline__ void arrive_at_rank(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-// A box into this CTA's shared memory, its bytes counted at a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m, int c0, int c1,
-                                              uint32_t cluster_bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(cluster_bar) : "memory");
-}
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t add) {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
-        ::"r"(d_tmem), "l"(ad), "l"(bd), "r"(idesc), "r"(add) : "memory");
-}
-// Arrive at `bar` in both CTAs when every product issued so far is done.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
-}
-// Columns contiguous, 128-byte rows in the 128-byte swizzle: 8 tokens an
-// atom of 1024 bytes, the next 64 columns a box further on.
-__device__ __forceinline__ uint64_t desc_columns(uint32_t addr) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
-// 32, or 16, columns of this warp's 32 lanes, there when it returns.
-__device__ __forceinline__ void tmem_ld32_now(uint32_t taddr, uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr) : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint64_t *v) {
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        w[2 * e] = static_cast<uint32_t>(v[e]);
-        w[2 * e + 1] = static_cast<uint32_t>(v[e] >> 32);
-    }
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
-        ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
-          "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(taddr) : "memory");
-}
-__device__ __forceinline__ void tmem_ld16_now(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr) : "memory");
-}
 
 // 2^(top - 127 - shift), what sums of fp16 operands are multiplied by; top >= 1 and shift < 23, so
 // that it is subnormal at the least.
@@ -214,7 +136,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *const turn = reinterpret_cast<float *>(basep + kStages * kStageBytes + 256);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = dw_cluster_rank();
+    const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int items = a.tiles_n * a.tiles_k * a.splits;
 
@@ -240,7 +162,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
     }
     tc_fence_before();
     __syncthreads();
-    dw_cluster_sync();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
@@ -262,7 +184,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                     break;
                 }
                 if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kBoxBytes * (a.tile_k == kTile ? 8 : 6));
-                const uint32_t bar = dw_map_to_rank(full + 8 * s, 0), dst = base + s * kStageBytes;
+                const uint32_t bar = map_to_rank(full + 8 * s, 0), dst = base + s * kStageBytes;
                 const int t = st * kStep;
                 tma_load_pair(dst, &map_d, ci, t, bar);
                 tma_load_pair(dst + kBoxBytes, &map_d, ci + 64, t, bar);
@@ -385,7 +307,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
                 if (last) break;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at_rank(dw_map_to_rank(acc_empty + 8 * buf, 0));
+                if (lane == 0) arrive_at_rank(map_to_rank(acc_empty + 8 * buf, 0));
             }
             if (!ok) break;
             const int i = ti * kTile + static_cast<int>(rank) * kHalf + quad * 32 + lane;
@@ -424,7 +346,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at_rank(dw_map_to_rank(acc_empty + 8 * (done & 1), 0));
+            if (lane == 0) arrive_at_rank(map_to_rank(acc_empty + 8 * (done & 1), 0));
             ++done;
         }
     }
@@ -432,7 +354,7 @@ dw_gemm_kernel(const __grid_constant__ CUtensorMap map_d, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     __syncwarp();
-    dw_cluster_sync();
+    cluster_sync();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }

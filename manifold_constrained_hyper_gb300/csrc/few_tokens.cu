@@ -1,0 +1,242 @@
+// The product with its epilogue for up to 64 rows (the tokens of a decode step): bound by reading the
+// weights once. The weights take the place of the tensor core's 128 rows and the tokens that of its
+// columns, so a CTA streams 128 rows of weights (16 KB for 64 of k) beside a few KB of tokens through
+// as many stages as shared memory holds. To have every SM read, the k of a tile is split over
+// the CTAs of a cluster, whose sums meet in distributed shared memory, in the order of the CTAs: no
+// second kernel, and the same result run to run.
+#include <atomic>
+
+#include "epilogue.cuh"
+#include "mhc_internal.h"
+#include "pair_mma.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr int kRows = 128;                          // of weights by a cluster
+constexpr int kWeightBytes = 2 * kPairBoxBytes;
+constexpr int kThreads = 192;                       // loads, products, four epilogue warps
+constexpr int kMaxStages = 11;
+constexpr int kStageBudget = 208 * 1024;
+constexpr int kMaxSplit = 8;
+
+enum FewSite : int { SITE_F_EMPTY = 90, SITE_F_FULL, SITE_F_ACC, SITE_F_DRAIN };
+
+struct FewArgs {
+    int m, n, width;                // tokens, rows of weights, tokens rounded up to 16
+    int steps, per, split, stages;  // steps of 64 of k, of a CTA, CTAs of a cluster
+    int chain, sums;                // steps of one sum in tensor memory, and how many such sums
+    int tmem_cols, w_turned;
+    uint32_t idesc;
+    unsigned int *status;
+    unsigned long long timeout_ns;
+    EpilogueArgs e;
+};
+
+__device__ __forceinline__ float load_at_rank(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_rank(addr, rank)) : "memory");
+    return v;
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                  const __grid_constant__ FewArgs a) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    uint8_t *const basep = raw + (base - smem_addr(raw));
+    const int stage_bytes = kWeightBytes + a.width * 128;
+    const uint32_t bars = base + a.stages * stage_bytes;
+    const uint32_t full = bars, empty = bars + 8 * kMaxStages, acc_full = bars + 16 * kMaxStages, drain = acc_full + 8;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + a.stages * stage_bytes + 16 * kMaxStages + 16);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    // the sums, [tokens][128], over the stages once nothing is on its way to them
+    float *const sums = reinterpret_cast<float *>(basep);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = blockIdx.x / a.split, rank = blockIdx.x - tile * a.split;
+    const int s0 = rank * a.per, s1 = min(s0 + a.per, a.steps), mine = max(s1 - s0, 0);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&map_w);
+    }
+    if (warp == 2) {
+        tmem_alloc(smem_addr(tmem_slot), a.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+
+    if (warp == 0 && lane == 0) {
+        const uint64_t policy = policy_evict_normal();
+        int it = 0;
+        bool ok = true;
+        for (; it < mine; ++it) {
+            const int s = it % a.stages, ph = (it / a.stages) & 1, k = (s0 + it) * kPairStep;
+            if (!mbar_wait(empty + 8 * s, ph ^ 1, abort_flag, a.timeout_ns, a.status, SITE_F_EMPTY)) {
+                ok = false;
+                break;
+            }
+            const uint32_t bar = full + 8 * s, dst = base + s * stage_bytes;
+            mbar_arrive_expect_tx(bar, stage_bytes);
+            if (a.w_turned) {
+                tma_load_3d(dst, &map_w, tile * kRows, k, 0, bar, policy);
+                tma_load_3d(dst + kPairBoxBytes, &map_w, tile * kRows + 64, k, 0, bar, policy);
+            } else {
+                tma_load_3d(dst, &map_w, k, tile * kRows, 0, bar, policy);
+            }
+            tma_load_3d(dst + kWeightBytes, &map_x, k, 0, 0, bar, policy);
+        }
+        // the last products' releases of their stages have arrived before this CTA may exit
+        for (int k = it > a.stages ? it - a.stages : 0; k < it && ok; ++k)
+            ok = mbar_wait(empty + 8 * (k % a.stages), (k / a.stages) & 1, abort_flag, a.timeout_ns, a.status, SITE_F_EMPTY);
+        if (!ok) {
+            // gave up: the copies still in flight land before this CTA exits
+            int gave_up = 0;
+            for (int k = it > a.stages ? it - a.stages : 0; k < it; ++k)
+                mbar_wait(full + 8 * (k % a.stages), (k / a.stages) & 1, &gave_up, a.timeout_ns, a.status, SITE_F_DRAIN);
+        }
+    } else if (warp == 1 && lane == 0) {
+        bool ok = true;
+        for (int it = 0; it < mine && ok; ++it) {
+            const int s = it % a.stages;
+            ok = mbar_wait(full + 8 * s, (it / a.stages) & 1, abort_flag, a.timeout_ns, a.status, SITE_F_FULL);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sw = base + s * stage_bytes, acc = tmem + it / a.chain * a.width;
+            const uint64_t dw = a.w_turned ? desc_columns(sw) : desc_rows(sw), nw = a.w_turned ? 2048 >> 4 : 32 >> 4;
+            const uint64_t dx = desc_rows(sw + kWeightBytes);
+#pragma unroll
+            for (int q = 0; q < kPairStep / 16; ++q)
+                tc_mma_bf16(acc, dw + q * nw, dx + q * (32 >> 4), a.idesc, it % a.chain > 0 || q > 0);
+            tc_commit(empty + 8 * s);
+        }
+        if (ok) {
+            if (mine) tc_commit(acc_full);
+        } else {
+            // the products issued end before tensor memory is freed
+            int gave_up = 0;
+            tc_commit(drain);
+            mbar_wait(drain, 0, &gave_up, a.timeout_ns, a.status, SITE_F_DRAIN);
+        }
+    } else if (warp >= 2) {
+        const int quad = warp & 3, row = quad * 32 + lane;
+        bool ok = true;
+        if (mine) ok = mbar_wait(acc_full, 0, abort_flag, a.timeout_ns, a.status, SITE_F_ACC);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        const int live = mine ? (mine + a.chain - 1) / a.chain : 0;
+        for (int t0 = 0; t0 < a.width && ok; t0 += 16) {
+            float v[16] = {};
+            for (int p = 0; p < live; ++p) {
+                uint32_t w[16];
+                tmem_ld16_now(tmem + p * a.width + t0 + (static_cast<uint32_t>(quad * 32) << 16), w);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sums[(t0 + e) * kRows + row] = v[e];
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    __syncwarp();
+    if (a.split > 1) cluster_sync();
+    // each CTA the same rows of every token
+    const int rows = kRows / a.split, r0 = rank * rows;
+    if (!*abort_flag) {
+        for (int q = threadIdx.x; q < a.m * rows; q += kThreads) {
+            const int t = q / rows, r = r0 + q - t * rows, j = tile * kRows + r;
+            if (j >= a.n) continue;
+            float x = 0.f;
+            if (a.split == 1) {
+                x = sums[t * kRows + r];
+            } else {
+                float part[kMaxSplit];
+                const uint32_t at = smem_addr(sums + t * kRows + r);
+#pragma unroll
+                for (int p = 0; p < kMaxSplit; ++p) part[p] = p < a.split ? load_at_rank(at, p) : 0.f;
+#pragma unroll
+                for (int p = 0; p < kMaxSplit; ++p) x += part[p];
+            }
+            finish_element<KIND>(a.e, t, static_cast<long long>(t) * a.n + j, j, x);
+        }
+    }
+    __syncwarp();
+    if (a.split > 1) cluster_sync();        // no CTA's sums go while another reads them
+    if (warp == 2) tmem_dealloc(tmem, a.tmem_cols);
+}
+
+std::atomic<int> g_smem[64];
+
+}  // namespace
+
+int launch_few_tokens(const Product &p, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
+    FewArgs a = {};
+    a.m = static_cast<int>(p.m);
+    a.n = p.n;
+    a.width = (a.m + 15) / 16 * 16;
+    a.steps = static_cast<int>((p.k + kPairStep - 1) / kPairStep);
+    const int tiles = (p.n + kRows - 1) / kRows;
+    a.split = 1;
+    while (a.split < kMaxSplit && 2 * a.split * tiles <= sms && a.steps >= 4 * a.split) a.split *= 2;
+    a.per = (a.steps + a.split - 1) / a.split;
+    const int most = 512 / a.width;
+    a.chain = p.exact ? (a.per + most - 1) / most > 8 ? (a.per + most - 1) / most : 8 : a.per;
+    a.sums = (a.per + a.chain - 1) / a.chain;
+    a.tmem_cols = 32;
+    while (a.tmem_cols < a.sums * a.width) a.tmem_cols *= 2;
+    const int stage_bytes = kWeightBytes + a.width * 128;
+    a.stages = kStageBudget / stage_bytes < kMaxStages ? kStageBudget / stage_bytes : kMaxStages;
+    a.w_turned = p.b.turned;
+    const uint32_t fmt = p.bf16 ? 1u : 0u;
+    a.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((p.b.turned ? 1u : 0u) << 15) |
+              (static_cast<uint32_t>(a.width >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+    a.status = status;
+    a.timeout_ns = wait_timeout_ns();
+    a.e = p.epi;
+    CUtensorMap mx, mw;
+    if (!encode_matrices16(&mx, p.bf16, p.a.hi, p.k, p.m, 1, p.a.pitch * 2, 0, a.width) ||
+        !(p.b.turned ? encode_matrices16(&mw, p.bf16, p.b.hi, p.n, p.k, 1, p.b.pitch * 2, 0, kPairStep)
+                     : encode_matrices16(&mw, p.bf16, p.b.hi, p.k, p.n, 1, p.b.pitch * 2, 0, kRows)))
+        return MHC_ERR_CUDA;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
+    constexpr int smem_most = kStageBudget + 1024 + 16 * kMaxStages + 64;
+    auto *const kern = p.kind == EPI_SLOPE ? few_tokens_kernel<EPI_SLOPE> : few_tokens_kernel<EPI_LINEAR>;
+    if (!g_smem[dev & 63].load(std::memory_order_acquire)) {
+        for (auto k : {few_tokens_kernel<EPI_SLOPE>, few_tokens_kernel<EPI_LINEAR>})
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most) != cudaSuccess) return MHC_ERR_CUDA;
+        g_smem[dev & 63].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles) * a.split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.stages) * stage_bytes + 1024 + 16 * kMaxStages + 64;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    return note_launch(cudaLaunchKernelEx(&cfg, kern, mx, mw, a));
+}
+
+}  // namespace mhc

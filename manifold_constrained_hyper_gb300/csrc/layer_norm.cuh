@@ -1,0 +1,67 @@
+// Layer norm's row kernels share: a group of warps holds a row, eight consecutive columns a run.
+#pragma once
+#include "linear_internal.h"
+#include "vec_io.cuh"
+
+namespace mhc {
+
+constexpr int kLnThreads = 512;                     // of a CTA: as many groups as fit
+constexpr int kLnMaxHeld = 8192;                    // columns that a group holds in registers
+
+// Sums over a group of `warps` warps (whole ones), the same in every thread. red: [2][16][N] floats of the
+// group; `turn` alternates between calls, so that one barrier a call is enough.
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], int warps, int warp, int lane, int barrier, float *red, int *turn) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+    if (warps == 1) return;
+    float *const here = red + *turn * 16 * N;
+    *turn ^= 1;
+    if (lane == 0)
+#pragma unroll
+        for (int e = 0; e < N; ++e) here[warp * N + e] = v[e];
+    named_barrier_sync(barrier, warps * 32);
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = lane < warps ? here[lane * N + e] : 0.f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+    // lanes 16 and up hold the sum of nothing
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = __shfl_sync(0xffffffffu, v[e], 0);
+}
+template <bool RUNS, class T>
+__device__ __forceinline__ Run ln_load(const T *row, int c, int H) {
+    if constexpr (RUNS) return load8(row + c);
+    else return load8_any(row, c, H);
+}
+template <bool RUNS, class T>
+__device__ __forceinline__ void ln_store(T *row, int c, int H, const Run &r) {
+    if constexpr (RUNS) store8(row + c, r);
+    else store8_any(row + c, r, (reinterpret_cast<uintptr_t>(row + c) & (2 * sizeof(T) - 1)) == 0, H - c < 8 ? H - c : 8);
+}
+// 8 parameters from column c on; `otherwise` where there are none.
+template <bool RUNS>
+__device__ __forceinline__ Run ln_param(const void *p, int dtype, int c, int H, float otherwise) {
+    if (!p) return run_splat(otherwise);
+    if (dtype == MHC_F32) return ln_load<RUNS>(static_cast<const float *>(p), c, H);
+    if (dtype == MHC_BF16) return ln_load<RUNS>(static_cast<const __nv_bfloat16 *>(p), c, H);
+    return ln_load<RUNS>(static_cast<const __half *>(p), c, H);
+}
+// Lanes past the row's end hold 0 of v.
+__device__ __forceinline__ Run ln_masked(Run v, int c, int H) {
+    if (c + 8 <= H) return v;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = c + e < H ? run_at(v, e) : 0.f;
+    return run_of(f);
+}
+__device__ __forceinline__ float run_sum(const Run &r) {
+    const uint64_t s = add2(add2(r.p[0], r.p[1]), add2(r.p[2], r.p[3]));
+    return f2_lo(s) + f2_hi(s);
+}
+
+}  // namespace mhc

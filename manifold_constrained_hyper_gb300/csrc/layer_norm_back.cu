@@ -1,0 +1,244 @@
+// Layer norm's backward pass. With h = (x - mean) * rstd and e = d_out * w:
+//   d_x = rstd * (e - mean(e) - h * mean(e * h)) + d_residual,   d_w = sum_t d_out * h,   d_b = sum_t d_out.
+// One pass over the rows: the two row sums in one reduction, the sums over tokens in registers, a set for
+// each group of warps; a CTA's groups meet in shared memory, and the CTAs' sets are added by a second
+// kernel in their order.
+#include "layer_norm.cuh"
+#include "mhc_internal.h"
+
+namespace mhc {
+namespace {
+
+constexpr int kR = 2;                               // runs of 8 columns a thread at most
+
+template <class TX, class TD, int R, bool RUNS>
+__global__ void __launch_bounds__(kLnThreads) ln_back_rows_kernel(const LayerNormBackArgs a, int warps) {
+    extern __shared__ float sums[];                 // [2][H] where a CTA has several groups
+    __shared__ float red[16][2 * 16 * 2];
+    const int lane = threadIdx.x & 31, groups = blockDim.x / (32 * warps), group = threadIdx.x / (32 * warps);
+    const int mine = threadIdx.x - group * 32 * warps, warp = mine >> 5;
+    const bool want = a.d_w || a.d_b;
+    int turn = 0;
+    Run dw[R], db[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) dw[r] = db[r] = run_splat(0.f);
+    griddep_wait();
+    for (long long t = static_cast<long long>(blockIdx.x) * groups + group; t < a.T; t += static_cast<long long>(gridDim.x) * groups) {
+        const TX *const x = static_cast<const TX *>(a.x) + t * a.x_stride;
+        const TD *const d = static_cast<const TD *>(a.d_out) + t * a.d_stride;
+        const float mean = a.stats[2 * t], rstd = a.stats[2 * t + 1];
+        Run h[R], e[R];
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * warps * 32 + mine) * 8;
+            h[r] = e[r] = run_splat(0.f);
+            if (c >= a.H) continue;
+            h[r] = ln_load<RUNS>(x, c, a.H);
+            e[r] = ln_load<RUNS>(d, c, a.H);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * warps * 32 + mine) * 8;
+            if (c >= a.H) continue;
+            const Run w = ln_param<RUNS>(a.w, a.w_dtype, c, a.H, 1.f);
+            uint64_t s1 = 0ull, s2 = 0ull;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[r].p[q] = mul2(add2(h[r].p[q], splat2(-mean)), splat2(rstd));
+            if (!RUNS) h[r] = ln_masked(h[r], c, a.H);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                dw[r].p[q] = fma2(e[r].p[q], h[r].p[q], dw[r].p[q]);
+                db[r].p[q] = add2(db[r].p[q], e[r].p[q]);
+                e[r].p[q] = mul2(e[r].p[q], w.p[q]);
+                s1 = add2(s1, e[r].p[q]);
+                s2 = fma2(e[r].p[q], h[r].p[q], s2);
+            }
+            s[0] += f2_lo(s1) + f2_hi(s1);
+            s[1] += f2_lo(s2) + f2_hi(s2);
+        }
+        group_sums(s, warps, warp, lane, group + 1, red[group], &turn);
+        const float m1 = -s[0] * a.inv_h, m2 = -s[1] * a.inv_h;
+        TX *const out = static_cast<TX *>(a.d_x) + t * a.H;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * warps * 32 + mine) * 8;
+            if (c >= a.H) continue;
+            Run add = run_splat(0.f);
+            if (a.d_residual) add = ln_load<RUNS>(static_cast<const TX *>(a.d_residual) + t * a.r_stride, c, a.H);
+            Run o;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o.p[q] = fma2(fma2(h[r].p[q], splat2(m2), add2(e[r].p[q], splat2(m1))), splat2(rstd), add.p[q]);
+            ln_store<RUNS>(out, c, a.H, o);
+        }
+    }
+    if (!want) return;
+    // the groups one after another into shared memory, then the CTA's set
+    float *const set = a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H;
+    for (int g = 0; g < groups; ++g) {
+        if (g == group) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (r * warps * 32 + mine) * 8;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (c + k >= a.H) break;
+                    float w = run_at(dw[r], k), b = run_at(db[r], k);
+                    if (g) {
+                        w += sums[c + k];
+                        b += sums[a.H + c + k];
+                    }
+                    float *const to = g == groups - 1 ? set : sums;
+                    to[c + k] = w;
+                    to[a.H + c + k] = b;
+                }
+            }
+        }
+        if (g < groups - 1) __syncthreads();
+    }
+}
+
+// Rows too wide to be held: a CTA a row, read twice; its sums over tokens in its set, each column its thread's.
+template <class TX, class TD>
+__global__ void __launch_bounds__(kLnThreads) ln_back_loop_kernel(const LayerNormBackArgs a) {
+    __shared__ float red[2 * 16 * 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kLnThreads / 32;
+    const bool want = a.d_w || a.d_b;
+    float *const set = a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H;
+    int turn = 0;
+    griddep_wait();
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const TX *const x = static_cast<const TX *>(a.x) + t * a.x_stride;
+        const TD *const d = static_cast<const TD *>(a.d_out) + t * a.d_stride;
+        const float mean = a.stats[2 * t], rstd = a.stats[2 * t + 1];
+        const bool first = t == blockIdx.x;
+        auto load = [&](int c, Run *h, Run *e) {
+            *h = load8_any(x, c, a.H);
+            *e = load8_any(d, c, a.H);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h->p[q] = mul2(add2(h->p[q], splat2(-mean)), splat2(rstd));
+            *h = ln_masked(*h, c, a.H);
+        };
+        float s[2] = {0.f, 0.f};
+        for (int c = threadIdx.x * 8; c < a.H; c += kLnThreads * 8) {
+            Run h, e;
+            load(c, &h, &e);
+            if (want)
+                for (int k = 0; k < 8 && c + k < a.H; ++k) {
+                    const float w = run_at(e, k) * run_at(h, k), b = run_at(e, k);
+                    set[c + k] = first ? w : set[c + k] + w;
+                    set[a.H + c + k] = first ? b : set[a.H + c + k] + b;
+                }
+            const Run w = ln_param<false>(a.w, a.w_dtype, c, a.H, 1.f);
+            Run p;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                e.p[q] = mul2(e.p[q], w.p[q]);
+                p.p[q] = mul2(e.p[q], h.p[q]);
+            }
+            s[0] += run_sum(e);
+            s[1] += run_sum(p);
+        }
+        group_sums(s, warps, warp, lane, 1, red, &turn);
+        const float m1 = -s[0] * a.inv_h, m2 = -s[1] * a.inv_h;
+        TX *const out = static_cast<TX *>(a.d_x) + t * a.H;
+        for (int c = threadIdx.x * 8; c < a.H; c += kLnThreads * 8) {
+            Run h, e;
+            load(c, &h, &e);
+            const Run w = ln_param<false>(a.w, a.w_dtype, c, a.H, 1.f);
+            Run add = run_splat(0.f), o;
+            if (a.d_residual) add = load8_any(static_cast<const TX *>(a.d_residual) + t * a.r_stride, c, a.H);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o.p[q] = fma2(fma2(h.p[q], splat2(m2), fma2(e.p[q], w.p[q], splat2(m1))), splat2(rstd), add.p[q]);
+            ln_store<false>(out, c, a.H, o);
+        }
+    }
+}
+
+// The sets in their order (none: zeros); a CTA 32 columns of one of the two sums, its 8 warps shares of the sets.
+__global__ void __launch_bounds__(256) ln_back_join_kernel(const float *sums, int parts, int H, float *d_w, float *d_b) {
+    __shared__ float red[8][33];
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, c = blockIdx.x * 32 + lane;
+    float *const out = which ? d_b : d_w;
+    if (!out) return;
+    float v = 0.f;
+    if (c < H)
+#pragma unroll 8
+        for (int p = warp; p < parts; p += 8) v += sums[(static_cast<long long>(p) * 2 + which) * H + c];
+    red[warp][lane] = v;
+    __syncthreads();
+    if (warp || c >= H) return;
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += red[k][lane];
+    out[c] = v;
+}
+
+bool on_runs(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == MHC_F32 ? 31u : 15u)) == 0; }
+
+struct Shape {
+    int R, warps, groups, parts;
+};
+// The row kernel's shape: as many groups as 512 threads give, a CTA an SM (two of the loop kernel's).
+Shape shape_of(long long T, int H) {
+    Shape p = {1, kLnThreads / 32, 1, 0};
+    if (H <= kLnMaxHeld) {
+        const int need = (H + 255) / 256;
+        p.R = need <= 1 ? 1 : kR;
+        p.warps = (need + p.R - 1) / p.R;
+        p.groups = kLnThreads / (32 * p.warps);
+    }
+    const long long blocks = (T + p.groups - 1) / p.groups;
+    p.parts = static_cast<int>(blocks < kGridCap ? blocks : kGridCap);
+    return p;
+}
+
+template <class TX, class TD>
+cudaError_t launch_types(const LayerNormBackArgs &a, bool pdl, cudaStream_t s) {
+    const Shape p = shape_of(a.T, a.H);
+    if (a.H > kLnMaxHeld)
+        return launch_block_kernel(ln_back_loop_kernel<TX, TD>, static_cast<unsigned>(p.parts), kLnThreads, 0, pdl, s, a);
+    const bool runs = a.H % 8 == 0 && a.x_stride % 8 == 0 && a.d_stride % 8 == 0 && on_runs(a.x, a.x_dtype) &&
+                      on_runs(a.d_out, a.d_dtype) && on_runs(a.d_x, a.x_dtype) && on_runs(a.w, a.w_dtype) &&
+                      (!a.d_residual || (a.r_stride % 8 == 0 && on_runs(a.d_residual, a.x_dtype)));
+    auto *const kern = p.R == 1 ? (runs ? ln_back_rows_kernel<TX, TD, 1, true> : ln_back_rows_kernel<TX, TD, 1, false>)
+                                : (runs ? ln_back_rows_kernel<TX, TD, kR, true> : ln_back_rows_kernel<TX, TD, kR, false>);
+    const size_t smem = p.groups > 1 ? static_cast<size_t>(a.H) * 8 : 0;     // at most 4096 columns
+    return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * p.warps * p.groups, smem, pdl, s, a, p.warps);
+}
+
+}  // namespace
+
+size_t layer_norm_sums_bytes(long long T, int H) {
+    return T > 0 ? static_cast<size_t>(shape_of(T, H).parts) * 2 * H * 4 : 0;
+}
+
+int launch_layer_norm_back(const LayerNormBackArgs &a, int, bool pdl, cudaStream_t s) {
+    int parts = 0;
+    if (a.T > 0) {
+        cudaError_t e;
+        if (a.x_dtype == MHC_BF16) e = launch_types<__nv_bfloat16, __nv_bfloat16>(a, pdl, s);
+        else if (a.x_dtype == MHC_F16) e = launch_types<__half, __half>(a, pdl, s);
+        else if (a.d_dtype == MHC_BF16) e = launch_types<float, __nv_bfloat16>(a, pdl, s);
+        else if (a.d_dtype == MHC_F16) e = launch_types<float, __half>(a, pdl, s);
+        else e = launch_types<float, float>(a, pdl, s);
+        if (int r = note_launch(e)) return r;
+        parts = shape_of(a.T, a.H).parts;
+    }
+    if (!a.d_w && !a.d_b) return MHC_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.H + 31) / 32, 2);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return note_launch(cudaLaunchKernelEx(&cfg, ln_back_join_kernel, static_cast<const float *>(a.sums), parts, a.H, a.d_w, a.d_b));
+}
+
+}  // namespace mhc

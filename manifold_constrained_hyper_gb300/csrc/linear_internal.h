@@ -1,0 +1,119 @@
+// Internal declarations of the products with an epilogue, their gradients, layer norm and the
+// orthogonalised update. Not part of the C ABI; the enums' values are mhc.h's.
+#pragma once
+#include "block_internal.h"
+
+namespace mhc {
+
+// cuTensorMapEncodeTiled for `batch` row-major matrices of 16-bit elements: rows of `inner` elements
+// `pitch_bytes` apart, matrices `batch_bytes`; boxes of 64 x box_rows in the 128-byte swizzle.
+bool encode_matrices16(CUtensorMap *m, bool bf16, const void *ptr, unsigned long long inner, unsigned long long rows,
+                       unsigned long long batch, unsigned long long pitch_bytes, unsigned long long batch_bytes,
+                       unsigned int box_rows);
+
+// One operand of a product: element (row, k) of matrix b is at
+// hi[b * batch_stride + row * pitch + k], or with `turned` at [b * batch_stride + k * pitch + row];
+// its value hi, or hi + lo with lo.
+struct Operand {
+    const void *hi, *lo;
+    long long pitch, batch_stride;                  // in elements, multiples of 8; pointers on 16 bytes
+    bool turned;
+};
+
+// What is done to the sums before they are stored.
+enum Epilogue : int {
+    EPI_SUMS,       // out = acc, or added to out; of the splits: fp32 sums
+    EPI_LINEAR,     // z = unit * acc + bias, out = act(z) + residual
+    EPI_SLOPE,      // out = acc * act'(z)
+    EPI_PAIR        // unit * acc, with a polynomial in the first operand or without, as hi + lo in fp16
+};
+struct EpilogueArgs {
+    void *out;                                      // [batch][m][n], contiguous
+    int out_dtype, accumulate;
+    float unit;
+    const void *bias;                               // [n] or NULL
+    int bias_dtype;
+    const void *residual;                           // rows or NULL
+    long long residual_stride;
+    int residual_dtype;
+    void *z;                                        // LINEAR: [m][n] contiguous, to write, or NULL; SLOPE: rows to read
+    long long z_stride;
+    int z_dtype;
+    int act;
+    // PAIR: rows on 16-byte boundaries
+    void *hi, *lo;
+    long long pitch, batch_stride;
+    const void *x_hi, *x_lo;                        // of the same layout, or NULL
+    float of_x, of_unit;                            // out = of_unit * I + of_x * x + unit * acc
+    int wide;                                       // every row that is touched lies on the boundaries of runs of 8
+};
+struct Product {
+    long long m;
+    int n;
+    long long k;
+    int batch;
+    bool bf16;                                      // the operands' type, else fp16
+    bool symmetric;                                 // PAIR: m == n and out is symmetric
+    bool exact;                                     // sums in short pieces, for an fp32 result
+    Operand a, b;                                   // [m][k], [n][k]
+    Epilogue kind;
+    EpilogueArgs epi;
+    float *parts;                                   // of split sums, product_parts_bytes()
+};
+size_t product_parts_bytes(long long m, int n, long long k);
+// An mhc_status: one launch, or two where the summed axis is split.
+int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cudaStream_t s);
+
+// Up to kFewTokens rows of a: the same product by a kernel that is bound by reading b once.
+constexpr int kFewTokens = 64;
+int launch_few_tokens(const Product &p, int sms, unsigned int *status, bool pdl, cudaStream_t s);
+
+// 16-bit rows to rows `pitch` apart, on 16-byte boundaries.
+cudaError_t launch_copy_rows16(const void *src, long long stride, long long rows, int n, void *dst, long long pitch, int sms,
+                               bool pdl, cudaStream_t s);
+// Sums over rows of a 16-bit [rows][n]: out[n] fp32 (accumulate: added). parts: column_sums_bytes().
+size_t column_sums_bytes(long long rows, int n);
+int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, float *parts,
+                       int sms, bool pdl, cudaStream_t s);
+
+struct LayerNormArgs {
+    long long T;
+    int H;
+    const void *x, *w, *b;
+    long long x_stride;
+    int x_dtype, w_dtype, b_dtype, out_dtype;
+    float eps, inv_h;
+    void *out;
+    float *stats;                                   // [T][2]: mean, rstd; or NULL
+};
+cudaError_t launch_layer_norm(const LayerNormArgs &a, int sms, bool pdl, cudaStream_t s);
+
+struct LayerNormBackArgs {
+    long long T;
+    int H;
+    const void *d_out, *x, *d_residual, *w;
+    long long d_stride, x_stride, r_stride;
+    int d_dtype, x_dtype, w_dtype;
+    const float *stats;
+    float inv_h;
+    void *d_x;
+    float *d_w, *d_b;                               // each or NULL
+    float *sums;                                    // layer_norm_sums_bytes()
+};
+size_t layer_norm_sums_bytes(long long T, int H);
+int launch_layer_norm_back(const LayerNormBackArgs &a, int sms, bool pdl, cudaStream_t s);
+
+struct OrthogonalArgs {
+    const void *g;
+    int dtype;
+    long long row_stride, batch_stride;
+    int batch, m, n, steps;
+    float a, b, c, eps;
+    void *out;
+    int out_dtype;
+    void *workspace;
+};
+size_t orthogonal_workspace(int batch, int m, int n);
+int launch_orthogonal(const OrthogonalArgs &a, int sms, unsigned int *status, bool pdl, cudaStream_t s);
+
+}  // namespace mhc

@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 
 #include "block_internal.h"
+#include "linear_internal.h"
 #include "mhc.h"
 #include "mhc_internal.h"
 
@@ -615,6 +616,21 @@ bool encode_rows16(CUtensorMap *m, bool bf16, const void *ptr, unsigned long lon
     cuuint32_t box[2] = {64, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                    const_cast<void *>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_matrices16(CUtensorMap *m, bool bf16, const void *ptr, unsigned long long inner, unsigned long long rows,
+                       unsigned long long batch, unsigned long long pitch_bytes, unsigned long long batch_bytes,
+                       unsigned int box_rows) {
+    if (!get_encoder()) return false;
+    cuuint64_t dims[3] = {inner, rows, batch};
+    cuuint64_t strides[2] = {pitch_bytes, batch == 1 ? pitch_bytes : batch_bytes};
+    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                     const_cast<void *>(ptr), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

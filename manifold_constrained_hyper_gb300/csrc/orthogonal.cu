@@ -1,0 +1,242 @@
+// The orthogonalised update: X = G / (|G| + eps), then `steps` times
+//   A = X X^T,   P = a I + b A + c A A,   X <- P X          (rows and columns exchanged where G is tall),
+// an odd polynomial of G's singular values that drives them towards 1. Bound by its products: with p the
+// shorter side and q the longer, 2 p^2 q + 2 p^3 + 2 p^2 q operations a step, of which the two symmetric
+// products form half.
+//
+// What is lost in a weak direction at the first step is amplified with it, by a^steps (480 for five
+// steps of 3.4445) against the strong ones, so 11 or 8 bits of X do not give 16-bit results. Every
+// matrix is held in two fp16 parts, hi + lo, 22 bits, and every product takes three on the tensor
+// cores; sums are fp32. Elements are at most 1 (X), about 1.5 (A) or a (P): a factor of 2^12 in all of them
+// keeps what matters of lo above fp16's smallest values, and leaves room for 16 times 1.
+//
+// G may lie in strided rows. A tall G is not turned: its Gram matrix is X^T X, the product reading both
+// operands with the summed axis outermost.
+#include "layer_norm.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr float kScale = 4096.f;
+constexpr int kNormParts = 64;                      // shares of a matrix's squares
+constexpr int kRuns = 4;
+
+struct Shape {
+    int p, q;                       // the shorter and the longer side
+    long long x_pitch, p_pitch;     // elements of a row of X, of A and P
+    long long x_size, p_size;       // elements of one matrix
+    size_t parts_at, x_at, a_at, total;
+};
+long long pitch8(long long w) { return (w + 7) / 8 * 8; }
+size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+Shape shape_of(int batch, int m, int n) {
+    Shape s;
+    s.p = m < n ? m : n;
+    s.q = m < n ? n : m;
+    s.x_pitch = pitch8(n);
+    s.p_pitch = pitch8(s.p);
+    s.x_size = up256(static_cast<size_t>(m) * s.x_pitch * 2) / 2;
+    s.p_size = up256(static_cast<size_t>(s.p) * s.p_pitch * 2) / 2;
+    s.parts_at = 0;
+    s.x_at = up256(static_cast<size_t>(batch) * kNormParts * 8);
+    s.a_at = s.x_at + 4 * static_cast<size_t>(batch) * s.x_size * 2;
+    s.total = s.a_at + 4 * static_cast<size_t>(batch) * s.p_size * 2;
+    return s;
+}
+
+// A share of the sum of one matrix's squares, in double between threads. A share that
+// leaves fp32's range, or its accurate part, is formed again in double throughout.
+template <class T>
+__global__ void __launch_bounds__(256) ns_norm_kernel(const T *g, long long row_stride, long long batch_stride, int m, int n, bool runs,
+                                                      double *parts) {
+    __shared__ double red[8];
+    griddep_wait();
+    const long long per_row = (n + 7) / 8, total = per_row * m;
+    const T *const x = g + blockIdx.y * batch_stride;
+    const long long step = static_cast<long long>(gridDim.x) * 256;
+    auto load = [&](long long i) {
+        const long long t = i / per_row;
+        const int c = static_cast<int>(i - t * per_row) * 8;
+        return runs ? load8(x + t * row_stride + c) : load8_any(x + t * row_stride, c, n);
+    };
+    double s = 0.;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += step * kRuns) {
+        Run v[kRuns];
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r) {
+            v[r] = run_splat(0.f);
+            if (i + r * step < total) v[r] = load(i + r * step);
+        }
+        uint64_t q2 = 0ull;
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) q2 = fma2(v[r].p[q], v[r].p[q], q2);
+        const float f = f2_lo(q2) + f2_hi(q2);
+        if (f < 1e30f && f > 1e-30f) {
+            s += f;
+        } else {
+#pragma unroll
+            for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += static_cast<double>(run_at(v[r], e)) * run_at(v[r], e);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    s = 0.;
+    for (int w = 0; w < 8; ++w) s += red[w];
+    parts[blockIdx.y * kNormParts + blockIdx.x] = s;
+}
+
+// X in two fp16 parts, times 2^12.
+template <class T>
+__global__ void __launch_bounds__(256) ns_split_kernel(const T *g, long long row_stride, long long batch_stride, int m, int n, bool runs,
+                                                       float eps, const double *parts, int count, __half *hi, __half *lo, long long pitch,
+                                                       long long size) {
+    __shared__ float factor[2];
+    griddep_wait();
+    if (threadIdx.x < 32) {
+        double s = 0.;
+        for (int p = threadIdx.x; p < count; p += 32) s += parts[blockIdx.y * kNormParts + p];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) {
+            // by a power of two first where fp32 does not hold the factor
+            const double norm = sqrt(s) + static_cast<double>(eps);
+            const float first = norm > 0x1p100 ? 0x1p-100f : norm < 0x1p-100 ? 0x1p100f : 1.f;
+            factor[0] = first;
+            // a matrix of zeros, with no eps, stays one
+            factor[1] = norm == 0. ? 0.f : static_cast<float>(kScale / (norm * first));
+        }
+    }
+    __syncthreads();
+    const float f0 = factor[0], f1 = factor[1];
+    const long long per_row = (n + 7) / 8, total = per_row * m;
+    const T *const x = g + blockIdx.y * batch_stride;
+    hi += blockIdx.y * size;
+    lo += blockIdx.y * size;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<long long>(gridDim.x) * 256) {
+        const long long t = i / per_row;
+        const int c = static_cast<int>(i - t * per_row) * 8;
+        const Run v = runs ? load8(x + t * row_stride + c) : load8_any(x + t * row_stride, c, n);
+        uint4 hw, lw;
+        uint32_t *const hp = &hw.x, *const lp = &lw.x;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint64_t y = mul2(mul2(v.p[q], splat2(f0)), splat2(f1));
+            hp[q] = pack2(y, static_cast<const __half *>(nullptr));
+            lp[q] = pack2(fma2(unpack2(hp[q], static_cast<const __half *>(nullptr)), splat2(-1.f), y), static_cast<const __half *>(nullptr));
+        }
+        *reinterpret_cast<uint4 *>(hi + t * pitch + c) = hw;
+        *reinterpret_cast<uint4 *>(lo + t * pitch + c) = lw;
+    }
+}
+
+template <class T>
+int launch_start(const OrthogonalArgs &a, const Shape &sh, __half *hi, __half *lo, int sms, bool pdl, cudaStream_t s) {
+    const T *const g = static_cast<const T *>(a.g);
+    const bool runs = a.n % 8 == 0 && a.row_stride % 8 == 0 && a.batch_stride % 8 == 0 &&
+                      (reinterpret_cast<uintptr_t>(g) & (sizeof(T) == 4 ? 31u : 15u)) == 0;
+    double *const parts = reinterpret_cast<double *>(static_cast<uint8_t *>(a.workspace) + sh.parts_at);
+    const long long all = static_cast<long long>(a.m) * ((a.n + 7) / 8);
+    // shares of 1024 runs at least, and not more of them than fill the machine four times
+    long long count = (all + 1023) / 1024, most = (4LL * sms + a.batch - 1) / a.batch;
+    if (most > kNormParts) most = kNormParts;
+    if (count > most) count = most;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(count), a.batch);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    if (int e = note_launch(cudaLaunchKernelEx(&cfg, ns_norm_kernel<T>, g, a.row_stride, a.batch_stride, a.m, a.n, runs, parts))) return e;
+    long long blocks = (all + 255) / 256, cap = (8LL * sms + a.batch - 1) / a.batch;
+    if (blocks > cap) blocks = cap;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), a.batch);
+    return note_launch(cudaLaunchKernelEx(&cfg, ns_split_kernel<T>, g, a.row_stride, a.batch_stride, a.m, a.n, runs, a.eps,
+                                          static_cast<const double *>(parts), static_cast<int>(count), hi, lo, sh.x_pitch, sh.x_size));
+}
+
+}  // namespace
+
+size_t orthogonal_workspace(int batch, int m, int n) { return shape_of(batch, m, n).total; }
+
+int launch_orthogonal(const OrthogonalArgs &a, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
+    const Shape sh = shape_of(a.batch, a.m, a.n);
+    uint8_t *const ws = static_cast<uint8_t *>(a.workspace);
+    __half *const x0 = reinterpret_cast<__half *>(ws + sh.x_at), *const p0 = reinterpret_cast<__half *>(ws + sh.a_at);
+    const long long xs = sh.x_size * a.batch, ps = sh.p_size * a.batch;
+    __half *x_hi = x0, *x_lo = x0 + xs, *y_hi = x0 + 2 * xs, *y_lo = x0 + 3 * xs;
+    __half *const a_hi = p0, *const a_lo = p0 + ps, *const p_hi = p0 + 2 * ps, *const p_lo = p0 + 3 * ps;
+    const int e = a.dtype == MHC_F32    ? launch_start<float>(a, sh, x_hi, x_lo, sms, pdl, s)
+                  : a.dtype == MHC_BF16 ? launch_start<__nv_bfloat16>(a, sh, x_hi, x_lo, sms, pdl, s)
+                                        : launch_start<__half>(a, sh, x_hi, x_lo, sms, pdl, s);
+    if (e) return e;
+    const bool wide = a.m <= a.n;
+    for (int step = 0; step < a.steps; ++step) {
+        Product g = {};
+        g.m = g.n = sh.p;
+        g.k = sh.q;
+        g.batch = a.batch;
+        g.symmetric = true;
+        g.a = g.b = {x_hi, x_lo, sh.x_pitch, sh.x_size, !wide};
+        g.kind = EPI_PAIR;
+        g.epi.unit = 1.f / kScale;
+        g.epi.hi = a_hi;
+        g.epi.lo = a_lo;
+        g.epi.pitch = sh.p_pitch;
+        g.epi.batch_stride = sh.p_size;
+        if (int r = launch_product(g, sms, status, pdl, s)) return r;
+
+        g.k = sh.p;
+        g.a = g.b = {a_hi, a_lo, sh.p_pitch, sh.p_size, false};
+        g.epi.unit = a.c / kScale;
+        g.epi.hi = p_hi;
+        g.epi.lo = p_lo;
+        g.epi.x_hi = a_hi;
+        g.epi.x_lo = a_lo;
+        g.epi.of_x = a.b;
+        g.epi.of_unit = a.a * kScale;
+        if (int r = launch_product(g, sms, status, pdl, s)) return r;
+
+        Product x = {};
+        x.m = a.m;
+        x.n = a.n;
+        x.k = sh.p;
+        x.batch = a.batch;
+        const Operand poly = {p_hi, p_lo, sh.p_pitch, sh.p_size, false};
+        x.a = wide ? poly : Operand{x_hi, x_lo, sh.x_pitch, sh.x_size, false};
+        x.b = wide ? Operand{x_hi, x_lo, sh.x_pitch, sh.x_size, true} : poly;
+        if (step + 1 < a.steps) {
+            x.kind = EPI_PAIR;
+            x.epi.unit = 1.f / kScale;
+            x.epi.hi = y_hi;
+            x.epi.lo = y_lo;
+            x.epi.pitch = sh.x_pitch;
+            x.epi.batch_stride = sh.x_size;
+        } else {
+            x.kind = EPI_LINEAR;
+            x.epi.unit = 1.f / (kScale * kScale);
+            x.epi.out = a.out;
+            x.epi.out_dtype = a.out_dtype;
+            x.epi.wide = a.n % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+        }
+        if (int r = launch_product(x, sms, status, pdl, s)) return r;
+        __half *t = x_hi;
+        x_hi = y_hi;
+        y_hi = t;
+        t = x_lo;
+        x_lo = y_lo;
+        y_lo = t;
+    }
+    return MHC_OK;
+}
+
+}  // namespace mhc

@@ -1,5 +1,6 @@
 """Thin binding of libmhc.so (include/mhc.h): ctypes, and for the gated residual
-block, the checkpoints and the weight gradient the C++ of csrc/binding.cpp.
+block, the checkpoints, the projections, layer norm and the orthogonalised update
+the C++ of csrc/binding.cpp.
 
 Argument marshalling only: every step of the boundary runs in the library's
 CUDA kernels. Tensors are torch CUDA tensors (bf16 tensors travel as their
@@ -33,7 +34,11 @@ EXPORTS = ("mhc_weight_bytes", "mhc_prepare_weight", "mhc_post", "mhc_workspace_
            "mhc_debug_set_decode_path", "mhc_debug_set_pdl", "mhc_debug_delayed_copy",
            "mhc_debug_launch_count", "mhc_block_norm", "mhc_block_norm_backward",
            "mhc_block_norm_backward_workspace_bytes", "mhc_ckpt_pack", "mhc_ckpt_unpack",
-           "mhc_ckpt_linear_dw", "mhc_ckpt_linear_dw_workspace_bytes")
+           "mhc_ckpt_linear_dw", "mhc_ckpt_linear_dw_workspace_bytes", "mhc_linear",
+           "mhc_linear_workspace_bytes", "mhc_linear_dx", "mhc_linear_dx_workspace_bytes",
+           "mhc_linear_dw", "mhc_linear_dw_workspace_bytes", "mhc_linear_rows_aligned",
+           "mhc_layer_norm", "mhc_layer_norm_backward", "mhc_layer_norm_backward_workspace_bytes",
+           "mhc_orthogonalize", "mhc_orthogonalize_workspace_bytes")
 
 
 class MhcError(RuntimeError):
@@ -114,6 +119,20 @@ def load():
         "mhc_ckpt_unpack": (i32, [PC, i32, i64, i32, i32, P, P]),
         "mhc_ckpt_linear_dw_workspace_bytes": (sz, [i64, i32, i32, i32]),
         "mhc_ckpt_linear_dw": (i32, [P, i64, i32, PC, i32, i64, i32, i32, P, i32, i32, P, sz, P]),
+        "mhc_linear_rows_aligned": (i32, [P, i64, i64, i32]),
+        "mhc_linear_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
+        "mhc_linear_dx_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
+        "mhc_linear_dw_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32]),
+        "mhc_linear": (i32, [P, i64, P, i64, i32, i64, i32, i32, P, i32, P, i64, i32, P, i32, P, P, sz, P]),
+        "mhc_linear_dx": (i32, [P, i64, P, i64, i32, i64, i32, i32, P, i64, i32, P, i32, P, sz, P]),
+        "mhc_linear_dw": (i32, [P, i64, P, i64, i32, i64, i32, i32, P, i32, P, i32, P, sz, P]),
+        "mhc_layer_norm": (i32, [P, i64, i32, i64, i32, P, i32, P, i32, ctypes.c_float, P, i32, P, P]),
+        "mhc_layer_norm_backward_workspace_bytes": (sz, [i64, i32]),
+        "mhc_layer_norm_backward": (i32, [P, i64, i32, P, i64, i32, P, i64, i32, P, i32, P, i64, P, P, P,
+                                          P, sz, P]),
+        "mhc_orthogonalize_workspace_bytes": (sz, [i32, i32, i32]),
+        "mhc_orthogonalize": (i32, [P, i64, i64, i32, i32, i32, i32, i32, *[ctypes.c_float] * 4, P, i32, P, sz,
+                                    P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -436,7 +455,11 @@ def load_binding():
         _binding.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
             "mhc_block_norm", "mhc_block_norm_backward", "mhc_block_norm_backward_workspace_bytes",
             "mhc_ckpt_pack", "mhc_ckpt_unpack", "mhc_ckpt_linear_dw",
-            "mhc_ckpt_linear_dw_workspace_bytes")), MhcError)
+            "mhc_ckpt_linear_dw_workspace_bytes", "mhc_linear", "mhc_linear_workspace_bytes",
+            "mhc_linear_dx", "mhc_linear_dx_workspace_bytes", "mhc_linear_dw",
+            "mhc_linear_dw_workspace_bytes", "mhc_linear_rows_aligned", "mhc_layer_norm",
+            "mhc_layer_norm_backward", "mhc_layer_norm_backward_workspace_bytes", "mhc_orthogonalize",
+            "mhc_orthogonalize_workspace_bytes")), MhcError)
         _fast = _binding
     return _fast
 
@@ -643,3 +666,129 @@ def mhc_ckpt_linear_dw(d_out, x: Checkpoint, *, d_w=None, dtype=torch.float32,
         raise ValueError("accumulate needs the d_w to add to")
     return _at(stream, (_fast or load_binding()).ckpt_linear_dw, d_out, x.codes, x.scales,
                _FORMATS[x.fmt], d_w, _dtype_number(dtype, "d_w"), accumulate, workspace)
+
+
+# ---------------------------------------------------------------------------
+# Layer norm, projections with their epilogue, and the orthogonalised update
+
+_ACTS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+
+
+def _act_number(act):
+    n = _ACTS.get(act)
+    if n is None:
+        raise ValueError(f"act must be one of {list(_ACTS)}: got {act!r}")
+    return n
+
+
+def _type_number(dtype, name):
+    return -1 if dtype is None else _dtype_number(dtype, name)
+
+
+def mhc_linear(x, w, bias=None, residual=None, act="none", *, out=None, z=None, keep_z: bool = False,
+               dtype=None, workspace=None, stream=None):
+    """A projection with its epilogue in one pass over its sums:
+
+        z = x w^T + bias
+        out = act(z) + residual
+
+    x [T, K] and w [N, K], bfloat16 or float16, rows may be strided; bias [N]
+    of their type or float32; residual [T, N] of out's type; act "none",
+    "relu", "relu2", "silu", "gelu" or "gelu_tanh". out is float32 or of x's
+    type: as given, as `dtype` says, the residual's type, or x's. Returns out,
+    or (out, z) with keep_z or a z [T, N] given: z in x's type, what
+    mhc_linear_dx needs of the activation. out may be the residual itself. Up
+    to 64 tokens (a decode step) the weights are streamed once through every
+    SM. No history is recorded: while gradients are, tensors that require them
+    are refused."""
+    return _at(stream, (_fast or load_binding()).linear, x, w, bias, residual, _act_number(act), out, z,
+               keep_z, _type_number(dtype, "out"), workspace)
+
+
+def mhc_linear_dx(d_out, w, z=None, act="none", *, d_x=None, dtype=None, workspace=None, stream=None):
+    """d_x [T, K] = (d_out w) * act'(z): the gradient of a projection's input
+    x, taken on through the activation of the layer below, x = act(z). d_out
+    [T, N], w [N, K] and z [T, K] of one type, bfloat16 or float16, rows may be
+    strided; act "none" without a z. d_x is of d_out's type or float32."""
+    return _at(stream, (_fast or load_binding()).linear_dx, d_out, w, z, _act_number(act), d_x,
+               _type_number(dtype, "d_x"), workspace)
+
+
+def mhc_linear_dw(d_out, x, *, bias: bool = False, d_w=None, d_bias=None, dtype=torch.float32,
+                  accumulate: bool = False, workspace=None, stream=None):
+    """d_w [N, K] = d_out^T x, the weight gradient of a projection, from d_out
+    [T, N] and x [T, K] of one type, bfloat16 or float16, rows may be strided
+    (mhc_ckpt_linear_dw where x was checkpointed). With bias, or a d_bias
+    given: (d_w, d_bias), d_bias [N] float32 the sum of d_out over tokens.
+    accumulate adds to the d_w, and the d_bias, given."""
+    if d_w is not None:
+        dtype = d_w.dtype
+    if accumulate and (d_w is None or (bias and d_bias is None)):
+        raise ValueError("accumulate needs the d_w, and with bias the d_bias, to add to")
+    return _at(stream, (_fast or load_binding()).linear_dw, d_out, x, d_w, _dtype_number(dtype, "d_w"), bias,
+               d_bias, accumulate, workspace)
+
+
+def linear_workspace_bytes(tokens: int, n: int, k: int, x_aligned: bool = True, w_aligned: bool = True) -> int:
+    """aligned: on a 16-byte boundary, the row stride a multiple of 16 bytes and at least a row."""
+    return int(load().mhc_linear_workspace_bytes(tokens, n, k, int(x_aligned), int(w_aligned)))
+
+
+def linear_dx_workspace_bytes(tokens: int, n: int, k: int, d_out_aligned: bool = True, w_aligned: bool = True) -> int:
+    return int(load().mhc_linear_dx_workspace_bytes(tokens, n, k, int(d_out_aligned), int(w_aligned)))
+
+
+def linear_dw_workspace_bytes(tokens: int, n: int, k: int, d_out_aligned: bool = True, x_aligned: bool = True,
+                              bias: bool = False) -> int:
+    return int(load().mhc_linear_dw_workspace_bytes(tokens, n, k, int(d_out_aligned), int(x_aligned), int(bias)))
+
+
+def mhc_layer_norm(x, w=None, b=None, eps: float = 1e-5, *, out=None, stats=None, dtype=None, stream=None):
+    """Layer norm of each row: out = (x - mean) * rstd * w + b. x [T, H]
+    (float32, bfloat16 or float16, rows may be strided); w, b [H] of any of
+    these or None. out is of x's type, or of any beside a float32 x. Returns
+    (out, stats), stats [T, 2] float32 (mean, rstd) being what
+    mhc_layer_norm_backward needs beside x."""
+    return _at(stream, (_fast or load_binding()).layer_norm, x, w, b, eps, out, stats, _type_number(dtype, "out"))
+
+
+class LayerNormGrads(NamedTuple):
+    """Gradients of mhc_layer_norm's inputs; None where there is no such input."""
+    d_x: torch.Tensor
+    d_w: torch.Tensor | None
+    d_b: torch.Tensor | None
+
+
+def layer_norm_backward_workspace_bytes(tokens: int, hidden: int) -> int:
+    return int(load().mhc_layer_norm_backward_workspace_bytes(tokens, hidden))
+
+
+def mhc_layer_norm_backward(d_out, x, stats, w=None, *, bias: bool = True, d_residual=None, d_x=None,
+                            workspace=None, stream=None) -> LayerNormGrads:
+    """Gradients of mhc_layer_norm's inputs from that of out. x, stats, w as in
+    the forward call; bias: whether there was a b. d_residual [T, H] of x's
+    type is added to d_x: the gradient that reaches x past the norm; d_x may be
+    d_residual itself. d_w and d_b are float32 (parts of one allocation)."""
+    return LayerNormGrads._make(_at(stream, (_fast or load_binding()).layer_norm_backward, d_out, x, stats, w,
+                                    bias, d_residual, d_x, workspace))
+
+
+def orthogonalize_workspace_bytes(batch: int, m: int, n: int) -> int:
+    return int(load().mhc_orthogonalize_workspace_bytes(batch, m, n))
+
+
+def mhc_orthogonalize(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, *,
+                      dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """The orthogonalised update of a weight [M, N] (or of a batch [B, M, N]),
+    by `steps` Newton-Schulz products from X = g / (|g| + eps):
+
+        A = X X^T,   X <- (a I + b A + c A A) X      (a, b, c = coeffs)
+
+    which brings g's singular values towards 1. g is float32, bfloat16 or
+    float16, its rows contiguous; out is bfloat16 or float16. Between the
+    products every matrix is held in 22 bits. Returns out, of g's shape."""
+    if out is not None:
+        dtype = out.dtype
+    a, b, c = coeffs
+    return _at(stream, (_fast or load_binding()).orthogonalize, g, steps, a, b, c, eps, out,
+               _dtype_number(dtype, "out"), workspace)
