@@ -450,12 +450,10 @@ typedef enum {
 int mhc_linear_rows_aligned(const void *p, int64_t stride, int64_t rows, int n);
 
 /* Bytes of device scratch of mhc_linear, mhc_linear_dx and mhc_linear_dw: sums
- * of a split product, column sums (dw with a bias) and copies of operands that
- * are not aligned as above. 0 when T == 0 or the call would be refused for its sizes. */
+ * of a split product, and copies of operands that are not aligned as above. 0 when T == 0 or the call would be refused for its sizes. */
 size_t mhc_linear_workspace_bytes(int64_t tokens, int n, int k, int x_aligned, int w_aligned);
 size_t mhc_linear_dx_workspace_bytes(int64_t tokens, int n, int k, int d_out_aligned, int w_aligned);
-size_t mhc_linear_dw_workspace_bytes(int64_t tokens, int n, int k, int d_out_aligned, int x_aligned,
-                                     int bias);
+size_t mhc_linear_dw_workspace_bytes(int64_t tokens, int n, int k, int d_out_aligned, int x_aligned);
 
 /*
  * A projection with its epilogue:

@@ -616,7 +616,7 @@ PyObject *linear_dw(PyObject *, PyObject *const *a, Py_ssize_t n) {
         made.add_or(&d_w, tensor(a[2], "d_w", true), "d_w", {s.H, K}, scalar_of(type));
         if (bias.defined() || PyObject_IsTrue(a[4]) == 1) made.add_or(&d_bias, bias, "d_bias", {s.H}, at::kFloat);
         const bool with_bias = bias.defined() || PyObject_IsTrue(a[4]) == 1;
-        workspace_or(&workspace, g_lib.linear_dw_bytes(s.T, dr.width, width_of(K), dr.aligned, xr.aligned, with_bias), &made);
+        workspace_or(&workspace, g_lib.linear_dw_bytes(s.T, dr.width, width_of(K), dr.aligned, xr.aligned), &made);
         made.make();
         check(g_lib.linear_dw(d_out.data_ptr(), dr.stride, x.data_ptr(), xr.stride, mhc_type(t), s.T, dr.width, width_of(K),
                               d_w.data_ptr(), static_cast<mhc_dtype>(type), static_cast<float *>(ptr(d_bias)),

@@ -33,12 +33,6 @@ struct FewArgs {
     EpilogueArgs e;
 };
 
-__device__ __forceinline__ float load_at_rank(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_rank(addr, rank)) : "memory");
-    return v;
-}
-
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
@@ -53,9 +47,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     // the sums, [tokens][128], over the stages once nothing is on its way to them
     float *const sums = reinterpret_cast<float *>(basep);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int tile = blockIdx.x / a.split, rank = blockIdx.x - tile * a.split;
-    const int s0 = rank * a.per, s1 = min(s0 + a.per, a.steps), mine = max(s1 - s0, 0);
+    // steps of 64 of k in turn: what a cluster reads at a time lies together
+    const int mine = (a.steps - rank + a.split - 1) / a.split;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
@@ -79,12 +74,12 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         const uint64_t policy = policy_evict_normal();
         int it = 0;
         bool ok = true;
         for (; it < mine; ++it) {
-            const int s = it % a.stages, ph = (it / a.stages) & 1, k = (s0 + it) * kPairStep;
+            const int s = it % a.stages, ph = (it / a.stages) & 1, k = (it * a.split + rank) * kPairStep;
             if (!mbar_wait(empty + 8 * s, ph ^ 1, abort_flag, a.timeout_ns, a.status, SITE_F_EMPTY)) {
                 ok = false;
                 break;
@@ -108,7 +103,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             for (int k = it > a.stages ? it - a.stages : 0; k < it; ++k)
                 mbar_wait(full + 8 * (k % a.stages), (k / a.stages) & 1, &gave_up, a.timeout_ns, a.status, SITE_F_DRAIN);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
         bool ok = true;
         for (int it = 0; it < mine && ok; ++it) {
             const int s = it % a.stages;

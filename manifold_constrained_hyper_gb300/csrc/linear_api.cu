@@ -21,14 +21,17 @@ size_t copy_bytes(int64_t rows, int w, bool aligned) { return aligned ? 0 : up25
 bool on_runs(const void *p, mhc_dtype d) { return aligned(p, d == MHC_F32 ? 32 : 16); }
 
 // Operand `o` from rows that lie as they do, or from a copy of them at *at, which moves on past it.
-int operand(Operand *o, const void *p, int64_t stride, int64_t rows, int w, bool turned, uint8_t **at, int sms, bool pdl,
-            cudaStream_t s) {
+void operand(Operand *o, CopyJob *job, const void *p, int64_t stride, int64_t rows, int w, bool turned, uint8_t **at) {
     *o = {p, nullptr, rows == 1 ? pitch16(w) : stride, 0, turned};
-    if (mhc_linear_rows_aligned(p, stride, rows, w)) return MHC_OK;
-    void *const copy = *at;
+    *job = {};
+    if (mhc_linear_rows_aligned(p, stride, rows, w)) return;
+    *o = {*at, nullptr, pitch16(w), 0, turned};
+    *job = {p, stride, rows, w, *at, pitch16(w)};
     *at += copy_bytes(rows, w, false);
-    *o = {copy, nullptr, pitch16(w), 0, turned};
-    return note_launch(launch_copy_rows16(p, stride, rows, w, copy, pitch16(w), sms, pdl, s));
+}
+int copy(const CopyJob (&jobs)[2], int sms, bool pdl, cudaStream_t s) {
+    if (!jobs[0].rows && !jobs[1].rows) return MHC_OK;
+    return note_launch(launch_copy_rows16(jobs[0], jobs[1], sms, pdl, s));
 }
 
 // mhc_linear and mhc_linear_dx: x [T, k], w [n, k] or, turned, [k, n], into out [T, n].
@@ -56,9 +59,10 @@ mhc_status forward(const Forward &f, void *stream) {
     cudaStream_t const s = static_cast<cudaStream_t>(stream);
     uint8_t *at = static_cast<uint8_t *>(f.workspace);
     Product p = {};
-    if (int r = operand(&p.a, f.x, f.x_stride, f.T, f.k, false, &at, sms, pdl, s)) return static_cast<mhc_status>(r);
-    if (int r = operand(&p.b, f.w, f.w_stride, f.turned ? f.k : f.n, f.turned ? f.n : f.k, f.turned, &at, sms, pdl, s))
-        return static_cast<mhc_status>(r);
+    CopyJob jobs[2];
+    operand(&p.a, &jobs[0], f.x, f.x_stride, f.T, f.k, false, &at);
+    operand(&p.b, &jobs[1], f.w, f.w_stride, f.turned ? f.k : f.n, f.turned ? f.n : f.k, f.turned, &at);
+    if (int r = copy(jobs, sms, pdl, s)) return static_cast<mhc_status>(r);
     p.m = f.T;
     p.n = f.n;
     p.k = f.k;
@@ -84,10 +88,10 @@ size_t mhc_linear_workspace_bytes(int64_t tokens, int n, int k, int x_aligned, i
 size_t mhc_linear_dx_workspace_bytes(int64_t tokens, int n, int k, int d_out_aligned, int w_aligned) {
     return forward_bytes(tokens, k, n, d_out_aligned != 0, w_aligned != 0, true);
 }
-size_t mhc_linear_dw_workspace_bytes(int64_t tokens, int n, int k, int d_out_aligned, int x_aligned, int bias) {
+size_t mhc_linear_dw_workspace_bytes(int64_t tokens, int n, int k, int d_out_aligned, int x_aligned) {
     if (!sizes_ok(tokens, n, k)) return 0;
     return copy_bytes(tokens, n, d_out_aligned != 0) + copy_bytes(tokens, k, x_aligned != 0) +
-           (bias ? up256(column_sums_bytes(tokens, n)) : 0) + product_parts_bytes(n, k, tokens);
+           product_parts_bytes(n, k, tokens);
 }
 
 mhc_status mhc_linear(const void *x, int64_t x_stride, const void *w, int64_t w_stride, mhc_dtype dtype, int64_t tokens,
@@ -175,7 +179,7 @@ mhc_status mhc_linear_dw(const void *d_out, int64_t d_out_stride, const void *x,
     if (!aligned(d_out, 2) || !aligned(x, 2) || !aligned(d_w, size_of(d_w_dtype)) || !aligned(d_bias, 4) || !aligned(workspace, 16))
         return MHC_ERR_ALIGN;
     const bool da = mhc_linear_rows_aligned(d_out, d_out_stride, tokens, n), xa = mhc_linear_rows_aligned(x, x_stride, tokens, k);
-    const size_t need = mhc_linear_dw_workspace_bytes(tokens, n, k, da, xa, d_bias != nullptr);
+    const size_t need = mhc_linear_dw_workspace_bytes(tokens, n, k, da, xa);
     if (need && !workspace) return MHC_ERR_NULL;
     if (workspace_bytes < need) return MHC_ERR_WORKSPACE;
     Span ins[2] = {};
@@ -205,16 +209,14 @@ mhc_status mhc_linear_dw(const void *d_out, int64_t d_out_stride, const void *x,
     p.epi.accumulate = accumulate != 0;
     p.epi.wide = k % 8 == 0 && on_runs(d_w, d_w_dtype);
     if (tokens > 0) {
-        if (int r = operand(&p.a, d_out, d_out_stride, tokens, n, true, &at, sms, pdl, s)) return static_cast<mhc_status>(r);
-        if (int r = operand(&p.b, x, x_stride, tokens, k, true, &at, sms, pdl, s)) return static_cast<mhc_status>(r);
+        CopyJob jobs[2];
+        operand(&p.a, &jobs[0], d_out, d_out_stride, tokens, n, true, &at);
+        operand(&p.b, &jobs[1], x, x_stride, tokens, k, true, &at);
+        if (int r = copy(jobs, sms, pdl, s)) return static_cast<mhc_status>(r);
     }
-    if (d_bias) {
-        // of the copy where there is one: runs of 8
-        const void *const rows = tokens > 0 ? p.a.hi : nullptr;
-        if (int r = launch_column_sums(rows, p.a.pitch, dtype, tokens, n, d_bias, accumulate, reinterpret_cast<float *>(at), sms, pdl, s))
-            return static_cast<mhc_status>(r);
-        at += up256(column_sums_bytes(tokens, n));
-    }
+    // of the copy where there is one: runs of 8
+    if (d_bias)
+        if (int r = launch_column_sums(p.a.hi, p.a.pitch, dtype, tokens, n, d_bias, accumulate, pdl, s)) return static_cast<mhc_status>(r);
     p.parts = product_parts_bytes(n, k, tokens) ? reinterpret_cast<float *>(at) : nullptr;
     return static_cast<mhc_status>(launch_product(p, sms, status, pdl, s));
 }

@@ -68,13 +68,18 @@ int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cu
 constexpr int kFewTokens = 64;
 int launch_few_tokens(const Product &p, int sms, unsigned int *status, bool pdl, cudaStream_t s);
 
-// 16-bit rows to rows `pitch` apart, on 16-byte boundaries.
-cudaError_t launch_copy_rows16(const void *src, long long stride, long long rows, int n, void *dst, long long pitch, int sms,
-                               bool pdl, cudaStream_t s);
-// Sums over rows of a 16-bit [rows][n]: out[n] fp32 (accumulate: added). parts: column_sums_bytes().
-size_t column_sums_bytes(long long rows, int n);
-int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, float *parts,
-                       int sms, bool pdl, cudaStream_t s);
+// 16-bit rows to rows `pitch` apart, on 16-byte boundaries; two such jobs, either with no rows.
+struct CopyJob {
+    const void *src;
+    long long stride, rows;
+    int n;
+    void *dst;
+    long long pitch;
+};
+cudaError_t launch_copy_rows16(const CopyJob &a, const CopyJob &b, int sms, bool pdl, cudaStream_t s);
+// Sums over rows of a 16-bit [rows][n]: out[n] fp32 (accumulate: added).
+int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, bool pdl,
+                       cudaStream_t s);
 
 struct LayerNormArgs {
     long long T;

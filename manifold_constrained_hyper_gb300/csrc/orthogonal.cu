@@ -12,12 +12,13 @@
 //
 // G may lie in strided rows. A tall G is not turned: its Gram matrix is X^T X, the product reading both
 // operands with the summed axis outermost.
-#include "layer_norm.cuh"
+#include "orthogonal.h"
+#include "vec_io.cuh"
 
 namespace mhc {
 namespace {
 
-constexpr float kScale = 4096.f;
+constexpr float kScale = kNsScale;
 constexpr int kNormParts = 64;                      // shares of a matrix's squares
 constexpr int kRuns = 4;
 
@@ -25,7 +26,7 @@ struct Shape {
     int p, q;                       // the shorter and the longer side
     long long x_pitch, p_pitch;     // elements of a row of X, of A and P
     long long x_size, p_size;       // elements of one matrix
-    size_t parts_at, x_at, a_at, total;
+    size_t parts_at, x_at, a_at, sums_at, counters_at, total;
 };
 long long pitch8(long long w) { return (w + 7) / 8 * 8; }
 size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
@@ -40,7 +41,9 @@ Shape shape_of(int batch, int m, int n) {
     s.parts_at = 0;
     s.x_at = up256(static_cast<size_t>(batch) * kNormParts * 8);
     s.a_at = s.x_at + 4 * static_cast<size_t>(batch) * s.x_size * 2;
-    s.total = s.a_at + 4 * static_cast<size_t>(batch) * s.p_size * 2;
+    s.sums_at = s.a_at + 4 * static_cast<size_t>(batch) * s.p_size * 2;
+    s.counters_at = s.sums_at + kNsPartsBytes;
+    s.total = s.counters_at + up256(kNsCounters * 4);
     return s;
 }
 
@@ -48,9 +51,11 @@ Shape shape_of(int batch, int m, int n) {
 // leaves fp32's range, or its accurate part, is formed again in double throughout.
 template <class T>
 __global__ void __launch_bounds__(256) ns_norm_kernel(const T *g, long long row_stride, long long batch_stride, int m, int n, bool runs,
-                                                      double *parts) {
+                                                      double *parts, unsigned int *counters) {
     __shared__ double red[8];
     griddep_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < kNsCounters; i += 256) counters[i] = 0;
     const long long per_row = (n + 7) / 8, total = per_row * m;
     const T *const x = g + blockIdx.y * batch_stride;
     const long long step = static_cast<long long>(gridDim.x) * 256;
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(256) ns_split_kernel(const T *g, long long row
 }
 
 template <class T>
-int launch_start(const OrthogonalArgs &a, const Shape &sh, __half *hi, __half *lo, int sms, bool pdl, cudaStream_t s) {
+int launch_start(const OrthogonalArgs &a, const Shape &sh, const NsCall &c, int sms, bool pdl, cudaStream_t s) {
     const T *const g = static_cast<const T *>(a.g);
     const bool runs = a.n % 8 == 0 && a.row_stride % 8 == 0 && a.batch_stride % 8 == 0 &&
                       (reinterpret_cast<uintptr_t>(g) & (sizeof(T) == 4 ? 31u : 15u)) == 0;
@@ -156,12 +161,12 @@ int launch_start(const OrthogonalArgs &a, const Shape &sh, __half *hi, __half *l
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    if (int e = note_launch(cudaLaunchKernelEx(&cfg, ns_norm_kernel<T>, g, a.row_stride, a.batch_stride, a.m, a.n, runs, parts))) return e;
+    if (int e = note_launch(cudaLaunchKernelEx(&cfg, ns_norm_kernel<T>, g, a.row_stride, a.batch_stride, a.m, a.n, runs, parts, c.counters))) return e;
     long long blocks = (all + 255) / 256, cap = (8LL * sms + a.batch - 1) / a.batch;
     if (blocks > cap) blocks = cap;
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), a.batch);
     return note_launch(cudaLaunchKernelEx(&cfg, ns_split_kernel<T>, g, a.row_stride, a.batch_stride, a.m, a.n, runs, a.eps,
-                                          static_cast<const double *>(parts), static_cast<int>(count), hi, lo, sh.x_pitch, sh.x_size));
+                                          static_cast<const double *>(parts), static_cast<int>(count), c.x[0][0], c.x[0][1], sh.x_pitch, sh.x_size));
 }
 
 }  // namespace
@@ -171,72 +176,15 @@ size_t orthogonal_workspace(int batch, int m, int n) { return shape_of(batch, m,
 int launch_orthogonal(const OrthogonalArgs &a, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
     const Shape sh = shape_of(a.batch, a.m, a.n);
     uint8_t *const ws = static_cast<uint8_t *>(a.workspace);
-    __half *const x0 = reinterpret_cast<__half *>(ws + sh.x_at), *const p0 = reinterpret_cast<__half *>(ws + sh.a_at);
+    __half *const x = reinterpret_cast<__half *>(ws + sh.x_at), *const p = reinterpret_cast<__half *>(ws + sh.a_at);
     const long long xs = sh.x_size * a.batch, ps = sh.p_size * a.batch;
-    __half *x_hi = x0, *x_lo = x0 + xs, *y_hi = x0 + 2 * xs, *y_lo = x0 + 3 * xs;
-    __half *const a_hi = p0, *const a_lo = p0 + ps, *const p_hi = p0 + 2 * ps, *const p_lo = p0 + 3 * ps;
-    const int e = a.dtype == MHC_F32    ? launch_start<float>(a, sh, x_hi, x_lo, sms, pdl, s)
-                  : a.dtype == MHC_BF16 ? launch_start<__nv_bfloat16>(a, sh, x_hi, x_lo, sms, pdl, s)
-                                        : launch_start<__half>(a, sh, x_hi, x_lo, sms, pdl, s);
-    if (e) return e;
-    const bool wide = a.m <= a.n;
-    for (int step = 0; step < a.steps; ++step) {
-        Product g = {};
-        g.m = g.n = sh.p;
-        g.k = sh.q;
-        g.batch = a.batch;
-        g.symmetric = true;
-        g.a = g.b = {x_hi, x_lo, sh.x_pitch, sh.x_size, !wide};
-        g.kind = EPI_PAIR;
-        g.epi.unit = 1.f / kScale;
-        g.epi.hi = a_hi;
-        g.epi.lo = a_lo;
-        g.epi.pitch = sh.p_pitch;
-        g.epi.batch_stride = sh.p_size;
-        if (int r = launch_product(g, sms, status, pdl, s)) return r;
-
-        g.k = sh.p;
-        g.a = g.b = {a_hi, a_lo, sh.p_pitch, sh.p_size, false};
-        g.epi.unit = a.c / kScale;
-        g.epi.hi = p_hi;
-        g.epi.lo = p_lo;
-        g.epi.x_hi = a_hi;
-        g.epi.x_lo = a_lo;
-        g.epi.of_x = a.b;
-        g.epi.of_unit = a.a * kScale;
-        if (int r = launch_product(g, sms, status, pdl, s)) return r;
-
-        Product x = {};
-        x.m = a.m;
-        x.n = a.n;
-        x.k = sh.p;
-        x.batch = a.batch;
-        const Operand poly = {p_hi, p_lo, sh.p_pitch, sh.p_size, false};
-        x.a = wide ? poly : Operand{x_hi, x_lo, sh.x_pitch, sh.x_size, false};
-        x.b = wide ? Operand{x_hi, x_lo, sh.x_pitch, sh.x_size, true} : poly;
-        if (step + 1 < a.steps) {
-            x.kind = EPI_PAIR;
-            x.epi.unit = 1.f / kScale;
-            x.epi.hi = y_hi;
-            x.epi.lo = y_lo;
-            x.epi.pitch = sh.x_pitch;
-            x.epi.batch_stride = sh.x_size;
-        } else {
-            x.kind = EPI_LINEAR;
-            x.epi.unit = 1.f / (kScale * kScale);
-            x.epi.out = a.out;
-            x.epi.out_dtype = a.out_dtype;
-            x.epi.wide = a.n % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
-        }
-        if (int r = launch_product(x, sms, status, pdl, s)) return r;
-        __half *t = x_hi;
-        x_hi = y_hi;
-        y_hi = t;
-        t = x_lo;
-        x_lo = y_lo;
-        y_lo = t;
-    }
-    return MHC_OK;
+    NsCall c = {a.batch, a.m, a.n, a.steps, a.a, a.b, a.c, {{x, x + xs}, {x + 2 * xs, x + 3 * xs}}, {p, p + ps}, {p + 2 * ps, p + 3 * ps},
+                sh.x_pitch, sh.x_size, sh.p_pitch, sh.p_size, a.out, a.out_dtype, reinterpret_cast<float *>(ws + sh.sums_at),
+                reinterpret_cast<unsigned int *>(ws + sh.counters_at)};
+    const int e = a.dtype == MHC_F32    ? launch_start<float>(a, sh, c, sms, pdl, s)
+                  : a.dtype == MHC_BF16 ? launch_start<__nv_bfloat16>(a, sh, c, sms, pdl, s)
+                                        : launch_start<__half>(a, sh, c, sms, pdl, s);
+    return e ? e : launch_ns(c, status, s);
 }
 
 }  // namespace mhc

@@ -1,0 +1,685 @@
+// All the products of an orthogonalised update in one cooperative launch: pairs of CTAs stay on their
+// SMs and walk the products one after another, a barrier of the grid between two. Products with few
+// tiles split the summed axis over the pairs; those of a tile wait for one another's parts, and each
+// then adds them, in their order, for some of the tile's columns.
+//
+// A pair forms a 256 x 256 or 256 x 128 tile as the products with an epilogue do (64 of k a stage, six
+// stages, two buffers of sums in tensor memory); every operand is two fp16 parts, three products a step.
+// A symmetric result's tiles left of the diagonal are not formed: those right of it are stored twice,
+// the second time a column a store, which is contiguous across a warp's lanes.
+#include <atomic>
+#include <cmath>
+
+#include "epilogue.cuh"
+#include "mhc_internal.h"
+#include "orthogonal.h"
+#include "pair_mma.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr int kTile = 256;
+constexpr int kHalf = kTile / 2;
+constexpr int kStageBytes = 4 * kPairBoxBytes;
+constexpr int kStages = 5;
+constexpr int kSumWarps = 8;
+constexpr int kThreads = 64 + 32 * kSumWarps;
+constexpr int kBars = 2 * kStages + 7;
+constexpr int kOutBytes = 32 * 128;                 // 32 rows of 64 columns of 16 bits, of hi or of lo
+constexpr int kSmem = kStages * kStageBytes + 1024 + 2 * kSumWarps * kOutBytes + 256;
+constexpr int kTmemCols = 512;
+constexpr int kBand = 8;
+
+enum NsSite : int { SITE_N_EMPTY = 100, SITE_N_FULL, SITE_N_ACC_EMPTY, SITE_N_ACC_FULL, SITE_N_DRAIN, SITE_N_GRID, SITE_N_GO, SITE_N_MEET, SITE_N_PARTS };
+
+// One of the three products of a step.
+struct Phase {
+    int m, n;
+    int tiles_m, tiles_n, tile_n, steps, splits, per, items;
+    int symmetric, a_turned, b_turned;
+    uint32_t idesc;
+};
+struct NsArgs {
+    Phase phase[3];                 // A = X X^T, P = a I + b A + c A A, X <- P X
+    int batch, rounds;              // of the three
+    int wide;                       // X is the second operand of the third product, else the first
+    __half *x[2][2], *g[2], *p[2];  // [turn][hi, lo]
+    long long x_pitch, x_size, p_pitch, p_size;
+    float of_sum[3], of_a, of_unit[2], of_out;
+    void *out;
+    int out_dtype, out_wide;
+    float *parts;
+    unsigned int *counters;         // [0]: the grid's barrier; from 32 on, parts of a tile that are there
+    unsigned int *status;
+    unsigned long long timeout_ns;
+};
+struct NsMaps {
+    CUtensorMap gram_a[2][2], gram_b[2][2], last_x[2][2], poly_a[2], poly_b[2], last_p[2];
+    CUtensorMap to_x[2][2], to_g[2], to_p[2], to_out;   // 32 rows of 64 columns, to store
+};
+
+struct Place {
+    int batch, split, ti, tj, tile;
+};
+__device__ __forceinline__ Place place_of(const Phase &f, int item) {
+    Place p;
+    const int ratio = kTile / f.tile_n;
+    const int tiles = f.tiles_m * f.tiles_n - (f.symmetric ? ratio * (f.tiles_m * (f.tiles_m - 1) / 2) : 0);
+    p.tile = item / f.splits;
+    p.split = item - p.tile * f.splits;
+    p.batch = p.tile / tiles;
+    int r = p.tile - p.batch * tiles;
+    if (f.symmetric) {
+        p.ti = 0;
+        while (r >= f.tiles_n - ratio * p.ti) r -= f.tiles_n - ratio * p.ti++;
+        p.tj = ratio * p.ti + r;
+        return p;
+    }
+    const int band = r / (kBand * f.tiles_n), first = band * kBand;
+    const int rows = f.tiles_m - first < kBand ? f.tiles_m - first : kBand;
+    const int q = r - band * kBand * f.tiles_n;
+    p.tj = q / rows;
+    p.ti = first + q - p.tj * rows;
+    return p;
+}
+
+// Whether the count has come to `target`, within the limit.
+__device__ __forceinline__ bool count_wait(const unsigned int *count, unsigned int target, const NsArgs &a, volatile int *abort_flag, int site) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        unsigned int v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+        if (v >= target) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > a.timeout_ns) {
+            record_failure(a.status, 7, site);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+// Where a product's sums go: as hi + lo (and the mirrored place), or to the output.
+struct Target {
+    __half *hi, *lo;
+    long long pitch;
+    float unit;
+    const __half *x_hi, *x_lo;      // what is added, times of_x, and of_unit on the diagonal; or NULL
+    float of_x, of_unit;            // of_unit: where there is no x too
+    bool mirror, final;
+    int m, n;
+};
+// 16 columns of a row of x.
+struct X16 {
+    uint4 h[2], l[2];
+};
+__device__ __forceinline__ void load_x16(X16 &x, const Target &t, int i, int j) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        x.h[k] = x.l[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (!t.x_hi || i >= t.m || j + 8 * k >= t.n) continue;
+        const long long at = static_cast<long long>(i) * t.pitch + j + 8 * k;
+        x.h[k] = __ldcg(reinterpret_cast<const uint4 *>(t.x_hi + at));
+        x.l[k] = __ldcg(reinterpret_cast<const uint4 *>(t.x_lo + at));
+    }
+}
+// Eight sums of row i from column j on in two parts.
+__device__ __forceinline__ void pair8(const Target &t, int i, int j, const float *v, const uint4 &xh, const uint4 &xl, uint4 *hi, uint4 *lo) {
+    const __half *const tag = nullptr;
+    const uint32_t h4[4] = {xh.x, xh.y, xh.z, xh.w}, l4[4] = {xl.x, xl.y, xl.z, xl.w};
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint64_t r = mul2(f2_pack(v[2 * q], v[2 * q + 1]), splat2(t.unit));
+        if (t.x_hi) r = fma2(add2(unpack2(h4[q], tag), unpack2(l4[q], tag)), splat2(t.of_x), r);
+        if (t.of_unit != 0.f) r = add2(r, f2_pack(i == j + 2 * q ? t.of_unit : 0.f, i == j + 2 * q + 1 ? t.of_unit : 0.f));
+        hw[q] = pack2(r, tag);
+        lw[q] = pack2(fma2(unpack2(hw[q], tag), splat2(-1.f), r), tag);
+    }
+    *hi = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    *lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+}
+// The same eight at the mirrored place: a column of the warp's 32 rows a store.
+__device__ __forceinline__ void mirror8(const Target &t, int i, int j, const uint4 &hi, const uint4 &lo) {
+    const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+    const long long step = here(t.pitch);
+    uint16_t *h = reinterpret_cast<uint16_t *>(t.hi) + j * step + i, *l = reinterpret_cast<uint16_t *>(t.lo) + j * step + i;
+#pragma unroll
+    for (int q = 0; q < 8; ++q, h += step, l += step) {
+        if (j + q >= t.n) break;
+        *h = static_cast<uint16_t>(hw[q >> 1] >> (q & 1) * 16);
+        *l = static_cast<uint16_t>(lw[q >> 1] >> (q & 1) * 16);
+    }
+}
+__device__ __forceinline__ void tma_store_3d_plain(const CUtensorMap *m, int c0, int c1, int c2, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(src) : "memory");
+}
+// 64 columns of the warp's 32 rows, through shared memory (128-byte rows in the 128-byte swizzle) by TMA,
+// which writes whole lines; a row a lane to global memory would be 32 lines a store. `sums`: in tensor memory.
+__device__ __forceinline__ void put64(const NsArgs &a, const Target &t, const CUtensorMap *hi_map, const CUtensorMap *lo_map, int batch, int i0,
+                                      int j, uint32_t sums, uint32_t held) {
+    const int lane = threadIdx.x & 31, i = i0 + lane;
+    // the last pieces have been read
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+        X16 x[2];
+        load_x16(x[0], t, i, j + c);
+        load_x16(x[1], t, i, j + c + 16);
+        uint32_t u[32];
+        tmem_ld32_now(sums + c, u);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const uint32_t at = held + lane * 128 + (((c / 8 + h) ^ (lane & 7)) << 4);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[8 * h + e]);
+            if (t.final) {
+                uint32_t o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t r = f2_pack(v[2 * q] * a.of_out, v[2 * q + 1] * a.of_out);
+                    o[q] = a.out_dtype == MHC_BF16 ? bf2_pack_rn(r) : pack2(r, static_cast<const __half *>(nullptr));
+                }
+                st_shared_v4(at, make_uint4(o[0], o[1], o[2], o[3]));
+            } else {
+                uint4 hw, lw;
+                pair8(t, i, j + c + 8 * h, v, x[h / 2].h[h & 1], x[h / 2].l[h & 1], &hw, &lw);
+                st_shared_v4(at, hw);
+                st_shared_v4(at + kOutBytes, lw);
+                if (t.mirror && i < t.m && j + c + 8 * h < t.n) mirror8(t, i, j + c + 8 * h, hw, lw);
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_3d_plain(hi_map, j, i0, batch, held);
+        if (!t.final) tma_store_3d_plain(lo_map, j, i0, batch, held + kOutBytes);
+        bulk_commit();
+    }
+}
+// Columns [j, j + 16) of the warp's 32 rows from i0 on, a row a lane; `piece`: 32 x 17 floats of the warp.
+__device__ __forceinline__ void put16(const NsArgs &a, const Target &t, int batch, int i0, int j, float (&v)[16], const X16 &x, float *piece) {
+    const int lane = threadIdx.x & 31, i = i0 + lane;
+    if (!t.final) {
+        if (i >= t.m) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (j + 8 * h >= t.n) break;
+            uint4 hw, lw;
+            pair8(t, i, j + 8 * h, v + 8 * h, x.h[h], x.l[h], &hw, &lw);
+            const long long at = static_cast<long long>(i) * t.pitch + j + 8 * h;
+            *reinterpret_cast<uint4 *>(t.hi + at) = hw;
+            *reinterpret_cast<uint4 *>(t.lo + at) = lw;
+            if (t.mirror) mirror8(t, i, j + 8 * h, hw, lw);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] *= a.of_out;
+    const long long row0 = static_cast<long long>(batch) * t.m + i0;
+    if (a.out_wide) {
+        if (i >= t.m) return;
+        with_type(a.out_dtype, [&](auto tag) {
+            using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (j + 8 * h >= t.n) break;
+                float u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = v[8 * h + e];
+                store8(static_cast<T *>(a.out) + (row0 + lane) * t.n + j + 8 * h, run_of(u));
+            }
+        });
+        return;
+    }
+    // rows on any boundary: turned in shared memory, 16 columns of two rows a store
+#pragma unroll
+    for (int e = 0; e < 16; ++e) piece[lane * 17 + e] = v[e];
+    __syncwarp();
+    const int rows = t.m - i0 < 32 ? t.m - i0 : 32, col = lane & 15;
+    if (j + col < t.n)
+#pragma unroll 4
+        for (int r = lane >> 4; r < rows; r += 2) store_any(a.out, a.out_dtype, (row0 + r) * t.n + j + col, piece[r * 17 + col]);
+    __syncwarp();
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    uint8_t *const basep = raw + (base - smem_addr(raw));
+    const uint32_t bars = base + kStages * kStageBytes + 2 * kSumWarps * kOutBytes;
+    const uint32_t full = bars, empty = bars + 8 * kStages, acc_full = bars + 16 * kStages,
+                   acc_empty = acc_full + 16, drain = acc_full + 32,
+                   go = acc_full + 40 /* the grid's barrier is passed */, together = acc_full + 48 /* the epilogue's warps */;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + (bars - base) + 8 * kBars);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, phases = 3 * a.rounds;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full + 8 * b, 1);
+            mbar_init(acc_empty + 8 * b, 2 * kSumWarps);
+        }
+        mbar_init(drain, 1);
+        mbar_init(go, 1);
+        mbar_init(together, kSumWarps);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(tmem_slot)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+
+    if (warp == 0 && elect_one()) {
+        // ------------------------------------------------ loads, either CTA its halves
+        uint32_t it = 0;
+        bool ok = true;
+        for (int ph = 0; ph < phases && ok; ++ph) {
+            const int which = ph % 3, x = ph / 3 & 1;
+            const Phase &f = a.phase[which];
+            if (ph) {
+                // one thread a CTA asks, for the epilogue too
+                ok = count_wait(a.counters, ph * gridDim.x, a, abort_flag, SITE_N_GRID);
+                if (!ok) break;
+                fence_proxy_async_global();
+                mbar_arrive(go);
+            }
+            const CUtensorMap *const ma = which == 0   ? maps.gram_a[x]
+                                          : which == 1 ? maps.poly_a
+                                          : a.wide     ? maps.last_p
+                                                       : maps.last_x[x];
+            const CUtensorMap *const mb = which == 0   ? maps.gram_b[x]
+                                          : which == 1 ? maps.poly_b
+                                          : a.wide     ? maps.last_x[x]
+                                                       : maps.last_p;
+            const int half = f.tile_n / 2;
+            for (int item = pair; item < f.items && ok; item += pairs) {
+                const Place p = place_of(f, item);
+                const int s0 = p.split * f.per, s1 = s0 + f.per < f.steps ? s0 + f.per : f.steps;
+                const int ci = p.ti * kTile + static_cast<int>(rank) * kHalf, cj = p.tj * f.tile_n + static_cast<int>(rank) * half;
+                int kb = s0 / 3, part = s0 - 3 * kb;
+                for (int st = s0; st < s1; ++st, ++it) {
+                    const uint32_t s = it % kStages, turn_of = (it / kStages) & 1;
+                    if (!mbar_wait(empty + 8 * s, turn_of ^ 1, abort_flag, a.timeout_ns, a.status, SITE_N_EMPTY)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kPairBoxBytes * (half == kHalf ? 8 : 6));
+                    const uint32_t bar = map_to_rank(full + 8 * s, 0), da = base + s * kStageBytes, db = da + 2 * kPairBoxBytes;
+                    const int k = kb * kPairStep;
+                    const CUtensorMap *const am = ma + (part == 2), *const bm = mb + (part == 1);
+                    if (f.a_turned) {
+                        tma_load_pair_3d(da, am, ci, k, p.batch, bar);
+                        tma_load_pair_3d(da + kPairBoxBytes, am, ci + 64, k, p.batch, bar);
+                    } else {
+                        tma_load_pair_3d(da, am, k, ci, p.batch, bar);
+                    }
+                    if (f.b_turned) {
+                        tma_load_pair_3d(db, bm, cj, k, p.batch, bar);
+                        if (half == kHalf) tma_load_pair_3d(db + kPairBoxBytes, bm, cj + 64, k, p.batch, bar);
+                    } else {
+                        tma_load_pair_3d(db, bm, k, cj, p.batch, bar);
+                    }
+                    if (++part == 3) {
+                        part = 0;
+                        ++kb;
+                    }
+                }
+            }
+        }
+        // every stage's last release has arrived before this CTA may exit
+        for (uint32_t k = it > kStages ? it - kStages : 0; k < it && ok; ++k)
+            ok = mbar_wait(empty + 8 * (k % kStages), (k / kStages) & 1, abort_flag, a.timeout_ns, a.status, SITE_N_EMPTY);
+        if (!ok && rank == 0) {
+            // gave up: both CTAs' copies still in flight land before they exit
+            int gave_up = 0;
+            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
+                mbar_wait(full + 8 * (k % kStages), (k / kStages) & 1, &gave_up, a.timeout_ns, a.status, SITE_N_DRAIN);
+        }
+    } else if (warp == 1 && rank == 0 && elect_one()) {
+        // ------------------------------------------------ products, the leader for both
+        uint32_t it = 0, done = 0;
+        bool ok = true;
+        for (int ph = 0; ph < phases && ok; ++ph) {
+            const Phase &f = a.phase[ph % 3];
+            const uint64_t na = f.a_turned ? 2048 >> 4 : 32 >> 4, nb = f.b_turned ? 2048 >> 4 : 32 >> 4;
+            for (int item = pair; item < f.items && ok; item += pairs, ++done) {
+                const int split = item % f.splits, s0 = split * f.per, s1 = s0 + f.per < f.steps ? s0 + f.per : f.steps;
+                const uint32_t buf = done & 1, acc = tmem + buf * kTile;
+                // a barrier of the grid may lie between: as long as it may take
+                if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status, SITE_N_ACC_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int st = s0; st < s1; ++st, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!mbar_wait(full + 8 * s, (it / kStages) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_FULL)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = base + s * kStageBytes, sb = sa + 2 * kPairBoxBytes;
+                    const uint64_t da = f.a_turned ? desc_columns(sa) : desc_rows(sa), db = f.b_turned ? desc_columns(sb) : desc_rows(sb);
+#pragma unroll
+                    for (int q = 0; q < kPairStep / 16; ++q) mma_pair(acc, da + q * na, db + q * nb, f.idesc, st > s0 || q > 0);
+                    commit_pair(empty + 8 * s);
+                }
+                if (ok) commit_pair(acc_full + 8 * buf);
+            }
+        }
+        if (!ok) {
+            // the products issued end before tensor memory is freed
+            int gave_up = 0;
+            commit_pair(drain);
+            mbar_wait(drain, 0, &gave_up, a.timeout_ns, a.status, SITE_N_DRAIN);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------ epilogue, either CTA its 128 rows
+        const int quad = warp & 3, w = warp - 2;
+        const uint32_t held = base + kStages * kStageBytes + 2 * w * kOutBytes;     // this warp's hi, then lo
+        float *const piece = reinterpret_cast<float *>(basep + (held - base));
+        uint32_t done = 0, met = 0;
+        bool ok = true;
+        // the epilogue's warps wait for one another, within the limit
+        auto meet = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(together);
+            const bool all = mbar_wait(together, met++ & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_MEET);
+            return __all_sync(0xffffffffu, all) != 0;
+        };
+        for (int ph = 0; ph < phases && ok; ++ph) {
+            const int which = ph % 3, x = ph / 3 & 1;
+            const bool final = ph + 1 == phases;
+            const Phase &f = a.phase[which];
+            const int width = f.tile_n / 2, first = w / 4 * width;
+            if (ph) {
+                ok = mbar_wait(go, (ph - 1) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_GO);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
+            for (int item = pair; item < f.items && ok; item += pairs, ++done) {
+                const Place p = place_of(f, item);
+                const uint32_t buf = done & 1;
+                const int i0 = p.ti * kTile + static_cast<int>(rank) * kHalf + quad * 32, i = i0 + lane, j0 = p.tj * f.tile_n;
+                Target t;
+                const long long at = p.batch * (which == 2 ? a.x_size : a.p_size);
+                __half *const *const to_pair = which == 0 ? a.g : which == 1 ? a.p : a.x[x ^ 1];
+                t.hi = to_pair[0] + at;
+                t.lo = to_pair[1] + at;
+                t.pitch = which == 2 ? a.x_pitch : a.p_pitch;
+                t.unit = a.of_sum[which];
+                t.x_hi = which == 1 && a.of_a != 0.f ? a.g[0] + at : nullptr;
+                t.x_lo = a.g[1] + at;
+                t.of_x = a.of_a;
+                t.of_unit = which == 2 ? 0.f : a.of_unit[which];
+                t.mirror = f.symmetric && j0 >= (p.ti + 1) * kTile;
+                t.final = final;
+                t.m = f.m;
+                t.n = f.n;
+                ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_ACC_FULL);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sums = tmem + buf * kTile + first + (static_cast<uint32_t>(quad * 32) << 16);
+                if (f.splits == 1) {
+                    const CUtensorMap *const to = final ? &maps.to_out : which == 0 ? maps.to_g : which == 1 ? maps.to_p : maps.to_x[x ^ 1];
+#pragma unroll 1
+                    for (int c = 0; c < width && i0 < f.m && j0 + first + c < f.n; c += 64) {
+                        if (!final || a.out_wide) {
+                            put64(a, t, to, to + 1, p.batch, i0, j0 + first + c, sums + c, held);
+                            continue;
+                        }
+                        for (int k = c; k < c + 64 && j0 + first + k < f.n; k += 16) {
+                            uint32_t u[16];
+                            tmem_ld16_now(sums + k, u);
+                            float v[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[e]);
+                            put16(a, t, p.batch, i0, j0 + first + k, v, X16{}, piece);
+                        }
+                    }
+                } else {
+                    // the tile's parts, [split][column][128 rows], a column of 32 rows a store
+                    const long long part_size = static_cast<long long>(f.tile_n) * kHalf;
+                    float *const parts = a.parts + (static_cast<long long>(p.tile) * 2 + rank) * f.splits * part_size + quad * 32 + lane;
+                    float *const to = parts + p.split * part_size + first * kHalf;
+#pragma unroll 1
+                    for (int c = 0; c < width; c += 32) {
+                        uint32_t u[32];
+                        tmem_ld32_now(sums + c, u);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) __stcg(to + (c + e) * kHalf, __uint_as_float(u[e]));
+                    }
+                    // every part of the tile is there (its CTAs are all resident); each finishes some columns
+                    __threadfence();
+                    ok = meet();
+                    if (!ok) break;
+                    if (threadIdx.x == 64) {
+                        unsigned int *const count = a.counters + 32 + (which * kNsMostPairs + p.tile) * 2 + rank;
+                        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
+                        count_wait(count, f.splits * (ph / 3 + 1), a, abort_flag, SITE_N_PARTS);
+                    }
+                    ok = meet() && !*abort_flag;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    for (int g = p.split + f.splits * (w / 4); g < f.tile_n / 16; g += 2 * f.splits) {
+                        const int j = p.tj * f.tile_n + 16 * g;
+                        if (j >= f.n) break;
+                        X16 now;
+                        load_x16(now, t, i, j);
+                        float v[16] = {};
+                        for (int s0 = 0; s0 < f.splits; s0 += 4) {
+                            float u[4][16];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    u[q][e] = s0 + q < f.splits ? __ldcg(parts + (s0 + q) * part_size + (16 * g + e) * kHalf) : 0.f;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) v[e] += u[q][e];
+                        }
+                        put16(a, t, p.batch, i0, j, v, now, piece);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at_rank(map_to_rank(acc_empty + 8 * buf, 0));
+            }
+            if (!ok || final) break;
+            // what this CTA wrote, before it arrives: seen by other CTAs' loads of either kind
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
+            fence_proxy_async_global();
+            __threadfence();
+            ok = meet();
+            if (ok && threadIdx.x == 64) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counters) : "memory");
+        }
+    }
+    if (warp >= 2 && lane == 0) bulk_wait_all();
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// Pairs of CTAs that the device holds at once: 0 before it was asked.
+std::atomic<int> g_pairs[64];
+
+int resident_pairs(int *pairs) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
+    int n = g_pairs[dev & 63].load(std::memory_order_acquire);
+    if (!n) {
+        if (cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return MHC_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, ns_kernel, &cfg) != cudaSuccess || n < 1) return MHC_ERR_CUDA;
+        if (n > kNsMostPairs) n = kNsMostPairs;
+        g_pairs[dev & 63].store(n, std::memory_order_release);
+    }
+    *pairs = n;
+    return MHC_OK;
+}
+
+// Tiles of 128 columns, and the summed axis split, where there are few tiles.
+Phase phase_of(int m, int n, int k, int batch, bool symmetric, bool a_turned, bool b_turned, int pairs) {
+    Phase f = {};
+    f.m = m;
+    f.n = n;
+    f.symmetric = symmetric;
+    f.a_turned = a_turned;
+    f.b_turned = b_turned;
+    f.tiles_m = (m + kTile - 1) / kTile;
+    f.steps = 3 * ((k + kPairStep - 1) / kPairStep);
+    auto tiles = [&](int tile_n) {
+        const long long c = (n + tile_n - 1) / tile_n, all = f.tiles_m * c;
+        return batch * (symmetric ? all - kTile / tile_n * (static_cast<long long>(f.tiles_m) * (f.tiles_m - 1) / 2) : all);
+    };
+    // The cheapest of both tiles' widths and of splitting or not, by what a step of a pair takes (256
+    // columns 0.33 us, where the tensor cores are busy, 128 columns 0.22) and what joining parts costs (3.5 us).
+    double best = 1e30;
+    long long count = 0;
+    for (int tile_n : {kTile, kHalf}) {
+        const long long c = tiles(tile_n);
+        const int most = static_cast<int>(c <= pairs ? pairs / c : 1);
+        for (int s : {1, most < f.steps / 6 ? most : f.steps / 6}) {
+            if (s < 1 || s > tile_n / 16) continue;
+            const int per = (f.steps + s - 1) / s;
+            const double cost = static_cast<double>((c * s + pairs - 1) / pairs) * per * (tile_n == kTile ? 0.33 : 0.22) + (s > 1 ? 3.5 : 0.);
+            if (cost >= best) continue;
+            best = cost;
+            count = c;
+            f.tile_n = tile_n;
+            f.per = per;
+            f.splits = (f.steps + per - 1) / per;
+        }
+    }
+    f.tiles_n = (n + f.tile_n - 1) / f.tile_n;
+    f.items = static_cast<int>(count * f.splits);
+    f.idesc = (1u << 4) | ((a_turned ? 1u : 0u) << 15) | ((b_turned ? 1u : 0u) << 16) | (static_cast<uint32_t>(f.tile_n >> 3) << 17) |
+              (static_cast<uint32_t>(kTile >> 4) << 24);
+    return f;
+}
+
+}  // namespace
+
+int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
+    int pairs = 0;
+    if (int e = resident_pairs(&pairs)) return e;
+    const int p = c.m < c.n ? c.m : c.n, q = c.m < c.n ? c.n : c.m;
+    const bool wide = c.m <= c.n;
+    NsArgs a = {};
+    a.phase[0] = phase_of(p, p, q, c.batch, true, !wide, !wide, pairs);
+    a.phase[1] = phase_of(p, p, p, c.batch, true, false, false, pairs);
+    a.phase[2] = phase_of(c.m, c.n, p, c.batch, false, false, wide, pairs);
+    a.batch = c.batch;
+    a.rounds = c.steps;
+    a.wide = wide;
+    for (int h = 0; h < 2; ++h) {
+        a.x[0][h] = c.x[0][h];
+        a.x[1][h] = c.x[1][h];
+        a.g[h] = c.g[h];
+        a.p[h] = c.p[h];
+    }
+    a.x_pitch = c.x_pitch;
+    a.x_size = c.x_size;
+    a.p_pitch = c.p_pitch;
+    a.p_size = c.p_size;
+    a.of_sum[0] = a.of_sum[2] = 1.f / kNsScale;
+    a.of_sum[1] = c.c / kNsScale;
+    // a I + b A + c A A = c (A + h I)^2 + (a - c h^2) I with h = b / 2c: A is kept with h on its diagonal and is not
+    // read again. Where c h^2 is far above the coefficients that would cancel, and b A is added instead.
+    const double h = c.c != 0.f ? c.b / (2. * c.c) : 0., square = c.c * h * h;
+    if (c.c != 0.f && std::fabs(square) <= 4. * (std::fabs(c.a) + std::fabs(c.b) + std::fabs(c.c)) && std::fabs(h) <= 8.) {
+        a.of_unit[0] = static_cast<float>(h * kNsScale);
+        a.of_unit[1] = static_cast<float>((c.a - square) * kNsScale);
+    } else {
+        a.of_a = c.b;
+        a.of_unit[1] = c.a * kNsScale;
+    }
+    a.of_out = 1.f / (kNsScale * kNsScale);
+    a.out = c.out;
+    a.out_dtype = c.out_dtype;
+    a.out_wide = c.n % 8 == 0 && (reinterpret_cast<uintptr_t>(c.out) & 15u) == 0;
+    a.parts = c.parts;
+    a.counters = c.counters;
+    a.status = status;
+    a.timeout_ns = wait_timeout_ns();
+    NsMaps maps = {};
+    auto rows = [&](CUtensorMap *m, const __half *x, int inner, int count, long long pitch, long long size, int box) {
+        return encode_matrices16(m, false, x, inner, count, c.batch, pitch * 2, size * 2, box);
+    };
+    bool ok = true;
+    for (int h = 0; h < 2; ++h) {
+        for (int t = 0; t < 2; ++t) {
+            ok = ok && rows(&maps.gram_a[t][h], c.x[t][h], c.n, c.m, c.x_pitch, c.x_size, wide ? kHalf : kPairStep);
+            ok = ok && rows(&maps.gram_b[t][h], c.x[t][h], c.n, c.m, c.x_pitch, c.x_size, wide ? a.phase[0].tile_n / 2 : kPairStep);
+            ok = ok && rows(&maps.last_x[t][h], c.x[t][h], c.n, c.m, c.x_pitch, c.x_size, wide ? kPairStep : kHalf);
+        }
+        ok = ok && rows(&maps.poly_a[h], c.g[h], p, p, c.p_pitch, c.p_size, kHalf);
+        ok = ok && rows(&maps.poly_b[h], c.g[h], p, p, c.p_pitch, c.p_size, a.phase[1].tile_n / 2);
+        ok = ok && rows(&maps.last_p[h], c.p[h], p, p, c.p_pitch, c.p_size, wide ? kHalf : a.phase[2].tile_n / 2);
+    }
+    for (int h = 0; h < 2; ++h) {
+        for (int t = 0; t < 2; ++t) ok = ok && rows(&maps.to_x[t][h], c.x[t][h], c.n, c.m, c.x_pitch, c.x_size, 32);
+        ok = ok && rows(&maps.to_g[h], c.g[h], p, p, c.p_pitch, c.p_size, 32);
+        ok = ok && rows(&maps.to_p[h], c.p[h], p, p, c.p_pitch, c.p_size, 32);
+    }
+    if (a.out_wide)
+        ok = ok && encode_matrices16(&maps.to_out, c.out_dtype == MHC_BF16, c.out, c.n, c.m, c.batch, static_cast<unsigned long long>(c.n) * 2,
+                                     static_cast<unsigned long long>(c.m) * c.n * 2, 32);
+    if (!ok) return MHC_ERR_CUDA;
+    int most = 0;
+    for (const Phase &f : a.phase) most = most > f.items ? most : f.items;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(most < pairs ? most : pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return note_launch(cudaLaunchKernelEx(&cfg, ns_kernel, maps, a));
+}
+
+}  // namespace mhc

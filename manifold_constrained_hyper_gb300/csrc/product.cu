@@ -44,7 +44,7 @@ struct Args {
     int chain;                      // steps between two additions in registers
     int passes;                     // products a step: 1, or 3 of operands in two parts
     int symmetric;                  // tiles left of the diagonal are mirrored, not formed
-    long long items;
+    int items;
     int a_turned, b_turned;
     uint32_t idesc;
     unsigned int *status;
@@ -60,25 +60,24 @@ struct Place {
 
 // Work item -> its matrix, part of the summed axis and tile. Tiles are walked in bands of kBand rows, so
 // that those in flight share columns of both operands in L2; symmetric ones row by row from the diagonal.
-__device__ __forceinline__ Place place_of(const Args &a, long long item) {
+__device__ __forceinline__ Place place_of(const Args &a, int item) {
     Place p;
     if (a.symmetric) {
         const int ratio = kTile / a.tile_n;
         const int tiles = a.tiles_m * a.tiles_n - ratio * (a.tiles_m * (a.tiles_m - 1) / 2);
-        p.batch = static_cast<int>(item / tiles);
-        int r = static_cast<int>(item - static_cast<long long>(p.batch) * tiles);
+        p.batch = item / tiles;
+        int r = item - p.batch * tiles;
         p.split = p.ti = 0;
         while (r >= a.tiles_n - ratio * p.ti) r -= a.tiles_n - ratio * p.ti++;
         p.tj = ratio * p.ti + r;
         return p;
     }
-    const long long tiles = static_cast<long long>(a.tiles_m) * a.tiles_n, which = item / tiles;
-    p.batch = static_cast<int>(which / a.splits);
-    p.split = static_cast<int>(which - static_cast<long long>(p.batch) * a.splits);
-    const long long r = item - which * tiles;
-    const int band = static_cast<int>(r / (kBand * a.tiles_n)), first = band * kBand;
+    const int tiles = a.tiles_m * a.tiles_n, which = item / tiles;
+    p.batch = which / a.splits;
+    p.split = which - p.batch * a.splits;
+    const int r = item - which * tiles, band = r / (kBand * a.tiles_n), first = band * kBand;
     const int rows = a.tiles_m - first < kBand ? a.tiles_m - first : kBand;
-    const int q = static_cast<int>(r - static_cast<long long>(band) * kBand * a.tiles_n);
+    const int q = r - band * kBand * a.tiles_n;
     p.tj = q / rows;
     p.ti = first + q - p.tj * rows;
     return p;
@@ -87,115 +86,53 @@ __device__ __forceinline__ Place place_of(const Args &a, long long item) {
 __device__ __forceinline__ uint64_t pair_of(const uint32_t (&v)[32], int e) {
     return (static_cast<uint64_t>(v[e + 1]) << 32) | v[e];
 }
-// Columns [j, j + 32) of row i, whose elements lie on the boundaries of runs of 8 (n is a multiple of
-// 8): the whole epilogue of them. `row` is the row's first element in a contiguous output.
-template <int KIND>
-__device__ __forceinline__ void finish_row(const Args &a, long long i, long long row, int j, uint32_t (&v)[32]) {
-    const EpilogueArgs &e = a.e;
-    if constexpr (KIND == EPI_LINEAR) {
-        const uint64_t unit = splat2(e.unit);
-#pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-            if (j + c >= a.n) break;
-            Run r;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) r.p[q] = mul2(pair_of(v, c + 2 * q), unit);
-            if (e.bias) {
-                const Run b = load_run(e.bias, e.bias_dtype, j + c);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) r.p[q] = add2(r.p[q], b.p[q]);
-            }
-            if (e.z) store_run(e.z, e.z_dtype, row + j + c, r);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                v[c + 2 * q] = static_cast<uint32_t>(r.p[q]);
-                v[c + 2 * q + 1] = static_cast<uint32_t>(r.p[q] >> 32);
-            }
-        }
-        if (e.act != MHC_LINEAR_NONE)
-            with_act(e.act, [&](auto act) {
-#pragma unroll
-                for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(act_value<decltype(act)::value>(__uint_as_float(v[q])));
-            });
-    }
-#pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-        if (j + c >= a.n) break;
-        Run r;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) r.p[q] = pair_of(v, c + 2 * q);
-        if constexpr (KIND == EPI_LINEAR) {
-            if (e.residual) {
-                const Run x = load_run(e.residual, e.residual_dtype, i * e.residual_stride + j + c);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) r.p[q] = add2(r.p[q], x.p[q]);
-            }
-        } else if constexpr (KIND == EPI_SLOPE) {
-            const Run z = load_run(e.z, e.z_dtype, i * e.z_stride + j + c);
-            with_act(e.act, [&](auto act) {
-                constexpr int ACT = decltype(act)::value;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    r.p[q] = mul2(r.p[q], f2_pack(act_slope<ACT>(f2_lo(z.p[q])), act_slope<ACT>(f2_hi(z.p[q]))));
-            });
-        } else if (e.accumulate) {
-            const Run x = load_run(e.out, e.out_dtype, row + j + c);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) r.p[q] = add2(x.p[q], r.p[q]);
-        }
-        store_run(e.out, e.out_dtype, row + j + c, r);
-    }
-}
 // PAIR: columns [j, j + 32) of row i as hi + lo; mirror: at the transposed place too, a column a store
-// of 32 rows (i0 the first of the warp's 32 rows, all of which hold sums).
-__device__ __forceinline__ void finish_pair(const Args &a, int batch, long long i, int j, bool mirror, const uint32_t (&v)[32]) {
+// of 32 rows. x: the row's 16 words of hi, then of lo, where there is an x.
+__device__ __forceinline__ void load_pair(Raw &x, const Args &a, int batch, long long i, int j) {
+    const EpilogueArgs &e = a.e;
+    if (!e.x_hi || i >= a.m) return;
+    const long long at = static_cast<long long>(batch) * e.batch_stride + i * e.pitch + j;
+    const Piece p = {true, a.n - j};
+    Raw lo = {};
+    load_raw(x, p, e.x_hi, MHC_F16, at, 0);
+    load_raw(lo, p, e.x_lo, MHC_F16, at, 0);
+#pragma unroll
+    for (int q = 0; q < 16; ++q) x.w[16 + q] = lo.w[q];
+}
+__device__ __forceinline__ void finish_pair(const Args &a, int batch, long long i, int j, bool mirror, const uint32_t (&v)[32], const Raw &x) {
     const EpilogueArgs &e = a.e;
     const long long base = static_cast<long long>(batch) * e.batch_stride;
     __half *const hi = static_cast<__half *>(e.hi) + base, *const lo = static_cast<__half *>(e.lo) + base;
     const uint64_t unit = splat2(e.unit);
+    uint32_t hw[16], lw[16];
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-        if (j + c >= a.n) break;
-        Run r;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) r.p[q] = mul2(pair_of(v, c + 2 * q), unit);
-        const long long at = i * e.pitch + j + c;
+    for (int q = 0; q < 16; ++q) {
+        uint64_t r = mul2(pair_of(v, 2 * q), unit);
         if (e.x_hi) {
-            Run xh = run_splat(0.f), xl = xh;
-            if (i < a.m) {
-                xh = load8(static_cast<const __half *>(e.x_hi) + base + at);
-                xl = load8(static_cast<const __half *>(e.x_lo) + base + at);
-            }
-            const uint64_t f = splat2(e.of_x);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) r.p[q] = fma2(add2(xh.p[q], xl.p[q]), f, r.p[q]);
+            const __half *const tag = nullptr;
+            r = fma2(add2(unpack2(x.w[q], tag), unpack2(x.w[16 + q], tag)), splat2(e.of_x), r);
             // the unit matrix
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                r.p[q] = add2(r.p[q], f2_pack(i == j + c + 2 * q ? e.of_unit : 0.f, i == j + c + 2 * q + 1 ? e.of_unit : 0.f));
+            r = add2(r, f2_pack(i == j + 2 * q ? e.of_unit : 0.f, i == j + 2 * q + 1 ? e.of_unit : 0.f));
         }
-        uint4 hw, lw;
-        uint32_t *const hp = &hw.x, *const lp = &lw.x;
+        hw[q] = pack2(r, static_cast<const __half *>(nullptr));
+        lw[q] = pack2(fma2(unpack2(hw[q], static_cast<const __half *>(nullptr)), splat2(-1.f), r), static_cast<const __half *>(nullptr));
+    }
+    if (i >= a.m) return;
+    const long long at = i * e.pitch + j;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            hp[q] = pack2(r.p[q], static_cast<const __half *>(nullptr));
-            const uint64_t back = unpack2(hp[q], static_cast<const __half *>(nullptr));
-            lp[q] = pack2(fma2(back, splat2(-1.f), r.p[q]), static_cast<const __half *>(nullptr));
-        }
-        if (i < a.m) {
-            *reinterpret_cast<uint4 *>(hi + at) = hw;
-            *reinterpret_cast<uint4 *>(lo + at) = lw;
-            if (mirror) {
+    for (int c = 0; c < 4; ++c) {
+        if (j + 8 * c >= a.n) break;
+        *reinterpret_cast<uint4 *>(hi + at + 8 * c) = make_uint4(hw[4 * c], hw[4 * c + 1], hw[4 * c + 2], hw[4 * c + 3]);
+        *reinterpret_cast<uint4 *>(lo + at + 8 * c) = make_uint4(lw[4 * c], lw[4 * c + 1], lw[4 * c + 2], lw[4 * c + 3]);
+    }
+    if (!mirror) return;
+    uint16_t *h = reinterpret_cast<uint16_t *>(hi) + j * e.pitch + i, *l = reinterpret_cast<uint16_t *>(lo) + j * e.pitch + i;
+    const long long step = here(e.pitch);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    if (j + c + q >= a.n) break;
-                    const long long to = static_cast<long long>(j + c + q) * e.pitch + i;
-                    const uint32_t sh = (q & 1) * 16;
-                    reinterpret_cast<uint16_t *>(hi)[to] = static_cast<uint16_t>(hp[q >> 1] >> sh);
-                    reinterpret_cast<uint16_t *>(lo)[to] = static_cast<uint16_t>(lp[q >> 1] >> sh);
-                }
-            }
-        }
+    for (int q = 0; q < 32; ++q, h += step, l += step) {
+        if (j + q >= a.n) break;
+        *h = static_cast<uint16_t>(hw[q >> 1] >> (q & 1) * 16);
+        *l = static_cast<uint16_t>(lw[q >> 1] >> (q & 1) * 16);
     }
 }
 
@@ -211,7 +148,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + kStages * kStageBytes + 8 * kBars);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *const turn = reinterpret_cast<float *>(basep + kStages * kStageBytes + 256);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -242,11 +179,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         // ------------------------------------------------ loads, either CTA its halves
         uint32_t it = 0;
         bool ok = true;
-        for (long long item = pair; item < a.items && ok; item += pairs) {
+        for (int item = pair; item < a.items && ok; item += pairs) {
             const Place p = place_of(a, item);
             const int s0 = p.split * a.steps_per_split;
             const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
@@ -290,11 +227,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
             for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
                 mbar_wait(full + 8 * (k % kStages), (k / kStages) & 1, &gave_up, a.timeout_ns, a.status, SITE_P_DRAIN);
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
         // ------------------------------------------------ products, the leader for both
         uint32_t it = 0, done = 0;
         bool ok = true;
-        for (long long item = pair; item < a.items && ok; item += pairs) {
+        for (int item = pair; item < a.items && ok; item += pairs) {
             const Place p = place_of(a, item);
             const int s0 = p.split * a.steps_per_split;
             const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
@@ -340,10 +277,30 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
         float *const piece = turn + (warp - 2) * 32 * 33;
         uint32_t done = 0;
         bool ok = true;
-        for (long long item = pair; item < a.items && ok; item += pairs) {
+        for (int item = pair; item < a.items && ok; item += pairs) {
             const Place p = place_of(a, item);
             const int s0 = p.split * a.steps_per_split;
             const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
+            const long long i = static_cast<long long>(p.ti) * kTile + static_cast<int>(rank) * kHalf + quad * 32 + lane;
+            // the output's matrices follow one another, and so do the splits' sums
+            const long long row = ((static_cast<long long>(p.batch) * a.splits + p.split) * a.m + i) * a.n;
+            const int j0 = p.tj * a.tile_n + first;
+            auto piece_at = [&](int j) {
+                if (a.e.wide) return Piece{true, i < a.m ? a.n - j : 0};
+                const long long rows = a.m - (i - lane);
+                return Piece{false, j + lane >= a.n ? 0 : rows < 32 ? static_cast<int>(rows) : 32};
+            };
+            // what the piece from column j on is combined with
+            auto ahead = [&](Raw &r, float &bias, int j) {
+                if constexpr (KIND == EPI_PAIR) {
+                    load_pair(r, a, p.batch, i, j);
+                } else {
+                    const bool wide = a.e.wide;
+                    if (KIND == EPI_LINEAR && a.e.bias && j + lane < a.n) bias = load_any(a.e.bias, a.e.bias_dtype, j + lane);
+                    load_extra<KIND>(r, piece_at(j), a.e, wide ? i : i - lane, wide ? j : j + lane,
+                                     wide ? row + j : row - static_cast<long long>(lane) * a.n + j + lane, a.n);
+                }
+            };
             uint64_t sum[4][16];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -381,37 +338,41 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
                 if (lane == 0) arrive_at_rank(map_to_rank(acc_empty + 8 * buf, 0));
             }
             if (!ok) break;
-            const long long i = static_cast<long long>(p.ti) * kTile + static_cast<int>(rank) * kHalf + quad * 32 + lane;
-            // the output's matrices follow one another, and so do the splits' sums
-            const long long row = ((static_cast<long long>(p.batch) * a.splits + p.split) * a.m + i) * a.n;
+            // the sums' registers are free from here on: a piece's operands are on their way while the one
+            // before is finished
+            Raw extra = {};
+            float bias = 0.f;
+            if (j0 < a.n) ahead(extra, bias, j0);
             const bool mirror = a.symmetric && p.tj * a.tile_n >= (p.ti + 1) * kTile;
 #pragma unroll 1
             for (int c = 0; c < width; c += 32) {
-                const int j = p.tj * a.tile_n + first + c;
+                const int j = j0 + c;
                 if (j >= a.n) break;
                 uint32_t v[32];
                 tmem_ld32_now(part + c, v);
+                Raw next = {};
+                float next_bias = 0.f;
+                if (c + 32 < width && j + 32 < a.n) ahead(next, next_bias, j + 32);
                 if constexpr (KIND == EPI_PAIR) {
-                    finish_pair(a, p.batch, i, j, mirror, v);
+                    finish_pair(a, p.batch, i, j, mirror, v, extra);
                 } else {
+                    float f[32];
                     if (a.e.wide) {
-                        if (i < a.m) finish_row<KIND>(a, i, row, j, v);
-                        continue;
-                    }
-                    // rows on any boundary: the piece turned in shared memory, then a row a store
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) piece[lane * 33 + e] = __uint_as_float(v[e]);
-                    __syncwarp();
-                    const long long i0 = i - lane;
-                    const int rows = a.m - i0 < 32 ? static_cast<int>(a.m - i0) : 32;
-                    if (j + lane < a.n) {
-                        const long long at = row - static_cast<long long>(lane) * a.n + j + lane;
-#pragma unroll 2
-                        for (int r = 0; r < rows; ++r)
-                            finish_element<KIND>(a.e, i0 + r, at + static_cast<long long>(r) * a.n, j + lane, piece[r * 33 + lane]);
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
+                    } else {
+                        // rows on any boundary: turned in shared memory, then a column a lane
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) piece[lane * 33 + e] = __uint_as_float(v[e]);
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = piece[e * 33 + lane];
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    finish_piece<KIND>(piece_at(j), a.e, a.e.wide ? row + j : row - static_cast<long long>(lane) * a.n + j + lane, a.n, bias, f, extra);
                 }
+                extra = next;
+                bias = next_bias;
             }
             tc_fence_before();
             __syncwarp();
@@ -496,39 +457,54 @@ __global__ void __launch_bounds__(256) product_join_kernel(const float *parts, i
     }
 }
 
-__global__ void __launch_bounds__(256) copy_rows16_kernel(const uint16_t *src, long long stride, long long rows, int n,
-                                                          uint16_t *dst, long long pitch) {
+// Rows of either job in runs of 8, the second job's after the first's.
+__global__ void __launch_bounds__(256) copy_rows16_kernel(const CopyJob a, const CopyJob b) {
     griddep_wait();
-    const long long per_row = (n + 7) / 8, total = rows * per_row;
+    const long long per_a = (a.n + 7) / 8, per_b = (b.n + 7) / 8, first = a.rows * per_a, total = first + b.rows * per_b;
     for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<long long>(gridDim.x) * 256) {
-        const long long t = i / per_row;
-        const int c = static_cast<int>(i - t * per_row) * 8;
-        const uintptr_t row = reinterpret_cast<uintptr_t>(src + t * stride);
+        const bool second = i >= first;
+        const CopyJob &job = second ? b : a;
+        const long long k = second ? i - first : i, per_row = second ? per_b : per_a;
+        const long long t = total < (1ll << 31) ? static_cast<unsigned>(k) / static_cast<unsigned>(per_row) : k / per_row;
+        const int c = static_cast<int>(k - t * per_row) * 8;
+        const uintptr_t row = reinterpret_cast<uintptr_t>(static_cast<const uint16_t *>(job.src) + t * job.stride);
         uint64_t v[2];
-        load_words<2>(row + 2 * c, row + 2 * static_cast<uintptr_t>(n), v);
-        *reinterpret_cast<uint4 *>(dst + t * pitch + c) =
+        load_words<2>(row + 2 * c, row + 2 * static_cast<uintptr_t>(job.n), v);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(job.dst) + t * job.pitch + c) =
             make_uint4(static_cast<uint32_t>(v[0]), static_cast<uint32_t>(v[0] >> 32), static_cast<uint32_t>(v[1]),
                        static_cast<uint32_t>(v[1] >> 32));
     }
 }
 
-// Sums over rows: a CTA takes 64 columns (8 lanes of 8) of a share of the rows, 32 of them at a time.
-constexpr int kSumColumns = 64, kSumParts = 64;
+// Sums over rows: a cluster of CTAs takes 64 columns (8 lanes of 8 each, 32 rows at a time), each a share of
+// the rows; their sums meet in distributed shared memory, in the order of the shares.
+constexpr int kSumColumns = 64, kSumSplit = 8;
 template <class T>
-__global__ void __launch_bounds__(256) column_sums_kernel(const T *x, long long stride, long long rows, int n, bool runs,
-                                                          float *parts) {
-    __shared__ float red[32][kSumColumns + 1];
+__global__ void __launch_bounds__(256) column_sums_kernel(const T *x, long long stride, long long rows, int n, bool runs, float *out,
+                                                          int accumulate) {
+    __shared__ float red[32][kSumColumns + 1], mine[kSumColumns];
     griddep_wait();
-    const int lane = threadIdx.x & 7, row0 = threadIdx.x >> 3, c = blockIdx.x * kSumColumns + lane * 8;
-    const long long share = (rows + gridDim.y - 1) / gridDim.y, r0 = share * blockIdx.y, r1 = r0 + share < rows ? r0 + share : rows;
+    const int rank = blockIdx.x % kSumSplit, first = blockIdx.x / kSumSplit * kSumColumns;
+    const int lane = threadIdx.x & 7, row0 = threadIdx.x >> 3, c = first + lane * 8;
+    const long long share = (rows + kSumSplit - 1) / kSumSplit, r0 = share * rank, r1 = r0 + share < rows ? r0 + share : rows;
     Run s = run_splat(0.f);
-    if (c < n)
-#pragma unroll 4
-        for (long long r = r0 + row0; r < r1; r += 32) {
-            const Run v = runs ? load8(x + r * stride + c) : load8_any(x + r * stride, c, n);
+    if (c < n) {
+        if (runs) {
+#pragma unroll 8
+            for (long long r = r0 + row0; r < r1; r += 32) {
+                const Run v = load8(x + r * stride + c);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) s.p[q] = add2(s.p[q], v.p[q]);
+                for (int q = 0; q < 4; ++q) s.p[q] = add2(s.p[q], v.p[q]);
+            }
+        } else {
+#pragma unroll 4
+            for (long long r = r0 + row0; r < r1; r += 32) {
+                const Run v = load8_any(x + r * stride, c, n);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) s.p[q] = add2(s.p[q], v.p[q]);
+            }
         }
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) red[row0][lane * 8 + e] = run_at(s, e);
     __syncthreads();
@@ -536,24 +512,22 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const T *x, long long 
         float v = 0.f;
 #pragma unroll
         for (int r = 0; r < 32; ++r) v += red[r][threadIdx.x];
-        const int j = blockIdx.x * kSumColumns + threadIdx.x;
-        if (j < n) parts[static_cast<long long>(blockIdx.y) * n + j] = v;
+        mine[threadIdx.x] = v;
     }
-}
-__global__ void __launch_bounds__(256) column_join_kernel(const float *parts, int count, int n, float *out, int accumulate) {
-    griddep_wait();
-    const int j = blockIdx.x * 256 + threadIdx.x;
-    if (j >= n) return;
-    float v = 0.f;
-#pragma unroll 8
-    for (int p = 0; p < count; ++p) v += parts[static_cast<long long>(p) * n + j];
-    out[j] = accumulate ? out[j] + v : v;
-}
-int sum_parts(long long rows, int n) {
-    const long long columns = (n + kSumColumns - 1) / kSumColumns, by_rows = (rows + 127) / 128;
-    long long p = (4 * kGridCap + columns - 1) / columns;
-    if (p > by_rows) p = by_rows;
-    return static_cast<int>(p > kSumParts ? kSumParts : p < 1 ? 1 : p);
+    __syncthreads();
+    cluster_sync();
+    constexpr int kEach = kSumColumns / kSumSplit;
+    if (threadIdx.x < kEach) {
+        const int k = rank * kEach + threadIdx.x;
+        float part[kSumSplit], v = 0.f;
+#pragma unroll
+        for (int p = 0; p < kSumSplit; ++p) part[p] = load_at_rank(smem_addr(mine + k), p);
+#pragma unroll
+        for (int p = 0; p < kSumSplit; ++p) v += part[p];
+        if (first + k < n) out[first + k] = accumulate ? out[first + k] + v : v;
+    }
+    __syncwarp();
+    cluster_sync();         // no CTA's sums go while another reads them
 }
 
 std::atomic<int> g_smem[64];
@@ -626,8 +600,10 @@ int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cu
     a.passes = passes;
     a.symmetric = p.symmetric;
     const long long all = static_cast<long long>(q.tiles_m) * q.tiles_n;
-    a.items = p.symmetric ? p.batch * (all - static_cast<long long>(kTile / q.tile_n) * q.tiles_m * (q.tiles_m - 1) / 2)
-                          : p.batch * all * q.splits;
+    const long long items = p.symmetric ? p.batch * (all - static_cast<long long>(kTile / q.tile_n) * q.tiles_m * (q.tiles_m - 1) / 2)
+                                        : p.batch * all * q.splits;
+    if (items > INT32_MAX - 1024) return MHC_ERR_UNSUPPORTED;
+    a.items = static_cast<int>(items);
     a.a_turned = p.a.turned;
     a.b_turned = p.b.turned;
     const uint32_t fmt = p.bf16 ? 1u : 0u;
@@ -675,38 +651,31 @@ int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cu
                                   : launch_join<EPI_SLOPE>(p.parts, q.splits, p, sms, pdl, s);
 }
 
-cudaError_t launch_copy_rows16(const void *src, long long stride, long long rows, int n, void *dst, long long pitch, int sms,
-                               bool pdl, cudaStream_t s) {
-    const long long need = (rows * ((n + 7) / 8) + 255) / 256, cap = static_cast<long long>(sms) * 8;
-    return launch_block_kernel(copy_rows16_kernel, static_cast<unsigned>(need < cap ? need : cap), 256, 0, pdl, s,
-                               static_cast<const uint16_t *>(src), stride, rows, n, static_cast<uint16_t *>(dst), pitch);
+cudaError_t launch_copy_rows16(const CopyJob &a, const CopyJob &b, int sms, bool pdl, cudaStream_t s) {
+    const long long need = (a.rows * ((a.n + 7) / 8) + b.rows * ((b.n + 7) / 8) + 255) / 256, cap = static_cast<long long>(sms) * 8;
+    return launch_block_kernel(copy_rows16_kernel, static_cast<unsigned>(need < cap ? need : cap), 256, 0, pdl, s, a, b);
 }
 
-size_t column_sums_bytes(long long rows, int n) { return rows > 0 ? static_cast<size_t>(sum_parts(rows, n)) * n * 4 : 0; }
-
-int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, float *parts,
-                       int sms, bool pdl, cudaStream_t s) {
-    const int count = rows > 0 ? sum_parts(rows, n) : 0;
-    if (count) {
-        const bool runs = n % 8 == 0 && stride % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((n + kSumColumns - 1) / kSumColumns, count);
-        cfg.blockDim = dim3(256);
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = pdl ? 1 : 0;
-        const cudaError_t e = dtype == MHC_BF16
-                                  ? cudaLaunchKernelEx(&cfg, column_sums_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16 *>(x),
-                                                       stride, rows, n, runs, parts)
-                                  : cudaLaunchKernelEx(&cfg, column_sums_kernel<__half>, static_cast<const __half *>(x), stride, rows,
-                                                       n, runs, parts);
-        if (int r = note_launch(e)) return r;
-    }
-    return note_launch(launch_block_kernel(column_join_kernel, static_cast<unsigned>((n + 255) / 256), 256, 0, pdl, s,
-                                           static_cast<const float *>(parts), count, n, out, accumulate));
+int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, bool pdl,
+                       cudaStream_t s) {
+    const bool runs = n % 8 == 0 && stride % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((n + kSumColumns - 1) / kSumColumns * kSumSplit);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSumSplit;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    return note_launch(dtype == MHC_BF16 ? cudaLaunchKernelEx(&cfg, column_sums_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16 *>(x),
+                                                              stride, rows, n, runs, out, accumulate)
+                                         : cudaLaunchKernelEx(&cfg, column_sums_kernel<__half>, static_cast<const __half *>(x), stride,
+                                                              rows, n, runs, out, accumulate));
 }
 
 }  // namespace mhc

@@ -122,7 +122,7 @@ def load():
         "mhc_linear_rows_aligned": (i32, [P, i64, i64, i32]),
         "mhc_linear_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
         "mhc_linear_dx_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
-        "mhc_linear_dw_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32]),
+        "mhc_linear_dw_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
         "mhc_linear": (i32, [P, i64, P, i64, i32, i64, i32, i32, P, i32, P, i64, i32, P, i32, P, P, sz, P]),
         "mhc_linear_dx": (i32, [P, i64, P, i64, i32, i64, i32, i32, P, i64, i32, P, i32, P, sz, P]),
         "mhc_linear_dw": (i32, [P, i64, P, i64, i32, i64, i32, i32, P, i32, P, i32, P, sz, P]),
@@ -738,9 +738,8 @@ def linear_dx_workspace_bytes(tokens: int, n: int, k: int, d_out_aligned: bool =
     return int(load().mhc_linear_dx_workspace_bytes(tokens, n, k, int(d_out_aligned), int(w_aligned)))
 
 
-def linear_dw_workspace_bytes(tokens: int, n: int, k: int, d_out_aligned: bool = True, x_aligned: bool = True,
-                              bias: bool = False) -> int:
-    return int(load().mhc_linear_dw_workspace_bytes(tokens, n, k, int(d_out_aligned), int(x_aligned), int(bias)))
+def linear_dw_workspace_bytes(tokens: int, n: int, k: int, d_out_aligned: bool = True, x_aligned: bool = True) -> int:
+    return int(load().mhc_linear_dw_workspace_bytes(tokens, n, k, int(d_out_aligned), int(x_aligned)))
 
 
 def mhc_layer_norm(x, w=None, b=None, eps: float = 1e-5, *, out=None, stats=None, dtype=None, stream=None):
