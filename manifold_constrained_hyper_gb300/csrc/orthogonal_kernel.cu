@@ -109,19 +109,13 @@ struct Target {
     bool mirror, final;
     int m, n;
 };
-// 16 columns of a row of x.
-struct X16 {
-    uint4 h[2], l[2];
-};
-__device__ __forceinline__ void load_x16(X16 &x, const Target &t, int i, int j) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        x.h[k] = x.l[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (!t.x_hi || i >= t.m || j + 8 * k >= t.n) continue;
-        const long long at = static_cast<long long>(i) * t.pitch + j + 8 * k;
-        x.h[k] = __ldcg(reinterpret_cast<const uint4 *>(t.x_hi + at));
-        x.l[k] = __ldcg(reinterpret_cast<const uint4 *>(t.x_lo + at));
-    }
+// 8 columns of a row of x.
+__device__ __forceinline__ void load_x8(uint4 &h, uint4 &l, const Target &t, int i, int j) {
+    h = l = make_uint4(0u, 0u, 0u, 0u);
+    if (!t.x_hi || i >= t.m || j >= t.n) return;
+    const long long at = static_cast<long long>(i) * t.pitch + j;
+    h = __ldcg(reinterpret_cast<const uint4 *>(t.x_hi + at));
+    l = __ldcg(reinterpret_cast<const uint4 *>(t.x_lo + at));
 }
 // Eight sums of row i from column j on in two parts.
 __device__ __forceinline__ void pair8(const Target &t, int i, int j, const float *v, const uint4 &xh, const uint4 &xl, uint4 *hi, uint4 *lo) {
@@ -133,8 +127,11 @@ __device__ __forceinline__ void pair8(const Target &t, int i, int j, const float
         uint64_t r = mul2(f2_pack(v[2 * q], v[2 * q + 1]), splat2(t.unit));
         if (t.x_hi) r = fma2(add2(unpack2(h4[q], tag), unpack2(l4[q], tag)), splat2(t.of_x), r);
         if (t.of_unit != 0.f) r = add2(r, f2_pack(i == j + 2 * q ? t.of_unit : 0.f, i == j + 2 * q + 1 ? t.of_unit : 0.f));
-        hw[q] = pack2(r, tag);
-        lw[q] = pack2(fma2(unpack2(hw[q], tag), splat2(-1.f), r), tag);
+        // hi: the leading 11 bits, cut, not rounded (two masks where a conversion back would take four
+        // times as long); lo, up to 2^-10 of it, holds 11 more
+        const uint64_t h = r & 0xFFFFE000FFFFE000ull;
+        hw[q] = pack2(h, tag);
+        lw[q] = pack2(fma2(h, splat2(-1.f), r), tag);
     }
     *hi = make_uint4(hw[0], hw[1], hw[2], hw[3]);
     *lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
@@ -163,34 +160,31 @@ __device__ __forceinline__ void put64(const NsArgs &a, const Target &t, const CU
     // the last pieces have been read
     if (lane == 0) bulk_wait_read_all();
     __syncwarp();
+    // eight columns at a time: a short loop, whose instructions are fetched once
 #pragma unroll 1
-    for (int c = 0; c < 64; c += 32) {
-        X16 x[2];
-        load_x16(x[0], t, i, j + c);
-        load_x16(x[1], t, i, j + c + 16);
-        uint32_t u[32];
-        tmem_ld32_now(sums + c, u);
+    for (int c = 0; c < 64; c += 8) {
+        uint4 xh, xl;
+        load_x8(xh, xl, t, i, j + c);
+        uint32_t u[8];
+        tmem_ld8_now(sums + c, u);
+        float v[8];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const uint32_t at = held + lane * 128 + (((c / 8 + h) ^ (lane & 7)) << 4);
-            float v[8];
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[e]);
+        const uint32_t at = held + lane * 128 + (((c >> 3) ^ (lane & 7)) << 4);
+        if (t.final) {
+            uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[8 * h + e]);
-            if (t.final) {
-                uint32_t o[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint64_t r = f2_pack(v[2 * q] * a.of_out, v[2 * q + 1] * a.of_out);
-                    o[q] = a.out_dtype == MHC_BF16 ? bf2_pack_rn(r) : pack2(r, static_cast<const __half *>(nullptr));
-                }
-                st_shared_v4(at, make_uint4(o[0], o[1], o[2], o[3]));
-            } else {
-                uint4 hw, lw;
-                pair8(t, i, j + c + 8 * h, v, x[h / 2].h[h & 1], x[h / 2].l[h & 1], &hw, &lw);
-                st_shared_v4(at, hw);
-                st_shared_v4(at + kOutBytes, lw);
-                if (t.mirror && i < t.m && j + c + 8 * h < t.n) mirror8(t, i, j + c + 8 * h, hw, lw);
+            for (int q = 0; q < 4; ++q) {
+                const uint64_t r = f2_pack(v[2 * q] * a.of_out, v[2 * q + 1] * a.of_out);
+                o[q] = a.out_dtype == MHC_BF16 ? bf2_pack_rn(r) : pack2(r, static_cast<const __half *>(nullptr));
             }
+            st_shared_v4(at, make_uint4(o[0], o[1], o[2], o[3]));
+        } else {
+            uint4 hw, lw;
+            pair8(t, i, j + c, v, xh, xl, &hw, &lw);
+            st_shared_v4(at, hw);
+            st_shared_v4(at + kOutBytes, lw);
+            if (t.mirror && i < t.m && j + c < t.n) mirror8(t, i, j + c, hw, lw);
         }
     }
     fence_proxy_async_smem();
@@ -201,49 +195,41 @@ __device__ __forceinline__ void put64(const NsArgs &a, const Target &t, const CU
         bulk_commit();
     }
 }
-// Columns [j, j + 16) of the warp's 32 rows from i0 on, a row a lane; `piece`: 32 x 17 floats of the warp.
-__device__ __forceinline__ void put16(const NsArgs &a, const Target &t, int batch, int i0, int j, float (&v)[16], const X16 &x, float *piece) {
+// Columns [j, j + 8) of the warp's 32 rows from i0 on, a row a lane; `piece`: 32 x 9 floats of the warp.
+__device__ __forceinline__ void put8(const NsArgs &a, const Target &t, int batch, int i0, int j, float (&v)[8], float *piece) {
     const int lane = threadIdx.x & 31, i = i0 + lane;
     if (!t.final) {
-        if (i >= t.m) return;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (j + 8 * h >= t.n) break;
-            uint4 hw, lw;
-            pair8(t, i, j + 8 * h, v + 8 * h, x.h[h], x.l[h], &hw, &lw);
-            const long long at = static_cast<long long>(i) * t.pitch + j + 8 * h;
-            *reinterpret_cast<uint4 *>(t.hi + at) = hw;
-            *reinterpret_cast<uint4 *>(t.lo + at) = lw;
-            if (t.mirror) mirror8(t, i, j + 8 * h, hw, lw);
-        }
+        if (i >= t.m || j >= t.n) return;
+        uint4 xh, xl, hw, lw;
+        load_x8(xh, xl, t, i, j);
+        pair8(t, i, j, v, xh, xl, &hw, &lw);
+        const long long at = static_cast<long long>(i) * t.pitch + j;
+        *reinterpret_cast<uint4 *>(t.hi + at) = hw;
+        *reinterpret_cast<uint4 *>(t.lo + at) = lw;
+        if (t.mirror) mirror8(t, i, j, hw, lw);
         return;
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] *= a.of_out;
+    for (int e = 0; e < 8; ++e) v[e] *= a.of_out;
     const long long row0 = static_cast<long long>(batch) * t.m + i0;
     if (a.out_wide) {
-        if (i >= t.m) return;
+        if (i >= t.m || j >= t.n) return;
         with_type(a.out_dtype, [&](auto tag) {
             using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (j + 8 * h >= t.n) break;
-                float u[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = v[8 * h + e];
-                store8(static_cast<T *>(a.out) + (row0 + lane) * t.n + j + 8 * h, run_of(u));
-            }
+            store8(static_cast<T *>(a.out) + (row0 + lane) * t.n + j, run_of(v));
         });
         return;
     }
-    // rows on any boundary: turned in shared memory, 16 columns of two rows a store
+    // rows on any boundary: turned in shared memory, 8 columns of four rows a store
 #pragma unroll
-    for (int e = 0; e < 16; ++e) piece[lane * 17 + e] = v[e];
+    for (int e = 0; e < 8; ++e) piece[lane * 9 + e] = v[e];
     __syncwarp();
-    const int rows = t.m - i0 < 32 ? t.m - i0 : 32, col = lane & 15;
+    const int rows = t.m - i0 < 32 ? t.m - i0 : 32, col = lane & 7;
     if (j + col < t.n)
-#pragma unroll 4
-        for (int r = lane >> 4; r < rows; r += 2) store_any(a.out, a.out_dtype, (row0 + r) * t.n + j + col, piece[r * 17 + col]);
+#pragma unroll
+        for (int r = 0; r < 32; r += 4)
+            if (r + (lane >> 3) < rows)
+                store_any(a.out, a.out_dtype, (row0 + r + (lane >> 3)) * t.n + j + col, piece[(r + (lane >> 3)) * 9 + col]);
     __syncwarp();
 }
 
@@ -420,7 +406,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
             for (int item = pair; item < f.items && ok; item += pairs, ++done) {
                 const Place p = place_of(f, item);
                 const uint32_t buf = done & 1;
-                const int i0 = p.ti * kTile + static_cast<int>(rank) * kHalf + quad * 32, i = i0 + lane, j0 = p.tj * f.tile_n;
+                const int i0 = p.ti * kTile + static_cast<int>(rank) * kHalf + quad * 32, j0 = p.tj * f.tile_n;
                 Target t;
                 const long long at = p.batch * (which == 2 ? a.x_size : a.p_size);
                 __half *const *const to_pair = which == 0 ? a.g : which == 1 ? a.p : a.x[x ^ 1];
@@ -449,13 +435,14 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                             put64(a, t, to, to + 1, p.batch, i0, j0 + first + c, sums + c, held);
                             continue;
                         }
-                        for (int k = c; k < c + 64 && j0 + first + k < f.n; k += 16) {
-                            uint32_t u[16];
-                            tmem_ld16_now(sums + k, u);
-                            float v[16];
+#pragma unroll 1
+                        for (int k = c; k < c + 64 && j0 + first + k < f.n; k += 8) {
+                            uint32_t u[8];
+                            tmem_ld8_now(sums + k, u);
+                            float v[8];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(u[e]);
-                            put16(a, t, p.batch, i0, j0 + first + k, v, X16{}, piece);
+                            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[e]);
+                            put8(a, t, p.batch, i0, j0 + first + k, v, piece);
                         }
                     }
                 } else {
@@ -485,22 +472,23 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     for (int g = p.split + f.splits * (w / 4); g < f.tile_n / 16; g += 2 * f.splits) {
                         const int j = p.tj * f.tile_n + 16 * g;
                         if (j >= f.n) break;
-                        X16 now;
-                        load_x16(now, t, i, j);
-                        float v[16] = {};
-                        for (int s0 = 0; s0 < f.splits; s0 += 4) {
-                            float u[4][16];
+#pragma unroll 1
+                        for (int h = 0; h < 16; h += 8) {
+                            float v[8] = {};
+                            for (int s0 = 0; s0 < f.splits; s0 += 4) {
+                                float u[4][8];
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
+                                for (int q = 0; q < 4; ++q)
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    u[q][e] = s0 + q < f.splits ? __ldcg(parts + (s0 + q) * part_size + (16 * g + e) * kHalf) : 0.f;
+                                    for (int e = 0; e < 8; ++e)
+                                        u[q][e] = s0 + q < f.splits ? __ldcg(parts + (s0 + q) * part_size + (16 * g + h + e) * kHalf) : 0.f;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
+                                for (int q = 0; q < 4; ++q)
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) v[e] += u[q][e];
+                                    for (int e = 0; e < 8; ++e) v[e] += u[q][e];
+                            }
+                            put8(a, t, p.batch, i0, j + h, v, piece);
                         }
-                        put16(a, t, p.batch, i0, j, v, now, piece);
                     }
                 }
                 tc_fence_before();
@@ -569,8 +557,9 @@ Phase phase_of(int m, int n, int k, int batch, bool symmetric, bool a_turned, bo
         const long long c = (n + tile_n - 1) / tile_n, all = f.tiles_m * c;
         return batch * (symmetric ? all - kTile / tile_n * (static_cast<long long>(f.tiles_m) * (f.tiles_m - 1) / 2) : all);
     };
-    // The cheapest of both tiles' widths and of splitting or not, by what a step of a pair takes (256
-    // columns 0.33 us, where the tensor cores are busy, 128 columns 0.22) and what joining parts costs (3.5 us).
+    // The cheapest of both tiles' widths and of splitting or not, by what was measured: a step of a pair
+    // takes 0.33 us with 256 columns, where the tensor cores are busy, and 0.22 with 128; finishing a tile 4.8
+    // and 2.4; writing parts, waiting for the others' and adding them 10 and 5.4.
     double best = 1e30;
     long long count = 0;
     for (int tile_n : {kTile, kHalf}) {
@@ -579,7 +568,8 @@ Phase phase_of(int m, int n, int k, int batch, bool symmetric, bool a_turned, bo
         for (int s : {1, most < f.steps / 6 ? most : f.steps / 6}) {
             if (s < 1 || s > tile_n / 16) continue;
             const int per = (f.steps + s - 1) / s;
-            const double cost = static_cast<double>((c * s + pairs - 1) / pairs) * per * (tile_n == kTile ? 0.33 : 0.22) + (s > 1 ? 3.5 : 0.);
+            const double cost = static_cast<double>((c * s + pairs - 1) / pairs) * per * (tile_n == kTile ? 0.33 : 0.22) +
+                                (s > 1 ? 5.0 : 2.4) * (tile_n == kTile ? 2. : 1.);
             if (cost >= best) continue;
             best = cost;
             count = c;

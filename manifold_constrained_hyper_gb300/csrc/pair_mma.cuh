@@ -111,4 +111,12 @@ __device__ __forceinline__ void tmem_ld16_now(uint32_t taddr, uint32_t (&v)[16])
         : "r"(taddr) : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8_now(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+        : "r"(taddr) : "memory");
+}
+
 }  // namespace mhc
