@@ -99,6 +99,130 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_rows_kernel(const LayerNor
     }
 }
 
+// The same for many rows on the boundaries of runs: rows to come staged in shared memory, where the
+// weight lies too.
+template <class TX, class TD, int R>
+__global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNormBackArgs a, const __grid_constant__ LnRing ring, int warps) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float red[16][2 * 16 * 2];
+    __shared__ int abort_flag;
+    const int lane = threadIdx.x & 31, groups = blockDim.x / (32 * warps), group = threadIdx.x / (32 * warps);
+    const int mine = threadIdx.x - group * 32 * warps, warp = mine >> 5;
+    float *const par = reinterpret_cast<float *>(smem + 512);
+    const int par_bytes = (4 * a.H + 127) / 128 * 128, stages_at = 512 + par_bytes + group * ring.stages * ring.stage_bytes;
+    const LnStages rows{ring, smem_addr(smem) + group * ring.stages * 8, smem_addr(smem) + stages_at, smem + stages_at, &abort_flag};
+    int turn = 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < groups * ring.stages; ++s) mbar_init(smem_addr(smem) + 8 * s, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    const long long first = static_cast<long long>(blockIdx.x) * groups + group, step = static_cast<long long>(gridDim.x) * groups;
+    auto order = [&](int k) {
+        const long long t = first + k * step;
+        if (t < a.T)
+            rows.order(k, {static_cast<const TX *>(a.x) + t * a.x_stride, static_cast<const TD *>(a.d_out) + t * a.d_stride,
+                           static_cast<const TX *>(a.d_residual) + (a.d_residual ? t * a.r_stride : 0)});
+    };
+    if (mine == 0)
+        for (int k = 0; k < ring.stages; ++k) order(k);
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x) par[c] = a.w ? load_any(a.w, a.w_dtype, c) : 1.f;
+    Run dw[R], db[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) dw[r] = db[r] = run_splat(0.f);
+    __syncthreads();
+    int k = 0;
+    float2 stats = first < a.T ? *reinterpret_cast<const float2 *>(a.stats + 2 * first) : make_float2(0.f, 0.f);
+    for (long long t = first; t < a.T; t += step, ++k) {
+        const float mean = stats.x, rstd = stats.y;
+        if (t + step < a.T) stats = *reinterpret_cast<const float2 *>(a.stats + 2 * (t + step));
+        rows.wait(k);
+        const TX *const x = reinterpret_cast<const TX *>(rows.row(k, 0));
+        const TD *const d = reinterpret_cast<const TD *>(rows.row(k, 1));
+        const TX *const res = reinterpret_cast<const TX *>(rows.row(k, 2));
+        Run h[R], e[R];
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * warps * 32 + mine) * 8;
+            h[r] = e[r] = run_splat(0.f);
+            if (c >= a.H) continue;
+            h[r] = load8_shared(x + c);
+            e[r] = load8_shared(d + c);
+            const Run w = load8_shared(par + c);
+            uint64_t s1 = 0ull, s2 = 0ull;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                h[r].p[q] = mul2(add2(h[r].p[q], splat2(-mean)), splat2(rstd));
+                dw[r].p[q] = fma2(e[r].p[q], h[r].p[q], dw[r].p[q]);
+                db[r].p[q] = add2(db[r].p[q], e[r].p[q]);
+                e[r].p[q] = mul2(e[r].p[q], w.p[q]);
+                s1 = add2(s1, e[r].p[q]);
+                s2 = fma2(e[r].p[q], h[r].p[q], s2);
+            }
+            s[0] += f2_lo(s1) + f2_hi(s1);
+            s[1] += f2_lo(s2) + f2_hi(s2);
+        }
+        group_sums(s, warps, warp, lane, group + 1, red[group], &turn);
+        // every thread of the group has the row; with d_residual, which is read below, it has done with the one before
+        if (mine == 0) {
+            if (!a.d_residual) order(k + ring.stages);
+            else if (k) order(k - 1 + ring.stages);
+        }
+        const float m1 = -s[0] * a.inv_h, m2 = -s[1] * a.inv_h;
+        TX *const out = static_cast<TX *>(a.d_x) + t * a.H;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * warps * 32 + mine) * 8;
+            if (c >= a.H) continue;
+            Run o, add = run_splat(0.f);
+            if (a.d_residual) add = load8_shared(res + c);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o.p[q] = fma2(fma2(h[r].p[q], splat2(m2), add2(e[r].p[q], splat2(m1))), splat2(rstd), add.p[q]);
+            store8(out + c, o);
+        }
+    }
+    if (abort_flag && mine == 0) {
+        const long long left = first < a.T ? (a.T - first + step - 1) / step : 0;
+        rows.drain(static_cast<int>(left));
+    }
+    if (!a.d_w && !a.d_b) return;
+    // the groups' sums meet in the stages, which hold nothing on its way any more, and each thread adds some columns
+    __syncthreads();
+    float *const meet = reinterpret_cast<float *>(smem + 512 + par_bytes);
+    float *const set = a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H;
+    if (groups > 1) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * warps * 32 + mine) * 8;
+            if (c >= a.H) continue;
+            float *const to = meet + static_cast<long long>(group) * 2 * a.H + c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                *reinterpret_cast<uint64_t *>(to + 2 * q) = dw[r].p[q];
+                *reinterpret_cast<uint64_t *>(to + a.H + 2 * q) = db[r].p[q];
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * a.H; c += blockDim.x) {
+            float v = meet[c];
+            for (int g = 1; g < groups; ++g) v += meet[static_cast<long long>(g) * 2 * a.H + c];
+            set[c] = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * warps * 32 + mine) * 8;
+        if (c >= a.H) continue;
+        store8(set + c, dw[r]);
+        store8(set + a.H + c, db[r]);
+    }
+}
+
 // Rows too wide to be held: a CTA a row, read twice; its sums over tokens in its set, each column its thread's.
 template <class TX, class TD>
 __global__ void __launch_bounds__(kLnThreads) ln_back_loop_kernel(const LayerNormBackArgs a) {
@@ -196,14 +320,38 @@ Shape shape_of(long long T, int H) {
     return p;
 }
 
+constexpr int kRingSmem = 220 * 1024;
+
 template <class TX, class TD>
-cudaError_t launch_types(const LayerNormBackArgs &a, bool pdl, cudaStream_t s) {
+cudaError_t launch_types(const LayerNormBackArgs &a, unsigned int *status, bool pdl, cudaStream_t s) {
     const Shape p = shape_of(a.T, a.H);
     if (a.H > kLnMaxHeld)
         return launch_block_kernel(ln_back_loop_kernel<TX, TD>, static_cast<unsigned>(p.parts), kLnThreads, 0, pdl, s, a);
     const bool runs = a.H % 8 == 0 && a.x_stride % 8 == 0 && a.d_stride % 8 == 0 && on_runs(a.x, a.x_dtype) &&
                       on_runs(a.d_out, a.d_dtype) && on_runs(a.d_x, a.x_dtype) && on_runs(a.w, a.w_dtype) &&
                       (!a.d_residual || (a.r_stride % 8 == 0 && on_runs(a.d_residual, a.x_dtype)));
+    if (runs && p.R == kR && a.T >= 4LL * p.parts * p.groups && (reinterpret_cast<uintptr_t>(a.sums) & 31u) == 0 &&
+        (reinterpret_cast<uintptr_t>(a.stats) & 7u) == 0) {
+        LnRing ring = {};
+        ring.row_bytes[0] = a.H * static_cast<int>(sizeof(TX));
+        ring.row_bytes[1] = a.H * static_cast<int>(sizeof(TD));
+        ring.row_bytes[2] = a.d_residual ? ring.row_bytes[0] : 0;
+        ring.stage_bytes = (ring.row_bytes[0] + ring.row_bytes[1] + ring.row_bytes[2] + 127) / 128 * 128;
+        const int par = (4 * a.H + 127) / 128 * 128, room = kRingSmem - 512 - par;
+        ring.stages = room / (p.groups * ring.stage_bytes);
+        if (ring.stages > 4) ring.stages = 4;
+        ring.status = status;
+        ring.timeout_ns = wait_timeout_ns();
+        int stages = p.groups * ring.stages * ring.stage_bytes;
+        const int meet = p.groups > 1 ? p.groups * 8 * a.H : 0;
+        if (stages < meet) stages = meet;
+        if (ring.stages >= (a.d_residual ? 2 : 1) && stages <= room) {
+            auto *const kern = ln_back_ring_kernel<TX, TD, kR>;
+            static std::atomic<uint64_t> done;
+            if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kRingSmem, &done)) return e;
+            return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * p.warps * p.groups, 512 + par + stages, pdl, s, a, ring, p.warps);
+        }
+    }
     auto *const kern = p.R == 1 ? (runs ? ln_back_rows_kernel<TX, TD, 1, true> : ln_back_rows_kernel<TX, TD, 1, false>)
                                 : (runs ? ln_back_rows_kernel<TX, TD, kR, true> : ln_back_rows_kernel<TX, TD, kR, false>);
     const size_t smem = p.groups > 1 ? static_cast<size_t>(a.H) * 8 : 0;     // at most 4096 columns
@@ -216,15 +364,15 @@ size_t layer_norm_sums_bytes(long long T, int H) {
     return T > 0 ? static_cast<size_t>(shape_of(T, H).parts) * 2 * H * 4 : 0;
 }
 
-int launch_layer_norm_back(const LayerNormBackArgs &a, int, bool pdl, cudaStream_t s) {
+int launch_layer_norm_back(const LayerNormBackArgs &a, unsigned int *status, bool pdl, cudaStream_t s) {
     int parts = 0;
     if (a.T > 0) {
         cudaError_t e;
-        if (a.x_dtype == MHC_BF16) e = launch_types<__nv_bfloat16, __nv_bfloat16>(a, pdl, s);
-        else if (a.x_dtype == MHC_F16) e = launch_types<__half, __half>(a, pdl, s);
-        else if (a.d_dtype == MHC_BF16) e = launch_types<float, __nv_bfloat16>(a, pdl, s);
-        else if (a.d_dtype == MHC_F16) e = launch_types<float, __half>(a, pdl, s);
-        else e = launch_types<float, float>(a, pdl, s);
+        if (a.x_dtype == MHC_BF16) e = launch_types<__nv_bfloat16, __nv_bfloat16>(a, status, pdl, s);
+        else if (a.x_dtype == MHC_F16) e = launch_types<__half, __half>(a, status, pdl, s);
+        else if (a.d_dtype == MHC_BF16) e = launch_types<float, __nv_bfloat16>(a, status, pdl, s);
+        else if (a.d_dtype == MHC_F16) e = launch_types<float, __half>(a, status, pdl, s);
+        else e = launch_types<float, float>(a, status, pdl, s);
         if (int r = note_launch(e)) return r;
         parts = shape_of(a.T, a.H).parts;
     }

@@ -241,10 +241,11 @@ mhc_status mhc_layer_norm(const void *x, int64_t x_stride, mhc_dtype dtype, int6
                          {stats, stats ? static_cast<size_t>(tokens) * 8 : 0}};
     if (aliased(outs, 2, ins, 3, -1, -1)) return MHC_ERR_ALIAS;
     int sms = 0;
-    if (int r = require_device(&sms, nullptr)) return static_cast<mhc_status>(r);
+    unsigned int *status = nullptr;
+    if (int r = require_device(&sms, &status)) return static_cast<mhc_status>(r);
     const LayerNormArgs a = {tokens, hidden, x, w, b, tokens == 1 ? hidden : x_stride, dtype, w_dtype, b_dtype, out_dtype, eps,
                              1.f / static_cast<float>(hidden), out, stats};
-    return static_cast<mhc_status>(note_launch(launch_layer_norm(a, sms, pdl_enabled(), static_cast<cudaStream_t>(stream))));
+    return static_cast<mhc_status>(note_launch(launch_layer_norm(a, sms, status, pdl_enabled(), static_cast<cudaStream_t>(stream))));
 }
 
 size_t mhc_layer_norm_backward_workspace_bytes(int64_t tokens, int hidden) {
@@ -282,12 +283,13 @@ mhc_status mhc_layer_norm_backward(const void *d_out, int64_t d_out_stride, mhc_
                          {workspace, need}};
     if (aliased(outs, 4, ins, 5, 0, 2)) return MHC_ERR_ALIAS;
     int sms = 0;
-    if (int r = require_device(&sms, nullptr)) return static_cast<mhc_status>(r);
+    unsigned int *status = nullptr;
+    if (int r = require_device(&sms, &status)) return static_cast<mhc_status>(r);
     const bool one = tokens == 1;
     const LayerNormBackArgs a = {tokens, hidden, d_out, x, d_residual, w, one ? hidden : d_out_stride, one ? hidden : x_stride,
                                  one ? hidden : d_residual_stride, out_dtype, dtype, w_dtype, stats,
                                  1.f / static_cast<float>(hidden), d_x, d_w, d_b, static_cast<float *>(workspace)};
-    return static_cast<mhc_status>(launch_layer_norm_back(a, sms, pdl_enabled(), static_cast<cudaStream_t>(stream)));
+    return static_cast<mhc_status>(launch_layer_norm_back(a, status, pdl_enabled(), static_cast<cudaStream_t>(stream)));
 }
 
 size_t mhc_orthogonalize_workspace_bytes(int batch, int m, int n) {

@@ -91,7 +91,7 @@ struct LayerNormArgs {
     void *out;
     float *stats;                                   // [T][2]: mean, rstd; or NULL
 };
-cudaError_t launch_layer_norm(const LayerNormArgs &a, int sms, bool pdl, cudaStream_t s);
+cudaError_t launch_layer_norm(const LayerNormArgs &a, int sms, unsigned int *status, bool pdl, cudaStream_t s);
 
 struct LayerNormBackArgs {
     long long T;
@@ -106,7 +106,7 @@ struct LayerNormBackArgs {
     float *sums;                                    // layer_norm_sums_bytes()
 };
 size_t layer_norm_sums_bytes(long long T, int H);
-int launch_layer_norm_back(const LayerNormBackArgs &a, int sms, bool pdl, cudaStream_t s);
+int launch_layer_norm_back(const LayerNormBackArgs &a, unsigned int *status, bool pdl, cudaStream_t s);
 
 struct OrthogonalArgs {
     const void *g;

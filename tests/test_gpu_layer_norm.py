@@ -107,3 +107,31 @@ def test_the_same_run_to_run_in_a_graph_and_on_another_stream(T, H):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(first, held))
+
+
+@pytest.mark.parametrize("T,H,types,pad", [(1300, 520, (BF, BF), 8), (2500, 2048, (FP16, FP16), 0), (2000, 4096, (BF, BF), 0),
+                                           (1500, 1544, (FP32, FP32), 8), (1400, 7168, (FP32, BF), 0), (1300, 8192, (FP32, FP32), 0),
+                                           (1250, 7168, (BF, BF), 16), (5000, 264, (FP16, FP16), 0), (4000, 64, (BF, BF), 0)])
+@pytest.mark.parametrize("res", [False, True])
+def test_many_rows(T, H, types, pad, res):
+    """More rows than are on the way at once, every place of the stages filled several times."""
+    xt, ot = types
+    g = gen(T + H)
+    x, d = rows(g, T, H, xt, pad), rows(g, T, H, ot, pad, 0, 0.1)
+    r = rows(g, T, H, xt, pad) if res else None
+    w, b = 1 + 0.1 * torch.randn(H, generator=g, device="cuda"), torch.randn(H, generator=g, device="cuda")
+    if res:
+        b = None
+    out, stats = ops.mhc_layer_norm(x, w, b, 1e-5, dtype=ot)
+    want, ws, e, es = ref.layer_norm(x, w, b, 1e-5)
+    ref.within(out, want, e)
+    assert ((stats.double() - ws).abs() <= es).all()
+    got = ops.mhc_layer_norm_backward(d, x, stats, w, bias=b is not None, d_residual=r)
+    bw = ref.layer_norm_backward(d, x, stats, w, r)
+    for k in ("d_x", "d_w", "d_b"):
+        if getattr(got, k) is not None:
+            ref.within(getattr(got, k), *bw[k])
+
+
+def test_device_status_is_clean():
+    assert ops.mhc_get_device_status() == 0
