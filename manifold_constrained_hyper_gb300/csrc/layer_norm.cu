@@ -60,57 +60,57 @@ __global__ void __launch_bounds__(kLnThreads) ln_rows_kernel(const LayerNormArgs
     }
 }
 
-// The same for many rows on the boundaries of runs: rows to come staged in shared memory, where the
-// parameters lie too.
+// The same for many rows: rows to come staged in shared memory, where the parameters lie too.
 constexpr int kRingThreads = 768;
-template <class TX, class TO, int R>
+template <class TX, class TO, int R, bool RUNS>
 __global__ void __launch_bounds__(kRingThreads) ln_ring_kernel(const LayerNormArgs a, const __grid_constant__ LnRing ring, int warps) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[8][2 * 16];
     __shared__ int abort_flag;
-    const int lane = threadIdx.x & 31, groups = blockDim.x / (32 * warps), group = threadIdx.x / (32 * warps);
+    const int lane = threadIdx.x & 31, groups = (blockDim.x - 32) / (32 * warps), group = threadIdx.x / (32 * warps);
     const int mine = threadIdx.x - group * 32 * warps, warp = mine >> 5;
-    const bool affine = a.w || a.b;
-    float *const par = reinterpret_cast<float *>(smem + 256);
-    const int par_bytes = affine ? (8 * a.H + 127) / 128 * 128 : 0, stages_at = 256 + par_bytes + group * ring.stages * ring.stage_bytes;
-    const LnStages rows{ring, smem_addr(smem) + group * ring.stages * 8, smem_addr(smem) + stages_at, smem + stages_at, &abort_flag};
-    int turn = 0;
+    const bool affine = a.w || a.b, filler = threadIdx.x >= blockDim.x - 32;
+    float *const par = reinterpret_cast<float *>(smem + 512);
+    const int Hp = (a.H + 7) / 8 * 8, par_bytes = affine ? (8 * Hp + 127) / 128 * 128 : 0;
+    const int which = filler ? lane : group, places_at = 512 + par_bytes + which * ring.stages * ring.place[kLnArrays];
+    LnPlace place = {smem_addr(smem) + which * ring.stages * 16, smem_addr(smem) + places_at, 0, 0};
     if (threadIdx.x == 0) {
-        for (int s = 0; s < groups * ring.stages; ++s) mbar_init(smem_addr(smem) + 8 * s, 1);
+        ln_bars_init(smem_addr(smem), groups * ring.stages, warps);
         abort_flag = 0;
-        fence_mbar_init();
     }
     __syncthreads();
     griddep_wait();
-    const long long first = static_cast<long long>(blockIdx.x) * groups + group, step = static_cast<long long>(gridDim.x) * groups;
-    auto order = [&](int k) {
-        const long long t = first + k * step;
-        if (t < a.T) rows.order(k, {static_cast<const TX *>(a.x) + t * a.x_stride, nullptr, nullptr});
-    };
-    if (mine == 0)
-        for (int k = 0; k < ring.stages; ++k) order(k);
-    if (affine) {
-        for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
-            par[c] = a.w ? load_any(a.w, a.w_dtype, c) : 1.f;
-            par[a.H + c] = a.b ? load_any(a.b, a.b_dtype, c) : 0.f;
-        }
+    const long long first = static_cast<long long>(blockIdx.x) * groups + which, step = static_cast<long long>(gridDim.x) * groups;
+    if (filler) {
+        ln_fill(ring, place, lane < groups, first < a.T ? static_cast<int>((a.T - first + step - 1) / step) : 0, &abort_flag,
+                [&](int k, const void *(&src)[kLnArrays]) {
+                    src[0] = static_cast<const TX *>(a.x) + (first + k * step) * a.x_stride;
+                    src[1] = src[2] = nullptr;
+                });
+        return;
     }
-    __syncthreads();
-    int k = 0;
-    for (long long t = first; t < a.T; t += step, ++k) {
-        rows.wait(k);
-        const TX *const x = reinterpret_cast<const TX *>(rows.row(k, 0));
+    if (affine) {
+        ln_stage_param(par, a.w, a.w_dtype, a.H, Hp, 1.f, 32 * warps * groups);
+        ln_stage_param(par + Hp, a.b, a.b_dtype, a.H, Hp, 0.f, 32 * warps * groups);
+        named_barrier_sync(15, 32 * warps * groups);
+    }
+    int turn = 0;
+    for (long long t = first; t < a.T; t += step, place.next(ring)) {
+        mbar_wait(place.full(), place.turn, &abort_flag, ring.timeout_ns, ring.status, SITE_LN_ROW);
+        const uint8_t *const x = smem + places_at + place.at * ring.place[kLnArrays];
+        const TX *const from = static_cast<const TX *>(a.x) + t * a.x_stride;
         Run v[R];
         float s[1] = {0.f};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int c = (r * warps * 32 + mine) * 8;
             v[r] = run_splat(0.f);
-            if (c < a.H) v[r] = load8_shared(x + c);
+            if (c < a.H) v[r] = ln_staged<RUNS>(x, ln_skew(from), c, a.H, from);
             s[0] += run_sum(v[r]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(place.empty());      // the row is in registers
         group_sums(s, warps, warp, lane, group + 1, red[group], &turn);
-        if (mine == 0) order(k + ring.stages);      // every thread of the group has the row
         const float mean = s[0] * a.inv_h;
         s[0] = 0.f;
 #pragma unroll
@@ -119,9 +119,10 @@ __global__ void __launch_bounds__(kRingThreads) ln_ring_kernel(const LayerNormAr
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[r].p[q] = add2(v[r].p[q], splat2(-mean));
             if (c >= a.H) continue;
-            uint64_t q2 = mul2(v[r].p[0], v[r].p[0]);
+            const Run m = RUNS ? v[r] : ln_masked(v[r], c, a.H);
+            uint64_t q2 = mul2(m.p[0], m.p[0]);
 #pragma unroll
-            for (int q = 1; q < 4; ++q) q2 = fma2(v[r].p[q], v[r].p[q], q2);
+            for (int q = 1; q < 4; ++q) q2 = fma2(m.p[q], m.p[q], q2);
             s[0] += f2_lo(q2) + f2_hi(q2);
         }
         group_sums(s, warps, warp, lane, group + 1, red[group], &turn);
@@ -138,16 +139,12 @@ __global__ void __launch_bounds__(kRingThreads) ln_ring_kernel(const LayerNormAr
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[r].p[q] = mul2(v[r].p[q], splat2(rstd));
             if (affine) {
-                const Run w = load8_shared(par + c), b = load8_shared(par + a.H + c);
+                const Run w = load8_shared(par + c), b = load8_shared(par + Hp + c);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[r].p[q] = fma2(v[r].p[q], w.p[q], b.p[q]);
             }
-            store8(out + c, v[r]);
+            ln_store<RUNS>(out, c, a.H, v[r]);
         }
-    }
-    if (abort_flag && mine == 0) {
-        const long long left = first < a.T ? (a.T - first + step - 1) / step : 0;
-        rows.drain(static_cast<int>(left));
     }
 }
 
@@ -195,27 +192,27 @@ bool on_runs(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) 
 
 constexpr int kRingSmem = 220 * 1024;
 
-// Many rows on the boundaries of runs: a CTA an SM, as many groups as 768 threads give, as many stages as
-// shared memory holds, at most 4 a group.
+// Many rows: a CTA an SM, as many groups as 768 threads give, as many stages as shared memory holds, at most 4 a group.
 template <class TX, class TO>
-cudaError_t launch_ring(const LayerNormArgs &a, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
+cudaError_t launch_ring(const LayerNormArgs &a, bool runs, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
     const int need = (a.H + 255) / 256, R = need <= 6 ? 2 : 4, warps = (need + R - 1) / R;
-    int groups = kRingThreads / (32 * warps);
+    int groups = (kRingThreads - 32) / (32 * warps);
     if (groups > 8) groups = 8;
     LnRing ring = {};
-    ring.row_bytes[0] = ring.stage_bytes = a.H * static_cast<int>(sizeof(TX));
-    ring.stage_bytes = (ring.stage_bytes + 127) / 128 * 128;
-    const int par = a.w || a.b ? (8 * a.H + 127) / 128 * 128 : 0;
-    ring.stages = (kRingSmem - 256 - par) / (groups * ring.stage_bytes);
+    ring.row_bytes[0] = a.H * static_cast<int>(sizeof(TX));
+    ln_places(&ring);
+    const int par = a.w || a.b ? (8 * ((a.H + 7) / 8 * 8) + 127) / 128 * 128 : 0;
+    ring.stages = (kRingSmem - 512 - par) / (groups * ring.place[kLnArrays]);
     if (ring.stages > 4) ring.stages = 4;
     ring.status = status;
     ring.timeout_ns = wait_timeout_ns();
-    const int smem = 256 + par + groups * ring.stages * ring.stage_bytes;
-    auto *const kern = R == 2 ? ln_ring_kernel<TX, TO, 2> : ln_ring_kernel<TX, TO, 4>;
-    static std::atomic<uint64_t> done[2];
-    if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kRingSmem, &done[R == 2])) return e;
+    const int smem = 512 + par + groups * ring.stages * ring.place[kLnArrays];
+    auto *const kern = R == 2 ? (runs ? ln_ring_kernel<TX, TO, 2, true> : ln_ring_kernel<TX, TO, 2, false>)
+                              : (runs ? ln_ring_kernel<TX, TO, 4, true> : ln_ring_kernel<TX, TO, 4, false>);
+    static std::atomic<uint64_t> done[4];
+    if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kRingSmem, &done[2 * (R == 2) + runs])) return e;
     const long long blocks = (a.T + groups - 1) / groups;
-    return launch_block_kernel(kern, static_cast<unsigned>(blocks < sms ? blocks : sms), 32 * warps * groups, smem, pdl, s, a, ring, warps);
+    return launch_block_kernel(kern, static_cast<unsigned>(blocks < sms ? blocks : sms), 32 * (warps * groups + 1), smem, pdl, s, a, ring, warps);
 }
 
 template <class TX, class TO>
@@ -224,7 +221,7 @@ cudaError_t launch_types(const LayerNormArgs &a, int sms, unsigned int *status, 
         return launch_block_kernel(ln_loop_kernel<TX, TO>, static_cast<unsigned>(a.T < 4 * sms ? a.T : 4 * sms), kLnThreads, 0, pdl, s, a);
     const bool runs = a.H % 8 == 0 && a.x_stride % 8 == 0 && on_runs(a.x, a.x_dtype) && on_runs(a.out, a.out_dtype) &&
                       on_runs(a.w, a.w_dtype) && on_runs(a.b, a.b_dtype);
-    if (runs && a.H > 512 && a.T >= 8LL * sms) return launch_ring<TX, TO>(a, sms, status, pdl, s);
+    if (a.H > 512 && a.T >= 8LL * sms) return launch_ring<TX, TO>(a, runs, sms, status, pdl, s);
     const int need = (a.H + 255) / 256;             // warps of one run a lane
     const int R = need <= 1 ? 1 : need <= 2 ? 2 : 4, warps = (need + R - 1) / R, groups = kLnThreads / (32 * warps);
     const long long blocks = (a.T + groups - 1) / groups, cap = 4LL * sms;

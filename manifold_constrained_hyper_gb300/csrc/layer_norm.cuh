@@ -68,13 +68,14 @@ __device__ __forceinline__ float run_sum(const Run &r) {
 
 // ---------------------------------------------------------------- staged rows
 // Rows on the way to shared memory by bulk copies while others are worked on: each group of warps has
-// `stages` places of its own, filled in turn; row k of the group is the k/stages-th filling of place
-// k % stages, and thread 0 of the group orders the next one when the group has the row in registers. A wait
-// that runs out raises the flag, after which none waits: the CTA then goes through its rows without
-// their values, so that no thread misses a barrier, and the status says so.
+// `stages` places of its own, filled in turn by a lane of the CTA's last warp, which does nothing else
+// (ordering a row takes some 600 cycles, too long for a thread that others wait for). A place is free again when
+// each warp of the group has said so. A wait that runs out raises the flag, after which none waits:
+// the CTA then goes through its rows without their values, so that no thread misses a barrier, and the
+// status says so. A row on no boundary of 16 bytes comes with the 16-byte words that hold its ends.
 constexpr int kLnArrays = 3;
 struct LnRing {
-    int stages, row_bytes[kLnArrays], stage_bytes;      // of each array (a multiple of 16), 0 where there is none
+    int stages, row_bytes[kLnArrays], place[kLnArrays + 1];     // bytes of a row of each array (0: none), where they lie in a stage; its size
     unsigned int *status;
     unsigned long long timeout_ns;
 };
@@ -88,42 +89,121 @@ inline cudaError_t ln_allow_smem(const void *kern, int bytes, std::atomic<uint64
     done->fetch_or(bit, std::memory_order_release);
     return cudaSuccess;
 }
-enum LnSite : int { SITE_LN_ROW = 120, SITE_LN_DRAIN };
+enum LnSite : int { SITE_LN_ROW = 120, SITE_LN_FREE, SITE_LN_DRAIN };
 
-struct LnStages {
-    const LnRing &ring;
-    uint32_t bars, base;                            // of the group
-    uint8_t *basep;
-    volatile int *abort_flag;
-
-    __device__ __forceinline__ void order(int k, const void *const (&src)[kLnArrays]) const {
-        const int s = k % ring.stages;
-        uint32_t total = 0, dst = base + s * ring.stage_bytes;
-#pragma unroll
-        for (int i = 0; i < kLnArrays; ++i) total += ring.row_bytes[i];
-        mbar_arrive_expect_tx(bars + 8 * s, total);
-        const uint64_t policy = policy_evict_first();
-#pragma unroll
-        for (int i = 0; i < kLnArrays; ++i) {
-            if (!ring.row_bytes[i]) continue;
-            bulk_load(dst, src[i], ring.row_bytes[i], bars + 8 * s, policy);
-            dst += ring.row_bytes[i];
+// The next filling of a group's places: 16 bytes of barriers each (filled, free), then the rows.
+struct LnPlace {
+    uint32_t bars, base;
+    int at, turn;
+    __device__ __forceinline__ uint32_t full() const { return bars + 16 * at; }
+    __device__ __forceinline__ uint32_t empty() const { return bars + 16 * at + 8; }
+    __device__ __forceinline__ void next(const LnRing &ring) {
+        if (++at == ring.stages) {
+            at = 0;
+            turn ^= 1;
         }
     }
-    __device__ __forceinline__ void wait(int k) const {
-        mbar_wait(bars + 8 * (k % ring.stages), (k / ring.stages) & 1, abort_flag, ring.timeout_ns, ring.status, SITE_LN_ROW);
-    }
-    // Gave up: the copies still on their way land before the CTA exits. `ordered`: how many rows were.
-    __device__ __forceinline__ void drain(int ordered) const {
-        int gave_up = 0;
-        for (int k = ordered > ring.stages ? ordered - ring.stages : 0; k < ordered; ++k)
-            mbar_wait(bars + 8 * (k % ring.stages), (k / ring.stages) & 1, &gave_up, ring.timeout_ns, ring.status, SITE_LN_DRAIN);
-    }
-    __device__ __forceinline__ const uint8_t *row(int k, int array) const {
-        int at = k % ring.stages * ring.stage_bytes;
-        for (int i = 0; i < array; ++i) at += ring.row_bytes[i];
-        return basep + at;
-    }
 };
+__device__ __forceinline__ void ln_bars_init(uint32_t bars, int places, int warps) {
+    for (int s = 0; s < places; ++s) {
+        mbar_init(bars + 16 * s, 1);
+        mbar_init(bars + 16 * s + 8, warps);
+    }
+    fence_mbar_init();
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// One row on its way to a place.
+__device__ __forceinline__ void ln_order(const LnRing &ring, const LnPlace &p, const void *const (&src)[kLnArrays], uint64_t policy) {
+    uint32_t bytes[kLnArrays], total = 0;
+    uintptr_t from[kLnArrays];
+#pragma unroll
+    for (int i = 0; i < kLnArrays; ++i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(src[i]), low = static_cast<uintptr_t>(15);
+        from[i] = at & ~low;
+        bytes[i] = ring.row_bytes[i] ? static_cast<uint32_t>(((at + ring.row_bytes[i] + 15) & ~low) - from[i]) : 0;
+        total += bytes[i];
+    }
+    mbar_arrive_expect_tx(p.full(), total);
+#pragma unroll
+    for (int i = 0; i < kLnArrays; ++i)
+        if (bytes[i])
+            bulk_load(p.base + p.at * ring.place[kLnArrays] + ring.place[i], reinterpret_cast<const void *>(from[i]), bytes[i], p.full(), policy);
+}
+// Gave up: the copies still on their way land before the CTA exits. p: the next place to be filled, after k rows.
+__device__ __forceinline__ void ln_drain(const LnRing &ring, const LnPlace &p, int k) {
+    int gave_up = 0;
+    LnPlace q = p;
+    for (int back = k < ring.stages ? k : ring.stages; back > 0; --back) {
+        q.at = p.at - back;
+        q.turn = p.turn;
+        if (q.at < 0) {
+            q.at += ring.stages;
+            q.turn ^= 1;
+        }
+        mbar_wait(q.full(), q.turn, &gave_up, ring.timeout_ns, ring.status, SITE_LN_DRAIN);
+    }
+}
+// The last warp: lane g fills group g's places with `rows` rows, sources(k, src) naming the k-th's arrays.
+template <class F>
+__device__ __forceinline__ void ln_fill(const LnRing &ring, LnPlace p, bool mine, int rows, int *abort_flag, F &&sources) {
+    const uint64_t policy = policy_evict_first();
+    uint64_t t0 = globaltimer_ns();
+    int k = 0;
+    while (true) {
+        const bool todo = mine && k < rows && !*reinterpret_cast<volatile int *>(abort_flag);
+        if (!__any_sync(0xffffffffu, todo)) break;
+        if (todo && mbar_test(p.empty(), p.turn ^ 1)) {
+            const void *src[kLnArrays];
+            sources(k, src);
+            ln_order(ring, p, src, policy);
+            p.next(ring);
+            ++k;
+            t0 = globaltimer_ns();
+        } else if (todo && globaltimer_ns() - t0 > ring.timeout_ns) {
+            record_failure(ring.status, 7, SITE_LN_FREE);
+            *reinterpret_cast<volatile int *>(abort_flag) = 1;
+        }
+    }
+    if (mine && *reinterpret_cast<volatile int *>(abort_flag)) ln_drain(ring, p, k);
+}
+// Columns [c, c + 8) of a staged row, `skew` bytes into its first word; RUNS: none. Past the row's end 0.
+template <bool RUNS, class T>
+__device__ __forceinline__ Run ln_staged(const uint8_t *row, uint32_t skew, int c, int H, const T *tag) {
+    if constexpr (RUNS) return load8_shared(reinterpret_cast<const T *>(row) + c);
+    else return ln_masked(load8_skewed(reinterpret_cast<const uint4 *>(row + c * sizeof(T)), skew, tag), c, H);
+}
+template <class T>
+__device__ __forceinline__ uint32_t ln_skew(const T *p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+}
+// A stage's places for rows of these sizes, wherever the rows begin; a run read past a row's end
+// touches at most 48 bytes more.
+inline void ln_places(LnRing *r) {
+    int at = 0;
+    for (int i = 0; i < kLnArrays; ++i) {
+        r->place[i] = at;
+        if (r->row_bytes[i]) at += (r->row_bytes[i] + 15 + 64 + 127) / 128 * 128;
+    }
+    r->place[kLnArrays] = at;
+}
+// A parameter's H values, zeros up to Hp, to shared memory by the CTA's first `threads` threads, eight loads of each on their way at once.
+__device__ __forceinline__ void ln_stage_param(float *to, const void *p, int dtype, int H, int Hp, float otherwise, int threads) {
+    for (int c0 = threadIdx.x; c0 < Hp; c0 += 8 * threads) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = c0 + e * threads;
+            v[e] = c >= H ? 0.f : p ? load_any(p, dtype, c) : otherwise;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c0 + e * threads < Hp) to[c0 + e * threads] = v[e];
+    }
+}
 
 }  // namespace mhc

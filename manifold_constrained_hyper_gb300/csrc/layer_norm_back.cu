@@ -10,10 +10,37 @@ namespace mhc {
 namespace {
 
 constexpr int kR = 2;                               // runs of 8 columns a thread at most
+constexpr int kAllBarrier = 15;                     // of all groups (of several warps there are at most 8)
+
+// The groups' sums over tokens to the CTA's set, in the groups' order, through meet [groups][2][Hp].
+template <int R>
+__device__ __forceinline__ void meet_sums(float *meet, float *set, const Run (&dw)[R], const Run (&db)[R], int H, int Hp, int groups, int group,
+                                          int warps, int mine) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * warps * 32 + mine) * 8;
+        if (c >= H) continue;
+        float *const to = meet + static_cast<long long>(group) * 2 * Hp + c;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            *reinterpret_cast<uint64_t *>(to + 2 * q) = dw[r].p[q];
+            *reinterpret_cast<uint64_t *>(to + Hp + 2 * q) = db[r].p[q];
+        }
+    }
+    const int threads = 32 * warps * groups;
+    named_barrier_sync(kAllBarrier, threads);
+    for (int c = threadIdx.x; c < 2 * Hp; c += threads) {
+        const int col = c < Hp ? c : c - Hp;
+        if (col >= H) continue;
+        float v = meet[c];
+        for (int g = 1; g < groups; ++g) v += meet[static_cast<long long>(g) * 2 * Hp + c];
+        set[(c < Hp ? 0 : H) + col] = v;
+    }
+}
 
 template <class TX, class TD, int R, bool RUNS>
 __global__ void __launch_bounds__(kLnThreads) ln_back_rows_kernel(const LayerNormBackArgs a, int warps) {
-    extern __shared__ float sums[];                 // [2][H] where a CTA has several groups
+    extern __shared__ float sums[];                 // [groups][2][H]
     __shared__ float red[16][2 * 16 * 2];
     const int lane = threadIdx.x & 31, groups = blockDim.x / (32 * warps), group = threadIdx.x / (32 * warps);
     const int mine = threadIdx.x - group * 32 * warps, warp = mine >> 5;
@@ -74,74 +101,73 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_rows_kernel(const LayerNor
         }
     }
     if (!want) return;
-    // the groups one after another into shared memory, then the CTA's set
-    float *const set = a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H;
-    for (int g = 0; g < groups; ++g) {
-        if (g == group) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int c = (r * warps * 32 + mine) * 8;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (c + k >= a.H) break;
-                    float w = run_at(dw[r], k), b = run_at(db[r], k);
-                    if (g) {
-                        w += sums[c + k];
-                        b += sums[a.H + c + k];
-                    }
-                    float *const to = g == groups - 1 ? set : sums;
-                    to[c + k] = w;
-                    to[a.H + c + k] = b;
-                }
-            }
-        }
-        if (g < groups - 1) __syncthreads();
-    }
+    meet_sums<R>(sums, a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H, dw, db, a.H, (a.H + 7) / 8 * 8, groups, group, warps, mine);
 }
 
-// The same for many rows on the boundaries of runs: rows to come staged in shared memory, where the
+// The same for many rows: rows to come staged in shared memory, where the
 // weight lies too.
-template <class TX, class TD, int R>
+// SELF: a group is 8 or 16 warps, and with one more warp there would be room for one group less, or for 96
+// registers a thread: its first thread orders its rows itself (8192 x 4096 bf16: 57 us, with a warp for it and one
+// group 62, with 96 registers 67; 8192 x 7168, where there is one group anyway, 99 us by its first thread and 83 by a warp).
+template <class TX, class TD, int R, bool RUNS, bool SELF>
 __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNormBackArgs a, const __grid_constant__ LnRing ring, int warps) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[16][2 * 16 * 2];
     __shared__ int abort_flag;
-    const int lane = threadIdx.x & 31, groups = blockDim.x / (32 * warps), group = threadIdx.x / (32 * warps);
-    const int mine = threadIdx.x - group * 32 * warps, warp = mine >> 5;
-    float *const par = reinterpret_cast<float *>(smem + 512);
-    const int par_bytes = (4 * a.H + 127) / 128 * 128, stages_at = 512 + par_bytes + group * ring.stages * ring.stage_bytes;
-    const LnStages rows{ring, smem_addr(smem) + group * ring.stages * 8, smem_addr(smem) + stages_at, smem + stages_at, &abort_flag};
-    int turn = 0;
+    const int lane = threadIdx.x & 31, groups = (blockDim.x - (SELF ? 0 : 32)) / (32 * warps), group = threadIdx.x / (32 * warps);
+    const int mine = threadIdx.x - group * 32 * warps, warp = mine >> 5, threads = 32 * warps * groups;
+    const bool filler = !SELF && threadIdx.x >= threads;
+    float *const par = reinterpret_cast<float *>(smem + 1024);
+    const int Hp = (a.H + 7) / 8 * 8, par_bytes = (4 * Hp + 127) / 128 * 128;
+    const int which = filler ? lane : group, places_at = 1024 + par_bytes + which * ring.stages * ring.place[kLnArrays];
+    LnPlace place = {smem_addr(smem) + which * ring.stages * 16, smem_addr(smem) + places_at, 0, 0};
     if (threadIdx.x == 0) {
-        for (int s = 0; s < groups * ring.stages; ++s) mbar_init(smem_addr(smem) + 8 * s, 1);
+        ln_bars_init(smem_addr(smem), groups * ring.stages, warps);
         abort_flag = 0;
-        fence_mbar_init();
     }
     __syncthreads();
     griddep_wait();
-    const long long first = static_cast<long long>(blockIdx.x) * groups + group, step = static_cast<long long>(gridDim.x) * groups;
-    auto order = [&](int k) {
-        const long long t = first + k * step;
-        if (t < a.T)
-            rows.order(k, {static_cast<const TX *>(a.x) + t * a.x_stride, static_cast<const TD *>(a.d_out) + t * a.d_stride,
-                           static_cast<const TX *>(a.d_residual) + (a.d_residual ? t * a.r_stride : 0)});
+    const long long first = static_cast<long long>(blockIdx.x) * groups + which, step = static_cast<long long>(gridDim.x) * groups;
+    auto sources = [&](long long t, const void *(&src)[kLnArrays]) {
+        src[0] = static_cast<const TX *>(a.x) + t * a.x_stride;
+        src[1] = static_cast<const TD *>(a.d_out) + t * a.d_stride;
+        src[2] = a.d_residual ? static_cast<const TX *>(a.d_residual) + t * a.r_stride : nullptr;
     };
-    if (mine == 0)
-        for (int k = 0; k < ring.stages; ++k) order(k);
-    for (int c = threadIdx.x; c < a.H; c += blockDim.x) par[c] = a.w ? load_any(a.w, a.w_dtype, c) : 1.f;
+    if (filler) {
+        ln_fill(ring, place, lane < groups, first < a.T ? static_cast<int>((a.T - first + step - 1) / step) : 0, &abort_flag,
+                [&](int k, const void *(&src)[kLnArrays]) { sources(first + k * step, src); });
+        return;
+    }
+    // SELF: the next place to fill and its row
+    LnPlace fill = place;
+    long long next = first;
+    auto order = [&] {
+        if (next >= a.T) return;
+        const void *src[kLnArrays];
+        sources(next, src);
+        ln_order(ring, fill, src, policy_evict_first());
+        fill.next(ring);
+        next += step;
+    };
+    if (SELF && mine == 0)
+        for (int k = 0; k < ring.stages; ++k) order();
+    ln_stage_param(par, a.w, a.w_dtype, a.H, Hp, 1.f, threads);
     Run dw[R], db[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) dw[r] = db[r] = run_splat(0.f);
-    __syncthreads();
-    int k = 0;
-    float2 stats = first < a.T ? *reinterpret_cast<const float2 *>(a.stats + 2 * first) : make_float2(0.f, 0.f);
-    for (long long t = first; t < a.T; t += step, ++k) {
-        const float mean = stats.x, rstd = stats.y;
-        if (t + step < a.T) stats = *reinterpret_cast<const float2 *>(a.stats + 2 * (t + step));
-        rows.wait(k);
-        const TX *const x = reinterpret_cast<const TX *>(rows.row(k, 0));
-        const TD *const d = reinterpret_cast<const TD *>(rows.row(k, 1));
-        const TX *const res = reinterpret_cast<const TX *>(rows.row(k, 2));
+    named_barrier_sync(kAllBarrier, threads);
+    int turn = 0;
+    float next_mean = first < a.T ? a.stats[2 * first] : 0.f, next_rstd = first < a.T ? a.stats[2 * first + 1] : 0.f;
+    for (long long t = first; t < a.T; t += step, place.next(ring)) {
+        const float mean = next_mean, rstd = next_rstd;
+        if (t + step < a.T) {
+            next_mean = a.stats[2 * (t + step)];
+            next_rstd = a.stats[2 * (t + step) + 1];
+        }
+        mbar_wait(place.full(), place.turn, &abort_flag, ring.timeout_ns, ring.status, SITE_LN_ROW);
+        const TX *const x = static_cast<const TX *>(a.x) + t * a.x_stride;
+        const TD *const d = static_cast<const TD *>(a.d_out) + t * a.d_stride;
+        const uint8_t *const staged = smem + places_at + place.at * ring.place[kLnArrays];
         Run h[R], e[R];
         float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -149,13 +175,15 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNor
             const int c = (r * warps * 32 + mine) * 8;
             h[r] = e[r] = run_splat(0.f);
             if (c >= a.H) continue;
-            h[r] = load8_shared(x + c);
-            e[r] = load8_shared(d + c);
+            h[r] = ln_staged<RUNS>(staged, ln_skew(x), c, a.H, x);
+            e[r] = ln_staged<RUNS>(staged + ring.place[1], ln_skew(d), c, a.H, d);
             const Run w = load8_shared(par + c);
             uint64_t s1 = 0ull, s2 = 0ull;
 #pragma unroll
+            for (int q = 0; q < 4; ++q) h[r].p[q] = mul2(add2(h[r].p[q], splat2(-mean)), splat2(rstd));
+            if (!RUNS) h[r] = ln_masked(h[r], c, a.H);
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
-                h[r].p[q] = mul2(add2(h[r].p[q], splat2(-mean)), splat2(rstd));
                 dw[r].p[q] = fma2(e[r].p[q], h[r].p[q], dw[r].p[q]);
                 db[r].p[q] = add2(db[r].p[q], e[r].p[q]);
                 e[r].p[q] = mul2(e[r].p[q], w.p[q]);
@@ -165,12 +193,13 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNor
             s[0] += f2_lo(s1) + f2_hi(s1);
             s[1] += f2_lo(s2) + f2_hi(s2);
         }
-        group_sums(s, warps, warp, lane, group + 1, red[group], &turn);
-        // every thread of the group has the row; with d_residual, which is read below, it has done with the one before
-        if (mine == 0) {
-            if (!a.d_residual) order(k + ring.stages);
-            else if (k) order(k - 1 + ring.stages);
+        if (!SELF && !a.d_residual) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(place.empty());      // the row is in registers
         }
+        group_sums(s, warps, warp, lane, group + 1, red[group], &turn);
+        // SELF: every thread of the group has the row; with d_residual, which is read below, it has done with the one before
+        if (SELF && mine == 0 && (!a.d_residual || t > first)) order();
         const float m1 = -s[0] * a.inv_h, m2 = -s[1] * a.inv_h;
         TX *const out = static_cast<TX *>(a.d_x) + t * a.H;
 #pragma unroll
@@ -178,49 +207,27 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNor
             const int c = (r * warps * 32 + mine) * 8;
             if (c >= a.H) continue;
             Run o, add = run_splat(0.f);
-            if (a.d_residual) add = load8_shared(res + c);
+            if (a.d_residual) {
+                const TX *const g = static_cast<const TX *>(a.d_residual) + t * a.r_stride;
+                add = ln_staged<RUNS>(staged + ring.place[2], ln_skew(g), c, a.H, g);
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 o.p[q] = fma2(fma2(h[r].p[q], splat2(m2), add2(e[r].p[q], splat2(m1))), splat2(rstd), add.p[q]);
-            store8(out + c, o);
+            ln_store<RUNS>(out, c, a.H, o);
+        }
+        if (!SELF && a.d_residual) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(place.empty());
         }
     }
-    if (abort_flag && mine == 0) {
-        const long long left = first < a.T ? (a.T - first + step - 1) / step : 0;
-        rows.drain(static_cast<int>(left));
-    }
+    if (SELF && mine == 0 && *reinterpret_cast<volatile int *>(&abort_flag))
+        ln_drain(ring, fill, first < a.T ? static_cast<int>((next - first) / step) : 0);
     if (!a.d_w && !a.d_b) return;
     // the groups' sums meet in the stages, which hold nothing on its way any more, and each thread adds some columns
-    __syncthreads();
-    float *const meet = reinterpret_cast<float *>(smem + 512 + par_bytes);
-    float *const set = a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H;
-    if (groups > 1) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int c = (r * warps * 32 + mine) * 8;
-            if (c >= a.H) continue;
-            float *const to = meet + static_cast<long long>(group) * 2 * a.H + c;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                *reinterpret_cast<uint64_t *>(to + 2 * q) = dw[r].p[q];
-                *reinterpret_cast<uint64_t *>(to + a.H + 2 * q) = db[r].p[q];
-            }
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < 2 * a.H; c += blockDim.x) {
-            float v = meet[c];
-            for (int g = 1; g < groups; ++g) v += meet[static_cast<long long>(g) * 2 * a.H + c];
-            set[c] = v;
-        }
-        return;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int c = (r * warps * 32 + mine) * 8;
-        if (c >= a.H) continue;
-        store8(set + c, dw[r]);
-        store8(set + a.H + c, db[r]);
-    }
+    named_barrier_sync(kAllBarrier, threads);
+    meet_sums<R>(reinterpret_cast<float *>(smem + 1024 + par_bytes), a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H, dw, db, a.H, Hp,
+                 groups, group, warps, mine);
 }
 
 // Rows too wide to be held: a CTA a row, read twice; its sums over tokens in its set, each column its thread's.
@@ -305,22 +312,30 @@ bool on_runs(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) 
 
 struct Shape {
     int R, warps, groups, parts;
+    bool ring, self;
 };
-// The row kernel's shape: as many groups as 512 threads give, a CTA an SM (two of the loop kernel's).
+// The row kernels' shape: as many groups as 512 threads give, a CTA an SM. With several rows a group they
+// are staged, by one more warp. (A stage is 3 x 32 KB at most, beside 32 KB of weights: one fits.)
 Shape shape_of(long long T, int H) {
-    Shape p = {1, kLnThreads / 32, 1, 0};
+    Shape p = {1, kLnThreads / 32, 1, 0, false, false};
     if (H <= kLnMaxHeld) {
         const int need = (H + 255) / 256;
         p.R = need <= 1 ? 1 : kR;
         p.warps = (need + p.R - 1) / p.R;
         p.groups = kLnThreads / (32 * p.warps);
+        if (p.R == kR && T > static_cast<long long>(kGridCap) * p.groups) {
+            p.ring = true;
+            p.self = p.warps % 8 == 0;
+            if (!p.self) p.groups = (kLnThreads - 32) / (32 * p.warps);
+        }
     }
     const long long blocks = (T + p.groups - 1) / p.groups;
     p.parts = static_cast<int>(blocks < kGridCap ? blocks : kGridCap);
     return p;
 }
 
-constexpr int kRingSmem = 220 * 1024;
+constexpr int kRingSmem = 216 * 1024;
+constexpr int kMeetSmem = 64 * 1024;                // 512 threads of two runs: 8192 columns in all groups, two sums
 
 template <class TX, class TD>
 cudaError_t launch_types(const LayerNormBackArgs &a, unsigned int *status, bool pdl, cudaStream_t s) {
@@ -330,32 +345,35 @@ cudaError_t launch_types(const LayerNormBackArgs &a, unsigned int *status, bool 
     const bool runs = a.H % 8 == 0 && a.x_stride % 8 == 0 && a.d_stride % 8 == 0 && on_runs(a.x, a.x_dtype) &&
                       on_runs(a.d_out, a.d_dtype) && on_runs(a.d_x, a.x_dtype) && on_runs(a.w, a.w_dtype) &&
                       (!a.d_residual || (a.r_stride % 8 == 0 && on_runs(a.d_residual, a.x_dtype)));
-    if (runs && p.R == kR && a.T >= 4LL * p.parts * p.groups && (reinterpret_cast<uintptr_t>(a.sums) & 31u) == 0 &&
-        (reinterpret_cast<uintptr_t>(a.stats) & 7u) == 0) {
+    const int Hp = (a.H + 7) / 8 * 8, meet = p.groups * 8 * Hp;
+    if (p.ring) {
         LnRing ring = {};
         ring.row_bytes[0] = a.H * static_cast<int>(sizeof(TX));
         ring.row_bytes[1] = a.H * static_cast<int>(sizeof(TD));
         ring.row_bytes[2] = a.d_residual ? ring.row_bytes[0] : 0;
-        ring.stage_bytes = (ring.row_bytes[0] + ring.row_bytes[1] + ring.row_bytes[2] + 127) / 128 * 128;
-        const int par = (4 * a.H + 127) / 128 * 128, room = kRingSmem - 512 - par;
-        ring.stages = room / (p.groups * ring.stage_bytes);
+        ln_places(&ring);
+        const int par = (4 * Hp + 127) / 128 * 128, room = kRingSmem - 1024 - par;
+        ring.stages = room / (p.groups * ring.place[kLnArrays]);
         if (ring.stages > 4) ring.stages = 4;
         ring.status = status;
         ring.timeout_ns = wait_timeout_ns();
-        int stages = p.groups * ring.stages * ring.stage_bytes;
-        const int meet = p.groups > 1 ? p.groups * 8 * a.H : 0;
-        if (stages < meet) stages = meet;
-        if (ring.stages >= (a.d_residual ? 2 : 1) && stages <= room) {
-            auto *const kern = ln_back_ring_kernel<TX, TD, kR>;
-            static std::atomic<uint64_t> done;
-            if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kRingSmem, &done)) return e;
-            return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * p.warps * p.groups, 512 + par + stages, pdl, s, a, ring, p.warps);
+        int places = p.groups * ring.stages * ring.place[kLnArrays];
+        if (places < meet) places = meet;
+        const bool self = p.self;
+        auto *const kern = self ? (runs ? ln_back_ring_kernel<TX, TD, kR, true, true> : ln_back_ring_kernel<TX, TD, kR, false, true>)
+                                : (runs ? ln_back_ring_kernel<TX, TD, kR, true, false> : ln_back_ring_kernel<TX, TD, kR, false, false>);
+        // with d_residual a group's first thread orders a row later: two places at least
+        if (ring.stages >= (self && a.d_residual ? 2 : 1)) {
+            static std::atomic<uint64_t> done[4];
+            if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kRingSmem, &done[2 * self + runs])) return e;
+            return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * (p.warps * p.groups + !self), 1024 + par + places, pdl, s, a, ring, p.warps);
         }
     }
     auto *const kern = p.R == 1 ? (runs ? ln_back_rows_kernel<TX, TD, 1, true> : ln_back_rows_kernel<TX, TD, 1, false>)
                                 : (runs ? ln_back_rows_kernel<TX, TD, kR, true> : ln_back_rows_kernel<TX, TD, kR, false>);
-    const size_t smem = p.groups > 1 ? static_cast<size_t>(a.H) * 8 : 0;     // at most 4096 columns
-    return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * p.warps * p.groups, smem, pdl, s, a, p.warps);
+    static std::atomic<uint64_t> done[4];
+    if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kMeetSmem, &done[2 * (p.R == 1) + runs])) return e;
+    return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * p.warps * p.groups, a.d_w || a.d_b ? meet : 0, pdl, s, a, p.warps);
 }
 
 }  // namespace

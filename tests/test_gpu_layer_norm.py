@@ -111,7 +111,9 @@ def test_the_same_run_to_run_in_a_graph_and_on_another_stream(T, H):
 
 @pytest.mark.parametrize("T,H,types,pad", [(1300, 520, (BF, BF), 8), (2500, 2048, (FP16, FP16), 0), (2000, 4096, (BF, BF), 0),
                                            (1500, 1544, (FP32, FP32), 8), (1400, 7168, (FP32, BF), 0), (1300, 8192, (FP32, FP32), 0),
-                                           (1250, 7168, (BF, BF), 16), (5000, 264, (FP16, FP16), 0), (4000, 64, (BF, BF), 0)])
+                                           (1250, 7168, (BF, BF), 16), (5000, 264, (FP16, FP16), 0), (4000, 64, (BF, BF), 0),
+                                           (1300, 1999, (BF, BF), 3), (1600, 1102, (FP32, FP32), 0), (1400, 1999, (FP32, FP16), 1),
+                                           (1300, 7167, (FP16, FP16), 2), (1250, 8191, (FP32, FP32), 0), (3000, 514, (BF, BF), 1)])
 @pytest.mark.parametrize("res", [False, True])
 def test_many_rows(T, H, types, pad, res):
     """More rows than are on the way at once, every place of the stages filled several times."""
