@@ -139,14 +139,11 @@ __device__ __forceinline__ void finish_piece(const Piece &p, const EpilogueArgs 
         if (e.bias) {
             if (p.wide) {
 #pragma unroll
-                for (int q = 0; q < 32; ++q) v[q] = fmaf(v[q], e.unit, __shfl_sync(0xffffffffu, bias, q));
+                for (int q = 0; q < 32; ++q) v[q] += __shfl_sync(0xffffffffu, bias, q);
             } else {
 #pragma unroll
-                for (int q = 0; q < 32; ++q) v[q] = fmaf(v[q], e.unit, bias);
+                for (int q = 0; q < 32; ++q) v[q] += bias;
             }
-        } else {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] *= e.unit;
         }
         if (e.z) store_piece(p, e.z, e.z_dtype, at, n, v);
         if (e.act != MHC_LINEAR_NONE)
@@ -171,7 +168,6 @@ __device__ __forceinline__ void finish_piece(const Piece &p, const EpilogueArgs 
 template <int KIND>
 __device__ __forceinline__ void finish_element(const EpilogueArgs &e, long long i, long long at, int j, float x) {
     if constexpr (KIND == EPI_LINEAR) {
-        x *= e.unit;
         if (e.bias) x += load_any(e.bias, e.bias_dtype, j);
         if (e.z) store_any(e.z, e.z_dtype, at, x);
         with_act(e.act, [&](auto act) { x = act_value<decltype(act)::value>(x); });

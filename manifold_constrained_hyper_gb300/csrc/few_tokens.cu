@@ -204,9 +204,9 @@ int launch_few_tokens(const Product &p, int sms, unsigned int *status, bool pdl,
     a.timeout_ns = wait_timeout_ns();
     a.e = p.epi;
     CUtensorMap mx, mw;
-    if (!encode_matrices16(&mx, p.bf16, p.a.hi, p.k, p.m, 1, p.a.pitch * 2, 0, a.width) ||
-        !(p.b.turned ? encode_matrices16(&mw, p.bf16, p.b.hi, p.n, p.k, 1, p.b.pitch * 2, 0, kPairStep)
-                     : encode_matrices16(&mw, p.bf16, p.b.hi, p.k, p.n, 1, p.b.pitch * 2, 0, kRows)))
+    if (!encode_matrices16(&mx, p.bf16, p.a.p, p.k, p.m, 1, p.a.pitch * 2, 0, a.width) ||
+        !(p.b.turned ? encode_matrices16(&mw, p.bf16, p.b.p, p.n, p.k, 1, p.b.pitch * 2, 0, kPairStep)
+                     : encode_matrices16(&mw, p.bf16, p.b.p, p.k, p.n, 1, p.b.pitch * 2, 0, kRows)))
         return MHC_ERR_CUDA;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;

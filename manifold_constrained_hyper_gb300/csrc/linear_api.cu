@@ -22,10 +22,10 @@ bool on_runs(const void *p, mhc_dtype d) { return aligned(p, d == MHC_F32 ? 32 :
 
 // Operand `o` from rows that lie as they do, or from a copy of them at *at, which moves on past it.
 void operand(Operand *o, CopyJob *job, const void *p, int64_t stride, int64_t rows, int w, bool turned, uint8_t **at) {
-    *o = {p, nullptr, rows == 1 ? pitch16(w) : stride, 0, turned};
+    *o = {p, rows == 1 ? pitch16(w) : stride, turned};
     *job = {};
     if (mhc_linear_rows_aligned(p, stride, rows, w)) return;
-    *o = {*at, nullptr, pitch16(w), 0, turned};
+    *o = {*at, pitch16(w), turned};
     *job = {p, stride, rows, w, *at, pitch16(w)};
     *at += copy_bytes(rows, w, false);
 }
@@ -66,7 +66,6 @@ mhc_status forward(const Forward &f, void *stream) {
     p.m = f.T;
     p.n = f.n;
     p.k = f.k;
-    p.batch = 1;
     p.bf16 = f.dtype == MHC_BF16;
     p.exact = f.e.out_dtype == MHC_F32;
     p.kind = f.kind;
@@ -120,7 +119,6 @@ mhc_status mhc_linear(const void *x, int64_t x_stride, const void *w, int64_t w_
                          {workspace, need}};
     if (aliased(outs, 3, ins, 4, 0, 3)) return MHC_ERR_ALIAS;
     Forward f = {x, w, x_stride, w_stride, dtype, tokens, n, k, false, EPI_LINEAR, {}, workspace};
-    f.e.unit = 1.f;
     f.e.out = out;
     f.e.out_dtype = out_dtype;
     f.e.bias = bias;
@@ -157,7 +155,6 @@ mhc_status mhc_linear_dx(const void *d_out, int64_t d_out_stride, const void *w,
     if (aliased(outs, 2, ins, 3, -1, -1)) return MHC_ERR_ALIAS;
     const bool slope = act != MHC_LINEAR_NONE;
     Forward f = {d_out, w, d_out_stride, w_stride, dtype, tokens, k, n, true, slope ? EPI_SLOPE : EPI_LINEAR, {}, workspace};
-    f.e.unit = 1.f;
     f.e.out = d_x;
     f.e.out_dtype = d_x_dtype;
     if (slope) {
@@ -200,7 +197,6 @@ mhc_status mhc_linear_dw(const void *d_out, int64_t d_out_stride, const void *x,
     p.m = n;
     p.n = k;
     p.k = tokens;
-    p.batch = 1;
     p.bf16 = dtype == MHC_BF16;
     p.exact = d_w_dtype == MHC_F32;
     p.kind = EPI_SUMS;
@@ -208,15 +204,15 @@ mhc_status mhc_linear_dw(const void *d_out, int64_t d_out_stride, const void *x,
     p.epi.out_dtype = d_w_dtype;
     p.epi.accumulate = accumulate != 0;
     p.epi.wide = k % 8 == 0 && on_runs(d_w, d_w_dtype);
+    CopyJob jobs[2] = {};
     if (tokens > 0) {
-        CopyJob jobs[2];
         operand(&p.a, &jobs[0], d_out, d_out_stride, tokens, n, true, &at);
         operand(&p.b, &jobs[1], x, x_stride, tokens, k, true, &at);
-        if (int r = copy(jobs, sms, pdl, s)) return static_cast<mhc_status>(r);
     }
-    // of the copy where there is one: runs of 8
-    if (d_bias)
-        if (int r = launch_column_sums(p.a.hi, p.a.pitch, dtype, tokens, n, d_bias, accumulate, pdl, s)) return static_cast<mhc_status>(r);
+    // with a bias the copies go beside its sums
+    if (int r = d_bias ? launch_column_sums(d_out, tokens == 1 ? n : d_out_stride, dtype, tokens, n, d_bias, accumulate, jobs[0], jobs[1], sms, pdl, s)
+                       : copy(jobs, sms, pdl, s))
+        return static_cast<mhc_status>(r);
     p.parts = product_parts_bytes(n, k, tokens) ? reinterpret_cast<float *>(at) : nullptr;
     return static_cast<mhc_status>(launch_product(p, sms, status, pdl, s));
 }

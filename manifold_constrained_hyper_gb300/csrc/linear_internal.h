@@ -11,26 +11,22 @@ bool encode_matrices16(CUtensorMap *m, bool bf16, const void *ptr, unsigned long
                        unsigned long long batch, unsigned long long pitch_bytes, unsigned long long batch_bytes,
                        unsigned int box_rows);
 
-// One operand of a product: element (row, k) of matrix b is at
-// hi[b * batch_stride + row * pitch + k], or with `turned` at [b * batch_stride + k * pitch + row];
-// its value hi, or hi + lo with lo.
+// One operand of a product: element (row, k) is at p[row * pitch + k], or with `turned` at p[k * pitch + row].
 struct Operand {
-    const void *hi, *lo;
-    long long pitch, batch_stride;                  // in elements, multiples of 8; pointers on 16 bytes
+    const void *p;
+    long long pitch;                                // in elements, a multiple of 8; p on 16 bytes
     bool turned;
 };
 
 // What is done to the sums before they are stored.
 enum Epilogue : int {
     EPI_SUMS,       // out = acc, or added to out; of the splits: fp32 sums
-    EPI_LINEAR,     // z = unit * acc + bias, out = act(z) + residual
-    EPI_SLOPE,      // out = acc * act'(z)
-    EPI_PAIR        // unit * acc, with a polynomial in the first operand or without, as hi + lo in fp16
+    EPI_LINEAR,     // z = acc + bias, out = act(z) + residual
+    EPI_SLOPE       // out = acc * act'(z)
 };
 struct EpilogueArgs {
-    void *out;                                      // [batch][m][n], contiguous
+    void *out;                                      // [m][n], contiguous
     int out_dtype, accumulate;
-    float unit;
     const void *bias;                               // [n] or NULL
     int bias_dtype;
     const void *residual;                           // rows or NULL
@@ -40,20 +36,13 @@ struct EpilogueArgs {
     long long z_stride;
     int z_dtype;
     int act;
-    // PAIR: rows on 16-byte boundaries
-    void *hi, *lo;
-    long long pitch, batch_stride;
-    const void *x_hi, *x_lo;                        // of the same layout, or NULL
-    float of_x, of_unit;                            // out = of_unit * I + of_x * x + unit * acc
     int wide;                                       // every row that is touched lies on the boundaries of runs of 8
 };
 struct Product {
     long long m;
     int n;
     long long k;
-    int batch;
     bool bf16;                                      // the operands' type, else fp16
-    bool symmetric;                                 // PAIR: m == n and out is symmetric
     bool exact;                                     // sums in short pieces, for an fp32 result
     Operand a, b;                                   // [m][k], [n][k]
     Epilogue kind;
@@ -77,9 +66,9 @@ struct CopyJob {
     long long pitch;
 };
 cudaError_t launch_copy_rows16(const CopyJob &a, const CopyJob &b, int sms, bool pdl, cudaStream_t s);
-// Sums over rows of a 16-bit [rows][n]: out[n] fp32 (accumulate: added).
-int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, bool pdl,
-                       cudaStream_t s);
+// Sums over rows of a 16-bit [rows][n]: out[n] fp32 (accumulate: added); the copies beside it.
+int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, const CopyJob &a,
+                       const CopyJob &b, int sms, bool pdl, cudaStream_t s);
 
 struct LayerNormArgs {
     long long T;

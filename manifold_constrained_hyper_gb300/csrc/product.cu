@@ -1,13 +1,14 @@
 // Products of 16-bit matrices with an epilogue, D[i][j] = sum_k A(i, k) B(j, k), on the 5th-generation
-// tensor cores: the projection, its two gradients, and the products of the orthogonalised update.
+// tensor cores: the projection and its two gradients.
 //
-// A pair of CTAs (cta_group::2) forms a 256 x 256 tile of D (256 x 128 where there are few tiles): each
-// loads 128 rows of A and half of the tile's of B for every 64 elements of k (32 KB, six steps in
-// flight), and holds its half of the sums in tensor memory, in two buffers, so that the epilogue of
-// one tile runs under the products of the next. Either operand may lie with k contiguous or outermost:
-// TMA brings both into the layout that the tensor core reads, so nothing is transposed beforehand. An
-// operand in two fp16 parts (hi + lo, 22 bits) takes three products a step, hi hi, hi lo and lo hi, into
-// the same sums.
+// A pair of CTAs (cta_group::2) forms a 256 x 256 or 256 x 128 tile of D, or, where there are few tiles, one
+// CTA a 128 x 128 or 128 x 64 one: each loads 128 rows of A and its part of the tile's of B for every 64
+// elements of k (32 KB at most, six steps in flight), and holds its sums in tensor memory, in two buffers,
+// so that the epilogue of one tile runs under the products of the next. Either operand may lie with k
+// contiguous or outermost: TMA brings both into the layout that the tensor core reads, so nothing is
+// transposed beforehand. The products are issued by an elected thread: by one that a comparison of lane
+// numbers picks, each takes 80 ns, of which 256 x 256 sums hide all and 256 x 128 half (8192 x 4096 x 7168: 300 us
+// against 278).
 #include <atomic>
 
 #include "epilogue.cuh"
@@ -40,10 +41,8 @@ struct Args {
     long long m;
     int n;
     int tiles_m, tiles_n, splits, steps_per_split, steps;
-    int tile_n;                     // 256 or 128
+    int tile_n;                     // 256 or 128 of a pair of CTAs, 128 or 64 of one
     int chain;                      // steps between two additions in registers
-    int passes;                     // products a step: 1, or 3 of operands in two parts
-    int symmetric;                  // tiles left of the diagonal are mirrored, not formed
     int items;
     int a_turned, b_turned;
     uint32_t idesc;
@@ -51,31 +50,17 @@ struct Args {
     unsigned long long timeout_ns;
     EpilogueArgs e;
 };
-struct Maps {
-    CUtensorMap a[2], b[2];         // hi, lo
-};
 struct Place {
-    int batch, split, ti, tj;
+    int split, ti, tj;
 };
 
-// Work item -> its matrix, part of the summed axis and tile. Tiles are walked in bands of kBand rows, so
-// that those in flight share columns of both operands in L2; symmetric ones row by row from the diagonal.
+// Work item -> its part of the summed axis and tile. Tiles are walked in bands of kBand rows, so that those
+// in flight share columns of both operands in L2.
 __device__ __forceinline__ Place place_of(const Args &a, int item) {
+    const int tiles = a.tiles_m * a.tiles_n;
     Place p;
-    if (a.symmetric) {
-        const int ratio = kTile / a.tile_n;
-        const int tiles = a.tiles_m * a.tiles_n - ratio * (a.tiles_m * (a.tiles_m - 1) / 2);
-        p.batch = item / tiles;
-        int r = item - p.batch * tiles;
-        p.split = p.ti = 0;
-        while (r >= a.tiles_n - ratio * p.ti) r -= a.tiles_n - ratio * p.ti++;
-        p.tj = ratio * p.ti + r;
-        return p;
-    }
-    const int tiles = a.tiles_m * a.tiles_n, which = item / tiles;
-    p.batch = which / a.splits;
-    p.split = which - p.batch * a.splits;
-    const int r = item - which * tiles, band = r / (kBand * a.tiles_n), first = band * kBand;
+    p.split = item / tiles;
+    const int r = item - p.split * tiles, band = r / (kBand * a.tiles_n), first = band * kBand;
     const int rows = a.tiles_m - first < kBand ? a.tiles_m - first : kBand;
     const int q = r - band * kBand * a.tiles_n;
     p.tj = q / rows;
@@ -83,62 +68,34 @@ __device__ __forceinline__ Place place_of(const Args &a, int item) {
     return p;
 }
 
-__device__ __forceinline__ uint64_t pair_of(const uint32_t (&v)[32], int e) {
-    return (static_cast<uint64_t>(v[e + 1]) << 32) | v[e];
+// What differs between a pair of CTAs and one.
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
+    if constexpr (PAIR)
+        tma_load_pair(dst, m, c0, c1, bar);
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                     ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar) : "memory");
 }
-// PAIR: columns [j, j + 32) of row i as hi + lo; mirror: at the transposed place too, a column a store
-// of 32 rows. x: the row's 16 words of hi, then of lo, where there is an x.
-__device__ __forceinline__ void load_pair(Raw &x, const Args &a, int batch, long long i, int j) {
-    const EpilogueArgs &e = a.e;
-    if (!e.x_hi || i >= a.m) return;
-    const long long at = static_cast<long long>(batch) * e.batch_stride + i * e.pitch + j;
-    const Piece p = {true, a.n - j};
-    Raw lo = {};
-    load_raw(x, p, e.x_hi, MHC_F16, at, 0);
-    load_raw(lo, p, e.x_lo, MHC_F16, at, 0);
-#pragma unroll
-    for (int q = 0; q < 16; ++q) x.w[16 + q] = lo.w[q];
+template <bool PAIR>
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    if constexpr (PAIR) mma_pair(d, a, b, idesc, add);
+    else tc_mma_bf16(d, a, b, idesc, add);
 }
-__device__ __forceinline__ void finish_pair(const Args &a, int batch, long long i, int j, bool mirror, const uint32_t (&v)[32], const Raw &x) {
-    const EpilogueArgs &e = a.e;
-    const long long base = static_cast<long long>(batch) * e.batch_stride;
-    __half *const hi = static_cast<__half *>(e.hi) + base, *const lo = static_cast<__half *>(e.lo) + base;
-    const uint64_t unit = splat2(e.unit);
-    uint32_t hw[16], lw[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-        uint64_t r = mul2(pair_of(v, 2 * q), unit);
-        if (e.x_hi) {
-            const __half *const tag = nullptr;
-            r = fma2(add2(unpack2(x.w[q], tag), unpack2(x.w[16 + q], tag)), splat2(e.of_x), r);
-            // the unit matrix
-            r = add2(r, f2_pack(i == j + 2 * q ? e.of_unit : 0.f, i == j + 2 * q + 1 ? e.of_unit : 0.f));
-        }
-        hw[q] = pack2(r, static_cast<const __half *>(nullptr));
-        lw[q] = pack2(fma2(unpack2(hw[q], static_cast<const __half *>(nullptr)), splat2(-1.f), r), static_cast<const __half *>(nullptr));
-    }
-    if (i >= a.m) return;
-    const long long at = i * e.pitch + j;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (j + 8 * c >= a.n) break;
-        *reinterpret_cast<uint4 *>(hi + at + 8 * c) = make_uint4(hw[4 * c], hw[4 * c + 1], hw[4 * c + 2], hw[4 * c + 3]);
-        *reinterpret_cast<uint4 *>(lo + at + 8 * c) = make_uint4(lw[4 * c], lw[4 * c + 1], lw[4 * c + 2], lw[4 * c + 3]);
-    }
-    if (!mirror) return;
-    uint16_t *h = reinterpret_cast<uint16_t *>(hi) + j * e.pitch + i, *l = reinterpret_cast<uint16_t *>(lo) + j * e.pitch + i;
-    const long long step = here(e.pitch);
-#pragma unroll
-    for (int q = 0; q < 32; ++q, h += step, l += step) {
-        if (j + q >= a.n) break;
-        *h = static_cast<uint16_t>(hw[q >> 1] >> (q & 1) * 16);
-        *l = static_cast<uint16_t>(lw[q >> 1] >> (q & 1) * 16);
-    }
+template <bool PAIR>
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+    if constexpr (PAIR) arrive_at_rank(map_to_rank(bar, 0));
+    else mbar_arrive(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (PAIR) commit_pair(bar);
+    else tc_commit(bar);
 }
 
-template <int KIND>
+template <int KIND, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
+product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ Args a) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     uint8_t *const basep = raw + (base - smem_addr(raw));
@@ -149,8 +106,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *const turn = reinterpret_cast<float *>(basep + kStages * kStageBytes + 256);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    constexpr int kCtas = PAIR ? 2 : 1, kRows = kCtas * kHalf;      // of a tile
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const int pair = blockIdx.x / kCtas, pairs = gridDim.x / kCtas;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -159,22 +117,27 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full + 8 * b, 1);
-            mbar_init(acc_empty + 8 * b, 2 * kSumWarps);    // the leader's: the epilogue warps of either CTA
+            mbar_init(acc_empty + 8 * b, kCtas * kSumWarps);    // the leader's: the epilogue warps of either CTA
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&maps.a[0]);
-        tma_prefetch_desc(&maps.b[0]);
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_addr(tmem_slot)), "r"(kTmemCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(smem_addr(tmem_slot)), "r"(kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            tmem_alloc(smem_addr(tmem_slot), kTmemCols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    if constexpr (PAIR) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
@@ -187,34 +150,28 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
             const Place p = place_of(a, item);
             const int s0 = p.split * a.steps_per_split;
             const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
-            const int half = a.tile_n / 2;
-            const int ci = p.ti * kTile + static_cast<int>(rank) * kHalf, cj = p.tj * a.tile_n + static_cast<int>(rank) * half;
+            const int half = a.tile_n / kCtas;
+            const int ci = p.ti * kRows + static_cast<int>(rank) * kHalf, cj = p.tj * a.tile_n + static_cast<int>(rank) * half;
             for (int st = s0; st < s1; ++st, ++it) {
                 const uint32_t s = it % kStages, ph = (it / kStages) & 1;
                 if (!mbar_wait(empty + 8 * s, ph ^ 1, abort_flag, a.timeout_ns, a.status, SITE_P_EMPTY)) {
                     ok = false;
                     break;
                 }
-                if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kBoxBytes * (a.tile_n == kTile ? 8 : 6));
-                const uint32_t bar = map_to_rank(full + 8 * s, 0), dst = base + s * kStageBytes, db = dst + 2 * kBoxBytes;
-                int k = st * kStep, part = 0;
-                if (a.passes == 3) {
-                    const int kb = st / 3;
-                    k = kb * kStep;
-                    part = st - 3 * kb;
-                }
-                const CUtensorMap *const ma = &maps.a[part == 2], *const mb = &maps.b[part == 1];
+                if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kCtas * (2 * kBoxBytes + half * 128));
+                const uint32_t bar = PAIR ? map_to_rank(full + 8 * s, 0) : full + 8 * s, dst = base + s * kStageBytes, db = dst + 2 * kBoxBytes;
+                const int k = st * kStep;
                 if (a.a_turned) {
-                    tma_load_pair_3d(dst, ma, ci, k, p.batch, bar);
-                    tma_load_pair_3d(dst + kBoxBytes, ma, ci + 64, k, p.batch, bar);
+                    load_box<PAIR>(dst, &map_a, ci, k, bar);
+                    load_box<PAIR>(dst + kBoxBytes, &map_a, ci + 64, k, bar);
                 } else {
-                    tma_load_pair_3d(dst, ma, k, ci, p.batch, bar);
+                    load_box<PAIR>(dst, &map_a, k, ci, bar);
                 }
                 if (a.b_turned) {
-                    tma_load_pair_3d(db, mb, cj, k, p.batch, bar);
-                    if (half == kHalf) tma_load_pair_3d(db + kBoxBytes, mb, cj + 64, k, p.batch, bar);
+                    load_box<PAIR>(db, &map_b, cj, k, bar);
+                    if (half == kHalf) load_box<PAIR>(db + kBoxBytes, &map_b, cj + 64, k, bar);
                 } else {
-                    tma_load_pair_3d(db, mb, k, cj, p.batch, bar);
+                    load_box<PAIR>(db, &map_b, k, cj, bar);
                 }
             }
         }
@@ -257,16 +214,16 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
                     const uint64_t db = a.b_turned ? desc_columns(sb) : desc_rows(sb), nb = a.b_turned ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
                     for (int q = 0; q < kStep / 16; ++q)
-                        mma_pair(acc, da + q * na, db + q * nb, a.idesc, st > c0 || q > 0);
-                    commit_pair(empty + 8 * s);
+                        multiply<PAIR>(acc, da + q * na, db + q * nb, a.idesc, st > c0 || q > 0);
+                    commit<PAIR>(empty + 8 * s);
                 }
-                if (ok) commit_pair(acc_full + 8 * buf);
+                if (ok) commit<PAIR>(acc_full + 8 * buf);
             }
         }
         if (!ok) {
             // the products issued end before tensor memory is freed
             int gave_up = 0;
-            commit_pair(drain);
+            commit<PAIR>(drain);
             mbar_wait(drain, 0, &gave_up, a.timeout_ns, a.status, SITE_P_DRAIN);
         }
     } else if (warp >= 2) {
@@ -281,9 +238,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
             const Place p = place_of(a, item);
             const int s0 = p.split * a.steps_per_split;
             const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
-            const long long i = static_cast<long long>(p.ti) * kTile + static_cast<int>(rank) * kHalf + quad * 32 + lane;
-            // the output's matrices follow one another, and so do the splits' sums
-            const long long row = ((static_cast<long long>(p.batch) * a.splits + p.split) * a.m + i) * a.n;
+            const long long i = static_cast<long long>(p.ti) * kRows + static_cast<int>(rank) * kHalf + quad * 32 + lane;
+            const long long row = (p.split * a.m + i) * a.n;     // the splits' sums follow one another
             const int j0 = p.tj * a.tile_n + first;
             auto piece_at = [&](int j) {
                 if (a.e.wide) return Piece{true, i < a.m ? a.n - j : 0};
@@ -292,14 +248,10 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
             };
             // what the piece from column j on is combined with
             auto ahead = [&](Raw &r, float &bias, int j) {
-                if constexpr (KIND == EPI_PAIR) {
-                    load_pair(r, a, p.batch, i, j);
-                } else {
-                    const bool wide = a.e.wide;
-                    if (KIND == EPI_LINEAR && a.e.bias && j + lane < a.n) bias = load_any(a.e.bias, a.e.bias_dtype, j + lane);
-                    load_extra<KIND>(r, piece_at(j), a.e, wide ? i : i - lane, wide ? j : j + lane,
-                                     wide ? row + j : row - static_cast<long long>(lane) * a.n + j + lane, a.n);
-                }
+                const bool wide = a.e.wide;
+                if (KIND == EPI_LINEAR && a.e.bias && j + lane < a.n) bias = load_any(a.e.bias, a.e.bias_dtype, j + lane);
+                load_extra<KIND>(r, piece_at(j), a.e, wide ? i : i - lane, wide ? j : j + lane,
+                                 wide ? row + j : row - static_cast<long long>(lane) * a.n + j + lane, a.n);
             };
             uint64_t sum[4][16];
 #pragma unroll
@@ -335,7 +287,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
                 if (last) break;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at_rank(map_to_rank(acc_empty + 8 * buf, 0));
+                if (lane == 0) arrive_leader<PAIR>(acc_empty + 8 * buf);
             }
             if (!ok) break;
             // the sums' registers are free from here on: a piece's operands are on their way while the one
@@ -343,7 +295,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
             Raw extra = {};
             float bias = 0.f;
             if (j0 < a.n) ahead(extra, bias, j0);
-            const bool mirror = a.symmetric && p.tj * a.tile_n >= (p.ti + 1) * kTile;
 #pragma unroll 1
             for (int c = 0; c < width; c += 32) {
                 const int j = j0 + c;
@@ -353,30 +304,26 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
                 Raw next = {};
                 float next_bias = 0.f;
                 if (c + 32 < width && j + 32 < a.n) ahead(next, next_bias, j + 32);
-                if constexpr (KIND == EPI_PAIR) {
-                    finish_pair(a, p.batch, i, j, mirror, v, extra);
+                float f[32];
+                if (a.e.wide) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
                 } else {
-                    float f[32];
-                    if (a.e.wide) {
+                    // rows on any boundary: turned in shared memory, then a column a lane
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
-                    } else {
-                        // rows on any boundary: turned in shared memory, then a column a lane
+                    for (int e = 0; e < 32; ++e) piece[lane * 33 + e] = __uint_as_float(v[e]);
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) piece[lane * 33 + e] = __uint_as_float(v[e]);
-                        __syncwarp();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = piece[e * 33 + lane];
-                        __syncwarp();
-                    }
-                    finish_piece<KIND>(piece_at(j), a.e, a.e.wide ? row + j : row - static_cast<long long>(lane) * a.n + j + lane, a.n, bias, f, extra);
+                    for (int e = 0; e < 32; ++e) f[e] = piece[e * 33 + lane];
+                    __syncwarp();
                 }
+                finish_piece<KIND>(piece_at(j), a.e, a.e.wide ? row + j : row - static_cast<long long>(lane) * a.n + j + lane, a.n, bias, f, extra);
                 extra = next;
                 bias = next_bias;
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at_rank(map_to_rank(acc_empty + 8 * (done & 1), 0));
+            if (lane == 0) arrive_leader<PAIR>(acc_empty + 8 * (done & 1));
             ++done;
         }
     }
@@ -384,9 +331,13 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a
     tc_fence_before();
     __syncthreads();
     __syncwarp();
-    cluster_sync();
-    if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    if constexpr (PAIR) cluster_sync();
+    if (warp == 2) {
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        else
+            tmem_dealloc(tmem, kTmemCols);
+    }
 }
 
 // The splits' sums in their order, then the epilogue. VEC elements of a row a thread (8 where every row
@@ -424,10 +375,11 @@ __global__ void __launch_bounds__(256) product_join_kernel(const float *parts, i
         } else {
             Run r = run_of(v);
             if constexpr (KIND == EPI_LINEAR) {
-                const uint64_t unit = splat2(e.unit);
-                const Run b = e.bias ? load_run(e.bias, e.bias_dtype, j) : run_splat(0.f);
+                if (e.bias) {
+                    const Run b = load_run(e.bias, e.bias_dtype, j);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) r.p[q] = add2(mul2(r.p[q], unit), b.p[q]);
+                    for (int q = 0; q < 4; ++q) r.p[q] = add2(r.p[q], b.p[q]);
+                }
                 if (e.z) store_run(e.z, e.z_dtype, at, r);
                 with_act(e.act, [&](auto act) {
                     constexpr int ACT = decltype(act)::value;
@@ -457,11 +409,10 @@ __global__ void __launch_bounds__(256) product_join_kernel(const float *parts, i
     }
 }
 
-// Rows of either job in runs of 8, the second job's after the first's.
-__global__ void __launch_bounds__(256) copy_rows16_kernel(const CopyJob a, const CopyJob b) {
-    griddep_wait();
+// Rows of either job in runs of 8, the second job's after the first's, by `blocks` CTAs of 256 threads.
+__device__ __forceinline__ void copy_rows(const CopyJob &a, const CopyJob &b, int block, int blocks) {
     const long long per_a = (a.n + 7) / 8, per_b = (b.n + 7) / 8, first = a.rows * per_a, total = first + b.rows * per_b;
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<long long>(gridDim.x) * 256) {
+    for (long long i = static_cast<long long>(block) * 256 + threadIdx.x; i < total; i += static_cast<long long>(blocks) * 256) {
         const bool second = i >= first;
         const CopyJob &job = second ? b : a;
         const long long k = second ? i - first : i, per_row = second ? per_b : per_a;
@@ -475,15 +426,22 @@ __global__ void __launch_bounds__(256) copy_rows16_kernel(const CopyJob a, const
                        static_cast<uint32_t>(v[1] >> 32));
     }
 }
+__global__ void __launch_bounds__(256) copy_rows16_kernel(const CopyJob a, const CopyJob b) {
+    griddep_wait();
+    copy_rows(a, b, blockIdx.x, gridDim.x);
+}
 
 // Sums over rows: a cluster of CTAs takes 64 columns (8 lanes of 8 each, 32 rows at a time), each a share of
-// the rows; their sums meet in distributed shared memory, in the order of the shares.
+// the rows; their sums meet in distributed shared memory, in the order of the shares. The clusters past
+// the columns copy rows.
 constexpr int kSumColumns = 64, kSumSplit = 8;
 template <class T>
 __global__ void __launch_bounds__(256) column_sums_kernel(const T *x, long long stride, long long rows, int n, bool runs, float *out,
-                                                          int accumulate) {
+                                                          int accumulate, const CopyJob a, const CopyJob b) {
     __shared__ float red[32][kSumColumns + 1], mine[kSumColumns];
     griddep_wait();
+    const int summing = (n + kSumColumns - 1) / kSumColumns * kSumSplit;
+    if (blockIdx.x >= summing) return copy_rows(a, b, blockIdx.x - summing, gridDim.x - summing);
     const int rank = blockIdx.x % kSumSplit, first = blockIdx.x / kSumSplit * kSumColumns;
     const int lane = threadIdx.x & 7, row0 = threadIdx.x >> 3, c = first + lane * 8;
     const long long share = (rows + kSumSplit - 1) / kSumSplit, r0 = share * rank, r1 = r0 + share < rows ? r0 + share : rows;
@@ -534,31 +492,49 @@ std::atomic<int> g_smem[64];
 
 // How a product runs.
 struct Plan {
+    bool pair;
     int tile_n, tiles_m, tiles_n, steps, splits, steps_per_split;
 };
-// Tiles of 128 columns where those of 256 would leave half of the pairs of CTAs idle; with fewer tiles
-// than pairs the summed axis is split, as many times as give every pair an item of at least 4 steps.
-Plan plan_of(long long m, int n, long long k, int batch, int passes, bool symmetric, bool may_split) {
-    Plan p;
-    p.tiles_m = static_cast<int>((m + kTile - 1) / kTile);
-    auto tiles = [&](int tile_n) {
-        const long long c = (n + tile_n - 1) / tile_n, all = static_cast<long long>(p.tiles_m) * c;
-        return batch * (symmetric ? all - static_cast<long long>(kTile / tile_n) * p.tiles_m * (p.tiles_m - 1) / 2 : all);
+// The cheapest form, by what was measured on one GB300: a step of 64 takes 0.33 us where a pair's 256 x 256
+// products keep the tensor cores busy, else what it takes to issue and to load; a tile's epilogue runs
+// under the next tile's products, the last one's alone; splitting the summed axis costs writing and reading
+// the parts in fp32 and a launch.
+Plan plan_of(long long m, int n, long long k, bool may_split) {
+    struct Form {
+        bool pair;
+        int tile_n;
+        double step, epilogue;
     };
-    p.tile_n = tiles(kTile) <= kGridCap / 4 ? kTile / 2 : kTile;
-    p.tiles_n = (n + p.tile_n - 1) / p.tile_n;
-    p.steps = static_cast<int>((k + kStep - 1) / kStep) * passes;
-    long long s = may_split ? kGridCap / 2 / tiles(p.tile_n) : 1;
-    if (s > p.steps / 4) s = p.steps / 4;
-    if (p.steps < 12 || s < 1) s = 1;
-    p.steps_per_split = static_cast<int>((p.steps + s - 1) / s);
-    p.splits = (p.steps + p.steps_per_split - 1) / p.steps_per_split;
-    return p;
+    constexpr Form forms[] = {{true, 256, 0.33, 5.2}, {true, 128, 0.22, 2.6}, {false, 128, 0.20, 2.6}, {false, 64, 0.17, 1.3}};
+    Plan best = {};
+    double least = 1e300;
+    for (const Form &f : forms) {
+        Plan p = {f.pair, f.tile_n, 0, 0, 0, 0, 0};
+        const int rows = f.pair ? kTile : kHalf, places = f.pair ? kGridCap / 2 : kGridCap;
+        p.tiles_m = static_cast<int>((m + rows - 1) / rows);
+        p.tiles_n = (n + f.tile_n - 1) / f.tile_n;
+        p.steps = static_cast<int>((k + kStep - 1) / kStep);
+        const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+        long long most = may_split ? places / tiles : 1;
+        if (most > p.steps / 4) most = p.steps / 4;
+        for (long long s : {1LL, most}) {
+            if (s < 1) continue;
+            p.steps_per_split = static_cast<int>((p.steps + s - 1) / s);
+            p.splits = (p.steps + p.steps_per_split - 1) / p.steps_per_split;
+            const double rounds = static_cast<double>((tiles * p.splits + places - 1) / places), products = p.steps_per_split * f.step;
+            const double parts = p.splits > 1 ? 4. + static_cast<double>(m) * n * 4 * (p.splits + 1) / 6e6 : 0.;
+            const double cost = (rounds - 1) * (products > f.epilogue ? products : f.epilogue) + products + f.epilogue + parts;
+            if (cost < least) {
+                least = cost;
+                best = p;
+            }
+        }
+    }
+    return best;
 }
 
-bool encode_operand(CUtensorMap *m, const Product &p, const Operand &o, const void *ptr, long long rows, int box_rows) {
-    return o.turned ? encode_matrices16(m, p.bf16, ptr, rows, p.k, p.batch, o.pitch * 2, o.batch_stride * 2, kStep)
-                    : encode_matrices16(m, p.bf16, ptr, p.k, rows, p.batch, o.pitch * 2, o.batch_stride * 2, box_rows);
+bool encode_operand(CUtensorMap *m, const Product &p, const Operand &o, long long rows, int box_rows) {
+    return o.turned ? encode_rows16(m, p.bf16, o.p, rows, p.k, o.pitch * 2, kStep) : encode_rows16(m, p.bf16, o.p, p.k, rows, o.pitch * 2, box_rows);
 }
 
 template <int KIND>
@@ -574,19 +550,16 @@ int launch_join(const float *parts, int splits, const Product &p, int sms, bool 
 
 size_t product_parts_bytes(long long m, int n, long long k) {
     if (m <= 0) return 0;
-    const Plan q = plan_of(m, n, k, 1, 1, false, true);
+    const Plan q = plan_of(m, n, k, true);
     return q.splits > 1 ? static_cast<size_t>(q.splits) * m * n * 4 : 0;
 }
 
 int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
     if (p.k == 0) return launch_join<EPI_SUMS>(nullptr, 0, p, sms, pdl, s);
-    const int passes = p.a.lo ? 3 : 1;
-    const Plan q = plan_of(p.m, p.n, p.k, p.batch, passes, p.symmetric, p.parts != nullptr);
-    Maps maps;
-    if (!encode_operand(&maps.a[0], p, p.a, p.a.hi, p.m, kHalf) || !encode_operand(&maps.b[0], p, p.b, p.b.hi, p.n, q.tile_n / 2) ||
-        !encode_operand(&maps.a[1], p, p.a, p.a.lo ? p.a.lo : p.a.hi, p.m, kHalf) ||
-        !encode_operand(&maps.b[1], p, p.b, p.b.lo ? p.b.lo : p.b.hi, p.n, q.tile_n / 2))
-        return MHC_ERR_CUDA;
+    const Plan q = plan_of(p.m, p.n, p.k, p.parts != nullptr);
+    const int ctas = q.pair ? 2 : 1;
+    CUtensorMap ma, mb;
+    if (!encode_operand(&ma, p, p.a, p.m, kHalf) || !encode_operand(&mb, p, p.b, p.n, q.tile_n / ctas)) return MHC_ERR_CUDA;
     Args a = {};
     a.m = p.m;
     a.n = p.n;
@@ -597,18 +570,14 @@ int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cu
     a.steps = q.steps;
     a.tile_n = q.tile_n;
     a.chain = p.exact ? kChainExact : kChain;
-    a.passes = passes;
-    a.symmetric = p.symmetric;
-    const long long all = static_cast<long long>(q.tiles_m) * q.tiles_n;
-    const long long items = p.symmetric ? p.batch * (all - static_cast<long long>(kTile / q.tile_n) * q.tiles_m * (q.tiles_m - 1) / 2)
-                                        : p.batch * all * q.splits;
+    const long long items = static_cast<long long>(q.tiles_m) * q.tiles_n * q.splits;
     if (items > INT32_MAX - 1024) return MHC_ERR_UNSUPPORTED;
     a.items = static_cast<int>(items);
     a.a_turned = p.a.turned;
     a.b_turned = p.b.turned;
     const uint32_t fmt = p.bf16 ? 1u : 0u;
     a.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((p.a.turned ? 1u : 0u) << 15) | ((p.b.turned ? 1u : 0u) << 16) |
-              (static_cast<uint32_t>(q.tile_n >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+              (static_cast<uint32_t>(q.tile_n >> 3) << 17) | (static_cast<uint32_t>(ctas * kHalf >> 4) << 24);
     a.status = status;
     a.timeout_ns = wait_timeout_ns();
     a.e = p.epi;
@@ -622,45 +591,53 @@ int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cu
     }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
-    void (*const kernels[])(const Maps, const Args) = {product_kernel<EPI_SUMS>, product_kernel<EPI_LINEAR>,
-                                                       product_kernel<EPI_SLOPE>, product_kernel<EPI_PAIR>};
+    void (*const kernels[2][3])(const CUtensorMap, const CUtensorMap, const Args) = {
+        {product_kernel<EPI_SUMS, false>, product_kernel<EPI_LINEAR, false>, product_kernel<EPI_SLOPE, false>},
+        {product_kernel<EPI_SUMS, true>, product_kernel<EPI_LINEAR, true>, product_kernel<EPI_SLOPE, true>}};
     if (!g_smem[dev & 63].load(std::memory_order_acquire)) {
-        for (auto kern : kernels)
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return MHC_ERR_CUDA;
+        for (auto &row : kernels)
+            for (auto kern : row)
+                if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return MHC_ERR_CUDA;
         g_smem[dev & 63].store(1, std::memory_order_release);
     }
-    const long long pairs = sms / 2;
+    const long long places = sms / ctas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * static_cast<unsigned>(a.items < pairs ? a.items : pairs));
+    cfg.gridDim = dim3(ctas * static_cast<unsigned>(a.items < places ? a.items : places));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    if (int e = note_launch(cudaLaunchKernelEx(&cfg, kernels[kind], maps, a))) return e;
+    if (int e = note_launch(cudaLaunchKernelEx(&cfg, kernels[q.pair][kind], ma, mb, a))) return e;
     if (q.splits == 1) return MHC_OK;
     return p.kind == EPI_SUMS     ? launch_join<EPI_SUMS>(p.parts, q.splits, p, sms, pdl, s)
            : p.kind == EPI_LINEAR ? launch_join<EPI_LINEAR>(p.parts, q.splits, p, sms, pdl, s)
                                   : launch_join<EPI_SLOPE>(p.parts, q.splits, p, sms, pdl, s);
 }
 
-cudaError_t launch_copy_rows16(const CopyJob &a, const CopyJob &b, int sms, bool pdl, cudaStream_t s) {
+namespace {
+unsigned copy_blocks(const CopyJob &a, const CopyJob &b, int sms) {
     const long long need = (a.rows * ((a.n + 7) / 8) + b.rows * ((b.n + 7) / 8) + 255) / 256, cap = static_cast<long long>(sms) * 8;
-    return launch_block_kernel(copy_rows16_kernel, static_cast<unsigned>(need < cap ? need : cap), 256, 0, pdl, s, a, b);
+    return static_cast<unsigned>(need < cap ? need : cap);
+}
+}  // namespace
+
+cudaError_t launch_copy_rows16(const CopyJob &a, const CopyJob &b, int sms, bool pdl, cudaStream_t s) {
+    return launch_block_kernel(copy_rows16_kernel, copy_blocks(a, b, sms), 256, 0, pdl, s, a, b);
 }
 
-int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, bool pdl,
-                       cudaStream_t s) {
+int launch_column_sums(const void *x, long long stride, int dtype, long long rows, int n, float *out, int accumulate, const CopyJob &a,
+                       const CopyJob &b, int sms, bool pdl, cudaStream_t s) {
     const bool runs = n % 8 == 0 && stride % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((n + kSumColumns - 1) / kSumColumns * kSumSplit);
+    cfg.gridDim = dim3((n + kSumColumns - 1) / kSumColumns * kSumSplit + (copy_blocks(a, b, sms) + kSumSplit - 1) / kSumSplit * kSumSplit);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -673,9 +650,9 @@ int launch_column_sums(const void *x, long long stride, int dtype, long long row
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
     return note_launch(dtype == MHC_BF16 ? cudaLaunchKernelEx(&cfg, column_sums_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16 *>(x),
-                                                              stride, rows, n, runs, out, accumulate)
+                                                              stride, rows, n, runs, out, accumulate, a, b)
                                          : cudaLaunchKernelEx(&cfg, column_sums_kernel<__half>, static_cast<const __half *>(x), stride,
-                                                              rows, n, runs, out, accumulate));
+                                                              rows, n, runs, out, accumulate, a, b));
 }
 
 }  // namespace mhc
