@@ -16,8 +16,8 @@ namespace {
 constexpr int kRows = 128;                          // of weights by a cluster
 constexpr int kWeightBytes = 2 * kPairBoxBytes;
 constexpr int kThreads = 192;                       // loads, products, four epilogue warps
-constexpr int kMaxStages = 11;
-constexpr int kStageBudget = 208 * 1024;
+constexpr int kMaxStages = 6;
+constexpr int kStageBudget = 100 * 1024;             // two CTAs an SM: 1 x 7168 into 4096 15.6 -> 13.6 us, 1 x 2048 into 2048 10.0 -> 6.0
 constexpr int kMaxSplit = 8;
 
 enum FewSite : int { SITE_F_EMPTY = 90, SITE_F_FULL, SITE_F_ACC, SITE_F_DRAIN };
@@ -34,7 +34,7 @@ struct FewArgs {
 };
 
 template <int KIND>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
 few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ FewArgs a) {
     extern __shared__ uint8_t raw[];
@@ -75,7 +75,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     griddep_wait();
 
     if (warp == 0 && elect_one()) {
-        const uint64_t policy = policy_evict_normal();
+        const uint64_t policy = policy_evict_first();      // weights: past L2 before they come again
         int it = 0;
         bool ok = true;
         for (; it < mine; ++it) {
@@ -187,7 +187,7 @@ int launch_few_tokens(const Product &p, int sms, unsigned int *status, bool pdl,
     a.steps = static_cast<int>((p.k + kPairStep - 1) / kPairStep);
     const int tiles = (p.n + kRows - 1) / kRows;
     a.split = 1;
-    while (a.split < kMaxSplit && 2 * a.split * tiles <= sms && a.steps >= 4 * a.split) a.split *= 2;
+    while (a.split < kMaxSplit && 2 * a.split * tiles <= 2 * sms && a.steps >= 2 * a.split) a.split *= 2;
     a.per = (a.steps + a.split - 1) / a.split;
     const int most = 512 / a.width;
     a.chain = p.exact ? (a.per + most - 1) / most > 8 ? (a.per + most - 1) / most : 8 : a.per;

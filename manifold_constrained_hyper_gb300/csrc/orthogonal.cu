@@ -41,7 +41,7 @@ Shape shape_of(int batch, int m, int n) {
     s.parts_at = 0;
     s.x_at = up256(static_cast<size_t>(batch) * kNormParts * 8);
     s.a_at = s.x_at + 4 * static_cast<size_t>(batch) * s.x_size * 2;
-    s.sums_at = s.a_at + 4 * static_cast<size_t>(batch) * s.p_size * 2;
+    s.sums_at = s.a_at + 8 * static_cast<size_t>(batch) * s.p_size * 2;
     s.counters_at = s.sums_at + kNsPartsBytes;
     s.total = s.counters_at + up256(kNsCounters * 4);
     return s;
@@ -178,7 +178,7 @@ int launch_orthogonal(const OrthogonalArgs &a, int sms, unsigned int *status, bo
     uint8_t *const ws = static_cast<uint8_t *>(a.workspace);
     __half *const x = reinterpret_cast<__half *>(ws + sh.x_at), *const p = reinterpret_cast<__half *>(ws + sh.a_at);
     const long long xs = sh.x_size * a.batch, ps = sh.p_size * a.batch;
-    NsCall c = {a.batch, a.m, a.n, a.steps, a.a, a.b, a.c, {{x, x + xs}, {x + 2 * xs, x + 3 * xs}}, {p, p + ps}, {p + 2 * ps, p + 3 * ps},
+    NsCall c = {a.batch, a.m, a.n, a.steps, a.a, a.b, a.c, {{x, x + xs}, {x + 2 * xs, x + 3 * xs}}, {{p, p + ps}, {p + 2 * ps, p + 3 * ps}, {p + 4 * ps, p + 5 * ps}, {p + 6 * ps, p + 7 * ps}},
                 sh.x_pitch, sh.x_size, sh.p_pitch, sh.p_size, a.out, a.out_dtype, reinterpret_cast<float *>(ws + sh.sums_at),
                 reinterpret_cast<unsigned int *>(ws + sh.counters_at)};
     const int e = a.dtype == MHC_F32    ? launch_start<float>(a, sh, c, sms, pdl, s)

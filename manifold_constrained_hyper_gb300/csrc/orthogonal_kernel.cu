@@ -32,20 +32,28 @@ constexpr int kBand = 8;
 
 enum NsSite : int { SITE_N_EMPTY = 100, SITE_N_FULL, SITE_N_ACC_EMPTY, SITE_N_ACC_FULL, SITE_N_DRAIN, SITE_N_GRID, SITE_N_GO, SITE_N_MEET, SITE_N_PARTS };
 
-// One of the three products of a step.
+// The matrices [p][p] of a step: A and P, and where two steps are one, P A (then the two P's product) and the
+// second P.
+enum NsMatrix : int { M_A, M_P, M_T, M_R, M_COUNT };
+enum NsRole : int { R_GRAM, R_SQUARE, R_APPLY };
+// One product.
 struct Phase {
-    int m, n;
-    int tiles_m, tiles_n, tile_n, steps, splits, per, items;
+    int role;                       // GRAM: of X with itself; SQUARE: of two matrices; APPLY: of one with X
+    int a, b, out, add;             // matrices; add: what is added times of_add (-1: nothing)
+    int m, n, tiles_m, tiles_n, tile_n, steps, passes, splits, per, items;
     int symmetric, a_turned, b_turned;
     uint32_t idesc;
+    float of_sum, of_add, of_unit;  // of_unit: on the diagonal
 };
+constexpr int kPairPhases = 7, kStepPhases = 3, kPhases = kPairPhases + 2 * kStepPhases;
 struct NsArgs {
-    Phase phase[3];                 // A = X X^T, P = a I + b A + c A A, X <- P X
-    int batch, rounds;              // of the three
-    int wide;                       // X is the second operand of the third product, else the first
-    __half *x[2][2], *g[2], *p[2];  // [turn][hi, lo]
+    // two steps as one (`pairs` times), a step (`singles` times), the last step
+    Phase phase[kPhases];
+    int pairs, singles;
+    int wide;                       // X is the second operand where it is applied to, else the first
+    __half *x[2][2], *mat[M_COUNT][2];      // [turn][hi, lo]
     long long x_pitch, x_size, p_pitch, p_size;
-    float of_sum[3], of_a, of_unit[2], of_out;
+    float of_out;
     void *out;
     int out_dtype, out_wide;
     float *parts;
@@ -54,9 +62,31 @@ struct NsArgs {
     unsigned long long timeout_ns;
 };
 struct NsMaps {
-    CUtensorMap gram_a[2][2], gram_b[2][2], last_x[2][2], poly_a[2], poly_b[2], last_p[2];
-    CUtensorMap to_x[2][2], to_g[2], to_p[2], to_out;   // 32 rows of 64 columns, to store
+    CUtensorMap gram_a[2][2], gram_b[2][2], apply_x[2][2];      // [turn][hi, lo]
+    CUtensorMap mat_a[M_COUNT][2], mat_b[M_COUNT][2];
+    CUtensorMap to_x[2][2], to_mat[M_COUNT][2], to_out;         // 32 rows of 64 columns, to store
 };
+// Which of the phases the ph-th product is, how many like it came before, and X's turn.
+struct Step {
+    int phase, round, x;
+};
+__device__ __forceinline__ Step step_of(const NsArgs &a, int ph) {
+    const int in_pairs = kPairPhases * a.pairs;
+    Step s;
+    if (ph < in_pairs) {
+        s.round = ph / kPairPhases;
+        s.phase = ph - s.round * kPairPhases;
+        s.x = s.round & 1;
+        return s;
+    }
+    ph -= in_pairs;
+    const int step = ph / kStepPhases;
+    const bool last = step == a.singles;
+    s.round = last ? 0 : step;
+    s.phase = kPairPhases + (last ? kStepPhases : 0) + ph - step * kStepPhases;
+    s.x = (a.pairs + step) & 1;
+    return s;
+}
 
 struct Place {
     int batch, split, ti, tj, tile;
@@ -106,7 +136,7 @@ struct Target {
     float unit;
     const __half *x_hi, *x_lo;      // what is added, times of_x, and of_unit on the diagonal; or NULL
     float of_x, of_unit;            // of_unit: where there is no x too
-    bool mirror, final;
+    bool mirror, final, one;        // one: hi alone, rounded
     int m, n;
 };
 // 8 columns of a row of x.
@@ -129,7 +159,7 @@ __device__ __forceinline__ void pair8(const Target &t, int i, int j, const float
         if (t.of_unit != 0.f) r = add2(r, f2_pack(i == j + 2 * q ? t.of_unit : 0.f, i == j + 2 * q + 1 ? t.of_unit : 0.f));
         // hi: the leading 11 bits, cut, not rounded (two masks where a conversion back would take four
         // times as long); lo, up to 2^-10 of it, holds 11 more
-        const uint64_t h = r & 0xFFFFE000FFFFE000ull;
+        const uint64_t h = t.one ? r : r & 0xFFFFE000FFFFE000ull;
         hw[q] = pack2(h, tag);
         lw[q] = pack2(fma2(h, splat2(-1.f), r), tag);
     }
@@ -145,7 +175,7 @@ __device__ __forceinline__ void mirror8(const Target &t, int i, int j, const uin
     for (int q = 0; q < 8; ++q, h += step, l += step) {
         if (j + q >= t.n) break;
         *h = static_cast<uint16_t>(hw[q >> 1] >> (q & 1) * 16);
-        *l = static_cast<uint16_t>(lw[q >> 1] >> (q & 1) * 16);
+        if (!t.one) *l = static_cast<uint16_t>(lw[q >> 1] >> (q & 1) * 16);
     }
 }
 __device__ __forceinline__ void tma_store_3d_plain(const CUtensorMap *m, int c0, int c1, int c2, uint32_t src) {
@@ -191,7 +221,7 @@ __device__ __forceinline__ void put64(const NsArgs &a, const Target &t, const CU
     __syncwarp();
     if (lane == 0) {
         tma_store_3d_plain(hi_map, j, i0, batch, held);
-        if (!t.final) tma_store_3d_plain(lo_map, j, i0, batch, held + kOutBytes);
+        if (!t.final && !t.one) tma_store_3d_plain(lo_map, j, i0, batch, held + kOutBytes);
         bulk_commit();
     }
 }
@@ -205,7 +235,7 @@ __device__ __forceinline__ void put8(const NsArgs &a, const Target &t, int batch
         pair8(t, i, j, v, xh, xl, &hw, &lw);
         const long long at = static_cast<long long>(i) * t.pitch + j;
         *reinterpret_cast<uint4 *>(t.hi + at) = hw;
-        *reinterpret_cast<uint4 *>(t.lo + at) = lw;
+        if (!t.one) *reinterpret_cast<uint4 *>(t.lo + at) = lw;
         if (t.mirror) mirror8(t, i, j, hw, lw);
         return;
     }
@@ -246,7 +276,8 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, phases = 3 * a.rounds;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int phases = kPairPhases * a.pairs + kStepPhases * (a.singles + 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -280,8 +311,8 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
         uint32_t it = 0;
         bool ok = true;
         for (int ph = 0; ph < phases && ok; ++ph) {
-            const int which = ph % 3, x = ph / 3 & 1;
-            const Phase &f = a.phase[which];
+            const Step at = step_of(a, ph);
+            const Phase &f = a.phase[at.phase];
             if (ph) {
                 // one thread a CTA asks, for the epilogue too
                 ok = count_wait(a.counters, ph * gridDim.x, a, abort_flag, SITE_N_GRID);
@@ -289,20 +320,18 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 fence_proxy_async_global();
                 mbar_arrive(go);
             }
-            const CUtensorMap *const ma = which == 0   ? maps.gram_a[x]
-                                          : which == 1 ? maps.poly_a
-                                          : a.wide     ? maps.last_p
-                                                       : maps.last_x[x];
-            const CUtensorMap *const mb = which == 0   ? maps.gram_b[x]
-                                          : which == 1 ? maps.poly_b
-                                          : a.wide     ? maps.last_x[x]
-                                                       : maps.last_p;
+            const CUtensorMap *const ma = f.role == R_GRAM                ? maps.gram_a[at.x]
+                                          : f.role == R_APPLY && !a.wide ? maps.apply_x[at.x]
+                                                                         : maps.mat_a[f.a];
+            const CUtensorMap *const mb = f.role == R_GRAM               ? maps.gram_b[at.x]
+                                          : f.role == R_APPLY && a.wide ? maps.apply_x[at.x]
+                                                                        : maps.mat_b[f.b];
             const int half = f.tile_n / 2;
             for (int item = pair; item < f.items && ok; item += pairs) {
                 const Place p = place_of(f, item);
                 const int s0 = p.split * f.per, s1 = s0 + f.per < f.steps ? s0 + f.per : f.steps;
                 const int ci = p.ti * kTile + static_cast<int>(rank) * kHalf, cj = p.tj * f.tile_n + static_cast<int>(rank) * half;
-                int kb = s0 / 3, part = s0 - 3 * kb;
+                int kb = s0 / f.passes, part = s0 - f.passes * kb;
                 for (int st = s0; st < s1; ++st, ++it) {
                     const uint32_t s = it % kStages, turn_of = (it / kStages) & 1;
                     if (!mbar_wait(empty + 8 * s, turn_of ^ 1, abort_flag, a.timeout_ns, a.status, SITE_N_EMPTY)) {
@@ -325,7 +354,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     } else {
                         tma_load_pair_3d(db, bm, k, cj, p.batch, bar);
                     }
-                    if (++part == 3) {
+                    if (++part == f.passes) {
                         part = 0;
                         ++kb;
                     }
@@ -346,7 +375,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
         uint32_t it = 0, done = 0;
         bool ok = true;
         for (int ph = 0; ph < phases && ok; ++ph) {
-            const Phase &f = a.phase[ph % 3];
+            const Phase &f = a.phase[step_of(a, ph).phase];
             const uint64_t na = f.a_turned ? 2048 >> 4 : 32 >> 4, nb = f.b_turned ? 2048 >> 4 : 32 >> 4;
             for (int item = pair; item < f.items && ok; item += pairs, ++done) {
                 const int split = item % f.splits, s0 = split * f.per, s1 = s0 + f.per < f.steps ? s0 + f.per : f.steps;
@@ -394,9 +423,9 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
             return __all_sync(0xffffffffu, all) != 0;
         };
         for (int ph = 0; ph < phases && ok; ++ph) {
-            const int which = ph % 3, x = ph / 3 & 1;
+            const Step st = step_of(a, ph);
             const bool final = ph + 1 == phases;
-            const Phase &f = a.phase[which];
+            const Phase &f = a.phase[st.phase];
             const int width = f.tile_n / 2, first = w / 4 * width;
             if (ph) {
                 ok = mbar_wait(go, (ph - 1) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_GO);
@@ -408,18 +437,20 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 const uint32_t buf = done & 1;
                 const int i0 = p.ti * kTile + static_cast<int>(rank) * kHalf + quad * 32, j0 = p.tj * f.tile_n;
                 Target t;
-                const long long at = p.batch * (which == 2 ? a.x_size : a.p_size);
-                __half *const *const to_pair = which == 0 ? a.g : which == 1 ? a.p : a.x[x ^ 1];
+                const bool to_x = f.role == R_APPLY;
+                const long long at = p.batch * (to_x ? a.x_size : a.p_size);
+                __half *const *const to_pair = to_x ? a.x[st.x ^ 1] : a.mat[f.out];
                 t.hi = to_pair[0] + at;
                 t.lo = to_pair[1] + at;
-                t.pitch = which == 2 ? a.x_pitch : a.p_pitch;
-                t.unit = a.of_sum[which];
-                t.x_hi = which == 1 && a.of_a != 0.f ? a.g[0] + at : nullptr;
-                t.x_lo = a.g[1] + at;
-                t.of_x = a.of_a;
-                t.of_unit = which == 2 ? 0.f : a.of_unit[which];
+                t.pitch = to_x ? a.x_pitch : a.p_pitch;
+                t.unit = f.of_sum;
+                t.x_hi = f.add < 0 ? nullptr : a.mat[f.add][0] + at;
+                t.x_lo = f.add < 0 ? nullptr : a.mat[f.add][1] + at;
+                t.of_x = f.of_add;
+                t.of_unit = f.of_unit;
                 t.mirror = f.symmetric && j0 >= (p.ti + 1) * kTile;
                 t.final = final;
+                t.one = a.phase[kPhases - 1].passes == 1 && ph + 4 >= phases;   // what the last step reads
                 t.m = f.m;
                 t.n = f.n;
                 ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_ACC_FULL);
@@ -428,7 +459,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 tc_fence_after();
                 const uint32_t sums = tmem + buf * kTile + first + (static_cast<uint32_t>(quad * 32) << 16);
                 if (f.splits == 1) {
-                    const CUtensorMap *const to = final ? &maps.to_out : which == 0 ? maps.to_g : which == 1 ? maps.to_p : maps.to_x[x ^ 1];
+                    const CUtensorMap *const to = final ? &maps.to_out : to_x ? maps.to_x[st.x ^ 1] : maps.to_mat[f.out];
 #pragma unroll 1
                     for (int c = 0; c < width && i0 < f.m && j0 + first + c < f.n; c += 64) {
                         if (!final || a.out_wide) {
@@ -462,9 +493,9 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     ok = meet();
                     if (!ok) break;
                     if (threadIdx.x == 64) {
-                        unsigned int *const count = a.counters + 32 + (which * kNsMostPairs + p.tile) * 2 + rank;
+                        unsigned int *const count = a.counters + 32 + (st.phase * kNsMostPairs + p.tile) * 2 + rank;
                         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
-                        count_wait(count, f.splits * (ph / 3 + 1), a, abort_flag, SITE_N_PARTS);
+                        count_wait(count, f.splits * (st.round + 1), a, abort_flag, SITE_N_PARTS);
                     }
                     ok = meet() && !*abort_flag;
                     ok = __all_sync(0xffffffffu, ok);
@@ -544,15 +575,20 @@ int resident_pairs(int *pairs) {
 }
 
 // Tiles of 128 columns, and the summed axis split, where there are few tiles.
-Phase phase_of(int m, int n, int k, int batch, bool symmetric, bool a_turned, bool b_turned, int pairs) {
+Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turned, bool b_turned, int pairs) {
     Phase f = {};
+    const bool symmetric = role != R_APPLY;
+    f.role = role;
+    f.add = -1;
+    f.of_sum = 1.f / kNsScale;
     f.m = m;
     f.n = n;
+    f.passes = passes;
     f.symmetric = symmetric;
     f.a_turned = a_turned;
     f.b_turned = b_turned;
     f.tiles_m = (m + kTile - 1) / kTile;
-    f.steps = 3 * ((k + kPairStep - 1) / kPairStep);
+    f.steps = passes * ((k + kPairStep - 1) / kPairStep);
     auto tiles = [&](int tile_n) {
         const long long c = (n + tile_n - 1) / tile_n, all = f.tiles_m * c;
         return batch * (symmetric ? all - kTile / tile_n * (static_cast<long long>(f.tiles_m) * (f.tiles_m - 1) / 2) : all);
@@ -593,34 +629,90 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     const int p = c.m < c.n ? c.m : c.n, q = c.m < c.n ? c.n : c.m;
     const bool wide = c.m <= c.n;
     NsArgs a = {};
-    a.phase[0] = phase_of(p, p, q, c.batch, true, !wide, !wide, pairs);
-    a.phase[1] = phase_of(p, p, p, c.batch, true, false, false, pairs);
-    a.phase[2] = phase_of(c.m, c.n, p, c.batch, false, false, wide, pairs);
-    a.batch = c.batch;
-    a.rounds = c.steps;
+    // The last step of a bf16 result takes hi alone (11 bits): what is lost there is amplified once, by at most a, and
+    // comes to 0.2 to 1.4e-3 of the result (worst where an eighth of the directions is strong and the rest 0.003 of them),
+    // beside the 1.7e-3 of its rounding; fp16 rounds 2e-4. One step earlier it would come to 2.5e-3.
+    const int last_passes = c.out_dtype == MHC_BF16 ? 1 : 3;
+    // Two steps as one, X <- (P1 P0) X with A1 = P0 P0 A: two products of X less, three of matrices [p][p] more. The product
+    // of two P has to stay below 16. 4096 x 7168: 17 % fewer operations; small matrices are bound by the number of products.
+    double largest = 0.;
+    for (int i = 0; i <= 64; ++i) {
+        const double l = i / 32., v = std::fabs(c.a + l * (c.b + l * c.c));
+        if (v > largest) largest = v;
+    }
     a.wide = wide;
-    for (int h = 0; h < 2; ++h) {
-        a.x[0][h] = c.x[0][h];
-        a.x[1][h] = c.x[1][h];
-        a.g[h] = c.g[h];
-        a.p[h] = c.p[h];
+    const Phase gram = phase_of(R_GRAM, p, p, q, c.batch, 3, !wide, !wide, pairs), square = phase_of(R_SQUARE, p, p, p, c.batch, 3, false, false, pairs),
+                apply = phase_of(R_APPLY, c.m, c.n, p, c.batch, 3, false, wide, pairs);
+    const bool two = p >= 2048 && q >= p + p / 4 && largest <= 3.8 && square.tile_n == apply.tile_n;
+    a.pairs = two ? (c.steps - 1) / 2 : 0;
+    a.singles = c.steps - 1 - 2 * a.pairs;
+    // a I + b A + c A A = c (A + h I)^2 + (a - c h^2) I with h = b / 2c: A is kept with h on its diagonal and is not
+    // read again. Where c h^2 is far above the coefficients that would cancel, and b A is added instead.
+    const double h = c.c != 0.f ? c.b / (2. * c.c) : 0., square_of = c.c * h * h;
+    const bool complete = c.c != 0.f && std::fabs(square_of) <= 4. * (std::fabs(c.a) + std::fabs(c.b) + std::fabs(c.c)) && std::fabs(h) <= 8.;
+    auto poly = [&](Phase f, int out) {
+        f.a = f.b = M_A;
+        f.out = out;
+        f.of_sum = c.c / kNsScale;
+        f.add = M_A;
+        f.of_add = c.b;
+        f.of_unit = c.a * kNsScale;
+        return f;
+    };
+    auto times = [&](Phase f, int x, int y, int out) {
+        f.a = x;
+        f.b = y;
+        f.out = out;
+        return f;
+    };
+    Phase *f = a.phase;
+    *f++ = times(gram, 0, 0, M_A);
+    *f++ = poly(square, M_P);
+    *f++ = times(square, M_P, M_A, M_T);
+    *f++ = times(square, M_P, M_T, M_A);
+    *f++ = poly(square, M_R);
+    *f++ = times(square, M_R, M_P, M_T);
+    *f++ = times(apply, M_T, M_T, 0);
+    for (int last = 0; last < 2; ++last) {
+        const int passes = last ? last_passes : 3;
+        Phase g = last ? phase_of(R_GRAM, p, p, q, c.batch, passes, !wide, !wide, pairs) : gram;
+        Phase s2 = last ? phase_of(R_SQUARE, p, p, p, c.batch, passes, false, false, pairs) : square;
+        const Phase ap = last ? phase_of(R_APPLY, c.m, c.n, p, c.batch, passes, false, wide, pairs) : apply;
+        g = times(g, 0, 0, M_A);
+        s2 = poly(s2, M_P);
+        if (complete) {
+            g.of_unit = static_cast<float>(h * kNsScale);
+            s2.add = -1;
+            s2.of_unit = static_cast<float>((c.a - square_of) * kNsScale);
+        }
+        *f++ = g;
+        *f++ = s2;
+        *f++ = times(ap, M_P, M_P, 0);
+    }
+    // one load map a matrix and operand: the phases that share one have tiles of one width
+    for (Phase &g : a.phase)
+        if (g.role == R_GRAM ? g.tile_n != gram.tile_n : g.role == R_SQUARE ? g.tile_n != square.tile_n : g.tile_n != apply.tile_n) {
+            const int at = static_cast<int>(&g - a.phase);
+            const Phase &like = g.role == R_GRAM ? gram : g.role == R_SQUARE ? square : apply;
+            Phase n = like;
+            n.steps = g.steps;
+            n.passes = g.passes;
+            n.per = (g.steps + like.splits - 1) / like.splits;
+            n.splits = (g.steps + n.per - 1) / n.per;
+            n.items = like.items / like.splits * n.splits;
+            n.a = g.a, n.b = g.b, n.out = g.out, n.add = g.add;
+            n.of_sum = g.of_sum, n.of_add = g.of_add, n.of_unit = g.of_unit;
+            a.phase[at] = n;
+        }
+    for (int k = 0; k < 2; ++k) {
+        a.x[0][k] = c.x[0][k];
+        a.x[1][k] = c.x[1][k];
+        for (int t = 0; t < M_COUNT; ++t) a.mat[t][k] = c.mat[t][k];
     }
     a.x_pitch = c.x_pitch;
     a.x_size = c.x_size;
     a.p_pitch = c.p_pitch;
     a.p_size = c.p_size;
-    a.of_sum[0] = a.of_sum[2] = 1.f / kNsScale;
-    a.of_sum[1] = c.c / kNsScale;
-    // a I + b A + c A A = c (A + h I)^2 + (a - c h^2) I with h = b / 2c: A is kept with h on its diagonal and is not
-    // read again. Where c h^2 is far above the coefficients that would cancel, and b A is added instead.
-    const double h = c.c != 0.f ? c.b / (2. * c.c) : 0., square = c.c * h * h;
-    if (c.c != 0.f && std::fabs(square) <= 4. * (std::fabs(c.a) + std::fabs(c.b) + std::fabs(c.c)) && std::fabs(h) <= 8.) {
-        a.of_unit[0] = static_cast<float>(h * kNsScale);
-        a.of_unit[1] = static_cast<float>((c.a - square) * kNsScale);
-    } else {
-        a.of_a = c.b;
-        a.of_unit[1] = c.a * kNsScale;
-    }
     a.of_out = 1.f / (kNsScale * kNsScale);
     a.out = c.out;
     a.out_dtype = c.out_dtype;
@@ -634,20 +726,23 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
         return encode_matrices16(m, false, x, inner, count, c.batch, pitch * 2, size * 2, box);
     };
     bool ok = true;
-    for (int h = 0; h < 2; ++h) {
+    for (int k = 0; k < 2; ++k) {
         for (int t = 0; t < 2; ++t) {
-            ok = ok && rows(&maps.gram_a[t][h], c.x[t][h], c.n, c.m, c.x_pitch, c.x_size, wide ? kHalf : kPairStep);
-            ok = ok && rows(&maps.gram_b[t][h], c.x[t][h], c.n, c.m, c.x_pitch, c.x_size, wide ? a.phase[0].tile_n / 2 : kPairStep);
-            ok = ok && rows(&maps.last_x[t][h], c.x[t][h], c.n, c.m, c.x_pitch, c.x_size, wide ? kPairStep : kHalf);
+            const __half *const x = c.x[t][k];
+            ok = ok && rows(&maps.gram_a[t][k], x, c.n, c.m, c.x_pitch, c.x_size, wide ? kHalf : kPairStep);
+            ok = ok && rows(&maps.gram_b[t][k], x, c.n, c.m, c.x_pitch, c.x_size, wide ? gram.tile_n / 2 : kPairStep);
+            ok = ok && rows(&maps.apply_x[t][k], x, c.n, c.m, c.x_pitch, c.x_size, wide ? kPairStep : kHalf);
+            ok = ok && rows(&maps.to_x[t][k], x, c.n, c.m, c.x_pitch, c.x_size, 32);
         }
-        ok = ok && rows(&maps.poly_a[h], c.g[h], p, p, c.p_pitch, c.p_size, kHalf);
-        ok = ok && rows(&maps.poly_b[h], c.g[h], p, p, c.p_pitch, c.p_size, a.phase[1].tile_n / 2);
-        ok = ok && rows(&maps.last_p[h], c.p[h], p, p, c.p_pitch, c.p_size, wide ? kHalf : a.phase[2].tile_n / 2);
-    }
-    for (int h = 0; h < 2; ++h) {
-        for (int t = 0; t < 2; ++t) ok = ok && rows(&maps.to_x[t][h], c.x[t][h], c.n, c.m, c.x_pitch, c.x_size, 32);
-        ok = ok && rows(&maps.to_g[h], c.g[h], p, p, c.p_pitch, c.p_size, 32);
-        ok = ok && rows(&maps.to_p[h], c.p[h], p, p, c.p_pitch, c.p_size, 32);
+        // without pairs A is squared and P applied, no more
+        for (int t = 0; t < (a.pairs ? M_COUNT : M_T); ++t) {
+            const __half *const x = c.mat[t][k];
+            // where it is the second operand it has the rows of the tile's columns: of a square, or applied to a tall X
+            const bool applied = a.pairs ? false : t == M_P;
+            ok = ok && rows(&maps.mat_a[t][k], x, p, p, c.p_pitch, c.p_size, kHalf);
+            ok = ok && rows(&maps.mat_b[t][k], x, p, p, c.p_pitch, c.p_size, (applied ? apply.tile_n : square.tile_n) / 2);
+            ok = ok && rows(&maps.to_mat[t][k], x, p, p, c.p_pitch, c.p_size, 32);
+        }
     }
     if (a.out_wide)
         ok = ok && encode_matrices16(&maps.to_out, c.out_dtype == MHC_BF16, c.out, c.n, c.m, c.batch, static_cast<unsigned long long>(c.n) * 2,

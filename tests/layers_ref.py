@@ -116,20 +116,24 @@ def layer_norm_backward(d, x, stats, w, d_residual):
 
 
 def orthogonalize(g, steps, coeffs, eps, noise=None):
-    """In 64 bits. noise(value, terms): what a product's result is off by, added where given."""
+    """In 64 bits. noise(value, terms, last): what a product's result is off by, added where given; last:
+    what the last step reads."""
     a, b, c = coeffs
-    off = noise if noise is not None else (lambda v, terms: 0)
+    off = noise if noise is not None else (lambda v, terms, last: 0)
     X = g.double()
     X = X / (torch.linalg.vector_norm(X, dim=(-2, -1), keepdim=True) + eps)
-    X = X + off(X, X.abs())
+    X = X + off(X, X.abs(), steps == 1)
     wide = X.shape[-2] <= X.shape[-1]
-    for _ in range(steps):
+    for k in range(steps):
+        last = k == steps - 1
         Y = X if wide else X.mT
         A = Y @ Y.mT
-        A = A + off(A, Y.abs() @ Y.abs().mT)
+        A = A + off(A, Y.abs() @ Y.abs().mT, last)
         P = a * torch.eye(A.shape[-1], dtype=A.dtype, device=A.device) + b * A + c * (A @ A)
-        P = P + off(P, P.abs() + abs(b) * A.abs() + abs(c) * (A.abs() @ A.abs()))
-        Y = P @ Y + off(Y, P.abs() @ Y.abs())
+        P = P + off(P, P.abs() + abs(b) * A.abs() + abs(c) * (A.abs() @ A.abs()), last)
+        Y = P @ Y
+        if not last:
+            Y = Y + off(Y, P.abs() @ (X if wide else X.mT).abs(), k == steps - 2)
         X = Y if wide else Y.mT
     return X
 
@@ -137,22 +141,33 @@ def orthogonalize(g, steps, coeffs, eps, noise=None):
 def orthogonalize_error(g, steps, coeffs, eps, out_type):
     """The result and how far a run on the tensor cores may be from it. Each product is off by 2^-21 of
     the sizes of its terms (two fp16 parts hold 22 bits, what is left out of the product of two
-    pairs is of that size too) and by what the additions cut; both ways of random sign, carried through
-    the steps in 64 bits; four times the largest of three such runs, and the rounding at the end."""
+    pairs is of that size too) and by what the additions cut; what the last step of a bf16 result reads is rounded to
+    fp16, 2^-11 of itself, which on the diagonal A has b / 2c beside it; all of random sign, carried through
+    the steps in 64 bits, three times. What comes out is a sum of many independent terms: the largest of N such values lies
+    near sqrt(2 ln N) root mean squares (5.5 for three million, where four were not enough), and one
+    more makes it rare; or four times an element's own largest sample; and the rounding at the end."""
     want = orthogonalize(g, steps, coeffs, eps)
     k = max(g.shape[-2:])
     size = 2.0 ** -21 + 2.0 ** -23 * math.sqrt(12 * min(-(-k // 64), 64))
+    shift = abs(coeffs[1] / (2 * coeffs[2])) if coeffs[2] else 0.0
     worst = torch.zeros_like(want)
     for seed in range(3):
         r = torch.Generator(device=g.device).manual_seed(seed)
 
-        def noise(v, terms):
+        def noise(v, terms, last):
             s = torch.randint(0, 2, v.shape, generator=r, device=v.device, dtype=torch.int8).double() * 2 - 1
-            return s * size * terms
+            tol = size * terms
+            if last and out_type == torch.bfloat16:
+                held = v.abs()
+                if v.shape[-1] == v.shape[-2]:
+                    held = held + shift * torch.eye(v.shape[-1], dtype=v.dtype, device=v.device)
+                tol = tol + held * 2.0 ** -11
+            return s * tol
         worst = torch.maximum(worst, (orthogonalize(g, steps, coeffs, eps, noise) - want).abs())
-    # one element's three samples may all be small: at least the matrix's root mean square
+    # worst is the largest of three samples: its root mean square is above one sample's
     floor = worst.square().mean((-2, -1), keepdim=True).sqrt()
-    return want, 4 * torch.maximum(worst, floor) + half_step(out_type, want)
+    most = 1 + math.sqrt(2 * math.log(max(g.numel(), 2)))
+    return want, torch.maximum(4 * worst, most * floor) + half_step(out_type, want)
 
 
 def within(got, want, error, t=None):

@@ -25,6 +25,11 @@ def momentum(g, shape, dtype, scale=1e-3):
     return (scale * (u @ torch.randn(*B, r, N, generator=g, device="cuda") + 0.5 * torch.randn(*B, M, N, generator=g, device="cuda"))).to(dtype)
 
 
+def near(got, want, e):
+    off = float(((got.double() - want).abs() / e).max())
+    assert off <= 1, off
+
+
 SHAPES = [(1, 1), (1, 70), (70, 1), (5, 3), (64, 64), (65, 130), (130, 65), (200, 72), (128, 500), (300, 300), (257, 600), (513, 260),
           (3, 40, 72), (6, 128, 500), (2, 260, 129), (17, 8, 8)]
 
@@ -36,7 +41,19 @@ def test_against_64_bits(shape, dtype, out):
     got = ops.mhc_orthogonalize(g, dtype=out)
     assert got.shape == g.shape and got.dtype == out
     want, e = ref.orthogonalize_error(g, 5, MUON, 1e-7, out)
-    assert ((got.double() - want).abs() <= e).all(), float(((got.double() - want).abs() / e).max())
+    near(got, want, e)
+
+
+@pytest.mark.parametrize("shape", [(2048, 2600), (2600, 2056), (2, 2050, 2570)], ids=str)
+@pytest.mark.parametrize("steps,out", [(2, BF), (3, FP16), (4, BF), (5, BF)])
+def test_two_steps_as_one(shape, steps, out):
+    """Large enough for two steps to be one product of X."""
+    g = momentum(gen(steps), shape, FP32)
+    got = ops.mhc_orthogonalize(g, steps, dtype=out)
+    want, e = ref.orthogonalize_error(g, steps, MUON, 1e-7, out)
+    near(got, want, e)
+    # in the 2-norm what was lost stays below the rounding of the result
+    assert float((got.double() - want).norm() / want.norm()) < 1.2 * torch.finfo(out).eps / 2
 
 
 @pytest.mark.parametrize("steps,coeffs", [(1, MUON), (2, (2.0, -1.5, 0.5)), (12, (1.875, -1.25, 0.375)), (3, (1.5, -0.5, 0.0))])
@@ -44,7 +61,7 @@ def test_other_steps_and_coefficients(steps, coeffs):
     g = momentum(gen(steps), (96, 200), FP32)
     got = ops.mhc_orthogonalize(g, steps, coeffs)
     want, e = ref.orthogonalize_error(g, steps, coeffs, 1e-7, BF)
-    assert ((got.double() - want).abs() <= e).all()
+    near(got, want, e)
 
 
 def test_many_steps_give_the_orthogonal_factor():
@@ -60,7 +77,7 @@ def test_sizes_of_any_magnitude(scale):
     g = momentum(gen(9), (80, 144), FP32, 1.0)
     want, e = ref.orthogonalize_error(g * scale, 5, MUON, 0.0, BF)
     got = ops.mhc_orthogonalize(g * scale, eps=0.0)
-    assert ((got.double() - want).abs() <= e).all()
+    near(got, want, e)
 
 
 def test_zeros_and_values_that_are_not_finite():
