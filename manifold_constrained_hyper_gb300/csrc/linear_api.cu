@@ -301,7 +301,7 @@ mhc_status mhc_orthogonalize(const void *g, int64_t row_stride, int64_t batch_st
     if (!width_ok(m) || !width_ok(n) || batch > 65535 || !half_ok(out_dtype)) return MHC_ERR_UNSUPPORTED;
     if (batch == 0) return MHC_OK;
     const size_t need = mhc_orthogonalize_workspace_bytes(batch, m, n);
-    if (!g || !out || !workspace) return MHC_ERR_NULL;
+    if (!g || !out || (need && !workspace)) return MHC_ERR_NULL;
     if (!aligned(g, size_of(dtype)) || !aligned(out, 2) || !aligned(workspace, 16)) return MHC_ERR_ALIGN;
     if (workspace_bytes < need) return MHC_ERR_WORKSPACE;
     Span in;

@@ -171,9 +171,10 @@ int launch_start(const OrthogonalArgs &a, const Shape &sh, const NsCall &c, int 
 
 }  // namespace
 
-size_t orthogonal_workspace(int batch, int m, int n) { return shape_of(batch, m, n).total; }
+size_t orthogonal_workspace(int batch, int m, int n) { return ns_small_fits(m, n) ? 0 : shape_of(batch, m, n).total; }
 
 int launch_orthogonal(const OrthogonalArgs &a, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
+    if (ns_small_fits(a.m, a.n)) return launch_ns_small(a, ns_polynomial(a.a, a.b, a.c, true), status, pdl, s);
     const Shape sh = shape_of(a.batch, a.m, a.n);
     uint8_t *const ws = static_cast<uint8_t *>(a.workspace);
     __half *const x = reinterpret_cast<__half *>(ws + sh.x_at), *const p = reinterpret_cast<__half *>(ws + sh.a_at);

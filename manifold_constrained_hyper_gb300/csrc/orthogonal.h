@@ -13,6 +13,19 @@ constexpr int kNsMostPairs = 76;                    // pairs of CTAs that share 
 constexpr size_t kNsPartsBytes = static_cast<size_t>(kNsMostPairs) * 2 * 256 * 128 * 4;
 constexpr size_t kNsCounters = 32 + 13 * 2 * kNsMostPairs;
 
+// a I + b A + c A A = c (A + h I)^2 + (a - c h^2) I with h = b / 2c: A is kept with h on its diagonal, and is not
+// read again. Where c h^2 is far above the coefficients that would cancel, and b A is added instead.
+struct NsPolynomial {
+    float of_square, of_a, shift, of_unit;          // of A A, of A; what A has on its diagonal, and the result
+};
+inline NsPolynomial ns_polynomial(float a, float b, float c, bool may_complete) {
+    const double h = c != 0.f ? b / (2. * c) : 0., square = c * h * h;
+    const double size = (a < 0.f ? -a : a) + (b < 0.f ? -b : b) + (c < 0.f ? -c : c);
+    if (may_complete && c != 0.f && (square < 0. ? -square : square) <= 4. * size && (h < 0. ? -h : h) <= 8.)
+        return {c, 0.f, static_cast<float>(h), static_cast<float>(a - square)};
+    return {c, b, 0.f, a};
+}
+
 struct NsCall {
     int batch, m, n, steps;
     float a, b, c;
@@ -23,6 +36,9 @@ struct NsCall {
     float *parts;
     unsigned int *counters;                         // zero
 };
+// A side of at most 128, the other of at most 2048: all of it by clusters of CTAs.
+bool ns_small_fits(int m, int n);
+int launch_ns_small(const OrthogonalArgs &a, const NsPolynomial &f, unsigned int *status, bool pdl, cudaStream_t s);
 int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s);
 
 }  // namespace mhc

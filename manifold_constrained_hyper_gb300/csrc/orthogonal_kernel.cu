@@ -646,19 +646,16 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     const bool two = p >= 2048 && q >= p + p / 4 && largest <= 3.8 && square.tile_n == apply.tile_n;
     a.pairs = two ? (c.steps - 1) / 2 : 0;
     a.singles = c.steps - 1 - 2 * a.pairs;
-    // a I + b A + c A A = c (A + h I)^2 + (a - c h^2) I with h = b / 2c: A is kept with h on its diagonal and is not
-    // read again. Where c h^2 is far above the coefficients that would cancel, and b A is added instead.
-    const double h = c.c != 0.f ? c.b / (2. * c.c) : 0., square_of = c.c * h * h;
-    const bool complete = c.c != 0.f && std::fabs(square_of) <= 4. * (std::fabs(c.a) + std::fabs(c.b) + std::fabs(c.c)) && std::fabs(h) <= 8.;
-    auto poly = [&](Phase f, int out) {
+    auto poly = [&](Phase f, int out, const NsPolynomial &n) {
         f.a = f.b = M_A;
         f.out = out;
-        f.of_sum = c.c / kNsScale;
-        f.add = M_A;
-        f.of_add = c.b;
-        f.of_unit = c.a * kNsScale;
+        f.of_sum = n.of_square / kNsScale;
+        f.add = n.of_a != 0.f ? M_A : -1;
+        f.of_add = n.of_a;
+        f.of_unit = n.of_unit * kNsScale;
         return f;
     };
+    const NsPolynomial plain = ns_polynomial(c.a, c.b, c.c, false), complete = ns_polynomial(c.a, c.b, c.c, true);
     auto times = [&](Phase f, int x, int y, int out) {
         f.a = x;
         f.b = y;
@@ -667,10 +664,10 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     };
     Phase *f = a.phase;
     *f++ = times(gram, 0, 0, M_A);
-    *f++ = poly(square, M_P);
+    *f++ = poly(square, M_P, plain);
     *f++ = times(square, M_P, M_A, M_T);
     *f++ = times(square, M_P, M_T, M_A);
-    *f++ = poly(square, M_R);
+    *f++ = poly(square, M_R, plain);
     *f++ = times(square, M_R, M_P, M_T);
     *f++ = times(apply, M_T, M_T, 0);
     for (int last = 0; last < 2; ++last) {
@@ -679,12 +676,8 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
         Phase s2 = last ? phase_of(R_SQUARE, p, p, p, c.batch, passes, false, false, pairs) : square;
         const Phase ap = last ? phase_of(R_APPLY, c.m, c.n, p, c.batch, passes, false, wide, pairs) : apply;
         g = times(g, 0, 0, M_A);
-        s2 = poly(s2, M_P);
-        if (complete) {
-            g.of_unit = static_cast<float>(h * kNsScale);
-            s2.add = -1;
-            s2.of_unit = static_cast<float>((c.a - square_of) * kNsScale);
-        }
+        g.of_unit = complete.shift * kNsScale;
+        s2 = poly(s2, M_P, complete);
         *f++ = g;
         *f++ = s2;
         *f++ = times(ap, M_P, M_P, 0);

@@ -1,0 +1,371 @@
+// The whole orthogonalised update of matrices with a side of at most 128, a cluster of CTAs a matrix and
+// one launch: no product leaves the SMs. X lies with its short side as rows (128 of them, zeros past the
+// end), 64 or 128 of its columns in each CTA's shared memory, in two fp16 parts and in the layout that the
+// tensor core reads, both along k (for A = X X^T) and across it (for P X). Per step:
+//   each CTA's part of A over its columns, in fp32, to its shared memory;
+//   each CTA adds some of the 2048 runs of 8 of A over the CTAs, in their order, and writes them to all
+//     of them (distributed shared memory);
+//   each CTA forms P, the same everywhere, and its columns of P X, which take X's place.
+// Two barriers of the cluster a step, some 8 us in all, where a barrier of the grid and a trip through
+// L2 after each of the three products come to 28.
+#include <atomic>
+
+#include "epilogue.cuh"
+#include "mhc_internal.h"
+#include "orthogonal.h"
+#include "pair_mma.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr int kP = 128;                             // rows of X, sides of A and P
+constexpr int kThreads = 256;
+constexpr int kBox = kP * 128;                      // 128 rows of 64 columns of 16 bits
+constexpr int kPitch = kP + 4;                      // floats of a row of the sums
+constexpr int kMost = 16;                           // CTAs of a cluster
+// X hi, lo (two boxes each), A and then P hi, lo, sums
+constexpr int kXAt = 0, kMAt = 4 * kBox, kSumsAt = 8 * kBox, kSmallBars = kSumsAt + kP * kPitch * 4;
+constexpr int kSmem = kSmallBars + 256 + 1024;
+
+enum SmallSite : int { SITE_S_MMA = 130 };
+
+struct SmallArgs {
+    const void *g;
+    int dtype, tall;
+    long long row_stride, batch_stride;
+    int p, q, width, ctas, steps, last_passes;
+    float eps, of_sum, of_square, of_a, shift, of_unit;     // of_a: what is added of A; shift: what A has on its diagonal
+    void *out;
+    int out_dtype;
+    unsigned int *status;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ uint4 load16_at_rank(uint32_t addr, uint32_t rank) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(map_to_rank(addr, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store16_at_rank(uint32_t addr, uint32_t rank, const uint4 &v) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(map_to_rank(addr, rank)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Where run c (8 columns) of a row lies in a matrix of boxes of 64 columns in the 128-byte swizzle.
+__device__ __forceinline__ uint32_t run_at_box(int row, int c) {
+    return (c >> 3) * kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+// 8 values as hi (cut, or with `one` rounded, and then all there is) and lo.
+__device__ __forceinline__ void two_parts(const float (&v)[8], bool one, uint4 *hi, uint4 *lo) {
+    const __half *const tag = nullptr;
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint64_t r = f2_pack(v[2 * q], v[2 * q + 1]), h = one ? r : r & 0xFFFFE000FFFFE000ull;
+        hw[q] = pack2(h, tag);
+        lw[q] = pack2(fma2(h, splat2(-1.f), r), tag);
+    }
+    *hi = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    *lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+}
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// The columns' descriptor, the next 64 columns a box of 128 rows further on.
+__device__ __forceinline__ uint64_t desc_across(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(kBox >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_constant__ SmallArgs a) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    uint8_t *const basep = raw + (base - smem_addr(raw));
+    float *const sums = reinterpret_cast<float *>(basep + kSumsAt);
+    const uint32_t bar = base + kSmallBars;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + kSmallBars + 16);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    double *const squares = reinterpret_cast<double *>(basep + kSmallBars + 32);      // [0]: of the CTA; then of the warps
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % a.ctas, batch = blockIdx.x / a.ctas, j0 = rank * a.width;
+    const int live = min(a.width, a.q - j0);        // of the CTA's columns; not above 0 in a last CTA
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+
+    // ------------------------------------------------ X's columns, in fp32 to the sums' place, and their squares
+    {
+        const long long at = batch * a.batch_stride;
+        float f = 0.f;
+        // the axis that is contiguous in memory across the lanes
+        const int inner = a.tall ? kP : a.width, count = kP * a.width;
+#pragma unroll 8
+        for (int e = threadIdx.x; e < count; e += kThreads) {
+            const int o = e / inner, c = e - o * inner, i = a.tall ? c : o, j = a.tall ? o : c;
+            float v = 0.f;
+            if (i < a.p && j < live)
+                v = load_any(a.g, a.dtype, at + (a.tall ? (j0 + j) * a.row_stride + i : i * a.row_stride + j0 + j));
+            sums[i * kPitch + j] = v;
+            f = fmaf(v, v, f);
+        }
+        double s = f;
+        if (!(f < 1e30f && f > 1e-30f)) {           // out of fp32's range, or of its accurate part
+            s = 0.;
+            for (int e = threadIdx.x; e < count; e += kThreads) {
+                const int o = e / inner, c = e - o * inner;
+                const double v = sums[(a.tall ? c : o) * kPitch + (a.tall ? o : c)];
+                s += v * v;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) squares[1 + warp] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            s = 0.;
+            for (int w = 0; w < kThreads / 32; ++w) s += squares[1 + w];
+            squares[0] = s;
+        }
+        __syncthreads();
+        cluster_sync();
+        s = 0.;
+        for (int r = 0; r < a.ctas; ++r) {
+            double v;
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_rank(smem_addr(squares), r)) : "memory");
+            s += v;
+        }
+        const double norm = sqrt(s) + static_cast<double>(a.eps);
+        // by a power of two first where fp32 does not hold the factor; a matrix of zeros, with no eps, stays one
+        const float first = norm > 0x1p100 ? 0x1p-100f : norm < 0x1p-100 ? 0x1p100f : 1.f;
+        const float second = norm == 0. ? 0.f : static_cast<float>(kNsScale / (norm * first));
+        for (int u = threadIdx.x; u < kP * (a.width / 8); u += kThreads) {
+            const int i = u & (kP - 1), c = u / kP;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = sums[i * kPitch + 8 * c + e] * first * second;
+            uint4 h, l;
+            two_parts(v, a.steps == 1 && a.last_passes == 1, &h, &l);
+            st_shared_v4(base + kXAt + run_at_box(i, c), h);
+            st_shared_v4(base + kXAt + 2 * kBox + run_at_box(i, c), l);
+        }
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+
+    const uint32_t x = base + kXAt, m = base + kMAt;
+    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(kP >> 4) << 24);
+    const uint32_t square = idesc | (static_cast<uint32_t>(kP >> 3) << 17), across = idesc | (1u << 16) | (static_cast<uint32_t>(a.width >> 3) << 17);
+    uint32_t turns = 0;
+    // hi hi, hi lo and lo hi, one after another into the same sums; B along k, or across it
+    auto multiply = [&](uint32_t acc, uint32_t left, uint32_t right, int k, int passes, bool along) {
+        if (warp == 0 && elect_one()) {
+            tc_fence_after();
+            for (int part = 0; part < passes; ++part) {
+                const uint32_t l = left + (part == 2 ? 2 * kBox : 0), r = right + (part == 1 ? 2 * kBox : 0);
+                for (int q = 0; q < k; q += 16) {
+                    const uint32_t inside = (q >> 6) * kBox + (q & 63) * 2;
+                    tc_mma_bf16(acc, desc_rows(l + inside), along ? desc_rows(r + inside) : desc_across(r + q * 128), along ? square : across,
+                                part > 0 || q > 0);
+                }
+            }
+            tc_commit(bar);
+        }
+        __syncwarp();
+        // on a wait that ran out the rest goes on without its values, so that every barrier is met
+        mbar_wait(bar, turns++ & 1, abort_flag, a.timeout_ns, a.status, SITE_S_MMA);
+        __syncwarp();
+        tc_fence_after();
+    };
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    // the warp's half of the columns of sums, eight at a time
+    auto each8 = [&](uint32_t acc, int width, auto &&f) {
+#pragma unroll 1
+        for (int c = half * (width / 2); c < (half + 1) * (width / 2); c += 8) {
+            uint32_t u[8];
+            tmem_ld8_now(acc + c + lanes, u);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[e]);
+            f(c, v);
+        }
+        tc_fence_before();
+    };
+
+    for (int step = 0; step < a.steps; ++step) {
+        const bool last = step + 1 == a.steps, one = last && a.last_passes == 1, next_one = step + 2 == a.steps && a.last_passes == 1;
+        const int passes = one ? 1 : 3;
+        // A, over this CTA's columns
+        multiply(tmem, x, x, a.width, passes, true);
+        each8(tmem, kP, [&](int c, float (&v)[8]) {
+            float *const to = sums + row * kPitch + c;
+            *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        });
+        __syncthreads();
+        cluster_sync();
+        // over all columns: run u of the 128 x 16 by the CTA u % ctas, to every CTA
+        for (int u = rank + a.ctas * threadIdx.x; u < kP * (kP / 8); u += a.ctas * kThreads) {
+            const int i = u >> 4, c = u & 15;
+            const uint32_t from = base + kSumsAt + (i * kPitch + 8 * c) * 4;
+            float v[8] = {};
+            for (int r0 = 0; r0 < a.ctas; r0 += 4) {
+                uint4 w[4][2];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        w[r][h] = r0 + r < a.ctas ? load16_at_rank(from + 16 * h, r0 + r) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        v[4 * h] += __uint_as_float(w[r][h].x);
+                        v[4 * h + 1] += __uint_as_float(w[r][h].y);
+                        v[4 * h + 2] += __uint_as_float(w[r][h].z);
+                        v[4 * h + 3] += __uint_as_float(w[r][h].w);
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * a.of_sum + (i == 8 * c + e ? a.shift : 0.f);
+            uint4 h, l;
+            two_parts(v, one, &h, &l);
+            const uint32_t to = m + run_at_box(i, c);
+            for (int r = 0; r < a.ctas; ++r) {
+                store16_at_rank(to, r, h);
+                if (!one) store16_at_rank(to + 2 * kBox, r, l);
+            }
+        }
+        fence_proxy_async_all();        // the tensor cores of other CTAs read what this one wrote
+        __syncthreads();
+        cluster_sync();
+        fence_proxy_async_all();
+        __syncthreads();
+        // P, in A's place
+        multiply(tmem + kP, m, m, kP, passes, true);
+        each8(tmem + kP, kP, [&](int c, float (&v)[8]) {
+            const uint32_t to = m + run_at_box(row, c >> 3);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * a.of_square + (row == c + e ? a.of_unit : 0.f);
+            if (a.of_a != 0.f) {
+                const __half *const tag = nullptr;
+                const uint4 h = ld_shared_v4(to), l = one ? make_uint4(0u, 0u, 0u, 0u) : ld_shared_v4(to + 2 * kBox);
+                const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t s = add2(unpack2(hw[q], tag), unpack2(lw[q], tag));
+                    v[2 * q] = fmaf(a.of_a, f2_lo(s), v[2 * q]);
+                    v[2 * q + 1] = fmaf(a.of_a, f2_hi(s), v[2 * q + 1]);
+                }
+            }
+            uint4 h, l;
+            two_parts(v, one, &h, &l);
+            st_shared_v4(to, h);
+            if (!one) st_shared_v4(to + 2 * kBox, l);
+        });
+        fence_proxy_async_smem();
+        __syncthreads();
+        // P X, in X's place
+        multiply(tmem + 2 * kP, m, x, kP, passes, false);
+        if (last) break;
+        each8(tmem + 2 * kP, a.width, [&](int c, float (&v)[8]) {
+            const uint32_t to = x + run_at_box(row, c >> 3);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= a.of_sum;
+            uint4 h, l;
+            two_parts(v, next_one, &h, &l);
+            st_shared_v4(to, h);
+            if (!next_one) st_shared_v4(to + 2 * kBox, l);
+        });
+        fence_proxy_async_smem();
+        __syncthreads();
+    }
+    // ------------------------------------------------ the output, through the sums' place
+    const float of_out = a.of_sum * a.of_sum;
+    each8(tmem + 2 * kP, a.width, [&](int c, float (&v)[8]) {
+        float *const to = sums + row * kPitch + c;
+        *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    });
+    __syncthreads();
+    const long long out_at = static_cast<long long>(batch) * a.p * a.q;
+    const int inner = a.tall ? kP : a.width;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < kP * a.width; e += kThreads) {
+        const int o = e / inner, c = e - o * inner, i = a.tall ? c : o, j = a.tall ? o : c;
+        if (i < a.p && j < live)
+            store_any(a.out, a.out_dtype, out_at + (a.tall ? static_cast<long long>(j0 + j) * a.p + i : static_cast<long long>(i) * a.q + j0 + j),
+                      sums[i * kPitch + j] * of_out);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();         // nothing of this CTA is read or written any more
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// 1: may be launched with clusters of up to 16; asked once a device.
+std::atomic<int> g_ready[64];
+
+}  // namespace
+
+bool ns_small_fits(int m, int n) { return (m < n ? m : n) <= kP && (m < n ? n : m) <= kP * kMost; }
+
+int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int *status, bool pdl, cudaStream_t s) {
+    SmallArgs a = {};
+    a.g = o.g;
+    a.dtype = o.dtype;
+    a.tall = o.m > o.n;
+    a.row_stride = o.row_stride;
+    a.batch_stride = o.batch_stride;
+    a.p = a.tall ? o.n : o.m;
+    a.q = a.tall ? o.m : o.n;
+    a.width = a.q <= 8 * 64 ? 64 : 128;
+    a.ctas = (a.q + a.width - 1) / a.width;
+    a.steps = o.steps;
+    a.last_passes = o.out_dtype == MHC_BF16 ? 1 : 3;
+    a.eps = o.eps;
+    a.of_sum = 1.f / kNsScale;
+    a.of_square = f.of_square / kNsScale;
+    a.of_a = f.of_a;
+    a.shift = f.shift * kNsScale;
+    a.of_unit = f.of_unit * kNsScale;
+    a.out = o.out;
+    a.out_dtype = o.out_dtype;
+    a.status = status;
+    a.timeout_ns = wait_timeout_ns();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
+    if (!g_ready[dev & 63].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return MHC_ERR_CUDA;
+        g_ready[dev & 63].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(o.batch) * a.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    return note_launch(cudaLaunchKernelEx(&cfg, ns_small_kernel, a));
+}
+
+}  // namespace mhc

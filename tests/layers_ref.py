@@ -141,14 +141,17 @@ def orthogonalize(g, steps, coeffs, eps, noise=None):
 def orthogonalize_error(g, steps, coeffs, eps, out_type):
     """The result and how far a run on the tensor cores may be from it. Each product is off by 2^-21 of
     the sizes of its terms (two fp16 parts hold 22 bits, what is left out of the product of two
-    pairs is of that size too) and by what the additions cut; what the last step of a bf16 result reads is rounded to
+    pairs is of that size too) and by what the additions cut: each of the 12 instructions for 64 of the summed axis
+    leaves out between 0 and 2^-23 of the sum, which adds up to 2^-24 of it for each, towards zero, and varies by the root of
+    their number; what the last step of a bf16 result reads is rounded to
     fp16, 2^-11 of itself, which on the diagonal A has b / 2c beside it; all of random sign, carried through
     the steps in 64 bits, three times. What comes out is a sum of many independent terms: the largest of N such values lies
     near sqrt(2 ln N) root mean squares (5.5 for three million, where four were not enough), and one
     more makes it rare; or four times an element's own largest sample; and the rounding at the end."""
     want = orthogonalize(g, steps, coeffs, eps)
     k = max(g.shape[-2:])
-    size = 2.0 ** -21 + 2.0 ** -23 * math.sqrt(12 * min(-(-k // 64), 64))
+    n = 12 * -(-k // 64)
+    size, drift = 2.0 ** -21 + 2.0 ** -23 * math.sqrt(n), n * 2.0 ** -24
     shift = abs(coeffs[1] / (2 * coeffs[2])) if coeffs[2] else 0.0
     worst = torch.zeros_like(want)
     for seed in range(3):
@@ -162,7 +165,7 @@ def orthogonalize_error(g, steps, coeffs, eps, out_type):
                 if v.shape[-1] == v.shape[-2]:
                     held = held + shift * torch.eye(v.shape[-1], dtype=v.dtype, device=v.device)
                 tol = tol + held * 2.0 ** -11
-            return s * tol
+            return s * tol - drift * v
         worst = torch.maximum(worst, (orthogonalize(g, steps, coeffs, eps, noise) - want).abs())
     # worst is the largest of three samples: its root mean square is above one sample's
     floor = worst.square().mean((-2, -1), keepdim=True).sqrt()

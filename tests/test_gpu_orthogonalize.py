@@ -31,7 +31,8 @@ def near(got, want, e):
 
 
 SHAPES = [(1, 1), (1, 70), (70, 1), (5, 3), (64, 64), (65, 130), (130, 65), (200, 72), (128, 500), (300, 300), (257, 600), (513, 260),
-          (3, 40, 72), (6, 128, 500), (2, 260, 129), (17, 8, 8)]
+          (3, 40, 72), (6, 128, 500), (2, 260, 129), (17, 8, 8), (512, 128), (128, 513),
+          (100, 1024), (1025, 127), (33, 2048), (2049, 128), (129, 129), (200, 16, 96), (40, 300, 100)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
