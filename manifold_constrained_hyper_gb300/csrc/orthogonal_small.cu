@@ -3,8 +3,8 @@
 // end), 64 or 128 of its columns in each CTA's shared memory, in two fp16 parts and in the layout that the
 // tensor core reads, both along k (for A = X X^T) and across it (for P X). Per step:
 //   each CTA's part of A over its columns, in fp32, to its shared memory;
-//   each CTA adds some of the 2048 runs of 8 of A over the CTAs, in their order, and writes them to all
-//     of them (distributed shared memory);
+//   each CTA adds some rows of A over the CTAs, in their order, and writes them to all of them
+//     (distributed shared memory, a row a warp: whole lines; 16 bytes here and there took eight times as long);
 //   each CTA forms P, the same everywhere, and its columns of P X, which take X's place.
 // Two barriers of the cluster a step, some 8 us in all, where a barrier of the grid and a trip through
 // L2 after each of the three products come to 28.
@@ -47,26 +47,25 @@ __device__ __forceinline__ uint4 load16_at_rank(uint32_t addr, uint32_t rank) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(map_to_rank(addr, rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ void store16_at_rank(uint32_t addr, uint32_t rank, const uint4 &v) {
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
-                 ::"r"(map_to_rank(addr, rank)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+__device__ __forceinline__ void store8_at_rank(uint32_t addr, uint32_t rank, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(map_to_rank(addr, rank)), "r"(x), "r"(y) : "memory");
 }
 // Where run c (8 columns) of a row lies in a matrix of boxes of 64 columns in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t run_at_box(int row, int c) {
     return (c >> 3) * kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
-// 8 values as hi (cut, or with `one` rounded, and then all there is) and lo.
-__device__ __forceinline__ void two_parts(const float (&v)[8], bool one, uint4 *hi, uint4 *lo) {
+// Two values as hi (cut, or with `one` rounded, and then all there is) and lo.
+__device__ __forceinline__ void two_parts(float v0, float v1, bool one, uint32_t *hi, uint32_t *lo) {
     const __half *const tag = nullptr;
-    uint32_t hw[4], lw[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint64_t r = f2_pack(v[2 * q], v[2 * q + 1]), h = one ? r : r & 0xFFFFE000FFFFE000ull;
-        hw[q] = pack2(h, tag);
-        lw[q] = pack2(fma2(h, splat2(-1.f), r), tag);
-    }
-    *hi = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-    *lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+    const uint64_t r = f2_pack(v0, v1), h = one ? r : r & 0xFFFFE000FFFFE000ull;
+    *hi = pack2(h, tag);
+    *lo = pack2(fma2(h, splat2(-1.f), r), tag);
+}
+__device__ __forceinline__ void two_parts(const float (&v)[8], bool one, uint4 *hi, uint4 *lo) {
+    two_parts(v[0], v[1], one, &hi->x, &lo->x);
+    two_parts(v[2], v[3], one, &hi->y, &lo->y);
+    two_parts(v[4], v[5], one, &hi->z, &lo->z);
+    two_parts(v[6], v[7], one, &hi->w, &lo->w);
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 // The columns' descriptor, the next 64 columns a box of 128 rows further on.
@@ -107,28 +106,42 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     {
         const long long at = batch * a.batch_stride;
         float f = 0.f;
-        // the axis that is contiguous in memory across the lanes
-        const int inner = a.tall ? kP : a.width, count = kP * a.width;
-#pragma unroll 8
-        for (int e = threadIdx.x; e < count; e += kThreads) {
-            const int o = e / inner, c = e - o * inner, i = a.tall ? c : o, j = a.tall ? o : c;
-            float v = 0.f;
-            if (i < a.p && j < live)
-                v = load_any(a.g, a.dtype, at + (a.tall ? (j0 + j) * a.row_stride + i : i * a.row_stride + j0 + j));
-            sums[i * kPitch + j] = v;
-            f = fmaf(v, v, f);
-        }
-        double s = f;
-        if (!(f < 1e30f && f > 1e-30f)) {           // out of fp32's range, or of its accurate part
+        // the axis that is contiguous in memory across the lanes, 16 loads of each on their way at once
+        const int shift = a.tall || a.width == kP ? 7 : 6, mask = (1 << shift) - 1, count = kP * a.width;
+        with_type(a.dtype, [&](auto tag) {
+            const auto *const g = static_cast<decltype(tag)>(a.g) + at;
+#pragma unroll 1
+            for (int e0 = threadIdx.x; e0 < count; e0 += 16 * kThreads) {
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int e = e0 + k * kThreads, o = e >> shift, c = e & mask, i = a.tall ? c : o, j = a.tall ? o : c;
+                    v[k] = 0.f;
+                    if (i < a.p && j < live) v[k] = to_f32(g[a.tall ? (j0 + j) * a.row_stride + i : i * a.row_stride + j0 + j]);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int e = e0 + k * kThreads, o = e >> shift, c = e & mask;
+                    sums[(a.tall ? c : o) * kPitch + (a.tall ? o : c)] = v[k];
+                    f = fmaf(v[k], v[k], f);
+                }
+            }
+        });
+        // the warp's in fp32, unless that leaves its range, or its accurate part: then all again in double
+        float all = f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        double s = all;
+        if (!(all < 1e30f && all > 1e-30f)) {
             s = 0.;
             for (int e = threadIdx.x; e < count; e += kThreads) {
-                const int o = e / inner, c = e - o * inner;
+                const int o = e >> shift, c = e & mask;
                 const double v = sums[(a.tall ? c : o) * kPitch + (a.tall ? o : c)];
                 s += v * v;
             }
-        }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        }
         if (lane == 0) squares[1 + warp] = s;
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -138,21 +151,29 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
         }
         __syncthreads();
         cluster_sync();
-        s = 0.;
-        for (int r = 0; r < a.ctas; ++r) {
-            double v;
-            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_rank(smem_addr(squares), r)) : "memory");
-            s += v;
+        // one thread finds the factor: double precision is slow here
+        float *const factor = reinterpret_cast<float *>(squares + 10);
+        if (warp == 0) {
+            s = 0.;
+            if (lane < a.ctas)
+                asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(s) : "r"(map_to_rank(smem_addr(squares), lane)) : "memory");
+#pragma unroll
+            for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0) {
+                const double norm = sqrt(s) + static_cast<double>(a.eps);
+                // by a power of two first where fp32 does not hold the factor; a matrix of zeros, with no eps, stays one
+                factor[0] = norm > 0x1p100 ? 0x1p-100f : norm < 0x1p-100 ? 0x1p100f : 1.f;
+                factor[1] = norm == 0. ? 0.f : static_cast<float>(kNsScale / (norm * factor[0]));
+            }
         }
-        const double norm = sqrt(s) + static_cast<double>(a.eps);
-        // by a power of two first where fp32 does not hold the factor; a matrix of zeros, with no eps, stays one
-        const float first = norm > 0x1p100 ? 0x1p-100f : norm < 0x1p-100 ? 0x1p100f : 1.f;
-        const float second = norm == 0. ? 0.f : static_cast<float>(kNsScale / (norm * first));
+        __syncthreads();
+        const float first = factor[0], second = factor[1];
         for (int u = threadIdx.x; u < kP * (a.width / 8); u += kThreads) {
             const int i = u & (kP - 1), c = u / kP;
-            float v[8];
+            const float4 lo4 = *reinterpret_cast<const float4 *>(sums + i * kPitch + 8 * c), hi4 = *reinterpret_cast<const float4 *>(sums + i * kPitch + 8 * c + 4);
+            float v[8] = {lo4.x, lo4.y, lo4.z, lo4.w, hi4.x, hi4.y, hi4.z, hi4.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = sums[i * kPitch + 8 * c + e] * first * second;
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * first * second;
             uint4 h, l;
             two_parts(v, a.steps == 1 && a.last_passes == 1, &h, &l);
             st_shared_v4(base + kXAt + run_at_box(i, c), h);
@@ -214,36 +235,44 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
         });
         __syncthreads();
         cluster_sync();
-        // over all columns: run u of the 128 x 16 by the CTA u % ctas, to every CTA
-        for (int u = rank + a.ctas * threadIdx.x; u < kP * (kP / 8); u += a.ctas * kThreads) {
-            const int i = u >> 4, c = u & 15;
-            const uint32_t from = base + kSumsAt + (i * kPitch + 8 * c) * 4;
-            float v[8] = {};
-            for (int r0 = 0; r0 < a.ctas; r0 += 4) {
-                uint4 w[4][2];
+        // over all columns: every ctas-th row from this CTA's on, a warp a row, four columns a lane, to every CTA
+        // (two rows of a warp at a time)
+        const int next_row = a.ctas * (kThreads / 32);
+        for (int i0 = rank + a.ctas * warp; i0 < kP; i0 += 2 * next_row) {
+            float v[2][4] = {};
+            for (int r0 = 0; r0 < a.ctas; r0 += 8) {
+                uint4 w[2][8];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        w[r][h] = r0 + r < a.ctas ? load16_at_rank(from + 16 * h, r0 + r) : make_uint4(0u, 0u, 0u, 0u);
+                    for (int r = 0; r < 8; ++r)
+                        w[k][r] = r0 + r < a.ctas && i0 + k * next_row < kP
+                                      ? load16_at_rank(base + kSumsAt + ((i0 + k * next_row) * kPitch + 4 * lane) * 4, r0 + r)
+                                      : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        v[4 * h] += __uint_as_float(w[r][h].x);
-                        v[4 * h + 1] += __uint_as_float(w[r][h].y);
-                        v[4 * h + 2] += __uint_as_float(w[r][h].z);
-                        v[4 * h + 3] += __uint_as_float(w[r][h].w);
+                    for (int r = 0; r < 8; ++r) {
+                        v[k][0] += __uint_as_float(w[k][r].x);
+                        v[k][1] += __uint_as_float(w[k][r].y);
+                        v[k][2] += __uint_as_float(w[k][r].z);
+                        v[k][3] += __uint_as_float(w[k][r].w);
                     }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * a.of_sum + (i == 8 * c + e ? a.shift : 0.f);
-            uint4 h, l;
-            two_parts(v, one, &h, &l);
-            const uint32_t to = m + run_at_box(i, c);
-            for (int r = 0; r < a.ctas; ++r) {
-                store16_at_rank(to, r, h);
-                if (!one) store16_at_rank(to + 2 * kBox, r, l);
+            for (int k = 0; k < 2; ++k) {
+                const int i = i0 + k * next_row;
+                if (i >= kP) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[k][e] = v[k][e] * a.of_sum + (i == 4 * lane + e ? a.shift : 0.f);
+                uint32_t h[2], l[2];
+                two_parts(v[k][0], v[k][1], one, &h[0], &l[0]);
+                two_parts(v[k][2], v[k][3], one, &h[1], &l[1]);
+                const uint32_t to = m + run_at_box(i, lane >> 1) + (lane & 1) * 8;
+                for (int r = 0; r < a.ctas; ++r) {
+                    store8_at_rank(to, r, h[0], h[1]);
+                    if (!one) store8_at_rank(to + 2 * kBox, r, l[0], l[1]);
+                }
             }
         }
         fence_proxy_async_all();        // the tensor cores of other CTAs read what this one wrote
@@ -299,14 +328,18 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     });
     __syncthreads();
     const long long out_at = static_cast<long long>(batch) * a.p * a.q;
-    const int inner = a.tall ? kP : a.width;
-#pragma unroll 4
-    for (int e = threadIdx.x; e < kP * a.width; e += kThreads) {
-        const int o = e / inner, c = e - o * inner, i = a.tall ? c : o, j = a.tall ? o : c;
-        if (i < a.p && j < live)
-            store_any(a.out, a.out_dtype, out_at + (a.tall ? static_cast<long long>(j0 + j) * a.p + i : static_cast<long long>(i) * a.q + j0 + j),
-                      sums[i * kPitch + j] * of_out);
-    }
+    const int shift = a.tall || a.width == kP ? 7 : 6, mask = (1 << shift) - 1;
+    with_type(a.out_dtype, [&](auto tag) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
+        T *const out = static_cast<T *>(a.out) + out_at;
+#pragma unroll 8
+        for (int e = threadIdx.x; e < kP * a.width; e += kThreads) {
+            const int o = e >> shift, c = e & mask, i = a.tall ? c : o, j = a.tall ? o : c;
+            if (i < a.p && j < live)
+                out[a.tall ? static_cast<long long>(j0 + j) * a.p + i : static_cast<long long>(i) * a.q + j0 + j] =
+                    from_f32<T>(sums[i * kPitch + j] * of_out);
+        }
+    });
     tc_fence_before();
     __syncthreads();
     cluster_sync();         // nothing of this CTA is read or written any more
