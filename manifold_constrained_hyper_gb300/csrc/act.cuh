@@ -20,6 +20,22 @@ __device__ __forceinline__ void sigmoid_pair(float z, float *s, float *t) {
 // gelu's tanh form is z * sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3): no cancellation far below zero.
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.07135481627260025f;   // 2 sqrt(2/pi), and 0.044715 of it
 
+// What the normal distribution has beyond |z|, E = exp(-z^2 / 2) given: erfc(|z| / sqrt 2) / 2 = E t P(t) with t = 1 / (1 +
+// 0.4 |z| / sqrt 2). P fits exp(x^2) erfc(x) / t to 1.3e-7 of itself for all x >= 0 (least squares on 6000 Chebyshev points, weighted
+// until the largest relative errors are level); 5e-7 in fp32. Some 15 instructions, a third of erfcf's.
+__device__ __forceinline__ float normal_tail(float z, float E) {
+    const float t = __fdividef(1.f, fmaf(0.28284271247461903f, fabsf(z), 1.f));
+    float p = 0.05025513097643852f * 0.5f;
+    p = fmaf(p, t, -0.18287666141986847f * 0.5f);
+    p = fmaf(p, t, 0.16905011236667633f * 0.5f);
+    p = fmaf(p, t, -0.005581708624958992f * 0.5f);
+    p = fmaf(p, t, 0.1414211392402649f * 0.5f);
+    p = fmaf(p, t, 0.16854415833950043f * 0.5f);
+    p = fmaf(p, t, 0.20784246921539307f * 0.5f);
+    p = fmaf(p, t, 0.22566960752010345f * 0.5f);
+    p = fmaf(p, t, 0.22567586600780487f * 0.5f);
+    return p * t * E;
+}
 // act(z). The approximate exponential is off by 2 + |z| * 1.2 ulp, which the exact one is not; every
 // output is of 16 bits, or has z's own rounding of an fp32 sum beside it.
 template <int ACT>
@@ -27,7 +43,10 @@ __device__ __forceinline__ float act_value(float z) {
     if (ACT == MHC_LINEAR_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
     if (ACT == MHC_LINEAR_RELU2) return z > 0.f ? z * z : (z != z ? z : 0.f);
     if (ACT == MHC_LINEAR_SILU) return z * sigmoid_of(z);
-    if (ACT == MHC_LINEAR_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    if (ACT == MHC_LINEAR_GELU) {
+        const float q = normal_tail(z, __expf(-0.5f * z * z));
+        return z * (z < 0.f ? q : 1.f - q);
+    }
     if (ACT == MHC_LINEAR_GELU_TANH) return z * sigmoid_of(z * fmaf(kGeluB, z * z, kGeluA));
     return z;
 }
@@ -41,8 +60,11 @@ __device__ __forceinline__ float act_slope(float z) {
         sigmoid_pair(z, &s, &t);
         return fmaf(z * s, t, s);
     }
-    if (ACT == MHC_LINEAR_GELU)
-        return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), 0.5f * erfcf(-0.70710678118654752f * z));
+    if (ACT == MHC_LINEAR_GELU) {
+        // far out, where the slope is 0 or 1, z times 0 stays finite
+        const float E = __expf(-0.5f * z * z), q = normal_tail(z, E);
+        return fmaf(z * 0.39894228040143268f, E, z < 0.f ? q : 1.f - q);
+    }
     if (ACT == MHC_LINEAR_GELU_TANH) {
         // far out, where the slope is 0 or 1, the square stays finite
         const float q = fminf(z * z, 1e8f);

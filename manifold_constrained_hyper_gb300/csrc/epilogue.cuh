@@ -24,56 +24,92 @@ __device__ __forceinline__ void with_type(int dtype, F &&f) {
     else f(static_cast<const __half *>(nullptr));
 }
 
-// A piece of 32 x 32 sums, as the 32 lanes of a warp hold it: `wide`, a row a lane, 32 columns, of which
-// `n` (a multiple of 8) are in the matrix; else turned, a column a lane, 32 rows, of which `n` are in
-// it (none of a lane past the last column). at: the first element's index, of a matrix whose rows are
-// `pitch` apart.
+// A piece of 32 x 32 sums, as the 32 lanes of a warp hold it: `wide`, a row a lane, 32 columns, where `rows` and `columns` (a
+// multiple of 8) of it are in the matrix; else turned, a column a lane, 32 rows, of which the lane's column has `rows` in the
+// matrix (none past the last column). `row0`: the index of the piece's first element, or, turned, of the lane's first,
+// in a matrix whose rows are `pitch` apart. Between memory and a row a lane, wide pieces go through the warp's 4 KB
+// of shared memory, `buf`, so that an access of the warp touches whole rows and not 32 lines.
 struct Piece {
     bool wide;
-    int n;
+    int rows, columns;
 };
 // The compiler would keep the 32 rows' distances in registers from the kernel's start on.
 __device__ __forceinline__ long long here(long long pitch) {
     asm volatile("" : "+l"(pitch));
     return pitch;
 }
-// What it is combined with, as it lies in memory: on its way while the products go on, or while the
-// piece before is stored.
+// Where the 16 bytes `c` of a row lie in buf: 8 of them a row (fp32), or 4, so that neither lanes with a row each nor lanes
+// along rows meet on a bank.
+template <int PER_ROW>
+__device__ __forceinline__ uint32_t buf_at(int row, int c) {
+    return PER_ROW == 8 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+}
+// What a piece is combined with, as it lies in memory: on its way while the products go on.
 struct Raw {
     uint32_t w[32];
 };
-__device__ __forceinline__ void load_raw(Raw &r, const Piece &p, const void *from, int dtype, long long at, long long pitch) {
+template <int PER_ROW>
+__device__ __forceinline__ void load_rows(Raw &r, const Piece &p, const uint8_t *from, long long pitch_bytes) {
+    const int lane = threadIdx.x & 31, c = lane % PER_ROW;
+    constexpr int kRowsAtOnce = 32 / PER_ROW, kSize = PER_ROW == 8 ? 4 : 2;
+    const long long step = here(pitch_bytes * kRowsAtOnce);
+    const uint8_t *q = from + lane / PER_ROW * pitch_bytes + 16 * c;
+#pragma unroll
+    for (int k = 0; k < PER_ROW; ++k, q += step)
+        if (lane / PER_ROW + k * kRowsAtOnce < p.rows && c * 16 < p.columns * kSize) {
+            const uint4 t = *reinterpret_cast<const uint4 *>(q);
+            r.w[4 * k] = t.x, r.w[4 * k + 1] = t.y, r.w[4 * k + 2] = t.z, r.w[4 * k + 3] = t.w;
+        }
+}
+// runs: the source's rows lie on the boundaries of runs of 8; others are read a row a lane, by the words that hold them.
+__device__ __forceinline__ void load_raw(Raw &r, const Piece &p, const void *from, int dtype, long long row0, long long pitch, bool runs) {
+    const int size = dtype == MHC_F32 ? 4 : 2, lane = threadIdx.x & 31;
     if (p.wide) {
-        if (dtype == MHC_F32) {
-            const uint4 *const q = reinterpret_cast<const uint4 *>(static_cast<const float *>(from) + at);
+        const uint8_t *const first = static_cast<const uint8_t *>(from) + row0 * size;
+        if (runs) {
+            if (size == 4) load_rows<8>(r, p, first, pitch * 4);
+            else load_rows<4>(r, p, first, pitch * 2);
+            return;
+        }
+        if (lane >= p.rows) return;
+        const uintptr_t addr = reinterpret_cast<uintptr_t>(first) + lane * pitch * size, end = addr + static_cast<uintptr_t>(p.columns) * size;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (4 * c < p.n) {
-                    const uint4 t = q[c];
-                    r.w[4 * c] = t.x, r.w[4 * c + 1] = t.y, r.w[4 * c + 2] = t.z, r.w[4 * c + 3] = t.w;
-                }
-        } else {
-            const uint4 *const q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(from) + at);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (8 * c < p.n) {
-                    const uint4 t = q[c];
-                    r.w[4 * c] = t.x, r.w[4 * c + 1] = t.y, r.w[4 * c + 2] = t.z, r.w[4 * c + 3] = t.w;
-                }
+        for (int c = 0; c < 16; c += 2) {
+            if (8 * c >= 32 * size || 8 * c >= p.columns * size) break;
+            uint64_t v[2];
+            load_words<2>(addr + 8 * c, end, v);
+            r.w[2 * c] = static_cast<uint32_t>(v[0]), r.w[2 * c + 1] = static_cast<uint32_t>(v[0] >> 32);
+            r.w[2 * c + 2] = static_cast<uint32_t>(v[1]), r.w[2 * c + 3] = static_cast<uint32_t>(v[1] >> 32);
         }
         return;
     }
-    pitch = here(pitch);
-    if (dtype == MHC_F32) {
-        const uint32_t *q = static_cast<const uint32_t *>(from) + at;
+    const long long step = here(pitch);
+    if (size == 4) {
+        const uint32_t *q = static_cast<const uint32_t *>(from) + row0;
 #pragma unroll
-        for (int c = 0; c < 32; ++c, q += pitch)
-            if (c < p.n) r.w[c] = *q;
+        for (int c = 0; c < 32; ++c, q += step)
+            if (c < p.rows) r.w[c] = *q;
     } else {
-        const uint16_t *q = static_cast<const uint16_t *>(from) + at;
+        const uint16_t *q = static_cast<const uint16_t *>(from) + row0;
 #pragma unroll
-        for (int c = 0; c < 32; ++c, q += pitch)
-            if (c < p.n) r.w[c] = *q;
+        for (int c = 0; c < 32; ++c, q += step)
+            if (c < p.rows) r.w[c] = *q;
+    }
+}
+// From whole rows to a row a lane.
+template <int PER_ROW>
+__device__ __forceinline__ void spread_rows(Raw &r, uint32_t buf) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < PER_ROW; ++k)
+        st_shared_v4(buf + buf_at<PER_ROW>(lane / PER_ROW + k * (32 / PER_ROW), lane % PER_ROW),
+                     make_uint4(r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]));
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < PER_ROW; ++k) {
+        const uint4 t = ld_shared_v4(buf + buf_at<PER_ROW>(lane, k));
+        r.w[4 * k] = t.x, r.w[4 * k + 1] = t.y, r.w[4 * k + 2] = t.z, r.w[4 * k + 3] = t.w;
     }
 }
 // Value e of it.
@@ -87,7 +123,11 @@ __device__ __forceinline__ float raw_at(const Raw &r, bool wide, int e, const __
 }
 // f(e, the value) for each of the 32.
 template <class F>
-__device__ __forceinline__ void each_raw(const Raw &r, bool wide, int dtype, F &&f) {
+__device__ __forceinline__ void each_raw(Raw &r, bool wide, int dtype, bool runs, uint32_t buf, F &&f) {
+    if (wide && runs) {
+        if (dtype == MHC_F32) spread_rows<8>(r, buf);
+        else spread_rows<4>(r, buf);
+    }
     with_type(dtype, [&](auto tag) {
         if (wide) {
 #pragma unroll
@@ -98,43 +138,63 @@ __device__ __forceinline__ void each_raw(const Raw &r, bool wide, int dtype, F &
         }
     });
 }
-__device__ __forceinline__ void store_piece(const Piece &p, void *to, int dtype, long long at, long long pitch, const float (&v)[32]) {
+// A row a lane, in words, to whole rows.
+template <int PER_ROW>
+__device__ __forceinline__ void store_rows(const Piece &p, uint8_t *to, long long pitch_bytes, const uint4 (&v)[PER_ROW], uint32_t buf) {
+    const int lane = threadIdx.x & 31, c = lane % PER_ROW;
+    constexpr int kRowsAtOnce = 32 / PER_ROW, kSize = PER_ROW == 8 ? 4 : 2;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < PER_ROW; ++k) st_shared_v4(buf + buf_at<PER_ROW>(lane, k), v[k]);
+    __syncwarp();
+    const long long step = here(pitch_bytes * kRowsAtOnce);
+    uint8_t *q = to + lane / PER_ROW * pitch_bytes + 16 * c;
+#pragma unroll
+    for (int k = 0; k < PER_ROW; ++k, q += step) {
+        const int row = lane / PER_ROW + k * kRowsAtOnce;
+        const uint4 t = ld_shared_v4(buf + buf_at<PER_ROW>(row, c));
+        if (row < p.rows && c * 16 < p.columns * kSize) *reinterpret_cast<uint4 *>(q) = t;
+    }
+}
+__device__ __forceinline__ void store_piece(const Piece &p, void *to, int dtype, long long row0, long long pitch, const float (&v)[32], uint32_t buf) {
     with_type(dtype, [&](auto tag) {
         using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
-        T *q = static_cast<T *>(to) + at;
+        T *q = static_cast<T *>(to) + row0;
         if (p.wide) {
+            constexpr int kPerRow = sizeof(T) == 4 ? 8 : 4;
+            uint4 w[kPerRow];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (8 * c >= p.n) break;
-                Run r;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) r.p[k] = f2_pack(v[8 * c + 2 * k], v[8 * c + 2 * k + 1]);
-                store8(q + 8 * c, r);
+            for (int c = 0; c < kPerRow; ++c) {
+                if constexpr (sizeof(T) == 4)
+                    w[c] = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+                else
+                    w[c] = make_uint4(pack2(f2_pack(v[8 * c], v[8 * c + 1]), q), pack2(f2_pack(v[8 * c + 2], v[8 * c + 3]), q),
+                                      pack2(f2_pack(v[8 * c + 4], v[8 * c + 5]), q), pack2(f2_pack(v[8 * c + 6], v[8 * c + 7]), q));
             }
+            store_rows<kPerRow>(p, reinterpret_cast<uint8_t *>(q), pitch * static_cast<long long>(sizeof(T)), w, buf);
         } else {
             const long long step = here(pitch);
 #pragma unroll
             for (int c = 0; c < 32; ++c, q += step)
-                if (c < p.n) *q = from_f32<T>(v[c]);
+                if (c < p.rows) *q = from_f32<T>(v[c]);
         }
     });
 }
-// What finish_piece combines a piece with: loaded ahead of it.
+// What finish_piece combines a piece with: loaded ahead of it. (i, j): the piece's first element, or the lane's.
 template <int KIND>
-__device__ __forceinline__ void load_extra(Raw &r, const Piece &p, const EpilogueArgs &e, long long i, int j, long long at, int n) {
+__device__ __forceinline__ void load_extra(Raw &r, const Piece &p, const EpilogueArgs &e, long long i, int j, long long row0, int n) {
     if constexpr (KIND == EPI_LINEAR) {
-        if (e.residual) load_raw(r, p, e.residual, e.residual_dtype, i * e.residual_stride + j, e.residual_stride);
+        if (e.residual) load_raw(r, p, e.residual, e.residual_dtype, i * e.residual_stride + j, e.residual_stride, e.extra_runs);
     } else if constexpr (KIND == EPI_SLOPE) {
-        load_raw(r, p, e.z, e.z_dtype, i * e.z_stride + j, e.z_stride);
+        load_raw(r, p, e.z, e.z_dtype, i * e.z_stride + j, e.z_stride, e.extra_runs);
     } else if constexpr (KIND == EPI_SUMS) {
-        if (e.accumulate) load_raw(r, p, e.out, e.out_dtype, at, n);
+        if (e.accumulate) load_raw(r, p, e.out, e.out_dtype, row0, n, true);
     }
 }
-// The epilogue of a piece whose first element is (i, j), `at` its index in a contiguous output of n
-// columns; bias: of column j + lane.
+// The epilogue of a piece, `row0` as above in a contiguous output of n columns; bias: of column j + lane.
 template <int KIND>
-__device__ __forceinline__ void finish_piece(const Piece &p, const EpilogueArgs &e, long long at, int n, float bias, float (&v)[32],
-                                             const Raw &r) {
+__device__ __forceinline__ void finish_piece(const Piece &p, const EpilogueArgs &e, long long row0, int n, float bias, float (&v)[32], Raw &r,
+                                             uint32_t buf) {
     if constexpr (KIND == EPI_LINEAR) {
         if (e.bias) {
             if (p.wide) {
@@ -145,24 +205,24 @@ __device__ __forceinline__ void finish_piece(const Piece &p, const EpilogueArgs 
                 for (int q = 0; q < 32; ++q) v[q] += bias;
             }
         }
-        if (e.z) store_piece(p, e.z, e.z_dtype, at, n, v);
+        if (e.z) store_piece(p, e.z, e.z_dtype, row0, n, v, buf);
         if (e.act != MHC_LINEAR_NONE)
             with_act(e.act, [&](auto act) {
 #pragma unroll
                 for (int q = 0; q < 32; ++q) v[q] = act_value<decltype(act)::value>(v[q]);
             });
-        if (e.residual) each_raw(r, p.wide, e.residual_dtype, [&](int q, float x) { v[q] += x; });
+        if (e.residual) each_raw(r, p.wide, e.residual_dtype, e.extra_runs, buf, [&](int q, float x) { v[q] += x; });
     } else if constexpr (KIND == EPI_SLOPE) {
         float z[32];
-        each_raw(r, p.wide, e.z_dtype, [&](int q, float x) { z[q] = x; });
+        each_raw(r, p.wide, e.z_dtype, e.extra_runs, buf, [&](int q, float x) { z[q] = x; });
         with_act(e.act, [&](auto act) {
 #pragma unroll
             for (int q = 0; q < 32; ++q) v[q] *= act_slope<decltype(act)::value>(z[q]);
         });
     } else {
-        if (e.accumulate) each_raw(r, p.wide, e.out_dtype, [&](int q, float x) { v[q] += x; });
+        if (e.accumulate) each_raw(r, p.wide, e.out_dtype, true, buf, [&](int q, float x) { v[q] += x; });
     }
-    store_piece(p, e.out, e.out_dtype, at, n, v);
+    store_piece(p, e.out, e.out_dtype, row0, n, v, buf);
 }
 // One element on any boundary.
 template <int KIND>

@@ -153,21 +153,48 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     // each CTA the same rows of every token
     const int rows = kRows / a.split, r0 = rank * rows;
     if (!*abort_flag) {
-        for (int q = threadIdx.x; q < a.m * rows; q += kThreads) {
-            const int t = q / rows, r = r0 + q - t * rows, j = tile * kRows + r;
-            if (j >= a.n) continue;
-            float x = 0.f;
-            if (a.split == 1) {
-                x = sums[t * kRows + r];
-            } else {
-                float part[kMaxSplit];
-                const uint32_t at = smem_addr(sums + t * kRows + r);
+        // four elements of a thread at a time, what they are combined with on its way beside the sums
+        constexpr int kAtOnce = 4;
+        const int shift = 31 - __clz(rows), count = a.m << shift;
+        for (int q0 = threadIdx.x; q0 < count; q0 += kAtOnce * kThreads) {
+            float x[kAtOnce], extra[kAtOnce], bias[kAtOnce];
 #pragma unroll
-                for (int p = 0; p < kMaxSplit; ++p) part[p] = p < a.split ? load_at_rank(at, p) : 0.f;
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int q = q0 + u * kThreads, t = q >> shift, r = r0 + (q & (rows - 1)), j = tile * kRows + r;
+                x[u] = extra[u] = bias[u] = 0.f;
+                if (q >= count || j >= a.n) continue;
+                if constexpr (KIND == EPI_LINEAR) {
+                    if (a.e.bias) bias[u] = load_any(a.e.bias, a.e.bias_dtype, j);
+                    if (a.e.residual) extra[u] = load_any(a.e.residual, a.e.residual_dtype, t * a.e.residual_stride + j);
+                } else {
+                    extra[u] = load_any(a.e.z, a.e.z_dtype, t * a.e.z_stride + j);
+                }
+                if (a.split == 1) {
+                    x[u] = sums[t * kRows + r];
+                } else {
+                    float part[kMaxSplit];
+                    const uint32_t at = smem_addr(sums + t * kRows + r);
 #pragma unroll
-                for (int p = 0; p < kMaxSplit; ++p) x += part[p];
+                    for (int p = 0; p < kMaxSplit; ++p) part[p] = p < a.split ? load_at_rank(at, p) : 0.f;
+#pragma unroll
+                    for (int p = 0; p < kMaxSplit; ++p) x[u] += part[p];
+                }
             }
-            finish_element<KIND>(a.e, t, static_cast<long long>(t) * a.n + j, j, x);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int q = q0 + u * kThreads, t = q >> shift, j = tile * kRows + r0 + (q & (rows - 1));
+                if (q >= count || j >= a.n) continue;
+                const long long to = static_cast<long long>(t) * a.n + j;
+                if constexpr (KIND == EPI_LINEAR) {
+                    x[u] += bias[u];
+                    if (a.e.z) store_any(a.e.z, a.e.z_dtype, to, x[u]);
+                    with_act(a.e.act, [&](auto act) { x[u] = act_value<decltype(act)::value>(x[u]); });
+                    x[u] += extra[u];
+                } else {
+                    with_act(a.e.act, [&](auto act) { x[u] *= act_slope<decltype(act)::value>(extra[u]); });
+                }
+                store_any(a.e.out, a.e.out_dtype, to, x[u]);
+            }
         }
     }
     __syncwarp();
@@ -187,7 +214,8 @@ int launch_few_tokens(const Product &p, int sms, unsigned int *status, bool pdl,
     a.steps = static_cast<int>((p.k + kPairStep - 1) / kPairStep);
     const int tiles = (p.n + kRows - 1) / kRows;
     a.split = 1;
-    while (a.split < kMaxSplit && 2 * a.split * tiles <= 2 * sms && a.steps >= 2 * a.split) a.split *= 2;
+    // also where there is nothing to split, so that more CTAs finish many tokens (512 elements of a CTA at least)
+    while (a.split < kMaxSplit && 2 * a.split * tiles <= 2 * sms && (a.steps >= 2 * a.split || a.m * kRows / a.split >= 1024)) a.split *= 2;
     a.per = (a.steps + a.split - 1) / a.split;
     const int most = 512 / a.width;
     a.chain = p.exact ? (a.per + most - 1) / most > 8 ? (a.per + most - 1) / most : 8 : a.per;

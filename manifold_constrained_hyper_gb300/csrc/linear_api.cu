@@ -129,8 +129,9 @@ mhc_status mhc_linear(const void *x, int64_t x_stride, const void *w, int64_t w_
     f.e.z = z_out;
     f.e.z_dtype = dtype;
     f.e.act = act;
-    f.e.wide = n % 8 == 0 && on_runs(out, out_dtype) && on_runs(z_out, dtype) && (!bias || on_runs(bias, bias_dtype)) &&
-               on_runs(residual, out_dtype) && f.e.residual_stride % 8 == 0;
+    f.e.wide = n % 8 == 0 && on_runs(out, out_dtype) && on_runs(z_out, dtype);
+    f.e.extra_runs = on_runs(residual, out_dtype) && f.e.residual_stride % 8 == 0;
+    f.e.bias_runs = !bias || on_runs(bias, bias_dtype);
     return forward(f, stream);
 }
 
@@ -163,7 +164,9 @@ mhc_status mhc_linear_dx(const void *d_out, int64_t d_out_stride, const void *w,
         f.e.z_stride = tokens == 1 ? k : z_stride;
         f.e.act = act;
     }
-    f.e.wide = k % 8 == 0 && on_runs(d_x, d_x_dtype) && (!slope || (on_runs(z, dtype) && f.e.z_stride % 8 == 0));
+    f.e.wide = k % 8 == 0 && on_runs(d_x, d_x_dtype);
+    f.e.extra_runs = !slope || (on_runs(z, dtype) && f.e.z_stride % 8 == 0);
+    f.e.bias_runs = 1;
     return forward(f, stream);
 }
 
@@ -204,6 +207,7 @@ mhc_status mhc_linear_dw(const void *d_out, int64_t d_out_stride, const void *x,
     p.epi.out_dtype = d_w_dtype;
     p.epi.accumulate = accumulate != 0;
     p.epi.wide = k % 8 == 0 && on_runs(d_w, d_w_dtype);
+    p.epi.extra_runs = p.epi.bias_runs = 1;
     CopyJob jobs[2] = {};
     if (tokens > 0) {
         operand(&p.a, &jobs[0], d_out, d_out_stride, tokens, n, true, &at);

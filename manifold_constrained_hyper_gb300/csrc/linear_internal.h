@@ -36,7 +36,8 @@ struct EpilogueArgs {
     long long z_stride;
     int z_dtype;
     int act;
-    int wide;                                       // every row that is touched lies on the boundaries of runs of 8
+    int wide;                                       // every row that is written lies on the boundaries of runs of 8
+    int extra_runs, bias_runs;                      // and of residual or of z that is read, and the bias
 };
 struct Product {
     long long m;

@@ -600,9 +600,11 @@ Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turn
     long long count = 0;
     for (int tile_n : {kTile, kHalf}) {
         const long long c = tiles(tile_n);
-        const int most = static_cast<int>(c <= pairs ? pairs / c : 1);
-        for (int s : {1, most < f.steps / 6 ? most : f.steps / 6}) {
-            if (s < 1 || s > tile_n / 16) continue;
+        int most = static_cast<int>(c <= pairs ? pairs / c : 1);
+        if (most > f.steps / 6) most = f.steps / 6;
+        if (most > tile_n / 16) most = tile_n / 16;     // each of them finishes 16 columns at least
+        for (int s : {1, most}) {
+            if (s < 1) continue;
             const int per = (f.steps + s - 1) / s;
             const double cost = static_cast<double>((c * s + pairs - 1) / pairs) * per * (tile_n == kTile ? 0.33 : 0.22) +
                                 (s > 1 ? 5.0 : 2.4) * (tile_n == kTile ? 2. : 1.);

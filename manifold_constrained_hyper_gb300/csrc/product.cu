@@ -24,13 +24,15 @@ constexpr int kStep = kPairStep;
 constexpr int kBoxBytes = kPairBoxBytes;
 constexpr int kStageBytes = 4 * kBoxBytes;
 constexpr int kStages = 6;
-constexpr int kSumWarps = 8;                        // epilogue: two to a quadrant of tensor-memory lanes
+// Epilogue: two to a quadrant of tensor-memory lanes. With four, 96 registers a thread and five stages are left (8192 x 4096 x 7168
+// 283 -> 307 us, 4195 x 254 x 1216 with gelu 28 -> 34).
+constexpr int kSumWarps = 8;
 constexpr int kThreads = 64 + 32 * kSumWarps;       // loads, products, epilogue
 // Steps that tensor memory adds up by itself: the tensor cores cut what an addition shifts out, and a
 // chain of 64 steps drifts by 4e-6 of the result, one of 8 by 4e-7. The epilogue adds the pieces in fp32.
 constexpr int kChainExact = 8, kChain = 64;
 constexpr int kBars = 2 * kStages + 5;
-constexpr int kTurnBytes = kSumWarps * 32 * 33 * 4;
+constexpr int kTurnBytes = kSumWarps * 32 * 32 * 4;     // a piece each, to turn it or to store it by rows
 constexpr int kSmem = kStages * kStageBytes + 1024 + 256 + kTurnBytes;
 constexpr int kTmemCols = 512;
 constexpr int kBand = 8;                            // rows of tiles that are walked together
@@ -99,12 +101,12 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     uint8_t *const basep = raw + (base - smem_addr(raw));
-    const uint32_t bars = base + kStages * kStageBytes;
+    const uint32_t bars = base + kStages * kStageBytes + kTurnBytes;
     const uint32_t full = bars, empty = bars + 8 * kStages, acc_full = bars + 16 * kStages,
                    acc_empty = acc_full + 16, drain = acc_full + 32;
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + kStages * kStageBytes + 8 * kBars);
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + (bars - base) + 8 * kBars);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    float *const turn = reinterpret_cast<float *>(basep + kStages * kStageBytes + 256);
+    float *const turn = reinterpret_cast<float *>(basep + kStages * kStageBytes);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     constexpr int kCtas = PAIR ? 2 : 1, kRows = kCtas * kHalf;      // of a tile
     const uint32_t rank = PAIR ? cluster_rank() : 0;
@@ -231,27 +233,26 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int quad = warp & 3;                  // the tensor-memory lanes this warp may read
         const int width = a.tile_n / 2;             // the columns it sums: the tile's first or second half
         const int first = (warp - 2) / 4 * width;
-        float *const piece = turn + (warp - 2) * 32 * 33;
+        float *const piece = turn + (warp - 2) * 32 * 32;
         uint32_t done = 0;
         bool ok = true;
         for (int item = pair; item < a.items && ok; item += pairs) {
             const Place p = place_of(a, item);
             const int s0 = p.split * a.steps_per_split;
             const int s1 = s0 + a.steps_per_split < a.steps ? s0 + a.steps_per_split : a.steps;
-            const long long i = static_cast<long long>(p.ti) * kRows + static_cast<int>(rank) * kHalf + quad * 32 + lane;
-            const long long row = (p.split * a.m + i) * a.n;     // the splits' sums follow one another
-            const int j0 = p.tj * a.tile_n + first;
+            const long long i0 = static_cast<long long>(p.ti) * kRows + static_cast<int>(rank) * kHalf + quad * 32;
+            const long long row = (p.split * a.m + i0) * a.n;    // the splits' sums follow one another
+            const int j0 = p.tj * a.tile_n + first, rows = a.m - i0 >= 32 ? 32 : a.m > i0 ? static_cast<int>(a.m - i0) : 0;
+            const bool wide = a.e.wide;
+            const uint32_t buf = smem_addr(piece);
             auto piece_at = [&](int j) {
-                if (a.e.wide) return Piece{true, i < a.m ? a.n - j : 0};
-                const long long rows = a.m - (i - lane);
-                return Piece{false, j + lane >= a.n ? 0 : rows < 32 ? static_cast<int>(rows) : 32};
+                if (wide) return Piece{true, rows, a.n - j};
+                return Piece{false, j + lane >= a.n ? 0 : rows, 1};
             };
             // what the piece from column j on is combined with
             auto ahead = [&](Raw &r, float &bias, int j) {
-                const bool wide = a.e.wide;
                 if (KIND == EPI_LINEAR && a.e.bias && j + lane < a.n) bias = load_any(a.e.bias, a.e.bias_dtype, j + lane);
-                load_extra<KIND>(r, piece_at(j), a.e, wide ? i : i - lane, wide ? j : j + lane,
-                                 wide ? row + j : row - static_cast<long long>(lane) * a.n + j + lane, a.n);
+                load_extra<KIND>(r, piece_at(j), a.e, i0, wide ? j : j + lane, row + (wide ? j : j + lane), a.n);
             };
             uint64_t sum[4][16];
 #pragma unroll
@@ -290,8 +291,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 if (lane == 0) arrive_leader<PAIR>(acc_empty + 8 * buf);
             }
             if (!ok) break;
-            // the sums' registers are free from here on: a piece's operands are on their way while the one
-            // before is finished
+// the sums' registers are free from here on: a piece's operands are on their way while the one before is finished
             Raw extra = {};
             float bias = 0.f;
             if (j0 < a.n) ahead(extra, bias, j0);
@@ -305,19 +305,19 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 float next_bias = 0.f;
                 if (c + 32 < width && j + 32 < a.n) ahead(next, next_bias, j + 32);
                 float f[32];
-                if (a.e.wide) {
+                if (wide) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
                 } else {
                     // rows on any boundary: turned in shared memory, then a column a lane
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) piece[lane * 33 + e] = __uint_as_float(v[e]);
                     __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = piece[e * 33 + lane];
+                    for (int e = 0; e < 32; ++e) piece[lane * 32 + (e ^ lane)] = __uint_as_float(v[e]);
                     __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = piece[e * 32 + (lane ^ e)];
                 }
-                finish_piece<KIND>(piece_at(j), a.e, a.e.wide ? row + j : row - static_cast<long long>(lane) * a.n + j + lane, a.n, bias, f, extra);
+                finish_piece<KIND>(piece_at(j), a.e, row + (wide ? j : j + lane), a.n, bias, f, extra, buf);
                 extra = next;
                 bias = next_bias;
             }
@@ -539,7 +539,7 @@ bool encode_operand(CUtensorMap *m, const Product &p, const Operand &o, long lon
 
 template <int KIND>
 int launch_join(const float *parts, int splits, const Product &p, int sms, bool pdl, cudaStream_t s) {
-    const int vec = p.epi.wide ? 8 : 1;
+    const int vec = p.epi.wide && p.epi.extra_runs && p.epi.bias_runs ? 8 : 1;
     const long long need = (p.m * p.n + 256 * vec - 1) / (256 * vec), cap = static_cast<long long>(sms) * 16;
     return note_launch(launch_block_kernel(vec == 8 ? product_join_kernel<KIND, 8> : product_join_kernel<KIND, 1>,
                                            static_cast<unsigned>(need < cap ? need : cap), 256, 0, pdl, s, parts, splits, p.m, p.n,

@@ -110,6 +110,41 @@ def test_the_gradients_of_the_weight_and_bias(T, N, K, dtype, out, bias, pad):
     ref.within(w1, s, e + 2 * ref.U * s.abs())
 
 
+@pytest.mark.parametrize("act", ref.ACTS)
+@pytest.mark.parametrize("dtype", [BF, FP16])
+def test_the_activations_and_their_slopes_over_their_range(act, dtype):
+    """The weights a unit matrix, so that z is x itself: act(z) in fp32 is off by what its evaluation is, relative to
+    itself, far out too."""
+    K = 64
+    x = torch.cat((torch.linspace(-12, 12, 4000), torch.logspace(-4, 0, 500), -torch.logspace(-4, 0, 500), torch.zeros(120)))
+    x = x.to(dtype).view(-1, K).cuda()
+    eye = torch.eye(K, device="cuda").to(dtype)
+    z = x.double()
+    out, slope, ea, es = ref.act(z, act)
+    for rows in (x, x[:40]):
+        got = ops.mhc_linear(rows, eye, act=act, dtype=FP32).double()
+        n = rows.shape[0]
+        assert ((got - out[:n]).abs() <= 2 * ref.U * ea[:n] + 1e-37).all()
+        if act != "none":
+            d = ops.mhc_linear_dx(torch.ones_like(rows), eye, rows, act, dtype=FP32).double()
+            assert ((d - slope[:n]).abs() <= 2 * ref.U * es[:n] + 1e-37).all()
+
+
+@pytest.mark.parametrize("T,N", [(300, 264), (90, 72)])
+@pytest.mark.parametrize("pad", [1, 3, 8])
+def test_rows_of_the_residual_and_of_z_on_any_boundary(T, N, pad):
+    g = gen(T + pad)
+    K = 96
+    x, w = rows(g, T, K, BF), rows(g, N, K, BF, 0, 0, K ** -0.5)
+    for dt in (BF, FP32):
+        r = rows(g, T, N, dt, pad, 1)
+        want, _, e, _ = ref.linear(x, w, None, r, "silu")
+        ref.within(ops.mhc_linear(x, w, None, r, "silu"), want, e)
+    d, w2, z = rows(g, T, K, BF), rows(g, K, N, BF, 0, 0, K ** -0.5), rows(g, T, N, BF, pad, 1)
+    want, e = ref.linear_dx(d, w2, z, "gelu")
+    ref.within(ops.mhc_linear_dx(d, w2, z, "gelu"), want, e)
+
+
 def test_no_tokens():
     w = torch.randn(96, 64, device="cuda").to(BF)
     x = torch.empty(0, 64, device="cuda", dtype=BF)
