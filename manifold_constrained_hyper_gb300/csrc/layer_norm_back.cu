@@ -12,10 +12,14 @@ namespace {
 constexpr int kR = 2;                               // runs of 8 columns a thread at most
 constexpr int kAllBarrier = 15;                     // of all groups (of several warps there are at most 8)
 
-// The groups' sums over tokens to the CTA's set, in the groups' order, through meet [groups][2][Hp].
+// The groups' sums over tokens to the CTA's set, or, where it is the only CTA, to the outputs, in the groups' order, through
+// meet [groups][2][Hp].
 template <int R>
-__device__ __forceinline__ void meet_sums(float *meet, float *set, const Run (&dw)[R], const Run (&db)[R], int H, int Hp, int groups, int group,
+__device__ __forceinline__ void meet_sums(float *meet, const LayerNormBackArgs &a, const Run (&dw)[R], const Run (&db)[R], int groups, int group,
                                           int warps, int mine) {
+    const int H = a.H, Hp = (H + 7) / 8 * 8;
+    float *const set = a.sums + static_cast<long long>(blockIdx.x) * 2 * H;
+    float *const to_w = gridDim.x == 1 ? a.d_w : set, *const to_b = gridDim.x == 1 ? a.d_b : set + H;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int c = (r * warps * 32 + mine) * 8;
@@ -34,7 +38,8 @@ __device__ __forceinline__ void meet_sums(float *meet, float *set, const Run (&d
         if (col >= H) continue;
         float v = meet[c];
         for (int g = 1; g < groups; ++g) v += meet[static_cast<long long>(g) * 2 * Hp + c];
-        set[(c < Hp ? 0 : H) + col] = v;
+        float *const out = c < Hp ? to_w : to_b;
+        if (out) out[col] = v;
     }
 }
 
@@ -101,7 +106,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_rows_kernel(const LayerNor
         }
     }
     if (!want) return;
-    meet_sums<R>(sums, a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H, dw, db, a.H, (a.H + 7) / 8 * 8, groups, group, warps, mine);
+    meet_sums<R>(sums, a, dw, db, groups, group, warps, mine);
 }
 
 // The same for many rows: rows to come staged in shared memory, where the
@@ -226,8 +231,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNor
     if (!a.d_w && !a.d_b) return;
     // the groups' sums meet in the stages, which hold nothing on its way any more, and each thread adds some columns
     named_barrier_sync(kAllBarrier, threads);
-    meet_sums<R>(reinterpret_cast<float *>(smem + 1024 + par_bytes), a.sums + static_cast<long long>(blockIdx.x) * 2 * a.H, dw, db, a.H, Hp,
-                 groups, group, warps, mine);
+    meet_sums<R>(reinterpret_cast<float *>(smem + 1024 + par_bytes), a, dw, db, groups, group, warps, mine);
 }
 
 // Rows too wide to be held: a CTA a row, read twice; its sums over tokens in its set, each column its thread's.
@@ -379,7 +383,8 @@ cudaError_t launch_types(const LayerNormBackArgs &a, unsigned int *status, bool 
 }  // namespace
 
 size_t layer_norm_sums_bytes(long long T, int H) {
-    return T > 0 ? static_cast<size_t>(shape_of(T, H).parts) * 2 * H * 4 : 0;
+    const int parts = T > 0 ? shape_of(T, H).parts : 0;
+    return parts > 1 || H > kLnMaxHeld ? static_cast<size_t>(parts) * 2 * H * 4 : 0;
 }
 
 int launch_layer_norm_back(const LayerNormBackArgs &a, unsigned int *status, bool pdl, cudaStream_t s) {
@@ -393,6 +398,7 @@ int launch_layer_norm_back(const LayerNormBackArgs &a, unsigned int *status, boo
         else e = launch_types<float, float>(a, status, pdl, s);
         if (int r = note_launch(e)) return r;
         parts = shape_of(a.T, a.H).parts;
+        if (parts == 1 && a.H <= kLnMaxHeld) return MHC_OK;     // the row kernel wrote the sums
     }
     if (!a.d_w && !a.d_b) return MHC_OK;
     cudaLaunchConfig_t cfg = {};

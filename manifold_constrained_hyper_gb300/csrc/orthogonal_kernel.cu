@@ -1,9 +1,9 @@
-// All the products of an orthogonalised update in one cooperative launch: pairs of CTAs stay on their
+// All the products of an orthogonalised update in one cooperative launch: CTAs, or pairs of them, stay on their
 // SMs and walk the products one after another, a barrier of the grid between two. Products with few
 // tiles split the summed axis over the pairs; those of a tile wait for one another's parts, and each
 // then adds them, in their order, for some of the tile's columns.
 //
-// A pair forms a 256 x 256 or 256 x 128 tile as the products with an epilogue do (64 of k a stage, six
+// A pair forms a 256 x 256 or 256 x 128 tile, a CTA a 128 x 128 or 128 x 64 one, as the products with an epilogue do (64 of k a stage, six
 // stages, two buffers of sums in tensor memory); every operand is two fp16 parts, three products a step.
 // A symmetric result's tiles left of the diagonal are not formed: those right of it are stored twice,
 // the second time a column a store, which is contiguous across a warp's lanes.
@@ -18,8 +18,7 @@
 namespace mhc {
 namespace {
 
-constexpr int kTile = 256;
-constexpr int kHalf = kTile / 2;
+constexpr int kHalf = 128;                          // rows of a tile by a CTA
 constexpr int kStageBytes = 4 * kPairBoxBytes;
 constexpr int kStages = 5;
 constexpr int kSumWarps = 8;
@@ -41,7 +40,7 @@ struct Phase {
     int role;                       // GRAM: of X with itself; SQUARE: of two matrices; APPLY: of one with X
     int a, b, out, add;             // matrices; add: what is added times of_add (-1: nothing)
     int m, n, tiles_m, tiles_n, tile_n, steps, passes, splits, per, items;
-    int symmetric, a_turned, b_turned;
+    int symmetric, ratio, a_turned, b_turned;       // ratio: of a tile's rows to its columns
     uint32_t idesc;
     float of_sum, of_add, of_unit;  // of_unit: on the diagonal
 };
@@ -64,7 +63,6 @@ struct NsArgs {
 struct NsMaps {
     CUtensorMap gram_a[2][2], gram_b[2][2], apply_x[2][2];      // [turn][hi, lo]
     CUtensorMap mat_a[M_COUNT][2], mat_b[M_COUNT][2];
-    CUtensorMap to_x[2][2], to_mat[M_COUNT][2], to_out;         // 32 rows of 64 columns, to store
 };
 // Which of the phases the ph-th product is, how many like it came before, and X's turn.
 struct Step {
@@ -93,7 +91,7 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(const Phase &f, int item) {
     Place p;
-    const int ratio = kTile / f.tile_n;
+    const int ratio = f.ratio;
     const int tiles = f.tiles_m * f.tiles_n - (f.symmetric ? ratio * (f.tiles_m * (f.tiles_m - 1) / 2) : 0);
     p.tile = item / f.splits;
     p.split = item - p.tile * f.splits;
@@ -178,21 +176,26 @@ __device__ __forceinline__ void mirror8(const Target &t, int i, int j, const uin
         if (!t.one) *l = static_cast<uint16_t>(lw[q >> 1] >> (q & 1) * 16);
     }
 }
-__device__ __forceinline__ void tma_store_3d_plain(const CUtensorMap *m, int c0, int c1, int c2, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
-                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(src) : "memory");
+// The warp's 32 x 64 elements of 16 bits at `held` (a row a 128-byte line, its 16 bytes c at c ^ (row & 7)) to whole lines.
+__device__ __forceinline__ void put_lines(uint8_t *to, long long pitch_bytes, int rows, int columns, uint32_t held) {
+    const int lane = threadIdx.x & 31, c = lane & 7;
+    const long long step = here(4 * pitch_bytes);
+    uint8_t *q = to + (lane >> 3) * pitch_bytes + 16 * c;
+#pragma unroll
+    for (int k = 0; k < 8; ++k, q += step) {
+        const int row = 4 * k + (lane >> 3);
+        const uint4 v = ld_shared_v4(held + row * 128 + ((c ^ (row & 7)) << 4));
+        if (row < rows && 8 * c < columns) *reinterpret_cast<uint4 *>(q) = v;
+    }
 }
-// 64 columns of the warp's 32 rows, through shared memory (128-byte rows in the 128-byte swizzle) by TMA,
-// which writes whole lines; a row a lane to global memory would be 32 lines a store. `sums`: in tensor memory.
-__device__ __forceinline__ void put64(const NsArgs &a, const Target &t, const CUtensorMap *hi_map, const CUtensorMap *lo_map, int batch, int i0,
-                                      int j, uint32_t sums, uint32_t held) {
+// 64 columns (width: or 32) of the warp's 32 rows, through shared memory: a row a lane to global memory would be 32 lines
+// a store (by TMA from there: 1 us more until the stores are complete). `sums`: in tensor memory.
+__device__ __forceinline__ void put_piece(const NsArgs &a, const Target &t, int batch, int i0, int j, int width, uint32_t sums, uint32_t held) {
     const int lane = threadIdx.x & 31, i = i0 + lane;
-    // the last pieces have been read
-    if (lane == 0) bulk_wait_read_all();
-    __syncwarp();
+    __syncwarp();       // the piece before has been read
     // eight columns at a time: a short loop, whose instructions are fetched once
 #pragma unroll 1
-    for (int c = 0; c < 64; c += 8) {
+    for (int c = 0; c < width; c += 8) {
         uint4 xh, xl;
         load_x8(xh, xl, t, i, j + c);
         uint32_t u[8];
@@ -217,13 +220,16 @@ __device__ __forceinline__ void put64(const NsArgs &a, const Target &t, const CU
             if (t.mirror && i < t.m && j + c < t.n) mirror8(t, i, j + c, hw, lw);
         }
     }
-    fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-        tma_store_3d_plain(hi_map, j, i0, batch, held);
-        if (!t.final && !t.one) tma_store_3d_plain(lo_map, j, i0, batch, held + kOutBytes);
-        bulk_commit();
+    const int rows = t.m - i0, columns = t.n - j < width ? t.n - j : width;
+    if (t.final) {
+        put_lines(static_cast<uint8_t *>(a.out) + ((static_cast<long long>(batch) * t.m + i0) * t.n + j) * 2, static_cast<long long>(t.n) * 2, rows,
+                  columns, held);
+        return;
     }
+    const long long at = static_cast<long long>(i0) * t.pitch + j;
+    put_lines(reinterpret_cast<uint8_t *>(t.hi + at), t.pitch * 2, rows, columns, held);
+    if (!t.one) put_lines(reinterpret_cast<uint8_t *>(t.lo + at), t.pitch * 2, rows, columns, held + kOutBytes);
 }
 // Columns [j, j + 8) of the warp's 32 rows from i0 on, a row a lane; `piece`: 32 x 9 floats of the warp.
 __device__ __forceinline__ void put8(const NsArgs &a, const Target &t, int batch, int i0, int j, float (&v)[8], float *piece) {
@@ -263,6 +269,7 @@ __device__ __forceinline__ void put8(const NsArgs &a, const Target &t, int batch
     __syncwarp();
 }
 
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a) {
     extern __shared__ uint8_t raw[];
@@ -275,8 +282,9 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + (bars - base) + 8 * kBars);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    constexpr int kCtas = PAIR ? 2 : 1, kTile = kCtas * kHalf;
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const int unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
     const int phases = kPairPhases * a.pairs + kStepPhases * (a.singles + 1);
 
     if (threadIdx.x == 0) {
@@ -286,7 +294,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full + 8 * b, 1);
-            mbar_init(acc_empty + 8 * b, 2 * kSumWarps);
+            mbar_init(acc_empty + 8 * b, kCtas * kSumWarps);
         }
         mbar_init(drain, 1);
         mbar_init(go, 1);
@@ -295,13 +303,11 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
         fence_mbar_init();
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_addr(tmem_slot)), "r"(kTmemCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        unit_tmem_alloc<PAIR>(smem_addr(tmem_slot), kTmemCols);
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    if constexpr (PAIR) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
@@ -326,8 +332,8 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
             const CUtensorMap *const mb = f.role == R_GRAM               ? maps.gram_b[at.x]
                                           : f.role == R_APPLY && a.wide ? maps.apply_x[at.x]
                                                                         : maps.mat_b[f.b];
-            const int half = f.tile_n / 2;
-            for (int item = pair; item < f.items && ok; item += pairs) {
+            const int half = f.tile_n / kCtas;
+            for (int item = unit; item < f.items && ok; item += units) {
                 const Place p = place_of(f, item);
                 const int s0 = p.split * f.per, s1 = s0 + f.per < f.steps ? s0 + f.per : f.steps;
                 const int ci = p.ti * kTile + static_cast<int>(rank) * kHalf, cj = p.tj * f.tile_n + static_cast<int>(rank) * half;
@@ -338,21 +344,21 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kPairBoxBytes * (half == kHalf ? 8 : 6));
-                    const uint32_t bar = map_to_rank(full + 8 * s, 0), da = base + s * kStageBytes, db = da + 2 * kPairBoxBytes;
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kCtas * (2 * kPairBoxBytes + half * 128));
+                    const uint32_t bar = PAIR ? map_to_rank(full + 8 * s, 0) : full + 8 * s, da = base + s * kStageBytes, db = da + 2 * kPairBoxBytes;
                     const int k = kb * kPairStep;
                     const CUtensorMap *const am = ma + (part == 2), *const bm = mb + (part == 1);
                     if (f.a_turned) {
-                        tma_load_pair_3d(da, am, ci, k, p.batch, bar);
-                        tma_load_pair_3d(da + kPairBoxBytes, am, ci + 64, k, p.batch, bar);
+                        unit_load<PAIR>(da, am, ci, k, p.batch, bar);
+                        unit_load<PAIR>(da + kPairBoxBytes, am, ci + 64, k, p.batch, bar);
                     } else {
-                        tma_load_pair_3d(da, am, k, ci, p.batch, bar);
+                        unit_load<PAIR>(da, am, k, ci, p.batch, bar);
                     }
                     if (f.b_turned) {
-                        tma_load_pair_3d(db, bm, cj, k, p.batch, bar);
-                        if (half == kHalf) tma_load_pair_3d(db + kPairBoxBytes, bm, cj + 64, k, p.batch, bar);
+                        unit_load<PAIR>(db, bm, cj, k, p.batch, bar);
+                        if (half == kHalf) unit_load<PAIR>(db + kPairBoxBytes, bm, cj + 64, k, p.batch, bar);
                     } else {
-                        tma_load_pair_3d(db, bm, k, cj, p.batch, bar);
+                        unit_load<PAIR>(db, bm, k, cj, p.batch, bar);
                     }
                     if (++part == f.passes) {
                         part = 0;
@@ -377,9 +383,9 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
         for (int ph = 0; ph < phases && ok; ++ph) {
             const Phase &f = a.phase[step_of(a, ph).phase];
             const uint64_t na = f.a_turned ? 2048 >> 4 : 32 >> 4, nb = f.b_turned ? 2048 >> 4 : 32 >> 4;
-            for (int item = pair; item < f.items && ok; item += pairs, ++done) {
+            for (int item = unit; item < f.items && ok; item += units, ++done) {
                 const int split = item % f.splits, s0 = split * f.per, s1 = s0 + f.per < f.steps ? s0 + f.per : f.steps;
-                const uint32_t buf = done & 1, acc = tmem + buf * kTile;
+                const uint32_t buf = done & 1, acc = tmem + buf * 256;
                 // a barrier of the grid may lie between: as long as it may take
                 if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status, SITE_N_ACC_EMPTY)) {
                     ok = false;
@@ -396,16 +402,16 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     const uint32_t sa = base + s * kStageBytes, sb = sa + 2 * kPairBoxBytes;
                     const uint64_t da = f.a_turned ? desc_columns(sa) : desc_rows(sa), db = f.b_turned ? desc_columns(sb) : desc_rows(sb);
 #pragma unroll
-                    for (int q = 0; q < kPairStep / 16; ++q) mma_pair(acc, da + q * na, db + q * nb, f.idesc, st > s0 || q > 0);
-                    commit_pair(empty + 8 * s);
+                    for (int q = 0; q < kPairStep / 16; ++q) unit_multiply<PAIR>(acc, da + q * na, db + q * nb, f.idesc, st > s0 || q > 0);
+                    unit_commit<PAIR>(empty + 8 * s);
                 }
-                if (ok) commit_pair(acc_full + 8 * buf);
+                if (ok) unit_commit<PAIR>(acc_full + 8 * buf);
             }
         }
         if (!ok) {
             // the products issued end before tensor memory is freed
             int gave_up = 0;
-            commit_pair(drain);
+            unit_commit<PAIR>(drain);
             mbar_wait(drain, 0, &gave_up, a.timeout_ns, a.status, SITE_N_DRAIN);
         }
     } else if (warp >= 2) {
@@ -432,7 +438,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
             }
-            for (int item = pair; item < f.items && ok; item += pairs, ++done) {
+            for (int item = unit; item < f.items && ok; item += units, ++done) {
                 const Place p = place_of(f, item);
                 const uint32_t buf = done & 1;
                 const int i0 = p.ti * kTile + static_cast<int>(rank) * kHalf + quad * 32, j0 = p.tj * f.tile_n;
@@ -457,17 +463,16 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sums = tmem + buf * kTile + first + (static_cast<uint32_t>(quad * 32) << 16);
+                const uint32_t sums = tmem + buf * 256 + first + (static_cast<uint32_t>(quad * 32) << 16);
                 if (f.splits == 1) {
-                    const CUtensorMap *const to = final ? &maps.to_out : to_x ? maps.to_x[st.x ^ 1] : maps.to_mat[f.out];
 #pragma unroll 1
                     for (int c = 0; c < width && i0 < f.m && j0 + first + c < f.n; c += 64) {
                         if (!final || a.out_wide) {
-                            put64(a, t, to, to + 1, p.batch, i0, j0 + first + c, sums + c, held);
+                            put_piece(a, t, p.batch, i0, j0 + first + c, width < 64 ? width : 64, sums + c, held);
                             continue;
                         }
 #pragma unroll 1
-                        for (int k = c; k < c + 64 && j0 + first + k < f.n; k += 8) {
+                        for (int k = c; k < c + 64 && k < width && j0 + first + k < f.n; k += 8) {
                             uint32_t u[8];
                             tmem_ld8_now(sums + k, u);
                             float v[8];
@@ -479,7 +484,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 } else {
                     // the tile's parts, [split][column][128 rows], a column of 32 rows a store
                     const long long part_size = static_cast<long long>(f.tile_n) * kHalf;
-                    float *const parts = a.parts + (static_cast<long long>(p.tile) * 2 + rank) * f.splits * part_size + quad * 32 + lane;
+                    float *const parts = a.parts + (static_cast<long long>(p.tile) * kCtas + rank) * f.splits * part_size + quad * 32 + lane;
                     float *const to = parts + p.split * part_size + first * kHalf;
 #pragma unroll 1
                     for (int c = 0; c < width; c += 32) {
@@ -493,7 +498,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     ok = meet();
                     if (!ok) break;
                     if (threadIdx.x == 64) {
-                        unsigned int *const count = a.counters + 32 + (st.phase * kNsMostPairs + p.tile) * 2 + rank;
+                        unsigned int *const count = a.counters + 32 + st.phase * kNsMostCtas + p.tile * kCtas + rank;
                         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
                         count_wait(count, f.splits * (st.round + 1), a, abort_flag, SITE_N_PARTS);
                     }
@@ -524,60 +529,62 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at_rank(map_to_rank(acc_empty + 8 * buf, 0));
+                if (lane == 0) unit_arrive<PAIR>(acc_empty + 8 * buf);
             }
             if (!ok || final) break;
             // what this CTA wrote, before it arrives: seen by other CTAs' loads of either kind
-            if (lane == 0) bulk_wait_all();
-            __syncwarp();
             fence_proxy_async_global();
             __threadfence();
             ok = meet();
             if (ok && threadIdx.x == 64) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counters) : "memory");
         }
     }
-    if (warp >= 2 && lane == 0) bulk_wait_all();
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     __syncwarp();
-    cluster_sync();
-    if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    if constexpr (PAIR) cluster_sync();
+    if (warp == 2) unit_tmem_free<PAIR>(tmem, kTmemCols);
 }
 
-// Pairs of CTAs that the device holds at once: 0 before it was asked.
-std::atomic<int> g_pairs[64];
+// Pairs of CTAs, and CTAs, that the device holds at once: 0 before it was asked.
+std::atomic<int> g_units[2][64];
 
-int resident_pairs(int *pairs) {
+template <bool PAIR>
+int resident_units(int *units) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
-    int n = g_pairs[dev & 63].load(std::memory_order_acquire);
+    constexpr int kCtas = PAIR ? 2 : 1;
+    int n = g_units[PAIR][dev & 63].load(std::memory_order_acquire);
     if (!n) {
-        if (cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return MHC_ERR_CUDA;
+        if (cudaFuncSetAttribute(ns_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return MHC_ERR_CUDA;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
+        cfg.gridDim = dim3(kCtas);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.x = kCtas;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, ns_kernel, &cfg) != cudaSuccess || n < 1) return MHC_ERR_CUDA;
-        if (n > kNsMostPairs) n = kNsMostPairs;
-        g_pairs[dev & 63].store(n, std::memory_order_release);
+        if (cudaOccupancyMaxActiveClusters(&n, ns_kernel<PAIR>, &cfg) != cudaSuccess || n < 1) return MHC_ERR_CUDA;
+        if (n > kNsMostCtas / kCtas) n = kNsMostCtas / kCtas;
+        g_units[PAIR][dev & 63].store(n, std::memory_order_release);
     }
-    *pairs = n;
+    *units = n;
     return MHC_OK;
 }
 
-// Tiles of 128 columns, and the summed axis split, where there are few tiles.
-Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turned, bool b_turned, int pairs) {
+// A product by `units` pairs of CTAs, or CTAs. The cheapest of both tiles' widths and of splitting or not, by what was
+// measured on one GB300: a step of 64 takes 0.33 us with a pair's 256 columns, where the tensor cores are busy, else
+// what it takes to issue and to load; finishing 64 columns of a tile by a warp 3 us; writing parts, waiting for the others' and
+// reading them 3.1 (256 columns 5.3), and finishing 16 columns of them 1.6.
+Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turned, bool b_turned, bool pair, int units, double *cost) {
     Phase f = {};
     const bool symmetric = role != R_APPLY;
+    const int rows = pair ? 2 * kHalf : kHalf;
     f.role = role;
     f.add = -1;
     f.of_sum = 1.f / kNsScale;
@@ -587,47 +594,46 @@ Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turn
     f.symmetric = symmetric;
     f.a_turned = a_turned;
     f.b_turned = b_turned;
-    f.tiles_m = (m + kTile - 1) / kTile;
+    f.tiles_m = (m + rows - 1) / rows;
     f.steps = passes * ((k + kPairStep - 1) / kPairStep);
     auto tiles = [&](int tile_n) {
         const long long c = (n + tile_n - 1) / tile_n, all = f.tiles_m * c;
-        return batch * (symmetric ? all - kTile / tile_n * (static_cast<long long>(f.tiles_m) * (f.tiles_m - 1) / 2) : all);
+        return batch * (symmetric ? all - rows / tile_n * (static_cast<long long>(f.tiles_m) * (f.tiles_m - 1) / 2) : all);
     };
-    // The cheapest of both tiles' widths and of splitting or not, by what was measured: a step of a pair
-    // takes 0.33 us with 256 columns, where the tensor cores are busy, and 0.22 with 128; finishing a tile 4.8
-    // and 2.4; writing parts, waiting for the others' and adding them 10 and 5.4.
-    double best = 1e30;
+    double best = 1e300;
     long long count = 0;
-    for (int tile_n : {kTile, kHalf}) {
+    for (int tile_n : {rows, rows / 2}) {
         const long long c = tiles(tile_n);
-        int most = static_cast<int>(c <= pairs ? pairs / c : 1);
+        const double step = tile_n == 256 ? 0.33 : pair ? 0.22 : tile_n == 128 ? 0.25 : 0.20;
+        int most = static_cast<int>(c <= units ? units / c : 1);
         if (most > f.steps / 6) most = f.steps / 6;
         if (most > tile_n / 16) most = tile_n / 16;     // each of them finishes 16 columns at least
         for (int s : {1, most}) {
             if (s < 1) continue;
             const int per = (f.steps + s - 1) / s;
-            const double cost = static_cast<double>((c * s + pairs - 1) / pairs) * per * (tile_n == kTile ? 0.33 : 0.22) +
-                                (s > 1 ? 5.0 : 2.4) * (tile_n == kTile ? 2. : 1.);
-            if (cost >= best) continue;
-            best = cost;
+            const double rounds = static_cast<double>((c * s + units - 1) / units), work = per * step, finish = 3. * tile_n / 128;
+            const double all = s > 1 ? work + (tile_n == 256 ? 5.3 : 3.1) + 1.6 * ((tile_n / 16 + 2 * s - 1) / (2 * s))
+                                     : (rounds - 1) * (work > finish ? work : finish) + work + finish;
+            if (all >= best) continue;
+            best = all;
             count = c;
             f.tile_n = tile_n;
             f.per = per;
             f.splits = (f.steps + per - 1) / per;
         }
     }
+    f.ratio = rows / f.tile_n;
     f.tiles_n = (n + f.tile_n - 1) / f.tile_n;
     f.items = static_cast<int>(count * f.splits);
     f.idesc = (1u << 4) | ((a_turned ? 1u : 0u) << 15) | ((b_turned ? 1u : 0u) << 16) | (static_cast<uint32_t>(f.tile_n >> 3) << 17) |
-              (static_cast<uint32_t>(kTile >> 4) << 24);
+              (static_cast<uint32_t>(rows >> 4) << 24);
+    *cost = best;
     return f;
 }
 
 }  // namespace
 
 int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
-    int pairs = 0;
-    if (int e = resident_pairs(&pairs)) return e;
     const int p = c.m < c.n ? c.m : c.n, q = c.m < c.n ? c.n : c.m;
     const bool wide = c.m <= c.n;
     NsArgs a = {};
@@ -643,8 +649,20 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
         if (v > largest) largest = v;
     }
     a.wide = wide;
-    const Phase gram = phase_of(R_GRAM, p, p, q, c.batch, 3, !wide, !wide, pairs), square = phase_of(R_SQUARE, p, p, p, c.batch, 3, false, false, pairs),
-                apply = phase_of(R_APPLY, c.m, c.n, p, c.batch, 3, false, wide, pairs);
+    // by pairs of CTAs or by CTAs, whichever makes a step the cheaper
+    int units[2] = {};
+    if (int e = resident_units<false>(&units[0])) return e;
+    if (int e = resident_units<true>(&units[1])) return e;
+    double cost[2][3];
+    Phase forms[2][3];
+    for (int k = 0; k < 2; ++k) {
+        forms[k][0] = phase_of(R_GRAM, p, p, q, c.batch, 3, !wide, !wide, k, units[k], &cost[k][0]);
+        forms[k][1] = phase_of(R_SQUARE, p, p, p, c.batch, 3, false, false, k, units[k], &cost[k][1]);
+        forms[k][2] = phase_of(R_APPLY, c.m, c.n, p, c.batch, 3, false, wide, k, units[k], &cost[k][2]);
+    }
+    const bool pair = cost[1][0] + cost[1][1] + cost[1][2] <= cost[0][0] + cost[0][1] + cost[0][2];
+    const int ctas = pair ? 2 : 1, places = units[pair];
+    const Phase gram = forms[pair][0], square = forms[pair][1], apply = forms[pair][2];
     const bool two = p >= 2048 && q >= p + p / 4 && largest <= 3.8 && square.tile_n == apply.tile_n;
     a.pairs = two ? (c.steps - 1) / 2 : 0;
     a.singles = c.steps - 1 - 2 * a.pairs;
@@ -674,9 +692,10 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     *f++ = times(apply, M_T, M_T, 0);
     for (int last = 0; last < 2; ++last) {
         const int passes = last ? last_passes : 3;
-        Phase g = last ? phase_of(R_GRAM, p, p, q, c.batch, passes, !wide, !wide, pairs) : gram;
-        Phase s2 = last ? phase_of(R_SQUARE, p, p, p, c.batch, passes, false, false, pairs) : square;
-        const Phase ap = last ? phase_of(R_APPLY, c.m, c.n, p, c.batch, passes, false, wide, pairs) : apply;
+        double ignored;
+        Phase g = last ? phase_of(R_GRAM, p, p, q, c.batch, passes, !wide, !wide, pair, places, &ignored) : gram;
+        Phase s2 = last ? phase_of(R_SQUARE, p, p, p, c.batch, passes, false, false, pair, places, &ignored) : square;
+        const Phase ap = last ? phase_of(R_APPLY, c.m, c.n, p, c.batch, passes, false, wide, pair, places, &ignored) : apply;
         g = times(g, 0, 0, M_A);
         g.of_unit = complete.shift * kNsScale;
         s2 = poly(s2, M_P, complete);
@@ -725,9 +744,8 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
         for (int t = 0; t < 2; ++t) {
             const __half *const x = c.x[t][k];
             ok = ok && rows(&maps.gram_a[t][k], x, c.n, c.m, c.x_pitch, c.x_size, wide ? kHalf : kPairStep);
-            ok = ok && rows(&maps.gram_b[t][k], x, c.n, c.m, c.x_pitch, c.x_size, wide ? gram.tile_n / 2 : kPairStep);
+            ok = ok && rows(&maps.gram_b[t][k], x, c.n, c.m, c.x_pitch, c.x_size, wide ? gram.tile_n / ctas : kPairStep);
             ok = ok && rows(&maps.apply_x[t][k], x, c.n, c.m, c.x_pitch, c.x_size, wide ? kPairStep : kHalf);
-            ok = ok && rows(&maps.to_x[t][k], x, c.n, c.m, c.x_pitch, c.x_size, 32);
         }
         // without pairs A is squared and P applied, no more
         for (int t = 0; t < (a.pairs ? M_COUNT : M_T); ++t) {
@@ -735,31 +753,27 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
             // where it is the second operand it has the rows of the tile's columns: of a square, or applied to a tall X
             const bool applied = a.pairs ? false : t == M_P;
             ok = ok && rows(&maps.mat_a[t][k], x, p, p, c.p_pitch, c.p_size, kHalf);
-            ok = ok && rows(&maps.mat_b[t][k], x, p, p, c.p_pitch, c.p_size, (applied ? apply.tile_n : square.tile_n) / 2);
-            ok = ok && rows(&maps.to_mat[t][k], x, p, p, c.p_pitch, c.p_size, 32);
+            ok = ok && rows(&maps.mat_b[t][k], x, p, p, c.p_pitch, c.p_size, (applied ? apply.tile_n : square.tile_n) / ctas);
         }
     }
-    if (a.out_wide)
-        ok = ok && encode_matrices16(&maps.to_out, c.out_dtype == MHC_BF16, c.out, c.n, c.m, c.batch, static_cast<unsigned long long>(c.n) * 2,
-                                     static_cast<unsigned long long>(c.m) * c.n * 2, 32);
     if (!ok) return MHC_ERR_CUDA;
     int most = 0;
     for (const Phase &f : a.phase) most = most > f.items ? most : f.items;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * static_cast<unsigned>(most < pairs ? most : pairs));
+    cfg.gridDim = dim3(ctas * static_cast<unsigned>(most < places ? most : places));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeCooperative;
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return note_launch(cudaLaunchKernelEx(&cfg, ns_kernel, maps, a));
+    return note_launch(cudaLaunchKernelEx(&cfg, pair ? ns_kernel<true> : ns_kernel<false>, maps, a));
 }
 
 }  // namespace mhc

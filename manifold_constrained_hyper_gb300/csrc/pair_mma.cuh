@@ -119,4 +119,54 @@ __device__ __forceinline__ void tmem_ld8_now(uint32_t taddr, uint32_t (&v)[8]) {
         : "r"(taddr) : "memory");
 }
 
+// What differs between a pair of CTAs and one.
+template <bool PAIR>
+__device__ __forceinline__ void unit_load(uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
+    if constexpr (PAIR)
+        tma_load_pair(dst, m, c0, c1, bar);
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                     ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void unit_load(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
+    if constexpr (PAIR)
+        tma_load_pair_3d(dst, m, c0, c1, c2, bar);
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                     ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void unit_multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    if constexpr (PAIR) mma_pair(d, a, b, idesc, add);
+    else tc_mma_bf16(d, a, b, idesc, add);
+}
+template <bool PAIR>
+__device__ __forceinline__ void unit_arrive(uint32_t bar) {
+    if constexpr (PAIR) arrive_at_rank(map_to_rank(bar, 0));
+    else mbar_arrive(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void unit_commit(uint32_t bar) {
+    if constexpr (PAIR) commit_pair(bar);
+    else tc_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void unit_tmem_alloc(uint32_t slot, int columns) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(slot, columns);
+        tmem_relinquish();
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void unit_tmem_free(uint32_t tmem, int columns) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+    else
+        tmem_dealloc(tmem, columns);
+}
+
 }  // namespace mhc

@@ -70,31 +70,6 @@ __device__ __forceinline__ Place place_of(const Args &a, int item) {
     return p;
 }
 
-// What differs between a pair of CTAs and one.
-template <bool PAIR>
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
-    if constexpr (PAIR)
-        tma_load_pair(dst, m, c0, c1, bar);
-    else
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                     ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar) : "memory");
-}
-template <bool PAIR>
-__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    if constexpr (PAIR) mma_pair(d, a, b, idesc, add);
-    else tc_mma_bf16(d, a, b, idesc, add);
-}
-template <bool PAIR>
-__device__ __forceinline__ void arrive_leader(uint32_t bar) {
-    if constexpr (PAIR) arrive_at_rank(map_to_rank(bar, 0));
-    else mbar_arrive(bar);
-}
-template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t bar) {
-    if constexpr (PAIR) commit_pair(bar);
-    else tc_commit(bar);
-}
-
 template <int KIND, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ Args a) {
@@ -128,14 +103,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         tma_prefetch_desc(&map_b);
     }
     if (warp == 2) {
-        if constexpr (PAIR) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                         ::"r"(smem_addr(tmem_slot)), "r"(kTmemCols) : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-        } else {
-            tmem_alloc(smem_addr(tmem_slot), kTmemCols);
-            tmem_relinquish();
-        }
+        unit_tmem_alloc<PAIR>(smem_addr(tmem_slot), kTmemCols);
     }
     tc_fence_before();
     __syncthreads();
@@ -164,16 +132,16 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 const uint32_t bar = PAIR ? map_to_rank(full + 8 * s, 0) : full + 8 * s, dst = base + s * kStageBytes, db = dst + 2 * kBoxBytes;
                 const int k = st * kStep;
                 if (a.a_turned) {
-                    load_box<PAIR>(dst, &map_a, ci, k, bar);
-                    load_box<PAIR>(dst + kBoxBytes, &map_a, ci + 64, k, bar);
+                    unit_load<PAIR>(dst, &map_a, ci, k, bar);
+                    unit_load<PAIR>(dst + kBoxBytes, &map_a, ci + 64, k, bar);
                 } else {
-                    load_box<PAIR>(dst, &map_a, k, ci, bar);
+                    unit_load<PAIR>(dst, &map_a, k, ci, bar);
                 }
                 if (a.b_turned) {
-                    load_box<PAIR>(db, &map_b, cj, k, bar);
-                    if (half == kHalf) load_box<PAIR>(db + kBoxBytes, &map_b, cj + 64, k, bar);
+                    unit_load<PAIR>(db, &map_b, cj, k, bar);
+                    if (half == kHalf) unit_load<PAIR>(db + kBoxBytes, &map_b, cj + 64, k, bar);
                 } else {
-                    load_box<PAIR>(db, &map_b, k, cj, bar);
+                    unit_load<PAIR>(db, &map_b, k, cj, bar);
                 }
             }
         }
@@ -216,16 +184,16 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     const uint64_t db = a.b_turned ? desc_columns(sb) : desc_rows(sb), nb = a.b_turned ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
                     for (int q = 0; q < kStep / 16; ++q)
-                        multiply<PAIR>(acc, da + q * na, db + q * nb, a.idesc, st > c0 || q > 0);
-                    commit<PAIR>(empty + 8 * s);
+                        unit_multiply<PAIR>(acc, da + q * na, db + q * nb, a.idesc, st > c0 || q > 0);
+                    unit_commit<PAIR>(empty + 8 * s);
                 }
-                if (ok) commit<PAIR>(acc_full + 8 * buf);
+                if (ok) unit_commit<PAIR>(acc_full + 8 * buf);
             }
         }
         if (!ok) {
             // the products issued end before tensor memory is freed
             int gave_up = 0;
-            commit<PAIR>(drain);
+            unit_commit<PAIR>(drain);
             mbar_wait(drain, 0, &gave_up, a.timeout_ns, a.status, SITE_P_DRAIN);
         }
     } else if (warp >= 2) {
@@ -288,7 +256,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 if (last) break;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_leader<PAIR>(acc_empty + 8 * buf);
+                if (lane == 0) unit_arrive<PAIR>(acc_empty + 8 * buf);
             }
             if (!ok) break;
 // the sums' registers are free from here on: a piece's operands are on their way while the one before is finished
@@ -323,7 +291,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_leader<PAIR>(acc_empty + 8 * (done & 1));
+            if (lane == 0) unit_arrive<PAIR>(acc_empty + 8 * (done & 1));
             ++done;
         }
     }
@@ -332,12 +300,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     __syncthreads();
     __syncwarp();
     if constexpr (PAIR) cluster_sync();
-    if (warp == 2) {
-        if constexpr (PAIR)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
-        else
-            tmem_dealloc(tmem, kTmemCols);
-    }
+    if (warp == 2) unit_tmem_free<PAIR>(tmem, kTmemCols);
 }
 
 // The splits' sums in their order, then the epilogue. VEC elements of a row a thread (8 where every row

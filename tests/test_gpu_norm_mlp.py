@@ -189,3 +189,36 @@ def test_refusals():
         ops.mhc_orthogonalize(leaf)
     with torch.no_grad():
         assert torch.equal(ops.mhc_linear(x, leaf), ops.mhc_linear(x, w))
+
+
+def test_more_than_2_to_31_elements():
+    """Offsets past 32 bits: the last rows of outputs of 2.3e9 elements, and of inputs of as many."""
+    from tests import layers_ref as ref
+    T, K, N = 280000, 64, 8200
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(T, K, generator=g, device="cuda").to(BF)
+    w = torch.randn(N, K, generator=g, device="cuda").to(BF)
+    out = ops.mhc_linear(x, w)
+    assert out.numel() > 1 << 31
+    at = torch.tensor([0, 1, T // 2, T - 257, T - 1], device="cuda")
+    want, _, e, _ = ref.linear(x[at], w, None, None, "none")
+    ref.within(out[at], want, e)
+    # read again, a row of 8200 a row of the summed axis and of the output
+    d_x = ops.mhc_linear_dx(out, w)
+    want, e = ref.linear_dx(out[at], w, None, "none")
+    ref.within(d_x[at], want, e)
+    d_w, d_b = ops.mhc_linear_dw(out, x, bias=True)
+    cols = [0, N - 1]
+    want = out[:, cols].double().t() @ x.double()
+    # one chain of 512 products of a piece and the pieces' sums: 2^-21 of the sizes
+    size = out[:, cols].double().abs().t() @ x.double().abs()
+    assert ((d_w[cols].double() - want).abs() <= 2.0 ** -20 * size).all()
+    want = out[:, cols].double().sum(0)
+    assert ((d_b[cols].double() - want).abs() <= T * ref.U * out[:, cols].double().abs().sum(0)).all()
+    n, stats = ops.mhc_layer_norm(out)
+    want, _, e, _ = ref.layer_norm(out[at], None, None, 1e-5)
+    ref.within(n[at], want, e)
+    del d_x
+    d = ops.mhc_layer_norm_backward(n, out, stats, None, bias=False).d_x
+    ref.within(d[at], *ref.layer_norm_backward(n[at], out[at], stats[at], None, None)["d_x"])
+    assert ops.mhc_get_device_status() == 0

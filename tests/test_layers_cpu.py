@@ -162,12 +162,12 @@ def test_refusals_of_layer_norm(lib):
         assert back(**bad) == 3, bad
     for bad in (dict(H=0), dict(H=65537), dict(ot=2), dict(t=1, ot=0)):
         assert back(**bad) == 4, bad
-    for bad in (dict(d=None), dict(x=None), dict(st=None), dict(dx=None), dict(ws=None)):
+    for bad in (dict(d=None), dict(x=None), dict(st=None), dict(dx=None), dict(T=400, ws=None)):
         assert back(**bad) == 1, bad
     for bad in (dict(d=A + 1), dict(dx=A * 6 + 1), dict(dw=A * 7 + 2), dict(db=A * 8 + 1), dict(ws=A * 9 + 8), dict(st=A * 3 + 2)):
         assert back(**bad) == 2, bad
-    assert back(wsb=64) == 8
-    for bad in (dict(dx=A), dict(dx=A * 2), dict(dx=A * 5 + 2), dict(dx=A * 5, rs=72), dict(dw=A * 8), dict(ws=A * 7)):
+    assert back(T=400, wsb=64) == 8
+    for bad in (dict(dx=A), dict(dx=A * 2), dict(dx=A * 5 + 2), dict(dx=A * 5, rs=72), dict(dw=A * 8), dict(T=400, ws=A * 7)):
         assert back(**bad) == 5, bad
 
 
@@ -199,7 +199,8 @@ def test_workspace_sizes(lib):
     assert ops.linear_dx_workspace_bytes(8, 100, 7, True, False) == 100 * 8 * 2 // 256 * 256 + 256
     assert ops.linear_dw_workspace_bytes(3, 8, 8, False, False) == 512
     assert ops.layer_norm_backward_workspace_bytes(0, 64) == 0
-    assert ops.layer_norm_backward_workspace_bytes(5, 64) >= 2 * 64 * 4
+    assert ops.layer_norm_backward_workspace_bytes(5, 64) == 0         # one CTA adds them up
+    assert ops.layer_norm_backward_workspace_bytes(500, 64) >= 2 * 64 * 4
     assert ops.layer_norm_backward_workspace_bytes(1 << 20, 64) == ops.layer_norm_backward_workspace_bytes(1 << 30, 64)
     assert ops.orthogonalize_workspace_bytes(0, 64, 64) == 0 and ops.orthogonalize_workspace_bytes(3, 128, 2048) == 0
     big = ops.orthogonalize_workspace_bytes(1, 2048, 4096)
