@@ -61,7 +61,7 @@ __device__ __forceinline__ void load_rows(Raw &r, const Piece &p, const uint8_t 
             r.w[4 * k] = t.x, r.w[4 * k + 1] = t.y, r.w[4 * k + 2] = t.z, r.w[4 * k + 3] = t.w;
         }
 }
-// runs: the source's rows lie on the boundaries of runs of 8; others are read a row a lane, by the words that hold them.
+// runs: the source's rows lie on the boundaries of runs of 8; others are read a column a lane, turned or not.
 __device__ __forceinline__ void load_raw(Raw &r, const Piece &p, const void *from, int dtype, long long row0, long long pitch, bool runs) {
     const int size = dtype == MHC_F32 ? 4 : 2, lane = threadIdx.x & 31;
     if (p.wide) {
@@ -71,17 +71,8 @@ __device__ __forceinline__ void load_raw(Raw &r, const Piece &p, const void *fro
             else load_rows<4>(r, p, first, pitch * 2);
             return;
         }
-        if (lane >= p.rows) return;
-        const uintptr_t addr = reinterpret_cast<uintptr_t>(first) + lane * pitch * size, end = addr + static_cast<uintptr_t>(p.columns) * size;
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-            if (8 * c >= 32 * size || 8 * c >= p.columns * size) break;
-            uint64_t v[2];
-            load_words<2>(addr + 8 * c, end, v);
-            r.w[2 * c] = static_cast<uint32_t>(v[0]), r.w[2 * c + 1] = static_cast<uint32_t>(v[0] >> 32);
-            r.w[2 * c + 2] = static_cast<uint32_t>(v[1]), r.w[2 * c + 3] = static_cast<uint32_t>(v[1] >> 32);
-        }
-        return;
+        if (lane >= p.columns) return;
+        row0 += lane;
     }
     const long long step = here(pitch);
     if (size == 4) {
@@ -112,6 +103,12 @@ __device__ __forceinline__ void spread_rows(Raw &r, uint32_t buf) {
         r.w[4 * k] = t.x, r.w[4 * k + 1] = t.y, r.w[4 * k + 2] = t.z, r.w[4 * k + 3] = t.w;
     }
 }
+__device__ __forceinline__ void st_shared_u32(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 // Value e of it.
 __device__ __forceinline__ float raw_at(const Raw &r, bool, int e, const float *) { return __uint_as_float(r.w[e]); }
 __device__ __forceinline__ float raw_at(const Raw &r, bool wide, int e, const __nv_bfloat16 *) {
@@ -124,18 +121,29 @@ __device__ __forceinline__ float raw_at(const Raw &r, bool wide, int e, const __
 // f(e, the value) for each of the 32.
 template <class F>
 __device__ __forceinline__ void each_raw(Raw &r, bool wide, int dtype, bool runs, uint32_t buf, F &&f) {
+    const int lane = threadIdx.x & 31;
     if (wide && runs) {
         if (dtype == MHC_F32) spread_rows<8>(r, buf);
         else spread_rows<4>(r, buf);
     }
     with_type(dtype, [&](auto tag) {
-        if (wide) {
+        if (wide && runs) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) f(e, raw_at(r, true, e, tag));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) f(e, raw_at(r, false, e, tag));
+            return;
         }
+        if (wide) {
+            // from a column a lane to a row a lane
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) st_shared_u32(buf + (e * 32 + (lane ^ e)) * 4, __float_as_uint(raw_at(r, false, e, tag)));
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f(e, __uint_as_float(ld_shared_u32(buf + (lane * 32 + (e ^ lane)) * 4)));
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f(e, raw_at(r, false, e, tag));
     });
 }
 // A row a lane, in words, to whole rows.

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_rows_kernel(const LayerNormArgs
             Run o;
 #pragma unroll
             for (int q = 0; q < 4; ++q) o.p[q] = fma2(mul2(v[r].p[q], splat2(rstd)), w.p[q], b.p[q]);
-            ln_store<RUNS>(out, c, a.H, o);
+            ln_store<RUNS>(out, c, a.H, o, a.out_runs);
         }
     }
 }
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_ring_kernel(const LayerNormAr
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[r].p[q] = fma2(v[r].p[q], w.p[q], b.p[q]);
             }
-            ln_store<RUNS>(out, c, a.H, v[r]);
+            ln_store<RUNS>(out, c, a.H, v[r], a.out_runs);
         }
     }
 }
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_loop_kernel(const LayerNormArgs
             const Run w = ln_param<false>(a.w, a.w_dtype, c, a.H, 1.f), b = ln_param<false>(a.b, a.b_dtype, c, a.H, 0.f);
 #pragma unroll
             for (int q = 0; q < 4; ++q) v.p[q] = fma2(mul2(add2(v.p[q], splat2(-mean)), splat2(rstd)), w.p[q], b.p[q]);
-            ln_store<false>(out, c, a.H, v);
+            ln_store<false>(out, c, a.H, v, a.out_runs);
         }
     }
 }
@@ -195,7 +195,8 @@ constexpr int kRingSmem = 220 * 1024;
 // Many rows: a CTA an SM, as many groups as 768 threads give, as many stages as shared memory holds, at most 4 a group.
 template <class TX, class TO>
 cudaError_t launch_ring(const LayerNormArgs &a, bool runs, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
-    const int need = (a.H + 255) / 256, R = need <= 6 ? 2 : 4, warps = (need + R - 1) / R;
+    // four runs a thread leave too few registers for rows that are shifted into place
+    const int need = (a.H + 255) / 256, R = need <= 6 || !runs ? 2 : 4, warps = (need + R - 1) / R;
     int groups = (kRingThreads - 32) / (32 * warps);
     if (groups > 8) groups = 8;
     LnRing ring = {};
@@ -208,7 +209,7 @@ cudaError_t launch_ring(const LayerNormArgs &a, bool runs, int sms, unsigned int
     ring.timeout_ns = wait_timeout_ns();
     const int smem = 512 + par + groups * ring.stages * ring.place[kLnArrays];
     auto *const kern = R == 2 ? (runs ? ln_ring_kernel<TX, TO, 2, true> : ln_ring_kernel<TX, TO, 2, false>)
-                              : (runs ? ln_ring_kernel<TX, TO, 4, true> : ln_ring_kernel<TX, TO, 4, false>);
+                              : ln_ring_kernel<TX, TO, 4, true>;
     static std::atomic<uint64_t> done[4];
     if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kRingSmem, &done[2 * (R == 2) + runs])) return e;
     const long long blocks = (a.T + groups - 1) / groups;

@@ -40,9 +40,10 @@ __device__ __forceinline__ Run ln_load(const T *row, int c, int H) {
     if constexpr (RUNS) return load8(row + c);
     else return load8_any(row, c, H);
 }
+// runs: the row that is written lies on them even where those that are read do not.
 template <bool RUNS, class T>
-__device__ __forceinline__ void ln_store(T *row, int c, int H, const Run &r) {
-    if constexpr (RUNS) store8(row + c, r);
+__device__ __forceinline__ void ln_store(T *row, int c, int H, const Run &r, bool runs) {
+    if (RUNS || runs) store8(row + c, r);
     else store8_any(row + c, r, (reinterpret_cast<uintptr_t>(row + c) & (2 * sizeof(T) - 1)) == 0, H - c < 8 ? H - c : 8);
 }
 // 8 parameters from column c on; `otherwise` where there are none.

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_rows_kernel(const LayerNor
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 o.p[q] = fma2(fma2(h[r].p[q], splat2(m2), add2(e[r].p[q], splat2(m1))), splat2(rstd), add.p[q]);
-            ln_store<RUNS>(out, c, a.H, o);
+            ln_store<RUNS>(out, c, a.H, o, a.out_runs);
         }
     }
     if (!want) return;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNor
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 o.p[q] = fma2(fma2(h[r].p[q], splat2(m2), add2(e[r].p[q], splat2(m1))), splat2(rstd), add.p[q]);
-            ln_store<RUNS>(out, c, a.H, o);
+            ln_store<RUNS>(out, c, a.H, o, a.out_runs);
         }
         if (!SELF && a.d_residual) {
             __syncwarp();
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_loop_kernel(const LayerNor
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 o.p[q] = fma2(fma2(h.p[q], splat2(m2), fma2(e.p[q], w.p[q], splat2(m1))), splat2(rstd), add.p[q]);
-            ln_store<false>(out, c, a.H, o);
+            ln_store<false>(out, c, a.H, o, a.out_runs);
         }
     }
 }

@@ -244,7 +244,7 @@ mhc_status mhc_layer_norm(const void *x, int64_t x_stride, mhc_dtype dtype, int6
     unsigned int *status = nullptr;
     if (int r = require_device(&sms, &status)) return static_cast<mhc_status>(r);
     const LayerNormArgs a = {tokens, hidden, x, w, b, tokens == 1 ? hidden : x_stride, dtype, w_dtype, b_dtype, out_dtype, eps,
-                             1.f / static_cast<float>(hidden), out, stats};
+                             1.f / static_cast<float>(hidden), out, stats, hidden % 8 == 0 && on_runs(out, out_dtype)};
     return static_cast<mhc_status>(note_launch(launch_layer_norm(a, sms, status, pdl_enabled(), static_cast<cudaStream_t>(stream))));
 }
 
@@ -288,7 +288,8 @@ mhc_status mhc_layer_norm_backward(const void *d_out, int64_t d_out_stride, mhc_
     const bool one = tokens == 1;
     const LayerNormBackArgs a = {tokens, hidden, d_out, x, d_residual, w, one ? hidden : d_out_stride, one ? hidden : x_stride,
                                  one ? hidden : d_residual_stride, out_dtype, dtype, w_dtype, stats,
-                                 1.f / static_cast<float>(hidden), d_x, d_w, d_b, static_cast<float *>(workspace)};
+                                 1.f / static_cast<float>(hidden), d_x, d_w, d_b, static_cast<float *>(workspace),
+                                 hidden % 8 == 0 && on_runs(d_x, dtype)};
     return static_cast<mhc_status>(launch_layer_norm_back(a, status, pdl_enabled(), static_cast<cudaStream_t>(stream)));
 }
 

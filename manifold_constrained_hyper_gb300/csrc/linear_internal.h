@@ -80,6 +80,7 @@ struct LayerNormArgs {
     float eps, inv_h;
     void *out;
     float *stats;                                   // [T][2]: mean, rstd; or NULL
+    int out_runs;                                   // out's rows lie on the boundaries of runs of 8
 };
 cudaError_t launch_layer_norm(const LayerNormArgs &a, int sms, unsigned int *status, bool pdl, cudaStream_t s);
 
@@ -94,6 +95,7 @@ struct LayerNormBackArgs {
     void *d_x;
     float *d_w, *d_b;                               // each or NULL
     float *sums;                                    // layer_norm_sums_bytes()
+    int out_runs;                                   // d_x's rows lie on the boundaries of runs of 8
 };
 size_t layer_norm_sums_bytes(long long T, int H);
 int launch_layer_norm_back(const LayerNormBackArgs &a, unsigned int *status, bool pdl, cudaStream_t s);
