@@ -6,8 +6,8 @@
 //   each CTA adds some rows of A over the CTAs, in their order, and writes them to all of them
 //     (distributed shared memory, a row a warp: whole lines; 16 bytes here and there took eight times as long);
 //   each CTA forms P, the same everywhere, and its columns of P X, which take X's place.
-// Two barriers of the cluster a step, some 8 us in all, where a barrier of the grid and a trip through
-// L2 after each of the three products come to 28.
+// Two barriers of the cluster a step, some 8 us in all (6 x 128 x 500: 47 us), where a barrier of the grid and a trip
+// through L2 after each of the three products come to 28 (143).
 #include <atomic>
 
 #include "epilogue.cuh"
