@@ -20,13 +20,14 @@ constexpr int kThreads = 192;                       // loads, products, four epi
 constexpr int kMaxStages = 6;
 constexpr int kStageBudget = 100 * 1024;             // two CTAs an SM: 1 x 7168 into 4096 15.6 -> 13.6 us, 1 x 2048 into 2048 10.0 -> 6.0
 constexpr int kMaxSplit = 8;
+constexpr int kChainExact = 8;
 
-enum FewSite : int { SITE_F_EMPTY = 90, SITE_F_FULL, SITE_F_ACC, SITE_F_DRAIN };
+enum FewSite : int { SITE_F_EMPTY = 90, SITE_F_FULL, SITE_F_ACC, SITE_F_DRAIN, SITE_F_ACC_EMPTY };
 
 struct FewArgs {
     int m, n, width;                // tokens, rows of weights, tokens rounded up to 16
     int steps, per, split, stages;  // steps of 64 of k, of a CTA, CTAs of a cluster
-    int chain, sums;                // steps of one sum in tensor memory, and how many such sums
+    int chain;                      // steps of one sum in tensor memory
     int tmem_cols, w_turned;
     uint32_t idesc;
     unsigned int *status;
@@ -43,8 +44,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     uint8_t *const basep = raw + (base - smem_addr(raw));
     const int stage_bytes = kWeightBytes + a.width * 128;
     const uint32_t bars = base + a.stages * stage_bytes;
-    const uint32_t full = bars, empty = bars + 8 * kMaxStages, acc_full = bars + 16 * kMaxStages, drain = acc_full + 8;
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + a.stages * stage_bytes + 16 * kMaxStages + 16);
+    const uint32_t full = bars, empty = bars + 8 * kMaxStages, acc_full = bars + 16 * kMaxStages, acc_empty = acc_full + 16,
+                   drain = acc_full + 32;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(basep + a.stages * stage_bytes + 16 * kMaxStages + 40);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     // the sums, [tokens][128], over the stages once nothing is on its way to them
     float *const sums = reinterpret_cast<float *>(basep);
@@ -58,7 +60,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
         }
-        mbar_init(acc_full, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full + 8 * b, 1);
+            mbar_init(acc_empty + 8 * b, 4);        // the epilogue warps
+        }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -106,22 +111,27 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
         }
     } else if (warp == 1 && elect_one()) {
         bool ok = true;
+        int in_chain = 0, done = 0;
         for (int it = 0; it < mine && ok; ++it) {
-            const int s = it % a.stages;
-            ok = mbar_wait(full + 8 * s, (it / a.stages) & 1, abort_flag, a.timeout_ns, a.status, SITE_F_FULL);
+            const int s = it % a.stages, buf = done & 1;
+            if (in_chain == 0) ok = mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status, SITE_F_ACC_EMPTY);
+            if (ok) ok = mbar_wait(full + 8 * s, (it / a.stages) & 1, abort_flag, a.timeout_ns, a.status, SITE_F_FULL);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sw = base + s * stage_bytes, acc = tmem + it / a.chain * a.width;
+            const uint32_t sw = base + s * stage_bytes, acc = tmem + buf * a.width;
             const uint64_t dw = a.w_turned ? desc_columns(sw) : desc_rows(sw), nw = a.w_turned ? 2048 >> 4 : 32 >> 4;
             const uint64_t dx = desc_rows(sw + kWeightBytes);
 #pragma unroll
             for (int q = 0; q < kPairStep / 16; ++q)
-                tc_mma_bf16(acc, dw + q * nw, dx + q * (32 >> 4), a.idesc, it % a.chain > 0 || q > 0);
+                tc_mma_bf16(acc, dw + q * nw, dx + q * (32 >> 4), a.idesc, in_chain > 0 || q > 0);
             tc_commit(empty + 8 * s);
+            if (++in_chain == a.chain || it + 1 == mine) {
+                tc_commit(acc_full + 8 * buf);
+                in_chain = 0;
+                ++done;
+            }
         }
-        if (ok) {
-            if (mine) tc_commit(acc_full);
-        } else {
+        if (!ok) {
             // the products issued end before tensor memory is freed
             int gave_up = 0;
             tc_commit(drain);
@@ -130,20 +140,32 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     } else if (warp >= 2) {
         const int quad = warp & 3, row = quad * 32 + lane;
         bool ok = true;
-        if (mine) ok = mbar_wait(acc_full, 0, abort_flag, a.timeout_ns, a.status, SITE_F_ACC);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
-        const int live = mine ? (mine + a.chain - 1) / a.chain : 0;
-        for (int t0 = 0; t0 < a.width && ok; t0 += 16) {
-            float v[16] = {};
-            for (int p = 0; p < live; ++p) {
+        const int live = (mine + a.chain - 1) / a.chain;
+        float v[kFewTokens / 16][16] = {};
+        for (int p = 0; p < live; ++p) {
+            const int buf = p & 1;
+            ok = mbar_wait(acc_full + 8 * buf, (p >> 1) & 1, abort_flag, a.timeout_ns, a.status, SITE_F_ACC);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < kFewTokens / 16; ++q) {
+                if (16 * q >= a.width) break;
                 uint32_t w[16];
-                tmem_ld16_now(tmem + p * a.width + t0 + (static_cast<uint32_t>(quad * 32) << 16), w);
+                tmem_ld16_now(tmem + buf * a.width + 16 * q + (static_cast<uint32_t>(quad * 32) << 16), w);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
+                for (int e = 0; e < 16; ++e) v[q][e] += __uint_as_float(w[e]);
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
+        }
+        // the last sum is there: so are all, and nothing is on its way to the stages
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sums[(t0 + e) * kRows + row] = v[e];
+        for (int q = 0; q < kFewTokens / 16; ++q) {
+            if (16 * q >= a.width || !ok) break;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sums[(16 * q + e) * kRows + row] = v[q][e];
         }
         tc_fence_before();
     }
@@ -218,11 +240,12 @@ int launch_few_tokens(const Product &p, int sms, unsigned int *status, bool pdl,
     // also where there is nothing to split, so that more CTAs finish many tokens (512 elements of a CTA at least)
     while (a.split < kMaxSplit && 2 * a.split * tiles <= 2 * sms && (a.steps >= 2 * a.split || a.m * kRows / a.split >= 1024)) a.split *= 2;
     a.per = (a.steps + a.split - 1) / a.split;
-    const int most = 512 / a.width;
-    a.chain = p.exact ? (a.per + most - 1) / most > 8 ? (a.per + most - 1) / most : 8 : a.per;
-    a.sums = (a.per + a.chain - 1) / a.chain;
+    // What an fp32 result is summed in, as in the other products: pieces of 8 steps, in two places of tensor memory in turn. At
+    // most 128 columns of it a CTA: two CTAs of different clusters lie on an SM, and one that waited for the other's
+    // columns while its own cluster waits for it would wait for ever.
+    a.chain = p.exact && a.per > kChainExact ? kChainExact : a.per;
     a.tmem_cols = 32;
-    while (a.tmem_cols < a.sums * a.width) a.tmem_cols *= 2;
+    while (a.tmem_cols < (a.per > a.chain ? 2 : 1) * a.width) a.tmem_cols *= 2;
     const int stage_bytes = kWeightBytes + a.width * 128;
     a.stages = kStageBudget / stage_bytes < kMaxStages ? kStageBudget / stage_bytes : kMaxStages;
     a.w_turned = p.b.turned;

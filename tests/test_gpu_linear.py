@@ -68,6 +68,24 @@ def test_sums_for_fp32_outputs_do_not_drift(T, K, N):
     assert float(((d.double() - want) / want).abs().max()) < 40 * 2.0 ** -24
 
 
+@pytest.mark.parametrize("T,K,N", [(64, 65536, 300), (64, 20000, 4096), (33, 65536, 4096), (2, 65528, 136)])
+def test_few_tokens_with_a_long_summed_axis_keep_fp32_sums(T, K, N):
+    """Many pieces of a sum and two CTAs on an SM, on two streams at once: each piece is off by 32 instructions of
+    2^-24 as above, and beside them stand the fp32 additions of K / 512 pieces and of at most 8 CTAs' sums."""
+    g = gen(K)
+    x = rows(g, T, K, BF).abs()
+    w = rows(g, N, K, BF).abs()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [ops.mhc_linear(x, w, dtype=FP32, stream=s) for _ in range(3) for s in (None, side)]
+    torch.cuda.synchronize()
+    want = x.double() @ w.double().t()
+    assert float(((outs[0].double() - want) / want).abs().max()) < (40 + K // 512 + 1) * 2.0 ** -24
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    d = ops.mhc_linear_dx(x, w.t().contiguous(), dtype=FP32)
+    assert float(((d.double() - want) / want).abs().max()) < (40 + K // 512 + 1) * 2.0 ** -24
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 1, 1), (1, 2048, 384), (3, 130, 4160), (17, 259, 131), (64, 640, 512), (65, 64, 64),
                                    (129, 130, 192), (300, 520, 1000), (513, 96, 2048), (700, 2050, 520)])
 @pytest.mark.parametrize("dtype,act,out,pad", [(BF, "none", None, 0), (BF, "silu", None, 0), (FP16, "gelu", FP32, 3),
