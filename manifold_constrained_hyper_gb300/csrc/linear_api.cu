@@ -213,8 +213,13 @@ mhc_status mhc_linear_dw(const void *d_out, int64_t d_out_stride, const void *x,
         operand(&p.a, &jobs[0], d_out, d_out_stride, tokens, n, true, &at);
         operand(&p.b, &jobs[1], x, x_stride, tokens, k, true, &at);
     }
-    // with a bias the copies go beside its sums
-    if (int r = d_bias ? launch_column_sums(d_out, tokens == 1 ? n : d_out_stride, dtype, tokens, n, d_bias, accumulate, jobs[0], jobs[1], sms, pdl, s)
+    // the bias's sums go beside the products, or else the copies beside them
+    const bool beside = d_bias && tokens > 0 && product_sums_rows(n, k, tokens);
+    if (beside) {
+        p.row_sums = d_bias;
+        p.add_row_sums = accumulate != 0;
+    }
+    if (int r = d_bias && !beside ? launch_column_sums(d_out, tokens == 1 ? n : d_out_stride, dtype, tokens, n, d_bias, accumulate, jobs[0], jobs[1], sms, pdl, s)
                        : copy(jobs, sms, pdl, s))
         return static_cast<mhc_status>(r);
     p.parts = product_parts_bytes(n, k, tokens) ? reinterpret_cast<float *>(at) : nullptr;

@@ -49,8 +49,12 @@ struct Product {
     Epilogue kind;
     EpilogueArgs epi;
     float *parts;                                   // of split sums, product_parts_bytes()
+    float *row_sums;                                // EPI_SUMS, a turned: [m], to take the sums over k of a's rows, or NULL
+    int add_row_sums;
 };
 size_t product_parts_bytes(long long m, int n, long long k);
+// Whether the sums over k of a's rows come cheaper beside the products than from launch_column_sums().
+bool product_sums_rows(long long m, int n, long long k);
 // An mhc_status: one launch, or two where the summed axis is split.
 int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cudaStream_t s);
 

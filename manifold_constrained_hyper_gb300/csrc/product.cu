@@ -51,6 +51,10 @@ struct Args {
     unsigned int *status;
     unsigned long long timeout_ns;
     EpilogueArgs e;
+    const void *rows;               // where the sums over k of A's rows are wanted: A [k][m], turned
+    long long row_pitch, k;
+    float *row_sums;
+    int bf16, add_row_sums;
 };
 struct Place {
     int split, ti, tj;
@@ -68,6 +72,54 @@ __device__ __forceinline__ Place place_of(const Args &a, int item) {
     p.tj = q / rows;
     p.ti = first + q - p.tj * rows;
     return p;
+}
+
+// Sums over k of A's rows (a bias's gradient), by the epilogue's warps while the first tile's products are on: a CTA takes
+// 32 of the rows, four lanes of 8, 64 of k at a time. `red`: 2 x 8 x 32 floats, the first warp's own once this returns.
+template <class T>
+__device__ __forceinline__ void sum_rows(const Args &a, float *red, int w, int lane) {
+    const T *const x = static_cast<const T *>(a.rows);
+    constexpr int kRowsAtOnce = 8 * kSumWarps;
+    const int m = static_cast<int>(a.m);
+    int turn = 0;
+    for (int first = 32 * blockIdx.x; first < m; first += 32 * gridDim.x, turn ^= 1) {
+        const int c = first + (lane & 3) * 8;
+        Run s = run_splat(0.f);
+        const T *from = x + (8 * w + (lane >> 2)) * a.row_pitch + c;
+        long long left = a.k - 8 * w - (lane >> 2);
+        // eight loads of a thread on their way at once; a run past the last column lies in its row's pitch, and is not written
+        for (; c < m && left > 0; left -= 8 * kRowsAtOnce, from += 8 * kRowsAtOnce * a.row_pitch) {
+            uint4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                v[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (left > u * kRowsAtOnce) v[u] = *reinterpret_cast<const uint4 *>(from + u * kRowsAtOnce * a.row_pitch);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const Run t = unpack8(v[u], x);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) s.p[q] = add2(s.p[q], t.p[q]);
+            }
+        }
+        float *const here = red + turn * kSumWarps * 32;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float v = run_at(s, e);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane < 4) here[w * 32 + lane * 8 + e] = v;
+        }
+        named_barrier_sync(1, kSumWarps * 32);
+        if (w == 0 && first + lane < m) {
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < kSumWarps; ++k) v += here[k * 32 + lane];
+            float *const to = a.row_sums + first + lane;
+            *to = a.add_row_sums ? *to + v : v;
+        }
+    }
+    __syncwarp();
 }
 
 template <int KIND, bool PAIR>
@@ -202,6 +254,12 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int width = a.tile_n / 2;             // the columns it sums: the tile's first or second half
         const int first = (warp - 2) / 4 * width;
         float *const piece = turn + (warp - 2) * 32 * 32;
+        if constexpr (KIND == EPI_SUMS) {
+            if (a.row_sums) {
+                if (a.bf16) sum_rows<__nv_bfloat16>(a, turn, warp - 2, lane);
+                else sum_rows<__half>(a, turn, warp - 2, lane);
+            }
+        }
         uint32_t done = 0;
         bool ok = true;
         for (int item = pair; item < a.items && ok; item += pairs) {
@@ -517,6 +575,16 @@ size_t product_parts_bytes(long long m, int n, long long k) {
     return q.splits > 1 ? static_cast<size_t>(q.splits) * m * n * 4 : 0;
 }
 
+// Up to 96 rounds of 64 of k a CTA, which the first tile's products hide, or which take less than a launch (777 x 1000 x 2048 8.9 us
+// against 11.8 by a kernel of their own, 6000 x 1000 x 1000 38.4 against 42.7, 1024 x 16384 x 128 12.3 against 24.0;
+// 4096 x 64 x 64 10.4 against 9.7). Longer ones wait behind the products' loads: 8192 x 2048 x 2048 60.9 against 54.8.
+bool product_sums_rows(long long m, int n, long long k) {
+    const Plan q = plan_of(m, n, k, true);
+    const long long items = static_cast<long long>(q.tiles_m) * q.tiles_n * q.splits, ctas = q.pair ? 2 : 1;
+    const long long grid = items * ctas < kGridCap ? items * ctas : kGridCap, groups = (m + 31) / 32;
+    return (groups + grid - 1) / grid * ((k + 63) / 64) <= 96;
+}
+
 int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
     if (p.k == 0) return launch_join<EPI_SUMS>(nullptr, 0, p, sms, pdl, s);
     const Plan q = plan_of(p.m, p.n, p.k, p.parts != nullptr);
@@ -544,6 +612,14 @@ int launch_product(const Product &p, int sms, unsigned int *status, bool pdl, cu
     a.status = status;
     a.timeout_ns = wait_timeout_ns();
     a.e = p.epi;
+    if (p.row_sums) {
+        a.rows = p.a.p;
+        a.row_pitch = p.a.pitch;
+        a.k = p.k;
+        a.row_sums = p.row_sums;
+        a.bf16 = p.bf16;
+        a.add_row_sums = p.add_row_sums;
+    }
     Epilogue kind = p.kind;
     if (q.splits > 1) {
         kind = EPI_SUMS;

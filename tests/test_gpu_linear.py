@@ -253,5 +253,29 @@ def test_rows_of_one_larger_tensor():
     ref.within(ops.mhc_linear(one, w), want, e)
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 40, 24), (511, 33, 200), (512, 4901, 64), (700, 9736, 16), (3000, 200, 136), (6144, 72, 64),
+                                   (6145, 72, 64), (70, 65531, 8)])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (8, 8), (1, 1)])
+def test_the_bias_gradient_beside_the_products_or_before_them(T, N, K, pad, offset):
+    """Columns past the last whole run and several groups of columns a CTA, on both sides of the rule; what lies between
+    the rows is not finite."""
+    g = gen(T + N)
+    flat = torch.full((T * (N + pad) + offset + 16,), float("nan"), device="cuda", dtype=BF)
+    d = flat[offset:offset + T * (N + pad)].view(T, N + pad)[:, :N]
+    d.copy_(torch.randn(T, N, generator=g, device="cuda"))
+    x = rows(g, T, K, BF)
+    d_w, d_b = ops.mhc_linear_dw(d, x, bias=True)
+    want = d.double().sum(0)
+    e = (T + 64) * ref.U * d.double().abs().sum(0)
+    ref.within(d_b, want, e)
+    ref.within(d_w, d.double().t() @ x.double(), ref.product_error(d.double().t(), x.double().t(), 64 + T // 512))
+    b0 = torch.randn(N, generator=g, device="cuda")
+    b1 = b0.clone()
+    ops.mhc_linear_dw(d, x, d_w=torch.zeros_like(d_w), d_bias=b1, accumulate=True)
+    s = want + b0.double()
+    ref.within(b1, s, e + 2 * ref.U * s.abs())
+    assert torch.equal(ops.mhc_linear_dw(d, x, bias=True)[1], d_b)
+
+
 def test_device_status_is_clean():
     assert ops.mhc_get_device_status() == 0
