@@ -10,7 +10,7 @@
 // cores; sums are fp32. Elements are at most 1 (X), about 1.5 (A) or a (P): a factor of 2^12 in all of them
 // keeps what matters of lo above fp16's smallest values, and leaves room for 16 times 1.
 //
-// By size: orthogonal_small.cu where a side is at most 128, else this file's two kernels (the norm; X in two parts) and
+// By size: orthogonal_small.cu where a side is at most 128 and the other not too long, else this file's two kernels (the norm; X in two parts) and
 // orthogonal_kernel.cu's one. 4096 x 7168 3.05 ms in a burst, 2048 x 1024 225 us, 256 x 256 118, 6 x 128 x 500 47.
 //
 // G may lie in strided rows. A tall G is not turned: its Gram matrix is X^T X, the product reading both

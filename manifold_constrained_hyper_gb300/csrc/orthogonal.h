@@ -35,7 +35,7 @@ struct NsCall {
     float *parts;
     unsigned int *counters;                         // zero
 };
-// A side of at most 128, the other of at most 2048: all of it by clusters of CTAs.
+// A side of at most 128 and the other of at most 2048 (64: 4096, 32: 8192): all of it by clusters of CTAs.
 bool ns_small_fits(int m, int n);
 int launch_ns_small(const OrthogonalArgs &a, const NsPolynomial &f, unsigned int *status, bool pdl, cudaStream_t s);
 int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s);

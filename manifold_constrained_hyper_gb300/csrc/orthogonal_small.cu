@@ -1,7 +1,9 @@
 // The whole orthogonalised update of matrices with a side of at most 128, a cluster of CTAs a matrix and
 // one launch: no product leaves the SMs. X lies with its short side as rows (128 of them, zeros past the
 // end), 64 or 128 of its columns in each CTA's shared memory, in two fp16 parts and in the layout that the
-// tensor core reads, both along k (for A = X X^T) and across it (for P X). Per step:
+// tensor core reads, both along k (for A = X X^T) and across it (for P X). A side of at most 64, or 32, leaves room for
+// two, or four, stretches of the columns, one below the other: A is the sum of what comes out on the diagonal, and stands there
+// as often (1024 x 64 60 -> 44 us, a batch of 46 237 -> 98, 32 x 8192 147 -> 51). Per step:
 //   each CTA's part of A over its columns, in fp32, to its shared memory;
 //   each CTA adds some rows of A over the CTAs, in their order, and writes them to all of them
 //     (distributed shared memory, a row a warp: whole lines; 16 bytes here and there took eight times as long);
@@ -34,6 +36,7 @@ struct SmallArgs {
     int dtype, tall;
     long long row_stride, batch_stride;
     int p, q, width, ctas, steps, last_passes;
+    int stretch;                    // columns of a stretch
     float eps, of_sum, of_square, of_a, shift, of_unit;     // of_a: what is added of A; shift: what A has on its diagonal
     void *out;
     int out_dtype;
@@ -74,6 +77,8 @@ __device__ __forceinline__ uint64_t desc_across(uint32_t addr) {
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
+// SHIFT: log2 of the rows of a stretch, 5 to 7.
+template <int SHIFT>
 __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_constant__ SmallArgs a) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -85,7 +90,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     double *const squares = reinterpret_cast<double *>(basep + kSmallBars + 32);      // [0]: of the CTA; then of the warps
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = blockIdx.x % a.ctas, batch = blockIdx.x / a.ctas, j0 = rank * a.width;
-    const int live = min(a.width, a.q - j0);        // of the CTA's columns; not above 0 in a last CTA
+    const int live = min(a.width, a.stretch - j0);  // of the CTA's columns of every stretch
+    constexpr int rows_p = 1 << SHIFT;
+    // element (r, j) of the CTA's X: row r & (rows_p - 1) of the matrix, and this column of it, or -1
+    auto column_of = [&](int r, int j) {
+        const int c = (rows_p == kP ? 0 : (r >> SHIFT) * a.stretch) + j0 + j;
+        return (r & (rows_p - 1)) < a.p && j < live && (rows_p == kP || c < a.q) ? c : -1;
+    };
 
     if (threadIdx.x == 0) {
         mbar_init(bar, 1);
@@ -115,9 +126,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
                 float v[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const int e = e0 + k * kThreads, o = e >> shift, c = e & mask, i = a.tall ? c : o, j = a.tall ? o : c;
+                    const int e = e0 + k * kThreads, o = e >> shift, c = e & mask, r = a.tall ? c : o, j = column_of(r, a.tall ? o : c), i = r & (rows_p - 1);
                     v[k] = 0.f;
-                    if (i < a.p && j < live) v[k] = to_f32(g[a.tall ? (j0 + j) * a.row_stride + i : i * a.row_stride + j0 + j]);
+                    if (j >= 0) v[k] = to_f32(g[a.tall ? j * a.row_stride + i : i * a.row_stride + j]);
                 }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
@@ -180,6 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
             st_shared_v4(base + kXAt + 2 * kBox + run_at_box(i, c), l);
         }
     }
+    // beside the diagonal A is zero, and what follows from it too
+    if (rows_p < kP)
+        for (int u = threadIdx.x; u < 4 * kBox / 16; u += kThreads) st_shared_v4(base + kMAt + 16 * u, make_uint4(0u, 0u, 0u, 0u));
     fence_proxy_async_smem();
     __syncthreads();
 
@@ -235,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
         });
         __syncthreads();
         cluster_sync();
-        // over all columns: every ctas-th row from this CTA's on, a warp a row, four columns a lane, to every CTA
+        // over all columns: every ctas-th row from this CTA's on, a warp a row (of every stretch), four columns a lane, to every CTA
         // (two rows of a warp at a time)
-        const int next_row = a.ctas * (kThreads / 32);
-        for (int i0 = rank + a.ctas * warp; i0 < kP; i0 += 2 * next_row) {
+        const int next_row = a.ctas * (kThreads / 32), below = 4 * lane >> SHIFT << SHIFT;      // the lane's stretch
+        for (int i0 = rank + a.ctas * warp; i0 < rows_p; i0 += 2 * next_row) {
             float v[2][4] = {};
             for (int r0 = 0; r0 < a.ctas; r0 += 8) {
                 uint4 w[2][8];
@@ -246,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int r = 0; r < 8; ++r)
-                        w[k][r] = r0 + r < a.ctas && i0 + k * next_row < kP
-                                      ? load16_at_rank(base + kSumsAt + ((i0 + k * next_row) * kPitch + 4 * lane) * 4, r0 + r)
+                        w[k][r] = r0 + r < a.ctas && i0 + k * next_row < rows_p
+                                      ? load16_at_rank(base + kSumsAt + ((below + i0 + k * next_row) * kPitch + 4 * lane) * 4, r0 + r)
                                       : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -261,8 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int i = i0 + k * next_row;
-                if (i >= kP) break;
+                const int i = below + i0 + k * next_row;
+                if (i0 + k * next_row >= rows_p) break;
+                // the stretches', the same in every lane that holds them
+#pragma unroll
+                for (int o = rows_p / 4; o < 32; o <<= 1)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[k][e] += __shfl_xor_sync(0xffffffffu, v[k][e], o);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[k][e] = v[k][e] * a.of_sum + (i == 4 * lane + e ? a.shift : 0.f);
                 uint32_t h[2], l[2];
@@ -334,10 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
         T *const out = static_cast<T *>(a.out) + out_at;
 #pragma unroll 8
         for (int e = threadIdx.x; e < kP * a.width; e += kThreads) {
-            const int o = e >> shift, c = e & mask, i = a.tall ? c : o, j = a.tall ? o : c;
-            if (i < a.p && j < live)
-                out[a.tall ? static_cast<long long>(j0 + j) * a.p + i : static_cast<long long>(i) * a.q + j0 + j] =
-                    from_f32<T>(sums[i * kPitch + j] * of_out);
+            const int o = e >> shift, c = e & mask, r = a.tall ? c : o, at = a.tall ? o : c, j = column_of(r, at), i = r & (rows_p - 1);
+            if (j >= 0)
+                out[a.tall ? static_cast<long long>(j) * a.p + i : static_cast<long long>(i) * a.q + j] =
+                    from_f32<T>(sums[r * kPitch + at] * of_out);
         }
     });
     tc_fence_before();
@@ -351,7 +370,15 @@ std::atomic<int> g_ready[64];
 
 }  // namespace
 
-bool ns_small_fits(int m, int n) { return (m < n ? m : n) <= kP && (m < n ? n : m) <= kP * kMost; }
+namespace {
+int shift_of(int p) { return p <= 32 ? 5 : p <= 64 ? 6 : 7; }
+int stretch_of(int p, int q) { return (q + (kP >> shift_of(p)) - 1) / (kP >> shift_of(p)); }
+}  // namespace
+
+bool ns_small_fits(int m, int n) {
+    const int p = m < n ? m : n, q = m < n ? n : m;
+    return p <= kP && stretch_of(p, q) <= kP * kMost;
+}
 
 int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int *status, bool pdl, cudaStream_t s) {
     SmallArgs a = {};
@@ -362,8 +389,19 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
     a.batch_stride = o.batch_stride;
     a.p = a.tall ? o.n : o.m;
     a.q = a.tall ? o.m : o.n;
-    a.width = a.q <= 8 * 64 ? 64 : 128;
-    a.ctas = (a.q + a.width - 1) / a.width;
+    void (*const kernels[])(const SmallArgs) = {ns_small_kernel<5>, ns_small_kernel<6>, ns_small_kernel<7>};
+    a.stretch = stretch_of(a.p, a.q);
+    // the width by how many clusters the GPU holds at once, and by a matrix's time: 128 columns a CTA take a seventh longer than
+    // 64 in a cluster of at most 8, and less than 64 in a larger one (128 x 1024 56 us against 61; 64 x 128 x 512 112 against 238)
+    double least = 1e300;
+    for (int width : {64, 128}) {
+        const int ctas = (a.stretch + width - 1) / width, at_once = kGridCap / ctas;
+        const double cost = (width == 128 ? 1.15 : ctas <= 8 ? 1. : 1.25) * ((o.batch + at_once - 1) / at_once);
+        if (ctas > kMost || cost >= least) continue;
+        least = cost;
+        a.width = width;
+        a.ctas = ctas;
+    }
     a.steps = o.steps;
     a.last_passes = o.out_dtype == MHC_BF16 ? 1 : 3;
     a.eps = o.eps;
@@ -379,9 +417,10 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
     if (!g_ready[dev & 63].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return MHC_ERR_CUDA;
+        for (auto kern : kernels)
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+                cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+                return MHC_ERR_CUDA;
         g_ready[dev & 63].store(1, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
@@ -398,7 +437,7 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    return note_launch(cudaLaunchKernelEx(&cfg, ns_small_kernel, a));
+    return note_launch(cudaLaunchKernelEx(&cfg, kernels[shift_of(a.p) - 5], a));
 }
 
 }  // namespace mhc

@@ -45,6 +45,18 @@ def test_against_64_bits(shape, dtype, out):
     near(got, want, e)
 
 
+@pytest.mark.parametrize("shape", [(64, 4096), (4097, 64), (32, 8192), (8190, 32), (31, 8193), (33, 1025), (61, 2049), (128, 1000), (3, 2047, 127),
+                                   (40, 60, 500), (30, 700, 60), (50, 32, 129), (20, 128, 520), (7, 20, 33), (9, 63, 64)], ids=str)
+@pytest.mark.parametrize("dtype,out", [(FP32, BF), (BF, FP16)])
+def test_short_sides_in_stretches(shape, dtype, out):
+    """A side of at most 64 or 32 lies in two or four stretches of the other, whole and broken ones; batches of more clusters than
+    lie on the GPU at once."""
+    g = momentum(gen(sum(shape)), shape, dtype)
+    got = ops.mhc_orthogonalize(g, dtype=out)
+    want, e = ref.orthogonalize_error(g, 5, MUON, 1e-7, out)
+    near(got, want, e)
+
+
 @pytest.mark.parametrize("shape", [(2048, 2600), (2600, 2056), (2, 2050, 2570)], ids=str)
 @pytest.mark.parametrize("steps,out", [(2, BF), (3, FP16), (4, BF), (5, BF)])
 def test_two_steps_as_one(shape, steps, out):
