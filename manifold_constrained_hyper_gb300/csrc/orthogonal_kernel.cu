@@ -4,9 +4,11 @@
 // then adds them, in their order, for some of the tile's columns. Every wait has a limit.
 //
 // A pair forms a 256 x 256 or 256 x 128 tile, a CTA a 128 x 128 or 128 x 64 one, as the products with an epilogue do (64 of k
-// a stage, five stages, two buffers of sums in tensor memory); every operand is two fp16 parts, three products a step.
+// a stage, five stages, two buffers of sums in tensor memory). Every operand is two fp16 parts: a step of 64 is one stage of both
+// operands' hi and one of their lo, and three products (with a stage for each product hi came twice: 2048 x 1024 222 us against 203,
+// 2944 x 1760 617 against 502).
 //
-// 4096 x 7168 3.05 ms, the tensor cores at the power cap; 2048 x 1024 225 us (15 launches 450), where a
+// 4096 x 7168 2.80 ms, the tensor cores at the power cap; 2048 x 1024 203 us (15 launches 450), where a
 // product takes some 6.5 us beside its own steps: 0.7 until the first stage is there, 1.5 to 3 the epilogue, 1.3 its
 // stores until they are seen, 1.5 the barrier; split, 3 more for the parts.
 // A symmetric result's tiles left of the diagonal are not formed: those right of it are stored twice,
@@ -341,8 +343,8 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 const Place p = place_of(f, item);
                 const int s0 = p.split * f.per, s1 = s0 + f.per < f.steps ? s0 + f.per : f.steps;
                 const int ci = p.ti * kTile + static_cast<int>(rank) * kHalf, cj = p.tj * f.tile_n + static_cast<int>(rank) * half;
-                int kb = s0 / f.passes, part = s0 - f.passes * kb;
-                for (int st = s0; st < s1; ++st, ++it) {
+                const int parts = f.passes == 1 ? 1 : 2;
+                for (int st = s0 * parts; st < s1 * parts; ++st, ++it) {
                     const uint32_t s = it % kStages, turn_of = (it / kStages) & 1;
                     if (!mbar_wait(empty + 8 * s, turn_of ^ 1, abort_flag, a.timeout_ns, a.status, SITE_N_EMPTY)) {
                         ok = false;
@@ -350,8 +352,8 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     }
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kCtas * (2 * kPairBoxBytes + half * 128));
                     const uint32_t bar = PAIR ? map_to_rank(full + 8 * s, 0) : full + 8 * s, da = base + s * kStageBytes, db = da + 2 * kPairBoxBytes;
-                    const int k = kb * kPairStep;
-                    const CUtensorMap *const am = ma + (part == 2), *const bm = mb + (part == 1);
+                    const int step = parts == 1 ? st : st >> 1, part = st - step * parts, k = step * kPairStep;
+                    const CUtensorMap *const am = ma + part, *const bm = mb + part;
                     if (f.a_turned) {
                         unit_load<PAIR>(da, am, ci, k, p.batch, bar);
                         unit_load<PAIR>(da + kPairBoxBytes, am, ci + 64, k, p.batch, bar);
@@ -363,10 +365,6 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                         if (half == kHalf) unit_load<PAIR>(db + kPairBoxBytes, bm, cj + 64, k, p.batch, bar);
                     } else {
                         unit_load<PAIR>(db, bm, k, cj, p.batch, bar);
-                    }
-                    if (++part == f.passes) {
-                        part = 0;
-                        ++kb;
                     }
                 }
             }
@@ -396,18 +394,37 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     break;
                 }
                 tc_fence_after();
-                for (int st = s0; st < s1; ++st, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!mbar_wait(full + 8 * s, (it / kStages) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_FULL)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = base + s * kStageBytes, sb = sa + 2 * kPairBoxBytes;
-                    const uint64_t da = f.a_turned ? desc_columns(sa) : desc_rows(sa), db = f.b_turned ? desc_columns(sb) : desc_rows(sb);
+                for (int st = s0; st < s1; ++st) {
+                    // hi of both; then lo, and the products of hi with it
+                    uint32_t held[2], a_at[2], b_at[2];
+                    const int parts = f.passes == 1 ? 1 : 2;
 #pragma unroll
-                    for (int q = 0; q < kPairStep / 16; ++q) unit_multiply<PAIR>(acc, da + q * na, db + q * nb, f.idesc, st > s0 || q > 0);
-                    unit_commit<PAIR>(empty + 8 * s);
+                    for (int part = 0; part < 2; ++part) {
+                        if (part == parts) break;
+                        const uint32_t s = it % kStages;
+                        ok = mbar_wait(full + 8 * s, (it / kStages) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_FULL);
+                        if (!ok) break;
+                        ++it;
+                        tc_fence_after();
+                        held[part] = s;
+                        a_at[part] = base + s * kStageBytes;
+                        b_at[part] = a_at[part] + 2 * kPairBoxBytes;
+                        auto multiply = [&](uint32_t left, uint32_t right, bool add) {
+                            const uint64_t da = f.a_turned ? desc_columns(left) : desc_rows(left), db = f.b_turned ? desc_columns(right) : desc_rows(right);
+#pragma unroll
+                            for (int q = 0; q < kPairStep / 16; ++q) unit_multiply<PAIR>(acc, da + q * na, db + q * nb, f.idesc, add || q > 0);
+                        };
+                        if (part == 0) {
+                            multiply(a_at[0], b_at[0], st > s0);
+                        } else {
+                            multiply(a_at[0], b_at[1], true);
+                            multiply(a_at[1], b_at[0], true);
+                        }
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                        if (part < parts) unit_commit<PAIR>(empty + 8 * held[part]);
                 }
                 if (ok) unit_commit<PAIR>(acc_full + 8 * buf);
             }
@@ -582,8 +599,9 @@ int resident_units(int *units) {
 }
 
 // A product by `units` pairs of CTAs, or CTAs. The cheapest of both tiles' widths and of splitting or not, by what was
-// measured on one GB300: a step of 64 takes 0.33 us with a pair's 256 columns, where the tensor cores are busy, else
-// what it takes to issue and to load; finishing 64 columns of a tile by a warp 3 us; writing parts, waiting for the others' and
+// measured on one GB300: three products of 64 take 0.95 us with a pair's 256 columns, where the tensor cores are busy, else
+// what it takes to load them, more where every SM loads for several tiles in turn (3 x 1408 x 6436 by pairs' tiles 1.38 ms, by CTAs' 1.57);
+// finishing 64 columns of a tile by a warp 3 us; writing parts, waiting for the others' and
 // reading them 3.1 (256 columns 5.3), and finishing 16 columns of them 1.6.
 Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turned, bool b_turned, bool pair, int units, double *cost) {
     Phase f = {};
@@ -599,7 +617,7 @@ Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turn
     f.a_turned = a_turned;
     f.b_turned = b_turned;
     f.tiles_m = (m + rows - 1) / rows;
-    f.steps = passes * ((k + kPairStep - 1) / kPairStep);
+    f.steps = (k + kPairStep - 1) / kPairStep;
     auto tiles = [&](int tile_n) {
         const long long c = (n + tile_n - 1) / tile_n, all = f.tiles_m * c;
         return batch * (symmetric ? all - rows / tile_n * (static_cast<long long>(f.tiles_m) * (f.tiles_m - 1) / 2) : all);
@@ -608,14 +626,16 @@ Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turn
     long long count = 0;
     for (int tile_n : {rows, rows / 2}) {
         const long long c = tiles(tile_n);
-        const double step = tile_n == 256 ? 0.33 : pair ? 0.22 : tile_n == 128 ? 0.25 : 0.20;
+        const int form = tile_n == 256 ? 0 : pair ? 1 : tile_n == 128 ? 2 : 3;
+        constexpr double kOne[] = {0.33, 0.22, 0.25, 0.20}, kThree[] = {0.95, 0.52, 0.55, 0.42}, kBusy[] = {0.95, 0.62, 0.68, 0.55};
         int most = static_cast<int>(c <= units ? units / c : 1);
-        if (most > f.steps / 6) most = f.steps / 6;
+        if (most > passes * f.steps / 6) most = passes * f.steps / 6;
         if (most > tile_n / 16) most = tile_n / 16;     // each of them finishes 16 columns at least
         for (int s : {1, most}) {
             if (s < 1) continue;
             const int per = (f.steps + s - 1) / s;
-            const double rounds = static_cast<double>((c * s + units - 1) / units), work = per * step, finish = 3. * tile_n / 128;
+            const double rounds = static_cast<double>((c * s + units - 1) / units), finish = 3. * tile_n / 128;
+            const double work = per * (passes == 1 ? kOne[form] : rounds > 1. ? kBusy[form] : kThree[form]);
             const double all = s > 1 ? work + (tile_n == 256 ? 5.3 : 3.1) + 1.6 * ((tile_n / 16 + 2 * s - 1) / (2 * s))
                                      : (rounds - 1) * (work > finish ? work : finish) + work + finish;
             if (all >= best) continue;
