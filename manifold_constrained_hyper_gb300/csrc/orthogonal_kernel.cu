@@ -3,14 +3,14 @@
 // tiles split the summed axis over the CTAs; those of a tile wait for one another's parts, and each
 // then adds them, in their order, for some of the tile's columns. Every wait has a limit.
 //
-// A pair forms a 256 x 256 or 256 x 128 tile, a CTA a 128 x 128 or 128 x 64 one, as the products with an epilogue do (64 of k
+// A pair forms a 256 x 256 or 256 x 128 tile, a CTA 128 rows of 128, 64 or 32 columns, as the products with an epilogue do (64 of k
 // a stage, five stages, two buffers of sums in tensor memory). Every operand is two fp16 parts: a step of 64 is one stage of both
 // operands' hi and one of their lo, and three products (with a stage for each product hi came twice: 2048 x 1024 222 us against 203,
 // 2944 x 1760 617 against 502).
 //
-// 4096 x 7168 2.80 ms, the tensor cores at the power cap; 2048 x 1024 203 us (15 launches 450), where a
-// product takes some 6.5 us beside its own steps: 0.7 until the first stage is there, 1.5 to 3 the epilogue, 1.3 its
-// stores until they are seen, 1.5 the barrier; split, 3 more for the parts.
+// 4096 x 7168 2.80 ms, the tensor cores at the power cap; 2048 x 1024 190 us (15 launches 450), where a
+// product takes some 5.5 us beside its own steps: 0.6 until the first stage is there, 1 to 3 the epilogue, 0.4 until the
+// CTA's warps have met, 1.5 to 2.3 the barrier; split, 3 more for the parts.
 // A symmetric result's tiles left of the diagonal are not formed: those right of it are stored twice,
 // the second time a column a store, which is contiguous across a warp's lanes.
 #include <atomic>
@@ -199,31 +199,36 @@ __device__ __forceinline__ void put_lines(uint8_t *to, long long pitch_bytes, in
 __device__ __forceinline__ void put_piece(const NsArgs &a, const Target &t, int batch, int i0, int j, int width, uint32_t sums, uint32_t held) {
     const int lane = threadIdx.x & 31, i = i0 + lane;
     __syncwarp();       // the piece before has been read
-    // eight columns at a time: a short loop, whose instructions are fetched once
+    // sixteen columns at a time: a short loop, whose instructions are fetched once
 #pragma unroll 1
-    for (int c = 0; c < width; c += 8) {
-        uint4 xh, xl;
-        load_x8(xh, xl, t, i, j + c);
-        uint32_t u[8];
-        tmem_ld8_now(sums + c, u);
-        float v[8];
+    for (int c0 = 0; c0 < width; c0 += 16) {
+        uint4 xh[2], xl[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[e]);
-        const uint32_t at = held + lane * 128 + (((c >> 3) ^ (lane & 7)) << 4);
-        if (t.final) {
-            uint32_t o[4];
+        for (int k = 0; k < 2; ++k) load_x8(xh[k], xl[k], t, i, j + c0 + 8 * k);
+        uint32_t u[16];
+        tmem_ld16_now(sums + c0, u);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint64_t r = f2_pack(v[2 * q] * a.of_out, v[2 * q + 1] * a.of_out);
-                o[q] = a.out_dtype == MHC_BF16 ? bf2_pack_rn(r) : pack2(r, static_cast<const __half *>(nullptr));
+        for (int k = 0; k < 2; ++k) {
+            const int c = c0 + 8 * k;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[8 * k + e]);
+            const uint32_t at = held + lane * 128 + (((c >> 3) ^ (lane & 7)) << 4);
+            if (t.final) {
+                uint32_t o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t r = f2_pack(v[2 * q] * a.of_out, v[2 * q + 1] * a.of_out);
+                    o[q] = a.out_dtype == MHC_BF16 ? bf2_pack_rn(r) : pack2(r, static_cast<const __half *>(nullptr));
+                }
+                st_shared_v4(at, make_uint4(o[0], o[1], o[2], o[3]));
+            } else {
+                uint4 hw, lw;
+                pair8(t, i, j + c, v, xh[k], xl[k], &hw, &lw);
+                st_shared_v4(at, hw);
+                st_shared_v4(at + kOutBytes, lw);
+                if (t.mirror && i < t.m && j + c < t.n) mirror8(t, i, j + c, hw, lw);
             }
-            st_shared_v4(at, make_uint4(o[0], o[1], o[2], o[3]));
-        } else {
-            uint4 hw, lw;
-            pair8(t, i, j + c, v, xh, xl, &hw, &lw);
-            st_shared_v4(at, hw);
-            st_shared_v4(at + kOutBytes, lw);
-            if (t.mirror && i < t.m && j + c < t.n) mirror8(t, i, j + c, hw, lw);
         }
     }
     __syncwarp();
@@ -623,13 +628,17 @@ Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turn
     };
     double best = 1e300;
     long long count = 0;
-    for (int tile_n : {rows, rows / 2}) {
+    for (int tile_n : {rows, rows / 2, 32}) {
+        // 32 columns where there are few tiles, with half the epilogue of 64 (256 x 256 104 -> 95 us, 400 x 416 124 -> 112).
+        // (Read across k a tile's columns come by 64.)
+        if (tile_n == 32 && (pair || b_turned)) continue;
         const long long c = tiles(tile_n);
-        const int form = tile_n == 256 ? 0 : pair ? 1 : tile_n == 128 ? 2 : 3;
-        constexpr double kOne[] = {0.33, 0.22, 0.25, 0.20}, kThree[] = {0.95, 0.52, 0.55, 0.42}, kBusy[] = {0.95, 0.62, 0.68, 0.55};
+        const int form = tile_n == 256 ? 0 : pair ? 1 : tile_n == 128 ? 2 : tile_n == 64 ? 3 : 4;
+        constexpr double kOne[] = {0.33, 0.22, 0.25, 0.20, 0.18}, kThree[] = {0.95, 0.52, 0.55, 0.42, 0.38}, kBusy[] = {0.95, 0.62, 0.68, 0.55, 0.50};
         int most = static_cast<int>(c <= units ? units / c : 1);
         if (most > passes * f.steps / 6) most = passes * f.steps / 6;
         if (most > tile_n / 16) most = tile_n / 16;     // each of them finishes 16 columns at least
+        if (tile_n == 32) most = 1;
         for (int s : {1, most}) {
             if (s < 1) continue;
             const int per = (f.steps + s - 1) / s;
