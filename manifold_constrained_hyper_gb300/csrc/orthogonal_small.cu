@@ -25,6 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kBox = kP * 128;                      // 128 rows of 64 columns of 16 bits
 constexpr int kPitch = kP + 4;                      // floats of a row of the sums
 constexpr int kMost = 16;                           // CTAs of a cluster
+constexpr int kTmemCols = 2 * kP;
 // X hi, lo (two boxes each), A and then P hi, lo, sums
 constexpr int kXAt = 0, kMAt = 4 * kBox, kSumsAt = 8 * kBox, kSmallBars = kSumsAt + kP * kPitch * 4;
 constexpr int kSmem = kSmallBars + 256 + 1024;
@@ -103,15 +104,17 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
         *abort_flag = 0;
         fence_mbar_init();
     }
+    // After the kernel before, and half of the columns: a CTA of another kernel's cluster with little shared memory may lie on the
+    // SM, and neither may wait for the other's columns while the rest of its cluster waits for it.
+    griddep_wait();
     if (warp == 0) {
-        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_alloc(smem_addr(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    griddep_wait();
+    const uint32_t tmem = *tmem_slot;       // A, and in its place P X; P
 
     // ------------------------------------------------ X's columns, in fp32 to the sums' place, and their squares
     {
@@ -324,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
         fence_proxy_async_smem();
         __syncthreads();
         // P X, in X's place
-        multiply(tmem + 2 * kP, m, x, kP, passes, false);
+        multiply(tmem, m, x, kP, passes, false);
         if (last) break;
-        each8(tmem + 2 * kP, a.width, [&](int c, float (&v)[8]) {
+        each8(tmem, a.width, [&](int c, float (&v)[8]) {
             const uint32_t to = x + run_at_box(row, c >> 3);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= a.of_sum;
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     }
     // ------------------------------------------------ the output, through the sums' place
     const float of_out = a.of_sum * a.of_sum;
-    each8(tmem + 2 * kP, a.width, [&](int c, float (&v)[8]) {
+    each8(tmem, a.width, [&](int c, float (&v)[8]) {
         float *const to = sums + row * kPitch + c;
         *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     tc_fence_before();
     __syncthreads();
     cluster_sync();         // nothing of this CTA is read or written any more
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
 // 1: may be launched with clusters of up to 16; asked once a device.

@@ -8,7 +8,8 @@ import sys
 import pytest
 import torch
 
-from manifold_constrained_hyper_gb300 import ops
+from manifold_constrained_hyper_gb300 import ops, synth
+from tests.mhc_testlib import dev_bf16, dev_f32
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
@@ -104,6 +105,42 @@ def test_calls_at_once_on_two_streams():
         assert ops.mhc_get_device_status() == 0
         assert torch.equal(one[0], want[0]) and torch.equal(two[0], want[1])
         assert torch.equal(one[1], want[2]) and torch.equal(two[1], want[3])
+
+
+def test_calls_at_once_beside_boundaries_of_small_clusters():
+    """Clusters that share SMs: boundaries of a few tokens on two streams, projections of a few tokens and small updates on two
+    others. None holds what another's cluster waits for, and all come out as alone."""
+    d = synth.make_inputs(4, 256, seed=7)
+    dev = {k: dev_bf16(d[k]) if k in ("x", "residual") else dev_f32(d[k])
+           for k in ("x", "residual", "post", "comb", "scale", "base", "norm_w", "pre_lag", "fn")}
+    weight = ops.mhc_prepare_weight(dev["fn"])
+    g = torch.Generator(device="cuda").manual_seed(9)
+    a = torch.randn(4, 128, 500, generator=g, device="cuda")
+    x, w = (torch.randn(n, 2048, generator=g, device="cuda").to(BF) for n in (64, 1024))
+
+    def boundary():
+        return ops.mhc_boundary_fused(dev["x"], dev["residual"], dev["post"], dev["comb"], weight, dev["scale"], dev["base"],
+                                      dev["norm_w"], dev["pre_lag"])
+
+    def flat(r):
+        return list(r) if isinstance(r, tuple) else [r]
+    calls = [boundary, boundary, lambda: ops.mhc_orthogonalize(a), lambda: ops.mhc_linear(x, w, dtype=torch.float32)]
+    want = [[t.clone() for t in flat(c())] for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(4):
+        got = [None] * len(calls)
+        for _ in range(8):
+            for i, (c, s) in enumerate(zip(calls, streams)):
+                with torch.cuda.stream(s):
+                    got[i] = flat(c())
+        torch.cuda.synchronize()
+        assert ops.mhc_get_device_status() == 0
+        for one, two in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(one, two))
+        # one after another on one stream too
+        for c, two in zip(calls, want):
+            assert all(torch.equal(p, q) for p, q in zip(flat(c()), two))
 
 
 def test_two_graphs_that_share_a_workspace():
