@@ -172,6 +172,13 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     __syncwarp();
     __syncthreads();
     __syncwarp();
+    // The sums are in shared memory: no columns are held while this CTA waits for others of its cluster, which may themselves wait
+    // for columns that other kernels' clusters hold.
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, a.tmem_cols);
+    }
+    __syncwarp();
     if (a.split > 1) cluster_sync();
     // each CTA the same rows of every token
     const int rows = kRows / a.split, r0 = rank * rows;
@@ -222,7 +229,6 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     }
     __syncwarp();
     if (a.split > 1) cluster_sync();        // no CTA's sums go while another reads them
-    if (warp == 2) tmem_dealloc(tmem, a.tmem_cols);
 }
 
 std::atomic<int> g_smem[64];

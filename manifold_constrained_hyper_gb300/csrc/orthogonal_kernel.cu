@@ -32,7 +32,7 @@ constexpr int kThreads = 64 + 32 * kSumWarps;
 constexpr int kBars = 2 * kStages + 7;
 constexpr int kOutBytes = 32 * 128;                 // 32 rows of 64 columns of 16 bits, of hi or of lo
 constexpr int kSmem = kStages * kStageBytes + 1024 + 2 * kSumWarps * kOutBytes + 256;
-constexpr int kTmemCols = 512;
+constexpr int kTmemCols = 512;                      // all of it: shared memory has no room for another kernel's CTA that takes some
 constexpr int kBand = 8;
 
 enum NsSite : int { SITE_N_EMPTY = 100, SITE_N_FULL, SITE_N_ACC_EMPTY, SITE_N_ACC_FULL, SITE_N_DRAIN, SITE_N_GRID, SITE_N_GO, SITE_N_MEET, SITE_N_PARTS };

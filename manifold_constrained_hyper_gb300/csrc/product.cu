@@ -34,7 +34,7 @@ constexpr int kChainExact = 8, kChain = 64;
 constexpr int kBars = 2 * kStages + 5;
 constexpr int kTurnBytes = kSumWarps * 32 * 32 * 4;     // a piece each, to turn it or to store it by rows
 constexpr int kSmem = kStages * kStageBytes + 1024 + 256 + kTurnBytes;
-constexpr int kTmemCols = 512;
+constexpr int kTmemCols = 512;                      // all of it: shared memory has no room for another kernel's CTA that takes some
 constexpr int kBand = 8;                            // rows of tiles that are walked together
 
 enum ProductSite : int { SITE_P_EMPTY = 80, SITE_P_FULL, SITE_P_ACC_EMPTY, SITE_P_ACC_FULL, SITE_P_DRAIN };
