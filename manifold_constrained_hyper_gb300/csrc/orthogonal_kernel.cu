@@ -531,26 +531,23 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     ok = meet() && !*abort_flag;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    for (int g = p.split + f.splits * (w / 4); g < f.tile_n / 16; g += 2 * f.splits) {
-                        const int j = p.tj * f.tile_n + 16 * g;
+                    for (int g = p.split + f.splits * (w / 4); g < f.tile_n / 8; g += 2 * f.splits) {
+                        const int j = p.tj * f.tile_n + 8 * g;
                         if (j >= f.n) break;
-#pragma unroll 1
-                        for (int h = 0; h < 16; h += 8) {
-                            float v[8] = {};
-                            for (int s0 = 0; s0 < f.splits; s0 += 4) {
-                                float u[4][8];
+                        float v[8] = {};
+                        for (int s0 = 0; s0 < f.splits; s0 += 4) {
+                            float u[4][8];
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
+                            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        u[q][e] = s0 + q < f.splits ? __ldcg(parts + (s0 + q) * part_size + (16 * g + h + e) * kHalf) : 0.f;
+                                for (int e = 0; e < 8; ++e)
+                                    u[q][e] = s0 + q < f.splits ? __ldcg(parts + (s0 + q) * part_size + (8 * g + e) * kHalf) : 0.f;
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
+                            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e) v[e] += u[q][e];
-                            }
-                            put8(a, t, p.batch, i0, j + h, v, piece);
+                                for (int e = 0; e < 8; ++e) v[e] += u[q][e];
                         }
+                        put8(a, t, p.batch, i0, j, v, piece);
                     }
                 }
                 tc_fence_before();
@@ -605,8 +602,9 @@ int resident_units(int *units) {
 // A product by `units` pairs of CTAs, or CTAs. The cheapest of both tiles' widths and of splitting or not, by what was
 // measured on one GB300: three products of 64 take 0.95 us with a pair's 256 columns, where the tensor cores are busy, else
 // what it takes to load them, more where every SM loads for several tiles in turn (3 x 1408 x 6436 by pairs' tiles 1.38 ms, by CTAs' 1.57);
-// finishing 64 columns of a tile by a warp 3 us; writing parts, waiting for the others' and
-// reading them 3.1 (256 columns 5.3), and finishing 16 columns of them 1.6.
+// finishing 64 columns of a tile by a warp 3 us; writing parts and waiting for the others'
+// 3.1 (256 columns 5.3), and finishing 8 columns of s parts 0.4 + 0.1 s. (By 16 columns, with half as many parts: 5331 x 149 142 us
+// against 124, 628 x 392 129 against 116.)
 Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turned, bool b_turned, bool pair, int units, double *cost) {
     Phase f = {};
     const bool symmetric = role != R_APPLY;
@@ -637,14 +635,14 @@ Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turn
         constexpr double kOne[] = {0.33, 0.22, 0.25, 0.20, 0.18}, kThree[] = {0.95, 0.52, 0.55, 0.42, 0.38}, kBusy[] = {0.95, 0.62, 0.68, 0.55, 0.50};
         int most = static_cast<int>(c <= units ? units / c : 1);
         if (most > passes * f.steps / 6) most = passes * f.steps / 6;
-        if (most > tile_n / 16) most = tile_n / 16;     // each of them finishes 16 columns at least
+        if (most > tile_n / 8) most = tile_n / 8;       // each of them finishes 8 columns at least
         if (tile_n == 32) most = 1;
         for (int s : {1, most}) {
             if (s < 1) continue;
             const int per = (f.steps + s - 1) / s;
             const double rounds = static_cast<double>((c * s + units - 1) / units), finish = 3. * tile_n / 128;
             const double work = per * (passes == 1 ? kOne[form] : rounds > 1. ? kBusy[form] : kThree[form]);
-            const double all = s > 1 ? work + (tile_n == 256 ? 5.3 : 3.1) + 1.6 * ((tile_n / 16 + 2 * s - 1) / (2 * s))
+            const double all = s > 1 ? work + (tile_n == 256 ? 5.3 : 3.1) + (0.4 + 0.1 * s) * ((tile_n / 8 + 2 * s - 1) / (2 * s))
                                      : (rounds - 1) * (work > finish ? work : finish) + work + finish;
             if (all >= best) continue;
             best = all;
