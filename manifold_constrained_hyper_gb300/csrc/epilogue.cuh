@@ -232,6 +232,88 @@ __device__ __forceinline__ void finish_piece(const Piece &p, const EpilogueArgs 
     }
     store_piece(p, e.out, e.out_dtype, row0, n, v, buf);
 }
+// A wide piece of plain sums, sixteen columns at a time (weight gradients: 128 tokens, 4096 x 7168 38.9 -> 34.1 us, 1024, 4096 x 4096 38.2 -> 36.5;
+// the projections' epilogue by 32 columns unrolled is 1 to 2 % faster). Between the loop and memory lie whole rows in buf; what
+// the sums are added to lies there where the result goes.
+template <int PER_ROW>
+__device__ __forceinline__ void rows_to_buf(const Raw &r, uint32_t buf) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < PER_ROW; ++k)
+        st_shared_v4(buf + buf_at<PER_ROW>(lane / PER_ROW + k * (32 / PER_ROW), lane % PER_ROW),
+                     make_uint4(r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]));
+}
+template <int PER_ROW>
+__device__ __forceinline__ void buf_to_rows(const Piece &p, uint8_t *to, long long pitch_bytes, uint32_t buf) {
+    const int lane = threadIdx.x & 31, c = lane % PER_ROW;
+    constexpr int kRowsAtOnce = 32 / PER_ROW, kSize = PER_ROW == 8 ? 4 : 2;
+    __syncwarp();
+    const long long step = here(pitch_bytes * kRowsAtOnce);
+    uint8_t *q = to + lane / PER_ROW * pitch_bytes + 16 * c;
+#pragma unroll
+    for (int k = 0; k < PER_ROW; ++k, q += step) {
+        const int row = lane / PER_ROW + k * kRowsAtOnce;
+        const uint4 t = ld_shared_v4(buf + buf_at<PER_ROW>(row, c));
+        if (row < p.rows && c * 16 < p.columns * kSize) *reinterpret_cast<uint4 *>(q) = t;
+    }
+    __syncwarp();
+}
+// Eight columns of the lane's row in buf, as type T.
+template <class T>
+__device__ __forceinline__ Run buf_load(uint32_t buf, int c, const T *tag) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (sizeof(T) == 4) {
+        const uint4 a = ld_shared_v4(buf + buf_at<8>(lane, c >> 2)), b = ld_shared_v4(buf + buf_at<8>(lane, (c >> 2) + 1));
+        const float f[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+                            __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
+        return run_of(f);
+    } else {
+        return unpack8(ld_shared_v4(buf + buf_at<4>(lane, c >> 3)), tag);
+    }
+}
+template <class T>
+__device__ __forceinline__ void buf_store(uint32_t buf, int c, const float *v, T *tag) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (sizeof(T) == 4) {
+        st_shared_v4(buf + buf_at<8>(lane, c >> 2), make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+        st_shared_v4(buf + buf_at<8>(lane, (c >> 2) + 1), make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+    } else {
+        st_shared_v4(buf + buf_at<4>(lane, c >> 3), make_uint4(pack2(f2_pack(v[0], v[1]), tag), pack2(f2_pack(v[2], v[3]), tag),
+                                                              pack2(f2_pack(v[4], v[5]), tag), pack2(f2_pack(v[6], v[7]), tag)));
+    }
+}
+// sums: the piece's in tensor memory; load16(address, values)
+template <class Load>
+__device__ __forceinline__ void finish_sums(const Piece &p, const EpilogueArgs &e, long long row0, int n, uint32_t sums, const Raw &r, uint32_t buf,
+                                            Load &&load16) {
+    with_type(e.out_dtype, [&](auto tag) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
+        constexpr int kPerRow = sizeof(T) == 4 ? 8 : 4;
+        __syncwarp();
+        if (e.accumulate) {
+            rows_to_buf<kPerRow>(r, buf);
+            __syncwarp();
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < 32; c0 += 16) {
+            uint32_t u[16];
+            load16(sums + c0, u);
+            float v[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(u[q]);
+#pragma unroll
+            for (int h = 0; h < 16; h += 8) {
+                if (e.accumulate) {
+                    const Run x = buf_load(buf, c0 + h, tag);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[h + q] += run_at(x, q);
+                }
+                buf_store(buf, c0 + h, v + h, static_cast<T *>(nullptr));
+            }
+        }
+        buf_to_rows<kPerRow>(p, static_cast<uint8_t *>(e.out) + row0 * static_cast<long long>(sizeof(T)), n * static_cast<long long>(sizeof(T)), buf);
+    });
+}
 // One element on any boundary.
 template <int KIND>
 __device__ __forceinline__ void finish_element(const EpilogueArgs &e, long long i, long long at, int j, float x) {

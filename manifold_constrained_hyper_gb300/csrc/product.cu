@@ -325,13 +325,20 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             for (int c = 0; c < width; c += 32) {
                 const int j = j0 + c;
                 if (j >= a.n) break;
-                uint32_t v[32];
-                tmem_ld32_now(part + c, v);
                 Raw next = {};
                 float next_bias = 0.f;
                 if (c + 32 < width && j + 32 < a.n) ahead(next, next_bias, j + 32);
+                if constexpr (KIND == EPI_SUMS) {
+                    if (wide) {
+                        finish_sums(piece_at(j), a.e, row + j, a.n, part + c, extra, buf, [](uint32_t at, uint32_t (&u)[16]) { tmem_ld16_now(at, u); });
+                        extra = next;
+                        continue;
+                    }
+                }
+                uint32_t v[32];
+                tmem_ld32_now(part + c, v);
                 float f[32];
-                if (wide) {
+                if (KIND != EPI_SUMS && wide) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
                 } else {
