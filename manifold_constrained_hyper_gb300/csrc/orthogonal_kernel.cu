@@ -138,7 +138,7 @@ struct Target {
     __half *hi, *lo;
     long long pitch;
     float unit;
-    const __half *x_hi, *x_lo;      // what is added, times of_x, and of_unit on the diagonal; or NULL
+    const __half *x_hi, *x_lo;      // what is added, times of_x, and of_unit on the diagonal; or NULL (x_lo alone: x is held as hi alone)
     float of_x, of_unit;            // of_unit: where there is no x too
     bool mirror, final, one;        // one: hi alone, rounded
     int m, n;
@@ -149,7 +149,7 @@ __device__ __forceinline__ void load_x8(uint4 &h, uint4 &l, const Target &t, int
     if (!t.x_hi || i >= t.m || j >= t.n) return;
     const long long at = static_cast<long long>(i) * t.pitch + j;
     h = __ldcg(reinterpret_cast<const uint4 *>(t.x_hi + at));
-    l = __ldcg(reinterpret_cast<const uint4 *>(t.x_lo + at));
+    if (t.x_lo) l = __ldcg(reinterpret_cast<const uint4 *>(t.x_lo + at));
 }
 // Eight sums of row i from column j on in two parts.
 __device__ __forceinline__ void pair8(const Target &t, int i, int j, const float *v, const uint4 &xh, const uint4 &xl, uint4 *hi, uint4 *lo) {
@@ -477,12 +477,13 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 t.pitch = to_x ? a.x_pitch : a.p_pitch;
                 t.unit = f.of_sum;
                 t.x_hi = f.add < 0 ? nullptr : a.mat[f.add][0] + at;
-                t.x_lo = f.add < 0 ? nullptr : a.mat[f.add][1] + at;
                 t.of_x = f.of_add;
                 t.of_unit = f.of_unit;
                 t.mirror = f.symmetric && j0 >= (p.ti + 1) * kTile;
                 t.final = final;
                 t.one = a.phase[kPhases - 1].passes == 1 && ph + 4 >= phases;   // what the last step reads
+                // the last step's A was stored as hi alone: its lo is an earlier step's, or nobody's
+                t.x_lo = f.add < 0 || t.one ? nullptr : a.mat[f.add][1] + at;
                 t.m = f.m;
                 t.n = f.n;
                 ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_ACC_FULL);
