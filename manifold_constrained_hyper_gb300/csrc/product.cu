@@ -526,7 +526,7 @@ struct Plan {
 // The cheapest form, by what was measured on one GB300: a step of 64 takes 0.33 us where a pair's 256 x 256
 // products keep the tensor cores busy, else what it takes to issue and to load; a tile's epilogue runs
 // under the next tile's products, the last one's alone; splitting the summed axis costs writing and reading
-// the parts in fp32 and a launch.
+// the parts in fp32 and a launch. k > 0.
 Plan plan_of(long long m, int n, long long k, bool may_split) {
     struct Form {
         bool pair;
@@ -577,7 +577,7 @@ int launch_join(const float *parts, int splits, const Product &p, int sms, bool 
 }  // namespace
 
 size_t product_parts_bytes(long long m, int n, long long k) {
-    if (m <= 0) return 0;
+    if (m <= 0 || k <= 0) return 0;     // a sum over nothing is written by the joining kernel alone
     const Plan q = plan_of(m, n, k, true);
     return q.splits > 1 ? static_cast<size_t>(q.splits) * m * n * 4 : 0;
 }
