@@ -10,7 +10,7 @@ constexpr float kNsScale = 4096.f;                  // what every matrix is held
 constexpr int kNsMostCtas = 152;                    // that share a product, at most an item each, or a pair of them
 // Scratch of the products: parts of split sums ([CTAs][tile columns, 256 at most][128]), and counters.
 constexpr size_t kNsPartsBytes = static_cast<size_t>(kNsMostCtas) * 256 * 128 * 4;
-constexpr size_t kNsCounters = 32 + 13 * kNsMostCtas;
+constexpr size_t kNsCounters = 32 + 10 * kNsMostCtas;
 
 // a I + b A + c A A = c (A + h I)^2 + (a - c h^2) I with h = b / 2c: A is kept with h on its diagonal, and is not
 // read again. Where c h^2 is far above the coefficients that would cancel, and b A is added instead.

@@ -45,14 +45,15 @@ enum NsRole : int { R_GRAM, R_SQUARE, R_APPLY };
 struct Phase {
     int role;                       // GRAM: of X with itself; SQUARE: of two matrices; APPLY: of one with X
     int a, b, out, add;             // matrices; add: what is added times of_add (-1: nothing)
-    int m, n, tiles_m, tiles_n, tile_n, steps, passes, splits, per, items;
+    int m, n, tiles_m, tiles_n, tile_n, steps, splits, per, items;
     int symmetric, ratio, a_turned, b_turned;       // ratio: of a tile's rows to its columns
     uint32_t idesc;
     float of_sum, of_add, of_unit;  // of_unit: on the diagonal
 };
-constexpr int kPairPhases = 7, kStepPhases = 3, kPhases = kPairPhases + 2 * kStepPhases;
+constexpr int kPairPhases = 7, kStepPhases = 3, kPhases = kPairPhases + kStepPhases;
+static_assert(kNsCounters == 32 + kPhases * kNsMostCtas, "a counter for each tile of each phase");
 struct NsArgs {
-    // two steps as one (`pairs` times), a step (`singles` times), the last step
+    // two steps as one (`pairs` times), then a step (`singles` times, once at least)
     Phase phase[kPhases];
     int pairs, singles;
     int wide;                       // X is the second operand where it is applied to, else the first
@@ -84,11 +85,9 @@ __device__ __forceinline__ Step step_of(const NsArgs &a, int ph) {
         return s;
     }
     ph -= in_pairs;
-    const int step = ph / kStepPhases;
-    const bool last = step == a.singles;
-    s.round = last ? 0 : step;
-    s.phase = kPairPhases + (last ? kStepPhases : 0) + ph - step * kStepPhases;
-    s.x = (a.pairs + step) & 1;
+    s.round = ph / kStepPhases;
+    s.phase = kPairPhases + ph - s.round * kStepPhases;
+    s.x = (a.pairs + s.round) & 1;
     return s;
 }
 
@@ -138,9 +137,9 @@ struct Target {
     __half *hi, *lo;
     long long pitch;
     float unit;
-    const __half *x_hi, *x_lo;      // what is added, times of_x, and of_unit on the diagonal; or NULL (x_lo alone: x is held as hi alone)
+    const __half *x_hi, *x_lo;      // what is added, times of_x, and of_unit on the diagonal; or NULL
     float of_x, of_unit;            // of_unit: where there is no x too
-    bool mirror, final, one;        // one: hi alone, rounded
+    bool mirror, final;
     int m, n;
 };
 // 8 columns of a row of x.
@@ -149,7 +148,7 @@ __device__ __forceinline__ void load_x8(uint4 &h, uint4 &l, const Target &t, int
     if (!t.x_hi || i >= t.m || j >= t.n) return;
     const long long at = static_cast<long long>(i) * t.pitch + j;
     h = __ldcg(reinterpret_cast<const uint4 *>(t.x_hi + at));
-    if (t.x_lo) l = __ldcg(reinterpret_cast<const uint4 *>(t.x_lo + at));
+    l = __ldcg(reinterpret_cast<const uint4 *>(t.x_lo + at));
 }
 // Eight sums of row i from column j on in two parts.
 __device__ __forceinline__ void pair8(const Target &t, int i, int j, const float *v, const uint4 &xh, const uint4 &xl, uint4 *hi, uint4 *lo) {
@@ -163,7 +162,7 @@ __device__ __forceinline__ void pair8(const Target &t, int i, int j, const float
         if (t.of_unit != 0.f) r = add2(r, f2_pack(i == j + 2 * q ? t.of_unit : 0.f, i == j + 2 * q + 1 ? t.of_unit : 0.f));
         // hi: the leading 11 bits, cut, not rounded (two masks where a conversion back would take four
         // times as long); lo, up to 2^-10 of it, holds 11 more
-        const uint64_t h = t.one ? r : r & 0xFFFFE000FFFFE000ull;
+        const uint64_t h = r & 0xFFFFE000FFFFE000ull;
         hw[q] = pack2(h, tag);
         lw[q] = pack2(fma2(h, splat2(-1.f), r), tag);
     }
@@ -179,7 +178,7 @@ __device__ __forceinline__ void mirror8(const Target &t, int i, int j, const uin
     for (int q = 0; q < 8; ++q, h += step, l += step) {
         if (j + q >= t.n) break;
         *h = static_cast<uint16_t>(hw[q >> 1] >> (q & 1) * 16);
-        if (!t.one) *l = static_cast<uint16_t>(lw[q >> 1] >> (q & 1) * 16);
+        *l = static_cast<uint16_t>(lw[q >> 1] >> (q & 1) * 16);
     }
 }
 // The warp's 32 x 64 elements of 16 bits at `held` (a row a 128-byte line, its 16 bytes c at c ^ (row & 7)) to whole lines.
@@ -240,7 +239,7 @@ __device__ __forceinline__ void put_piece(const NsArgs &a, const Target &t, int 
     }
     const long long at = static_cast<long long>(i0) * t.pitch + j;
     put_lines(reinterpret_cast<uint8_t *>(t.hi + at), t.pitch * 2, rows, columns, held);
-    if (!t.one) put_lines(reinterpret_cast<uint8_t *>(t.lo + at), t.pitch * 2, rows, columns, held + kOutBytes);
+    put_lines(reinterpret_cast<uint8_t *>(t.lo + at), t.pitch * 2, rows, columns, held + kOutBytes);
 }
 // Columns [j, j + 8) of the warp's 32 rows from i0 on, a row a lane; `piece`: 32 x 9 floats of the warp.
 __device__ __forceinline__ void put8(const NsArgs &a, const Target &t, int batch, int i0, int j, float (&v)[8], float *piece) {
@@ -252,7 +251,7 @@ __device__ __forceinline__ void put8(const NsArgs &a, const Target &t, int batch
         pair8(t, i, j, v, xh, xl, &hw, &lw);
         const long long at = static_cast<long long>(i) * t.pitch + j;
         *reinterpret_cast<uint4 *>(t.hi + at) = hw;
-        if (!t.one) *reinterpret_cast<uint4 *>(t.lo + at) = lw;
+        *reinterpret_cast<uint4 *>(t.lo + at) = lw;
         if (t.mirror) mirror8(t, i, j, hw, lw);
         return;
     }
@@ -296,7 +295,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
     constexpr int kCtas = PAIR ? 2 : 1, kTile = kCtas * kHalf;
     const uint32_t rank = PAIR ? cluster_rank() : 0;
     const int unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
-    const int phases = kPairPhases * a.pairs + kStepPhases * (a.singles + 1);
+    const int phases = kPairPhases * a.pairs + kStepPhases * a.singles;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -348,8 +347,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 const Place p = place_of(f, item);
                 const int s0 = p.split * f.per, s1 = s0 + f.per < f.steps ? s0 + f.per : f.steps;
                 const int ci = p.ti * kTile + static_cast<int>(rank) * kHalf, cj = p.tj * f.tile_n + static_cast<int>(rank) * half;
-                const int parts = f.passes == 1 ? 1 : 2;
-                for (int st = s0 * parts; st < s1 * parts; ++st, ++it) {
+                for (int st = 2 * s0; st < 2 * s1; ++st, ++it) {
                     const uint32_t s = it % kStages, turn_of = (it / kStages) & 1;
                     if (!mbar_wait(empty + 8 * s, turn_of ^ 1, abort_flag, a.timeout_ns, a.status, SITE_N_EMPTY)) {
                         ok = false;
@@ -357,7 +355,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     }
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, kCtas * (2 * kPairBoxBytes + half * 128));
                     const uint32_t bar = PAIR ? map_to_rank(full + 8 * s, 0) : full + 8 * s, da = base + s * kStageBytes, db = da + 2 * kPairBoxBytes;
-                    const int step = parts == 1 ? st : st >> 1, part = st - step * parts, k = step * kPairStep;
+                    const int part = st & 1, k = (st >> 1) * kPairStep;
                     const CUtensorMap *const am = ma + part, *const bm = mb + part;
                     if (f.a_turned) {
                         unit_load<PAIR>(da, am, ci, k, p.batch, bar);
@@ -402,10 +400,8 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 for (int st = s0; st < s1; ++st) {
                     // hi of both; then lo, and the products of hi with it
                     uint32_t held[2], a_at[2], b_at[2];
-                    const int parts = f.passes == 1 ? 1 : 2;
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
-                        if (part == parts) break;
                         const uint32_t s = it % kStages;
                         ok = mbar_wait(full + 8 * s, (it / kStages) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_FULL);
                         if (!ok) break;
@@ -428,8 +424,7 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                     }
                     if (!ok) break;
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        if (part < parts) unit_commit<PAIR>(empty + 8 * held[part]);
+                    for (int part = 0; part < 2; ++part) unit_commit<PAIR>(empty + 8 * held[part]);
                 }
                 if (ok) unit_commit<PAIR>(acc_full + 8 * buf);
             }
@@ -477,13 +472,11 @@ ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a)
                 t.pitch = to_x ? a.x_pitch : a.p_pitch;
                 t.unit = f.of_sum;
                 t.x_hi = f.add < 0 ? nullptr : a.mat[f.add][0] + at;
+                t.x_lo = f.add < 0 ? nullptr : a.mat[f.add][1] + at;
                 t.of_x = f.of_add;
                 t.of_unit = f.of_unit;
                 t.mirror = f.symmetric && j0 >= (p.ti + 1) * kTile;
                 t.final = final;
-                t.one = a.phase[kPhases - 1].passes == 1 && ph + 4 >= phases;   // what the last step reads
-                // the last step's A was stored as hi alone: its lo is an earlier step's, or nobody's
-                t.x_lo = f.add < 0 || t.one ? nullptr : a.mat[f.add][1] + at;
                 t.m = f.m;
                 t.n = f.n;
                 ok = mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, abort_flag, 2 * a.timeout_ns, a.status, SITE_N_ACC_FULL);
@@ -606,7 +599,7 @@ int resident_units(int *units) {
 // finishing 64 columns of a tile by a warp 3 us; writing parts and waiting for the others'
 // 3.1 (256 columns 5.3), and finishing 8 columns of s parts 0.4 + 0.1 s. (By 16 columns, with half as many parts: 5331 x 149 142 us
 // against 124, 628 x 392 129 against 116.)
-Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turned, bool b_turned, bool pair, int units, double *cost) {
+Phase phase_of(int role, int m, int n, int k, int batch, bool a_turned, bool b_turned, bool pair, int units, double *cost) {
     Phase f = {};
     const bool symmetric = role != R_APPLY;
     const int rows = pair ? 2 * kHalf : kHalf;
@@ -615,7 +608,6 @@ Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turn
     f.of_sum = 1.f / kNsScale;
     f.m = m;
     f.n = n;
-    f.passes = passes;
     f.symmetric = symmetric;
     f.a_turned = a_turned;
     f.b_turned = b_turned;
@@ -633,16 +625,16 @@ Phase phase_of(int role, int m, int n, int k, int batch, int passes, bool a_turn
         if (tile_n == 32 && (pair || b_turned)) continue;
         const long long c = tiles(tile_n);
         const int form = tile_n == 256 ? 0 : pair ? 1 : tile_n == 128 ? 2 : tile_n == 64 ? 3 : 4;
-        constexpr double kOne[] = {0.33, 0.22, 0.25, 0.20, 0.18}, kThree[] = {0.95, 0.52, 0.55, 0.42, 0.38}, kBusy[] = {0.95, 0.62, 0.68, 0.55, 0.50};
+        constexpr double kThree[] = {0.95, 0.52, 0.55, 0.42, 0.38}, kBusy[] = {0.95, 0.62, 0.68, 0.55, 0.50};
         int most = static_cast<int>(c <= units ? units / c : 1);
-        if (most > passes * f.steps / 6) most = passes * f.steps / 6;
+        if (most > f.steps / 2) most = f.steps / 2;
         if (most > tile_n / 8) most = tile_n / 8;       // each of them finishes 8 columns at least
         if (tile_n == 32) most = 1;
         for (int s : {1, most}) {
             if (s < 1) continue;
             const int per = (f.steps + s - 1) / s;
             const double rounds = static_cast<double>((c * s + units - 1) / units), finish = 3. * tile_n / 128;
-            const double work = per * (passes == 1 ? kOne[form] : rounds > 1. ? kBusy[form] : kThree[form]);
+            const double work = per * (rounds > 1. ? kBusy[form] : kThree[form]);
             const double all = s > 1 ? work + (tile_n == 256 ? 5.3 : 3.1) + (0.4 + 0.1 * s) * ((tile_n / 8 + 2 * s - 1) / (2 * s))
                                      : (rounds - 1) * (work > finish ? work : finish) + work + finish;
             if (all >= best) continue;
@@ -668,10 +660,6 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     const int p = c.m < c.n ? c.m : c.n, q = c.m < c.n ? c.n : c.m;
     const bool wide = c.m <= c.n;
     NsArgs a = {};
-    // The last step of a bf16 result takes hi alone (11 bits): what is lost there is amplified once, by at most a, and
-    // comes to 0.2 to 1.4e-3 of the result (worst where an eighth of the directions is strong and the rest 0.003 of them),
-    // beside the 1.7e-3 of its rounding; fp16 rounds 2e-4. One step earlier it would come to 2.5e-3.
-    const int last_passes = c.out_dtype == MHC_BF16 ? 1 : 3;
     // Two steps as one, X <- (P1 P0) X with A1 = P0 P0 A: two products of X less, three of matrices [p][p] more. The product
     // of two P has to stay below 16. 4096 x 7168: 17 % fewer operations; small matrices are bound by the number of products.
     double largest = 0.;
@@ -687,16 +675,16 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     double cost[2][3];
     Phase forms[2][3];
     for (int k = 0; k < 2; ++k) {
-        forms[k][0] = phase_of(R_GRAM, p, p, q, c.batch, 3, !wide, !wide, k, units[k], &cost[k][0]);
-        forms[k][1] = phase_of(R_SQUARE, p, p, p, c.batch, 3, false, false, k, units[k], &cost[k][1]);
-        forms[k][2] = phase_of(R_APPLY, c.m, c.n, p, c.batch, 3, false, wide, k, units[k], &cost[k][2]);
+        forms[k][0] = phase_of(R_GRAM, p, p, q, c.batch, !wide, !wide, k, units[k], &cost[k][0]);
+        forms[k][1] = phase_of(R_SQUARE, p, p, p, c.batch, false, false, k, units[k], &cost[k][1]);
+        forms[k][2] = phase_of(R_APPLY, c.m, c.n, p, c.batch, false, wide, k, units[k], &cost[k][2]);
     }
     const bool pair = cost[1][0] + cost[1][1] + cost[1][2] <= cost[0][0] + cost[0][1] + cost[0][2];
     const int ctas = pair ? 2 : 1, places = units[pair];
     const Phase gram = forms[pair][0], square = forms[pair][1], apply = forms[pair][2];
     const bool two = p >= 2048 && q >= p + p / 4 && largest <= 3.8 && square.tile_n == apply.tile_n;
     a.pairs = two ? (c.steps - 1) / 2 : 0;
-    a.singles = c.steps - 1 - 2 * a.pairs;
+    a.singles = c.steps - 2 * a.pairs;
     auto poly = [&](Phase f, int out, const NsPolynomial &n) {
         f.a = f.b = M_A;
         f.out = out;
@@ -721,34 +709,11 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     *f++ = poly(square, M_R, plain);
     *f++ = times(square, M_R, M_P, M_T);
     *f++ = times(apply, M_T, M_T, 0);
-    for (int last = 0; last < 2; ++last) {
-        const int passes = last ? last_passes : 3;
-        double ignored;
-        Phase g = last ? phase_of(R_GRAM, p, p, q, c.batch, passes, !wide, !wide, pair, places, &ignored) : gram;
-        Phase s2 = last ? phase_of(R_SQUARE, p, p, p, c.batch, passes, false, false, pair, places, &ignored) : square;
-        const Phase ap = last ? phase_of(R_APPLY, c.m, c.n, p, c.batch, passes, false, wide, pair, places, &ignored) : apply;
-        g = times(g, 0, 0, M_A);
-        g.of_unit = complete.shift * kNsScale;
-        s2 = poly(s2, M_P, complete);
-        *f++ = g;
-        *f++ = s2;
-        *f++ = times(ap, M_P, M_P, 0);
-    }
-    // one load map a matrix and operand: the phases that share one have tiles of one width
-    for (Phase &g : a.phase)
-        if (g.role == R_GRAM ? g.tile_n != gram.tile_n : g.role == R_SQUARE ? g.tile_n != square.tile_n : g.tile_n != apply.tile_n) {
-            const int at = static_cast<int>(&g - a.phase);
-            const Phase &like = g.role == R_GRAM ? gram : g.role == R_SQUARE ? square : apply;
-            Phase n = like;
-            n.steps = g.steps;
-            n.passes = g.passes;
-            n.per = (g.steps + like.splits - 1) / like.splits;
-            n.splits = (g.steps + n.per - 1) / n.per;
-            n.items = like.items / like.splits * n.splits;
-            n.a = g.a, n.b = g.b, n.out = g.out, n.add = g.add;
-            n.of_sum = g.of_sum, n.of_add = g.of_add, n.of_unit = g.of_unit;
-            a.phase[at] = n;
-        }
+    Phase shifted = times(gram, 0, 0, M_A);
+    shifted.of_unit = complete.shift * kNsScale;
+    *f++ = shifted;
+    *f++ = poly(square, M_P, complete);
+    *f++ = times(apply, M_P, M_P, 0);
     for (int k = 0; k < 2; ++k) {
         a.x[0][k] = c.x[0][k];
         a.x[1][k] = c.x[1][k];

@@ -36,7 +36,7 @@ struct SmallArgs {
     const void *g;
     int dtype, tall;
     long long row_stride, batch_stride;
-    int p, q, width, ctas, steps, last_passes;
+    int p, q, width, ctas, steps;
     int stretch;                    // columns of a stretch
     float eps, of_sum, of_square, of_a, shift, of_unit;     // of_a: what is added of A; shift: what A has on its diagonal
     void *out;
@@ -58,18 +58,18 @@ __device__ __forceinline__ void store8_at_rank(uint32_t addr, uint32_t rank, uin
 __device__ __forceinline__ uint32_t run_at_box(int row, int c) {
     return (c >> 3) * kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
-// Two values as hi (cut, or with `one` rounded, and then all there is) and lo.
-__device__ __forceinline__ void two_parts(float v0, float v1, bool one, uint32_t *hi, uint32_t *lo) {
+// Two values as hi (cut) and lo.
+__device__ __forceinline__ void two_parts(float v0, float v1, uint32_t *hi, uint32_t *lo) {
     const __half *const tag = nullptr;
-    const uint64_t r = f2_pack(v0, v1), h = one ? r : r & 0xFFFFE000FFFFE000ull;
+    const uint64_t r = f2_pack(v0, v1), h = r & 0xFFFFE000FFFFE000ull;
     *hi = pack2(h, tag);
     *lo = pack2(fma2(h, splat2(-1.f), r), tag);
 }
-__device__ __forceinline__ void two_parts(const float (&v)[8], bool one, uint4 *hi, uint4 *lo) {
-    two_parts(v[0], v[1], one, &hi->x, &lo->x);
-    two_parts(v[2], v[3], one, &hi->y, &lo->y);
-    two_parts(v[4], v[5], one, &hi->z, &lo->z);
-    two_parts(v[6], v[7], one, &hi->w, &lo->w);
+__device__ __forceinline__ void two_parts(const float (&v)[8], uint4 *hi, uint4 *lo) {
+    two_parts(v[0], v[1], &hi->x, &lo->x);
+    two_parts(v[2], v[3], &hi->y, &lo->y);
+    two_parts(v[4], v[5], &hi->z, &lo->z);
+    two_parts(v[6], v[7], &hi->w, &lo->w);
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 // The columns' descriptor, the next 64 columns a box of 128 rows further on.
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = v[e] * first * second;
             uint4 h, l;
-            two_parts(v, a.steps == 1 && a.last_passes == 1, &h, &l);
+            two_parts(v, &h, &l);
             st_shared_v4(base + kXAt + run_at_box(i, c), h);
             st_shared_v4(base + kXAt + 2 * kBox + run_at_box(i, c), l);
         }
@@ -205,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     const uint32_t square = idesc | (static_cast<uint32_t>(kP >> 3) << 17), across = idesc | (1u << 16) | (static_cast<uint32_t>(a.width >> 3) << 17);
     uint32_t turns = 0;
     // hi hi, hi lo and lo hi, one after another into the same sums; B along k, or across it
-    auto multiply = [&](uint32_t acc, uint32_t left, uint32_t right, int k, int passes, bool along) {
+    auto multiply = [&](uint32_t acc, uint32_t left, uint32_t right, int k, bool along) {
         if (warp == 0 && elect_one()) {
             tc_fence_after();
-            for (int part = 0; part < passes; ++part) {
+            for (int part = 0; part < 3; ++part) {
                 const uint32_t l = left + (part == 2 ? 2 * kBox : 0), r = right + (part == 1 ? 2 * kBox : 0);
                 for (int q = 0; q < k; q += 16) {
                     const uint32_t inside = (q >> 6) * kBox + (q & 63) * 2;
@@ -241,10 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     };
 
     for (int step = 0; step < a.steps; ++step) {
-        const bool last = step + 1 == a.steps, one = last && a.last_passes == 1, next_one = step + 2 == a.steps && a.last_passes == 1;
-        const int passes = one ? 1 : 3;
         // A, over this CTA's columns
-        multiply(tmem, x, x, a.width, passes, true);
+        multiply(tmem, x, x, a.width, true);
         each8(tmem, kP, [&](int c, float (&v)[8]) {
             float *const to = sums + row * kPitch + c;
             *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
@@ -288,12 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[k][e] = v[k][e] * a.of_sum + (i == 4 * lane + e ? a.shift : 0.f);
                 uint32_t h[2], l[2];
-                two_parts(v[k][0], v[k][1], one, &h[0], &l[0]);
-                two_parts(v[k][2], v[k][3], one, &h[1], &l[1]);
+                two_parts(v[k][0], v[k][1], &h[0], &l[0]);
+                two_parts(v[k][2], v[k][3], &h[1], &l[1]);
                 const uint32_t to = m + run_at_box(i, lane >> 1) + (lane & 1) * 8;
                 for (int r = 0; r < a.ctas; ++r) {
                     store8_at_rank(to, r, h[0], h[1]);
-                    if (!one) store8_at_rank(to + 2 * kBox, r, l[0], l[1]);
+                    store8_at_rank(to + 2 * kBox, r, l[0], l[1]);
                 }
             }
         }
@@ -303,14 +301,14 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
         fence_proxy_async_all();
         __syncthreads();
         // P, in A's place
-        multiply(tmem + kP, m, m, kP, passes, true);
+        multiply(tmem + kP, m, m, kP, true);
         each8(tmem + kP, kP, [&](int c, float (&v)[8]) {
             const uint32_t to = m + run_at_box(row, c >> 3);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = v[e] * a.of_square + (row == c + e ? a.of_unit : 0.f);
             if (a.of_a != 0.f) {
                 const __half *const tag = nullptr;
-                const uint4 h = ld_shared_v4(to), l = one ? make_uint4(0u, 0u, 0u, 0u) : ld_shared_v4(to + 2 * kBox);
+                const uint4 h = ld_shared_v4(to), l = ld_shared_v4(to + 2 * kBox);
                 const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -320,23 +318,23 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
                 }
             }
             uint4 h, l;
-            two_parts(v, one, &h, &l);
+            two_parts(v, &h, &l);
             st_shared_v4(to, h);
-            if (!one) st_shared_v4(to + 2 * kBox, l);
+            st_shared_v4(to + 2 * kBox, l);
         });
         fence_proxy_async_smem();
         __syncthreads();
         // P X, in X's place
-        multiply(tmem, m, x, kP, passes, false);
-        if (last) break;
+        multiply(tmem, m, x, kP, false);
+        if (step + 1 == a.steps) break;
         each8(tmem, a.width, [&](int c, float (&v)[8]) {
             const uint32_t to = x + run_at_box(row, c >> 3);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= a.of_sum;
             uint4 h, l;
-            two_parts(v, next_one, &h, &l);
+            two_parts(v, &h, &l);
             st_shared_v4(to, h);
-            if (!next_one) st_shared_v4(to + 2 * kBox, l);
+            st_shared_v4(to + 2 * kBox, l);
         });
         fence_proxy_async_smem();
         __syncthreads();
@@ -406,7 +404,6 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
         a.ctas = ctas;
     }
     a.steps = o.steps;
-    a.last_passes = o.out_dtype == MHC_BF16 ? 1 : 3;
     a.eps = o.eps;
     a.of_sum = 1.f / kNsScale;
     a.of_square = f.of_square / kNsScale;

@@ -43,5 +43,31 @@ def test_polynomials_that_are_not_completed(shape, steps, coeffs, out):
     assert torch.equal(got, ops.mhc_orthogonalize(g, steps, coeffs, dtype=out))
 
 
+@pytest.mark.parametrize("shape", GENERAL + [(96, 200), (2, 40, 700), (300, 30), (2048, 2600)], ids=str)
+@pytest.mark.parametrize("steps,coeffs", [(1, MUON), (2, MUON), (5, MUON), (1, (3.0, -30.0, 2.0)), (1, (3.0, -16.0, 1.0)), (2, (3.0, -16.0, 1.0)),
+                                          (1, (9.85, -8.8, 0.0)), (1, (2.13, 8.66, -0.83)), (3, (1.5, -0.5, 0.0))])
+def test_a_bf16_result_is_the_fp16_one_rounded(shape, steps, coeffs):
+    """Products do not know the type of the result, so either is a rounding of the same value: off by at most half a step, 2^-8
+    and 2^-11 of itself, or 2^-25 below fp16's smallest normal values."""
+    g = momentum(gen(sum(shape) + steps), shape, FP32)
+    bf, half = (ops.mhc_orthogonalize(g, steps, coeffs, dtype=t).double() for t in (BF, FP16))
+    assert torch.isfinite(half).all()
+    assert ((bf - half).abs() <= half.abs() * (2.0 ** -8 + 2.0 ** -11) * (1 + 2.0 ** -10) + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("shape", [(96, 200), (257, 600), (600, 257), (3, 150, 260)], ids=str)
+@pytest.mark.parametrize("steps,coeffs", [(1, (3.0, -30.0, 2.0)), (1, (3.0, -16.0, 1.0)), (2, (3.0, -16.0, 1.0)), (3, (2.0, -1.5, 0.5))])
+@pytest.mark.parametrize("out", [BF, FP16])
+def test_coefficients_that_all_but_cancel(shape, steps, coeffs, out):
+    """c (b / 2c)^2 far above a: what A has on its diagonal cancels in P, 112 beside 3. Rounding takes at most half a step of each
+    element, so of the norm too. The tensor cores cut up to 2^-24 of that 112 with each of the 12 instructions for 64 of the
+    summed axis, 1.4e-4 of P for 260 of it, and the 22 bits of A leave less: together below a fifth of fp16's half step beside
+    the half that its rounding takes at most on average."""
+    g = torch.randn(*shape, generator=gen(steps), device="cuda")
+    got = ops.mhc_orthogonalize(g, steps, coeffs, dtype=out)
+    want = ref.orthogonalize(g, steps, coeffs, 1e-7)
+    assert float((got.double() - want).norm() / want.norm()) < 1.2 * torch.finfo(out).eps / 2
+
+
 def test_device_status_is_clean():
     assert ops.mhc_get_device_status() == 0
