@@ -20,7 +20,11 @@ constexpr int kThreads = 192;                       // loads, products, four epi
 constexpr int kMaxStages = 6;
 constexpr int kStageBudget = 100 * 1024;             // two CTAs an SM: 1 x 7168 into 4096 15.6 -> 13.6 us, 1 x 2048 into 2048 10.0 -> 6.0
 constexpr int kMaxSplit = 8;
-constexpr int kChainExact = 8;
+// Steps of one sum in tensor memory, as in the other products. What an instruction cuts adds up where the products have one sign: 8 steps of
+// an fp32 result lose 9e-7 of it (fp16 operands 2.8e-6, their products having more bits to be cut), 64 of a 16-bit one some 8 times that, a
+// twentieth of fp16's half step. (Without a limit 65536 of k lose 4e-4, four fifths of it, and are no faster: 16 x 20000 into 20000
+// 129.6 us, by 64 130.1.)
+constexpr int kChainExact = 8, kChain = 64;
 
 enum FewSite : int { SITE_F_EMPTY = 90, SITE_F_FULL, SITE_F_ACC, SITE_F_DRAIN, SITE_F_ACC_EMPTY };
 
@@ -246,10 +250,11 @@ int launch_few_tokens(const Product &p, int sms, unsigned int *status, bool pdl,
     // also where there is nothing to split, so that more CTAs finish many tokens (512 elements of a CTA at least)
     while (a.split < kMaxSplit && 2 * a.split * tiles <= 2 * sms && (a.steps >= 2 * a.split || a.m * kRows / a.split >= 1024)) a.split *= 2;
     a.per = (a.steps + a.split - 1) / a.split;
-    // What an fp32 result is summed in, as in the other products: pieces of 8 steps, in two places of tensor memory in turn. At
+    // Longer sums go in pieces through two places of tensor memory in turn. At
     // most 128 columns of it a CTA: two CTAs of different clusters lie on an SM, and one that waited for the other's
     // columns while its own cluster waits for it would wait for ever.
-    a.chain = p.exact && a.per > kChainExact ? kChainExact : a.per;
+    const int most = p.exact ? kChainExact : kChain;
+    a.chain = a.per > most ? most : a.per;
     a.tmem_cols = 32;
     while (a.tmem_cols < (a.per > a.chain ? 2 : 1) * a.width) a.tmem_cols *= 2;
     const int stage_bytes = kWeightBytes + a.width * 128;

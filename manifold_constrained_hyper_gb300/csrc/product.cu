@@ -29,7 +29,8 @@ constexpr int kStages = 6;
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 64 + 32 * kSumWarps;       // loads, products, epilogue
 // Steps that tensor memory adds up by itself: the tensor cores cut what an addition shifts out, and a
-// chain of 64 steps drifts by 4e-6 of the result, one of 8 by 4e-7. The epilogue adds the pieces in fp32.
+// chain of 64 steps drifts by 4e-6 of the result, one of 8 by 4e-7 (fp16 operands, whose products have more bits to be cut, by 1e-5 and
+// 1.2e-6). The epilogue adds the pieces in fp32.
 constexpr int kChainExact = 8, kChain = 64;
 constexpr int kBars = 2 * kStages + 5;
 constexpr int kTurnBytes = kSumWarps * 32 * 32 * 4;     // a piece each, to turn it or to store it by rows

@@ -1,0 +1,49 @@
+"""Edges of the layers beside a boundary on the GPU that their own files leave out."""
+import pytest
+import torch
+
+from manifold_constrained_hyper_gb300 import ops
+from tests import layers_ref as ref
+from tests.test_gpu_linear import BF, FP16, FP32, gen, rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from manifold_constrained_hyper_gb300 import build
+    build.build()
+    ops.load()
+
+
+def half_ulp(t, value):
+    """Half a step of type t in each value's own binade (normal values)."""
+    return torch.exp2(torch.floor(torch.log2(value.abs()))) * torch.finfo(t).eps / 2
+
+
+@pytest.mark.parametrize("T,K,N", [(3, 65536, 19500), (64, 30000, 19500), (2, 65528, 136)])
+@pytest.mark.parametrize("dtype", [BF, FP16])
+def test_few_tokens_with_a_long_summed_axis_keep_sums_of_16_bit_results(T, K, N, dtype):
+    """Products of one sign, so that what the tensor cores cut adds up: pieces of 64 steps, 256 instructions, and the fp32 additions
+    of K / 4096 pieces and of at most 8 CTAs' sums. 19500 columns leave nothing to split. An instruction adds 16 products to the sum
+    and cuts each of the 17 terms below one and the same bit. bf16 products, 16 bits far below the sum, leave little there: 2^-24 of
+    the sum in all, as for the fp32 results elsewhere. fp16 products have 22 bits, so that each of them is cut, by half of that bit
+    on average and all of it at most: fp32 results of the same products, in pieces of 32 instructions, are 2.8e-6 too small on average, so
+    an instruction cuts 1.5 x 2^-24 on average and twice that, below 2^-22, at most. (One piece of 65536 products came to 4e-4.)"""
+    g = gen(K)
+    x = rows(g, T, K, dtype).abs()
+    w = torch.empty(N, K, dtype=dtype, device="cuda")
+    for i in range(0, N, 1000):
+        w[i:i + 1000] = torch.randn(min(1000, N - i), K, generator=g, device="cuda").abs_() / K
+    out = ops.mhc_linear(x, w)
+    d = ops.mhc_linear_dx(x, w[:256].t().contiguous()) if N > 256 else None
+    rel = (256 * (4 if dtype == FP16 else 1) + K // 4096 + 1 + 8) * 2.0 ** -24
+    for i in range(0, N, 1000):
+        want = x.double() @ w[i:i + 1000].double().t()
+        assert ((out[:, i:i + 1000].double() - want).abs() <= half_ulp(dtype, want * (1 + rel)) + rel * want).all()
+        if i == 0 and d is not None:
+            assert ((d.double() - want[:, :256]).abs() <= half_ulp(dtype, want[:, :256] * (1 + rel)) + rel * want[:, :256]).all()
+
+
+def test_device_status_is_clean():
+    assert ops.mhc_get_device_status() == 0
