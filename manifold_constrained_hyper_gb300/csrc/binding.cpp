@@ -670,7 +670,7 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject * {
         const at::Tensor d_out = tensor(a[0], "d_out"), x = tensor(a[1], "x"), stats = tensor(a[2], "stats"),
                          w = tensor(a[3], "w", true), d_residual = tensor(a[5], "d_residual", true);
-        for (auto [t, name] : {std::pair{&d_out, "d_out"}, {&d_residual, "d_residual"}})
+        for (auto [t, name] : {std::pair{&d_out, "d_out"}, {&x, "x"}, {&stats, "stats"}, {&w, "w"}, {&d_residual, "d_residual"}})
             no_history(*t, name, "mhc_layer_norm_backward");
         const Shape s = shape_2d(x, "x");
         const at::ScalarType t = x.scalar_type(), o = d_out.scalar_type();

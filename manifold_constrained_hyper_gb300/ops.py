@@ -767,7 +767,9 @@ def mhc_layer_norm_backward(d_out, x, stats, w=None, *, bias: bool = True, d_res
     """Gradients of mhc_layer_norm's inputs from that of out. x, stats, w as in
     the forward call; bias: whether there was a b. d_residual [T, H] of x's
     type is added to d_x: the gradient that reaches x past the norm; d_x may be
-    d_residual itself. d_w and d_b are float32 (parts of one allocation)."""
+    d_residual itself. d_w and d_b are float32 (parts of one allocation). Not
+    differentiable itself: while gradients are recorded, tensors that require
+    them are refused."""
     return LayerNormGrads._make(_at(stream, (_fast or load_binding()).layer_norm_backward, d_out, x, stats, w,
                                     bias, d_residual, d_x, workspace))
 

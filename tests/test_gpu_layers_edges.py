@@ -45,5 +45,23 @@ def test_few_tokens_with_a_long_summed_axis_keep_sums_of_16_bit_results(T, K, N,
             assert ((d.double() - want[:, :256]).abs() <= half_ulp(dtype, want[:, :256] * (1 + rel)) + rel * want[:, :256]).all()
 
 
+def test_gradients_do_not_go_missing():
+    """Every tensor of every call, where gradients of it are being recorded; the same calls without."""
+    x, w, d, z = (torch.randn(*n, device="cuda").to(BF) for n in ((8, 64), (32, 64), (8, 32), (8, 64)))
+    p, b, r, f = torch.randn(64, device="cuda"), torch.randn(32, device="cuda"), torch.randn(8, 32, device="cuda"), torch.randn(8, 64, device="cuda")
+    stats = ops.mhc_layer_norm(x)[1]
+    calls = ((lambda x, w, b, r: ops.mhc_linear(x, w, b, r), (x, w, b, r)), (lambda d, w, z: ops.mhc_linear_dx(d, w, z, "silu"), (d, w, z)),
+             (ops.mhc_linear_dw, (d, x)), (lambda x, w, b: ops.mhc_layer_norm(x, w, b)[0], (x, p, p)),
+             (lambda d, x, s, w, r: ops.mhc_layer_norm_backward(d, x, s, w, d_residual=r).d_x, (x, x, stats, p, z)), (ops.mhc_orthogonalize, (f,)))
+    for call, tensors in calls:
+        want = call(*tensors)
+        for i in range(len(tensors)):
+            leaf = [t.clone().requires_grad_(k == i) for k, t in enumerate(tensors)]
+            with pytest.raises(ValueError, match="requires grad"):
+                call(*leaf)
+            with torch.no_grad():
+                assert torch.equal(call(*leaf), want)
+
+
 def test_device_status_is_clean():
     assert ops.mhc_get_device_status() == 0
