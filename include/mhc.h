@@ -534,8 +534,8 @@ size_t mhc_orthogonalize_workspace_bytes(int batch, int m, int n);
  *   A = X X^T,  X <- (a I + b A + c A A) X
  * G of dtype (any); out [batch, m, n] of out_dtype (BF16 or F16: matrices are
  * held in 22 bits between the products, which is what a 16-bit result takes).
- * steps in [1, 100]; |a|, |b|, |c| <= 1000; elements of the products past
- * 16 overflow to infinity. A G of zeros gives zeros. batch in [0, 65535].
+ * steps in [1, 100]; |a| < 16, |b|, |c| <= 1000. Elements of A, of the
+ * polynomial and of X past 16 overflow to infinity. A G of zeros gives zeros. batch in [0, 65535].
  */
 mhc_status mhc_orthogonalize(const void *g, int64_t row_stride, int64_t batch_stride, mhc_dtype dtype,
                              int batch, int m, int n, int steps, float a, float b, float c, float eps,

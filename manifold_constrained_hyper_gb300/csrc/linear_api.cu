@@ -4,6 +4,7 @@
 
 #include "api_common.h"
 #include "linear_internal.h"
+#include "orthogonal.h"
 
 using namespace mhc;
 
@@ -306,7 +307,7 @@ mhc_status mhc_orthogonalize(const void *g, int64_t row_stride, int64_t batch_st
                              int steps, float a, float b, float c, float eps, void *out, mhc_dtype out_dtype, void *workspace,
                              size_t workspace_bytes, void *stream) {
     if (batch < 0 || row_stride < 0 || batch_stride < 0 || !dtype_ok(dtype) || steps < 1 || steps > 100 || !(eps >= 0.f) ||
-        std::isinf(eps) || !(std::fabs(a) <= 1000.f) || !(std::fabs(b) <= 1000.f) || !(std::fabs(c) <= 1000.f))
+        std::isinf(eps) || !(std::fabs(a) < kNsMostUnit) || !(std::fabs(b) <= 1000.f) || !(std::fabs(c) <= 1000.f))
         return MHC_ERR_SHAPE;
     if (!width_ok(m) || !width_ok(n) || batch > 65535 || !half_ok(out_dtype)) return MHC_ERR_UNSUPPORTED;
     if (batch == 0) return MHC_OK;

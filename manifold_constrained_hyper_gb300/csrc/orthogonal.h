@@ -7,6 +7,7 @@
 namespace mhc {
 
 constexpr float kNsScale = 4096.f;                  // what every matrix is held times
+constexpr float kNsMostUnit = 16.f;                 // what a is below: P has it on its diagonal, and fp16 holds kNsScale times that
 constexpr int kNsMostCtas = 152;                    // that share a product, at most an item each, or a pair of them
 // Scratch of the products: parts of split sums ([CTAs][tile columns, 256 at most][128]), and counters.
 constexpr size_t kNsPartsBytes = static_cast<size_t>(kNsMostCtas) * 256 * 128 * 4;

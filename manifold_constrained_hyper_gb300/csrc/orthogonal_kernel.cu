@@ -661,7 +661,7 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     const bool wide = c.m <= c.n;
     NsArgs a = {};
     // Two steps as one, X <- (P1 P0) X with A1 = P0 P0 A: two products of X less, three of matrices [p][p] more. The product
-    // of two P has to stay below 16. 4096 x 7168: 17 % fewer operations; small matrices are bound by the number of products.
+    // of two P has to stay below 16. (Where squared singular values pass 2 and it does not, the A after it is above 16 too, in either form.) 4096 x 7168: 17 % fewer operations; small matrices are bound by the number of products.
     double largest = 0.;
     for (int i = 0; i <= 64; ++i) {
         const double l = i / 32., v = std::fabs(c.a + l * (c.b + l * c.c));

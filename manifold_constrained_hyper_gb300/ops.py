@@ -785,7 +785,7 @@ def mhc_orthogonalize(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: 
 
         A = X X^T,   X <- (a I + b A + c A A) X      (a, b, c = coeffs)
 
-    which brings g's singular values towards 1. g is float32, bfloat16 or
+    which brings g's singular values towards 1 (|a| < 16). g is float32, bfloat16 or
     float16, its rows contiguous; out is bfloat16 or float16. Between the
     products every matrix is held in 22 bits. Returns out, of g's shape."""
     if out is not None:

@@ -69,5 +69,17 @@ def test_coefficients_that_all_but_cancel(shape, steps, coeffs, out):
     assert float((got.double() - want).norm() / want.norm()) < 1.2 * torch.finfo(out).eps / 2
 
 
+@pytest.mark.parametrize("shape", [(96, 200), (257, 600), (2, 130, 140)], ids=str)
+@pytest.mark.parametrize("a", [15.99, -15.99])
+def test_the_largest_coefficient(shape, a):
+    """Just below what is refused: P's diagonal is held, and zeros stay zeros."""
+    for coeffs in ((a, 0.0, 0.0), (a, 0.5, 0.25)):
+        g = torch.randn(*shape, generator=gen(3), device="cuda")
+        got = ops.mhc_orthogonalize(g, 1, coeffs, dtype=FP16)
+        want = ref.orthogonalize(g, 1, coeffs, 1e-7)
+        assert float((got.double() - want).norm() / want.norm()) < 1.2 * torch.finfo(FP16).eps / 2
+        assert not ops.mhc_orthogonalize(torch.zeros_like(g), 1, coeffs).any()
+
+
 def test_device_status_is_clean():
     assert ops.mhc_get_device_status() == 0

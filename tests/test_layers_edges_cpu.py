@@ -1,4 +1,5 @@
 """Edges of the projections', layer norm's and the update's host side that need no GPU."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -6,6 +7,7 @@ import sys
 import pytest
 
 from manifold_constrained_hyper_gb300 import build as mbuild
+from manifold_constrained_hyper_gb300 import ops
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -21,3 +23,16 @@ def test_a_product_over_nothing_has_no_parts(lib, m, n, k):
             f"f.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong]; assert f({m}, {n}, {k}) == 0")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(lib))
     assert r.returncode == 0, (r.returncode, r.stderr)
+
+
+@pytest.mark.parametrize("a,refused", [(16.0, True), (-16.0, True), (1000.0, True), (15.99, False), (-15.99, False), (0.0, False)])
+def test_coefficients_that_overflow_by_themselves_are_refused(a, refused):
+    """P has a on its diagonal, and overflows from 16 on whatever the matrix: zeros gave NaN. Without matrices nothing is launched."""
+    f, P, A = ctypes.c_float, ctypes.c_void_p, 0x1000000
+
+    def go(batch):
+        return ops.load().mhc_orthogonalize(P(A), 512, 512 * 256, 0, batch, 256, 512, 5, f(a), f(-1.0), f(0.5), f(1e-7), P(A * 2), 1, P(A * 4), 1 << 28, None)
+
+    assert go(0) == (3 if refused else 0)
+    if refused:
+        assert go(2) == 3
