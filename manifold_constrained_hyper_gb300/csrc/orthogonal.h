@@ -36,7 +36,9 @@ struct NsCall {
     float *parts;
     unsigned int *counters;                         // zero
 };
-// A side of at most 128 and the other of at most 2048 (64: 4096, 32: 8192): all of it by clusters of CTAs.
+// A side of at most 128 and the other of at most 2048 (64: 4096, 32: 8192) by a cluster of at most `ctas` CTAs, 16 of them where the
+// device holds such a cluster.
+bool ns_small_fits_in(int m, int n, int ctas);
 bool ns_small_fits(int m, int n);
 int launch_ns_small(const OrthogonalArgs &a, const NsPolynomial &f, unsigned int *status, bool pdl, cudaStream_t s);
 int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s);

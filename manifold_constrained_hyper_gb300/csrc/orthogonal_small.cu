@@ -366,8 +366,42 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-// 1: may be launched with clusters of up to 16; asked once a device.
-std::atomic<int> g_ready[64];
+using SmallKernel = void (*)(const SmallArgs);
+const SmallKernel kKernels[] = {ns_small_kernel<5>, ns_small_kernel<6>, ns_small_kernel<7>};
+// The largest cluster of at most kMost CTAs that the device holds, asked once a device: 0 before, and where it cannot be launched at all -1.
+std::atomic<int> g_most[64];
+int most_ctas() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return kMost;       // without a device: sizes for the one that the library is for
+    }
+    int most = g_most[dev & 63].load(std::memory_order_acquire);
+    if (most) return most;
+    most = -1;
+    bool ready = true;
+    for (auto kern : kKernels)
+        ready = ready && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
+                cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    for (int ctas = kMost; ready && ctas && most < 0; ctas /= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kKernels[0], &cfg) == cudaSuccess && n > 0) most = ctas;
+    }
+    cudaGetLastError();
+    g_most[dev & 63].store(most, std::memory_order_release);
+    return most;
+}
 
 }  // namespace
 
@@ -376,10 +410,11 @@ int shift_of(int p) { return p <= 32 ? 5 : p <= 64 ? 6 : 7; }
 int stretch_of(int p, int q) { return (q + (kP >> shift_of(p)) - 1) / (kP >> shift_of(p)); }
 }  // namespace
 
-bool ns_small_fits(int m, int n) {
+bool ns_small_fits_in(int m, int n, int ctas) {
     const int p = m < n ? m : n, q = m < n ? n : m;
-    return p <= kP && stretch_of(p, q) <= kP * kMost;
+    return p <= kP && stretch_of(p, q) <= kP * ctas;
 }
+bool ns_small_fits(int m, int n) { return ns_small_fits_in(m, n, kMost) && ns_small_fits_in(m, n, most_ctas()); }
 
 int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int *status, bool pdl, cudaStream_t s) {
     SmallArgs a = {};
@@ -390,7 +425,7 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
     a.batch_stride = o.batch_stride;
     a.p = a.tall ? o.n : o.m;
     a.q = a.tall ? o.m : o.n;
-    void (*const kernels[])(const SmallArgs) = {ns_small_kernel<5>, ns_small_kernel<6>, ns_small_kernel<7>};
+    const int most = most_ctas();
     a.stretch = stretch_of(a.p, a.q);
     // the width by how many clusters the GPU holds at once, and by a matrix's time: 128 columns a CTA take a seventh longer than
     // 64 in a cluster of at most 8, and less than 64 in a larger one (128 x 1024 56 us against 61; 64 x 128 x 512 112 against 238)
@@ -398,7 +433,7 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
     for (int width : {64, 128}) {
         const int ctas = (a.stretch + width - 1) / width, at_once = kGridCap / ctas;
         const double cost = (width == 128 ? 1.15 : ctas <= 8 ? 1. : 1.25) * ((o.batch + at_once - 1) / at_once);
-        if (ctas > kMost || cost >= least) continue;
+        if (ctas > most || cost >= least) continue;
         least = cost;
         a.width = width;
         a.ctas = ctas;
@@ -414,15 +449,6 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
     a.out_dtype = o.out_dtype;
     a.status = status;
     a.timeout_ns = wait_timeout_ns();
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MHC_ERR_CUDA;
-    if (!g_ready[dev & 63].load(std::memory_order_acquire)) {
-        for (auto kern : kernels)
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-                cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-                return MHC_ERR_CUDA;
-        g_ready[dev & 63].store(1, std::memory_order_release);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(o.batch) * a.ctas);
     cfg.blockDim = dim3(kThreads);
@@ -437,7 +463,7 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    return note_launch(cudaLaunchKernelEx(&cfg, kernels[shift_of(a.p) - 5], a));
+    return note_launch(cudaLaunchKernelEx(&cfg, kKernels[shift_of(a.p) - 5], a));
 }
 
 }  // namespace mhc

@@ -36,3 +36,14 @@ def test_coefficients_that_overflow_by_themselves_are_refused(a, refused):
     assert go(0) == (3 if refused else 0)
     if refused:
         assert go(2) == 3
+
+
+@pytest.mark.parametrize("m,n,ctas,fits", [(128, 2048, 16, True), (128, 2049, 16, False), (128, 2048, 8, False), (1024, 128, 8, True), (128, 1025, 8, False),
+                                           (64, 4096, 16, True), (64, 4096, 8, False), (2048, 64, 8, True), (32, 8192, 16, True), (4096, 32, 8, True),
+                                           (32, 4097, 8, False), (129, 129, 16, False), (1, 1, 1, True), (1, 1, -1, False)])
+def test_small_updates_take_no_larger_cluster_than_the_device_holds(lib, m, n, ctas, fits):
+    """16 CTAs in a cluster are not portable: where the device does not hold them (a part of it, say), the general form runs, and its
+    workspace is asked for."""
+    f = ctypes.CDLL(lib)._ZN3mhc16ns_small_fits_inEiii
+    f.restype, f.argtypes = ctypes.c_bool, [ctypes.c_int] * 3
+    assert f(m, n, ctas) == fits
