@@ -63,18 +63,17 @@ __global__ void __launch_bounds__(kLnThreads) ln_rows_kernel(const LayerNormArgs
 }
 
 // The same for many rows: rows to come staged in shared memory, where the parameters lie too.
-constexpr int kRingThreads = 768;
 template <class TX, class TO, int R, bool RUNS>
-__global__ void __launch_bounds__(kRingThreads) ln_ring_kernel(const LayerNormArgs a, const __grid_constant__ LnRing ring, int warps) {
+__global__ void __launch_bounds__(kLnRingThreads) ln_ring_kernel(const LayerNormArgs a, const __grid_constant__ LnRing ring, int warps) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[8][2 * 16];
+    __shared__ float red[kLnRingGroups][2 * 16];
     __shared__ int abort_flag;
     const int lane = threadIdx.x & 31, groups = (blockDim.x - 32) / (32 * warps), group = threadIdx.x / (32 * warps);
     const int mine = threadIdx.x - group * 32 * warps, warp = mine >> 5;
     const bool affine = a.w || a.b, filler = threadIdx.x >= blockDim.x - 32;
-    float *const par = reinterpret_cast<float *>(smem + 512);
+    float *const par = reinterpret_cast<float *>(smem + kLnRingBars);
     const int Hp = (a.H + 7) / 8 * 8, par_bytes = affine ? (8 * Hp + 127) / 128 * 128 : 0;
-    const int which = filler ? lane : group, places_at = 512 + par_bytes + which * ring.stages * ring.place[kLnArrays];
+    const int which = filler ? lane : group, places_at = kLnRingBars + par_bytes + which * ring.stages * ring.place[kLnArrays];
     LnPlace place = {smem_addr(smem) + which * ring.stages * 16, smem_addr(smem) + places_at, 0, 0};
     if (threadIdx.x == 0) {
         ln_bars_init(smem_addr(smem), groups * ring.stages, warps);
@@ -94,7 +93,7 @@ __global__ void __launch_bounds__(kRingThreads) ln_ring_kernel(const LayerNormAr
     if (affine) {
         ln_stage_param(par, a.w, a.w_dtype, a.H, Hp, 1.f, 32 * warps * groups);
         ln_stage_param(par + Hp, a.b, a.b_dtype, a.H, Hp, 0.f, 32 * warps * groups);
-        named_barrier_sync(15, 32 * warps * groups);
+        named_barrier_sync(kLnAllBarrier, 32 * warps * groups);
     }
     int turn = 0;
     for (long long t = first; t < a.T; t += step, place.next(ring)) {
@@ -192,30 +191,21 @@ __global__ void __launch_bounds__(kLnThreads) ln_loop_kernel(const LayerNormArgs
 
 bool on_runs(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == MHC_F32 ? 31u : 15u)) == 0; }
 
-constexpr int kRingSmem = 220 * 1024;
-
-// Many rows: a CTA an SM, as many groups as 768 threads give, as many stages as shared memory holds, at most 4 a group.
 template <class TX, class TO>
 cudaError_t launch_ring(const LayerNormArgs &a, bool runs, int sms, unsigned int *status, bool pdl, cudaStream_t s) {
-    // four runs a thread leave too few registers for rows that are shifted into place
-    const int need = (a.H + 255) / 256, R = need <= 6 || !runs ? 2 : 4, warps = (need + R - 1) / R;
-    int groups = (kRingThreads - 32) / (32 * warps);
-    if (groups > 8) groups = 8;
     LnRing ring = {};
     ring.row_bytes[0] = a.H * static_cast<int>(sizeof(TX));
-    ln_places(&ring);
-    const int par = a.w || a.b ? (8 * ((a.H + 7) / 8 * 8) + 127) / 128 * 128 : 0;
-    ring.stages = (kRingSmem - 512 - par) / (groups * ring.place[kLnArrays]);
-    if (ring.stages > 4) ring.stages = 4;
+    ln_places(ring.row_bytes, ring.place);
+    const LnRingShape p = ln_ring_shape(a.H, ring.place[kLnArrays], runs, a.w || a.b);
+    ring.stages = p.stages;
     ring.status = status;
     ring.timeout_ns = wait_timeout_ns();
-    const int smem = 512 + par + groups * ring.stages * ring.place[kLnArrays];
-    auto *const kern = R == 2 ? (runs ? ln_ring_kernel<TX, TO, 2, true> : ln_ring_kernel<TX, TO, 2, false>)
+    auto *const kern = p.R == 2 ? (runs ? ln_ring_kernel<TX, TO, 2, true> : ln_ring_kernel<TX, TO, 2, false>)
                               : ln_ring_kernel<TX, TO, 4, true>;
     static std::atomic<uint64_t> done[4];
-    if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kRingSmem, &done[2 * (R == 2) + runs])) return e;
-    const long long blocks = (a.T + groups - 1) / groups;
-    return launch_block_kernel(kern, static_cast<unsigned>(blocks < sms ? blocks : sms), 32 * (warps * groups + 1), smem, pdl, s, a, ring, warps);
+    if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kLnRingSmem, &done[2 * (p.R == 2) + runs])) return e;
+    const long long blocks = (a.T + p.groups - 1) / p.groups;
+    return launch_block_kernel(kern, static_cast<unsigned>(blocks < sms ? blocks : sms), 32 * (p.warps * p.groups + 1), p.smem, pdl, s, a, ring, p.warps);
 }
 
 template <class TX, class TO>
@@ -225,17 +215,16 @@ cudaError_t launch_types(const LayerNormArgs &a, int sms, unsigned int *status, 
     const bool runs = a.H % 8 == 0 && a.x_stride % 8 == 0 && on_runs(a.x, a.x_dtype) && on_runs(a.out, a.out_dtype) &&
                       on_runs(a.w, a.w_dtype) && on_runs(a.b, a.b_dtype);
     if (a.H > 512 && a.T >= 8LL * sms) return launch_ring<TX, TO>(a, runs, sms, status, pdl, s);
-    const int need = (a.H + 255) / 256;             // warps of one run a lane
-    const int R = need <= 1 ? 1 : need <= 2 ? 2 : 4, warps = (need + R - 1) / R, groups = kLnThreads / (32 * warps);
-    const long long blocks = (a.T + groups - 1) / groups, cap = 4LL * sms;
+    const LnRows p = ln_rows(a.H);
+    const long long blocks = (a.T + p.groups - 1) / p.groups, cap = 4LL * sms;
     auto pick = [&](auto r) {
         constexpr int N = decltype(r)::value;
         return runs ? ln_rows_kernel<TX, TO, N, true> : ln_rows_kernel<TX, TO, N, false>;
     };
-    auto *const kern = R == 1   ? pick(std::integral_constant<int, 1>())
-                       : R == 2 ? pick(std::integral_constant<int, 2>())
-                                : pick(std::integral_constant<int, 4>());
-    return launch_block_kernel(kern, static_cast<unsigned>(blocks < cap ? blocks : cap), 32 * warps * groups, 0, pdl, s, a, warps);
+    auto *const kern = p.R == 1   ? pick(std::integral_constant<int, 1>())
+                       : p.R == 2 ? pick(std::integral_constant<int, 2>())
+                                  : pick(std::integral_constant<int, 4>());
+    return launch_block_kernel(kern, static_cast<unsigned>(blocks < cap ? blocks : cap), 32 * p.warps * p.groups, 0, pdl, s, a, p.warps);
 }
 
 }  // namespace

@@ -2,13 +2,11 @@
 #pragma once
 #include <atomic>
 
+#include "layer_norm_shape.h"
 #include "linear_internal.h"
 #include "vec_io.cuh"
 
 namespace mhc {
-
-constexpr int kLnThreads = 512;                     // of a CTA: as many groups as fit
-constexpr int kLnMaxHeld = 8192;                    // columns that a group holds in registers
 
 // Sums over a group of `warps` warps (whole ones), the same in every thread. red: [2][16][N] floats of the
 // group; `turn` alternates between calls, so that one barrier a call is enough.
@@ -74,7 +72,6 @@ __device__ __forceinline__ float run_sum(const Run &r) {
 // each warp of the group has said so. A wait that runs out raises the flag, after which none waits:
 // the CTA then goes through its rows without their values, so that no thread misses a barrier, and the
 // status says so. A row on no boundary of 16 bytes comes with the 16-byte words that hold its ends.
-constexpr int kLnArrays = 3;
 struct LnRing {
     int stages, row_bytes[kLnArrays], place[kLnArrays + 1];     // bytes of a row of each array (0: none), where they lie in a stage; its size
     unsigned int *status;
@@ -181,16 +178,6 @@ __device__ __forceinline__ Run ln_staged(const uint8_t *row, uint32_t skew, int 
 template <class T>
 __device__ __forceinline__ uint32_t ln_skew(const T *p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
-}
-// A stage's places for rows of these sizes, wherever the rows begin; a run read past a row's end
-// touches at most 48 bytes more.
-inline void ln_places(LnRing *r) {
-    int at = 0;
-    for (int i = 0; i < kLnArrays; ++i) {
-        r->place[i] = at;
-        if (r->row_bytes[i]) at += (r->row_bytes[i] + 15 + 64 + 127) / 128 * 128;
-    }
-    r->place[kLnArrays] = at;
 }
 // A parameter's H values, zeros up to Hp, to shared memory by the CTA's first `threads` threads, eight loads of each on their way at once.
 __device__ __forceinline__ void ln_stage_param(float *to, const void *p, int dtype, int H, int Hp, float otherwise, int threads) {

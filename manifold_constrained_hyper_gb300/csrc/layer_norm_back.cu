@@ -10,8 +10,7 @@
 namespace mhc {
 namespace {
 
-constexpr int kR = 2;                               // runs of 8 columns a thread at most
-constexpr int kAllBarrier = 15;                     // of all groups (of several warps there are at most 8)
+constexpr int kR = kLnBackRuns;
 
 // The groups' sums over tokens to the CTA's set, or, where it is the only CTA, to the outputs, in the groups' order, through
 // meet [groups][2][Hp].
@@ -33,7 +32,7 @@ __device__ __forceinline__ void meet_sums(float *meet, const LayerNormBackArgs &
         }
     }
     const int threads = 32 * warps * groups;
-    named_barrier_sync(kAllBarrier, threads);
+    named_barrier_sync(kLnAllBarrier, threads);
     for (int c = threadIdx.x; c < 2 * Hp; c += threads) {
         const int col = c < Hp ? c : c - Hp;
         if (col >= H) continue;
@@ -123,9 +122,9 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNor
     const int lane = threadIdx.x & 31, groups = (blockDim.x - (SELF ? 0 : 32)) / (32 * warps), group = threadIdx.x / (32 * warps);
     const int mine = threadIdx.x - group * 32 * warps, warp = mine >> 5, threads = 32 * warps * groups;
     const bool filler = !SELF && threadIdx.x >= threads;
-    float *const par = reinterpret_cast<float *>(smem + 1024);
+    float *const par = reinterpret_cast<float *>(smem + kLnBackRingBars);
     const int Hp = (a.H + 7) / 8 * 8, par_bytes = (4 * Hp + 127) / 128 * 128;
-    const int which = filler ? lane : group, places_at = 1024 + par_bytes + which * ring.stages * ring.place[kLnArrays];
+    const int which = filler ? lane : group, places_at = kLnBackRingBars + par_bytes + which * ring.stages * ring.place[kLnArrays];
     LnPlace place = {smem_addr(smem) + which * ring.stages * 16, smem_addr(smem) + places_at, 0, 0};
     if (threadIdx.x == 0) {
         ln_bars_init(smem_addr(smem), groups * ring.stages, warps);
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNor
     Run dw[R], db[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) dw[r] = db[r] = run_splat(0.f);
-    named_barrier_sync(kAllBarrier, threads);
+    named_barrier_sync(kLnAllBarrier, threads);
     int turn = 0;
     float next_mean = first < a.T ? a.stats[2 * first] : 0.f, next_rstd = first < a.T ? a.stats[2 * first + 1] : 0.f;
     for (long long t = first; t < a.T; t += step, place.next(ring)) {
@@ -231,8 +230,8 @@ __global__ void __launch_bounds__(kLnThreads) ln_back_ring_kernel(const LayerNor
         ln_drain(ring, fill, first < a.T ? static_cast<int>((next - first) / step) : 0);
     if (!a.d_w && !a.d_b) return;
     // the groups' sums meet in the stages, which hold nothing on its way any more, and each thread adds some columns
-    named_barrier_sync(kAllBarrier, threads);
-    meet_sums<R>(reinterpret_cast<float *>(smem + 1024 + par_bytes), a, dw, db, groups, group, warps, mine);
+    named_barrier_sync(kLnAllBarrier, threads);
+    meet_sums<R>(reinterpret_cast<float *>(smem + kLnBackRingBars + par_bytes), a, dw, db, groups, group, warps, mine);
 }
 
 // Rows too wide to be held: a CTA a row, read twice; its sums over tokens in its set, each column its thread's.
@@ -315,76 +314,44 @@ __global__ void __launch_bounds__(256) ln_back_join_kernel(const float *sums, in
 
 bool on_runs(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == MHC_F32 ? 31u : 15u)) == 0; }
 
-struct Shape {
-    int R, warps, groups, parts;
-    bool ring, self;
-};
-// The row kernels' shape: as many groups as 512 threads give, a CTA an SM. With several rows a group they
-// are staged, by one more warp. (A stage is 3 x 32 KB at most, beside 32 KB of weights: one fits.)
-Shape shape_of(long long T, int H) {
-    Shape p = {1, kLnThreads / 32, 1, 0, false, false};
-    if (H <= kLnMaxHeld) {
-        const int need = (H + 255) / 256;
-        p.R = need <= 1 ? 1 : kR;
-        p.warps = (need + p.R - 1) / p.R;
-        p.groups = kLnThreads / (32 * p.warps);
-        if (p.R == kR && T > static_cast<long long>(kGridCap) * p.groups) {
-            p.ring = true;
-            p.self = p.warps % 8 == 0;
-            if (!p.self) p.groups = (kLnThreads - 32) / (32 * p.warps);
-        }
-    }
-    const long long blocks = (T + p.groups - 1) / p.groups;
-    p.parts = static_cast<int>(blocks < kGridCap ? blocks : kGridCap);
-    return p;
-}
-
-constexpr int kRingSmem = 216 * 1024;
-constexpr int kMeetSmem = 64 * 1024;                // 512 threads of two runs: 8192 columns in all groups, two sums
-
 template <class TX, class TD>
 cudaError_t launch_types(const LayerNormBackArgs &a, unsigned int *status, bool pdl, cudaStream_t s) {
-    const Shape p = shape_of(a.T, a.H);
+    const LnBack p = ln_back(a.T, a.H, kGridCap);
     if (a.H > kLnMaxHeld)
         return launch_block_kernel(ln_back_loop_kernel<TX, TD>, static_cast<unsigned>(p.parts), kLnThreads, 0, pdl, s, a);
     const bool runs = a.H % 8 == 0 && a.x_stride % 8 == 0 && a.d_stride % 8 == 0 && on_runs(a.x, a.x_dtype) &&
                       on_runs(a.d_out, a.d_dtype) && on_runs(a.d_x, a.x_dtype) && on_runs(a.w, a.w_dtype) &&
                       (!a.d_residual || (a.r_stride % 8 == 0 && on_runs(a.d_residual, a.x_dtype)));
-    const int Hp = (a.H + 7) / 8 * 8, meet = p.groups * 8 * Hp;
     if (p.ring) {
         LnRing ring = {};
         ring.row_bytes[0] = a.H * static_cast<int>(sizeof(TX));
         ring.row_bytes[1] = a.H * static_cast<int>(sizeof(TD));
         ring.row_bytes[2] = a.d_residual ? ring.row_bytes[0] : 0;
-        ln_places(&ring);
-        const int par = (4 * Hp + 127) / 128 * 128, room = kRingSmem - 1024 - par;
-        ring.stages = room / (p.groups * ring.place[kLnArrays]);
-        if (ring.stages > 4) ring.stages = 4;
+        ln_places(ring.row_bytes, ring.place);
+        const LnBackRing q = ln_back_ring(p, a.H, ring.place[kLnArrays], a.d_residual);
+        ring.stages = q.stages;
         ring.status = status;
         ring.timeout_ns = wait_timeout_ns();
-        int places = p.groups * ring.stages * ring.place[kLnArrays];
-        if (places < meet) places = meet;
         const bool self = p.self;
         auto *const kern = self ? (runs ? ln_back_ring_kernel<TX, TD, kR, true, true> : ln_back_ring_kernel<TX, TD, kR, false, true>)
                                 : (runs ? ln_back_ring_kernel<TX, TD, kR, true, false> : ln_back_ring_kernel<TX, TD, kR, false, false>);
-        // with d_residual a group's first thread orders a row later: two places at least
-        if (ring.stages >= (self && a.d_residual ? 2 : 1)) {
+        if (ring.stages) {
             static std::atomic<uint64_t> done[4];
-            if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kRingSmem, &done[2 * self + runs])) return e;
-            return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * (p.warps * p.groups + !self), 1024 + par + places, pdl, s, a, ring, p.warps);
+            if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kLnBackRingSmem, &done[2 * self + runs])) return e;
+            return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * (p.warps * p.groups + !self), q.smem, pdl, s, a, ring, p.warps);
         }
     }
     auto *const kern = p.R == 1 ? (runs ? ln_back_rows_kernel<TX, TD, 1, true> : ln_back_rows_kernel<TX, TD, 1, false>)
                                 : (runs ? ln_back_rows_kernel<TX, TD, kR, true> : ln_back_rows_kernel<TX, TD, kR, false>);
     static std::atomic<uint64_t> done[4];
-    if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kMeetSmem, &done[2 * (p.R == 1) + runs])) return e;
-    return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * p.warps * p.groups, a.d_w || a.d_b ? meet : 0, pdl, s, a, p.warps);
+    if (cudaError_t e = ln_allow_smem(reinterpret_cast<const void *>(kern), kLnBackMeetSmem, &done[2 * (p.R == 1) + runs])) return e;
+    return launch_block_kernel(kern, static_cast<unsigned>(p.parts), 32 * p.warps * p.groups, a.d_w || a.d_b ? ln_back_meet(p, a.H) : 0, pdl, s, a, p.warps);
 }
 
 }  // namespace
 
 size_t layer_norm_sums_bytes(long long T, int H) {
-    const int parts = T > 0 ? shape_of(T, H).parts : 0;
+    const int parts = T > 0 ? ln_back(T, H, kGridCap).parts : 0;
     return parts > 1 || H > kLnMaxHeld ? static_cast<size_t>(parts) * 2 * H * 4 : 0;
 }
 
@@ -398,7 +365,7 @@ int launch_layer_norm_back(const LayerNormBackArgs &a, unsigned int *status, boo
         else if (a.d_dtype == MHC_F16) e = launch_types<float, __half>(a, status, pdl, s);
         else e = launch_types<float, float>(a, status, pdl, s);
         if (int r = note_launch(e)) return r;
-        parts = shape_of(a.T, a.H).parts;
+        parts = ln_back(a.T, a.H, kGridCap).parts;
         if (parts == 1 && a.H <= kLnMaxHeld) return MHC_OK;     // the row kernel wrote the sums
     }
     if (!a.d_w && !a.d_b) return MHC_OK;

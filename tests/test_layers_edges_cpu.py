@@ -47,3 +47,67 @@ def test_small_updates_take_no_larger_cluster_than_the_device_holds(lib, m, n, c
     f = ctypes.CDLL(lib)._ZN3mhc16ns_small_fits_inEiii
     f.restype, f.argtypes = ctypes.c_bool, [ctypes.c_int] * 3
     assert f(m, n, ctas) == fits
+
+
+SHAPES = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "layer_norm_shape.h"
+using namespace mhc;
+static int bad = 0;
+#define CHECK(c) do { if (!(c)) { ++bad; std::printf("H %d: %s\n", H, #c); } } while (0)
+// Groups of several warps wait at barriers 1 .. groups, all of them at kLnAllBarrier; a reduction has 16 places a group at most.
+static void group(int H, int R, int warps, int groups, int most_groups) {
+    CHECK(R * warps * 256 >= H);
+    CHECK(warps >= 1 && warps <= 16 && groups >= 1 && groups <= most_groups);
+    CHECK(warps == 1 || groups < kLnAllBarrier);
+}
+int main() {
+    for (int H = 1; H <= kLnMaxHeld; ++H) {
+        const LnRows r = ln_rows(H);
+        group(H, r.R, r.warps, r.groups, 16);
+        CHECK(32 * r.warps * r.groups <= kLnThreads);
+        for (int x = 2; x <= 4; x += 2) {
+            int place[kLnArrays + 1];
+            const int one[kLnArrays] = {H * x, 0, 0};
+            ln_places(one, place);
+            // a row from any byte of its first 16, and what the last run reads past its end
+            CHECK(place[kLnArrays] >= H * x + 15 + 48 && place[kLnArrays] % 128 == 0);
+            for (int runs = 0; runs < 2; ++runs)
+                for (int affine = 0; affine < 2; ++affine) {
+                    const LnRingShape s = ln_ring_shape(H, place[kLnArrays], runs, affine);
+                    group(H, s.R, s.warps, s.groups, kLnRingGroups);
+                    CHECK(32 * (s.warps * s.groups + 1) <= kLnRingThreads);
+                    CHECK(s.stages >= 1 && 16 * s.groups * s.stages <= kLnRingBars);
+                    CHECK(s.smem <= kLnRingSmem && kLnRingSmem + 4096 <= 227 * 1024);
+                }
+            for (int d = 2; d <= x; d += 2)
+                for (int residual = 0; residual < 2; ++residual) {
+                    const int all[kLnArrays] = {H * x, H * d, residual ? H * x : 0};
+                    ln_places(all, place);
+                    for (long long T : {1LL, 2432LL, 1LL << 30}) {
+                        const LnBack p = ln_back(T, H, 152);
+                        group(H, p.R, p.warps, p.groups, 16);
+                        CHECK(32 * (p.warps * p.groups + (p.ring && !p.self)) <= kLnThreads);
+                        CHECK(p.parts >= 1 && p.parts <= 152 && ln_back_meet(p, H) <= kLnBackMeetSmem);
+                        if (!p.ring) continue;
+                        const LnBackRing s = ln_back_ring(p, H, place[kLnArrays], residual);
+                        CHECK(s.stages >= 0 && 16 * p.groups * s.stages <= kLnBackRingBars);
+                        CHECK(!s.stages || (s.smem <= kLnBackRingSmem && kLnBackRingSmem + 8192 <= 227 * 1024));
+                        CHECK(s.smem >= kLnBackRingBars + s.params + ln_back_meet(p, H));
+                    }
+                }
+        }
+    }
+    return bad != 0;
+}
+"""
+
+
+def test_layer_norm_s_launch_shapes_keep_the_kernels_limits_for_every_width(tmp_path):
+    """Barriers' numbers, threads, places of the reductions, stages and shared memory, of every form, type and width."""
+    src, exe = tmp_path / "shapes.cpp", tmp_path / "shapes"
+    src.write_text(SHAPES)
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-I", mbuild.CSRC, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout[:2000]
