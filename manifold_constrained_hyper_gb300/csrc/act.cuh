@@ -74,10 +74,6 @@ __device__ __forceinline__ float act_slope(float z) {
     }
     return 1.f;
 }
-template <bool SLOPE, int ACT>
-__device__ __forceinline__ float act_either(float z) {
-    return SLOPE ? act_slope<ACT>(z) : act_value<ACT>(z);
-}
 // f(an integral constant of the activation), the switch outside of what f loops over.
 template <class F>
 __device__ __forceinline__ void with_act(int act, F &&f) {
