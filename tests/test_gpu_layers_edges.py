@@ -63,5 +63,41 @@ def test_gradients_do_not_go_missing():
                 assert torch.equal(call(*leaf), want)
 
 
+@pytest.mark.parametrize("T,H,types", [(2500, 2048, (FP16, FP16)), (2000, 4096, (BF, BF)), (1300, 1999, (BF, BF)), (1600, 1102, (FP32, FP32)),
+                                       (1400, 7168, (FP32, BF)), (1300, 7167, (FP16, FP16)), (1250, 8191, (FP32, FP32)), (5000, 264, (FP16, FP16)),
+                                       (1300, 3585, (BF, BF)), (300, 9001, (BF, BF))])
+@pytest.mark.parametrize("affine", [True, False])
+def test_a_residual_gradient_in_place_among_many_rows(T, H, types, affine):
+    """d_x in d_residual's place, where later rows are on their way to shared memory while earlier ones are written, and rows off 16
+    bytes come with words that hold their neighbours' ends: by a warp that orders rows, by the groups' first threads, unstaged."""
+    xt, ot = types
+    g = gen(T + H)
+    x, d, r = rows(g, T, H, xt), rows(g, T, H, ot, 0, 0, 0.1), rows(g, T, H, xt)
+    w = 1 + 0.1 * torch.randn(H, generator=g, device="cuda") if affine else None
+    stats = ops.mhc_layer_norm(x, w, w)[1]
+    want = ops.mhc_layer_norm_backward(d, x, stats, w, bias=affine, d_residual=r)
+    ref.within(want.d_x, *ref.layer_norm_backward(d, x, stats, w, r)["d_x"])
+    for _ in range(3):
+        place = r.clone()
+        got = ops.mhc_layer_norm_backward(d, x, stats, w, bias=affine, d_residual=place, d_x=place)
+        assert got.d_x.data_ptr() == place.data_ptr()
+        assert all(a is b if a is None else torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("T,K,N,act", [(9000, 64, 2304, "gelu"), (9001, 72, 2305, "silu"), (4100, 2048, 1024, "none"), (300, 8192, 264, "relu2")])
+@pytest.mark.parametrize("dtype", [BF, FP32])
+def test_a_residual_in_place_with_several_tiles_a_cta(T, K, N, act, dtype):
+    """out in the residual's place: tiles in turn, and sums that are split and joined."""
+    g = gen(T)
+    x, w, b, r = rows(g, T, K, BF), rows(g, N, K, BF, 0, 0, K ** -0.5), torch.randn(N, generator=g, device="cuda"), rows(g, T, N, dtype)
+    want = ops.mhc_linear(x, w, b, r, act)
+    exact, _, e, _ = ref.linear(x, w, b, r, act)
+    ref.within(want, exact, e)
+    for _ in range(3):
+        place = r.clone()
+        out, z = ops.mhc_linear(x, w, b, place, act, out=place, keep_z=True)
+        assert out.data_ptr() == place.data_ptr() and torch.equal(out, want)
+
+
 def test_device_status_is_clean():
     assert ops.mhc_get_device_status() == 0
