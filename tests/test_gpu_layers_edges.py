@@ -99,5 +99,31 @@ def test_a_residual_in_place_with_several_tiles_a_cta(T, K, N, act, dtype):
         assert out.data_ptr() == place.data_ptr() and torch.equal(out, want)
 
 
+def _spaces(n):
+    """None, and a workspace of n bytes whose every element of any type is a NaN."""
+    return (None, torch.full((n,), 255, dtype=torch.uint8, device="cuda")) if n else (None,)
+
+
+@pytest.mark.parametrize("T,K,N,pad", [(5, 300, 200, 3), (64, 4096, 130, 0), (130, 4160, 264, 0), (300, 519, 1096, 3), (1000, 64, 64, 8), (700, 2050, 520, 1)])
+def test_workspaces_need_no_initialisation(T, K, N, pad):
+    """Copies of rows, parts of split sums and sums over tokens: written before they are read."""
+    g = gen(T + K)
+    x, w, d = rows(g, T, K, BF, pad), rows(g, N, K, BF, pad, 0, K ** -0.5), rows(g, T, N, BF, pad)
+    al = pad % 8 == 0 and K % 8 == 0 and N % 8 == 0
+    for call, n in ((lambda s: [ops.mhc_linear(x, w, workspace=s)], ops.linear_workspace_bytes(T, N, K, al, al)),
+                    (lambda s: [ops.mhc_linear_dx(d, w, workspace=s)], ops.linear_dx_workspace_bytes(T, N, K, al, al)),
+                    (lambda s: list(ops.mhc_linear_dw(d, x, bias=True, workspace=s)), ops.linear_dw_workspace_bytes(T, N, K, al, al))):
+        got = [call(s) for s in _spaces(n)]
+        assert all(torch.isfinite(t).all() for t in got[0])
+        assert all(torch.equal(p, q) for other in got[1:] for p, q in zip(got[0], other))
+    for H in (K, 8 * K + 1):
+        y, e = rows(g, T, H, FP32), rows(g, T, H, FP32)
+        p = torch.randn(H, generator=g, device="cuda")
+        stats = ops.mhc_layer_norm(y, p, p)[1]
+        got = [ops.mhc_layer_norm_backward(e, y, stats, p, workspace=s) for s in _spaces(ops.layer_norm_backward_workspace_bytes(T, H))]
+        assert all(torch.isfinite(t).all() for t in got[0])
+        assert all(torch.equal(a, b) for other in got[1:] for a, b in zip(got[0], other))
+
+
 def test_device_status_is_clean():
     assert ops.mhc_get_device_status() == 0
