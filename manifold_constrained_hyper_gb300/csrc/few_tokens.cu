@@ -5,6 +5,7 @@
 // the CTAs of a cluster, whose sums meet in distributed shared memory, in the order of the CTAs: no
 // second kernel, and the same result run to run. 1 x 7168 into 4096 bf16: 13.1 us among weights that L2 does not hold, 4.5 TB/s;
 // 7168 into 7168 19, 5.4 TB/s; 64 tokens 16.6.
+// Across the weights' rows (the gradient of the input, 4096 into 7168): 13.2 for a token, 14.2 for 16, 17.3 for 64.
 #include <atomic>
 
 #include "epilogue.cuh"

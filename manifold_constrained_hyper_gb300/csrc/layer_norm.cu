@@ -1,7 +1,7 @@
 // Layer norm, out = (x - mean) * rstd * w + b, bound by memory: each row is read once, into registers,
 // where the mean comes first and then the sum of the centred squares (no cancellation for rows far off zero).
 // 8192 x 7168 fp32 to bf16: 58.4 us, 0.89 of the copy rate (without rows to come 81); bf16 51.7, where the two sums of
-// a row, one after the other, bound it; 1 x 7168 3.4.
+// a row, one after the other, bound it; 1 x 7168 3.4. Rows above 8192 columns: 8192 x 8200 bf16 179, 0.22.
 #include "layer_norm.cuh"
 
 namespace mhc {
@@ -214,6 +214,10 @@ cudaError_t launch_types(const LayerNormArgs &a, int sms, unsigned int *status, 
         return launch_block_kernel(ln_loop_kernel<TX, TO>, static_cast<unsigned>(a.T < 4 * sms ? a.T : 4 * sms), kLnThreads, 0, pdl, s, a);
     const bool runs = a.H % 8 == 0 && a.x_stride % 8 == 0 && on_runs(a.x, a.x_dtype) && on_runs(a.out, a.out_dtype) &&
                       on_runs(a.w, a.w_dtype) && on_runs(a.b, a.b_dtype);
+    // Staged where a row takes several warps and there are several rows a group. Measured among rows that L2 does not hold, staged against
+    // from memory: 8192 x 7168 fp32 58 us against 83 (bf16 53 against 52), 8192 x 4096 bf16 32 against 43, 8192 x 1024 11.5 against 12.4; with
+    // 2432 rows 22 against 30 (7168 fp32), 21 against 18 (7168 bf16), 13.4 against 14.7 (4096 bf16), 5.7 against 4.3 (1024 bf16); with 608 rows
+    // always slower (4096 bf16 5.9 against 5.0). Up to 512 columns a row is one warp's work: 8192 x 512 7.9 against 5.4.
     if (a.H > 512 && a.T >= 8LL * sms) return launch_ring<TX, TO>(a, runs, sms, status, pdl, s);
     const LnRows p = ln_rows(a.H);
     const long long blocks = (a.T + p.groups - 1) / p.groups, cap = 4LL * sms;

@@ -46,7 +46,8 @@ struct LnRingShape {
 };
 inline LnRingShape ln_ring_shape(int H, int stage_bytes, bool runs, bool affine) {
     LnRingShape s;
-    // four runs a thread leave too few registers for rows that are shifted into place
+    // four runs a thread leave too few registers for rows that are shifted into place; others take four from 1537 columns on (8192 rows of bf16:
+    // 4096 columns 31 us against 36 with two, 7168 52 against 70, but 2048 17.6 against 17.5 and 1024 12.0 against 11.3)
     const int need = ln_runs8(H);
     s.R = need <= 6 || !runs ? 2 : 4;
     s.warps = (need + s.R - 1) / s.R;
@@ -58,7 +59,9 @@ inline LnRingShape ln_ring_shape(int H, int stage_bytes, bool runs, bool affine)
 }
 
 // Backward: as many groups as 512 threads give, a CTA an SM of `sms`. With several rows a group they are staged, by one more
-// warp, or (self) by each group's first thread where that warp would cost a group. parts: CTAs.
+// warp, or (self) by each group's first thread where that warp would cost a group. parts: CTAs. Staged against from memory, with
+// d_residual, among rows that L2 does not hold: 8192 x 4096 bf16 52 us against 98, 8192 x 520 16.5 against 21.3, 2432 x 2048 15.2 against 19.1, 2432 x 1024
+// 11.4 against 11.9; a row a group: 608 x 2048 10.2 against 9.1, 1216 x 1024 9.9 against 8.5. Up to 256 columns a thread holds one run, and a CTA 16 rows.
 constexpr int kLnBackRuns = 2, kLnBackRingSmem = 216 * 1024, kLnBackRingBars = 1024;
 constexpr int kLnBackMeetSmem = 64 * 1024;          // 512 threads of two runs: 8192 columns in all groups, two sums
 struct LnBack {

@@ -13,7 +13,7 @@
 // keeps what matters of lo above fp16's smallest values, and leaves room for 16 times 1.
 //
 // By size: orthogonal_small.cu where a side is at most 128 and the other not too long, else this file's two kernels (the norm; X in two parts) and
-// orthogonal_kernel.cu's one. 4096 x 7168 2.80 ms in a burst, 2048 x 1024 190 us, 256 x 256 95, 6 x 128 x 500 48.
+// orthogonal_kernel.cu's one. 4096 x 7168 3.28 ms in a burst, 2048 x 1024 201 us, 256 x 256 99, 6 x 128 x 500 49.
 //
 // G may lie in strided rows. A tall G is not turned: its Gram matrix is X^T X, the product reading both
 // operands with the summed axis outermost.

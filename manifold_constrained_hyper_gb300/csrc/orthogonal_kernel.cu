@@ -5,10 +5,10 @@
 //
 // A pair forms a 256 x 256 or 256 x 128 tile, a CTA 128 rows of 128, 64 or 32 columns, as the products with an epilogue do (64 of k
 // a stage, five stages, two buffers of sums in tensor memory). Every operand is two fp16 parts: a step of 64 is one stage of both
-// operands' hi and one of their lo, and three products (with a stage for each product hi came twice: 2048 x 1024 222 us against 203,
-// 2944 x 1760 617 against 502).
+// operands' hi and one of their lo, and three products (with a stage for each product hi came twice: 2048 x 1024 took 9 % longer,
+// 2944 x 1760 23 %).
 //
-// 4096 x 7168 2.80 ms, the tensor cores at the power cap; 2048 x 1024 190 us (15 launches 450), where a
+// 4096 x 7168 3.28 ms in a burst, 3.55 with the tensor cores at the power cap; 2048 x 1024 201 us (15 launches 450), where a
 // product takes some 5.5 us beside its own steps: 0.6 until the first stage is there, 1 to 3 the epilogue, 0.4 until the
 // CTA's warps have met, 1.5 to 2.3 the barrier; split, 3 more for the parts.
 // A symmetric result's tiles left of the diagonal are not formed: those right of it are stored twice,
@@ -595,10 +595,10 @@ int resident_units(int *units) {
 
 // A product by `units` pairs of CTAs, or CTAs. The cheapest of both tiles' widths and of splitting or not, by what was
 // measured on one GB300: three products of 64 take 0.95 us with a pair's 256 columns, where the tensor cores are busy, else
-// what it takes to load them, more where every SM loads for several tiles in turn (3 x 1408 x 6436 by pairs' tiles 1.38 ms, by CTAs' 1.57);
+// what it takes to load them, more where every SM loads for several tiles in turn (3 x 1408 x 6436 by CTAs' tiles takes 14 % longer than by pairs');
 // finishing 64 columns of a tile by a warp 3 us; writing parts and waiting for the others'
-// 3.1 (256 columns 5.3), and finishing 8 columns of s parts 0.4 + 0.1 s. (By 16 columns, with half as many parts: 5331 x 149 142 us
-// against 124, 628 x 392 129 against 116.)
+// 3.1 (256 columns 5.3), and finishing 8 columns of s parts 0.4 + 0.1 s. (By 16 columns, with half as many parts: 5331 x 149 took 15 %
+// longer, 628 x 392 11 %.)
 Phase phase_of(int role, int m, int n, int k, int batch, bool a_turned, bool b_turned, bool pair, int units, double *cost) {
     Phase f = {};
     const bool symmetric = role != R_APPLY;
@@ -620,7 +620,7 @@ Phase phase_of(int role, int m, int n, int k, int batch, bool a_turned, bool b_t
     double best = 1e300;
     long long count = 0;
     for (int tile_n : {rows, rows / 2, 32}) {
-        // 32 columns where there are few tiles, with half the epilogue of 64 (256 x 256 104 -> 95 us, 400 x 416 124 -> 112).
+        // 32 columns where there are few tiles, with half the epilogue of 64 (256 x 256 takes 9 % less, 400 x 416 10 %).
         // (Read across k a tile's columns come by 64.)
         if (tile_n == 32 && (pair || b_turned)) continue;
         const long long c = tiles(tile_n);
@@ -661,7 +661,7 @@ int launch_ns(const NsCall &c, unsigned int *status, cudaStream_t s) {
     const bool wide = c.m <= c.n;
     NsArgs a = {};
     // Two steps as one, X <- (P1 P0) X with A1 = P0 P0 A: two products of X less, three of matrices [p][p] more. The product
-    // of two P has to stay below 16. (Where squared singular values pass 2 and it does not, the A after it is above 16 too, in either form.) 4096 x 7168: 17 % fewer operations; small matrices are bound by the number of products.
+    // of two P has to stay below 16. (Where squared singular values pass 2 and it does not, the A after it is above 16 too, in either form.) 4096 x 7168: 15 % fewer operations; small matrices are bound by the number of products.
     double largest = 0.;
     for (int i = 0; i <= 64; ++i) {
         const double l = i / 32., v = std::fabs(c.a + l * (c.b + l * c.c));

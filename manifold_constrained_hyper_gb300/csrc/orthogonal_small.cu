@@ -3,12 +3,12 @@
 // end), 64 or 128 of its columns in each CTA's shared memory, in two fp16 parts and in the layout that the
 // tensor core reads, both along k (for A = X X^T) and across it (for P X). A side of at most 64, or 32, leaves room for
 // two, or four, stretches of the columns, one below the other: A is the sum of what comes out on the diagonal, and stands there
-// as often (1024 x 64 60 -> 44 us, a batch of 46 237 -> 98, 32 x 8192 147 -> 51). Per step:
+// as often (1024 x 64 60 -> 44 us, a batch of 46 237 -> 101, 32 x 8192 147 -> 53). Per step:
 //   each CTA's part of A over its columns, in fp32, to its shared memory;
 //   each CTA adds some rows of A over the CTAs, in their order, and writes them to all of them
 //     (distributed shared memory, a row a warp: whole lines; 16 bytes here and there took eight times as long);
 //   each CTA forms P, the same everywhere, and its columns of P X, which take X's place.
-// Two barriers of the cluster a step, some 8 us in all (6 x 128 x 500: 47 us), where a barrier of the grid and a trip
+// Two barriers of the cluster a step, some 8 us in all (6 x 128 x 500: 49 us), where a barrier of the grid and a trip
 // through L2 after each of the three products come to 28 (143).
 #include <atomic>
 
@@ -428,7 +428,7 @@ int launch_ns_small(const OrthogonalArgs &o, const NsPolynomial &f, unsigned int
     const int most = most_ctas();
     a.stretch = stretch_of(a.p, a.q);
     // the width by how many clusters the GPU holds at once, and by a matrix's time: 128 columns a CTA take a seventh longer than
-    // 64 in a cluster of at most 8, and less than 64 in a larger one (128 x 1024 56 us against 61; 64 x 128 x 512 112 against 238)
+    // 64 in a cluster of at most 8, and less than 64 in a larger one (128 x 1024 8 % less; 64 x 128 x 512, 115 us, less than half)
     double least = 1e300;
     for (int width : {64, 128}) {
         const int ctas = (a.stretch + width - 1) / width, at_once = kGridCap / ctas;

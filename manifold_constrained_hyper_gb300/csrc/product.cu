@@ -88,7 +88,8 @@ __device__ __forceinline__ void sum_rows(const Args &a, float *red, int w, int l
         Run s = run_splat(0.f);
         const T *from = x + (8 * w + (lane >> 2)) * a.row_pitch + c;
         long long left = a.k - 8 * w - (lane >> 2);
-        // eight loads of a thread on their way at once; a run past the last column lies in its row's pitch, and is not written
+        // eight loads of a thread on their way at once; a run past the last column lies in its row's pitch, or past the last row in the
+        // 16 bytes that hold its end, and its columns are not written
         for (; c < m && left > 0; left -= 8 * kRowsAtOnce, from += 8 * kRowsAtOnce * a.row_pitch) {
             uint4 v[8];
 #pragma unroll
