@@ -81,5 +81,15 @@ def test_the_largest_coefficient(shape, a):
         assert not ops.mhc_orthogonalize(torch.zeros_like(g), 1, coeffs).any()
 
 
+@pytest.mark.parametrize("shape", [(1, 65536), (65536, 1), (3, 50000), (50000, 5), (129, 20000), (2, 33, 9000)], ids=str)
+@pytest.mark.parametrize("out", [BF, FP16])
+def test_long_and_narrow(shape, out):
+    """A side that no cluster holds beside one of a few rows: tiles mostly of rows past the end, sums over up to 65536."""
+    g = momentum(gen(sum(shape)), shape, FP32)
+    got = ops.mhc_orthogonalize(g, dtype=out, workspace=space(shape))
+    want, e = ref.orthogonalize_error(g, 5, MUON, 1e-7, out)
+    near(got, want, e)
+
+
 def test_device_status_is_clean():
     assert ops.mhc_get_device_status() == 0
